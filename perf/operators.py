@@ -8,7 +8,8 @@ The cache is a pool of pages (uint8 [pages, page bytes]).  A page holds
     tile = K codes [D/32][16 tokens][32 values], K scales [D/32][16] fp16,
            V codes, V scales the same
 
-with one block of 32 values of one token as the unit of the format:
+(the scale of the tile's token r is at place 4 s + r / 4 of its 16, s = r % 4
+where r / 4 is even and 3 - r % 4 where it is odd) with one block of 32 values of one token as the unit of the format:
     q8_0  d = max|x| / 127, code = x / d rounded half away from zero, stored
           as code + 128 in one byte; the value is d code
     q4_0  d = -m / 8 with m the value of largest magnitude (the first of
@@ -191,6 +192,12 @@ def _place(slots, page):
     return slots // page, slots % page // TILE, slots % TILE
 
 
+def _scale_place(row):
+    """Where the scale of a tile's token stands among its 16."""
+    four = row // 4
+    return 4 * torch.where(four % 2 == 0, row % 4, 3 - row % 4) + four
+
+
 def _store(pool, case, k, v, slots):
     at, tile, row = _place(slots, case["page"])
     kc, ks, vc, vs = _parts(pool, case)
@@ -198,7 +205,7 @@ def _store(pool, case, k, v, slots):
         codes, scales = _quantize(x, case["fmt"])
         to[at, :, tile, :, row, :] = codes
         if scales is not None:
-            scale_to[at, :, tile, :, row, :] = scales.unsqueeze(-1).view(torch.uint8)
+            scale_to[at, :, tile, :, _scale_place(row), :] = scales.unsqueeze(-1).view(torch.uint8)
 
 
 def _load(pool, case, slots):
@@ -206,7 +213,7 @@ def _load(pool, case, slots):
     kc, ks, vc, vs = _parts(pool, case)
     got = []
     for codes, scales in ((kc, ks), (vc, vs)):
-        s = None if scales is None else scales[at, :, tile, :, row, :].contiguous().view(torch.float16)[..., 0]
+        s = None if scales is None else scales[at, :, tile, :, _scale_place(row), :].contiguous().view(torch.float16)[..., 0]
         got.append(_dequantize(codes[at, :, tile, :, row, :].contiguous(), s, case["fmt"]))
     return got
 
@@ -302,7 +309,8 @@ def _plain_attention(s):
     live = (position < s["lens"][:, None])[:, None, :, None]
     kv = []
     for codes, scales in ((kc, ks), (vc, vs)):
-        d = None if scales is None else scales[where].contiguous().view(torch.float16)[..., 0]
+        order = _scale_place(torch.arange(TILE, device="cuda"))
+        d = None if scales is None else scales[where].contiguous().view(torch.float16)[..., order, 0]
         d = None if d is None else d.movedim(4, -1)
         x = _dequantize(codes[where].movedim(4, -2).contiguous(), d, case["fmt"])
         x = x.movedim(2, 1).reshape(batch, kv_heads, position.numel(), dim)  # [batch, kv head, position, D]
@@ -419,7 +427,8 @@ def _exact_tiles(tiles, case):
             codes = part[:, :blocks * TILE * width].reshape(n, blocks, TILE, width).to(torch.int64)
             d = part[:, blocks * TILE * width:].contiguous().view(torch.float16).to(torch.float64)
             whole = codes - 128 if fmt == "q8_0" else torch.cat([codes % 16, codes // 16], dim=3) - 8
-            v = whole.to(torch.float64) * d.reshape(n, blocks, TILE, 1)
+            order = [4 * (r % 4 if r // 4 % 2 == 0 else 3 - r % 4) + r // 4 for r in range(TILE)]
+            v = whole.to(torch.float64) * d.reshape(n, blocks, TILE, 1)[:, :, order]
         halves.append(v.permute(0, 2, 1, 3).reshape(n * TILE, dim))
     return halves
 

@@ -69,6 +69,13 @@ SIGNATURES = {
     "qgemv_q6_k_plan": (_I, [_I, _I, _I, ctypes.POINTER(ctypes.c_int)]),
     "lmhead_q6_k_top1_plan": (_I, [_I, _I, _I, ctypes.POINTER(ctypes.c_int)]),
     "lmhead_q6_k_top1_noalloc": (_I, [_P, _P, _L, _P, _I, _I, _I, _P]),
+    "kv_page_bytes": (_S, [_I, _I, _I, _I]),
+    "kv_tile_offset": (_L, [_I, _L, _I, _I, _I, _L, _I]),
+    "kv_write": (_I, [_I, _I, _P, _L, _L, _P, _L, _L, _P, _P, _L, _I, _I, _I, _I, _P]),
+    "kv_read": (_I, [_I, _I, _P, _L, _I, _P, _P, _L, _L, _P, _L, _L, _I, _I, _I, _P]),
+    "attn_paged_workspace_bytes": (_S, [_I, _I, _I, _I, _I]),
+    "attn_paged": (_I, [_I, _I, _P, _L, _L, _P, _L, _I, _P, _L, _I, _P, _P, _L, _L, _P, _P, _S, _I, _I, _I, _I, _I,
+                        ctypes.c_float, _I, _P]),
 }
 
 
@@ -425,6 +432,145 @@ def argmax_f32_rows(y: torch.Tensor, N: int | None = None, ids: torch.Tensor | N
     _check("argmax_f32_rows", LIB.argmax_f32_rows(_dev(y, "y"), y.stride(0), _dev(ids, "ids"),
                                                   _dev(ws, "workspace"), ws.numel(), M, N, _stream(y)))
     return ids
+
+
+# ---------------------------------------------------------------- the paged key-value cache
+
+KV_FORMATS = {"f16": 0, "q8_0": 1, "q4_0": 2}
+_TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+
+
+def _kv_format(fmt: str) -> int:
+    if fmt not in KV_FORMATS:
+        raise ValueError(f"fmt must be one of {', '.join(KV_FORMATS)}, not {fmt!r}")
+    return KV_FORMATS[fmt]
+
+
+def _type(t: torch.Tensor, what: str) -> int:
+    if t.dtype not in _TYPES:
+        raise ValueError(f"{what} must be float32, float16 or bfloat16, not {t.dtype}")
+    return _TYPES[t.dtype]
+
+
+def _rows(t: torch.Tensor, what: str, like: torch.Tensor | None = None) -> int:
+    """A CUDA tensor [tokens, heads, head_dim] with contiguous rows; any strides between them."""
+    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+        raise ValueError(f"{what} must be [tokens, heads, head_dim] with contiguous rows")
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{what} must have the shape, type and device of its companion")
+    return _dev(t, what)
+
+
+def _kv_cache(cache: torch.Tensor, fmt: str, page_tokens: int, n_kv_heads: int, head_dim: int, near: torch.Tensor):
+    """(address, pages) of a cache: contiguous uint8, a whole number of pages."""
+    size = kv_page_bytes(fmt, page_tokens, n_kv_heads, head_dim)
+    if size == 0:
+        raise ValueError(f"no such cache: pages of {page_tokens} tokens, {n_kv_heads} kv heads of {head_dim}")
+    if cache.dtype != torch.uint8 or not cache.is_contiguous() or cache.numel() == 0 or cache.numel() % size:
+        raise ValueError(f"cache must be contiguous uint8, a whole number of pages of {size} bytes")
+    if cache.device != near.device:
+        raise ValueError("cache is on another device")
+    return _dev(cache, "cache"), cache.numel() // size
+
+
+def _kv_slots(slots: torch.Tensor, near: torch.Tensor) -> int:
+    if slots.dtype != torch.int64 or slots.dim() != 1 or not slots.is_contiguous() or slots.device != near.device:
+        raise ValueError("slots must be contiguous int64 [tokens] on the cache's device")
+    return _dev(slots, "slots")
+
+
+def kv_page_bytes(fmt: str, page_tokens: int, n_kv_heads: int, head_dim: int) -> int:
+    """Bytes of one page of the cache; 0 for sizes that the calls refuse."""
+    return LIB.kv_page_bytes(_kv_format(fmt), page_tokens, n_kv_heads, head_dim)
+
+
+def kv_tile_offset(fmt: str, n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int, slot: int,
+                   head: int) -> int:
+    """Byte offset in the cache of the 16-token tile that holds a slot of a kv head; -1 outside the cache."""
+    return LIB.kv_tile_offset(_kv_format(fmt), n_pages, page_tokens, n_kv_heads, head_dim, slot, head)
+
+
+def kv_write(cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, fmt: str,
+             page_tokens: int) -> None:
+    """Quantize k, v [tokens, kv heads, head_dim] into the cache (uint8, whole
+    pages of kv_page_bytes) at slots (int64 [tokens]; a slot outside the cache
+    skips its token).  k and v may be slices with any strides between rows."""
+    kp, vp = _rows(k, "k"), _rows(v, "v", like=k)
+    n, heads, dim = k.shape
+    cp, pages = _kv_cache(cache, fmt, page_tokens, heads, dim, k)
+    sp = _kv_slots(slots, k)
+    if slots.numel() != n:
+        raise ValueError(f"{slots.numel()} slots for {n} tokens")
+    if n == 0:
+        return
+    _check("kv_write", LIB.kv_write(_kv_format(fmt), _type(k, "k"), kp, k.stride(0), k.stride(1), vp, v.stride(0),
+                                    v.stride(1), sp, cp, pages, page_tokens, n, heads, dim, _stream(k)))
+
+
+def kv_read(cache: torch.Tensor, slots: torch.Tensor, fmt: str, page_tokens: int, n_kv_heads: int, head_dim: int,
+            dtype: torch.dtype = torch.float32, k: torch.Tensor | None = None, v: torch.Tensor | None = None):
+    """(k, v) [tokens, kv heads, head_dim]: the values of the cache's slots
+    (zeros for a slot outside the cache), in dtype or into the given tensors."""
+    n = slots.numel()
+    if k is None:
+        k = torch.empty((n, n_kv_heads, head_dim), dtype=dtype if v is None else v.dtype, device=cache.device)
+    if v is None:
+        v = torch.empty((n, n_kv_heads, head_dim), dtype=k.dtype, device=cache.device)
+    if k.shape != (n, n_kv_heads, head_dim):
+        raise ValueError(f"k must be [{n}, {n_kv_heads}, {head_dim}]")
+    kp, vp = _rows(k, "k"), _rows(v, "v", like=k)
+    cp, pages = _kv_cache(cache, fmt, page_tokens, n_kv_heads, head_dim, k)
+    sp = _kv_slots(slots, k)
+    if n:
+        _check("kv_read", LIB.kv_read(_kv_format(fmt), _type(k, "k"), cp, pages, page_tokens, sp, kp, k.stride(0),
+                                      k.stride(1), vp, v.stride(0), v.stride(1), n, n_kv_heads, head_dim, _stream(k)))
+    return k, v
+
+
+def attn_paged_workspace_bytes(dtype: torch.dtype, rows: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    if dtype not in _TYPES:
+        raise ValueError(f"dtype must be float32, float16 or bfloat16, not {dtype}")
+    return LIB.attn_paged_workspace_bytes(_TYPES[dtype], rows, n_heads, n_kv_heads, head_dim)
+
+
+def attn_paged(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor, fmt: str,
+               page_tokens: int, n_kv_heads: int, rows: int = 1, scale: float | None = None, window: int = 0,
+               out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+               ws: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of q [batch * rows, heads, head_dim], the last `rows` tokens
+    of each sequence, over the first kv_lens[b] (int32 [batch]) tokens of the
+    cache that page_table (int32 [batch, pages]) maps; causal among the new
+    rows, with an optional sliding window.  scale defaults to head_dim^-1/2;
+    lse (fp32 [batch * rows, heads]) receives the rows' log-sum-exp."""
+    qp = _rows(q, "q")
+    n, heads, dim = q.shape
+    if out is None:
+        out = torch.empty((n, heads, dim), dtype=q.dtype, device=q.device)
+    op = _rows(out, "out", like=q)
+    cp, pages = _kv_cache(cache, fmt, page_tokens, n_kv_heads, dim, q)
+    for t, what, d in ((page_table, "page_table", 2), (kv_lens, "kv_lens", 1)):
+        if t.dtype != torch.int32 or t.dim() != d or (t.shape[-1] > 1 and t.stride(-1) != 1) or t.device != q.device:
+            raise ValueError(f"{what} must be int32 with {d} dimension(s), contiguous in the last, on q's device")
+    batch = kv_lens.numel()
+    if rows < 1 or n != batch * rows or page_table.shape[0] != batch:
+        raise ValueError(f"q has {n} rows: {batch} sequences of {rows} need {batch * rows}, and as many table rows")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (n, heads) or not lse.is_contiguous()
+                            or lse.device != q.device):
+        raise ValueError(f"lse must be contiguous float32 [{n}, {heads}] on q's device")
+    need = attn_paged_workspace_bytes(q.dtype, rows, heads, n_kv_heads, dim)
+    if batch == 0:
+        return out
+    if ws is None:
+        # one that a capture allocates belongs to its graph, whose replays clear it
+        ws = torch.zeros(max(need, 256), dtype=torch.uint8, device=q.device) \
+            if torch.cuda.is_current_stream_capturing() else workspace(q.device, need, key="attn")
+    ld = page_table.stride(0) if batch > 1 else max(page_table.stride(0), page_table.shape[1])
+    _check("attn_paged", LIB.attn_paged(
+        _kv_format(fmt), _type(q, "q"), qp, q.stride(0), q.stride(1), cp, pages, page_tokens,
+        _dev(page_table, "page_table"), ld, page_table.shape[1], _dev(kv_lens, "kv_lens"), op, out.stride(0),
+        out.stride(1), None if lse is None else _dev(lse, "lse"), _dev(ws, "workspace"), ws.numel(), batch, rows, heads,
+        n_kv_heads, dim, dim ** -0.5 if scale is None else scale, window, _stream(q)))
+    return out
 
 
 def qgemv_block_dots_q4_0(w_pack: torch.Tensor, xq: torch.Tensor, M: int, K: int, N: int) -> torch.Tensor:

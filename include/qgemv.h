@@ -460,6 +460,117 @@ int qpack_q5_k(const void* w_canon, void* w_pack, int N, int K, void* stream);
 int qgemv_q5_k(const void* w_pack, const void* xq, float* y, int64_t ldy, int M, int K, int N, void* stream);
 int qgemv_q5_k_plan(int M, int K, int N, int* info);
 
+/* ---- the block-quantized paged key-value cache ------------------------- */
+
+/* Between the projections of a verifier step stands the attention over the
+ * tokens so far.  Their keys and values live in a cache of pages in the block
+ * formats of this library; kv_write quantizes new tokens into it, kv_read
+ * takes tokens out again, attn_paged attends to it without an unpacked copy.
+ * (Not from the pages.)
+ *
+ * The cache is n_pages pages of kv_page_bytes() bytes, 16-byte aligned, owned
+ * by the caller.  A page holds page_tokens tokens (a multiple of 16) of every
+ * kv head:
+ *     page = [kv head][tile of 16 tokens]
+ *     tile = K codes [head_dim/32][16 tokens][block], K scales
+ *            [head_dim/32][16] fp16, then V codes and V scales the same.
+ * The scale of the tile's token r stands at place 4 s + r / 4 of its 16, with
+ * s = r % 4 where r / 4 is even and 3 - r % 4 where it is odd (the order in
+ * which the attention reads them).  A block is 32 values of one token:
+ *   QGEMV_KV_Q8_0  32 bytes, code + 128; value d * code
+ *                  d = max|x| / 127, code = x / d rounded half away from zero
+ *   QGEMV_KV_Q4_0  16 bytes, byte i = code_i | code_{i+16} << 4; value
+ *                  d * (code - 8); d = -m / 8 with m the value of largest
+ *                  magnitude (the first of equals), code = floor(x / d + 8.5)
+ *                  limited to 0 .. 15
+ *   QGEMV_KV_F16   the 32 values in fp16, and no scales
+ * with d, x / d and x / d + 8.5 in fp32.  The stored scale is d rounded to
+ * fp16, at most 65504 in magnitude; a block that holds a NaN or an infinity
+ * gets the scale NaN, so that all of it reads as NaN.
+ * A token's place in the cache is its slot, page * page_tokens + offset. */
+#define QGEMV_KV_F16 0
+#define QGEMV_KV_Q8_0 1
+#define QGEMV_KV_Q4_0 2
+
+/* Element types of k, v, q and out. */
+#define QGEMV_F32 0
+#define QGEMV_F16 1
+#define QGEMV_BF16 2
+
+/* kv_page_bytes - bytes of one page; 0 for sizes that the calls refuse.
+ *   page_tokens  a multiple of 16, 16 .. 1024
+ *   n_kv_heads   1 .. 1024
+ *   head_dim     a multiple of 32, 32 .. 512.  Host-only. */
+size_t kv_page_bytes(int fmt, int page_tokens, int n_kv_heads, int head_dim);
+
+/* kv_tile_offset - byte offset in the cache of the tile of 16 tokens that
+ * holds the place `slot` of kv head `head`: the address that every kernel
+ * below computes; -1 for a slot or head outside the cache.  Host-only. */
+int64_t kv_tile_offset(int fmt, int64_t n_pages, int page_tokens, int n_kv_heads, int head_dim, int64_t slot,
+                       int head);
+
+/* kv_write - quantize the keys and values of n_tokens tokens into the cache.
+ *   k, v       rows of head_dim values of `type`, row (t, h) of k at element
+ *              t * k_token + h * k_head (v the same): any strides >= 0 that
+ *              leave the rows where the caller has them, e.g. slices of one
+ *              q|k|v projection.  Aligned to their element (16-byte aligned
+ *              rows load faster).  Read.
+ *   slots      int64 [n_tokens]: each token's slot; one outside the cache
+ *              (negative, or past its last page) skips the token.  Two tokens
+ *              with one slot in one call leave either's bytes.
+ *   cache      written at those slots and nowhere else
+ *   n_tokens   >= 0
+ * Errors: QGEMV_INVALID_ARG (null pointer, unknown fmt or type, sizes out of
+ * range), QGEMV_UNSUPPORTED_SHAPE (page_tokens % 16, head_dim % 32),
+ * QGEMV_MISALIGNED (cache, slots, or k / v off their element). */
+int kv_write(int fmt, int type, const void* k, int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
+             int64_t v_head, const int64_t* slots, void* cache, int64_t n_pages, int page_tokens, int n_tokens,
+             int n_kv_heads, int head_dim, void* stream);
+
+/* kv_read - the inverse: rows (t, h) of k and v from the cache's slots, in
+ * `type` (d * code is exact in fp32; one rounding to a 16-bit type).  A token
+ * whose slot is outside the cache gets zeros.  Strides, checks and errors as
+ * kv_write; k and v are written (rows must not overlap). */
+int kv_read(int fmt, int type, const void* cache, int64_t n_pages, int page_tokens, const int64_t* slots, void* k,
+            int64_t k_token, int64_t k_head, void* v, int64_t v_token, int64_t v_head, int n_tokens, int n_kv_heads,
+            int head_dim, void* stream);
+
+/* attn_paged - attention of the last `rows` tokens of each of `batch`
+ * sequences over the paged cache: with i = 0 .. rows - 1, row b * rows + i of
+ * q is the token at position kv_lens[b] - rows + i of sequence b; it attends
+ * to the positions p <= its own, of those only the last `window` ones when
+ * window > 0 (the kv head of q head h is h / (n_heads / n_kv_heads)):
+ *     out = sum_p softmax_p(scale q . k_p) v_p,   lse = ln sum_p e^{scale q . k_p}.
+ * A row that sees no position (kv_lens[b] < rows - i) gets zeros and an lse of
+ * minus infinity.  Scores, softmax and sums are fp32; products run on the
+ * tensor cores on operands that carry 22 bits for QGEMV_F32 and QGEMV_F16
+ * and 11 bits for QGEMV_BF16; one rounding to `type` at the end.  The result
+ * is the same, bit for bit, on every call with the same arguments on one
+ * kind of device; what lies at masked places of the cache never reaches it.
+ *   q          rows of head_dim values, row (r, h) at r * q_row + h * q_head
+ *   out        written, row (r, h) at r * o_row + h * o_head; must not overlap q
+ *   lse        fp32 [batch * rows][n_heads] (written), or NULL
+ *   page_table int32, page of positions j page_tokens .. of sequence b at
+ *              b * ld_table + j, 0 <= j < max_pages; entries past a
+ *              sequence's length are not used
+ *   kv_lens    int32 [batch], the lengths with the new tokens in them; <= 0
+ *              for an unused place
+ *   workspace  attn_paged_workspace_bytes() bytes, 16-byte aligned; its first
+ *              1024 bytes zero-filled before the first use, and every call
+ *              leaves them so.  Calls that share it must not overlap in time.
+ *   scale      finite;  window >= 0 (0: none);  1 <= rows <= 17;
+ *   batch      1 .. 65536;  n_heads a multiple of n_kv_heads
+ *   head_dim   64, 96, 128 or 256
+ * A sequence longer than max_pages * page_tokens, or with a page outside
+ * 0 .. n_pages - 1 among those that its rows see, gets NaN in all its rows:
+ * nothing outside the cache is read.
+ * Errors as kv_write, and QGEMV_WORKSPACE_TOO_SMALL. */
+size_t attn_paged_workspace_bytes(int type, int rows, int n_heads, int n_kv_heads, int head_dim);
+int attn_paged(int fmt, int type, const void* q, int64_t q_row, int64_t q_head, const void* cache, int64_t n_pages,
+               int page_tokens, const int32_t* page_table, int64_t ld_table, int max_pages, const int32_t* kv_lens,
+               void* out, int64_t o_row, int64_t o_head, float* lse, void* workspace, size_t ws_bytes, int batch,
+               int rows, int n_heads, int n_kv_heads, int head_dim, float scale, int window, void* stream);
+
 /* qgemv_q8_0_plan - the launch qgemv_q8_0 would make for this shape; writes
  * info[5] = {1, CTAs per cluster (the K parts), grid size, ring stages per
  * warp, blocks per job (8: a whole pack region; 4: half of one, taken where

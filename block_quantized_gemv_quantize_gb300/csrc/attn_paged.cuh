@@ -5,53 +5,77 @@
 // head go together.  With codes c and block scales d (kvcache.cuh),
 //     s[row][p] = scale sum_b d_k[p][b] sum_{i in b} q[row][i] c_k[p][i]
 //     out[row][i] = sum_p w[row][p] d_v[p][b(i)] c_v[p][i] / sum_p w[row][p]
-// with w = 2^(s log2 e - m), m the running maximum of the row.  The codes are
-// small integers, so they are fp16 exactly and are the tensor cores' B operand
-// without ever being scaled: K's scales multiply the fp32 block sums, V's the
-// weights before they are rounded to fp16.  q and w d_v are fp16 pairs hi + lo
-// (22 bits) in the two halves of the A operand, eight rows to an instruction
-// of 16 (TWO; fp32 and fp16 callers), or 16 rows of one fp16 each (bf16
-// callers, whose output keeps 8 bits).  q is brought to 2^13 .. 2^14 by an exact
-// power of two per row, w d_v to below 2^14 by one that follows the largest
+// with w = 2^(s log2 e - m), m a maximum of the row that lags its true one by
+// at most 4 (so sums are rescaled a few times, not at every new maximum).  The
+// codes are small integers, so they are fp16 exactly and are the tensor cores'
+// B operand without ever being scaled: K's scales multiply the fp32 block
+// sums, V's the weights before they are rounded to fp16.  q and w d_v are fp16,
+// as one term (bf16 callers, whose output keeps 8 bits) or as a pair hi + lo of
+// 22 bits (fp32 and fp16 callers).  q is brought to 2^13 .. 2^14 by an exact
+// power of two per row, w d_v to below 2^15 by one that follows the largest
 // d_v seen so far, so that neither leaves fp16's range.
 //
+// Rows in an instruction of 16 (MODE):
+//   ATTN_ONE   16 rows, one term
+//   ATTN_PAIR  8 rows: their hi in the lower half, their lo in the upper
+//   ATTN_TWO   16 rows, hi and lo in two instructions; the blocks are unpacked
+//              once for 16 rows, which from 9 rows on beats two ATTN_PAIR tiles
+//
 // Split.  An item is a (sequence, kv head, group of row tiles).  All items'
-// tiles of 16 tokens stand in one line, cut into equal pieces, one a CTA: the
-// load is even however the lengths differ, and the lengths are read on the
-// device, so that a captured graph serves any.  In a CTA, WS warps take an
-// item's tiles in turn, pairs at a time, each through a ring of its own in
-// shared memory that bulk copies fill (a tile of a kv head is contiguous: one
-// copy); WR warps share each ring, one for every tile of rows.  The WS partial
-// results meet in shared memory; an item cut between CTAs leaves one partial
-// result a CTA in the workspace, and the CTA that finds itself last (a counter)
-// joins them in CTA order, so the result does not depend on the order in which
-// CTAs finish.
+// tiles of 16 tokens stand in one line, each item with ATTN_ITEM_COST units in
+// front for what it costs besides its tiles, and the line is cut into equal
+// pieces, one a split: the load is even however the lengths differ, and the
+// lengths are read on the device, so that a captured graph serves any.  A CTA
+// has WS splits; each streams its piece through a ring of its own in shared
+// memory that bulk copies fill (a tile of a kv head is contiguous: one copy),
+// and WR warps share the ring, one for every tile of rows.  One more warp issues
+// the copies, a lane a ring.  A split writes the outputs of an item that it has
+// whole; of one that it shares it leaves a partial result (at most two) in the
+// workspace.  At the end the CTA joins those of its splits, once; an item that
+// is cut between CTAs leaves one partial result a CTA, and the CTA that finds
+// itself last (a counter) joins them in CTA order, so that the result does not
+// depend on the order in which CTAs finish.
 #pragma once
 
 #include "kvcache.cuh"
 
 namespace qgemv {
 
-constexpr int ATTN_GRID = 160;  // most CTAs (one an SM): the workspace holds two partial results of each
+constexpr int ATTN_GRID = 160;     // most CTAs (one an SM): the workspace holds their partial results
+constexpr int ATTN_ITEM_COST = 4;  // of an item besides its tiles, in tiles
+constexpr int ATTN_MIN_PIECE = 4;  // least units of a split: shorter ones cost more to join than they save
 
-template <int FMT, int NB, bool TWO>
+enum AttnMode { ATTN_ONE = 0, ATTN_PAIR = 1, ATTN_TWO = 2 };
+
+// The mode for a call: by the type's precision and the rows of a kv head.
+inline int attn_mode(int type, int rows) { return type == QGEMV_BF16 ? ATTN_ONE : (rows > 8 ? ATTN_TWO : ATTN_PAIR); }
+
+// Warps that compute (one more copies): as many as 64 K registers hold.
+#ifndef AW
+#define AW 7
+#endif
+__host__ __device__ constexpr int attn_warps(int nb) { return nb > 4 ? 7 : AW; }
+
+template <int FMT, int NB, int MODE>
 struct AttnShape {
-    static constexpr int ROWS = TWO ? 8 : 16;            // rows of a row tile
-    static constexpr int NR = TWO ? 1 : 2;               // rows whose statistics a lane keeps
-    static constexpr int NO = NB * 4 * (TWO ? 2 : 4);    // output values of a lane in a partial result
-    static constexpr int PART = (NO + 2 * NR) * 32;      // floats of one row tile's partial result
+    static constexpr int ROWS = MODE == ATTN_PAIR ? 8 : 16;  // rows of a row tile
+    static constexpr int NR = ROWS / 8;                      // rows whose statistics a lane keeps
+    static constexpr int NC = 2 * NR;                        // output values of a lane and column tile
+    static constexpr int NO = NB * 4 * NC;                   // output values of a lane
+    static constexpr int PART = (NO + 2 * NR) * 32;          // floats of one row tile's partial result
     static constexpr int TILE = kv_tile_bytes(FMT, NB), HALF = kv_half_bytes(FMT, NB);
-    static constexpr bool Q_SMEM = NB > 4;               // q's fragments do not fit the registers next to the sums
-    static constexpr int MAX_WARPS = 8;
+    static constexpr bool Q_SMEM = NB > 4 || MODE == ATTN_TWO;  // else q's fragments stay in registers
+    static constexpr int Q_TERMS = MODE == ATTN_TWO ? 2 : 1;
+    static constexpr int WARPS = attn_warps(NB);
+    static constexpr int STEP = 2;                           // tiles a split takes at a time
 };
 
 struct AttnPlan {
     int type;
     int ws, wr;          // splits, row tiles at a time
-    int row_tiles, row_groups;
+    int row_groups;
     int stages;          // tiles a ring holds
-    int min_chunk;       // least tiles of a CTA
-    uint32_t off_merge, off_q, off_bar, bytes;  // shared memory
+    uint32_t off_q, off_bar, bytes;  // shared memory
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -166,73 +190,90 @@ struct AttnTiles {
     }
 };
 
-// A CTA's walk over its piece of the line of tiles: segments, each a run of
-// one item's tiles.
+// A split's walk over its piece of the line: segments, each a run of one item's
+// tiles.
 struct AttnWalk {
-    int64_t left;        // tiles of the piece from this segment's first on
-    int b, item;         // sequence, (kv head, row group) within it
-    int first, count;    // the item's tiles
-    int ta, tb;          // the segment's, counted from `first`
+    int64_t left;      // units of the piece from this segment's first on
+    int64_t line;      // the item's first unit
+    int b, item;       // sequence, (kv head, row group) within it
+    int first, count;  // the item's tiles
+    int ta, tb;        // the segment's, counted from `first`
+    int used;          // units of it
     __device__ __forceinline__ bool done() const { return left <= 0; }
-    __device__ __forceinline__ void clip() { tb = left < (int64_t)(count - ta) ? ta + (int)left : count; }
+    __device__ __forceinline__ void clip(int off)
+    {
+        const int units = ATTN_ITEM_COST + count - off;
+        used = left < (int64_t)units ? (int)left : units;
+        ta = max(0, off - ATTN_ITEM_COST);
+        tb = max(0, off + used - ATTN_ITEM_COST);
+    }
+    // to the next segment with tiles in it
     __device__ __forceinline__ void next(const AttnArgs& a, int items)
     {
-        left -= tb - ta;
-        if (left <= 0) return;
-        ta = 0;
-        if (++item == items) {
-            item = 0;
-            do {
-                const AttnTiles n{AttnSpan(a, a.lens[++b])};  // left > 0: a later sequence has tiles
-                first = n.first;
-                count = n.count;
-            } while (count == 0);
-        }
-        clip();
+        do {
+            left -= used;
+            if (left <= 0) return;
+            line += ATTN_ITEM_COST + count;
+            if (++item == items) {
+                item = 0;
+                do {
+                    const AttnTiles n{AttnSpan(a, a.lens[++b])};  // left > 0: a later sequence has tiles
+                    first = n.first;
+                    count = n.count;
+                } while (count == 0);
+            }
+            clip(0);
+        } while (tb == 0);
     }
 };
 
-// By one warp: the total of all sequences' tiles times `items`, and the walk
-// that starts at tile `start` of the line (when start < total).
+__device__ __forceinline__ int64_t attn_units(const AttnTiles& t, int items)
+{
+    return t.count ? (int64_t)(t.count + ATTN_ITEM_COST) * items : 0;
+}
+
+// By one warp: the length of the line, and the walk that starts at its unit
+// `start`.
 __device__ __forceinline__ int64_t attn_total(const AttnArgs& a, int items, int lane)
 {
     int64_t n = 0;
-    for (int b = lane; b < a.batch; b += 32) n += AttnTiles(AttnSpan(a, a.lens[b])).count;
+    for (int b = lane; b < a.batch; b += 32) n += attn_units(AttnTiles(AttnSpan(a, a.lens[b])), items);
 #pragma unroll
     for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    return n * items;
+    return n;
 }
 
 __device__ __forceinline__ AttnWalk attn_find(const AttnArgs& a, int items, int64_t start, int64_t left, int lane)
 {
     AttnWalk w{};
-    w.left = left;
+    if (left <= 0) return w;
     int64_t before = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 32) {
         const int b = b0 + lane;
         const AttnTiles t = b < a.batch ? AttnTiles(AttnSpan(a, a.lens[b])) : AttnTiles();
-        int64_t sum = (int64_t)t.count * items;
-        const int64_t own = sum;
+        const int64_t own = attn_units(t, items);
+        int64_t sum = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int64_t up = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o) sum += up;
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, before + sum > start && own > 0);
+        const unsigned hit = __ballot_sync(0xffffffffu, own > 0 && before + sum > start);
         if (hit) {
             const int src = __ffs(hit) - 1;
-            const int64_t off = start - (before + __shfl_sync(0xffffffffu, sum - own, src));
+            const int64_t at = before + __shfl_sync(0xffffffffu, sum - own, src);  // the sequence's first unit
+            w.left = left;
             w.b = b0 + src;
             w.first = __shfl_sync(0xffffffffu, t.first, src);
             w.count = __shfl_sync(0xffffffffu, t.count, src);
-            w.item = (int)(off / w.count);
-            w.ta = (int)(off - (int64_t)w.item * w.count);
-            w.clip();
+            w.item = (int)((start - at) / (w.count + ATTN_ITEM_COST));
+            w.line = at + (int64_t)w.item * (w.count + ATTN_ITEM_COST);
+            w.clip((int)(start - w.line));
+            if (w.tb == 0) w.next(a, items);
             return w;
         }
         before += __shfl_sync(0xffffffffu, sum, 31);
     }
-    w.left = 0;
     return w;
 }
 
@@ -258,13 +299,24 @@ __device__ __forceinline__ bool rows_wide(const void* p, int64_t row, int64_t he
     return type == QGEMV_F32 ? r.wide<float>() : r.wide<__half>();
 }
 
-// What a warp keeps of its row tile: running maximum (of s log2 e), sum of
-// weights and unnormalised outputs.  While a segment runs, l is this lane's
-// share and o is scaled by 2^(28 - e) (f16: 2^14), in the fragments' 16 rows.
-template <int FMT, int NB, bool TWO>
+// The fp16 pair hi + lo of two fp32 values.
+__device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint32_t& lo)
+{
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 f = __half22float2(h);
+    float dx, dy;
+    add_f32x2(dx, dy, x, y, -f.x, -f.y);
+    hi = h2_bits(h);
+    lo = h2_bits(__floats2half2_rn(dx, dy));
+}
+
+// What a warp keeps of its row tile while a segment runs: the rows' reference
+// maximum (of s log2 e), this lane's share of the sum of weights, and the
+// outputs times 2^(25 - e) (fp16 caches: 2^11) in the products' layout.
+template <int FMT, int NB, int MODE>
 struct AttnState {
-    using Sh = AttnShape<FMT, NB, TWO>;
-    float m[Sh::NR], l[Sh::NR];
+    using Sh = AttnShape<FMT, NB, MODE>;
+    float m[Sh::NR], l[Sh::NR], rs[Sh::NR];
     float o[NB][4][4];
     int e;
 
@@ -280,11 +332,8 @@ struct AttnState {
                 for (int c = 0; c < 4; ++c) o[b][n][c] = 0.0f;
         e = 0;
     }
-    // a finite base for exponents: a row that has seen nothing has m = -inf
-    static __device__ __forceinline__ float base(float m) { return m == -INFINITY ? 0.0f : m; }
-
-    // End of a segment: sums over the quad, the two halves of a split row
-    // added (an infinite output stands in the high half alone), the scale out.
+    // End of a segment: l over the quad; the two halves of a split row added
+    // (an infinite output stands in the high half alone); the scale out.
     __device__ __forceinline__ void finish(bool poison)
     {
 #pragma unroll
@@ -293,171 +342,468 @@ struct AttnState {
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
             if (poison) l[r] = __int_as_float(0x7fffffff);
         }
-        const float back = FMT == QGEMV_KV_F16 ? 0x1p-14f : __int_as_float((127 + e - 28) << 23);
+        const float back = FMT == QGEMV_KV_F16 ? 0x1p-11f : __int_as_float((127 + e - 25) << 23);
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    if (TWO && c >= 2) continue;
+                for (int c = 0; c < Sh::NC; ++c) {
                     float v = o[b][n][c];
-                    if (TWO) v = isinf(v) ? v : v + o[b][n][c + 2];
+                    if (MODE == ATTN_PAIR) v = isinf(v) ? v : v + o[b][n][c + 2];
                     o[b][n][c] = v * back;
                 }
     }
-    // this and another partial result of the same rows
-    template <typename Load>
-    __device__ __forceinline__ void join(Load load)
-    {
-        float wa[2], wb[2];
-#pragma unroll
-        for (int r = 0; r < Sh::NR; ++r) {
-            const float m2 = load(Sh::NO + r), l2 = load(Sh::NO + Sh::NR + r);
-            const float mn = fmaxf(m[r], m2), bs = base(mn);
-            wa[r] = ex2(m[r] - bs);
-            wb[r] = ex2(m2 - bs);
-            l[r] = l[r] * wa[r] + l2 * wb[r];
-            m[r] = mn;
-        }
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int c = 0; c < (TWO ? 2 : 4); ++c) {
-                    const int r = TWO ? 0 : c >> 1;
-                    o[b][n][c] = o[b][n][c] * wa[r] + load((b * 4 + n) * (TWO ? 2 : 4) + c) * wb[r];
-                }
-    }
-    template <typename Store>
-    __device__ __forceinline__ void put(Store store) const
-    {
-#pragma unroll
-        for (int r = 0; r < Sh::NR; ++r) store(Sh::NO + r, m[r]), store(Sh::NO + Sh::NR + r, l[r]);
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int c = 0; c < (TWO ? 2 : 4); ++c) store((b * 4 + n) * (TWO ? 2 : 4) + c, o[b][n][c]);
-    }
 };
 
-template <int FMT, int NB, bool TWO>
-__global__ void __launch_bounds__(AttnShape<FMT, NB, TWO>::MAX_WARPS * 32, 1)
+// a finite base for exponents: a row that has seen nothing has m = -inf
+__device__ __forceinline__ float attn_base(float m) { return m == -INFINITY ? 0.0f : m; }
+
+// What one step needs to know of its tiles.
+struct AttnStep {
+    const uint8_t* tile[2];
+    int n;            // tiles, 1 or 2 (2 without EDGE)
+    int pos;          // position of the first tile's first token
+    int first, last;  // positions that any row sees
+};
+
+// STEP tiles of a split into a warp's row tile.  EDGE: some tokens are hidden
+// from some rows, or there is one tile only.
+template <int FMT, int NB, int MODE, bool EDGE>
+__device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const AttnStep& x,
+                                          const uint32_t (&qf)[AttnShape<FMT, NB, MODE>::Q_SMEM ? 1 : NB * 2][4],
+                                          const uint4* q_smem, const int (&begin)[AttnShape<FMT, NB, MODE>::NR],
+                                          const int (&end)[AttnShape<FMT, NB, MODE>::NR], int lane)
+{
+    using Sh = AttnShape<FMT, NB, MODE>;
+    constexpr int NR = Sh::NR, NV = 4 * NR, SCALES = NB * KV_TILE * kv_code_bytes(FMT);
+    const int g = lane >> 2, t = lane & 3;
+
+    // ---- scores: y[u][4 r + i], row g + 8 r, token i of the lane's column pairs
+    float y[2][NV];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int k = 0; k < NV; ++k) y[u][k] = 0.0f;
+    float c16[2][2][4] = {};
+    // the tiles u0 .. u1 - 1 of block b: both at once where that halves the loads
+    // of q's fragments, else one after the other, which needs fewer registers
+    auto block = [&](int b, int u0, int u1) {
+        float c[2][2][4] = {};
+        uint32_t f[2][2][4];
+#pragma unroll
+        for (int u = u0; u < u1; ++u) {
+            if (EDGE && u >= x.n) continue;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) k_fragment<FMT>(x.tile[u], b, tile_token(g >> 1, 2 * j + (g & 1)), t, f[u][j]);
+        }
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int term = 0; term < Sh::Q_TERMS; ++term) {
+                uint32_t qa[4];
+                if constexpr (Sh::Q_SMEM) {
+                    const uint4 w = q_smem[((b * 2 + s) * Sh::Q_TERMS + term) * 32];
+                    qa[0] = w.x, qa[1] = w.y, qa[2] = w.z, qa[3] = w.w;
+                } else {
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) qa[z] = qf[b * 2 + s][z];
+                }
+#pragma unroll
+                for (int u = u0; u < u1; ++u) {
+                    if (EDGE && u >= x.n) continue;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        mma_f16(FMT == QGEMV_KV_F16 ? c16[u][j] : c[u][j], qa, f[u][j][2 * s], f[u][j][2 * s + 1]);
+                }
+            }
+        if constexpr (FMT != QGEMV_KV_F16) {
+#pragma unroll
+            for (int u = u0; u < u1; ++u) {
+                if (EDGE && u >= x.n) continue;
+                const uint2 w = *reinterpret_cast<const uint2*>(x.tile[u] + SCALES + b * 32 + 8 * t);
+                const float2 d[2] = {__half22float2(bits_h2(w.x)), __half22float2(bits_h2(w.y))};
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (MODE == ATTN_PAIR) add_f32x2(c[u][j][0], c[u][j][1], c[u][j][0], c[u][j][1], c[u][j][2], c[u][j][3]);
+#pragma unroll
+                    for (int r = 0; r < NR; ++r)
+                        fma_f32x2(y[u][4 * r + 2 * j], y[u][4 * r + 2 * j + 1], c[u][j][2 * r], c[u][j][2 * r + 1], d[j].x, d[j].y);
+                }
+            }
+        }
+    };
+    if constexpr (Sh::Q_SMEM) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) block(b, 0, 2);
+    } else {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) block(b, u, u + 1);
+    }
+    uint32_t hidden = 0;  // bit 8 u + k: y[u][k] is masked
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                float &v0 = y[u][4 * r + 2 * j], &v1 = y[u][4 * r + 2 * j + 1];
+                if constexpr (FMT == QGEMV_KV_F16) {
+                    v0 = c16[u][j][2 * r], v1 = c16[u][j][2 * r + 1];
+                    if (MODE == ATTN_PAIR) add_f32x2(v0, v1, v0, v1, c16[u][j][2], c16[u][j][3]);
+                }
+                mul_f32x2(v0, v1, v0, v1, st.rs[r], st.rs[r]);
+            }
+        if constexpr (EDGE) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int p = x.pos + u * KV_TILE + tile_token(t, k & 3);
+                if (u >= x.n || p >= end[k >> 2] || p < begin[k >> 2]) {
+                    y[u][k] = -INFINITY;
+                    hidden |= 1u << (u * 8 + k);
+                }
+            }
+        }
+    }
+    // tokens that no row sees: their scales and values are anything
+    uint32_t live[2][2] = {{~0u, ~0u}, {~0u, ~0u}};
+    if constexpr (EDGE) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int p = x.pos + u * KV_TILE + tile_token(t, i);
+                if (u >= x.n || p < x.first || p >= x.last) live[u][i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
+            }
+    }
+
+    // ---- the largest of V's scales
+    int e = st.e;
+    if constexpr (FMT != QGEMV_KV_F16) {
+        __half2 top = bits_h2(0u);  // hmax2 takes the number of a number and a NaN
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            if (EDGE && u >= x.n) continue;
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                uint2 w = *reinterpret_cast<const uint2*>(x.tile[u] + Sh::HALF + SCALES + b * 32 + 8 * t);
+                if (EDGE) w.x &= live[u][0], w.y &= live[u][1];
+                if (FMT == QGEMV_KV_Q4_0) w.x &= 0x7fff7fffu, w.y &= 0x7fff7fffu;  // q8_0's are never negative
+                top = __hmax2(top, __hmax2(bits_h2(w.x), bits_h2(w.y)));
+            }
+        }
+        top = __hmax2(top, __lowhigh2highlow(top));
+        const uint32_t bits = __reduce_max_sync(0xffffffffu, h2_bits(top) & 0xffffu);
+        if (bits < 0x7c00u) e = max(e, (int)(bits >> 10));  // d_v < 2^(e - 14)
+    }
+
+    // ---- the sums are rescaled only where a maximum is passed by 4 (a factor
+    // 2^4 in the weights, so w d_v stays below 2^15) or d_v takes another power of two
+    float mx[NR];
+    bool grow = e > st.e;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        float v = y[0][4 * r];
+#pragma unroll
+        for (int k = 1; k < 8; ++k) v = fmaxf(v, y[k >> 2][4 * r + (k & 3)]);
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
+        mx[r] = v;
+        grow |= v > st.m[r] + 4.0f;
+    }
+    if (__any_sync(0xffffffffu, grow)) {
+        const float down = __int_as_float((127 + st.e - e) << 23);
+        float f[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+            const float mn = fmaxf(st.m[r], mx[r]);
+            f[r] = ex2(st.m[r] - attn_base(mn));
+            st.l[r] *= f[r];
+            f[r] *= down;
+            st.m[r] = mn;
+        }
+        st.e = e;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int nn = 0; nn < 4; ++nn)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) st.o[b][nn][c] *= f[MODE == ATTN_PAIR ? 0 : c >> 1];
+    }
+    // weights, and from here on times the outputs' scale
+    const float up = FMT == QGEMV_KV_F16 ? 0x1p11f : __int_as_float((127 + 25 - st.e) << 23);
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+        const float bs = -attn_base(st.m[r]);
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float &v0 = y[u][4 * r + 2 * j], &v1 = y[u][4 * r + 2 * j + 1];
+                add_f32x2(v0, v1, v0, v1, bs, bs);
+                v0 = ex2(v0);
+                v1 = ex2(v1);
+                add_f32x2(s0, s1, s0, s1, v0, v1);
+                mul_f32x2(v0, v1, v0, v1, up, up);
+            }
+        st.l[r] += s0 + s1;
+    }
+
+    // ---- outputs
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        if (EDGE && u >= x.n) continue;
+        const uint8_t* v8 = x.tile[u] + Sh::HALF;
+        uint32_t hi[4], lo[4];  // A fragments; ATTN_PAIR: hi alone, with the low terms in its upper rows
+        auto weights = [&](const float2 (&d)[2]) {
+            float w[NV];
+#pragma unroll
+            for (int k = 0; k < NV; k += 2) mul_f32x2(w[k], w[k + 1], y[u][k], y[u][k + 1], d[(k >> 1) & 1].x, d[(k >> 1) & 1].y);
+            if constexpr (EDGE) {
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    if (hidden >> (u * 8 + k) & 1) w[k] = 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if constexpr (MODE == ATTN_PAIR) {
+                    split_pair(w[2 * j], w[2 * j + 1], hi[2 * j], hi[2 * j + 1]);
+                } else {
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        if constexpr (MODE == ATTN_TWO) split_pair(w[4 * r + 2 * j], w[4 * r + 2 * j + 1], hi[2 * j + r], lo[2 * j + r]);
+                        else hi[2 * j + r] = h2_bits(__floats2half2_rn(w[4 * r + 2 * j], w[4 * r + 2 * j + 1]));
+                    }
+                }
+            }
+        };
+        bool odd_values = false;  // fp16 caches at an edge: infinities or NaN that some row sees
+        if constexpr (FMT == QGEMV_KV_F16) {
+            const float2 one[2] = {{1.0f, 1.0f}, {1.0f, 1.0f}};
+            weights(one);
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            if constexpr (FMT != QGEMV_KV_F16) {
+                uint2 w = *reinterpret_cast<const uint2*>(v8 + SCALES + b * 32 + 8 * t);
+                const float2 d[2] = {__half22float2(bits_h2(w.x)), __half22float2(bits_h2(w.y))};
+                weights(d);
+            }
+            uint32_t v0[4], v1[4];
+            v_fragments<FMT>(v8, b, g, t, v0, v1);
+            if constexpr (FMT == QGEMV_KV_F16 && EDGE) {
+#pragma unroll
+                for (int nn = 0; nn < 4; ++nn) {
+                    auto finite = [&](uint32_t w) {
+                        if ((w & 0x7c00u) == 0x7c00u) w &= 0xffff0000u, odd_values = true;
+                        if ((w & 0x7c000000u) == 0x7c000000u) w &= 0x0000ffffu, odd_values = true;
+                        return w;
+                    };
+                    v0[nn] = finite(v0[nn] & live[u][0]), v1[nn] = finite(v1[nn] & live[u][1]);
+                }
+            }
+#pragma unroll
+            for (int nn = 0; nn < 4; ++nn) {
+                mma_f16(st.o[b][nn], hi, v0[nn], v1[nn]);
+                if constexpr (MODE == ATTN_TWO) mma_f16(st.o[b][nn], lo, v0[nn], v1[nn]);
+            }
+        }
+        if constexpr (FMT == QGEMV_KV_F16 && EDGE) {
+            // such values went in as zeros; add them to the rows that see them
+            if (__any_sync(0xffffffffu, odd_values)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll 1
+                    for (int tt = 0; tt < 4; ++tt) {
+                        const int tok = tile_token(tt, i);
+                        float w[NR];
+                        bool see[NR];
+#pragma unroll
+                        for (int r = 0; r < NR; ++r) {
+                            w[r] = __shfl_sync(0xffffffffu, y[u][4 * r + i], (lane & 28) | tt);
+                            see[r] = !(__shfl_sync(0xffffffffu, hidden, (lane & 28) | tt) >> (u * 8 + 4 * r + i) & 1);
+                        }
+#pragma unroll
+                        for (int b = 0; b < NB; ++b)
+#pragma unroll
+                            for (int nn = 0; nn < 4; ++nn)
+#pragma unroll
+                                for (int c = 0; c < 2; ++c) {
+                                    const float v = __half2float(
+                                        reinterpret_cast<const __half*>(v8)[(b * KV_TILE + tok) * 32 + 4 * (2 * t + c) + nn]);
+                                    if (isfinite(v)) continue;
+#pragma unroll
+                                    for (int r = 0; r < NR; ++r)
+                                        if (see[r]) st.o[b][nn][2 * r + c] += w[r] * v;
+                                }
+                    }
+            }
+        }
+    }
+}
+
+// What a split leaves in the workspace of an item that it shares.
+struct AttnLeft {
+    int64_t line;  // the item's first unit; -1: nothing
+    int b, item, count, ta, tb;
+};
+
+template <int FMT, int NB, int MODE>
+__global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
     attn_split_kernel(const AttnArgs a, const AttnPlan p, unsigned int* status)
 {
-    using Sh = AttnShape<FMT, NB, TWO>;
+    using Sh = AttnShape<FMT, NB, MODE>;
+    constexpr int STEP = Sh::STEP, NR = Sh::NR;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ AttnWalk s_walk;
-    __shared__ int64_t s_chunk;
-    __shared__ int s_last, s_dead;
+    __shared__ AttnWalk s_walk[Sh::WARPS];
+    __shared__ AttnLeft s_left[2 * Sh::WARPS];
+    __shared__ int s_last[2], s_dead;
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
+    const int warps = p.ws * p.wr;  // those that compute
     const int split = warp / p.wr, wrow = warp - split * p.wr;
     const int items = a.L.heads * p.row_groups;
     const int S = p.stages;
-    uint8_t* ring = smem + (size_t)split * S * Sh::TILE;
-    float* merge = reinterpret_cast<float*>(smem + p.off_merge);
-    uint4* q_smem = reinterpret_cast<uint4*>(smem + p.off_q) + wrow * (NB * 2 * 32) + lane;
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.off_bar) + split * S;
-    uint64_t* empty = reinterpret_cast<uint64_t*>(smem + p.off_bar) + (p.ws + split) * S;
-    int* bad_page = reinterpret_cast<int*>(smem + p.off_bar + 16 * p.ws * S) + split * S;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.off_bar);
+    uint64_t* empty = full + p.ws * S;
+    int* bad_page = reinterpret_cast<int*>(empty + p.ws * S);
 
     pdl_launch_dependents();
-    if (wrow == 0 && lane == 0) {
-        for (int s = 0; s < S; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], p.wr);
+    if (warp == warps) {
+        for (int i = lane; i < p.ws * S; i += 32) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], p.wr);
         }
         fence_barrier_init();
     }
     if (threadIdx.x == 0) s_dead = 0;
     pdl_wait();
 
-    if (warp == 0) {
-        const int64_t total = attn_total(a, items, lane);
-        int64_t chunk = (total + gridDim.x - 1) / gridDim.x;
-        if (chunk < p.min_chunk) chunk = p.min_chunk;
-        const int64_t start = chunk * blockIdx.x;
-        const int64_t left = total - start < chunk ? total - start : chunk;
-        AttnWalk w{};
-        if (left > 0) w = attn_find(a, items, start, left, lane);
-        if (lane == 0) {
-            s_walk = w;
-            s_chunk = chunk;
-        }
+    // the line, and this split's piece of it
+    const int64_t total = attn_total(a, items, lane);
+    int64_t piece = (total + (int64_t)gridDim.x * p.ws - 1) / ((int64_t)gridDim.x * p.ws);
+    if (piece < ATTN_MIN_PIECE) piece = ATTN_MIN_PIECE;
+    const int64_t chunk = piece * p.ws;  // the CTA's
+    AttnWalk seg{};
+    if (warp < warps) {
+        const int64_t start = chunk * blockIdx.x + piece * split;
+        seg = attn_find(a, items, start, total - start < piece ? total - start : piece, lane);
+        if (wrow == 0 && lane == 0) s_walk[split] = seg;
+        if (wrow == 0 && lane < 2) s_left[2 * split + lane].line = -1;
     }
     // sequences of which no row sees anything: zeros (NaN where the length is bad)
     for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
         const AttnSpan sp(a, a.lens[b]);
         if (AttnTiles(sp).count) continue;
-        const float none[4] = {sp.bad ? __int_as_float(0x7fffffff) : 0.0f, sp.bad ? __int_as_float(0x7fffffff) : 0.0f,
-                               sp.bad ? __int_as_float(0x7fffffff) : 0.0f, sp.bad ? __int_as_float(0x7fffffff) : 0.0f};
+        const float v = sp.bad ? __int_as_float(0x7fffffff) : 0.0f;
+        const float none[4] = {v, v, v, v};
         for (int i = threadIdx.x; i < a.rows * a.heads * NB * 8; i += blockDim.x) {
             const int rh = i / (NB * 8), d = (i - rh * (NB * 8)) * 4;
             const int64_t row = (int64_t)b * a.rows + rh / a.heads;
             const int head = rh % a.heads;
             store_row_part(a.out, row * a.o_row + head * a.o_head + d, p.type, false, none);
-            if (a.lse && d == 0) a.lse[row * a.heads + head] = sp.bad ? none[0] : -INFINITY;
+            if (a.lse && d == 0) a.lse[row * a.heads + head] = sp.bad ? v : -INFINITY;
         }
     }
+    if (chunk * blockIdx.x >= total) return;
     __syncthreads();
-    AttnWalk seg = s_walk;
-    if (seg.done()) return;
 
-    // ---- the ring: the lane that issues walks the same segments on its own
-    const bool issuer = wrow == 0 && lane == 0;
-    AttnWalk ahead = seg;
-    int ah_tile = 2 * split, ah_slot = 0, ah_round = 0, issued = 0;  // next tile, counted from ahead.ta
-    const uint64_t policy = l2_evict_first_policy();
-    bool dead = false;
-    const int tpp = a.L.tiles();
-    auto issue = [&](int upto) {  // tiles of this split until `upto` are in flight or done
-        while (issued < upto) {
-            while (!ahead.done() && ahead.ta + ah_tile >= ahead.tb) {
-                ahead.next(a, items);
-                ah_tile = 2 * split;
+    if (warp == warps) {
+        // ---- the copies: lane s walks split s's tiles
+        if (lane < p.ws) {
+            const uint64_t policy = l2_evict_first_policy();
+            const int tpp = a.L.tiles();
+            uint8_t* ring = smem + (size_t)lane * S * Sh::TILE;
+            uint64_t *fl = full + lane * S, *em = empty + lane * S;
+            AttnWalk w = s_walk[lane];
+            int at = w.ta, slot = 0, round = 0, issued = 0;
+            bool dead = false, more = !w.done();
+            int pg = -1, page = 0, tile_in = 0, head = 0;
+            auto settle = [&]() {  // on tile `at`, its page's number on the way
+                const int tile = w.first + at, n = tile / tpp;
+                tile_in = tile - n * tpp;
+                if (n != pg) page = a.table[w.b * a.ld_table + n];
+                pg = n;
+                head = w.item / p.row_groups;
+            };
+            if (more) settle();
+            while (more) {
+                const int64_t off = a.L.tile_offset(page, head, tile_in);
+                const bool ok = off >= 0 && QG_OK(qg_in(off, Sh::TILE, a.L.bytes()), status, 731);
+                if (++at >= w.tb) {
+                    const int b = w.b;
+                    w.next(a, items);
+                    at = w.ta;
+                    more = !w.done();
+                    if (w.b != b) pg = -1;
+                }
+                if (more) settle();
+                if (round > 0 && !mbar_wait_bounded(&em[slot], (round - 1) & 1)) {
+                    dead = true;
+                    break;
+                }
+                bad_page[lane * S + slot] = !ok;
+                mbar_arrive_expect_tx(&fl[slot], ok ? Sh::TILE : 0u);
+                if (ok) bulk_g2s(ring + (size_t)slot * Sh::TILE, a.cache + off, Sh::TILE, &fl[slot], policy);
+                ++issued;
+                if (++slot == S) slot = 0, ++round;
             }
-            if (ahead.done()) return;
-            if (ah_round > 0 && !mbar_wait_bounded(&empty[ah_slot], (ah_round - 1) & 1)) {
-                dead = true;
-                return;
+            if (dead) {  // its own copies in flight
+                for (int q = issued > S ? issued - S : 0; q < issued; ++q) mbar_wait_bounded(&fl[q % S], (q / S) & 1);
+                atomicAdd_system(status, 1u);
             }
-            const int tile = ahead.first + ahead.ta + ah_tile, pg = tile / tpp;
-            const int page = a.table[ahead.b * a.ld_table + pg];
-            const int64_t off = a.L.tile_offset(page, ahead.item / p.row_groups, tile - pg * tpp);
-            const bool ok = off >= 0 && QG_OK(qg_in(off, Sh::TILE, a.L.bytes()), status, 731);
-            bad_page[ah_slot] = !ok;
-            mbar_arrive_expect_tx(&full[ah_slot], ok ? Sh::TILE : 0u);
-            if (ok) bulk_g2s(ring + (size_t)ah_slot * Sh::TILE, a.cache + off, Sh::TILE, &full[ah_slot], policy);
-            ++issued;
-            ah_tile += (ah_tile & 1) ? 2 * p.ws - 1 : 1;
-            if (++ah_slot == S) ah_slot = 0, ++ah_round;
         }
-    };
-    if (issuer) issue(S);
-    int taken = 0, slot = 0, phase = 0;  // tiles of this split
+        return;
+    }
 
-    AttnState<FMT, NB, TWO> st;
+    // ---- the warps that compute
+    auto meet = [&]() { asm volatile("bar.sync 1, %0;" ::"r"(warps * 32) : "memory"); };
+    const uint8_t* ring = smem + (size_t)split * S * Sh::TILE;
+    uint4* q_smem = reinterpret_cast<uint4*>(smem + p.off_q) + warp * (NB * 2 * Sh::Q_TERMS * 32) + lane;
     const bool q_wide = rows_wide(a.q, a.q_row, a.q_head, p.type);
     const bool o_wide = rows_wide(a.out, a.o_row, a.o_head, p.type);
-    int n_seg = 0;
+    // the partial results: of split s of this CTA, and of CTA c
+    auto split_part = [&](int s, int which, int tile) {
+        return a.partials + (((size_t)blockIdx.x * p.ws + s) * 2 + which) * p.wr * Sh::PART + (size_t)tile * Sh::PART + lane;
+    };
+    auto cta_part = [&](int c, int which, int tile) {
+        return a.partials + ((size_t)gridDim.x * p.ws * 2 + 2 * c + which) * p.wr * Sh::PART + (size_t)tile * Sh::PART + lane;
+    };
+    // a row's four values from d on, normalised
+    auto emit = [&](int b_seq, int item, int tile, int b, int h, int r, const float (&v)[4], float m, float l) {
+        const int kvh = item / p.row_groups;
+        const int rr = ((item - kvh * p.row_groups) * p.wr + tile) * Sh::ROWS + g + 8 * r;
+        if (rr >= a.rows * a.group) return;
+        const int i = rr / a.group;
+        const int64_t row = (int64_t)b_seq * a.rows + i;
+        const int head = kvh * a.group + rr - i * a.group;
+        const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+        float o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[k] = l == 0.0f ? 0.0f : v[k] * inv;
+        const int d = b * 32 + (FMT == QGEMV_KV_Q4_0 ? 16 * h + 4 * t : 8 * t + 4 * h);
+        store_row_part(a.out, row * a.o_row + head * a.o_head + d, p.type, o_wide, o);
+        if (a.lse && t == 0 && b == 0 && h == 0)
+            a.lse[row * a.heads + head] = l == 0.0f ? -INFINITY : 0.6931471805599453f * m + logf(l);
+    };
+    int slot = 0, phase = 0, n_seg = 0;
+    bool dead = false;
+    AttnState<FMT, NB, MODE> st;
 
     for (; !seg.done(); seg.next(a, items), ++n_seg) {
-        const AttnSpan sp(a, a.lens[seg.b]);
         const int kvh = seg.item / p.row_groups;
-        const int row_tile = (seg.item - kvh * p.row_groups) * p.wr + wrow;
+        const int row0 = ((seg.item - kvh * p.row_groups) * p.wr + wrow) * Sh::ROWS;
+        const AttnSpan sp(a, a.lens[seg.b]);
         // ---- q: this lane's rows, scaled to 2^13 .. 2^14, as A fragments
         uint32_t qf[Sh::Q_SMEM ? 1 : NB * 2][4];
-        float rs[Sh::NR];
-        int end[Sh::NR], begin[Sh::NR];
-        if (Sh::Q_SMEM) __syncthreads();  // the previous segment's readers are done
+        int end[NR], begin[NR];
 #pragma unroll
-        for (int r = 0; r < Sh::NR; ++r) {
-            const int rr = row_tile * Sh::ROWS + g + 8 * r;
+        for (int r = 0; r < NR; ++r) {
+            const int rr = row0 + g + 8 * r;
             const bool in = rr < a.rows * a.group;
             const int i = in ? rr / a.group : 0;
             end[r] = in ? sp.end(i) : 0;
@@ -486,474 +832,261 @@ __global__ void __launch_bounds__(AttnShape<FMT, NB, TWO>::MAX_WARPS * 32, 1)
             int ex = (int)(top >> 23) - 127;  // |q| < 2^(ex + 1)
             ex = max(-100, min(127, ex));
             const float up = __int_as_float((127 + 13 - ex) << 23);
-            rs[r] = a.scale * 1.4426950408889634f * __int_as_float((127 - 13 + max(ex, -113)) << 23);
+            st.rs[r] = a.scale * 1.4426950408889634f * __int_as_float((127 - 13 + ex) << 23);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float x = qv[b][2 * k] * up, y = qv[b][2 * k + 1] * up;
-                    const __half2 h = __floats2half2_rn(x, y);
-                    hi[k] = h2_bits(h);
-                    if (TWO) {
-                        const float2 f = __half22float2(h);
-                        lo[k] = h2_bits(__floats2half2_rn(x - f.x, y - f.y));
-                    }
-                }
+                for (int k = 0; k < 4; ++k) split_pair(qv[b][2 * k] * up, qv[b][2 * k + 1] * up, hi[k], lo[k]);
                 // k step s: a0, a2 of row g (+ 8: a1, a3)
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
                     if constexpr (Sh::Q_SMEM) {
-                        uint32_t* w = reinterpret_cast<uint32_t*>(q_smem + (b * 2 + s) * 32);
-                        if (split == 0) {
-                            w[r] = hi[2 * s], w[2 + r] = hi[2 * s + 1];
-                            if (TWO) w[1] = lo[2 * s], w[3] = lo[2 * s + 1];
-                        }
+                        uint32_t* w = reinterpret_cast<uint32_t*>(q_smem + (b * 2 + s) * Sh::Q_TERMS * 32);
+                        w[r] = hi[2 * s], w[2 + r] = hi[2 * s + 1];
+                        if (MODE == ATTN_PAIR) w[1] = lo[2 * s], w[3] = lo[2 * s + 1];
+                        if (MODE == ATTN_TWO) w[128 + r] = lo[2 * s], w[130 + r] = lo[2 * s + 1];
                     } else {
                         qf[b * 2 + s][r] = hi[2 * s], qf[b * 2 + s][2 + r] = hi[2 * s + 1];
-                        if (TWO) qf[b * 2 + s][1] = lo[2 * s], qf[b * 2 + s][3] = lo[2 * s + 1];
+                        if (MODE == ATTN_PAIR) qf[b * 2 + s][1] = lo[2 * s], qf[b * 2 + s][3] = lo[2 * s + 1];
                     }
                 }
             }
         }
-        if (Sh::Q_SMEM) __syncthreads();
+        // (a lane reads back what it wrote itself: no barrier)
         // tiles all of whose tokens every row sees need no mask
         const int clear_from = sp.begin(a.rows - 1), clear_to = sp.end(0);
         bool poison = false;
         st.clear();
 
-        for (int tl = seg.ta + 2 * split; tl < seg.tb; tl += 2 * p.ws) {
-            const int n = min(2, seg.tb - tl);
-            if (issuer && !dead) issue(taken + S);
-            const uint8_t* tile[2];
-            uint64_t* done[2];
+        for (int tl = seg.ta; tl < seg.tb; tl += STEP) {
+            AttnStep x;
+            x.n = min(STEP, seg.tb - tl);
+            x.pos = (seg.first + tl) * KV_TILE;
+            x.first = sp.first();
+            x.last = sp.last();
+            int used[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                tile[u] = ring + (size_t)slot * Sh::TILE;
-                done[u] = &empty[slot];
-                if (u < n) {
-                    dead = __any_sync(0xffffffffu, dead) || !__all_sync(0xffffffffu, mbar_wait_bounded(&full[slot], phase));
-                    if (!dead && bad_page[slot]) poison = true;
+                x.tile[u] = ring + (size_t)slot * Sh::TILE;
+                used[u] = split * S + slot;
+                if (u < x.n) {
+                    if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait_bounded(&full[used[u]], phase));
+                    if (!dead && bad_page[used[u]]) poison = true;
                     if (++slot == S) slot = 0, phase ^= 1;
                 }
             }
-            taken += n;
             if (dead) break;
-            if (poison) {  // a stage without its tile: the rows are NaN whatever comes
-                __syncwarp();
-                if (lane == 0)
-                    for (int u = 0; u < n; ++u) mbar_arrive(done[u]);
-                continue;
-            }
-
-            // ---- scores
-            float y[2][4 * Sh::NR];
-            uint32_t hidden = 0;  // bit (tile, value): masked
-            bool edge[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-#pragma unroll
-                for (int k = 0; k < 4 * Sh::NR; ++k) y[u][k] = u < n ? 0.0f : -INFINITY;
-                const int pos = (seg.first + tl + u) * KV_TILE;
-                edge[u] = pos < clear_from || pos + KV_TILE > clear_to;
-                if (u >= n) continue;
-                const uint8_t* k8 = tile[u];
-                float c16[2][4] = {};
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    float c[2][4] = {};
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        uint32_t f[4];
-                        k_fragment<FMT>(k8, b, tile_token(g >> 1, 2 * j + (g & 1)), t, f);
-#pragma unroll
-                        for (int s = 0; s < 2; ++s) {
-                            uint32_t qa[4];
-                            if constexpr (Sh::Q_SMEM) {
-                                const uint4 w = q_smem[(b * 2 + s) * 32];
-                                qa[0] = w.x, qa[1] = w.y, qa[2] = w.z, qa[3] = w.w;
-                            } else {
-#pragma unroll
-                                for (int z = 0; z < 4; ++z) qa[z] = qf[b * 2 + s][z];
-                            }
-                            mma_f16(FMT == QGEMV_KV_F16 ? c16[j] : c[j], qa, f[2 * s], f[2 * s + 1]);
-                        }
-                    }
-                    if constexpr (FMT != QGEMV_KV_F16) {
-                        const uint2 w = *reinterpret_cast<const uint2*>(k8 + NB * KV_TILE * kv_code_bytes(FMT) + b * 32 + 8 * t);
-                        const float2 d01 = __half22float2(bits_h2(w.x)), d23 = __half22float2(bits_h2(w.y));
-                        const float d[4] = {d01.x, d01.y, d23.x, d23.y};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            if (TWO) {
-                                y[u][i] = fmaf(d[i], c[i >> 1][i & 1] + c[i >> 1][2 + (i & 1)], y[u][i]);
-                            } else {
-                                y[u][i] = fmaf(d[i], c[i >> 1][i & 1], y[u][i]);
-                                y[u][4 * (Sh::NR - 1) + i] = fmaf(d[i], c[i >> 1][2 + (i & 1)], y[u][4 * (Sh::NR - 1) + i]);
-                            }
-                        }
-                    }
-                }
-                if constexpr (FMT == QGEMV_KV_F16) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if (TWO) {
-                            y[u][i] = c16[i >> 1][i & 1] + c16[i >> 1][2 + (i & 1)];
-                        } else {
-                            y[u][i] = c16[i >> 1][i & 1];
-                            y[u][4 * (Sh::NR - 1) + i] = c16[i >> 1][2 + (i & 1)];
-                        }
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < 4 * Sh::NR; ++k) y[u][k] *= rs[k >> 2];
-                if (edge[u]) {
-#pragma unroll
-                    for (int k = 0; k < 4 * Sh::NR; ++k) {
-                        const int x = pos + tile_token(t, k & 3);
-                        if (x >= end[k >> 2] || x < begin[k >> 2]) {
-                            y[u][k] = -INFINITY;
-                            hidden |= 1u << (u * 8 + k);
-                        }
-                    }
-                }
-            }
-
-            // ---- V's scales and the largest of them, among tokens that any row sees
-            uint2 dv[FMT == QGEMV_KV_F16 ? 1 : 2][NB];
-            int e = st.e;
-            if constexpr (FMT != QGEMV_KV_F16) {
-                __half2 top = bits_h2(0u);
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    if (u >= n) continue;
-                    uint32_t live[2] = {0xffffffffu, 0xffffffffu};
-                    if (edge[u]) {
-                        const int pos = (seg.first + tl + u) * KV_TILE;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int x = pos + tile_token(t, i);
-                            if (x < sp.first() || x >= sp.last()) live[i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
-                        }
-                    }
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        uint2 w = *reinterpret_cast<const uint2*>(tile[u] + Sh::HALF + NB * KV_TILE * kv_code_bytes(FMT) +
-                                                                  b * 32 + 8 * t);
-                        w.x &= live[0], w.y &= live[1];
-                        dv[u][b] = w;
-                        top = __hmax2(top, __hmax2(__habs2(bits_h2(w.x)), __habs2(bits_h2(w.y))));
-                    }
-                }
-                uint32_t bits = max((uint32_t)__half_as_ushort(__low2half(top)), (uint32_t)__half_as_ushort(__high2half(top)));
-                bits = __reduce_max_sync(0xffffffffu, bits);
-                if (bits < 0x7c00u) e = max(e, (int)(bits >> 10));  // d_v < 2^(e - 14)
-            }
-
-            // ---- the running maximum; the sums are rescaled only where it or e grows
-            float mx[Sh::NR];
-            bool grow = e > st.e;
-#pragma unroll
-            for (int r = 0; r < Sh::NR; ++r) {
-                float v = -INFINITY;
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v = fmaxf(v, y[u][4 * r + i]);
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
-                mx[r] = v;
-                grow |= v > st.m[r];
-            }
-            if (__any_sync(0xffffffffu, grow)) {
-                const float down = __int_as_float((127 + st.e - e) << 23);
-                float f[Sh::NR];
-#pragma unroll
-                for (int r = 0; r < Sh::NR; ++r) {
-                    const float mn = fmaxf(st.m[r], mx[r]);
-                    f[r] = ex2(st.m[r] - st.base(mn));
-                    st.l[r] *= f[r];
-                    f[r] *= down;
-                    st.m[r] = mn;
-                }
-                st.e = e;
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int nn = 0; nn < 4; ++nn)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) st.o[b][nn][c] *= f[TWO ? 0 : c >> 1];
-            }
-#pragma unroll
-            for (int r = 0; r < Sh::NR; ++r) {
-                const float bs = st.base(st.m[r]);
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        y[u][4 * r + i] = ex2(y[u][4 * r + i] - bs);
-                        st.l[r] += y[u][4 * r + i];
-                    }
-            }
-
-            // ---- outputs
-            const float up = FMT == QGEMV_KV_F16 ? 0x1p14f : __int_as_float((127 + 28 - st.e) << 23);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                if (u >= n) continue;
-                const uint8_t* v8 = tile[u] + Sh::HALF;
-                uint32_t pa[4];
-                auto weights = [&](const float (&d)[4]) {
-                    float w[4 * Sh::NR];
-#pragma unroll
-                    for (int k = 0; k < 4 * Sh::NR; ++k) w[k] = y[u][k] * d[k & 3];
-                    if (edge[u]) {
-#pragma unroll
-                        for (int k = 0; k < 4 * Sh::NR; ++k)
-                            if (hidden >> (u * 8 + k) & 1) w[k] = 0.0f;
-                    }
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const __half2 h = __floats2half2_rn(w[2 * j], w[2 * j + 1]);
-                        pa[2 * j] = h2_bits(h);
-                        if (TWO) {
-                            const float2 f = __half22float2(h);
-                            pa[2 * j + 1] = h2_bits(__floats2half2_rn(w[2 * j] - f.x, w[2 * j + 1] - f.y));
-                        } else {
-                            pa[2 * j + 1] = h2_bits(__floats2half2_rn(w[4 * (Sh::NR - 1) + 2 * j], w[4 * (Sh::NR - 1) + 2 * j + 1]));
-                        }
-                    }
-                };
-                bool odd_values = false;  // f16 at the edge: infinities or NaN among the values that some row sees
-                uint32_t live[2] = {0xffffffffu, 0xffffffffu};
-                if constexpr (FMT == QGEMV_KV_F16) {
-                    const float one[4] = {up, up, up, up};
-                    weights(one);
-                    if (edge[u]) {
-                        const int pos = (seg.first + tl + u) * KV_TILE;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int x = pos + tile_token(t, i);
-                            if (x < sp.first() || x >= sp.last()) live[i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
-                        }
-                    }
-                }
-#pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    if constexpr (FMT != QGEMV_KV_F16) {
-                        const float2 d01 = __half22float2(bits_h2(dv[u][b].x)), d23 = __half22float2(bits_h2(dv[u][b].y));
-                        const float d[4] = {d01.x * up, d01.y * up, d23.x * up, d23.y * up};
-                        weights(d);
-                    }
-                    uint32_t lo[4], hi[4];
-                    v_fragments<FMT>(v8, b, g, t, lo, hi);
-                    if constexpr (FMT == QGEMV_KV_F16) {
-                        if (edge[u]) {
-#pragma unroll
-                            for (int nn = 0; nn < 4; ++nn) {
-                                lo[nn] &= live[0], hi[nn] &= live[1];
-                                auto finite = [&](uint32_t w) {
-                                    if ((w & 0x7c00u) == 0x7c00u) w &= 0xffff0000u, odd_values = true;
-                                    if ((w & 0x7c000000u) == 0x7c000000u) w &= 0x0000ffffu, odd_values = true;
-                                    return w;
-                                };
-                                lo[nn] = finite(lo[nn]), hi[nn] = finite(hi[nn]);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int nn = 0; nn < 4; ++nn) mma_f16(st.o[b][nn], pa, lo[nn], hi[nn]);
-                }
-                if constexpr (FMT == QGEMV_KV_F16) {
-                    // such values went in as zeros; add them to the rows that see them
-                    if (edge[u] && __any_sync(0xffffffffu, odd_values)) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            for (int tt = 0; tt < 4; ++tt) {
-                                const int tok = tile_token(tt, i);
-                                float w[Sh::NR];
-                                bool see[Sh::NR];
-#pragma unroll
-                                for (int r = 0; r < Sh::NR; ++r) {
-                                    w[r] = __shfl_sync(0xffffffffu, y[u][4 * r + i], (lane & 28) | tt) * up;
-                                    see[r] = !(__shfl_sync(0xffffffffu, hidden, (lane & 28) | tt) >> (u * 8 + 4 * r + i) & 1);
-                                }
-#pragma unroll
-                                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                                    for (int nn = 0; nn < 4; ++nn)
-#pragma unroll
-                                        for (int c = 0; c < 2; ++c) {
-                                            const float x = __half2float(reinterpret_cast<const __half*>(v8)[(b * KV_TILE + tok) * 32 + 4 * (2 * t + c) + nn]);
-                                            if (isfinite(x)) continue;
-#pragma unroll
-                                            for (int r = 0; r < Sh::NR; ++r)
-                                                if (see[r]) st.o[b][nn][2 * r + c] += w[r] * x;
-                                        }
-                            }
-                    }
-                }
+            if (!poison) {  // (a stage without its tile: the rows are NaN whatever comes)
+                if (x.n == STEP && x.pos >= clear_from && x.pos + STEP * KV_TILE <= clear_to)
+                    attn_step<FMT, NB, MODE, false>(st, x, qf, q_smem, begin, end, lane);
+                else
+                    attn_step<FMT, NB, MODE, true>(st, x, qf, q_smem, begin, end, lane);
             }
             __syncwarp();
             if (lane == 0)
-                for (int u = 0; u < n; ++u) mbar_arrive(done[u]);
+                for (int u = 0; u < x.n; ++u) mbar_arrive(&empty[used[u]]);
         }
         st.finish(poison || dead);
         if (dead && lane == 0) s_dead = 1;
 
-        // ---- the splits' partial results, in shared memory
-        auto meet = [&]() {
-            for (int k = p.ws; k > 1;) {
-                const int h = (k + 1) / 2;
-                float* buf = merge + (size_t)((split >= h ? split - h : split) * p.wr + wrow) * Sh::PART + lane;
-                __syncthreads();
-                if (split >= h && split < k) st.put([&](int i, float v) { buf[i * 32] = v; });
-                __syncthreads();
-                if (split < k - h) st.join([&](int i) { return buf[i * 32]; });
-                k = h;
-            }
-        };
-        auto write_out = [&]() {
+        if (seg.ta == 0 && seg.tb == seg.count) {
 #pragma unroll
-            for (int r = 0; r < Sh::NR; ++r) {
-                const int rr = row_tile * Sh::ROWS + g + 8 * r;
-                if (rr >= a.rows * a.group) continue;
-                const int i = rr / a.group;
-                const int64_t row = (int64_t)seg.b * a.rows + i;
-                const int head = kvh * a.group + rr - i * a.group;
-                const float inv = st.l[r] == 0.0f ? 0.0f : __fdiv_rn(1.0f, st.l[r]);
-                const bool none = st.l[r] == 0.0f;
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                    for (int r = 0; r < NR; ++r) {
                         float v[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            // q4_0: values 16 h + 4 t + k; else 8 t + 4 h + k
-                            const float x = FMT == QGEMV_KV_Q4_0 ? st.o[b][2 * (k & 1) + h][2 * r + (k >> 1)] : st.o[b][k][2 * r + h];
-                            v[k] = none ? 0.0f : x * inv;
-                        }
-                        const int d = b * 32 + (FMT == QGEMV_KV_Q4_0 ? 16 * h + 4 * t : 8 * t + 4 * h);
-                        store_row_part(a.out, row * a.o_row + head * a.o_head + d, p.type, o_wide, v);
+                        for (int k = 0; k < 4; ++k)
+                            v[k] = FMT == QGEMV_KV_Q4_0 ? st.o[b][2 * (k & 1) + h][2 * r + (k >> 1)] : st.o[b][k][2 * r + h];
+                        emit(seg.b, seg.item, wrow, b, h, r, v, st.m[r], st.l[r]);
                     }
-                if (a.lse && t == 0)
-                    a.lse[row * a.heads + head] = none ? -INFINITY : 0.6931471805599453f * st.m[r] + logf(st.l[r]);
+        } else {
+            const int which = n_seg > 0;
+            float* to = split_part(split, which, wrow);
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int c = 0; c < Sh::NC; ++c) __stcg(to + ((b * 4 + n) * Sh::NC + c) * 32, st.o[b][n][c]);
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                __stcg(to + (Sh::NO + r) * 32, st.m[r]);
+                __stcg(to + (Sh::NO + NR + r) * 32, st.l[r]);
             }
-        };
-        meet();
-        if (seg.ta == 0 && seg.tb == seg.count) {
-            if (split == 0) write_out();
-            continue;
+            if (wrow == 0 && lane == 0) s_left[2 * split + which] = {seg.line, seg.b, seg.item, seg.count, seg.ta, seg.tb};
         }
-        // ---- an item cut between CTAs
-        const int64_t chunk = s_chunk, here = chunk * blockIdx.x;
-        // the item's first tile in the line, and the CTAs that share it
-        const int64_t line = n_seg == 0 ? here - seg.ta : chunk * (blockIdx.x + 1) - seg.tb;
-        const int c0 = (int)(line / chunk), c1 = (int)((line + seg.count - 1) / chunk);
-        auto part = [&](int c) {
-            const int second = c == c0 && line != chunk * c;
-            return a.partials + ((size_t)(2 * c + second) * p.wr + wrow) * Sh::PART + lane;
-        };
-        if (split == 0) {
-            float* w = part(blockIdx.x);
-            st.put([&](int i, float v) { __stcg(w + i * 32, v); });
-            __threadfence();
-        }
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            const unsigned int before = atomicAdd(&a.counters[c0], 1u);
-            s_last = before == (unsigned)(c1 - c0);
-            if (s_last) a.counters[c0] = 0;
-            __threadfence();
-        }
-        __syncthreads();
-        if (!s_last) continue;
-        st.clear();
-        for (int c = c0 + split; c <= c1; c += p.ws) {
-            const float* w = part(c);
-            st.join([&](int i) { return __ldcg(w + i * 32); });
-        }
-        meet();
-        if (split == 0) write_out();
     }
 
-    if (issuer && dead) {  // copies of its own that it did not wait for
-        for (int q = taken < 2 ? 0 : taken - 2; q < issued; ++q) mbar_wait_bounded(&full[q % S], (q / S) & 1);
+    // ---- the items that splits share.  A unit of the work is four consecutive
+    // values of a row: block b, half h, row g + 8 r of a row tile.
+    constexpr int UNITS = NB * 2 * NR;
+    auto place = [](int b, int h, int r, int k) {  // value k of it among a lane's outputs
+        return FMT == QGEMV_KV_Q4_0 ? (b * 4 + 2 * (k & 1) + h) * Sh::NC + 2 * r + (k >> 1)
+                                    : (b * 4 + k) * Sh::NC + 2 * r + h;
+    };
+    // the sum of partial results from(0) .. from(n - 1) of the rows of unit w
+    auto join = [&](int n, int w, auto from, float (&v)[4], float& m, float& l) {
+        const int r = w % NR, h = w / NR % 2, b = w / (2 * NR);
+        m = -INFINITY;
+        l = v[0] = v[1] = v[2] = v[3] = 0.0f;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float* q = from(i);
+            const float m2 = __ldcg(q + (Sh::NO + r) * 32), l2 = __ldcg(q + (Sh::NO + NR + r) * 32);
+            const float mn = fmaxf(m, m2), bs = attn_base(mn), f1 = ex2(m - bs), f2 = ex2(m2 - bs);
+            m = mn;
+            l = l * f1 + l2 * f2;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = v[k] * f1 + __ldcg(q + place(b, h, r, k) * 32) * f2;
+        }
+    };
+    meet();
+    AttnLeft cut[2];  // those that go on in other CTAs: before this one, after it
+    cut[0].line = cut[1].line = -1;
+    for (int i = 0; i < 2 * p.ws;) {
+        AttnLeft x = s_left[i];
+        if (x.line < 0) {
+            ++i;
+            continue;
+        }
+        // its partial results in this CTA: entry i, then the first ones of the splits that follow
+        int n = 1;
+        for (int k = i + 1; k < 2 * p.ws; ++k) {
+            if (s_left[k].line < 0) continue;
+            if (s_left[k].line != x.line) break;
+            x.tb = s_left[k].tb;
+            ++n;
+        }
+        const bool whole = x.ta == 0 && x.tb == x.count;
+        const int after = x.ta == 0;  // only what lies before this CTA's piece is missing otherwise
+        for (int unit = warp; unit < p.wr * UNITS; unit += warps) {
+            const int tile = unit / UNITS, w = unit - tile * UNITS, r = w % NR, h = w / NR % 2, b = w / (2 * NR);
+            float v[4], m, l;
+            join(n, w, [&](int k) { return k == 0 ? split_part(i >> 1, i & 1, tile) : split_part((i >> 1) + k, 0, tile); }, v, m, l);
+            if (whole) {
+                emit(x.b, x.item, tile, b, h, r, v, m, l);
+            } else {
+                float* to = cta_part(blockIdx.x, after, tile);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) __stcg(to + place(b, h, r, k) * 32, v[k]);
+                if (b == 0 && h == 0) {
+                    __stcg(to + (Sh::NO + r) * 32, m);
+                    __stcg(to + (Sh::NO + NR + r) * 32, l);
+                }
+            }
+        }
+        if (!whole) cut[after] = x;
+        // on to the first entry of another item
+        for (++i; i < 2 * p.ws && (s_left[i].line < 0 || s_left[i].line == x.line); ++i) {}
     }
-    __syncthreads();
+    // ---- the items that CTAs share: the last one joins the partial results
+    auto first_cta = [&](const AttnLeft& x) { return (int)((x.line + ATTN_ITEM_COST) / chunk); };
+    auto last_cta = [&](const AttnLeft& x) { return (int)((x.line + ATTN_ITEM_COST + x.count - 1) / chunk); };
+    if (cut[0].line >= 0 || cut[1].line >= 0) {
+        __threadfence();
+        meet();
+        if (threadIdx.x < 2) {
+            const AttnLeft& x = cut[threadIdx.x];
+            int last = 0;
+            if (x.line >= 0) {
+                const int c0 = first_cta(x);
+                last = atomicAdd(&a.counters[c0], 1u) == (unsigned)(last_cta(x) - c0);
+                if (last) a.counters[c0] = 0;
+                __threadfence();
+            }
+            s_last[threadIdx.x] = last;
+        }
+        meet();
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (!s_last[k]) continue;
+            const AttnLeft& x = cut[k];
+            const int c0 = first_cta(x), n = last_cta(x) - c0 + 1;
+            for (int unit = warp; unit < p.wr * UNITS; unit += warps) {
+                const int tile = unit / UNITS, w = unit - tile * UNITS, r = w % NR, h = w / NR % 2, b = w / (2 * NR);
+                float v[4], m, l;
+                join(n, w, [&](int c) { return cta_part(c0 + c, c == 0, tile); }, v, m, l);
+                emit(x.b, x.item, tile, b, h, r, v, m, l);
+            }
+        }
+    }
+    meet();
     if (threadIdx.x == 0 && s_dead) atomicAdd_system(status, 1u);
 }
 
-template <int FMT, int NB, bool TWO>
+template <int FMT, int NB, int MODE>
 AttnPlan attn_plan(const DeviceInfo& di, int type, int rows)
 {
-    using Sh = AttnShape<FMT, NB, TWO>;
+    using Sh = AttnShape<FMT, NB, MODE>;
     AttnPlan p{};
     p.type = type;
-    p.row_tiles = (rows + Sh::ROWS - 1) / Sh::ROWS;
-    p.row_groups = (p.row_tiles + Sh::MAX_WARPS - 1) / Sh::MAX_WARPS;
-    p.wr = (p.row_tiles + p.row_groups - 1) / p.row_groups;
-    p.ws = Sh::MAX_WARPS / p.wr;
-    for (;; --p.ws) {
-        const uint32_t merge = (uint32_t)(p.ws / 2) * p.wr * Sh::PART * 4;
-        const uint32_t q = Sh::Q_SMEM ? (uint32_t)p.wr * NB * 2 * 32 * 16 : 0;
+    const int tiles = (rows + Sh::ROWS - 1) / Sh::ROWS;
+    p.row_groups = (tiles + Sh::WARPS - 1) / Sh::WARPS;
+    p.wr = (tiles + p.row_groups - 1) / p.row_groups;
+    for (p.ws = Sh::WARPS / p.wr; p.ws > 0; --p.ws) {
+        const uint32_t q = Sh::Q_SMEM ? (uint32_t)p.ws * p.wr * NB * 2 * Sh::Q_TERMS * 512 : 0;
         const uint32_t per_stage = (uint32_t)p.ws * (Sh::TILE + 2 * 8 + 4);
-        const uint32_t fixed = merge + q + 256;
-        const uint32_t budget = (uint32_t)di.smem_optin - 1024;
-        const int stages = budget > fixed ? (int)((budget - fixed) / per_stage) : 0;
-        if (stages < 4 && p.ws > 1) continue;
+        const uint32_t budget = (uint32_t)di.smem_optin - 2048;  // beside the static shared memory
+        const int stages = budget > q ? (int)((budget - q) / per_stage) : 0;
+        if (stages < 3 && p.ws > 1) continue;
         p.stages = stages > 8 ? 8 : stages;
-        p.off_merge = (uint32_t)p.ws * p.stages * Sh::TILE;
-        p.off_q = p.off_merge + merge;
+        p.off_q = (uint32_t)p.ws * p.stages * Sh::TILE;
         p.off_bar = p.off_q + q;
         p.bytes = p.off_bar + (uint32_t)p.ws * p.stages * 20;
         break;
     }
-    p.min_chunk = 2 * p.ws;
     return p;
 }
 
-template <int FMT, int NB, bool TWO>
+template <int FMT, int NB, int MODE>
 int launch_attn_split(int type, const AttnArgs& a, cudaStream_t s)
 {
+    using Sh = AttnShape<FMT, NB, MODE>;
     const DeviceInfo di = device_info();
     if (di.sms <= 0) return QGEMV_CUDA_ERROR;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return QGEMV_CUDA_ERROR;
-    const AttnPlan p = attn_plan<FMT, NB, TWO>(di, type, a.rows * a.group);
-    if (p.stages < 2) return QGEMV_UNSUPPORTED_SHAPE;
-    auto kern = attn_split_kernel<FMT, NB, TWO>;
+    const AttnPlan p = attn_plan<FMT, NB, MODE>(di, type, a.rows * a.group);
+    if (p.stages < Sh::STEP) return QGEMV_UNSUPPORTED_SHAPE;
+    auto kern = attn_split_kernel<FMT, NB, MODE>;
     static std::once_flag once[64];
     static bool ok[64];
     std::call_once(once[dev], [&]() {
-        ok[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, di.smem_optin - 1024) ==
+        ok[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, di.smem_optin - 2048) ==
                       cudaSuccess &&
                   wait_timeout_counter() != nullptr;
         if (!ok[dev]) cudaGetLastError();
     });
     if (!ok[dev]) return QGEMV_CUDA_ERROR;
     const int grid = di.sms < ATTN_GRID ? di.sms : ATTN_GRID;
-    if (launch_pdl(kern, dim3(grid), dim3(p.ws * p.wr * 32), p.bytes, s, a, p, wait_timeout_counter()) != cudaSuccess)
+    if (launch_pdl(kern, dim3(grid), dim3((p.ws * p.wr + 1) * 32), p.bytes, s, a, p, wait_timeout_counter()) != cudaSuccess)
         return QGEMV_CUDA_ERROR;
     return cudaGetLastError() == cudaSuccess ? QGEMV_OK : QGEMV_CUDA_ERROR;
 }
 
-template <int FMT, bool TWO>
+template <int FMT, int MODE>
 int launch_attn_dim(int type, const AttnArgs& a, cudaStream_t s)
 {
     switch (a.L.nb) {
-    case 2: return launch_attn_split<FMT, 2, TWO>(type, a, s);
-    case 3: return launch_attn_split<FMT, 3, TWO>(type, a, s);
-    case 4: return launch_attn_split<FMT, 4, TWO>(type, a, s);
-    default: return launch_attn_split<FMT, 8, TWO>(type, a, s);
+    case 2: return launch_attn_split<FMT, 2, MODE>(type, a, s);
+    case 3: return launch_attn_split<FMT, 3, MODE>(type, a, s);
+    case 4: return launch_attn_split<FMT, 4, MODE>(type, a, s);
+    default: return launch_attn_split<FMT, 8, MODE>(type, a, s);
     }
 }
 
 template <int FMT>
 int launch_attn_type(int type, const AttnArgs& a, cudaStream_t s)
 {
-    return type == QGEMV_BF16 ? launch_attn_dim<FMT, false>(type, a, s) : launch_attn_dim<FMT, true>(type, a, s);
+    switch (attn_mode(type, a.rows * a.group)) {
+    case ATTN_ONE: return launch_attn_dim<FMT, ATTN_ONE>(type, a, s);
+    case ATTN_PAIR: return launch_attn_dim<FMT, ATTN_PAIR>(type, a, s);
+    default: return launch_attn_dim<FMT, ATTN_TWO>(type, a, s);
+    }
 }
 
 int launch_attn_f16(int type, const AttnArgs& a, cudaStream_t s);

@@ -21,10 +21,11 @@ int check_layout(int fmt, int page_tokens, int n_kv_heads, int head_dim)
     return QGEMV_OK;
 }
 
-// the whole cache, and so every offset in it, within 62 bits
-bool pages_fit(int64_t n_pages, size_t page_bytes)
+// so that every offset in the cache is within 62 bits (a token of a cache has at
+// most 2^21 bytes)
+bool pages_fit(int64_t n_pages, int page_tokens)
 {
-    return n_pages >= 1 && (uint64_t)n_pages <= (UINT64_C(1) << 62) / page_bytes;
+    return n_pages >= 1 && n_pages <= KV_MAX_SLOTS / page_tokens;
 }
 
 int check_type(int type) { return type == QGEMV_F32 || type == QGEMV_F16 || type == QGEMV_BF16 ? QGEMV_OK : QGEMV_INVALID_ARG; }
@@ -41,7 +42,7 @@ int kv_call(bool write, int fmt, int type, const void* k, int64_t k_token, int64
     st = check_type(type);
     if (st) return st;
     if (k_token < 0 || k_head < 0 || v_token < 0 || v_head < 0) return QGEMV_INVALID_ARG;
-    if (!pages_fit(n_pages, kv_page_bytes(fmt, page_tokens, n_kv_heads, head_dim))) return QGEMV_INVALID_ARG;
+    if (!pages_fit(n_pages, page_tokens)) return QGEMV_INVALID_ARG;
     if (!aligned_to(cache, 16) || !aligned_to(slots, 8) || !aligned_to(k, type_bytes(type)) ||
         !aligned_to(v, type_bytes(type)))
         return QGEMV_MISALIGNED;
@@ -70,7 +71,7 @@ size_t kv_page_bytes(int fmt, int page_tokens, int n_kv_heads, int head_dim)
 int64_t kv_tile_offset(int fmt, int64_t n_pages, int page_tokens, int n_kv_heads, int head_dim, int64_t slot, int head)
 {
     const size_t page = kv_page_bytes(fmt, page_tokens, n_kv_heads, head_dim);
-    if (!page || !pages_fit(n_pages, page)) return -1;
+    if (!page || !pages_fit(n_pages, page_tokens)) return -1;
     return kv_layout(fmt, n_pages, page_tokens, n_kv_heads, head_dim).slot_offset(slot, head);
 }
 
@@ -116,7 +117,7 @@ int attn_paged(int fmt, int type, const void* q, int64_t q_row, int64_t q_head, 
     if (rows > QGEMV_MAX_M || n_heads % n_kv_heads ||
         (head_dim != 64 && head_dim != 96 && head_dim != 128 && head_dim != 256))
         return QGEMV_UNSUPPORTED_SHAPE;
-    if (!pages_fit(n_pages, kv_page_bytes(fmt, page_tokens, n_kv_heads, head_dim)) ||
+    if (!pages_fit(n_pages, page_tokens) ||
         (int64_t)max_pages * page_tokens > (INT64_C(1) << 30))
         return QGEMV_INVALID_ARG;
     if (ws_bytes < attn_paged_workspace_bytes(type, rows, n_heads, n_kv_heads, head_dim))

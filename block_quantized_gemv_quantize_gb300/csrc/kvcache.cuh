@@ -11,6 +11,7 @@ namespace qgemv {
 
 constexpr int KV_TILE = 16;  // tokens per tile
 constexpr int KV_MAX_PAGE = 1024, KV_MAX_HEADS = 1024, KV_MAX_DIM = 512;
+constexpr int64_t KV_MAX_SLOTS = INT64_C(1) << 35;
 
 // Bytes of one block's codes (32 values of one token) and of its scale.
 __host__ __device__ constexpr int kv_code_bytes(int fmt)
@@ -42,12 +43,23 @@ struct KvLayout {
         if (page < 0 || page >= n_pages || h < 0 || h >= heads || t < 0 || t >= tiles()) return -1;
         return ((page * heads + h) * tiles() + t) * (int64_t)tile_bytes;
     }
-    // of the tile that holds a slot
-    __host__ __device__ int64_t slot_offset(int64_t slot, int h) const
+    // Where a slot is; page -1 outside the cache.  A cache has at most
+    // KV_MAX_SLOTS of them, so that its tiles count in 31 bits.
+    struct Slot {
+        int64_t page;
+        int tile, row;
+    };
+    __host__ __device__ Slot slot(int64_t s) const
     {
-        if (slot < 0) return -1;
-        const int64_t page = slot / page_tokens;
-        return tile_offset(page, h, (int)(slot - page * page_tokens) / KV_TILE);
+        if (s < 0 || s >= n_pages * page_tokens) return {-1, 0, 0};
+        const uint32_t tile = (uint32_t)(s / KV_TILE), page = tile / (uint32_t)tiles();
+        return {page, (int)(tile - page * (uint32_t)tiles()), (int)(s & (KV_TILE - 1))};
+    }
+    // byte offset of the tile that holds a slot
+    __host__ __device__ int64_t slot_offset(int64_t s, int h) const
+    {
+        const Slot at = slot(s);
+        return tile_offset(at.page, h, at.tile);
     }
 };
 

@@ -487,7 +487,8 @@ int qgemv_q5_k_plan(int M, int K, int N, int* info);
  * with d, x / d and x / d + 8.5 in fp32.  The stored scale is d rounded to
  * fp16, at most 65504 in magnitude; a block that holds a NaN or an infinity
  * gets the scale NaN, so that all of it reads as NaN.
- * A token's place in the cache is its slot, page * page_tokens + offset. */
+ * A token's place in the cache is its slot, page * page_tokens + offset; a
+ * cache has at most 2^35 of them. */
 #define QGEMV_KV_F16 0
 #define QGEMV_KV_Q8_0 1
 #define QGEMV_KV_Q4_0 2

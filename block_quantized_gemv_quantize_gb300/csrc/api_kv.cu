@@ -146,8 +146,8 @@ int attn_paged(int fmt, int type, const void* q, int64_t q_row, int64_t q_head, 
     a.group = n_heads / n_kv_heads;
     a.scale = scale;
     a.window = window;
-    a.counters = static_cast<unsigned int*>(workspace);
-    a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ATTN_COUNTER_BYTES);
+    a.records = static_cast<AttnRecord*>(workspace);
+    a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + ATTN_RECORD_BYTES);
     return launch_attn_paged(fmt, type, a, static_cast<cudaStream_t>(stream));
 }
 

@@ -31,17 +31,20 @@
 // and WR warps share the ring, one for every tile of rows.  One more warp issues
 // the copies, a lane a ring.  A split writes the outputs of an item that it has
 // whole; of one that it shares it leaves a partial result (at most two) in the
-// workspace.  At the end the CTA joins those of its splits, once; an item that
-// is cut between CTAs leaves one partial result a CTA, and the CTA that finds
-// itself last (a counter) joins them in CTA order, so that the result does not
-// depend on the order in which CTAs finish.
+// workspace, and the split that has the item's first tile leaves its record.  A
+// second kernel joins the partial results of every recorded item, each output by
+// as many warps as there are to spare, in the order of the splits: the result
+// does not depend on the order in which CTAs finish.
 #pragma once
+
+#include <type_traits>
 
 #include "kvcache.cuh"
 
 namespace qgemv {
 
 constexpr int ATTN_GRID = 160;     // most CTAs (one an SM): the workspace holds their partial results
+constexpr int ATTN_JOIN_WARPS = 16;  // of a CTA of the joining kernel
 constexpr int ATTN_ITEM_COST = 4;  // of an item besides its tiles, in tiles
 constexpr int ATTN_MIN_PIECE = 4;  // least units of a split: shorter ones cost more to join than they save
 
@@ -51,10 +54,7 @@ enum AttnMode { ATTN_ONE = 0, ATTN_PAIR = 1, ATTN_TWO = 2 };
 inline int attn_mode(int type, int rows) { return type == QGEMV_BF16 ? ATTN_ONE : (rows > 8 ? ATTN_TWO : ATTN_PAIR); }
 
 // Warps that compute (one more copies): as many as 64 K registers hold.
-#ifndef AW
-#define AW 7
-#endif
-__host__ __device__ constexpr int attn_warps(int nb) { return nb > 4 ? 7 : AW; }
+__host__ __device__ constexpr int attn_warps(int nb) { return 7; }
 
 template <int FMT, int NB, int MODE>
 struct AttnShape {
@@ -67,11 +67,18 @@ struct AttnShape {
     static constexpr bool Q_SMEM = NB > 4 || MODE == ATTN_TWO;  // else q's fragments stay in registers
     static constexpr int Q_TERMS = MODE == ATTN_TWO ? 2 : 1;
     static constexpr int WARPS = attn_warps(NB);
-    static constexpr int STEP = 2;                           // tiles a split takes at a time
+    static constexpr int UNITS = NB * 2 * NR;                // runs of four output values of a lane
+    // where value k of the run (block b, half h, row g + 8 r) stands among a lane's outputs
+    __host__ __device__ static constexpr int place(int b, int h, int r, int k)
+    {
+        return FMT == QGEMV_KV_Q4_0 ? (b * 4 + 2 * (k & 1) + h) * NC + 2 * r + (k >> 1) : (b * 4 + k) * NC + 2 * r + h;
+    }
+    // and the first of them in the row, for lane column t
+    __device__ static int column(int b, int h, int t) { return b * 32 + (FMT == QGEMV_KV_Q4_0 ? 16 * h + 4 * t : 8 * t + 4 * h); }
 };
 
 struct AttnPlan {
-    int type;
+    int splits;          // of the whole grid
     int ws, wr;          // splits, row tiles at a time
     int row_groups;
     int stages;          // tiles a ring holds
@@ -277,28 +284,6 @@ __device__ __forceinline__ AttnWalk attn_find(const AttnArgs& a, int items, int6
     return w;
 }
 
-template <int N>
-__device__ __forceinline__ void load_row_part(const void* p, int64_t at, int type, bool wide, float (&v)[N])
-{
-    if (type == QGEMV_F32) load_values(static_cast<const float*>(p) + at, wide, v);
-    else if (type == QGEMV_F16) load_values(static_cast<const __half*>(p) + at, wide, v);
-    else load_values(static_cast<const __nv_bfloat16*>(p) + at, wide, v);
-}
-
-template <int N>
-__device__ __forceinline__ void store_row_part(void* p, int64_t at, int type, bool wide, const float (&v)[N])
-{
-    if (type == QGEMV_F32) store_values(static_cast<float*>(p) + at, wide, v);
-    else if (type == QGEMV_F16) store_values(static_cast<__half*>(p) + at, wide, v);
-    else store_values(static_cast<__nv_bfloat16*>(p) + at, wide, v);
-}
-
-__device__ __forceinline__ bool rows_wide(const void* p, int64_t row, int64_t head, int type)
-{
-    const KvRows r{const_cast<void*>(p), row, head};
-    return type == QGEMV_F32 ? r.wide<float>() : r.wide<__half>();
-}
-
 // The fp16 pair hi + lo of two fp32 values.
 __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint32_t& lo)
 {
@@ -362,13 +347,12 @@ __device__ __forceinline__ float attn_base(float m) { return m == -INFINITY ? 0.
 // What one step needs to know of its tiles.
 struct AttnStep {
     const uint8_t* tile[2];
-    int n;            // tiles, 1 or 2 (2 without EDGE)
     int pos;          // position of the first tile's first token
     int first, last;  // positions that any row sees
 };
 
-// STEP tiles of a split into a warp's row tile.  EDGE: some tokens are hidden
-// from some rows, or there is one tile only.
+// Two tiles of a split into a warp's row tile; or (EDGE) one, of which some
+// tokens may be hidden from some rows.
 template <int FMT, int NB, int MODE, bool EDGE>
 __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const AttnStep& x,
                                           const uint32_t (&qf)[AttnShape<FMT, NB, MODE>::Q_SMEM ? 1 : NB * 2][4],
@@ -376,16 +360,16 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
                                           const int (&end)[AttnShape<FMT, NB, MODE>::NR], int lane)
 {
     using Sh = AttnShape<FMT, NB, MODE>;
-    constexpr int NR = Sh::NR, NV = 4 * NR, SCALES = NB * KV_TILE * kv_code_bytes(FMT);
+    constexpr int NT = EDGE ? 1 : 2, NR = Sh::NR, NV = 4 * NR, SCALES = NB * KV_TILE * kv_code_bytes(FMT);
     const int g = lane >> 2, t = lane & 3;
 
     // ---- scores: y[u][4 r + i], row g + 8 r, token i of the lane's column pairs
-    float y[2][NV];
+    float y[NT][NV];
 #pragma unroll
-    for (int u = 0; u < 2; ++u)
+    for (int u = 0; u < NT; ++u)
 #pragma unroll
         for (int k = 0; k < NV; ++k) y[u][k] = 0.0f;
-    float c16[2][2][4] = {};
+    float c16[NT][2][4] = {};
     // the tiles u0 .. u1 - 1 of block b: both at once where that halves the loads
     // of q's fragments, else one after the other, which needs fewer registers
     auto block = [&](int b, int u0, int u1) {
@@ -393,7 +377,6 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
         uint32_t f[2][2][4];
 #pragma unroll
         for (int u = u0; u < u1; ++u) {
-            if (EDGE && u >= x.n) continue;
 #pragma unroll
             for (int j = 0; j < 2; ++j) k_fragment<FMT>(x.tile[u], b, tile_token(g >> 1, 2 * j + (g & 1)), t, f[u][j]);
         }
@@ -411,8 +394,7 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
                 }
 #pragma unroll
                 for (int u = u0; u < u1; ++u) {
-                    if (EDGE && u >= x.n) continue;
-#pragma unroll
+        #pragma unroll
                     for (int j = 0; j < 2; ++j)
                         mma_f16(FMT == QGEMV_KV_F16 ? c16[u][j] : c[u][j], qa, f[u][j][2 * s], f[u][j][2 * s + 1]);
                 }
@@ -420,8 +402,7 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
         if constexpr (FMT != QGEMV_KV_F16) {
 #pragma unroll
             for (int u = u0; u < u1; ++u) {
-                if (EDGE && u >= x.n) continue;
-                const uint2 w = *reinterpret_cast<const uint2*>(x.tile[u] + SCALES + b * 32 + 8 * t);
+                    const uint2 w = *reinterpret_cast<const uint2*>(x.tile[u] + SCALES + b * 32 + 8 * t);
                 const float2 d[2] = {__half22float2(bits_h2(w.x)), __half22float2(bits_h2(w.y))};
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -435,16 +416,16 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
     };
     if constexpr (Sh::Q_SMEM) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b) block(b, 0, 2);
+        for (int b = 0; b < NB; ++b) block(b, 0, NT);
     } else {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < NT; ++u)
 #pragma unroll
             for (int b = 0; b < NB; ++b) block(b, u, u + 1);
     }
     uint32_t hidden = 0;  // bit 8 u + k: y[u][k] is masked
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+    for (int u = 0; u < NT; ++u) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -460,7 +441,7 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
 #pragma unroll
             for (int k = 0; k < NV; ++k) {
                 const int p = x.pos + u * KV_TILE + tile_token(t, k & 3);
-                if (u >= x.n || p >= end[k >> 2] || p < begin[k >> 2]) {
+                if (p >= end[k >> 2] || p < begin[k >> 2]) {
                     y[u][k] = -INFINITY;
                     hidden |= 1u << (u * 8 + k);
                 }
@@ -468,14 +449,16 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
         }
     }
     // tokens that no row sees: their scales and values are anything
-    uint32_t live[2][2] = {{~0u, ~0u}, {~0u, ~0u}};
+    uint32_t live[NT][2];
+#pragma unroll
+    for (int u = 0; u < NT; ++u) live[u][0] = live[u][1] = ~0u;
     if constexpr (EDGE) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < NT; ++u)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int p = x.pos + u * KV_TILE + tile_token(t, i);
-                if (u >= x.n || p < x.first || p >= x.last) live[u][i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
+                if (p < x.first || p >= x.last) live[u][i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
             }
     }
 
@@ -484,8 +467,7 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
     if constexpr (FMT != QGEMV_KV_F16) {
         __half2 top = bits_h2(0u);  // hmax2 takes the number of a number and a NaN
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            if (EDGE && u >= x.n) continue;
+        for (int u = 0; u < NT; ++u) {
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 uint2 w = *reinterpret_cast<const uint2*>(x.tile[u] + Sh::HALF + SCALES + b * 32 + 8 * t);
@@ -507,7 +489,7 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
     for (int r = 0; r < NR; ++r) {
         float v = y[0][4 * r];
 #pragma unroll
-        for (int k = 1; k < 8; ++k) v = fmaxf(v, y[k >> 2][4 * r + (k & 3)]);
+        for (int k = 1; k < 4 * NT; ++k) v = fmaxf(v, y[k >> 2][4 * r + (k & 3)]);
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 1));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 2));
         mx[r] = v;
@@ -539,7 +521,7 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
         const float bs = -attn_base(st.m[r]);
         float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < NT; ++u)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 float &v0 = y[u][4 * r + 2 * j], &v1 = y[u][4 * r + 2 * j + 1];
@@ -554,8 +536,7 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
 
     // ---- outputs
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        if (EDGE && u >= x.n) continue;
+    for (int u = 0; u < NT; ++u) {
         const uint8_t* v8 = x.tile[u] + Sh::HALF;
         uint32_t hi[4], lo[4];  // A fragments; ATTN_PAIR: hi alone, with the low terms in its upper rows
         auto weights = [&](const float2 (&d)[2]) {
@@ -645,22 +626,47 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
     }
 }
 
-// What a split leaves in the workspace of an item that it shares.
-struct AttnLeft {
-    int64_t line;  // the item's first unit; -1: nothing
-    int b, item, count, ta, tb;
+// What the split that has a shared item's first tile leaves of it.
+struct AttnRecord {
+    int parts;    // partial results, from this split's on; 0: none
+    int b, item;  // sequence, (kv head, row group) within it
 };
 
-template <int FMT, int NB, int MODE>
+__device__ __forceinline__ float* attn_part(const AttnArgs& a, const AttnPlan& p, int split, int which, int tile, int floats)
+{
+    return a.partials + (((size_t)split * 2 + which) * p.wr + tile) * floats;
+}
+
+// A row's four values of one run, normalised; and with the first run its
+// log-sum-exp.
+template <int FMT, int NB, int MODE, typename T>
+__device__ __forceinline__ void attn_emit(const AttnArgs& a, const AttnPlan& p, bool wide, int b_seq, int item, int tile,
+                                          int b, int h, int r, int lane, const float (&v)[4], float m, float l)
+{
+    using Sh = AttnShape<FMT, NB, MODE>;
+    const int g = lane >> 2, t = lane & 3, kvh = item / p.row_groups;
+    const int rr = ((item - kvh * p.row_groups) * p.wr + tile) * Sh::ROWS + g + 8 * r;
+    if (rr >= a.rows * a.group) return;
+    const int i = rr / a.group;
+    const int64_t row = (int64_t)b_seq * a.rows + i;
+    const int head = kvh * a.group + rr - i * a.group;
+    const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
+    float o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] = l == 0.0f ? 0.0f : v[k] * inv;
+    store_values(static_cast<T*>(a.out) + row * a.o_row + head * a.o_head + Sh::column(b, h, t), wide, o);
+    if (a.lse && t == 0 && b == 0 && h == 0)
+        a.lse[row * a.heads + head] = l == 0.0f ? -INFINITY : 0.6931471805599453f * m + logf(l);
+}
+
+template <int FMT, int NB, int MODE, typename T>
 __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
     attn_split_kernel(const AttnArgs a, const AttnPlan p, unsigned int* status)
 {
     using Sh = AttnShape<FMT, NB, MODE>;
-    constexpr int STEP = Sh::STEP, NR = Sh::NR;
+    constexpr int NR = Sh::NR;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ AttnWalk s_walk[Sh::WARPS];
-    __shared__ AttnLeft s_left[2 * Sh::WARPS];
-    __shared__ int s_last[2], s_dead;
 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -680,22 +686,21 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
         }
         fence_barrier_init();
     }
-    if (threadIdx.x == 0) s_dead = 0;
     pdl_wait();
 
     // the line, and this split's piece of it
     const int64_t total = attn_total(a, items, lane);
-    int64_t piece = (total + (int64_t)gridDim.x * p.ws - 1) / ((int64_t)gridDim.x * p.ws);
+    int64_t piece = (total + p.splits - 1) / p.splits;
     if (piece < ATTN_MIN_PIECE) piece = ATTN_MIN_PIECE;
-    const int64_t chunk = piece * p.ws;  // the CTA's
+    const int split_id = blockIdx.x * p.ws + split;
     AttnWalk seg{};
     if (warp < warps) {
-        const int64_t start = chunk * blockIdx.x + piece * split;
+        const int64_t start = piece * split_id;
         seg = attn_find(a, items, start, total - start < piece ? total - start : piece, lane);
         if (wrow == 0 && lane == 0) s_walk[split] = seg;
-        if (wrow == 0 && lane < 2) s_left[2 * split + lane].line = -1;
     }
     // sequences of which no row sees anything: zeros (NaN where the length is bad)
+    const bool o_wide = KvRows{a.out, a.o_row, a.o_head}.wide<T>();
     for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
         const AttnSpan sp(a, a.lens[b]);
         if (AttnTiles(sp).count) continue;
@@ -705,11 +710,10 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
             const int rh = i / (NB * 8), d = (i - rh * (NB * 8)) * 4;
             const int64_t row = (int64_t)b * a.rows + rh / a.heads;
             const int head = rh % a.heads;
-            store_row_part(a.out, row * a.o_row + head * a.o_head + d, p.type, false, none);
+            store_values(static_cast<T*>(a.out) + row * a.o_row + head * a.o_head + d, o_wide, none);
             if (a.lse && d == 0) a.lse[row * a.heads + head] = sp.bad ? v : -INFINITY;
         }
     }
-    if (chunk * blockIdx.x >= total) return;
     __syncthreads();
 
     if (warp == warps) {
@@ -761,40 +765,15 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
     }
 
     // ---- the warps that compute
-    auto meet = [&]() { asm volatile("bar.sync 1, %0;" ::"r"(warps * 32) : "memory"); };
     const uint8_t* ring = smem + (size_t)split * S * Sh::TILE;
     uint4* q_smem = reinterpret_cast<uint4*>(smem + p.off_q) + warp * (NB * 2 * Sh::Q_TERMS * 32) + lane;
-    const bool q_wide = rows_wide(a.q, a.q_row, a.q_head, p.type);
-    const bool o_wide = rows_wide(a.out, a.o_row, a.o_head, p.type);
-    // the partial results: of split s of this CTA, and of CTA c
-    auto split_part = [&](int s, int which, int tile) {
-        return a.partials + (((size_t)blockIdx.x * p.ws + s) * 2 + which) * p.wr * Sh::PART + (size_t)tile * Sh::PART + lane;
-    };
-    auto cta_part = [&](int c, int which, int tile) {
-        return a.partials + ((size_t)gridDim.x * p.ws * 2 + 2 * c + which) * p.wr * Sh::PART + (size_t)tile * Sh::PART + lane;
-    };
-    // a row's four values from d on, normalised
-    auto emit = [&](int b_seq, int item, int tile, int b, int h, int r, const float (&v)[4], float m, float l) {
-        const int kvh = item / p.row_groups;
-        const int rr = ((item - kvh * p.row_groups) * p.wr + tile) * Sh::ROWS + g + 8 * r;
-        if (rr >= a.rows * a.group) return;
-        const int i = rr / a.group;
-        const int64_t row = (int64_t)b_seq * a.rows + i;
-        const int head = kvh * a.group + rr - i * a.group;
-        const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-        float o[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = l == 0.0f ? 0.0f : v[k] * inv;
-        const int d = b * 32 + (FMT == QGEMV_KV_Q4_0 ? 16 * h + 4 * t : 8 * t + 4 * h);
-        store_row_part(a.out, row * a.o_row + head * a.o_head + d, p.type, o_wide, o);
-        if (a.lse && t == 0 && b == 0 && h == 0)
-            a.lse[row * a.heads + head] = l == 0.0f ? -INFINITY : 0.6931471805599453f * m + logf(l);
-    };
-    int slot = 0, phase = 0, n_seg = 0;
+    const bool q_wide = KvRows{const_cast<void*>(a.q), a.q_row, a.q_head}.wide<T>();
+    int slot = 0, phase = 0;
     bool dead = false;
     AttnState<FMT, NB, MODE> st;
+    AttnRecord record{0, 0, 0};
 
-    for (; !seg.done(); seg.next(a, items), ++n_seg) {
+    for (; !seg.done(); seg.next(a, items)) {
         const int kvh = seg.item / p.row_groups;
         const int row0 = ((seg.item - kvh * p.row_groups) * p.wr + wrow) * Sh::ROWS;
         const AttnSpan sp(a, a.lens[seg.b]);
@@ -808,7 +787,8 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
             const int i = in ? rr / a.group : 0;
             end[r] = in ? sp.end(i) : 0;
             begin[r] = in ? sp.begin(i) : 0;
-            const int64_t at = ((int64_t)seg.b * a.rows + i) * a.q_row + (int64_t)(kvh * a.group + rr - i * a.group) * a.q_head;
+            const T* row = static_cast<const T*>(a.q) + ((int64_t)seg.b * a.rows + i) * a.q_row +
+                           (int64_t)(kvh * a.group + rr - i * a.group) * a.q_head;
             float qv[NB][8];
             uint32_t top = 0;
 #pragma unroll
@@ -816,8 +796,7 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    const int d = b * 32 + (FMT == QGEMV_KV_Q4_0 ? 16 * h + 4 * t : 8 * t + 4 * h);
-                    if (in) load_row_part(a.q, at + d, p.type, q_wide, x);
+                    if (in) load_values(row + Sh::column(b, h, t), q_wide, x);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         // q4_0: values 4 t + {0, 1, 2, 3} go to places {0, 2, 1, 3}
@@ -859,18 +838,18 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
         bool poison = false;
         st.clear();
 
-        for (int tl = seg.ta; tl < seg.tb; tl += STEP) {
+        for (int tl = seg.ta; tl < seg.tb;) {
             AttnStep x;
-            x.n = min(STEP, seg.tb - tl);
             x.pos = (seg.first + tl) * KV_TILE;
             x.first = sp.first();
             x.last = sp.last();
+            const int n = seg.tb - tl >= 2 && x.pos >= clear_from && x.pos + 2 * KV_TILE <= clear_to ? 2 : 1;
             int used[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 x.tile[u] = ring + (size_t)slot * Sh::TILE;
                 used[u] = split * S + slot;
-                if (u < x.n) {
+                if (u < n) {
                     if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait_bounded(&full[used[u]], phase));
                     if (!dead && bad_page[used[u]]) poison = true;
                     if (++slot == S) slot = 0, phase ^= 1;
@@ -878,17 +857,15 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
             }
             if (dead) break;
             if (!poison) {  // (a stage without its tile: the rows are NaN whatever comes)
-                if (x.n == STEP && x.pos >= clear_from && x.pos + STEP * KV_TILE <= clear_to)
-                    attn_step<FMT, NB, MODE, false>(st, x, qf, q_smem, begin, end, lane);
-                else
-                    attn_step<FMT, NB, MODE, true>(st, x, qf, q_smem, begin, end, lane);
+                if (n == 2) attn_step<FMT, NB, MODE, false>(st, x, qf, q_smem, begin, end, lane);
+                else attn_step<FMT, NB, MODE, true>(st, x, qf, q_smem, begin, end, lane);
             }
             __syncwarp();
             if (lane == 0)
-                for (int u = 0; u < x.n; ++u) mbar_arrive(&empty[used[u]]);
+                for (int u = 0; u < n; ++u) mbar_arrive(&empty[used[u]]);
+            tl += n;
         }
         st.finish(poison || dead);
-        if (dead && lane == 0) s_dead = 1;
 
         if (seg.ta == 0 && seg.tb == seg.count) {
 #pragma unroll
@@ -899,13 +876,15 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
                     for (int r = 0; r < NR; ++r) {
                         float v[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            v[k] = FMT == QGEMV_KV_Q4_0 ? st.o[b][2 * (k & 1) + h][2 * r + (k >> 1)] : st.o[b][k][2 * r + h];
-                        emit(seg.b, seg.item, wrow, b, h, r, v, st.m[r], st.l[r]);
+                        for (int k = 0; k < 4; ++k) {
+                            const int at = Sh::place(b, h, r, k);
+                            v[k] = st.o[at / (4 * Sh::NC)][at / Sh::NC % 4][at % Sh::NC];
+                        }
+                        attn_emit<FMT, NB, MODE, T>(a, p, o_wide, seg.b, seg.item, wrow, b, h, r, lane, v, st.m[r], st.l[r]);
                     }
         } else {
-            const int which = n_seg > 0;
-            float* to = split_part(split, which, wrow);
+            // an item that goes on after this piece is the last of it; one that began before, the first
+            float* to = attn_part(a, p, split_id, seg.ta == 0, wrow, Sh::PART) + lane;
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -917,113 +896,108 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
                 __stcg(to + (Sh::NO + r) * 32, st.m[r]);
                 __stcg(to + (Sh::NO + NR + r) * 32, st.l[r]);
             }
-            if (wrow == 0 && lane == 0) s_left[2 * split + which] = {seg.line, seg.b, seg.item, seg.count, seg.ta, seg.tb};
+            if (seg.ta == 0) {
+                const int64_t last = (seg.line + ATTN_ITEM_COST + seg.count - 1) / piece;
+                record = {(int)last - split_id + 1, seg.b, seg.item};
+            }
         }
     }
+    if (wrow == 0 && lane == 0) a.records[split_id] = record;
+    if (dead && lane == 0) atomicAdd_system(status, 1u);
+}
 
-    // ---- the items that splits share.  A unit of the work is four consecutive
-    // values of a row: block b, half h, row g + 8 r of a row tile.
-    constexpr int UNITS = NB * 2 * NR;
-    auto place = [](int b, int h, int r, int k) {  // value k of it among a lane's outputs
-        return FMT == QGEMV_KV_Q4_0 ? (b * 4 + 2 * (k & 1) + h) * Sh::NC + 2 * r + (k >> 1)
-                                    : (b * 4 + k) * Sh::NC + 2 * r + h;
-    };
-    // the sum of partial results from(0) .. from(n - 1) of the rows of unit w
-    auto join = [&](int n, int w, auto from, float (&v)[4], float& m, float& l) {
+// The items that splits share: out of their partial results, in the order of
+// the splits.  A job is one run of four values of a row of an item: a warp's
+// lanes hold its rows and columns as the splits' lanes did.  `per` warps of a
+// CTA take a job's partial results in turn.
+template <int FMT, int NB, int MODE, typename T>
+__global__ void __launch_bounds__(ATTN_JOIN_WARPS * 32) attn_join_kernel(const AttnArgs a, const AttnPlan p)
+{
+    using Sh = AttnShape<FMT, NB, MODE>;
+    constexpr int NR = Sh::NR;
+    __shared__ int s_split[ATTN_MAX_SPLITS], s_items;
+    __shared__ uint32_t s_has[ATTN_MAX_SPLITS / 32];
+    __shared__ float s_sum[ATTN_JOIN_WARPS][6][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_launch_dependents();
+    pdl_wait();
+    // the splits with a record, in order (the same for every CTA)
+    const int words = (p.splits + 31) / 32;
+    for (int w = warp; w < words; w += ATTN_JOIN_WARPS) {
+        const int i = w * 32 + lane;
+        const uint32_t has = __ballot_sync(0xffffffffu, i < p.splits && a.records[i].parts > 0);
+        if (lane == 0) s_has[w] = has;
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < words) {
+        int at = 0;
+        for (int w = 0; w < (int)threadIdx.x; ++w) at += __popc(s_has[w]);
+        for (uint32_t has = s_has[threadIdx.x]; has; has &= has - 1) s_split[at++] = threadIdx.x * 32 + __ffs(has) - 1;
+        if ((int)threadIdx.x == words - 1) s_items = at;
+    }
+    __syncthreads();
+    const int jobs = s_items * p.wr * Sh::UNITS;
+    int per = ATTN_JOIN_WARPS;
+    while (per > 1 && jobs * per > (int)gridDim.x * ATTN_JOIN_WARPS) per >>= 1;
+    const int at_once = ATTN_JOIN_WARPS / per, part0 = warp % per;
+    const bool o_wide = KvRows{a.out, a.o_row, a.o_head}.wide<T>();
+    for (int base = blockIdx.x * at_once; base < jobs; base += gridDim.x * at_once) {
+        const int job = base + warp / per;
+        const int unit = job % (p.wr * Sh::UNITS), tile = unit / Sh::UNITS, w = unit % Sh::UNITS;
         const int r = w % NR, h = w / NR % 2, b = w / (2 * NR);
-        m = -INFINITY;
-        l = v[0] = v[1] = v[2] = v[3] = 0.0f;
+        float m = -INFINITY, l = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        AttnRecord rec{0, 0, 0};
+        if (job < jobs) {
+            const int s0 = s_split[job / (p.wr * Sh::UNITS)];
+            rec = a.records[s0];
 #pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float* q = from(i);
-            const float m2 = __ldcg(q + (Sh::NO + r) * 32), l2 = __ldcg(q + (Sh::NO + NR + r) * 32);
-            const float mn = fmaxf(m, m2), bs = attn_base(mn), f1 = ex2(m - bs), f2 = ex2(m2 - bs);
-            m = mn;
-            l = l * f1 + l2 * f2;
+            for (int i = part0; i < rec.parts; i += per) {
+                const float* from = attn_part(a, p, s0 + i, i == 0, tile, Sh::PART) + lane;
+                const float m2 = __ldcg(from + (Sh::NO + r) * 32), l2 = __ldcg(from + (Sh::NO + NR + r) * 32);
+                const float mn = fmaxf(m, m2), bs = attn_base(mn), f1 = ex2(m - bs), f2 = ex2(m2 - bs);
+                m = mn;
+                l = l * f1 + l2 * f2;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = v[k] * f1 + __ldcg(q + place(b, h, r, k) * 32) * f2;
-        }
-    };
-    meet();
-    AttnLeft cut[2];  // those that go on in other CTAs: before this one, after it
-    cut[0].line = cut[1].line = -1;
-    for (int i = 0; i < 2 * p.ws;) {
-        AttnLeft x = s_left[i];
-        if (x.line < 0) {
-            ++i;
-            continue;
-        }
-        // its partial results in this CTA: entry i, then the first ones of the splits that follow
-        int n = 1;
-        for (int k = i + 1; k < 2 * p.ws; ++k) {
-            if (s_left[k].line < 0) continue;
-            if (s_left[k].line != x.line) break;
-            x.tb = s_left[k].tb;
-            ++n;
-        }
-        const bool whole = x.ta == 0 && x.tb == x.count;
-        const int after = x.ta == 0;  // only what lies before this CTA's piece is missing otherwise
-        for (int unit = warp; unit < p.wr * UNITS; unit += warps) {
-            const int tile = unit / UNITS, w = unit - tile * UNITS, r = w % NR, h = w / NR % 2, b = w / (2 * NR);
-            float v[4], m, l;
-            join(n, w, [&](int k) { return k == 0 ? split_part(i >> 1, i & 1, tile) : split_part((i >> 1) + k, 0, tile); }, v, m, l);
-            if (whole) {
-                emit(x.b, x.item, tile, b, h, r, v, m, l);
-            } else {
-                float* to = cta_part(blockIdx.x, after, tile);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) __stcg(to + place(b, h, r, k) * 32, v[k]);
-                if (b == 0 && h == 0) {
-                    __stcg(to + (Sh::NO + r) * 32, m);
-                    __stcg(to + (Sh::NO + NR + r) * 32, l);
+                for (int k = 0; k < 4; ++k) {
+                    const int at = FMT == QGEMV_KV_Q4_0 ? (b * 4 + 2 * (k & 1) + h) * Sh::NC + 2 * r + (k >> 1)
+                                                        : (b * 4 + k) * Sh::NC + 2 * r + h;
+                    v[k] = v[k] * f1 + __ldcg(from + at * 32) * f2;
                 }
             }
         }
-        if (!whole) cut[after] = x;
-        // on to the first entry of another item
-        for (++i; i < 2 * p.ws && (s_left[i].line < 0 || s_left[i].line == x.line); ++i) {}
-    }
-    // ---- the items that CTAs share: the last one joins the partial results
-    auto first_cta = [&](const AttnLeft& x) { return (int)((x.line + ATTN_ITEM_COST) / chunk); };
-    auto last_cta = [&](const AttnLeft& x) { return (int)((x.line + ATTN_ITEM_COST + x.count - 1) / chunk); };
-    if (cut[0].line >= 0 || cut[1].line >= 0) {
-        __threadfence();
-        meet();
-        if (threadIdx.x < 2) {
-            const AttnLeft& x = cut[threadIdx.x];
-            int last = 0;
-            if (x.line >= 0) {
-                const int c0 = first_cta(x);
-                last = atomicAdd(&a.counters[c0], 1u) == (unsigned)(last_cta(x) - c0);
-                if (last) a.counters[c0] = 0;
-                __threadfence();
-            }
-            s_last[threadIdx.x] = last;
-        }
-        meet();
+        if (per > 1) {
+            float(*mine)[32] = s_sum[warp];
+            mine[0][lane] = m, mine[1][lane] = l;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            if (!s_last[k]) continue;
-            const AttnLeft& x = cut[k];
-            const int c0 = first_cta(x), n = last_cta(x) - c0 + 1;
-            for (int unit = warp; unit < p.wr * UNITS; unit += warps) {
-                const int tile = unit / UNITS, w = unit - tile * UNITS, r = w % NR, h = w / NR % 2, b = w / (2 * NR);
-                float v[4], m, l;
-                join(n, w, [&](int c) { return cta_part(c0 + c, c == 0, tile); }, v, m, l);
-                emit(x.b, x.item, tile, b, h, r, v, m, l);
+            for (int k = 0; k < 4; ++k) mine[2 + k][lane] = v[k];
+            __syncthreads();
+            if (part0 == 0) {
+                float top = m;
+                for (int i = 1; i < per; ++i) top = fmaxf(top, s_sum[warp + i][0][lane]);
+                const float bs = attn_base(top), f0 = ex2(m - bs);
+                l *= f0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] *= f0;
+                for (int i = 1; i < per; ++i) {
+                    const float f = ex2(s_sum[warp + i][0][lane] - bs);
+                    l += s_sum[warp + i][1][lane] * f;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[k] += s_sum[warp + i][2 + k][lane] * f;
+                }
+                m = top;
             }
+            __syncthreads();
         }
+        if (part0 == 0 && job < jobs)
+            attn_emit<FMT, NB, MODE, T>(a, p, o_wide, rec.b, rec.item, tile, b, h, r, lane, v, m, l);
     }
-    meet();
-    if (threadIdx.x == 0 && s_dead) atomicAdd_system(status, 1u);
 }
 
 template <int FMT, int NB, int MODE>
-AttnPlan attn_plan(const DeviceInfo& di, int type, int rows)
+AttnPlan attn_plan(const DeviceInfo& di, int rows)
 {
     using Sh = AttnShape<FMT, NB, MODE>;
     AttnPlan p{};
-    p.type = type;
     const int tiles = (rows + Sh::ROWS - 1) / Sh::ROWS;
     p.row_groups = (tiles + Sh::WARPS - 1) / Sh::WARPS;
     p.wr = (tiles + p.row_groups - 1) / p.row_groups;
@@ -1039,20 +1013,20 @@ AttnPlan attn_plan(const DeviceInfo& di, int type, int rows)
         p.bytes = p.off_bar + (uint32_t)p.ws * p.stages * 20;
         break;
     }
+    p.splits = (di.sms < ATTN_GRID ? di.sms : ATTN_GRID) * p.ws;
     return p;
 }
 
-template <int FMT, int NB, int MODE>
-int launch_attn_split(int type, const AttnArgs& a, cudaStream_t s)
+template <int FMT, int NB, int MODE, typename T>
+int launch_attn(const AttnArgs& a, cudaStream_t s)
 {
-    using Sh = AttnShape<FMT, NB, MODE>;
     const DeviceInfo di = device_info();
     if (di.sms <= 0) return QGEMV_CUDA_ERROR;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return QGEMV_CUDA_ERROR;
-    const AttnPlan p = attn_plan<FMT, NB, MODE>(di, type, a.rows * a.group);
-    if (p.stages < Sh::STEP) return QGEMV_UNSUPPORTED_SHAPE;
-    auto kern = attn_split_kernel<FMT, NB, MODE>;
+    const AttnPlan p = attn_plan<FMT, NB, MODE>(di, a.rows * a.group);
+    if (p.stages < 2) return QGEMV_UNSUPPORTED_SHAPE;
+    auto kern = attn_split_kernel<FMT, NB, MODE, T>;
     static std::once_flag once[64];
     static bool ok[64];
     std::call_once(once[dev], [&]() {
@@ -1062,35 +1036,35 @@ int launch_attn_split(int type, const AttnArgs& a, cudaStream_t s)
         if (!ok[dev]) cudaGetLastError();
     });
     if (!ok[dev]) return QGEMV_CUDA_ERROR;
-    const int grid = di.sms < ATTN_GRID ? di.sms : ATTN_GRID;
-    if (launch_pdl(kern, dim3(grid), dim3((p.ws * p.wr + 1) * 32), p.bytes, s, a, p, wait_timeout_counter()) != cudaSuccess)
+    if (launch_pdl(kern, dim3(p.splits / p.ws), dim3((p.ws * p.wr + 1) * 32), p.bytes, s, a, p, wait_timeout_counter()) !=
+        cudaSuccess)
+        return QGEMV_CUDA_ERROR;
+    if (launch_pdl(attn_join_kernel<FMT, NB, MODE, T>, dim3(di.sms), dim3(ATTN_JOIN_WARPS * 32), 0, s, a, p) != cudaSuccess)
         return QGEMV_CUDA_ERROR;
     return cudaGetLastError() == cudaSuccess ? QGEMV_OK : QGEMV_CUDA_ERROR;
 }
 
-template <int FMT, int MODE>
-int launch_attn_dim(int type, const AttnArgs& a, cudaStream_t s)
+template <int FMT, int MODE, typename T>
+int launch_attn_dim(const AttnArgs& a, cudaStream_t s)
 {
     switch (a.L.nb) {
-    case 2: return launch_attn_split<FMT, 2, MODE>(type, a, s);
-    case 3: return launch_attn_split<FMT, 3, MODE>(type, a, s);
-    case 4: return launch_attn_split<FMT, 4, MODE>(type, a, s);
-    default: return launch_attn_split<FMT, 8, MODE>(type, a, s);
+    case 2: return launch_attn<FMT, 2, MODE, T>(a, s);
+    case 3: return launch_attn<FMT, 3, MODE, T>(a, s);
+    case 4: return launch_attn<FMT, 4, MODE, T>(a, s);
+    default: return launch_attn<FMT, 8, MODE, T>(a, s);
     }
 }
 
-template <int FMT>
-int launch_attn_type(int type, const AttnArgs& a, cudaStream_t s)
+// One translation unit for each format and type.
+template <int FMT, typename T>
+int launch_attn_rows(const AttnArgs& a, cudaStream_t s)
 {
-    switch (attn_mode(type, a.rows * a.group)) {
-    case ATTN_ONE: return launch_attn_dim<FMT, ATTN_ONE>(type, a, s);
-    case ATTN_PAIR: return launch_attn_dim<FMT, ATTN_PAIR>(type, a, s);
-    default: return launch_attn_dim<FMT, ATTN_TWO>(type, a, s);
+    if constexpr (sizeof(T) == 2 && !std::is_same_v<T, __half>) {
+        return launch_attn_dim<FMT, ATTN_ONE, T>(a, s);
+    } else {
+        if (attn_mode(QGEMV_F32, a.rows * a.group) == ATTN_PAIR) return launch_attn_dim<FMT, ATTN_PAIR, T>(a, s);
+        return launch_attn_dim<FMT, ATTN_TWO, T>(a, s);
     }
 }
-
-int launch_attn_f16(int type, const AttnArgs& a, cudaStream_t s);
-int launch_attn_q8_0(int type, const AttnArgs& a, cudaStream_t s);
-int launch_attn_q4_0(int type, const AttnArgs& a, cudaStream_t s);
 
 }  // namespace qgemv

@@ -1,0 +1,8 @@
+// attn_paged over f16 pages for f16 rows.
+#include "attn_paged.cuh"
+
+namespace qgemv {
+
+int launch_attn_f16_f16(const AttnArgs& a, cudaStream_t s) { return launch_attn_rows<QGEMV_KV_F16, __half>(a, s); }
+
+}  // namespace qgemv

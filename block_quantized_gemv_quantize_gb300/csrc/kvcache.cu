@@ -17,7 +17,7 @@ namespace {
 
 constexpr int KV_WARPS = 8, KV_THREADS = 32 * KV_WARPS;
 constexpr int KV_TOKENS = 4 * KV_WARPS;  // of a CTA
-constexpr int KV_PAIRS = 4;              // pairs of blocks of a warp
+constexpr int KV_PAIRS = 4;              // pairs of blocks of a warp, one for each lane of a quad
 
 // The eight values of lane sub (0 .. 3) of a block: 8 sub .. 8 sub + 7, or in
 // two runs, 4 sub .. + 3 and 16 + 4 sub .. + 3.  Two runs keep fp32 accesses of
@@ -25,18 +25,33 @@ constexpr int KV_PAIRS = 4;              // pairs of blocks of a warp
 template <int FMT, typename T>
 constexpr bool kv_two_runs = FMT == QGEMV_KV_Q4_0 || sizeof(T) == 4;
 
+// A lane's eight values as they are in memory.
+template <typename T>
+struct alignas(16) KvRaw {
+    T v[8];
+};
+
 template <bool RUNS, typename T>
-__device__ __forceinline__ void load_lane(const T* p, int sub, bool wide, float (&v)[8])
+__device__ __forceinline__ void load_lane(const T* p, int sub, bool wide, KvRaw<T>& x)
 {
-    if constexpr (RUNS) {
-        float lo[4], hi[4];
-        load_values(p + 4 * sub, wide, lo);
-        load_values(p + 16 + 4 * sub, wide, hi);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = lo[k], v[4 + k] = hi[k];
-    } else {
-        load_values(p + 8 * sub, wide, v);
+    if constexpr (RUNS && sizeof(T) == 4) {
+        if (wide) {
+            reinterpret_cast<uint4*>(x.v)[0] = reinterpret_cast<const uint4*>(p)[sub];
+            reinterpret_cast<uint4*>(x.v)[1] = reinterpret_cast<const uint4*>(p)[4 + sub];
+            return;
+        }
+    } else if constexpr (RUNS) {
+        if (wide) {
+            reinterpret_cast<uint2*>(x.v)[0] = reinterpret_cast<const uint2*>(p)[sub];
+            reinterpret_cast<uint2*>(x.v)[1] = reinterpret_cast<const uint2*>(p)[4 + sub];
+            return;
+        }
+    } else if (wide) {
+        *reinterpret_cast<uint4*>(x.v) = reinterpret_cast<const uint4*>(p)[sub];
+        return;
     }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x.v[k] = p[RUNS ? 4 * sub + (k & 3) + 4 * (k & 4) : 8 * sub + k];
 }
 
 template <bool RUNS, typename T>
@@ -57,109 +72,204 @@ __device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b, uint32_t c
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
+// The larger magnitude; NaN if either is.
+__device__ __forceinline__ float max_abs(float a, float b)
+{
+    float m;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(fabsf(a)), "f"(fabsf(b)));
+    return m;
+}
+
+// What the four lanes of a block's quad know of its values after the first
+// pass: the largest magnitude (NaN if one is) and, for q4_0, twice the place of
+// the first value that has it, plus its sign.
+struct KvTop {
+    float mag;
+    int key;
+    template <bool KEY>
+    __device__ __forceinline__ void join(const KvTop& o)
+    {
+        if (KEY && (o.mag > mag || (o.mag == mag && o.key < key))) key = o.key;
+        mag = max_abs(mag, o.mag);
+    }
+    template <bool KEY>
+    __device__ __forceinline__ KvTop from(int lanes) const
+    {
+        return {__shfl_xor_sync(0xffffffffu, mag, lanes), KEY ? __shfl_xor_sync(0xffffffffu, key, lanes) : 0};
+    }
+};
+
+// A lane's own eight values of a block.
+template <int FMT, bool RUNS>
+__device__ __forceinline__ KvTop kv_top(const float (&x)[8], int sub)
+{
+    KvTop t{fabsf(x[0]), 2 * (RUNS ? 4 : 8) * sub + (int)(__float_as_uint(x[0]) >> 31)};
+#pragma unroll
+    for (int k = 1; k < 8; ++k) {
+        if (FMT == QGEMV_KV_Q4_0) {
+            const int at = RUNS ? 4 * sub + (k & 3) + 4 * (k & 4) : 8 * sub + k;
+            if (fabsf(x[k]) > t.mag) t.key = 2 * at + (int)(__float_as_uint(x[k]) >> 31);
+        }
+        t.mag = max_abs(t.mag, x[k]);
+    }
+    return t;
+}
+
+// Four blocks' tops over the quad: lane sub gets that of block sub.
+template <bool KEY>
+__device__ __forceinline__ KvTop kv_scatter(const KvTop (&t)[4], int sub)
+{
+    const bool up = sub & 2, odd = sub & 1;
+    KvTop a = up ? t[2] : t[0], b = up ? t[3] : t[1];
+    a.join<KEY>((up ? t[0] : t[2]).from<KEY>(2));
+    b.join<KEY>((up ? t[1] : t[3]).from<KEY>(2));
+    KvTop own = odd ? b : a;
+    own.join<KEY>((odd ? a : b).from<KEY>(1));
+    return own;
+}
+
+// A block's d: NaN where a value is no number or infinite, 0 where all codes are
+// to be those of zero.
+template <int FMT>
+__device__ __forceinline__ float kv_d(const KvTop& t)
+{
+    if (!(t.mag < INFINITY)) return __int_as_float(0x7fffffff);
+    return FMT == QGEMV_KV_Q8_0 ? __fdiv_rn(t.mag, 127.0f) : __fmul_rn(t.key & 1 ? -t.mag : t.mag, -0.125f);
+}
+
 // Adding 3 * 2^22 rounds a number below 2^22 to a whole one, which then stands
 // in the low bits; the format's offset (128 or 8) goes in with it.
 constexpr float KV_ROUND = 12582912.0f;
 
-// A lane's eight values of a block -> its code words (q4_0: one) and the
-// block's scale; by all lanes of the warp, values beyond the rows being zero.
+// A lane's eight values of a block -> its code words (q4_0: one), given d and
+// kv_inverse(d); by all lanes of the warp, `d` standing in lane `from` of it.
 //
-// The code is defined by the fp32 quotient x / d.  x * (1 / d) differs from it
-// by less than 2^-15 (two roundings of at most 2^-24 against one, |x / d| <=
-// 127), so the two round to the same code unless the product lies within 2^-13
-// of where the code changes, or 1 / d overflows: those few lanes divide.
-template <int FMT, bool RUNS>
-__device__ __forceinline__ void kv_encode(float (&x)[8], int sub, uint32_t (&word)[2], float& scale)
+// The code is defined by the fp32 quotient x / d.  y = x * (1 / d) differs from
+// it by less than 2^-15 (two roundings of at most 2^-24 against one, |x / d| <=
+// 127), so the two round to the same code unless y lies within 2^-14 of where
+// the code changes.  bf16 rows often have such values (their quotients are
+// ratios of 8-bit numbers), so a division there costs as much as all the rest;
+// two corrections y += (x - y d) (1 / d) give the same fp32 number: after the
+// first y is within one unit of x / d, and the second is then exactly the
+// rounded quotient where 1 / d is the correctly rounded inverse of a d whose
+// mantissa is not all ones (P. W. Markstein, IBM J. Res. Dev. 34, 1990).
+// Blocks without such an inverse divide.
+__device__ __forceinline__ float kv_inverse(float d)
+{
+    if (d == 0.0f) return 0.0f;
+    const bool odd = (__float_as_uint(d) & 0x7fffffu) == 0x7fffffu;  // (a NaN d among them)
+    return fabsf(d) >= 0x1p-100f && !odd ? __frcp_rn(d) : INFINITY;
+}
+
+template <int FMT>
+__device__ __forceinline__ void kv_encode(const float (&x)[8], float d, float inverse, int from, uint32_t (&word)[2])
 {
     constexpr bool Q8 = FMT == QGEMV_KV_Q8_0;
-    // magnitudes compare as integers, a NaN above an infinity above the rest
-    uint32_t top = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(x[k]) & 0x7fffffffu);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const bool fine = top < 0x7f800000u;
-    float d;
-    if (Q8) {
-        d = __fdiv_rn(__uint_as_float(top), 127.0f);
-    } else {
-        // the first value of that magnitude, and its sign
-        int first = 64;
-#pragma unroll
-        for (int k = 7; k >= 0; --k) {
-            const int at = RUNS ? 4 * sub + (k & 3) + 4 * (k & 4) : 8 * sub + k;
-            const uint32_t bits = __float_as_uint(x[k]);
-            if ((bits & 0x7fffffffu) == top) first = 2 * at + (int)(bits >> 31);
-        }
-        first = min(first, __shfl_xor_sync(0xffffffffu, first, 1));
-        first = min(first, __shfl_xor_sync(0xffffffffu, first, 2));
-        d = __fmul_rn(__uint_as_float(top | (uint32_t)(first & 1) << 31), -0.125f);
-    }
-    scale = fine ? fminf(fmaxf(d, -65504.0f), 65504.0f) : __int_as_float(0x7fffffff);
-    const bool use = fine && d != 0.0f;
-    const float inv = use ? __frcp_rn(d) : 0.0f;
-    if (!fine) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = 0.0f;
-    }
     constexpr float magic = KV_ROUND + (Q8 ? 128.0f : 8.0f);
+    const float inv = __shfl_sync(0xffffffffu, inverse, from);
     uint32_t n[8];
-    float off = use && fabsf(d) < 0x1p-126f ? 1.0f : 0.0f;
+    float off = fabsf(inv) == INFINITY ? 1.0f : 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        float y = __fmul_rn(x[k], inv);
-        if (!Q8) y = fminf(y, 7.25f);  // from 7 on the code is 15
-        const float r = __fadd_rn(y, magic);
-        off = fmaxf(off, fabsf(__fsub_rn(y, __fsub_rn(r, magic))));
-        n[k] = __float_as_uint(r);
+    for (int k = 0; k < 8; k += 2) {
+        float y0, y1, r0, r1, w0 = magic, w1 = magic;
+        mul_f32x2(y0, y1, x[k], x[k + 1], inv, inv);
+        if (!Q8) y0 = fminf(y0, 7.25f), y1 = fminf(y1, 7.25f);  // from 7 on the code is 15
+        add_f32x2(r0, r1, y0, y1, magic, magic);
+        fma_f32x2(w0, w1, r0, r1, -1.0f, -1.0f);
+        add_f32x2(w0, w1, w0, w1, y0, y1);  // y less the whole number
+        off = fmaxf(off, fmaxf(fabsf(w0), fabsf(w1)));
+        n[k] = __float_as_uint(r0), n[k + 1] = __float_as_uint(r1);
     }
-    if (off > 0.5f - 0x1p-13f) {
+    auto code = [](float q) {
+        return Q8 ? (uint32_t)(max(-127, min(127, (int)roundf(q))) + 128)
+                  : (uint32_t)max(0, min(15, (int)floorf(__fadd_rn(q, 8.5f))));
+    };
+    const bool far = off > 0.5f - 0x1p-14f;
+    float dd = 0.0f;
+    if (__any_sync(0xffffffffu, far)) {
+        dd = __shfl_sync(0xffffffffu, d, from);
+        if (far) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float y = __fdiv_rn(x[k], d);
-            n[k] = Q8 ? (uint32_t)(max(-127, min(127, (int)roundf(y))) + 128)
-                      : (uint32_t)max(0, min(15, (int)floorf(__fadd_rn(y, 8.5f))));
+            for (int k = 0; k < 8; k += 2) {
+                float q0, q1;
+                mul_f32x2(q0, q1, x[k], x[k + 1], inv, inv);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float r0 = x[k], r1 = x[k + 1];
+                    fma_f32x2(r0, r1, q0, q1, -dd, -dd);
+                    fma_f32x2(q0, q1, r0, r1, inv, inv);
+                }
+                n[k] = code(q0), n[k + 1] = code(q1);
+            }
         }
     }
     word[0] = low_bytes(n[0], n[1], n[2], n[3]);
     word[1] = low_bytes(n[4], n[5], n[6], n[7]);
+    if (inv == INFINITY) {  // one at a time: rare, and so without registers of its own
+        word[0] = word[1] = 0;
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+            float v = x[0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) v = k == i ? x[i] : v;
+            const uint32_t c = code(fabsf(dd) > 0.0f ? __fdiv_rn(v, dd) : 0.0f) << (8 * (k & 3));  // (no d: zeros)
+            if (k < 4) word[0] |= c;
+            else word[1] |= c;
+        }
+    }
     if (!Q8) word[0] |= word[1] << 4;
 }
 
-// One lane's part of a unit of work: a token and, for pair j, a block.
-struct KvPlace {
-    int64_t token;
-    KvLayout::Slot at;
-    int block0, n_blocks;  // blocks in the order [K, V][head][block]
+// A lane's token: where its rows are, and its place in the cache.
+template <int FMT, typename T>
+struct KvToken {
+    T *k, *v;          // its rows
+    uint8_t* codes;    // block 0 of head 0's K; null outside the cache
+    uint32_t scales;   // from there to that block's scale
     bool in;
-    __device__ __forceinline__ KvPlace(const KvArgs& a, int64_t group, int lane)
+    __device__ __forceinline__ KvToken(const KvArgs& a, int64_t group, int lane)
     {
-        token = group * KV_TOKENS + (threadIdx.x >> 5) * 4 + (lane >> 3);
+        const int64_t token = group * KV_TOKENS + (threadIdx.x >> 5) * 4 + (lane >> 3);
         in = token < a.n_tokens;
-        at = a.L.slot(in ? a.slots[token] : -1);
-        n_blocks = 2 * a.L.heads * a.L.nb;
-        block0 = blockIdx.x * 2 * KV_PAIRS + (lane >> 2 & 1);
+        const KvLayout::Slot at = a.L.slot(in ? a.slots[token] : -1);
+        codes = at.page < 0 ? nullptr : a.cache + a.L.tile_offset(at.page, 0, at.tile) + at.row * kv_code_bytes(FMT);
+        scales = a.L.nb * KV_TILE * kv_code_bytes(FMT) + 2 * kv_scale_place(at.row) - at.row * kv_code_bytes(FMT);
+        k = static_cast<T*>(a.k.base) + token * a.k.token;
+        v = static_cast<T*>(a.v.base) + token * a.v.token;
     }
 };
 
+// Block n of a token, in the order [K, V][head][block].
 struct KvBlock {
-    int which, head, block;
-    __device__ __forceinline__ KvBlock(const KvLayout& L, int n)
+    bool second;        // V
+    uint32_t head, block;
+    __device__ __forceinline__ KvBlock(const KvArgs& a, uint32_t n)
     {
-        const int per = L.heads * L.nb;
-        which = n >= per;
-        n -= which * per;
-        head = (int)((uint32_t)n / (uint32_t)L.nb);
-        block = n - head * L.nb;
+        const uint32_t per = (uint32_t)(a.L.heads * a.L.nb);
+        second = n >= per;
+        if (second) n -= per;
+        head = a.L.nb == 1 ? n : __umulhi(n, a.nb_inverse);
+        block = n - head * (uint32_t)a.L.nb;
     }
-    __device__ __forceinline__ int64_t element(const KvRows& r, int64_t token) const
+    // from a token's first code to this block's (a page is below 4 GB)
+    template <int FMT>
+    __device__ __forceinline__ uint32_t codes(const KvArgs& a) const
     {
-        return token * r.token + head * r.head + block * QK;
+        return head * a.head_bytes + (second ? (uint32_t)kv_half_bytes(FMT, a.L.nb) : 0u) +
+               block * (KV_TILE * kv_code_bytes(FMT));
+    }
+    // from there to the scale, beyond KvToken::scales
+    template <int FMT>
+    __device__ __forceinline__ uint32_t scale() const { return block * KV_TILE * 2 - block * (KV_TILE * kv_code_bytes(FMT)); }
+    template <int FMT, typename T>
+    __device__ __forceinline__ T* row(const KvArgs& a, const KvToken<FMT, T>& t) const
+    {
+        return (second ? t.v : t.k) + (int64_t)head * (second ? a.v.head : a.k.head) + block * QK;
     }
 };
 
 template <int FMT, typename T>
-__global__ void __launch_bounds__(KV_THREADS) kv_write_kernel(const KvArgs a, unsigned int* st)
+__global__ void __launch_bounds__(KV_THREADS, 4) kv_write_kernel(const KvArgs a, unsigned int* st)
 {
     constexpr bool RUNS = kv_two_runs<FMT, T>;
     constexpr int CODE = kv_code_bytes(FMT);
@@ -167,40 +277,59 @@ __global__ void __launch_bounds__(KV_THREADS) kv_write_kernel(const KvArgs a, un
     pdl_wait();
     const int lane = threadIdx.x & 31, sub = lane & 3;
     const bool wide = a.k.wide<T>() && a.v.wide<T>();
+    const int n_blocks = 2 * a.L.heads * a.L.nb, block0 = blockIdx.x * 2 * KV_PAIRS + (lane >> 2 & 1);
     for (int64_t group = blockIdx.y; group * KV_TOKENS < a.n_tokens; group += gridDim.y) {
-        const KvPlace at(a, group, lane);
-        float x[KV_PAIRS][8];
+        const KvToken<FMT, T> t(a, group, lane);
+        KvRaw<T> raw[KV_PAIRS];
 #pragma unroll
         for (int j = 0; j < KV_PAIRS; ++j) {
+            const int n = block0 + 2 * j;
+            if (t.codes && n < n_blocks) {
+                load_lane<RUNS>(KvBlock(a, n).row(a, t), sub, wide, raw[j]);
+            } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[j][k] = 0.0f;
-            const int n = at.block0 + 2 * j;
-            if (at.at.page < 0 || n >= at.n_blocks) continue;
-            const KvBlock b(a.L, n);
-            const KvRows& rows = b.which ? a.v : a.k;
-            load_lane<RUNS>(static_cast<const T*>(rows.base) + b.element(rows, at.token), sub, wide, x[j]);
+                for (int k = 0; k < 8; ++k) raw[j].v[k] = from_f32<T>(0.0f);
+            }
+        }
+        // the scales: lane sub of a quad works out pair sub's
+        float d = 0.0f, inverse = 0.0f;
+        if constexpr (FMT != QGEMV_KV_F16) {
+            KvTop top[KV_PAIRS];
+#pragma unroll
+            for (int j = 0; j < KV_PAIRS; ++j) {
+                float x[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = to_f32(raw[j].v[k]);
+                top[j] = kv_top<FMT, RUNS>(x, sub);
+            }
+            d = kv_d<FMT>(kv_scatter<FMT == QGEMV_KV_Q4_0>(top, sub));
+            inverse = kv_inverse(d);
+            const int n = block0 + 2 * sub;
+            if (t.codes && n < n_blocks) {
+                const KvBlock b(a, n);
+                uint8_t* scale = t.codes + b.codes<FMT>(a) + (t.scales + b.scale<FMT>());
+                if (QG_OK(qg_in(scale - a.cache, 2, a.L.bytes()), st, 742))  // (a NaN stays)
+                    *reinterpret_cast<__half*>(scale) = __float2half_rn(fabsf(d) > 65504.0f ? copysignf(65504.0f, d) : d);
+            }
         }
 #pragma unroll
         for (int j = 0; j < KV_PAIRS; ++j) {
-            const int n = at.block0 + 2 * j;
+            const int n = block0 + 2 * j;
+            float x[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) x[k] = to_f32(raw[j].v[k]);
             uint32_t word[2];
-            float d;
-            if constexpr (FMT != QGEMV_KV_F16) kv_encode<FMT, RUNS>(x[j], sub, word, d);  // shuffles: every lane
-            if (at.at.page < 0 || n >= at.n_blocks) continue;
-            const KvBlock b(a.L, n);
-            uint8_t* half = a.cache + a.L.tile_offset(at.at.page, b.head, at.at.tile) + b.which * kv_half_bytes(FMT, a.L.nb);
-            uint8_t* codes = half + (b.block * KV_TILE + at.at.row) * CODE;
+            if constexpr (FMT != QGEMV_KV_F16) kv_encode<FMT>(x, d, inverse, (lane & 28) + j, word);  // shuffles: every lane
+            if (!t.codes || n >= n_blocks) continue;
+            uint8_t* codes = t.codes + KvBlock(a, n).codes<FMT>(a);
             if (!QG_OK(qg_in(codes - a.cache, CODE, a.L.bytes()), st, 741)) continue;
             if constexpr (FMT == QGEMV_KV_F16) {
-                store_lane<RUNS>(reinterpret_cast<__half*>(codes), sub, true, x[j]);
+                store_lane<RUNS>(reinterpret_cast<__half*>(codes), sub, true, x);
             } else {
                 uint32_t* w = reinterpret_cast<uint32_t*>(codes);
                 if constexpr (FMT == QGEMV_KV_Q4_0) w[sub] = word[0];
                 else if constexpr (RUNS) w[sub] = word[0], w[4 + sub] = word[1];
                 else reinterpret_cast<uint2*>(codes)[sub] = make_uint2(word[0], word[1]);
-                uint8_t* scale = half + a.L.nb * KV_TILE * CODE + (b.block * KV_TILE + kv_scale_place(at.at.row)) * 2;
-                if (sub == 0 && QG_OK(qg_in(scale - a.cache, 2, a.L.bytes()), st, 742))
-                    *reinterpret_cast<__half*>(scale) = __float2half_rn(d);
             }
         }
     }
@@ -210,11 +339,13 @@ __global__ void __launch_bounds__(KV_THREADS) kv_write_kernel(const KvArgs a, un
 __device__ __forceinline__ void kv_numbers(uint32_t w, float offset, float* v)
 {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 + k)) - (8388608.0f + offset);
+    for (int k = 0; k < 4; k += 2)
+        add_f32x2(v[k], v[k + 1], __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 + k)),
+                  __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7441 + k)), -(8388608.0f + offset), -(8388608.0f + offset));
 }
 
 template <int FMT, typename T>
-__global__ void __launch_bounds__(KV_THREADS) kv_read_kernel(const KvArgs a, unsigned int* st)
+__global__ void __launch_bounds__(KV_THREADS, 5) kv_read_kernel(const KvArgs a, unsigned int* st)
 {
     constexpr bool RUNS = kv_two_runs<FMT, T>;
     constexpr int CODE = kv_code_bytes(FMT);
@@ -222,9 +353,10 @@ __global__ void __launch_bounds__(KV_THREADS) kv_read_kernel(const KvArgs a, uns
     pdl_wait();
     const int lane = threadIdx.x & 31, sub = lane & 3;
     const bool wide = a.k.wide<T>() && a.v.wide<T>();
+    const int n_blocks = 2 * a.L.heads * a.L.nb, block0 = blockIdx.x * 2 * KV_PAIRS + (lane >> 2 & 1);
     for (int64_t group = blockIdx.y; group * KV_TOKENS < a.n_tokens; group += gridDim.y) {
-        const KvPlace at(a, group, lane);
-        if (!at.in) continue;
+        const KvToken<FMT, T> t(a, group, lane);
+        if (!t.in) continue;
         uint32_t word[KV_PAIRS][FMT == QGEMV_KV_F16 ? 4 : 2];
         __half d[KV_PAIRS];
 #pragma unroll
@@ -232,11 +364,10 @@ __global__ void __launch_bounds__(KV_THREADS) kv_read_kernel(const KvArgs a, uns
 #pragma unroll
             for (uint32_t& w : word[j]) w = 0;
             d[j] = __half(0.0f);
-            const int n = at.block0 + 2 * j;
-            if (at.at.page < 0 || n >= at.n_blocks) continue;
-            const KvBlock b(a.L, n);
-            const uint8_t* half = a.cache + a.L.tile_offset(at.at.page, b.head, at.at.tile) + b.which * kv_half_bytes(FMT, a.L.nb);
-            const uint8_t* codes = half + (b.block * KV_TILE + at.at.row) * CODE;
+            const int n = block0 + 2 * j;
+            if (!t.codes || n >= n_blocks) continue;
+            const KvBlock b(a, n);
+            const uint8_t* codes = t.codes + b.codes<FMT>(a);
             if (!QG_OK(qg_in(codes - a.cache, CODE, a.L.bytes()), st, 743)) continue;
             if constexpr (FMT == QGEMV_KV_F16) {
                 const uint2* w = reinterpret_cast<const uint2*>(codes);
@@ -252,14 +383,14 @@ __global__ void __launch_bounds__(KV_THREADS) kv_read_kernel(const KvArgs a, uns
                     const uint2 both = reinterpret_cast<const uint2*>(codes)[sub];
                     word[j][0] = both.x, word[j][1] = both.y;
                 }
-                const uint8_t* scale = half + a.L.nb * KV_TILE * CODE + (b.block * KV_TILE + kv_scale_place(at.at.row)) * 2;
+                const uint8_t* scale = codes + (t.scales + b.scale<FMT>());
                 if (QG_OK(qg_in(scale - a.cache, 2, a.L.bytes()), st, 744)) d[j] = *reinterpret_cast<const __half*>(scale);
             }
         }
 #pragma unroll
         for (int j = 0; j < KV_PAIRS; ++j) {
-            const int n = at.block0 + 2 * j;
-            if (n >= at.n_blocks) continue;
+            const int n = block0 + 2 * j;
+            if (n >= n_blocks) continue;
             float x[8];
             if constexpr (FMT == QGEMV_KV_F16) {
 #pragma unroll
@@ -275,17 +406,15 @@ __global__ void __launch_bounds__(KV_THREADS) kv_read_kernel(const KvArgs a, uns
                     kv_numbers(word[j][0], 128.0f, x);
                     kv_numbers(word[j][1], 128.0f, x + 4);
                 }
-                const float f = __half2float(d[j]);
+                const float f = __half2float(d[j]);  // 11 bits times 8: exact
 #pragma unroll
-                for (int k = 0; k < 8; ++k) x[k] *= f;  // 11 bits times 8: exact
-                if (at.at.page < 0) {                   // (zeros, not minus zeros)
+                for (int k = 0; k < 8; k += 2) mul_f32x2(x[k], x[k + 1], x[k], x[k + 1], f, f);
+                if (!t.codes) {  // (zeros, not minus zeros)
 #pragma unroll
                     for (int k = 0; k < 8; ++k) x[k] = 0.0f;
                 }
             }
-            const KvBlock b(a.L, n);
-            const KvRows& rows = b.which ? a.v : a.k;
-            store_lane<RUNS>(static_cast<T*>(rows.base) + b.element(rows, at.token), sub, wide, x);
+            store_lane<RUNS>(KvBlock(a, n).row(a, t), sub, wide, x);
         }
     }
 }
@@ -295,8 +424,11 @@ int launch_kv(const KvArgs& a, cudaStream_t s)
 {
     const int64_t groups = ((int64_t)a.n_tokens + KV_TOKENS - 1) / KV_TOKENS;
     const dim3 grid((2 * a.L.heads * a.L.nb + 2 * KV_PAIRS - 1) / (2 * KV_PAIRS), (unsigned)(groups < 65535 ? groups : 65535));
+    KvArgs args = a;
+    args.head_bytes = (uint32_t)(a.L.tiles() * a.L.tile_bytes);
+    args.nb_inverse = 0xffffffffu / (uint32_t)a.L.nb + 1;
     auto kern = WRITE ? kv_write_kernel<FMT, T> : kv_read_kernel<FMT, T>;
-    if (launch_pdl(kern, grid, dim3(KV_THREADS), 0, s, a, wait_timeout_counter()) != cudaSuccess)
+    if (launch_pdl(kern, grid, dim3(KV_THREADS), 0, s, args, wait_timeout_counter()) != cudaSuccess)
         return QGEMV_CUDA_ERROR;
     return cudaGetLastError() == cudaSuccess ? QGEMV_OK : QGEMV_CUDA_ERROR;
 }

@@ -148,6 +148,10 @@ struct KvArgs {
     uint8_t* cache;
     KvLayout L;
     int n_tokens;
+    uint32_t head_bytes;  // of a page, for one head
+    // ceil(2^32 / nb), nb > 1: the high word of n times it is n / nb (n below
+    // 2^16 and nb below 2^5 leave an error below 2^-11)
+    uint32_t nb_inverse;
 };
 
 int launch_kv_write(int fmt, int type, const KvArgs& a, cudaStream_t s);
@@ -155,8 +159,10 @@ int launch_kv_read(int fmt, int type, const KvArgs& a, cudaStream_t s);
 
 // ---- attention ---------------------------------------------------------------
 
-constexpr int ATTN_MAX_CTAS = 256;           // counters of the workspace
-constexpr size_t ATTN_COUNTER_BYTES = 1024;  // ATTN_MAX_CTAS words, zero between calls
+constexpr int ATTN_MAX_SPLITS = 2048;
+constexpr size_t ATTN_RECORD_BYTES = (size_t)ATTN_MAX_SPLITS * 12;  // of the workspace, before the partial results
+
+struct AttnRecord;
 
 struct AttnArgs {
     const void* q;
@@ -173,7 +179,7 @@ struct AttnArgs {
     int batch, rows, heads, group;  // group: q heads per kv head
     float scale;
     int window;
-    unsigned int* counters;
+    AttnRecord* records;
     float* partials;
 };
 

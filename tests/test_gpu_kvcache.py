@@ -114,6 +114,41 @@ def test_write_and_read(ops, fmt, kind, heads, dim, page, layout):
     assert torch.equal(torch.nan_to_num(buf[:, :heads, :dim]), torch.nan_to_num(gk)) and not bool(buf[:, heads].any())
 
 
+def border_rows(fmt, kind, n, dim, seed):
+    """Rows of blocks whose values lie on or next to where the code changes, for
+    scales of every size that a type holds."""
+    rng = np.random.default_rng(seed)
+    blocks = n * dim // 32
+    lo, hi = {"float32": (-120, 110), "float16": (-12, 14), "bfloat16": (-120, 110)}[kind]
+    top = np.ldexp(1 + rng.random(blocks), rng.integers(lo, hi, blocks)).astype(np.float32)
+    top[::7] = np.ldexp(1.0, rng.integers(lo, hi, top[::7].size))  # powers of two: exact halves
+    top[3::11] = np.nextafter(2 * top[3::11], np.float32(0)) if kind == "float32" else top[3::11]  # mantissas near all ones
+    steps = 127 if fmt == "q8_0" else 8
+    at = rng.integers(-steps, steps, (blocks, 32)) + 0.5
+    x = (top[:, None].astype(np.float64) * at / steps).astype(np.float32)
+    off = rng.integers(-3, 4, x.shape)  # units of the last place
+    bits = x.view(np.int32) + np.where(x != 0, off, 0).astype(np.int32)
+    x = np.where(rng.random(x.shape) < 0.5, bits.view(np.float32), x)
+    x[:, 0] = top
+    x[::2, 0] *= -1
+    x = torch.from_numpy(x.reshape(n, 1, dim)).to(TYPES[kind])
+    return x
+
+
+@pytest.mark.parametrize("fmt", ["q8_0", "q4_0"])
+@pytest.mark.parametrize("kind", TYPES)
+def test_codes_next_to_a_border(ops, fmt, kind):
+    n, dim, page = 16384, 128, 64
+    k, v = (border_rows(fmt, kind, n, dim, seed) for seed in (1, 2))
+    slots = torch.arange(n, device=DEV)
+    cache = cache_of(ops, fmt, n // page, page, 1, dim)
+    ops.kv_write(cache, k.to(DEV), v.to(DEV), slots, fmt, page)
+    for x, g in zip((k, v), ops.kv_read(cache, slots, fmt, page, 1, dim)):
+        with np.errstate(all="ignore"):
+            want = R.dequantize(*R.quantize(x.float().numpy(), fmt), fmt).astype(np.float32)
+        np.testing.assert_array_equal(g.cpu().numpy(), want)
+
+
 def attention_case(ops, fmt, kind, lens, rows, heads, kv_heads, dim, page, window, seed=0, plant=None, spread=2.0,
                    spare_table=2):
     """(ops arguments, reference): a cache of randomly placed pages, its

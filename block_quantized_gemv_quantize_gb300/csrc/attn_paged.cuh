@@ -54,7 +54,7 @@ enum AttnMode { ATTN_ONE = 0, ATTN_PAIR = 1, ATTN_TWO = 2 };
 inline int attn_mode(int type, int rows) { return type == QGEMV_BF16 ? ATTN_ONE : (rows > 8 ? ATTN_TWO : ATTN_PAIR); }
 
 // Warps that compute (one more copies): as many as 64 K registers hold.
-__host__ __device__ constexpr int attn_warps(int nb) { return 7; }
+__host__ __device__ constexpr int attn_warps(int) { return 7; }
 
 template <int FMT, int NB, int MODE>
 struct AttnShape {
@@ -67,6 +67,7 @@ struct AttnShape {
     static constexpr bool Q_SMEM = NB > 4 || MODE == ATTN_TWO;  // else q's fragments stay in registers
     static constexpr int Q_TERMS = MODE == ATTN_TWO ? 2 : 1;
     static constexpr int WARPS = attn_warps(NB);
+    static constexpr int STEP = 2;                           // tiles of a step without an edge
     static constexpr int UNITS = NB * 2 * NR;                // runs of four output values of a lane
     // where value k of the run (block b, half h, row g + 8 r) stands among a lane's outputs
     __host__ __device__ static constexpr int place(int b, int h, int r, int k)
@@ -103,6 +104,20 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], u
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar)
 {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Whether a phase is over, without waiting.
+__device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
 }
 
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
@@ -360,7 +375,7 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
                                           const int (&end)[AttnShape<FMT, NB, MODE>::NR], int lane)
 {
     using Sh = AttnShape<FMT, NB, MODE>;
-    constexpr int NT = EDGE ? 1 : 2, NR = Sh::NR, NV = 4 * NR, SCALES = NB * KV_TILE * kv_code_bytes(FMT);
+    constexpr int NT = EDGE ? 1 : Sh::STEP, NR = Sh::NR, NV = 4 * NR, SCALES = NB * KV_TILE * kv_code_bytes(FMT);
     const int g = lane >> 2, t = lane & 3;
 
     // ---- scores: y[u][4 r + i], row g + 8 r, token i of the lane's column pairs
@@ -672,6 +687,7 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
     const int g = lane >> 2, t = lane & 3;
     const int warps = p.ws * p.wr;  // those that compute
     const int split = warp / p.wr, wrow = warp - split * p.wr;
+    static_assert(ATTN_GRID * Sh::WARPS <= ATTN_MAX_SPLITS, "a record for every split");
     const int items = a.L.heads * p.row_groups;
     const int S = p.stages;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.off_bar);
@@ -717,49 +733,65 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
     __syncthreads();
 
     if (warp == warps) {
-        // ---- the copies: lane s walks split s's tiles
-        if (lane < p.ws) {
-            const uint64_t policy = l2_evict_first_policy();
-            const int tpp = a.L.tiles();
-            uint8_t* ring = smem + (size_t)lane * S * Sh::TILE;
-            uint64_t *fl = full + lane * S, *em = empty + lane * S;
-            AttnWalk w = s_walk[lane];
-            int at = w.ta, slot = 0, round = 0, issued = 0;
-            bool dead = false, more = !w.done();
-            int pg = -1, page = 0, tile_in = 0, head = 0;
-            auto settle = [&]() {  // on tile `at`, its page's number on the way
-                const int tile = w.first + at, n = tile / tpp;
-                tile_in = tile - n * tpp;
-                if (n != pg) page = a.table[w.b * a.ld_table + n];
-                pg = n;
-                head = w.item / p.row_groups;
-            };
-            if (more) settle();
-            while (more) {
-                const int64_t off = a.L.tile_offset(page, head, tile_in);
-                const bool ok = off >= 0 && QG_OK(qg_in(off, Sh::TILE, a.L.bytes()), status, 731);
-                if (++at >= w.tb) {
-                    const int b = w.b;
-                    w.next(a, items);
-                    at = w.ta;
-                    more = !w.done();
-                    if (w.b != b) pg = -1;
-                }
+        // ---- the copies: lane s walks split s's tiles.  All lanes stay
+        // together: in each round those whose next stage is free issue a copy
+        // (lanes that wait on their own stage, each in a loop of its own, ran
+        // one after the other and bounded the kernel at 150 ns a tile).
+        const uint64_t policy = l2_evict_first_policy();
+        const int tpp = a.L.tiles();
+        const bool mine = lane < p.ws;
+        uint8_t* ring = smem + (size_t)(mine ? lane : 0) * S * Sh::TILE;
+        uint64_t *fl = full + (mine ? lane : 0) * S, *em = empty + (mine ? lane : 0) * S;
+        int* bad = bad_page + (mine ? lane : 0) * S;
+        AttnWalk w{};
+        if (mine) w = s_walk[lane];
+        int at = w.ta, slot = 0, round = 0, issued = 0;
+        bool more = !w.done();
+        // the tile's page and the next one's number, which is on the way early
+        const int32_t* row = a.table;
+        int page = -1, page_next = -1, n = 0, tile_in = 0, head = 0;
+        auto settle = [&]() {  // a segment's first tile
+            const int tile = w.first + at;
+            n = tile / tpp;
+            tile_in = tile - n * tpp;
+            head = w.item / p.row_groups;
+            row = a.table + w.b * a.ld_table;
+            page = row[n];
+            if ((n + 1) * tpp < w.first + w.tb) page_next = row[n + 1];
+        };
+        if (more) settle();
+        int idle = 0;
+        while (__any_sync(0xffffffffu, more)) {
+            const bool go = more && (round == 0 || mbar_test_wait(&em[slot], (round - 1) & 1));
+            if (!__any_sync(0xffffffffu, go)) {
+                if (++idle > (1 << 24)) break;  // a second or more
+                __nanosleep(32);
+                continue;
+            }
+            idle = 0;
+            if (!go) continue;
+            const int64_t off = a.L.tile_offset(page, head, tile_in);
+            const bool ok = off >= 0 && QG_OK(qg_in(off, Sh::TILE, a.L.bytes()), status, 731);
+            bad[slot] = !ok;
+            mbar_arrive_expect_tx(&fl[slot], ok ? Sh::TILE : 0u);
+            if (ok) bulk_g2s(ring + (size_t)slot * Sh::TILE, a.cache + off, Sh::TILE, &fl[slot], policy);
+            ++issued;
+            if (++slot == S) slot = 0, ++round;
+            if (++at >= w.tb) {
+                w.next(a, items);
+                at = w.ta;
+                more = !w.done();
                 if (more) settle();
-                if (round > 0 && !mbar_wait_bounded(&em[slot], (round - 1) & 1)) {
-                    dead = true;
-                    break;
-                }
-                bad_page[lane * S + slot] = !ok;
-                mbar_arrive_expect_tx(&fl[slot], ok ? Sh::TILE : 0u);
-                if (ok) bulk_g2s(ring + (size_t)slot * Sh::TILE, a.cache + off, Sh::TILE, &fl[slot], policy);
-                ++issued;
-                if (++slot == S) slot = 0, ++round;
+            } else if (++tile_in == tpp) {
+                tile_in = 0;
+                ++n;
+                page = page_next;
+                if ((n + 1) * tpp < w.first + w.tb) page_next = row[n + 1];
             }
-            if (dead) {  // its own copies in flight
-                for (int q = issued > S ? issued - S : 0; q < issued; ++q) mbar_wait_bounded(&fl[q % S], (q / S) & 1);
-                atomicAdd_system(status, 1u);
-            }
+        }
+        if (more) {  // gave up: its own copies in flight
+            for (int q = issued > S ? issued - S : 0; q < issued; ++q) mbar_wait_bounded(&fl[q % S], (q / S) & 1);
+            atomicAdd_system(status, 1u);
         }
         return;
     }
@@ -843,10 +875,11 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
             x.pos = (seg.first + tl) * KV_TILE;
             x.first = sp.first();
             x.last = sp.last();
-            const int n = seg.tb - tl >= 2 && x.pos >= clear_from && x.pos + 2 * KV_TILE <= clear_to ? 2 : 1;
+            const bool clear = seg.tb - tl >= Sh::STEP && x.pos >= clear_from && x.pos + Sh::STEP * KV_TILE <= clear_to;
+            const int n = clear ? Sh::STEP : 1;
             int used[2];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < Sh::STEP; ++u) {
                 x.tile[u] = ring + (size_t)slot * Sh::TILE;
                 used[u] = split * S + slot;
                 if (u < n) {
@@ -857,7 +890,7 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
             }
             if (dead) break;
             if (!poison) {  // (a stage without its tile: the rows are NaN whatever comes)
-                if (n == 2) attn_step<FMT, NB, MODE, false>(st, x, qf, q_smem, begin, end, lane);
+                if (clear) attn_step<FMT, NB, MODE, false>(st, x, qf, q_smem, begin, end, lane);
                 else attn_step<FMT, NB, MODE, true>(st, x, qf, q_smem, begin, end, lane);
             }
             __syncwarp();
@@ -929,11 +962,21 @@ __global__ void __launch_bounds__(ATTN_JOIN_WARPS * 32) attn_join_kernel(const A
         if (lane == 0) s_has[w] = has;
     }
     __syncthreads();
-    if ((int)threadIdx.x < words) {
-        int at = 0;
-        for (int w = 0; w < (int)threadIdx.x; ++w) at += __popc(s_has[w]);
-        for (uint32_t has = s_has[threadIdx.x]; has; has &= has - 1) s_split[at++] = threadIdx.x * 32 + __ffs(has) - 1;
-        if ((int)threadIdx.x == words - 1) s_items = at;
+    if (warp == 0) {
+        int before = 0;
+        for (int w0 = 0; w0 < words; w0 += 32) {
+            uint32_t has = w0 + lane < words ? s_has[w0 + lane] : 0u;
+            int sum = __popc(has);
+            const int own = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += up;
+            }
+            for (int at = before + sum - own; has; has &= has - 1) s_split[at++] = (w0 + lane) * 32 + __ffs(has) - 1;
+            before += __shfl_sync(0xffffffffu, sum, 31);
+        }
+        if (lane == 0) s_items = before;
     }
     __syncthreads();
     const int jobs = s_items * p.wr * Sh::UNITS;

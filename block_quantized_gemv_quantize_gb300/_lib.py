@@ -10,6 +10,7 @@ library is missing, importing this module raises: build it first
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -115,8 +116,11 @@ def _check(name: str, status: int) -> None:
         raise QgemvError(name, status)
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream  # (a Stream object for it takes 2 us)
+
+
 def _stream(t: torch.Tensor) -> int:
-    return torch.cuda.current_stream(t.device).cuda_stream
+    return _raw_stream(t.get_device())
 
 
 def _dev(t: torch.Tensor, what: str) -> int:
@@ -160,9 +164,13 @@ _ws_cache: dict[tuple, torch.Tensor] = {}
 def workspace(device: torch.device, nbytes: int, key: str = "top1") -> torch.Tensor:
     """A zero-filled device workspace, one per (device, stream, key); the
     kernels leave it zero-filled after every call."""
-    device = torch.device(device)
-    stream = torch.cuda.current_stream(device).cuda_stream
-    k = (device.index, stream, key)
+    index = torch.device(device).index
+    if index is None:
+        index = torch.cuda.current_device()
+    k = (index, _raw_stream(index), key)
+    ws = _ws_cache.get(k)
+    if ws is not None and ws.numel() >= nbytes:
+        return ws
     with _ws_lock:
         ws = _ws_cache.get(k)
         if ws is None or ws.numel() < nbytes:
@@ -447,18 +455,23 @@ def _kv_format(fmt: str) -> int:
 
 
 def _type(t: torch.Tensor, what: str) -> int:
-    if t.dtype not in _TYPES:
+    code = _TYPES.get(t.dtype)
+    if code is None:
         raise ValueError(f"{what} must be float32, float16 or bfloat16, not {t.dtype}")
-    return _TYPES[t.dtype]
+    return code
 
 
-def _rows(t: torch.Tensor, what: str, like: torch.Tensor | None = None) -> int:
-    """A CUDA tensor [tokens, heads, head_dim] with contiguous rows; any strides between them."""
-    if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+def _rows(t: torch.Tensor, what: str, like: torch.Tensor | None = None) -> tuple[int, int, int]:
+    """(address, strides of the first two dimensions) of a CUDA tensor
+    [tokens, heads, head_dim] with contiguous rows; any strides between them."""
+    strides = t.stride()
+    if len(strides) != 3 or (strides[2] != 1 and t.shape[2] > 1):
         raise ValueError(f"{what} must be [tokens, heads, head_dim] with contiguous rows")
     if like is not None and (t.shape != like.shape or t.dtype != like.dtype or t.device != like.device):
         raise ValueError(f"{what} must have the shape, type and device of its companion")
-    return _dev(t, what)
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    return t.data_ptr(), strides[0], strides[1]
 
 
 def _kv_cache(cache: torch.Tensor, fmt: str, page_tokens: int, n_kv_heads: int, head_dim: int, near: torch.Tensor):
@@ -466,11 +479,12 @@ def _kv_cache(cache: torch.Tensor, fmt: str, page_tokens: int, n_kv_heads: int, 
     size = kv_page_bytes(fmt, page_tokens, n_kv_heads, head_dim)
     if size == 0:
         raise ValueError(f"no such cache: pages of {page_tokens} tokens, {n_kv_heads} kv heads of {head_dim}")
-    if cache.dtype != torch.uint8 or not cache.is_contiguous() or cache.numel() == 0 or cache.numel() % size:
+    pages, rest = divmod(cache.numel(), size)
+    if cache.dtype != torch.uint8 or not cache.is_contiguous() or pages == 0 or rest:
         raise ValueError(f"cache must be contiguous uint8, a whole number of pages of {size} bytes")
     if cache.device != near.device:
         raise ValueError("cache is on another device")
-    return _dev(cache, "cache"), cache.numel() // size
+    return _dev(cache, "cache"), pages
 
 
 def _kv_slots(slots: torch.Tensor, near: torch.Tensor) -> int:
@@ -479,6 +493,7 @@ def _kv_slots(slots: torch.Tensor, near: torch.Tensor) -> int:
     return _dev(slots, "slots")
 
 
+@functools.lru_cache(maxsize=1024)
 def kv_page_bytes(fmt: str, page_tokens: int, n_kv_heads: int, head_dim: int) -> int:
     """Bytes of one page of the cache; 0 for sizes that the calls refuse."""
     return LIB.kv_page_bytes(_kv_format(fmt), page_tokens, n_kv_heads, head_dim)
@@ -495,16 +510,17 @@ def kv_write(cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slots: torch
     """Quantize k, v [tokens, kv heads, head_dim] into the cache (uint8, whole
     pages of kv_page_bytes) at slots (int64 [tokens]; a slot outside the cache
     skips its token).  k and v may be slices with any strides between rows."""
-    kp, vp = _rows(k, "k"), _rows(v, "v", like=k)
+    kp, k0, k1 = _rows(k, "k")
+    vp, v0, v1 = _rows(v, "v", like=k)
     n, heads, dim = k.shape
     cp, pages = _kv_cache(cache, fmt, page_tokens, heads, dim, k)
     sp = _kv_slots(slots, k)
-    if slots.numel() != n:
+    if slots.shape[0] != n:
         raise ValueError(f"{slots.numel()} slots for {n} tokens")
     if n == 0:
         return
-    _check("kv_write", LIB.kv_write(_kv_format(fmt), _type(k, "k"), kp, k.stride(0), k.stride(1), vp, v.stride(0),
-                                    v.stride(1), sp, cp, pages, page_tokens, n, heads, dim, _stream(k)))
+    _check("kv_write", LIB.kv_write(KV_FORMATS[fmt], _type(k, "k"), kp, k0, k1, vp, v0, v1, sp, cp, pages, page_tokens,
+                                    n, heads, dim, _stream(k)))
 
 
 def kv_read(cache: torch.Tensor, slots: torch.Tensor, fmt: str, page_tokens: int, n_kv_heads: int, head_dim: int,
@@ -512,21 +528,24 @@ def kv_read(cache: torch.Tensor, slots: torch.Tensor, fmt: str, page_tokens: int
     """(k, v) [tokens, kv heads, head_dim]: the values of the cache's slots
     (zeros for a slot outside the cache), in dtype or into the given tensors."""
     n = slots.numel()
+    shape = (n, n_kv_heads, head_dim)
     if k is None:
-        k = torch.empty((n, n_kv_heads, head_dim), dtype=dtype if v is None else v.dtype, device=cache.device)
-    if v is None:
-        v = torch.empty((n, n_kv_heads, head_dim), dtype=k.dtype, device=cache.device)
-    if k.shape != (n, n_kv_heads, head_dim):
+        k = torch.empty(shape, dtype=dtype if v is None else v.dtype, device=cache.device)
+    elif k.shape != shape:
         raise ValueError(f"k must be [{n}, {n_kv_heads}, {head_dim}]")
-    kp, vp = _rows(k, "k"), _rows(v, "v", like=k)
+    if v is None:
+        v = torch.empty(shape, dtype=k.dtype, device=cache.device)
+    kp, k0, k1 = _rows(k, "k")
+    vp, v0, v1 = _rows(v, "v", like=k)
     cp, pages = _kv_cache(cache, fmt, page_tokens, n_kv_heads, head_dim, k)
     sp = _kv_slots(slots, k)
     if n:
-        _check("kv_read", LIB.kv_read(_kv_format(fmt), _type(k, "k"), cp, pages, page_tokens, sp, kp, k.stride(0),
-                                      k.stride(1), vp, v.stride(0), v.stride(1), n, n_kv_heads, head_dim, _stream(k)))
+        _check("kv_read", LIB.kv_read(KV_FORMATS[fmt], _type(k, "k"), cp, pages, page_tokens, sp, kp, k0, k1, vp, v0,
+                                      v1, n, n_kv_heads, head_dim, _stream(k)))
     return k, v
 
 
+@functools.lru_cache(maxsize=1024)
 def attn_paged_workspace_bytes(dtype: torch.dtype, rows: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
     if dtype not in _TYPES:
         raise ValueError(f"dtype must be float32, float16 or bfloat16, not {dtype}")
@@ -541,35 +560,44 @@ def attn_paged(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, k
     of each sequence, over the first kv_lens[b] (int32 [batch]) tokens of the
     cache that page_table (int32 [batch, pages]) maps; causal among the new
     rows, with an optional sliding window.  scale defaults to head_dim^-1/2;
-    lse (fp32 [batch * rows, heads]) receives the rows' log-sum-exp."""
-    qp = _rows(q, "q")
+    lse (fp32 [batch * rows, heads]) receives the rows' log-sum-exp; ws (uint8,
+    attn_paged_workspace_bytes) is scratch that calls in flight do not share."""
+    qp, q0, q1 = _rows(q, "q")
     n, heads, dim = q.shape
+    device = q.device
     if out is None:
-        out = torch.empty((n, heads, dim), dtype=q.dtype, device=q.device)
-    op = _rows(out, "out", like=q)
+        out = torch.empty((n, heads, dim), dtype=q.dtype, device=device)
+        op, o0, o1 = out.data_ptr(), heads * dim, dim
+    else:
+        op, o0, o1 = _rows(out, "out", like=q)
     cp, pages = _kv_cache(cache, fmt, page_tokens, n_kv_heads, dim, q)
-    for t, what, d in ((page_table, "page_table", 2), (kv_lens, "kv_lens", 1)):
-        if t.dtype != torch.int32 or t.dim() != d or (t.shape[-1] > 1 and t.stride(-1) != 1) or t.device != q.device:
-            raise ValueError(f"{what} must be int32 with {d} dimension(s), contiguous in the last, on q's device")
-    batch = kv_lens.numel()
-    if rows < 1 or n != batch * rows or page_table.shape[0] != batch:
-        raise ValueError(f"q has {n} rows: {batch} sequences of {rows} need {batch * rows}, and as many table rows")
+    ld = page_table.stride()
+    if page_table.dtype != torch.int32 or len(ld) != 2 or (ld[1] != 1 and page_table.shape[1] > 1) \
+            or page_table.device != device:
+        raise ValueError("page_table must be int32 [batch, pages], contiguous in the last, on q's device")
+    if kv_lens.dtype != torch.int32 or kv_lens.dim() != 1 or not kv_lens.is_contiguous() or kv_lens.device != device:
+        raise ValueError("kv_lens must be contiguous int32 [batch] on q's device")
+    batch, max_pages = page_table.shape
+    if rows < 1 or n != batch * rows or kv_lens.shape[0] != batch:
+        raise ValueError(f"q has {n} rows, kv_lens {kv_lens.shape[0]} and page_table {batch}: one length and one table "
+                         f"row for each {rows} rows of q")
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (n, heads) or not lse.is_contiguous()
-                            or lse.device != q.device):
+                            or lse.device != device):
         raise ValueError(f"lse must be contiguous float32 [{n}, {heads}] on q's device")
-    need = attn_paged_workspace_bytes(q.dtype, rows, heads, n_kv_heads, dim)
     if batch == 0:
         return out
     if ws is None:
-        # one that a capture allocates belongs to its graph, whose replays clear it
-        ws = torch.zeros(max(need, 256), dtype=torch.uint8, device=q.device) \
-            if torch.cuda.is_current_stream_capturing() else workspace(q.device, need, key="attn")
-    ld = page_table.stride(0) if batch > 1 else max(page_table.stride(0), page_table.shape[1])
+        need = attn_paged_workspace_bytes(q.dtype, rows, heads, n_kv_heads, dim)
+        # (one that a capture allocates belongs to its graph)
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=device) \
+            if torch.cuda.is_current_stream_capturing() else workspace(device, need, key="attn")
+    elif ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError("ws must be contiguous uint8 on q's device")
     _check("attn_paged", LIB.attn_paged(
-        _kv_format(fmt), _type(q, "q"), qp, q.stride(0), q.stride(1), cp, pages, page_tokens,
-        _dev(page_table, "page_table"), ld, page_table.shape[1], _dev(kv_lens, "kv_lens"), op, out.stride(0),
-        out.stride(1), None if lse is None else _dev(lse, "lse"), _dev(ws, "workspace"), ws.numel(), batch, rows, heads,
-        n_kv_heads, dim, dim ** -0.5 if scale is None else scale, window, _stream(q)))
+        KV_FORMATS[fmt], _type(q, "q"), qp, q0, q1, cp, pages, page_tokens, page_table.data_ptr(),
+        ld[0] if batch > 1 else max(ld[0], max_pages), max_pages, kv_lens.data_ptr(), op, o0, o1,
+        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), batch, rows, heads, n_kv_heads, dim,
+        dim ** -0.5 if scale is None else scale, window, _stream(q)))
     return out
 
 

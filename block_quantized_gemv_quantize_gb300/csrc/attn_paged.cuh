@@ -949,6 +949,7 @@ __global__ void __launch_bounds__(ATTN_JOIN_WARPS * 32) attn_join_kernel(const A
     using Sh = AttnShape<FMT, NB, MODE>;
     constexpr int NR = Sh::NR;
     __shared__ int s_split[ATTN_MAX_SPLITS], s_items;
+    __shared__ AttnRecord s_rec[ATTN_MAX_SPLITS];
     __shared__ uint32_t s_has[ATTN_MAX_SPLITS / 32];
     __shared__ float s_sum[ATTN_JOIN_WARPS][6][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -958,7 +959,9 @@ __global__ void __launch_bounds__(ATTN_JOIN_WARPS * 32) attn_join_kernel(const A
     const int words = (p.splits + 31) / 32;
     for (int w = warp; w < words; w += ATTN_JOIN_WARPS) {
         const int i = w * 32 + lane;
-        const uint32_t has = __ballot_sync(0xffffffffu, i < p.splits && a.records[i].parts > 0);
+        const AttnRecord rec = i < p.splits ? a.records[i] : AttnRecord{0, 0, 0};
+        s_rec[i] = rec;
+        const uint32_t has = __ballot_sync(0xffffffffu, rec.parts > 0);
         if (lane == 0) s_has[w] = has;
     }
     __syncthreads();
@@ -992,7 +995,7 @@ __global__ void __launch_bounds__(ATTN_JOIN_WARPS * 32) attn_join_kernel(const A
         AttnRecord rec{0, 0, 0};
         if (job < jobs) {
             const int s0 = s_split[job / (p.wr * Sh::UNITS)];
-            rec = a.records[s0];
+            rec = s_rec[s0];
 #pragma unroll 4
             for (int i = part0; i < rec.parts; i += per) {
                 const float* from = attn_part(a, p, s0 + i, i == 0, tile, Sh::PART) + lane;

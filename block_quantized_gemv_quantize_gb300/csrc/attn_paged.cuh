@@ -1085,7 +1085,7 @@ int launch_attn(const AttnArgs& a, cudaStream_t s)
     if (launch_pdl(kern, dim3(p.splits / p.ws), dim3((p.ws * p.wr + 1) * 32), p.bytes, s, a, p, wait_timeout_counter()) !=
         cudaSuccess)
         return QGEMV_CUDA_ERROR;
-    if (launch_pdl(attn_join_kernel<FMT, NB, MODE, T>, dim3(di.sms), dim3(ATTN_JOIN_WARPS * 32), 0, s, a, p) != cudaSuccess)
+    if (launch_pdl(attn_join_kernel<FMT, NB, MODE, T>, dim3(2 * di.sms), dim3(ATTN_JOIN_WARPS * 32), 0, s, a, p) != cudaSuccess)
         return QGEMV_CUDA_ERROR;
     return cudaGetLastError() == cudaSuccess ? QGEMV_OK : QGEMV_CUDA_ERROR;
 }

@@ -80,6 +80,7 @@ struct AttnShape {
 
 struct AttnPlan {
     int splits;          // of the whole grid
+    uint32_t magic;      // attn_magic
     int ws, wr;          // splits, row tiles at a time
     int row_groups;
     int stages;          // tiles a ring holds
@@ -124,21 +125,25 @@ __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cas
 __device__ __forceinline__ __half2 bits_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 
 // Codes to fp16 without a conversion: 0x6400 | n is the fp16 number 1024 + n.
+// The 0x64 bytes (`magic`) are an argument of the kernel, which the compiler does
+// not see through: an instruction has room for one constant, so with two of them
+// it would spend a second instruction on every word.
+constexpr uint32_t attn_magic(int fmt) { return fmt == QGEMV_KV_Q8_0 ? 0x64646464u : 0x64006400u; }
 // Two bytes of w, as 1024 + byte (code + 128), less 1152.
 template <int SEL>
-__device__ __forceinline__ uint32_t codes_q8(uint32_t w)
+__device__ __forceinline__ uint32_t codes_q8(uint32_t w, uint32_t magic)
 {
-    return h2_bits(__hsub2(bits_h2(__byte_perm(w, 0x64646464u, SEL)), bits_h2(0x64806480u)));
+    return h2_bits(__hsub2(bits_h2(__byte_perm(w, magic, SEL)), bits_h2(0x64806480u)));
 }
 // The low nibbles of bytes 0 and 2: 1024 + code less 1032 (code - 8).
-__device__ __forceinline__ uint32_t codes_q4_lo(uint32_t w)
+__device__ __forceinline__ uint32_t codes_q4_lo(uint32_t w, uint32_t magic)
 {
-    return h2_bits(__hsub2(bits_h2((w & 0x000F000Fu) | 0x64006400u), bits_h2(0x64086408u)));
+    return h2_bits(__hsub2(bits_h2((w & 0x000F000Fu) | magic), bits_h2(0x64086408u)));
 }
 // Their high nibbles: (1024 + 16 code) / 16 - 72, exact in one fma.
-__device__ __forceinline__ uint32_t codes_q4_hi(uint32_t w)
+__device__ __forceinline__ uint32_t codes_q4_hi(uint32_t w, uint32_t magic)
 {
-    return h2_bits(__hfma2(bits_h2((w & 0x00F000F0u) | 0x64006400u), bits_h2(0x2C002C00u), bits_h2(0xD480D480u)));
+    return h2_bits(__hfma2(bits_h2((w & 0x00F000F0u) | magic), bits_h2(0x2C002C00u), bits_h2(0xD480D480u)));
 }
 
 // The four tokens of a tile that column pair t of the products holds: i = 0..3
@@ -150,7 +155,7 @@ __device__ __forceinline__ int tile_token(int t, int i) { return 4 * i + (t ^ (3
 // 8 t .. 8 t + 7 of the lane's token (q8_0, f16); or (q4_0) 4 t + {0, 2, 1, 3},
 // then 16 + 4 t + {0, 2, 1, 3}.  q's fragments follow the same order.
 template <int FMT>
-__device__ __forceinline__ void k_fragment(const uint8_t* k, int b, int tok, int t, uint32_t (&f)[4])
+__device__ __forceinline__ void k_fragment(const uint8_t* k, int b, int tok, int t, uint32_t magic, uint32_t (&f)[4])
 {
     const uint8_t* p = k + (b * KV_TILE + tok) * kv_code_bytes(FMT) + t * (kv_code_bytes(FMT) / 4);
     if constexpr (FMT == QGEMV_KV_F16) {
@@ -158,11 +163,11 @@ __device__ __forceinline__ void k_fragment(const uint8_t* k, int b, int tok, int
         f[0] = w.x, f[1] = w.y, f[2] = w.z, f[3] = w.w;
     } else if constexpr (FMT == QGEMV_KV_Q8_0) {
         const uint2 w = *reinterpret_cast<const uint2*>(p);
-        f[0] = codes_q8<0x4140>(w.x), f[1] = codes_q8<0x4342>(w.x);
-        f[2] = codes_q8<0x4140>(w.y), f[3] = codes_q8<0x4342>(w.y);
+        f[0] = codes_q8<0x4140>(w.x, magic), f[1] = codes_q8<0x4342>(w.x, magic);
+        f[2] = codes_q8<0x4140>(w.y, magic), f[3] = codes_q8<0x4342>(w.y, magic);
     } else {
         const uint32_t w = *reinterpret_cast<const uint32_t*>(p), v = w >> 8;
-        f[0] = codes_q4_lo(w), f[1] = codes_q4_lo(v), f[2] = codes_q4_hi(w), f[3] = codes_q4_hi(v);
+        f[0] = codes_q4_lo(w, magic), f[1] = codes_q4_lo(v, magic), f[2] = codes_q4_hi(w, magic), f[3] = codes_q4_hi(v, magic);
     }
 }
 
@@ -170,7 +175,8 @@ __device__ __forceinline__ void k_fragment(const uint8_t* k, int b, int tok, int
 // lo, (2, 3) in hi; column n of tile nn is the block's value 4 n + nn, or (q4_0)
 // 2 n + {0, 16, 1, 17}[nn].
 template <int FMT>
-__device__ __forceinline__ void v_fragments(const uint8_t* v, int b, int g, int t, uint32_t (&lo)[4], uint32_t (&hi)[4])
+__device__ __forceinline__ void v_fragments(const uint8_t* v, int b, int g, int t, uint32_t magic, uint32_t (&lo)[4],
+                                            uint32_t (&hi)[4])
 {
     const uint8_t* p = v + b * KV_TILE * kv_code_bytes(FMT) + g * (kv_code_bytes(FMT) / 8);
     auto at = [&](int i) { return p + tile_token(t, i) * kv_code_bytes(FMT); };
@@ -187,17 +193,17 @@ __device__ __forceinline__ void v_fragments(const uint8_t* v, int b, int g, int 
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint32_t*>(at(i));
         uint32_t x = __byte_perm(w[0], w[1], 0x5140), y = __byte_perm(w[0], w[1], 0x7362);
-        lo[0] = codes_q8<0x4140>(x), lo[1] = codes_q8<0x4342>(x), lo[2] = codes_q8<0x4140>(y), lo[3] = codes_q8<0x4342>(y);
+        lo[0] = codes_q8<0x4140>(x, magic), lo[1] = codes_q8<0x4342>(x, magic), lo[2] = codes_q8<0x4140>(y, magic), lo[3] = codes_q8<0x4342>(y, magic);
         x = __byte_perm(w[2], w[3], 0x5140), y = __byte_perm(w[2], w[3], 0x7362);
-        hi[0] = codes_q8<0x4140>(x), hi[1] = codes_q8<0x4342>(x), hi[2] = codes_q8<0x4140>(y), hi[3] = codes_q8<0x4342>(y);
+        hi[0] = codes_q8<0x4140>(x, magic), hi[1] = codes_q8<0x4342>(x, magic), hi[2] = codes_q8<0x4140>(y, magic), hi[3] = codes_q8<0x4342>(y, magic);
     } else {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint16_t*>(at(i));
         uint32_t x = __byte_perm(w[0], w[1], 0x5410), y = x >> 8;
-        lo[0] = codes_q4_lo(x), lo[1] = codes_q4_hi(x), lo[2] = codes_q4_lo(y), lo[3] = codes_q4_hi(y);
+        lo[0] = codes_q4_lo(x, magic), lo[1] = codes_q4_hi(x, magic), lo[2] = codes_q4_lo(y, magic), lo[3] = codes_q4_hi(y, magic);
         x = __byte_perm(w[2], w[3], 0x5410), y = x >> 8;
-        hi[0] = codes_q4_lo(x), hi[1] = codes_q4_hi(x), hi[2] = codes_q4_lo(y), hi[3] = codes_q4_hi(y);
+        hi[0] = codes_q4_lo(x, magic), hi[1] = codes_q4_hi(x, magic), hi[2] = codes_q4_lo(y, magic), hi[3] = codes_q4_hi(y, magic);
     }
 }
 
@@ -319,6 +325,7 @@ struct AttnState {
     float m[Sh::NR], l[Sh::NR], rs[Sh::NR];
     float o[NB][4][4];
     int e;
+    uint32_t magic;
 
     __device__ __forceinline__ void clear()
     {
@@ -393,7 +400,7 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
 #pragma unroll
         for (int u = u0; u < u1; ++u) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) k_fragment<FMT>(x.tile[u], b, tile_token(g >> 1, 2 * j + (g & 1)), t, f[u][j]);
+            for (int j = 0; j < 2; ++j) k_fragment<FMT>(x.tile[u], b, tile_token(g >> 1, 2 * j + (g & 1)), t, st.magic, f[u][j]);
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s)
@@ -589,7 +596,7 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
                 weights(d);
             }
             uint32_t v0[4], v1[4];
-            v_fragments<FMT>(v8, b, g, t, v0, v1);
+            v_fragments<FMT>(v8, b, g, t, st.magic, v0, v1);
             if constexpr (FMT == QGEMV_KV_F16 && EDGE) {
 #pragma unroll
                 for (int nn = 0; nn < 4; ++nn) {
@@ -803,6 +810,7 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
     int slot = 0, phase = 0;
     bool dead = false;
     AttnState<FMT, NB, MODE> st;
+    st.magic = p.magic;
     AttnRecord record{0, 0, 0};
 
     for (; !seg.done(); seg.next(a, items)) {
@@ -1044,6 +1052,7 @@ AttnPlan attn_plan(const DeviceInfo& di, int rows)
 {
     using Sh = AttnShape<FMT, NB, MODE>;
     AttnPlan p{};
+    p.magic = attn_magic(FMT);
     const int tiles = (rows + Sh::ROWS - 1) / Sh::ROWS;
     p.row_groups = (tiles + Sh::WARPS - 1) / Sh::WARPS;
     p.wr = (tiles + p.row_groups - 1) / p.row_groups;

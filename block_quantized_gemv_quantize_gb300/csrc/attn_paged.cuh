@@ -27,7 +27,8 @@
 // pieces, one a split: the load is even however the lengths differ, and the
 // lengths are read on the device, so that a captured graph serves any.  A CTA
 // has WS splits; each streams its piece through a ring of its own in shared
-// memory that bulk copies fill (a tile of a kv head is contiguous: one copy),
+// memory that bulk copies fill, two tiles a stage (tiles of a kv head follow one
+// another in a page: one copy for both, or two where a page ends between them),
 // and WR warps share the ring, one for every tile of rows.  One more warp issues
 // the copies, a lane a ring.  A split writes the outputs of an item that it has
 // whole; of one that it shares it leaves a partial result (at most two) in the
@@ -45,7 +46,7 @@ namespace qgemv {
 
 constexpr int ATTN_GRID = 160;     // most CTAs (one an SM): the workspace holds their partial results
 constexpr int ATTN_JOIN_WARPS = 16;  // of a CTA of the joining kernel
-constexpr int ATTN_ITEM_COST = 4;  // of an item besides its tiles, in tiles
+constexpr int ATTN_ITEM_COST = 4;  // of an item besides its tiles, in tiles (even)
 constexpr int ATTN_MIN_PIECE = 4;  // least units of a split: shorter ones cost more to join than they save
 
 enum AttnMode { ATTN_ONE = 0, ATTN_PAIR = 1, ATTN_TWO = 2 };
@@ -83,7 +84,7 @@ struct AttnPlan {
     uint32_t magic;      // attn_magic
     int ws, wr;          // splits, row tiles at a time
     int row_groups;
-    int stages;          // tiles a ring holds
+    int stages;          // pairs of tiles a ring holds
     uint32_t off_q, off_bar, bytes;  // shared memory
 };
 
@@ -218,6 +219,10 @@ struct AttnTiles {
     }
 };
 
+// Units of an item on the line: even, as the pieces are, so that a split starts
+// at an even tile of an item and takes its tiles in pairs.
+__host__ __device__ constexpr int attn_item_units(int count) { return ATTN_ITEM_COST + count + (count & 1); }
+
 // A split's walk over its piece of the line: segments, each a run of one item's
 // tiles.
 struct AttnWalk {
@@ -230,10 +235,10 @@ struct AttnWalk {
     __device__ __forceinline__ bool done() const { return left <= 0; }
     __device__ __forceinline__ void clip(int off)
     {
-        const int units = ATTN_ITEM_COST + count - off;
+        const int units = attn_item_units(count) - off;
         used = left < (int64_t)units ? (int)left : units;
         ta = max(0, off - ATTN_ITEM_COST);
-        tb = max(0, off + used - ATTN_ITEM_COST);
+        tb = min(count, max(0, off + used - ATTN_ITEM_COST));
     }
     // to the next segment with tiles in it
     __device__ __forceinline__ void next(const AttnArgs& a, int items)
@@ -241,7 +246,7 @@ struct AttnWalk {
         do {
             left -= used;
             if (left <= 0) return;
-            line += ATTN_ITEM_COST + count;
+            line += attn_item_units(count);
             if (++item == items) {
                 item = 0;
                 do {
@@ -251,13 +256,13 @@ struct AttnWalk {
                 } while (count == 0);
             }
             clip(0);
-        } while (tb == 0);
+        } while (tb <= ta);
     }
 };
 
 __device__ __forceinline__ int64_t attn_units(const AttnTiles& t, int items)
 {
-    return t.count ? (int64_t)(t.count + ATTN_ITEM_COST) * items : 0;
+    return t.count ? (int64_t)attn_item_units(t.count) * items : 0;
 }
 
 // By one warp: the length of the line, and the walk that starts at its unit
@@ -294,10 +299,10 @@ __device__ __forceinline__ AttnWalk attn_find(const AttnArgs& a, int items, int6
             w.b = b0 + src;
             w.first = __shfl_sync(0xffffffffu, t.first, src);
             w.count = __shfl_sync(0xffffffffu, t.count, src);
-            w.item = (int)((start - at) / (w.count + ATTN_ITEM_COST));
-            w.line = at + (int64_t)w.item * (w.count + ATTN_ITEM_COST);
+            w.item = (int)((start - at) / attn_item_units(w.count));
+            w.line = at + (int64_t)w.item * attn_item_units(w.count);
             w.clip((int)(start - w.line));
-            if (w.tb == 0) w.next(a, items);
+            if (w.tb <= w.ta) w.next(a, items);
             return w;
         }
         before += __shfl_sync(0xffffffffu, sum, 31);
@@ -368,8 +373,8 @@ __device__ __forceinline__ float attn_base(float m) { return m == -INFINITY ? 0.
 
 // What one step needs to know of its tiles.
 struct AttnStep {
-    const uint8_t* tile[2];
-    int pos;          // position of the first tile's first token
+    const uint8_t* tile;  // the first one's, the other behind it
+    int pos;          // position of its first token
     int first, last;  // positions that any row sees
 };
 
@@ -400,7 +405,7 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
 #pragma unroll
         for (int u = u0; u < u1; ++u) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) k_fragment<FMT>(x.tile[u], b, tile_token(g >> 1, 2 * j + (g & 1)), t, st.magic, f[u][j]);
+            for (int j = 0; j < 2; ++j) k_fragment<FMT>(x.tile + u * Sh::TILE, b, tile_token(g >> 1, 2 * j + (g & 1)), t, st.magic, f[u][j]);
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s)
@@ -424,7 +429,7 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
         if constexpr (FMT != QGEMV_KV_F16) {
 #pragma unroll
             for (int u = u0; u < u1; ++u) {
-                    const uint2 w = *reinterpret_cast<const uint2*>(x.tile[u] + SCALES + b * 32 + 8 * t);
+                    const uint2 w = *reinterpret_cast<const uint2*>(x.tile + u * Sh::TILE + SCALES + b * 32 + 8 * t);
                 const float2 d[2] = {__half22float2(bits_h2(w.x)), __half22float2(bits_h2(w.y))};
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
@@ -492,7 +497,7 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
         for (int u = 0; u < NT; ++u) {
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                uint2 w = *reinterpret_cast<const uint2*>(x.tile[u] + Sh::HALF + SCALES + b * 32 + 8 * t);
+                uint2 w = *reinterpret_cast<const uint2*>(x.tile + u * Sh::TILE + Sh::HALF + SCALES + b * 32 + 8 * t);
                 if (EDGE) w.x &= live[u][0], w.y &= live[u][1];
                 if (FMT == QGEMV_KV_Q4_0) w.x &= 0x7fff7fffu, w.y &= 0x7fff7fffu;  // q8_0's are never negative
                 top = __hmax2(top, __hmax2(bits_h2(w.x), bits_h2(w.y)));
@@ -559,7 +564,7 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
     // ---- outputs
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
-        const uint8_t* v8 = x.tile[u] + Sh::HALF;
+        const uint8_t* v8 = x.tile + u * Sh::TILE + Sh::HALF;
         uint32_t hi[4], lo[4];  // A fragments; ATTN_PAIR: hi alone, with the low terms in its upper rows
         auto weights = [&](const float2 (&d)[2]) {
             float w[NV];
@@ -697,6 +702,7 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
     static_assert(ATTN_GRID * Sh::WARPS <= ATTN_MAX_SPLITS, "a record for every split");
     const int items = a.L.heads * p.row_groups;
     const int S = p.stages;
+    constexpr int STAGE = 2 * Sh::TILE;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.off_bar);
     uint64_t* empty = full + p.ws * S;
     int* bad_page = reinterpret_cast<int*>(empty + p.ws * S);
@@ -714,6 +720,7 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
     // the line, and this split's piece of it
     const int64_t total = attn_total(a, items, lane);
     int64_t piece = (total + p.splits - 1) / p.splits;
+    piece += piece & 1;
     if (piece < ATTN_MIN_PIECE) piece = ATTN_MIN_PIECE;
     const int split_id = blockIdx.x * p.ws + split;
     AttnWalk seg{};
@@ -747,7 +754,7 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
         const uint64_t policy = l2_evict_first_policy();
         const int tpp = a.L.tiles();
         const bool mine = lane < p.ws;
-        uint8_t* ring = smem + (size_t)(mine ? lane : 0) * S * Sh::TILE;
+        uint8_t* ring = smem + (size_t)(mine ? lane : 0) * S * STAGE;
         uint64_t *fl = full + (mine ? lane : 0) * S, *em = empty + (mine ? lane : 0) * S;
         int* bad = bad_page + (mine ? lane : 0) * S;
         AttnWalk w{};
@@ -757,6 +764,9 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
         // the tile's page and the next one's number, which is on the way early
         const int32_t* row = a.table;
         int page = -1, page_next = -1, n = 0, tile_in = 0, head = 0;
+        auto after = [&]() {  // the number of page n + 1, if the segment has tiles there
+            if ((n + 1) * tpp < w.first + w.tb) page_next = row[n + 1];
+        };
         auto settle = [&]() {  // a segment's first tile
             const int tile = w.first + at;
             n = tile / tpp;
@@ -764,7 +774,7 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
             head = w.item / p.row_groups;
             row = a.table + w.b * a.ld_table;
             page = row[n];
-            if ((n + 1) * tpp < w.first + w.tb) page_next = row[n + 1];
+            after();
         };
         if (more) settle();
         int idle = 0;
@@ -777,23 +787,38 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
             }
             idle = 0;
             if (!go) continue;
+            const int two = w.tb - at >= 2, apart = two && tile_in + 1 == tpp;
             const int64_t off = a.L.tile_offset(page, head, tile_in);
-            const bool ok = off >= 0 && QG_OK(qg_in(off, Sh::TILE, a.L.bytes()), status, 731);
+            const int64_t off2 = apart ? a.L.tile_offset(page_next, head, 0) : off;
+            const bool ok = off >= 0 && off2 >= 0 &&
+                            QG_OK(qg_in(off, apart ? Sh::TILE : (1 + two) * Sh::TILE, a.L.bytes()) &&
+                                      qg_in(off2, Sh::TILE, a.L.bytes()), status, 731);
             bad[slot] = !ok;
-            mbar_arrive_expect_tx(&fl[slot], ok ? Sh::TILE : 0u);
-            if (ok) bulk_g2s(ring + (size_t)slot * Sh::TILE, a.cache + off, Sh::TILE, &fl[slot], policy);
+            mbar_arrive_expect_tx(&fl[slot], ok ? (1 + two) * Sh::TILE : 0u);
+            if (ok) {
+                uint8_t* to = ring + (size_t)slot * STAGE;
+                bulk_g2s(to, a.cache + off, two && !apart ? 2 * Sh::TILE : Sh::TILE, &fl[slot], policy);
+                if (apart) bulk_g2s(to + Sh::TILE, a.cache + off2, Sh::TILE, &fl[slot], policy);
+            }
             ++issued;
             if (++slot == S) slot = 0, ++round;
-            if (++at >= w.tb) {
+            at += 1 + two;
+            if (at >= w.tb) {
                 w.next(a, items);
                 at = w.ta;
                 more = !w.done();
                 if (more) settle();
-            } else if (++tile_in == tpp) {
-                tile_in = 0;
-                ++n;
-                page = page_next;
-                if ((n + 1) * tpp < w.first + w.tb) page_next = row[n + 1];
+            } else if ((tile_in += 2) >= tpp) {
+                if (tpp == 1) {
+                    n += 2;
+                    page = row[n];
+                    tile_in = 0;
+                } else {
+                    ++n;
+                    page = page_next;
+                    tile_in -= tpp;
+                }
+                after();
             }
         }
         if (more) {  // gave up: its own copies in flight
@@ -804,7 +829,7 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
     }
 
     // ---- the warps that compute
-    const uint8_t* ring = smem + (size_t)split * S * Sh::TILE;
+    const uint8_t* ring = smem + (size_t)split * S * STAGE;
     uint4* q_smem = reinterpret_cast<uint4*>(smem + p.off_q) + warp * (NB * 2 * Sh::Q_TERMS * 32) + lane;
     const bool q_wide = KvRows{const_cast<void*>(a.q), a.q_row, a.q_head}.wide<T>();
     int slot = 0, phase = 0;
@@ -878,33 +903,32 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
         bool poison = false;
         st.clear();
 
-        for (int tl = seg.ta; tl < seg.tb;) {
+        for (int tl = seg.ta; tl < seg.tb; tl += 2) {
+            const int used = split * S + slot;
+            if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait_bounded(&full[used], phase));
+            if (dead) break;
+            // (a stage without its tiles: the rows are NaN whatever comes)
+            if (bad_page[used]) poison = true;
             AttnStep x;
+            x.tile = ring + (size_t)slot * STAGE;
             x.pos = (seg.first + tl) * KV_TILE;
             x.first = sp.first();
             x.last = sp.last();
-            const bool clear = seg.tb - tl >= Sh::STEP && x.pos >= clear_from && x.pos + Sh::STEP * KV_TILE <= clear_to;
-            const int n = clear ? Sh::STEP : 1;
-            int used[2];
-#pragma unroll
-            for (int u = 0; u < Sh::STEP; ++u) {
-                x.tile[u] = ring + (size_t)slot * Sh::TILE;
-                used[u] = split * S + slot;
-                if (u < n) {
-                    if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait_bounded(&full[used[u]], phase));
-                    if (!dead && bad_page[used[u]]) poison = true;
-                    if (++slot == S) slot = 0, phase ^= 1;
+            if (++slot == S) slot = 0, phase ^= 1;
+            if (!poison) {
+                if (tl + 2 <= seg.tb && x.pos >= clear_from && x.pos + 2 * KV_TILE <= clear_to) {
+                    attn_step<FMT, NB, MODE, false>(st, x, qf, q_smem, begin, end, lane);
+                } else {
+#pragma unroll 1
+                    for (int u = 0; u < 2 && tl + u < seg.tb; ++u) {
+                        attn_step<FMT, NB, MODE, true>(st, x, qf, q_smem, begin, end, lane);
+                        x.tile += Sh::TILE;
+                        x.pos += KV_TILE;
+                    }
                 }
             }
-            if (dead) break;
-            if (!poison) {  // (a stage without its tile: the rows are NaN whatever comes)
-                if (clear) attn_step<FMT, NB, MODE, false>(st, x, qf, q_smem, begin, end, lane);
-                else attn_step<FMT, NB, MODE, true>(st, x, qf, q_smem, begin, end, lane);
-            }
             __syncwarp();
-            if (lane == 0)
-                for (int u = 0; u < n; ++u) mbar_arrive(&empty[used[u]]);
-            tl += n;
+            if (lane == 0) mbar_arrive(&empty[used]);
         }
         st.finish(poison || dead);
 
@@ -1058,12 +1082,12 @@ AttnPlan attn_plan(const DeviceInfo& di, int rows)
     p.wr = (tiles + p.row_groups - 1) / p.row_groups;
     for (p.ws = Sh::WARPS / p.wr; p.ws > 0; --p.ws) {
         const uint32_t q = Sh::Q_SMEM ? (uint32_t)p.ws * p.wr * NB * 2 * Sh::Q_TERMS * 512 : 0;
-        const uint32_t per_stage = (uint32_t)p.ws * (Sh::TILE + 2 * 8 + 4);
+        const uint32_t per_stage = (uint32_t)p.ws * (2 * Sh::TILE + 2 * 8 + 4);
         const uint32_t budget = (uint32_t)di.smem_optin - 2048;  // beside the static shared memory
         const int stages = budget > q ? (int)((budget - q) / per_stage) : 0;
-        if (stages < 3 && p.ws > 1) continue;
-        p.stages = stages > 8 ? 8 : stages;
-        p.off_q = (uint32_t)p.ws * p.stages * Sh::TILE;
+        if (stages < 2 && p.ws > 1) continue;
+        p.stages = stages > 4 ? 4 : stages;
+        p.off_q = (uint32_t)p.ws * p.stages * 2 * Sh::TILE;
         p.off_bar = p.off_q + q;
         p.bytes = p.off_bar + (uint32_t)p.ws * p.stages * 20;
         break;

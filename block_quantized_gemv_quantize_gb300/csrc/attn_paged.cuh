@@ -44,18 +44,25 @@
 
 namespace qgemv {
 
-constexpr int ATTN_GRID = 160;     // most CTAs (one an SM): the workspace holds their partial results
+constexpr int ATTN_GRID = 160;       // most CTAs (one an SM): the workspace holds their partial results
 constexpr int ATTN_JOIN_WARPS = 16;  // of a CTA of the joining kernel
-constexpr int ATTN_ITEM_COST = 4;  // of an item besides its tiles, in tiles (even)
-constexpr int ATTN_MIN_PIECE = 4;  // least units of a split: shorter ones cost more to join than they save
+// What an item costs besides its tiles (q, a cut into partial results), in tiles;
+// even.  46 ragged sequences, and 17 rows with a window at D = 256: 94 and 84 us
+// with 4, 87 and 79 with 8, 90 and 80 with 16.
+constexpr int ATTN_ITEM_COST = 8;
+// Least units of a split: a single sequence of 197 tokens takes 10.8 us with 2,
+// 12.2 with 4, 15.1 with 8.
+constexpr int ATTN_MIN_PIECE = 2;
 
 enum AttnMode { ATTN_ONE = 0, ATTN_PAIR = 1, ATTN_TWO = 2 };
 
 // The mode for a call: by the type's precision and the rows of a kv head.
 inline int attn_mode(int type, int rows) { return type == QGEMV_BF16 ? ATTN_ONE : (rows > 8 ? ATTN_TWO : ATTN_PAIR); }
 
-// Warps that compute (one more copies): as many as 64 K registers hold.
-__host__ __device__ constexpr int attn_warps(int) { return 7; }
+// Warps that compute (one more copies): eight warps leave a thread 255 registers.
+// Eleven (168 registers, q in shared memory) measured 1 to 4 % faster where the
+// cache is long and 15 to 20 % slower on short sequences.
+constexpr int ATTN_WARPS = 7;
 
 template <int FMT, int NB, int MODE>
 struct AttnShape {
@@ -67,7 +74,7 @@ struct AttnShape {
     static constexpr int TILE = kv_tile_bytes(FMT, NB), HALF = kv_half_bytes(FMT, NB);
     static constexpr bool Q_SMEM = NB > 4 || MODE == ATTN_TWO;  // else q's fragments stay in registers
     static constexpr int Q_TERMS = MODE == ATTN_TWO ? 2 : 1;
-    static constexpr int WARPS = attn_warps(NB);
+    static constexpr int WARPS = ATTN_WARPS;
     static constexpr int STEP = 2;                           // tiles of a step without an edge
     static constexpr int UNITS = NB * 2 * NR;                // runs of four output values of a lane
     // where value k of the run (block b, half h, row g + 8 r) stands among a lane's outputs

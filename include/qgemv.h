@@ -556,9 +556,8 @@ int kv_read(int fmt, int type, const void* cache, int64_t n_pages, int page_toke
  *              sequence's length are not used
  *   kv_lens    int32 [batch], the lengths with the new tokens in them; <= 0
  *              for an unused place
- *   workspace  attn_paged_workspace_bytes() bytes, 16-byte aligned; its first
- *              1024 bytes zero-filled before the first use, and every call
- *              leaves them so.  Calls that share it must not overlap in time.
+ *   workspace  attn_paged_workspace_bytes() bytes, 16-byte aligned, with
+ *              anything in it.  Calls that share it must not overlap in time.
  *   scale      finite;  window >= 0 (0: none);  1 <= rows <= 17;
  *   batch      1 .. 65536;  n_heads a multiple of n_kv_heads
  *   head_dim   64, 96, 128 or 256

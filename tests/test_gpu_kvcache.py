@@ -226,6 +226,39 @@ def test_long_sequences_are_split_and_joined(ops, kind):
         assert torch.equal(ops.attn_paged(**args), out)
 
 
+@pytest.mark.parametrize("fmt,kind", [("q8_0", "float32"), ("q4_0", "float16"), ("f16", "bfloat16"), ("q8_0", "bfloat16")])
+def test_more_rows_than_the_warps_of_a_cta_hold(ops, fmt, kind):
+    lens = [300, 0, 77]
+    args, q, kv = attention_case(ops, fmt, kind, lens, 17, 32, 2, 64, 16, 0)  # 272 rows a kv head
+    check_attention(ops, args, q, kv, lens)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("page,window", [(48, 0), (48, 130), (16, 300), (1024, 33), (80, 640)])
+def test_pages_and_windows_that_cut_pairs_of_tiles(ops, fmt, page, window):
+    lens = [1333, 15, 16, 17, 31, 32, 33, 47, 48, 49, 641]
+    args, q, kv = attention_case(ops, fmt, "float32", lens, 2, 6, 2, 96, page, window)
+    check_attention(ops, args, q, kv, lens)
+
+
+def test_one_kv_head_over_all_splits(ops):
+    lens = [40000]
+    args, q, kv = attention_case(ops, "q4_0", "float32", lens, 1, 3, 1, 64, 32, 0, spread=5.0)
+    out = check_attention(ops, args, q, kv, lens)
+    for _ in range(3):
+        assert torch.equal(ops.attn_paged(**args), out)
+
+
+def test_the_workspace_may_hold_anything(ops):
+    lens = [500, 3, 90]
+    args, q, kv = attention_case(ops, "q8_0", "float32", lens, 2, 4, 2, 64, 16, 0)
+    want = ops.attn_paged(**args)
+    ws = torch.full((ops.attn_paged_workspace_bytes(torch.float32, 2, 4, 2, 64),), 255, dtype=torch.uint8, device=DEV)
+    for fill in (255, 127, 1, 0):
+        ws.fill_(fill)
+        assert torch.equal(ops.attn_paged(**args, ws=ws), want)
+
+
 def test_many_short_sequences(ops):
     lens = [int(n) for n in np.random.default_rng(3).integers(0, 40, 300)]
     args, q, kv = attention_case(ops, "q4_0", "float16", lens, 2, 4, 2, 64, 16, 0)

@@ -849,32 +849,56 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
         const int kvh = seg.item / p.row_groups;
         const int row0 = ((seg.item - kvh * p.row_groups) * p.wr + wrow) * Sh::ROWS;
         const AttnSpan sp(a, a.lens[seg.b]);
-        // ---- q: this lane's rows, scaled to 2^13 .. 2^14, as A fragments
+        // ---- q: this lane's rows, scaled to 2^13 .. 2^14, as A fragments.  All
+        // loads first (a row that does not exist loads the last one that does):
+        // behind a branch each they came one after the other, 3.3 us for 16 rows.
         uint32_t qf[Sh::Q_SMEM ? 1 : NB * 2][4];
         int end[NR], begin[NR];
+        bool in[NR];
+        alignas(16) T raw[NR][NB * 2][4];
+        {
+            const T* row[NR];
+#pragma unroll
+            for (int r = 0; r < NR; ++r) {
+                const int all = a.rows * a.group, rr = min(row0 + g + 8 * r, all - 1), i = rr / a.group;
+                in[r] = row0 + g + 8 * r < all;
+                end[r] = in[r] ? sp.end(i) : 0;
+                begin[r] = in[r] ? sp.begin(i) : 0;
+                row[r] = static_cast<const T*>(a.q) + ((int64_t)seg.b * a.rows + i) * a.q_row +
+                         (int64_t)(kvh * a.group + rr - i * a.group) * a.q_head;
+            }
+            if (q_wide) {
+                using Vec = std::conditional_t<sizeof(T) == 4, uint4, uint2>;
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+#pragma unroll
+                    for (int k = 0; k < NB * 2; ++k)
+                        *reinterpret_cast<Vec*>(raw[r][k]) =
+                            *reinterpret_cast<const Vec*>(row[r] + Sh::column(k >> 1, k & 1, t));
+            } else {
+#pragma unroll
+                for (int r = 0; r < NR; ++r)
+#pragma unroll
+                    for (int k = 0; k < NB * 2; ++k)
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) raw[r][k][z] = row[r][Sh::column(k >> 1, k & 1, t) + z];
+            }
+        }
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-            const int rr = row0 + g + 8 * r;
-            const bool in = rr < a.rows * a.group;
-            const int i = in ? rr / a.group : 0;
-            end[r] = in ? sp.end(i) : 0;
-            begin[r] = in ? sp.begin(i) : 0;
-            const T* row = static_cast<const T*>(a.q) + ((int64_t)seg.b * a.rows + i) * a.q_row +
-                           (int64_t)(kvh * a.group + rr - i * a.group) * a.q_head;
             float qv[NB][8];
             uint32_t top = 0;
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    if (in) load_values(row + Sh::column(b, h, t), q_wide, x);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         // q4_0: values 4 t + {0, 1, 2, 3} go to places {0, 2, 1, 3}
                         const int place = FMT == QGEMV_KV_Q4_0 ? 4 * h + ((k & 1) << 1) + (k >> 1) : 4 * h + k;
-                        qv[b][place] = x[k];
-                        top = max(top, __float_as_uint(x[k]) & 0x7fffffffu);
+                        const float x = in[r] ? to_f32(raw[r][2 * b + h][k]) : 0.0f;
+                        qv[b][place] = x;
+                        top = max(top, __float_as_uint(x) & 0x7fffffffu);
                     }
                 }
             }

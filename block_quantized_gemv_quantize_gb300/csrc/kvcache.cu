@@ -115,6 +115,22 @@ __device__ __forceinline__ KvTop kv_top(const float (&x)[8], int sub)
     return t;
 }
 
+// The largest magnitude alone, of 16-bit values two at a time.
+__device__ __forceinline__ float kv_top_pairs(const KvRaw<__half>& x)
+{
+    const __half2* p = reinterpret_cast<const __half2*>(x.v);
+    const __half2 m = __hmax2_nan(__hmax2_nan(__habs2(p[0]), __habs2(p[1])), __hmax2_nan(__habs2(p[2]), __habs2(p[3])));
+    return max_abs(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float kv_top_pairs(const KvRaw<__nv_bfloat16>& x)
+{
+    const __nv_bfloat162* p = reinterpret_cast<const __nv_bfloat162*>(x.v);
+    const __nv_bfloat162 m =
+        __hmax2_nan(__hmax2_nan(__habs2(p[0]), __habs2(p[1])), __hmax2_nan(__habs2(p[2]), __habs2(p[3])));
+    return max_abs(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float kv_top_pairs(const KvRaw<float>&) { return 0.0f; }  // (not called)
+
 // Four blocks' tops over the quad: lane sub gets that of block sub.
 template <bool KEY>
 __device__ __forceinline__ KvTop kv_scatter(const KvTop (&t)[4], int sub)
@@ -297,10 +313,14 @@ __global__ void __launch_bounds__(KV_THREADS, 4) kv_write_kernel(const KvArgs a,
             KvTop top[KV_PAIRS];
 #pragma unroll
             for (int j = 0; j < KV_PAIRS; ++j) {
-                float x[8];
+                if constexpr (FMT == QGEMV_KV_Q8_0 && sizeof(T) == 2) {
+                    top[j] = {kv_top_pairs(raw[j]), 0};
+                } else {
+                    float x[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) x[k] = to_f32(raw[j].v[k]);
-                top[j] = kv_top<FMT, RUNS>(x, sub);
+                    for (int k = 0; k < 8; ++k) x[k] = to_f32(raw[j].v[k]);
+                    top[j] = kv_top<FMT, RUNS>(x, sub);
+                }
             }
             d = kv_d<FMT>(kv_scatter<FMT == QGEMV_KV_Q4_0>(top, sub));
             inverse = kv_inverse(d);
@@ -362,7 +382,8 @@ __global__ void __launch_bounds__(KV_THREADS, 5) kv_read_kernel(const KvArgs a, 
 #pragma unroll
         for (int j = 0; j < KV_PAIRS; ++j) {
 #pragma unroll
-            for (uint32_t& w : word[j]) w = 0;
+            for (uint32_t& w : word[j])  // zeros, for a slot outside the cache
+                w = FMT == QGEMV_KV_F16 ? 0u : (FMT == QGEMV_KV_Q8_0 ? 0x80808080u : 0x88888888u);
             d[j] = __half(0.0f);
             const int n = block0 + 2 * j;
             if (!t.codes || n >= n_blocks) continue;
@@ -409,10 +430,6 @@ __global__ void __launch_bounds__(KV_THREADS, 5) kv_read_kernel(const KvArgs a, 
                 const float f = __half2float(d[j]);  // 11 bits times 8: exact
 #pragma unroll
                 for (int k = 0; k < 8; k += 2) mul_f32x2(x[k], x[k + 1], x[k], x[k + 1], f, f);
-                if (!t.codes) {  // (zeros, not minus zeros)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) x[k] = 0.0f;
-                }
             }
             store_lane<RUNS>(KvBlock(a, n).row(a, t), sub, wide, x);
         }

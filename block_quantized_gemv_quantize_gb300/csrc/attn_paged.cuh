@@ -36,6 +36,17 @@
 // second kernel joins the partial results of every recorded item, each output by
 // as many warps as there are to spare, in the order of the splits: the result
 // does not depend on the order in which CTAs finish.
+//
+// What bounds it.  46 ragged sequences of up to 8192 tokens (q8_0, bf16 rows):
+// 85 us, 5.3 TB/s; the copies alone, without the arithmetic, take 81.  One kv head
+// a query head in f16: 43 us, 4.9 TB/s, as the copies alone.  Two sequences of
+// 131071 tokens in q4_0 (fp16 rows, pairs of terms): 104 us where the copies alone
+// take 58: 470 instructions a tile of 16 tokens and 8 rows, of which 32 are the
+// products, at 0.6 an SM quarter and cycle.  Width 6 over 17391 tokens (30 rows a
+// kv head, two terms): 32 us, of them 21 in the splits at one instruction in three
+// cycles a warp (two warps a scheduler, 255 registers each).  A call of 197 tokens
+// takes 10 us: two launches, three dependent reads before the first tile arrives
+// (lengths, page number, tile) and the join.
 #pragma once
 
 #include <type_traits>

@@ -4,12 +4,19 @@
 // Both are bound by memory once their index arithmetic is small beside it:
 // (values * element size + values * (34/32 | 18/32 | 2)) bytes a direction.
 // Four lanes take one block (32 values of one token, head and K or V), eight
-// values each, so that a block's maximum takes two shuffles.  A warp takes four
-// consecutive tokens and KV_PAIRS pairs of neighbouring blocks: tokens that
-// follow one another in the cache then fill whole 128-byte lines of codes and
-// share the 32 bytes of scales, a row is read or written 128 bytes (16-bit
-// types) or 256 at a time, each lane has all its loads in flight at once, and
-// the slot's division by the page is done once for all its pairs.
+// values each.  A warp takes four consecutive tokens and KV_PAIRS pairs of
+// neighbouring blocks: tokens that follow one another in the cache then fill
+// whole 128-byte lines of codes and share the 32 bytes of scales, a row is read or
+// written 128 bytes (16-bit types) or 256 at a time, each lane has all its loads
+// in flight at once, and the slot's division by the page is done once for all its
+// pairs.  (Eight lanes a block, one block a lane at a time and 64-bit divisions a
+// block were bound by instructions at a fourth of these rates.)
+//
+// 60000 tokens of 8 heads of 128 (GB/s read and written, of 6790 measured for a
+// copy): kv_read 6.2 to 6.6 TB/s in every format and type but q4_0 to bf16 (5.8);
+// kv_write 6.2 (fp32 to q8_0), 5.2 (fp32 to q4_0), 6.4 to 6.7 (to f16), and 3.8
+// and 2.5 from bf16 to q8_0 and q4_0, where the instructions of the quantizing
+// bound it: half of a warp's blocks hold a value on a code's border (kv_encode).
 #include "kvcache.cuh"
 
 namespace qgemv {
@@ -17,6 +24,7 @@ namespace {
 
 constexpr int KV_WARPS = 8, KV_THREADS = 32 * KV_WARPS;
 constexpr int KV_TOKENS = 4 * KV_WARPS;  // of a CTA
+constexpr int KV_CTAS = 16;              // least CTAs for an SM that long calls are cut into
 constexpr int KV_PAIRS = 4;              // pairs of blocks of a warp, one for each lane of a quad
 
 // The eight values of lane sub (0 .. 3) of a block: 8 sub .. 8 sub + 7, or in
@@ -24,6 +32,12 @@ constexpr int KV_PAIRS = 4;              // pairs of blocks of a warp, one for e
 // 16 bytes next to one another, and hold both nibbles of q4_0's bytes.
 template <int FMT, typename T>
 constexpr bool kv_two_runs = FMT == QGEMV_KV_Q4_0 || sizeof(T) == 4;
+
+// Whether a CTA of kv_write goes through several chunks of a row.  It saves 5 to
+// 10 % where the quantizing leaves registers for it; from 16-bit rows to q4_0 it
+// costs 20 % (60000 tokens of 1024 values: 149 us against 124).
+template <int FMT, typename T>
+constexpr bool kv_write_loops = !(FMT == QGEMV_KV_Q4_0 && sizeof(T) == 2);
 
 // A lane's eight values as they are in memory.
 template <typename T>
@@ -293,64 +307,68 @@ __global__ void __launch_bounds__(KV_THREADS, 4) kv_write_kernel(const KvArgs a,
     pdl_wait();
     const int lane = threadIdx.x & 31, sub = lane & 3;
     const bool wide = a.k.wide<T>() && a.v.wide<T>();
-    const int n_blocks = 2 * a.L.heads * a.L.nb, block0 = blockIdx.x * 2 * KV_PAIRS + (lane >> 2 & 1);
+    const int n_blocks = 2 * a.L.heads * a.L.nb;
     for (int64_t group = blockIdx.y; group * KV_TOKENS < a.n_tokens; group += gridDim.y) {
         const KvToken<FMT, T> t(a, group, lane);
-        KvRaw<T> raw[KV_PAIRS];
-#pragma unroll
-        for (int j = 0; j < KV_PAIRS; ++j) {
-            const int n = block0 + 2 * j;
-            if (t.codes && n < n_blocks) {
-                load_lane<RUNS>(KvBlock(a, n).row(a, t), sub, wide, raw[j]);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) raw[j].v[k] = from_f32<T>(0.0f);
-            }
-        }
-        // the scales: lane sub of a quad works out pair sub's
-        float d = 0.0f, inverse = 0.0f;
-        if constexpr (FMT != QGEMV_KV_F16) {
-            KvTop top[KV_PAIRS];
+        for (int chunk = blockIdx.x; chunk * 2 * KV_PAIRS < n_blocks; chunk += gridDim.x) {
+            const int block0 = chunk * 2 * KV_PAIRS + (lane >> 2 & 1);
+            KvRaw<T> raw[KV_PAIRS];
 #pragma unroll
             for (int j = 0; j < KV_PAIRS; ++j) {
-                if constexpr (FMT == QGEMV_KV_Q8_0 && sizeof(T) == 2) {
-                    top[j] = {kv_top_pairs(raw[j]), 0};
+                const int n = block0 + 2 * j;
+                if (t.codes && n < n_blocks) {
+                    load_lane<RUNS>(KvBlock(a, n).row(a, t), sub, wide, raw[j]);
                 } else {
-                    float x[8];
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) x[k] = to_f32(raw[j].v[k]);
-                    top[j] = kv_top<FMT, RUNS>(x, sub);
+                    for (int k = 0; k < 8; ++k) raw[j].v[k] = from_f32<T>(0.0f);
                 }
             }
-            d = kv_d<FMT>(kv_scatter<FMT == QGEMV_KV_Q4_0>(top, sub));
-            inverse = kv_inverse(d);
-            const int n = block0 + 2 * sub;
-            if (t.codes && n < n_blocks) {
-                const KvBlock b(a, n);
-                uint8_t* scale = t.codes + b.codes<FMT>(a) + (t.scales + b.scale<FMT>());
-                if (QG_OK(qg_in(scale - a.cache, 2, a.L.bytes()), st, 742))  // (a NaN stays)
-                    *reinterpret_cast<__half*>(scale) = __float2half_rn(fabsf(d) > 65504.0f ? copysignf(65504.0f, d) : d);
-            }
-        }
+            // the scales: lane sub of a quad works out pair sub's
+            float d = 0.0f, inverse = 0.0f;
+            if constexpr (FMT != QGEMV_KV_F16) {
+                KvTop top[KV_PAIRS];
 #pragma unroll
-        for (int j = 0; j < KV_PAIRS; ++j) {
-            const int n = block0 + 2 * j;
-            float x[8];
+                for (int j = 0; j < KV_PAIRS; ++j) {
+                    if constexpr (FMT == QGEMV_KV_Q8_0 && sizeof(T) == 2) {
+                        top[j] = {kv_top_pairs(raw[j]), 0};
+                    } else {
+                        float x[8];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) x[k] = to_f32(raw[j].v[k]);
-            uint32_t word[2];
-            if constexpr (FMT != QGEMV_KV_F16) kv_encode<FMT>(x, d, inverse, (lane & 28) + j, word);  // shuffles: every lane
-            if (!t.codes || n >= n_blocks) continue;
-            uint8_t* codes = t.codes + KvBlock(a, n).codes<FMT>(a);
-            if (!QG_OK(qg_in(codes - a.cache, CODE, a.L.bytes()), st, 741)) continue;
-            if constexpr (FMT == QGEMV_KV_F16) {
-                store_lane<RUNS>(reinterpret_cast<__half*>(codes), sub, true, x);
-            } else {
-                uint32_t* w = reinterpret_cast<uint32_t*>(codes);
-                if constexpr (FMT == QGEMV_KV_Q4_0) w[sub] = word[0];
-                else if constexpr (RUNS) w[sub] = word[0], w[4 + sub] = word[1];
-                else reinterpret_cast<uint2*>(codes)[sub] = make_uint2(word[0], word[1]);
+                        for (int k = 0; k < 8; ++k) x[k] = to_f32(raw[j].v[k]);
+                        top[j] = kv_top<FMT, RUNS>(x, sub);
+                    }
+                }
+                d = kv_d<FMT>(kv_scatter<FMT == QGEMV_KV_Q4_0>(top, sub));
+                inverse = kv_inverse(d);
+                const int n = block0 + 2 * sub;
+                if (t.codes && n < n_blocks) {
+                    const KvBlock b(a, n);
+                    uint8_t* scale = t.codes + b.codes<FMT>(a) + (t.scales + b.scale<FMT>());
+                    if (QG_OK(qg_in(scale - a.cache, 2, a.L.bytes()), st, 742))  // (a NaN stays)
+                        *reinterpret_cast<__half*>(scale) = __float2half_rn(fabsf(d) > 65504.0f ? copysignf(65504.0f, d) : d);
+                }
             }
+#pragma unroll
+            for (int j = 0; j < KV_PAIRS; ++j) {
+                const int n = block0 + 2 * j;
+                float x[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] = to_f32(raw[j].v[k]);
+                uint32_t word[2];
+                if constexpr (FMT != QGEMV_KV_F16) kv_encode<FMT>(x, d, inverse, (lane & 28) + j, word);  // shuffles: every lane
+                if (!t.codes || n >= n_blocks) continue;
+                uint8_t* codes = t.codes + KvBlock(a, n).codes<FMT>(a);
+                if (!QG_OK(qg_in(codes - a.cache, CODE, a.L.bytes()), st, 741)) continue;
+                if constexpr (FMT == QGEMV_KV_F16) {
+                    store_lane<RUNS>(reinterpret_cast<__half*>(codes), sub, true, x);
+                } else {
+                    uint32_t* w = reinterpret_cast<uint32_t*>(codes);
+                    if constexpr (FMT == QGEMV_KV_Q4_0) w[sub] = word[0];
+                    else if constexpr (RUNS) w[sub] = word[0], w[4 + sub] = word[1];
+                    else reinterpret_cast<uint2*>(codes)[sub] = make_uint2(word[0], word[1]);
+                }
+            }
+            if constexpr (!kv_write_loops<FMT, T>) break;
         }
     }
 }
@@ -373,65 +391,68 @@ __global__ void __launch_bounds__(KV_THREADS, 5) kv_read_kernel(const KvArgs a, 
     pdl_wait();
     const int lane = threadIdx.x & 31, sub = lane & 3;
     const bool wide = a.k.wide<T>() && a.v.wide<T>();
-    const int n_blocks = 2 * a.L.heads * a.L.nb, block0 = blockIdx.x * 2 * KV_PAIRS + (lane >> 2 & 1);
+    const int n_blocks = 2 * a.L.heads * a.L.nb;
     for (int64_t group = blockIdx.y; group * KV_TOKENS < a.n_tokens; group += gridDim.y) {
         const KvToken<FMT, T> t(a, group, lane);
         if (!t.in) continue;
-        uint32_t word[KV_PAIRS][FMT == QGEMV_KV_F16 ? 4 : 2];
-        __half d[KV_PAIRS];
+        for (int chunk = blockIdx.x; chunk * 2 * KV_PAIRS < n_blocks; chunk += gridDim.x) {
+            const int block0 = chunk * 2 * KV_PAIRS + (lane >> 2 & 1);
+            uint32_t word[KV_PAIRS][FMT == QGEMV_KV_F16 ? 4 : 2];
+            __half d[KV_PAIRS];
 #pragma unroll
-        for (int j = 0; j < KV_PAIRS; ++j) {
+            for (int j = 0; j < KV_PAIRS; ++j) {
 #pragma unroll
-            for (uint32_t& w : word[j])  // zeros, for a slot outside the cache
-                w = FMT == QGEMV_KV_F16 ? 0u : (FMT == QGEMV_KV_Q8_0 ? 0x80808080u : 0x88888888u);
-            d[j] = __half(0.0f);
-            const int n = block0 + 2 * j;
-            if (!t.codes || n >= n_blocks) continue;
-            const KvBlock b(a, n);
-            const uint8_t* codes = t.codes + b.codes<FMT>(a);
-            if (!QG_OK(qg_in(codes - a.cache, CODE, a.L.bytes()), st, 743)) continue;
-            if constexpr (FMT == QGEMV_KV_F16) {
-                const uint2* w = reinterpret_cast<const uint2*>(codes);
-                const uint2 lo = w[RUNS ? sub : 2 * sub], hi = w[RUNS ? 4 + sub : 2 * sub + 1];
-                word[j][0] = lo.x, word[j][1] = lo.y, word[j][2] = hi.x, word[j][3] = hi.y;
-            } else {
-                const uint32_t* w = reinterpret_cast<const uint32_t*>(codes);
-                if constexpr (FMT == QGEMV_KV_Q4_0) {
-                    word[j][0] = w[sub];
-                } else if constexpr (RUNS) {
-                    word[j][0] = w[sub], word[j][1] = w[4 + sub];
+                for (uint32_t& w : word[j])  // zeros, for a slot outside the cache
+                    w = FMT == QGEMV_KV_F16 ? 0u : (FMT == QGEMV_KV_Q8_0 ? 0x80808080u : 0x88888888u);
+                d[j] = __half(0.0f);
+                const int n = block0 + 2 * j;
+                if (!t.codes || n >= n_blocks) continue;
+                const KvBlock b(a, n);
+                const uint8_t* codes = t.codes + b.codes<FMT>(a);
+                if (!QG_OK(qg_in(codes - a.cache, CODE, a.L.bytes()), st, 743)) continue;
+                if constexpr (FMT == QGEMV_KV_F16) {
+                    const uint2* w = reinterpret_cast<const uint2*>(codes);
+                    const uint2 lo = w[RUNS ? sub : 2 * sub], hi = w[RUNS ? 4 + sub : 2 * sub + 1];
+                    word[j][0] = lo.x, word[j][1] = lo.y, word[j][2] = hi.x, word[j][3] = hi.y;
                 } else {
-                    const uint2 both = reinterpret_cast<const uint2*>(codes)[sub];
-                    word[j][0] = both.x, word[j][1] = both.y;
+                    const uint32_t* w = reinterpret_cast<const uint32_t*>(codes);
+                    if constexpr (FMT == QGEMV_KV_Q4_0) {
+                        word[j][0] = w[sub];
+                    } else if constexpr (RUNS) {
+                        word[j][0] = w[sub], word[j][1] = w[4 + sub];
+                    } else {
+                        const uint2 both = reinterpret_cast<const uint2*>(codes)[sub];
+                        word[j][0] = both.x, word[j][1] = both.y;
+                    }
+                    const uint8_t* scale = codes + (t.scales + b.scale<FMT>());
+                    if (QG_OK(qg_in(scale - a.cache, 2, a.L.bytes()), st, 744)) d[j] = *reinterpret_cast<const __half*>(scale);
                 }
-                const uint8_t* scale = codes + (t.scales + b.scale<FMT>());
-                if (QG_OK(qg_in(scale - a.cache, 2, a.L.bytes()), st, 744)) d[j] = *reinterpret_cast<const __half*>(scale);
             }
-        }
 #pragma unroll
-        for (int j = 0; j < KV_PAIRS; ++j) {
-            const int n = block0 + 2 * j;
-            if (n >= n_blocks) continue;
-            float x[8];
-            if constexpr (FMT == QGEMV_KV_F16) {
+            for (int j = 0; j < KV_PAIRS; ++j) {
+                const int n = block0 + 2 * j;
+                if (n >= n_blocks) continue;
+                float x[8];
+                if constexpr (FMT == QGEMV_KV_F16) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&word[j][k]));
-                    x[2 * k] = f.x, x[2 * k + 1] = f.y;
-                }
-            } else {
-                if constexpr (FMT == QGEMV_KV_Q4_0) {
-                    kv_numbers(word[j][0] & 0x0F0F0F0Fu, 8.0f, x);
-                    kv_numbers(word[j][0] >> 4 & 0x0F0F0F0Fu, 8.0f, x + 4);
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&word[j][k]));
+                        x[2 * k] = f.x, x[2 * k + 1] = f.y;
+                    }
                 } else {
-                    kv_numbers(word[j][0], 128.0f, x);
-                    kv_numbers(word[j][1], 128.0f, x + 4);
-                }
-                const float f = __half2float(d[j]);  // 11 bits times 8: exact
+                    if constexpr (FMT == QGEMV_KV_Q4_0) {
+                        kv_numbers(word[j][0] & 0x0F0F0F0Fu, 8.0f, x);
+                        kv_numbers(word[j][0] >> 4 & 0x0F0F0F0Fu, 8.0f, x + 4);
+                    } else {
+                        kv_numbers(word[j][0], 128.0f, x);
+                        kv_numbers(word[j][1], 128.0f, x + 4);
+                    }
+                    const float f = __half2float(d[j]);  // 11 bits times 8: exact
 #pragma unroll
-                for (int k = 0; k < 8; k += 2) mul_f32x2(x[k], x[k + 1], x[k], x[k + 1], f, f);
+                    for (int k = 0; k < 8; k += 2) mul_f32x2(x[k], x[k + 1], x[k], x[k + 1], f, f);
+                }
+                store_lane<RUNS>(KvBlock(a, n).row(a, t), sub, wide, x);
             }
-            store_lane<RUNS>(KvBlock(a, n).row(a, t), sub, wide, x);
         }
     }
 }
@@ -439,8 +460,16 @@ __global__ void __launch_bounds__(KV_THREADS, 5) kv_read_kernel(const KvArgs a, 
 template <bool WRITE, int FMT, typename T>
 int launch_kv(const KvArgs& a, cudaStream_t s)
 {
+    const DeviceInfo di = device_info();
+    if (di.sms <= 0) return QGEMV_CUDA_ERROR;
     const int64_t groups = ((int64_t)a.n_tokens + KV_TOKENS - 1) / KV_TOKENS;
-    const dim3 grid((2 * a.L.heads * a.L.nb + 2 * KV_PAIRS - 1) / (2 * KV_PAIRS), (unsigned)(groups < 65535 ? groups : 65535));
+    // A CTA goes through several chunks of its tokens' rows where that leaves
+    // KV_CTAS for every SM, so that long calls find each slot's place once for many
+    // blocks (131071 tokens of q8_0: 149 us with a CTA a chunk, 129 so).
+    const int64_t chunks = (2 * a.L.heads * a.L.nb + 2 * KV_PAIRS - 1) / (2 * KV_PAIRS);
+    int64_t each = groups * chunks / ((int64_t)di.sms * KV_CTAS);
+    if ((WRITE && !kv_write_loops<FMT, T>) || each < 1) each = 1;
+    const dim3 grid((unsigned)((chunks + each - 1) / each), (unsigned)(groups < 65535 ? groups : 65535));
     KvArgs args = a;
     args.head_bytes = (uint32_t)(a.L.tiles() * a.L.tile_bytes);
     args.nb_inverse = 0xffffffffu / (uint32_t)a.L.nb + 1;

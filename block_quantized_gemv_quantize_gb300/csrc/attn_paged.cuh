@@ -70,6 +70,14 @@ enum AttnMode { ATTN_ONE = 0, ATTN_PAIR = 1, ATTN_TWO = 2 };
 // The mode for a call: by the type's precision and the rows of a kv head.
 inline int attn_mode(int type, int rows) { return type == QGEMV_BF16 ? ATTN_ONE : (rows > 8 ? ATTN_TWO : ATTN_PAIR); }
 
+// Shares of a split whose warps share their schedulers with another's, and of one
+// whose warps do not.  The latter is faster where arithmetic bounds the kernel: with
+// 10 instead of 8, two of 131071 tokens in q4_0 take 98 us, not 101, 46 ragged
+// sequences 83, not 86, width 6 over 17391 tokens 30, not 32; where memory does it
+// is not: D = 64 in q8_0 takes 63 us, not 58, an f16 cache 45.6, not 44.3.
+constexpr int ATTN_SHARE = 8;
+constexpr int attn_share_alone(int fmt, int nb) { return fmt != QGEMV_KV_F16 && nb > 2 ? 10 : ATTN_SHARE; }
+
 // Warps that compute (one more copies): eight warps leave a thread 255 registers.
 // Eleven (168 registers, q in shared memory) measured 1 to 4 % faster where the
 // cache is long and 15 to 20 % slower on short sequences.
@@ -103,7 +111,39 @@ struct AttnPlan {
     int ws, wr;          // splits, row tiles at a time
     int row_groups;
     int stages;          // pairs of tiles a ring holds
+    int cum[ATTN_WARPS + 1];  // shares of a CTA's part of the line: split s has cum[s] .. cum[s + 1] of cum[ws]
     uint32_t off_q, off_bar, bytes;  // shared memory
+};
+
+// How the line is cut: a CTA has `chunk` units of it, split s of the CTA those from
+// start(s) on.  All even.
+struct AttnCut {
+    int64_t chunk, piece;
+    bool even;  // all splits alike: too few units to weigh
+    __device__ __forceinline__ AttnCut(const AttnPlan& p, int64_t total)
+    {
+        piece = (total + p.splits - 1) / p.splits;
+        piece += piece & 1;
+        if (piece < ATTN_MIN_PIECE) piece = ATTN_MIN_PIECE;
+        even = piece < 8;  // (else the least share is of 4 units)
+        const int ctas = p.splits / p.ws;
+        chunk = even ? piece * p.ws : (total + ctas - 1) / ctas;
+        chunk += chunk & 1;
+    }
+    __device__ __forceinline__ int64_t start(const AttnPlan& p, int s) const
+    {
+        if (even) return piece * s;
+        return s == p.ws ? chunk : (chunk * p.cum[s] / p.cum[p.ws] + 1) & ~(int64_t)1;
+    }
+    // the split that has a unit of the line
+    __device__ __forceinline__ int split_of(const AttnPlan& p, int64_t unit) const
+    {
+        const int64_t cta = unit / chunk;
+        unit -= cta * chunk;
+        int s = 0;
+        while (s + 1 < p.ws && start(p, s + 1) <= unit) ++s;
+        return (int)cta * p.ws + s;
+    }
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -671,10 +711,19 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
     }
 }
 
-// What the split that has a shared item's first tile leaves of it.
+// What the split that has a shared item's first tile leaves of it, in one word:
+// the partial results from this split's on (0: none), the item ((kv head, row
+// group) within the sequence, below 2^24: at most 2^16 heads of 17 rows) and the
+// sequence.
 struct AttnRecord {
-    int parts;    // partial results, from this split's on; 0: none
-    int b, item;  // sequence, (kv head, row group) within it
+    uint64_t bits;
+    static __device__ __forceinline__ AttnRecord of(int parts, int b, int item)
+    {
+        return {(uint64_t)parts | (uint64_t)item << 16 | (uint64_t)b << 40};
+    }
+    __device__ __forceinline__ int parts() const { return (int)(bits & 0xffffu); }
+    __device__ __forceinline__ int item() const { return (int)(bits >> 16 & 0xffffffu); }
+    __device__ __forceinline__ int b() const { return (int)(bits >> 40); }
 };
 
 __device__ __forceinline__ float* attn_part(const AttnArgs& a, const AttnPlan& p, int split, int which, int tile, int floats)
@@ -706,7 +755,7 @@ __device__ __forceinline__ void attn_emit(const AttnArgs& a, const AttnPlan& p, 
 
 template <int FMT, int NB, int MODE, typename T>
 __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
-    attn_split_kernel(const AttnArgs a, const AttnPlan p, unsigned int* status)
+    attn_split_kernel(const AttnArgs a, const __grid_constant__ AttnPlan p, unsigned int* status)
 {
     using Sh = AttnShape<FMT, NB, MODE>;
     constexpr int NR = Sh::NR;
@@ -737,13 +786,12 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
 
     // the line, and this split's piece of it
     const int64_t total = attn_total(a, items, lane);
-    int64_t piece = (total + p.splits - 1) / p.splits;
-    piece += piece & 1;
-    if (piece < ATTN_MIN_PIECE) piece = ATTN_MIN_PIECE;
+    const AttnCut cut(p, total);
     const int split_id = blockIdx.x * p.ws + split;
     AttnWalk seg{};
     if (warp < warps) {
-        const int64_t start = piece * split_id;
+        const int64_t first = cut.start(p, split), start = cut.chunk * blockIdx.x + first;
+        const int64_t piece = cut.start(p, split + 1) - first;
         seg = attn_find(a, items, start, total - start < piece ? total - start : piece, lane);
         if (wrow == 0 && lane == 0) s_walk[split] = seg;
     }
@@ -854,7 +902,7 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
     bool dead = false;
     AttnState<FMT, NB, MODE> st;
     st.magic = p.magic;
-    AttnRecord record{0, 0, 0};
+    AttnRecord record{0};
 
     for (; !seg.done(); seg.next(a, items)) {
         const int kvh = seg.item / p.row_groups;
@@ -1004,8 +1052,8 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
                 __stcg(to + (Sh::NO + NR + r) * 32, st.l[r]);
             }
             if (seg.ta == 0) {
-                const int64_t last = (seg.line + ATTN_ITEM_COST + seg.count - 1) / piece;
-                record = {(int)last - split_id + 1, seg.b, seg.item};
+                const int last = cut.split_of(p, seg.line + ATTN_ITEM_COST + seg.count - 1);
+                record = AttnRecord::of(last - split_id + 1, seg.b, seg.item);
             }
         }
     }
@@ -1030,19 +1078,26 @@ __global__ void __launch_bounds__(ATTN_JOIN_WARPS * 32) attn_join_kernel(const A
     pdl_launch_dependents();
     pdl_wait();
     // the splits with a record, in order (the same for every CTA)
-    const int words = (p.splits + 31) / 32;
-    for (int w = warp; w < words; w += ATTN_JOIN_WARPS) {
-        const int i = w * 32 + lane;
-        const AttnRecord rec = i < p.splits ? a.records[i] : AttnRecord{0, 0, 0};
-        s_rec[i] = rec;
-        const uint32_t has = __ballot_sync(0xffffffffu, rec.parts > 0);
+    constexpr int WORDS = ATTN_MAX_SPLITS / 32;
+    AttnRecord got[WORDS / ATTN_JOIN_WARPS];
+#pragma unroll
+    for (int j = 0; j < WORDS / ATTN_JOIN_WARPS; ++j) {  // (all on the way at once)
+        const int i = (j * ATTN_JOIN_WARPS + warp) * 32 + lane;
+        got[j] = i < p.splits ? a.records[i] : AttnRecord{0};
+    }
+#pragma unroll
+    for (int j = 0; j < WORDS / ATTN_JOIN_WARPS; ++j) {
+        const int w = j * ATTN_JOIN_WARPS + warp;
+        s_rec[w * 32 + lane] = got[j];
+        const uint32_t has = __ballot_sync(0xffffffffu, got[j].parts() > 0);
         if (lane == 0) s_has[w] = has;
     }
     __syncthreads();
     if (warp == 0) {
         int before = 0;
-        for (int w0 = 0; w0 < words; w0 += 32) {
-            uint32_t has = w0 + lane < words ? s_has[w0 + lane] : 0u;
+#pragma unroll
+        for (int w0 = 0; w0 < WORDS; w0 += 32) {
+            uint32_t has = s_has[w0 + lane];
             int sum = __popc(has);
             const int own = sum;
 #pragma unroll
@@ -1066,12 +1121,12 @@ __global__ void __launch_bounds__(ATTN_JOIN_WARPS * 32) attn_join_kernel(const A
         const int unit = job % (p.wr * Sh::UNITS), tile = unit / Sh::UNITS, w = unit % Sh::UNITS;
         const int r = w % NR, h = w / NR % 2, b = w / (2 * NR);
         float m = -INFINITY, l = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        AttnRecord rec{0, 0, 0};
+        AttnRecord rec{0};
         if (job < jobs) {
             const int s0 = s_split[job / (p.wr * Sh::UNITS)];
             rec = s_rec[s0];
 #pragma unroll 4
-            for (int i = part0; i < rec.parts; i += per) {
+            for (int i = part0; i < rec.parts(); i += per) {
                 const float* from = attn_part(a, p, s0 + i, i == 0, tile, Sh::PART) + lane;
                 const float m2 = __ldcg(from + (Sh::NO + r) * 32), l2 = __ldcg(from + (Sh::NO + NR + r) * 32);
                 const float mn = fmaxf(m, m2), bs = attn_base(mn), f1 = ex2(m - bs), f2 = ex2(m2 - bs);
@@ -1109,7 +1164,7 @@ __global__ void __launch_bounds__(ATTN_JOIN_WARPS * 32) attn_join_kernel(const A
             __syncthreads();
         }
         if (part0 == 0 && job < jobs)
-            attn_emit<FMT, NB, MODE, T>(a, p, o_wide, rec.b, rec.item, tile, b, h, r, lane, v, m, l);
+            attn_emit<FMT, NB, MODE, T>(a, p, o_wide, rec.b(), rec.item(), tile, b, h, r, lane, v, m, l);
     }
 }
 
@@ -1135,6 +1190,15 @@ AttnPlan attn_plan(const DeviceInfo& di, int rows)
         break;
     }
     p.splits = (di.sms < ATTN_GRID ? di.sms : ATTN_GRID) * p.ws;
+    // A warp that has its scheduler (warp number mod 4) to itself is faster; the
+    // split whose warps all are gets more.
+    int on[4] = {0, 0, 0, 0};
+    for (int w = 0; w < p.ws * p.wr; ++w) ++on[w % 4];
+    for (int s = 0; s < p.ws; ++s) {
+        bool alone = true;
+        for (int w = s * p.wr; w < (s + 1) * p.wr; ++w) alone = alone && on[w % 4] == 1;
+        p.cum[s + 1] = p.cum[s] + (alone ? attn_share_alone(FMT, NB) : ATTN_SHARE);
+    }
     return p;
 }
 

@@ -160,7 +160,7 @@ int launch_kv_read(int fmt, int type, const KvArgs& a, cudaStream_t s);
 // ---- attention ---------------------------------------------------------------
 
 constexpr int ATTN_MAX_SPLITS = 2048;
-constexpr size_t ATTN_RECORD_BYTES = (size_t)ATTN_MAX_SPLITS * 12;  // of the workspace, before the partial results
+constexpr size_t ATTN_RECORD_BYTES = (size_t)ATTN_MAX_SPLITS * 8;  // of the workspace, before the partial results
 
 struct AttnRecord;
 

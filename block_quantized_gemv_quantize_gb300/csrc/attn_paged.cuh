@@ -95,8 +95,8 @@ struct AttnShape {
     static constexpr int Q_TERMS = MODE == ATTN_TWO ? 2 : 1;
     static constexpr int WARPS = ATTN_WARPS;
     static constexpr int STEP = 2;                           // tiles of a step without an edge
-    static constexpr int UNITS = NB * 2 * NR;                // runs of four output values of a lane
-    // where value k of the run (block b, half h, row g + 8 r) stands among a lane's outputs
+    static constexpr int RUNS = NB * NR;                     // runs of eight output values of a lane: (block b, row g + 8 r)
+    // where value k of a run's half h stands among a lane's outputs
     __host__ __device__ static constexpr int place(int b, int h, int r, int k)
     {
         return FMT == QGEMV_KV_Q4_0 ? (b * 4 + 2 * (k & 1) + h) * NC + 2 * r + (k >> 1) : (b * 4 + k) * NC + 2 * r + h;
@@ -1062,7 +1062,7 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
 }
 
 // The items that splits share: out of their partial results, in the order of
-// the splits.  A job is one run of four values of a row of an item: a warp's
+// the splits.  A job is a run of eight values of a row of an item, or half of it: a warp's
 // lanes hold its rows and columns as the splits' lanes did.  `per` warps of a
 // CTA take a job's partial results in turn.
 template <int FMT, int NB, int MODE, typename T>
@@ -1073,7 +1073,7 @@ __global__ void __launch_bounds__(ATTN_JOIN_WARPS * 32) attn_join_kernel(const A
     __shared__ int s_split[ATTN_MAX_SPLITS], s_items;
     __shared__ AttnRecord s_rec[ATTN_MAX_SPLITS];
     __shared__ uint32_t s_has[ATTN_MAX_SPLITS / 32];
-    __shared__ float s_sum[ATTN_JOIN_WARPS][6][32];
+    __shared__ float s_sum[ATTN_JOIN_WARPS][10][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_launch_dependents();
     pdl_wait();
@@ -1093,58 +1093,59 @@ __global__ void __launch_bounds__(ATTN_JOIN_WARPS * 32) attn_join_kernel(const A
         if (lane == 0) s_has[w] = has;
     }
     __syncthreads();
-    if (warp == 0) {
+#pragma unroll
+    for (int j = 0; j < WORDS / ATTN_JOIN_WARPS; ++j) {
+        const int w = j * ATTN_JOIN_WARPS + warp;
         int before = 0;
 #pragma unroll
-        for (int w0 = 0; w0 < WORDS; w0 += 32) {
-            uint32_t has = s_has[w0 + lane];
-            int sum = __popc(has);
-            const int own = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int up = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += up;
-            }
-            for (int at = before + sum - own; has; has &= has - 1) s_split[at++] = (w0 + lane) * 32 + __ffs(has) - 1;
-            before += __shfl_sync(0xffffffffu, sum, 31);
-        }
-        if (lane == 0) s_items = before;
+        for (int k = 0; k < WORDS; k += 32) before += k + lane < w ? __popc(s_has[k + lane]) : 0;
+        before = __reduce_add_sync(0xffffffffu, before);
+        const uint32_t has = s_has[w];
+        if (has >> lane & 1) s_split[before + __popc(has & ((1u << lane) - 1))] = w * 32 + lane;
+        if (w == WORDS - 1 && lane == 0) s_items = before + __popc(has);
     }
     __syncthreads();
-    const int jobs = s_items * p.wr * Sh::UNITS;
+    // one job a run where that fills the GPU, else one a half of it
+    const int halves = s_items * p.wr * Sh::RUNS * 2 > (int)gridDim.x * ATTN_JOIN_WARPS ? 1 : 2;
+    const int in_item = p.wr * Sh::RUNS * halves, jobs = s_items * in_item;
     int per = ATTN_JOIN_WARPS;
     while (per > 1 && jobs * per > (int)gridDim.x * ATTN_JOIN_WARPS) per >>= 1;
     const int at_once = ATTN_JOIN_WARPS / per, part0 = warp % per;
     const bool o_wide = KvRows{a.out, a.o_row, a.o_head}.wide<T>();
     for (int base = blockIdx.x * at_once; base < jobs; base += gridDim.x * at_once) {
         const int job = base + warp / per;
-        const int unit = job % (p.wr * Sh::UNITS), tile = unit / Sh::UNITS, w = unit % Sh::UNITS;
-        const int r = w % NR, h = w / NR % 2, b = w / (2 * NR);
-        float m = -INFINITY, l = 0.0f, v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const int run = job % in_item / halves, tile = run / Sh::RUNS, r = run % NR, b = run % Sh::RUNS / NR;
+        const int h = halves == 2 ? job & 1 : 0;  // of the run, its first half or all
+        float m = -INFINITY, l = 0.0f, v[8] = {};
         AttnRecord rec{0};
         if (job < jobs) {
-            const int s0 = s_split[job / (p.wr * Sh::UNITS)];
+            const int s0 = s_split[job / in_item];
             rec = s_rec[s0];
+            // (two loops, so that the loads of four partial results go together)
+            auto gather = [&](auto whole) {
 #pragma unroll 4
-            for (int i = part0; i < rec.parts(); i += per) {
-                const float* from = attn_part(a, p, s0 + i, i == 0, tile, Sh::PART) + lane;
-                const float m2 = __ldcg(from + (Sh::NO + r) * 32), l2 = __ldcg(from + (Sh::NO + NR + r) * 32);
-                const float mn = fmaxf(m, m2), bs = attn_base(mn), f1 = ex2(m - bs), f2 = ex2(m2 - bs);
-                m = mn;
-                l = l * f1 + l2 * f2;
+                for (int i = part0; i < rec.parts(); i += per) {
+                    const float* from = attn_part(a, p, s0 + i, i == 0, tile, Sh::PART) + lane;
+                    const float m2 = __ldcg(from + (Sh::NO + r) * 32), l2 = __ldcg(from + (Sh::NO + NR + r) * 32);
+                    float x[whole ? 8 : 4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int at = FMT == QGEMV_KV_Q4_0 ? (b * 4 + 2 * (k & 1) + h) * Sh::NC + 2 * r + (k >> 1)
-                                                        : (b * 4 + k) * Sh::NC + 2 * r + h;
-                    v[k] = v[k] * f1 + __ldcg(from + at * 32) * f2;
+                    for (int k = 0; k < (whole ? 8 : 4); ++k)
+                        x[k] = __ldcg(from + Sh::place(b, whole ? k >> 2 : h, r, k & 3) * 32);
+                    const float mn = fmaxf(m, m2), bs = attn_base(mn), f1 = ex2(m - bs), f2 = ex2(m2 - bs);
+                    m = mn;
+                    l = l * f1 + l2 * f2;
+#pragma unroll
+                    for (int k = 0; k < (whole ? 8 : 4); ++k) v[k] = v[k] * f1 + x[k] * f2;
                 }
-            }
+            };
+            if (halves == 1) gather(std::true_type{});
+            else gather(std::false_type{});
         }
         if (per > 1) {
             float(*mine)[32] = s_sum[warp];
             mine[0][lane] = m, mine[1][lane] = l;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) mine[2 + k][lane] = v[k];
+            for (int k = 0; k < 8; ++k) mine[2 + k][lane] = v[k];
             __syncthreads();
             if (part0 == 0) {
                 float top = m;
@@ -1152,19 +1153,22 @@ __global__ void __launch_bounds__(ATTN_JOIN_WARPS * 32) attn_join_kernel(const A
                 const float bs = attn_base(top), f0 = ex2(m - bs);
                 l *= f0;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) v[k] *= f0;
+                for (int k = 0; k < 8; ++k) v[k] *= f0;
                 for (int i = 1; i < per; ++i) {
                     const float f = ex2(s_sum[warp + i][0][lane] - bs);
                     l += s_sum[warp + i][1][lane] * f;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) v[k] += s_sum[warp + i][2 + k][lane] * f;
+                    for (int k = 0; k < 8; ++k) v[k] += s_sum[warp + i][2 + k][lane] * f;
                 }
                 m = top;
             }
             __syncthreads();
         }
-        if (part0 == 0 && job < jobs)
-            attn_emit<FMT, NB, MODE, T>(a, p, o_wide, rec.b(), rec.item(), tile, b, h, r, lane, v, m, l);
+        if (part0 == 0 && job < jobs) {
+            const float lo[4] = {v[0], v[1], v[2], v[3]}, hi[4] = {v[4], v[5], v[6], v[7]};
+            attn_emit<FMT, NB, MODE, T>(a, p, o_wide, rec.b(), rec.item(), tile, b, h, r, lane, lo, m, l);
+            if (halves == 1) attn_emit<FMT, NB, MODE, T>(a, p, o_wide, rec.b(), rec.item(), tile, b, 1, r, lane, hi, m, l);
+        }
     }
 }
 

@@ -1149,11 +1149,13 @@ __global__ void __launch_bounds__(ATTN_JOIN_WARPS * 32) attn_join_kernel(const A
             __syncthreads();
             if (part0 == 0) {
                 float top = m;
+#pragma unroll 5
                 for (int i = 1; i < per; ++i) top = fmaxf(top, s_sum[warp + i][0][lane]);
                 const float bs = attn_base(top), f0 = ex2(m - bs);
                 l *= f0;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) v[k] *= f0;
+#pragma unroll 5
                 for (int i = 1; i < per; ++i) {
                     const float f = ex2(s_sum[warp + i][0][lane] - bs);
                     l += s_sum[warp + i][1][lane] * f;
@@ -1187,7 +1189,7 @@ AttnPlan attn_plan(const DeviceInfo& di, int rows)
         const uint32_t budget = (uint32_t)di.smem_optin - 2048;  // beside the static shared memory
         const int stages = budget > q ? (int)((budget - q) / per_stage) : 0;
         if (stages < 2 && p.ws > 1) continue;
-        p.stages = stages > 4 ? 4 : stages;
+        p.stages = stages > 3 ? 3 : stages;
         p.off_q = (uint32_t)p.ws * p.stages * 2 * Sh::TILE;
         p.off_bar = p.off_q + q;
         p.bytes = p.off_bar + (uint32_t)p.ws * p.stages * 20;

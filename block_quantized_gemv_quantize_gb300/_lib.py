@@ -1,4 +1,5 @@
-"""Thin ctypes binding of libqgemv.so (argument marshalling only).
+"""Thin ctypes binding of libqgemv.so (argument marshalling only; the paged
+cache's calls first take the compiled short way of csrc/binding.cpp).
 
 Every function here has the name of the C entry point it calls, takes torch
 tensors (device memory) plus sizes, passes raw pointers and the current CUDA
@@ -11,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import importlib.util
 import os
 import threading
 
@@ -104,6 +106,22 @@ def _load() -> ctypes.CDLL:
 
 
 LIB = _load()
+
+
+def _load_calls():
+    """csrc/binding.cpp, bound to the loaded library."""
+    if not os.path.exists(_build.CALLS):
+        raise ImportError(f"{_build.CALLS} is missing: build the library first "
+                          f"(python -m block_quantized_gemv_quantize_gb300.build)")
+    spec = importlib.util.spec_from_file_location("qgemv_calls", _build.CALLS)
+    calls = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(calls)
+    calls.init(*(ctypes.cast(getattr(LIB, name), ctypes.c_void_p).value for name in (
+        "kv_write", "kv_read", "attn_paged", "kv_page_bytes", "attn_paged_workspace_bytes")))
+    return calls
+
+
+_CALLS = _load_calls()
 LIB_PATH = _build.LIB_DEBUG if BOUNDS_CHECK else _build.LIB
 
 
@@ -510,6 +528,9 @@ def kv_write(cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slots: torch
     """Quantize k, v [tokens, kv heads, head_dim] into the cache (uint8, whole
     pages of kv_page_bytes) at slots (int64 [tokens]; a slot outside the cache
     skips its token).  k and v may be slices with any strides between rows."""
+    done = _CALLS.kv_write(cache, k, v, slots, KV_FORMATS.get(fmt, -1), page_tokens)
+    if done is not None:
+        return _check("kv_write", done)
     kp, k0, k1 = _rows(k, "k")
     vp, v0, v1 = _rows(v, "v", like=k)
     n, heads, dim = k.shape
@@ -527,6 +548,12 @@ def kv_read(cache: torch.Tensor, slots: torch.Tensor, fmt: str, page_tokens: int
             dtype: torch.dtype = torch.float32, k: torch.Tensor | None = None, v: torch.Tensor | None = None):
     """(k, v) [tokens, kv heads, head_dim]: the values of the cache's slots
     (zeros for a slot outside the cache), in dtype or into the given tensors."""
+    done = _CALLS.kv_read(cache, slots, KV_FORMATS.get(fmt, -1), page_tokens, n_kv_heads, head_dim,
+                          _TYPES.get(dtype, -1), k, v)
+    if type(done) is tuple:
+        return done
+    if done is not None:
+        _check("kv_read", done)
     n = slots.numel()
     shape = (n, n_kv_heads, head_dim)
     if k is None:
@@ -562,6 +589,12 @@ def attn_paged(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, k
     rows, with an optional sliding window.  scale defaults to head_dim^-1/2;
     lse (fp32 [batch * rows, heads]) receives the rows' log-sum-exp; ws (uint8,
     attn_paged_workspace_bytes) is scratch that calls in flight do not share."""
+    done = _CALLS.attn_paged(q, cache, page_table, kv_lens, KV_FORMATS.get(fmt, -1), page_tokens, n_kv_heads, rows, scale,
+                             window, out, lse, ws)
+    if type(done) is int:
+        _check("attn_paged", done)
+    elif done is not None:
+        return done
     qp, q0, q1 = _rows(q, "q")
     n, heads, dim = q.shape
     device = q.device

@@ -1,7 +1,9 @@
 """In-tree build of ``libqgemv.so`` for sm_103a with nvcc (no cmake).
 
 Each translation unit compiles in its own nvcc process, in parallel, then the
-objects are linked into one shared library under ``_build/``.
+objects are linked into one shared library under ``_build/``.  ``csrc/binding.cpp``
+(the short way from Python into the paged cache's calls) becomes a Python module
+beside it.
 
 ``build(debug=True)`` (``python -m block_quantized_gemv_quantize_gb300.build
 --debug``) makes the bounds-checking library ``_build/debug/libqgemv.so``
@@ -21,6 +23,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libqgemv.so")
+CALLS = os.path.join(BUILD, "qgemv_calls.so")  # csrc/binding.cpp
 BUILD_DEBUG = os.path.join(BUILD, "debug")
 LIB_DEBUG = os.path.join(BUILD_DEBUG, "libqgemv.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
@@ -54,12 +57,40 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
+def build_calls(force: bool = False) -> str:
+    """Compile csrc/binding.cpp against the torch that is installed (host code
+    only); returns its path."""
+    src = os.path.join(CSRC, "binding.cpp")
+    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= os.path.getmtime(src):
+        return CALLS
+    import sysconfig
+
+    import torch
+
+    os.makedirs(BUILD, exist_ok=True)
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(_nvcc()))
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", src, "-o", tmp,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), "-L", os.path.join(root, "lib"),
+           "-Wl,-rpath," + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stderr[-4000:]}")
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None,
           debug: bool = False) -> str:
     """Compile every CUDA source and link libqgemv.so (the bounds-checking
     one under _build/debug with debug=True); returns its path."""
     lib, bdir = (LIB_DEBUG, BUILD_DEBUG) if debug else (LIB, BUILD)
     if not force and up_to_date(lib):
+        build_calls()
         return lib
     os.makedirs(bdir, exist_ok=True)
     nvcc = _nvcc()
@@ -76,8 +107,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         return obj
 
     srcs = sources()
-    with ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        calls = ex.submit(build_calls, force)
         objs = list(ex.map(compile_one, srcs))
+        calls.result()
     tmp = lib + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"], capture_output=True, text=True)
     if r.returncode != 0:

@@ -38,12 +38,12 @@
 // does not depend on the order in which CTAs finish.
 //
 // What bounds it.  46 ragged sequences of up to 8192 tokens (q8_0, bf16 rows):
-// 85 us, 5.3 TB/s; the copies alone, without the arithmetic, take 81.  One kv head
-// a query head in f16: 43 us, 4.9 TB/s, as the copies alone.  Two sequences of
-// 131071 tokens in q4_0 (fp16 rows, pairs of terms): 104 us where the copies alone
-// take 58: 470 instructions a tile of 16 tokens and 8 rows, of which 32 are the
-// products, at 0.6 an SM quarter and cycle.  Width 6 over 17391 tokens (30 rows a
-// kv head, two terms): 32 us, of them 21 in the splits at one instruction in three
+// 81 us, 5.5 TB/s, nearly what the copies and the join take without the arithmetic.
+// One kv head a query head in f16: 40 us, 5.2 TB/s, likewise.  Two sequences of
+// 131071 tokens in q4_0 (fp16 rows, pairs of terms): 96 us where the copies alone
+// take 58: 420 instructions a tile of 16 tokens and 8 rows, of which 32 are the
+// products, at 0.55 an SM quarter and cycle.  Width 6 over 17391 tokens (30 rows a
+// kv head, two terms): 30 us, of them 20 in the splits at one instruction in three
 // cycles a warp (two warps a scheduler, 255 registers each).  A call of 197 tokens
 // takes 10 us: two launches, three dependent reads before the first tile arrives
 // (lengths, page number, tile) and the join.
@@ -58,8 +58,8 @@ namespace qgemv {
 constexpr int ATTN_GRID = 160;       // most CTAs (one an SM): the workspace holds their partial results
 constexpr int ATTN_JOIN_WARPS = 16;  // of a CTA of the joining kernel
 // What an item costs besides its tiles (q, a cut into partial results), in tiles;
-// even.  46 ragged sequences, and 17 rows with a window at D = 256: 94 and 84 us
-// with 4, 87 and 79 with 8, 90 and 80 with 16.
+// even.  46 ragged sequences, and 17 rows with a window at D = 256, as they stood
+// then: 94 and 84 us with 4, 87 and 79 with 8, 90 and 80 with 16.
 constexpr int ATTN_ITEM_COST = 8;
 // Least units of a split: a single sequence of 197 tokens takes 10.8 us with 2,
 // 12.2 with 4, 15.1 with 8.

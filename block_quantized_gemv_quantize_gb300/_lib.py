@@ -462,6 +462,7 @@ def argmax_f32_rows(y: torch.Tensor, N: int | None = None, ids: torch.Tensor | N
 
 # ---------------------------------------------------------------- the paged key-value cache
 
+_attn_lock = threading.Lock()
 KV_FORMATS = {"f16": 0, "q8_0": 1, "q4_0": 2}
 _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
@@ -626,11 +627,13 @@ def attn_paged(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, k
             if torch.cuda.is_current_stream_capturing() else workspace(device, need, key="attn")
     elif ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
         raise ValueError("ws must be contiguous uint8 on q's device")
-    _check("attn_paged", LIB.attn_paged(
-        KV_FORMATS[fmt], _type(q, "q"), qp, q0, q1, cp, pages, page_tokens, page_table.data_ptr(),
-        ld[0] if batch > 1 else max(ld[0], max_pages), max_pages, kv_lens.data_ptr(), op, o0, o1,
-        None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), batch, rows, heads, n_kv_heads, dim,
-        dim ** -0.5 if scale is None else scale, window, _stream(q)))
+    with _attn_lock:  # no other thread's kernels between this call's two, which share the stream's workspace
+        done = LIB.attn_paged(
+            KV_FORMATS[fmt], _type(q, "q"), qp, q0, q1, cp, pages, page_tokens, page_table.data_ptr(),
+            ld[0] if batch > 1 else max(ld[0], max_pages), max_pages, kv_lens.data_ptr(), op, o0, o1,
+            None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), batch, rows, heads, n_kv_heads, dim,
+            dim ** -0.5 if scale is None else scale, window, _stream(q))
+    _check("attn_paged", done)
     return out
 
 

@@ -227,13 +227,14 @@ PyObject* attn_paged(PyObject*, PyObject* const* a, Py_ssize_t n_args)
         ws = workspace(device, stream, need);
     }
     const int64_t ld = batch > 1 ? table->stride(0) : std::max(table->stride(0), max_pages);
-    const int status = unlocked([&] {
-        return attn_entry(fmt, type, q->data_ptr(), q->stride(0), q->stride(1), cache->data_ptr(), pages, page,
-                          static_cast<const int32_t*>(table->data_ptr()), ld, (int)max_pages,
-                          static_cast<const int32_t*>(lens->data_ptr()), out.data_ptr(), out.stride(0), out.stride(1),
-                          lse ? static_cast<float*>(lse->data_ptr()) : nullptr, ws.data_ptr(), (size_t)ws.numel(),
-                          (int)batch, rows, heads, kv_heads, dim, (float)scale, window, stream);
-    });
+    // (With the interpreter's lock: the call's two kernels share the stream's
+    // workspace, and another thread's must not come between them.)
+    const int status =
+        attn_entry(fmt, type, q->data_ptr(), q->stride(0), q->stride(1), cache->data_ptr(), pages, page,
+                   static_cast<const int32_t*>(table->data_ptr()), ld, (int)max_pages,
+                   static_cast<const int32_t*>(lens->data_ptr()), out.data_ptr(), out.stride(0), out.stride(1),
+                   lse ? static_cast<float*>(lse->data_ptr()) : nullptr, ws.data_ptr(), (size_t)ws.numel(), (int)batch,
+                   rows, heads, kv_heads, dim, (float)scale, window, stream);
     if (status) return PyLong_FromLong(status);
     if (a[10] != Py_None) return Py_NewRef(a[10]);
     return THPVariable_Wrap(std::move(out));

@@ -378,6 +378,49 @@ def test_offsets_past_32_bits(ops):
     check_attention(ops, args, q.double().cpu().numpy(), [kv], [130])
 
 
+@pytest.mark.parametrize("short_way", [True, False])
+def test_threads_on_one_stream(ops, short_way, monkeypatch):
+    # the two kernels of a call and the workspace between them, with calls of other threads
+    import threading
+
+    if not short_way:
+        monkeypatch.setattr(ops._CALLS, "attn_paged", lambda *a: None)
+    cases = [attention_case(ops, "q8_0", "float32", [900 + 100 * i, 30], 2, 8, 2, 64, 16, 0, seed=i)[0] for i in range(4)]
+    wants = [ops.attn_paged(**c) for c in cases]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(i):
+        for _ in range(100):
+            if not torch.equal(ops.attn_paged(**cases[i]), wants[i]):
+                wrong.append(i)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+
+
+def test_the_short_way_and_ctypes_agree(ops, monkeypatch):
+    args, q, kv = attention_case(ops, "q4_0", "bfloat16", [100, 37], 3, 10, 2, 128, 16, 20)
+    cache, slots = args["cache"].clone(), torch.arange(40, device=DEV)
+    rows = torch.randn((40, 2, 128), device=DEV).bfloat16()
+
+    def both():
+        c = cache.clone()
+        ops.kv_write(c, rows, rows, slots, "q4_0", 16)
+        return (c, *ops.kv_read(c, slots, "q4_0", 16, 2, 128, dtype=torch.float16), ops.attn_paged(**args, scale=0.1))
+
+    first = both()
+    for name in ("kv_write", "kv_read", "attn_paged"):
+        monkeypatch.setattr(ops._CALLS, name, lambda *a: None)
+    for a, b in zip(first, both()):
+        assert a.dtype == b.dtype and a.shape == b.shape
+        assert torch.equal(torch.nan_to_num(a.float()), torch.nan_to_num(b.float()))
+
+
 def test_another_stream_and_a_graph(ops):
     lens = [333, 20]
     args, q, kv = attention_case(ops, "q4_0", "float16", lens, 2, 8, 2, 128, 32, 0)

@@ -252,17 +252,21 @@ __device__ __forceinline__ void v_fragments(const uint8_t* v, int b, int g, int 
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint32_t*>(at(i));
         uint32_t x = __byte_perm(w[0], w[1], 0x5140), y = __byte_perm(w[0], w[1], 0x7362);
-        lo[0] = codes_q8<0x4140>(x, magic), lo[1] = codes_q8<0x4342>(x, magic), lo[2] = codes_q8<0x4140>(y, magic), lo[3] = codes_q8<0x4342>(y, magic);
+        lo[0] = codes_q8<0x4140>(x, magic), lo[1] = codes_q8<0x4342>(x, magic);
+        lo[2] = codes_q8<0x4140>(y, magic), lo[3] = codes_q8<0x4342>(y, magic);
         x = __byte_perm(w[2], w[3], 0x5140), y = __byte_perm(w[2], w[3], 0x7362);
-        hi[0] = codes_q8<0x4140>(x, magic), hi[1] = codes_q8<0x4342>(x, magic), hi[2] = codes_q8<0x4140>(y, magic), hi[3] = codes_q8<0x4342>(y, magic);
+        hi[0] = codes_q8<0x4140>(x, magic), hi[1] = codes_q8<0x4342>(x, magic);
+        hi[2] = codes_q8<0x4140>(y, magic), hi[3] = codes_q8<0x4342>(y, magic);
     } else {
         uint32_t w[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const uint16_t*>(at(i));
         uint32_t x = __byte_perm(w[0], w[1], 0x5410), y = x >> 8;
-        lo[0] = codes_q4_lo(x, magic), lo[1] = codes_q4_hi(x, magic), lo[2] = codes_q4_lo(y, magic), lo[3] = codes_q4_hi(y, magic);
+        lo[0] = codes_q4_lo(x, magic), lo[1] = codes_q4_hi(x, magic);
+        lo[2] = codes_q4_lo(y, magic), lo[3] = codes_q4_hi(y, magic);
         x = __byte_perm(w[2], w[3], 0x5410), y = x >> 8;
-        hi[0] = codes_q4_lo(x, magic), hi[1] = codes_q4_hi(x, magic), hi[2] = codes_q4_lo(y, magic), hi[3] = codes_q4_hi(y, magic);
+        hi[0] = codes_q4_lo(x, magic), hi[1] = codes_q4_hi(x, magic);
+        hi[2] = codes_q4_lo(y, magic), hi[3] = codes_q4_hi(y, magic);
     }
 }
 
@@ -463,7 +467,8 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
 #pragma unroll
         for (int u = u0; u < u1; ++u) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) k_fragment<FMT>(x.tile + u * Sh::TILE, b, tile_token(g >> 1, 2 * j + (g & 1)), t, st.magic, f[u][j]);
+            for (int j = 0; j < 2; ++j)
+                k_fragment<FMT>(x.tile + u * Sh::TILE, b, tile_token(g >> 1, 2 * j + (g & 1)), t, st.magic, f[u][j]);
         }
 #pragma unroll
         for (int s = 0; s < 2; ++s)

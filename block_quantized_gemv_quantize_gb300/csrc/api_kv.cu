@@ -96,7 +96,7 @@ size_t attn_paged_workspace_bytes(int type, int rows, int n_heads, int n_kv_head
     if (check_type(type) || rows < 1 || rows > QGEMV_MAX_M || n_kv_heads < 1 || n_heads < 1 || n_heads % n_kv_heads ||
         head_dim < QK || head_dim % QK)
         return 0;
-    return attn_workspace_bytes(type, rows, n_heads, n_kv_heads, head_dim);
+    return attn_workspace_bytes(rows, n_heads, n_kv_heads, head_dim);
 }
 
 int attn_paged(int fmt, int type, const void* q, int64_t q_row, int64_t q_head, const void* cache, int64_t n_pages,

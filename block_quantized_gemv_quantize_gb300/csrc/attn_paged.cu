@@ -16,9 +16,9 @@ int launch_attn_q4_0_bf16(const AttnArgs& a, cudaStream_t s);
 
 // Records, then two partial results for every split: of an item that began
 // before its piece, and of one that goes on after it.
-size_t attn_workspace_bytes(int type, int rows, int heads, int kv_heads, int head_dim)
+size_t attn_workspace_bytes(int rows, int heads, int kv_heads, int head_dim)
 {
-    const int n = rows * (heads / kv_heads), nb = head_dim / QK, mode = attn_mode(type, n);
+    const int n = rows * (heads / kv_heads), nb = head_dim / QK, mode = attn_mode(n);
     const int per_tile = mode == ATTN_PAIR ? 8 : 16, most = ATTN_WARPS;
     const int tiles = (n + per_tile - 1) / per_tile, groups = (tiles + most - 1) / most, wr = (tiles + groups - 1) / groups;
     const size_t part = (size_t)(nb * 4 * (per_tile / 4) + 2 * (per_tile / 8)) * 32 * sizeof(float);

@@ -9,14 +9,14 @@
 // at most 4 (so sums are rescaled a few times, not at every new maximum).  The
 // codes are small integers, so they are fp16 exactly and are the tensor cores'
 // B operand without ever being scaled: K's scales multiply the fp32 block
-// sums, V's the weights before they are rounded to fp16.  q and w d_v are fp16,
-// as one term (bf16 callers, whose output keeps 8 bits) or as a pair hi + lo of
-// 22 bits (fp32 and fp16 callers).  q is brought to 2^13 .. 2^14 by an exact
-// power of two per row, w d_v to below 2^15 by one that follows the largest
+// sums, V's the weights before they are rounded to fp16.  q and w d_v are fp16
+// pairs hi + lo of 22 bits, whatever the rows' type (bf16 rows with one term of 11
+// bits had one output in a hundred at a neighbouring value and were no faster: 46
+// ragged sequences 80.5 us, 79.6 with a pair).  q is brought to 2^13 .. 2^14 by an
+// exact power of two per row, w d_v to below 2^15 by one that follows the largest
 // d_v seen so far, so that neither leaves fp16's range.
 //
 // Rows in an instruction of 16 (MODE):
-//   ATTN_ONE   16 rows, one term
 //   ATTN_PAIR  8 rows: their hi in the lower half, their lo in the upper
 //   ATTN_TWO   16 rows, hi and lo in two instructions; the blocks are unpacked
 //              once for 16 rows, which from 9 rows on beats two ATTN_PAIR tiles
@@ -65,10 +65,10 @@ constexpr int ATTN_ITEM_COST = 8;
 // 12.2 with 4, 15.1 with 8.
 constexpr int ATTN_MIN_PIECE = 2;
 
-enum AttnMode { ATTN_ONE = 0, ATTN_PAIR = 1, ATTN_TWO = 2 };
+enum AttnMode { ATTN_PAIR = 1, ATTN_TWO = 2 };
 
-// The mode for a call: by the type's precision and the rows of a kv head.
-inline int attn_mode(int type, int rows) { return type == QGEMV_BF16 ? ATTN_ONE : (rows > 8 ? ATTN_TWO : ATTN_PAIR); }
+// The mode for a call: by the rows of a kv head.
+inline int attn_mode(int rows) { return rows > 8 ? ATTN_TWO : ATTN_PAIR; }
 
 // Shares of a split whose warps share their schedulers with another's, and of one
 // whose warps do not.  The latter is faster where arithmetic bounds the kernel: with
@@ -644,10 +644,7 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
                     split_pair(w[2 * j], w[2 * j + 1], hi[2 * j], hi[2 * j + 1]);
                 } else {
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        if constexpr (MODE == ATTN_TWO) split_pair(w[4 * r + 2 * j], w[4 * r + 2 * j + 1], hi[2 * j + r], lo[2 * j + r]);
-                        else hi[2 * j + r] = h2_bits(__floats2half2_rn(w[4 * r + 2 * j], w[4 * r + 2 * j + 1]));
-                    }
+                    for (int r = 0; r < 2; ++r) split_pair(w[4 * r + 2 * j], w[4 * r + 2 * j + 1], hi[2 * j + r], lo[2 * j + r]);
                 }
             }
         };
@@ -1255,12 +1252,8 @@ int launch_attn_dim(const AttnArgs& a, cudaStream_t s)
 template <int FMT, typename T>
 int launch_attn_rows(const AttnArgs& a, cudaStream_t s)
 {
-    if constexpr (sizeof(T) == 2 && !std::is_same_v<T, __half>) {
-        return launch_attn_dim<FMT, ATTN_ONE, T>(a, s);
-    } else {
-        if (attn_mode(QGEMV_F32, a.rows * a.group) == ATTN_PAIR) return launch_attn_dim<FMT, ATTN_PAIR, T>(a, s);
-        return launch_attn_dim<FMT, ATTN_TWO, T>(a, s);
-    }
+    if (attn_mode(a.rows * a.group) == ATTN_PAIR) return launch_attn_dim<FMT, ATTN_PAIR, T>(a, s);
+    return launch_attn_dim<FMT, ATTN_TWO, T>(a, s);
 }
 
 }  // namespace qgemv

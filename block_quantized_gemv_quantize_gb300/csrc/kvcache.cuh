@@ -183,7 +183,7 @@ struct AttnArgs {
     float* partials;
 };
 
-size_t attn_workspace_bytes(int type, int rows, int heads, int kv_heads, int head_dim);
+size_t attn_workspace_bytes(int rows, int heads, int kv_heads, int head_dim);
 int launch_attn_paged(int fmt, int type, const AttnArgs& a, cudaStream_t s);
 
 // The positions that the rows of a sequence of `len` tokens see: row i sees

@@ -544,8 +544,8 @@ int kv_read(int fmt, int type, const void* cache, int64_t n_pages, int page_toke
  *     out = sum_p softmax_p(scale q . k_p) v_p,   lse = ln sum_p e^{scale q . k_p}.
  * A row that sees no position (kv_lens[b] < rows - i) gets zeros and an lse of
  * minus infinity.  Scores, softmax and sums are fp32; products run on the
- * tensor cores on operands that carry 22 bits for QGEMV_F32 and QGEMV_F16
- * and 11 bits for QGEMV_BF16; one rounding to `type` at the end.  The result
+ * tensor cores on operands that carry 22 bits, whatever `type` is; one
+ * rounding to `type` at the end.  The result
  * is the same, bit for bit, on every call with the same arguments on one
  * kind of device; what lies at masked places of the cache never reaches it.
  *   q          rows of head_dim values, row (r, h) at r * q_row + h * q_head

@@ -14,7 +14,13 @@
 // bits had one output in a hundred at a neighbouring value and were no faster: 46
 // ragged sequences 80.5 us, 79.6 with a pair).  q is brought to 2^13 .. 2^14 by an
 // exact power of two per row, w d_v to below 2^15 by one that follows the largest
-// d_v seen so far, so that neither leaves fp16's range.
+// d_v seen so far, so that neither leaves fp16's range.  That one power for all rows
+// and blocks loses nothing while the scales are within 2^12 of one another.  A warp
+// that has met scales further apart, or of zero, goes through its tiles again
+// (ATTN_AGAIN), with powers for each row and block: then neither what other rows see,
+// nor what other blocks hold, nor tokens without weight take bits from a product.  That
+// makes a split two to four times as long (all of them, 131071 tokens in q4_0: 335 us,
+// not 94); such powers everywhere cost every call (17 rows at D = 256 98 us, not 76).
 //
 // Rows in an instruction of 16 (MODE):
 //   ATTN_PAIR  8 rows: their hi in the lower half, their lo in the upper
@@ -383,6 +389,52 @@ __device__ __forceinline__ void split_pair(float x, float y, uint32_t& hi, uint3
     lo = h2_bits(__floats2half2_rn(dx, dy));
 }
 
+// The least scale that the power of the largest still serves, as fp16 bits, for scales
+// below 2^(e - 14): 2^(e - 27), whose products with a weight of 1 (every row has one)
+// stand at 2^-2 or above, so that a rounding to hi + lo (2^-25 at most there) is off by
+// 2^-23 of the row's and block's largest product.  (A scale of zero is too small: the
+// row's weight may be all on such a token.)
+__device__ __forceinline__ uint32_t attn_least_scale(int e)
+{
+    return e > 13 ? (uint32_t)(e - 12) << 10 : 1u << max(e - 3, 0);
+}
+
+// Powers of two for each row and block, a byte each: the upper byte of the float 2^s,
+// s odd.  They start at the largest, which brings a weight of 1 and the smallest fp16
+// number to 2^13, and fall where a product passes 2^15, to one that leaves the largest
+// at 2^10 .. 2^12 (weights reach 2^4, so the smallest, 2^-7, suffices for any scale).
+// Where the row's reference maximum grows, and all its weights shrink by f, they rise
+// by 1 / f or a little more.  So the largest product of a row and block stands at 2^10
+// or above, and no rounding is off by more than 2^-35 of it.
+constexpr int ATTN_POWER_MOST = 82, ATTN_POWER_LEAST = 60;  // 2^37, 2^-7
+__device__ __forceinline__ float attn_power(uint32_t word, int b)
+{
+    return __uint_as_float(__byte_perm(word, 0, 0x444 | (b & 3) << 12));
+}
+__device__ __forceinline__ float attn_inverse(float power) { return __int_as_float(0x7f000000 - __float_as_int(power)); }
+
+template <int NB, int NR>
+struct AttnPowers {
+    static constexpr int WORDS = (NB + 3) / 4;
+    uint32_t w[NR][WORDS];
+    __device__ __forceinline__ void clear()
+    {
+#pragma unroll
+        for (int r = 0; r < NR; ++r)
+#pragma unroll
+            for (uint32_t& x : w[r]) x = ATTN_POWER_MOST * 0x01010101u;
+    }
+    __device__ __forceinline__ float of(int r, int b) const { return attn_power(w[r][b / 4], b); }
+    // 4^rise times, at most the largest; negative: a fourth as often, at least the smallest
+    __device__ __forceinline__ float change(int r, int b, int rise)
+    {
+        uint32_t& x = w[r][b / 4];
+        const int at = 8 * (b & 3), old = x >> at & 0xff, now = max(ATTN_POWER_LEAST, min(old + rise, ATTN_POWER_MOST));
+        x += (uint32_t)(now - old) << at;
+        return __int_as_float((127 + 2 * (now - old)) << 23);
+    }
+};
+
 // What a warp keeps of its row tile while a segment runs: the rows' reference
 // maximum (of s log2 e), this lane's share of the sum of weights, and the
 // outputs times 2^(25 - e) (fp16 caches: 2^11) in the products' layout.
@@ -392,6 +444,7 @@ struct AttnState {
     float m[Sh::NR], l[Sh::NR], rs[Sh::NR];
     float o[NB][4][4];
     int e;
+    __half2 least;  // of the scales that some row sees, as far as this lane looks at them
     uint32_t magic;
 
     __device__ __forceinline__ void clear()
@@ -405,6 +458,23 @@ struct AttnState {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) o[b][n][c] = 0.0f;
         e = 0;
+        least = bits_h2(0x7c007c00u);
+    }
+    // the outputs of row r and block b times f
+    __device__ __forceinline__ void scale(int r, int b, float f)
+    {
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (MODE == ATTN_PAIR || c >> 1 == r) o[b][n][c] *= f;
+    }
+    // whether the segment's scales are too far apart for one power
+    __device__ __forceinline__ bool far() const
+    {
+        if constexpr (FMT == QGEMV_KV_F16) return false;
+        const uint32_t two = h2_bits(least), low = __reduce_min_sync(0xffffffffu, min(two & 0xffffu, two >> 16));
+        return low < attn_least_scale(e);
     }
     // End of a segment: l over the quad; the two halves of a split row added
     // (an infinite output stands in the high half alone); the scale out.
@@ -433,6 +503,10 @@ struct AttnState {
 // a finite base for exponents: a row that has seen nothing has m = -inf
 __device__ __forceinline__ float attn_base(float m) { return m == -INFINITY ? 0.0f : m; }
 
+// How a step takes its tiles: two whose tokens all rows see; one, of which some tokens
+// may be hidden from some rows; and such a one with powers for each row and block.
+enum AttnKind { ATTN_FULL, ATTN_EDGE, ATTN_AGAIN };
+
 // What one step needs to know of its tiles.
 struct AttnStep {
     const uint8_t* tile;  // the first one's, the other behind it
@@ -440,15 +514,16 @@ struct AttnStep {
     int first, last;  // positions that any row sees
 };
 
-// Two tiles of a split into a warp's row tile; or (EDGE) one, of which some
-// tokens may be hidden from some rows.
-template <int FMT, int NB, int MODE, bool EDGE>
+// One step of a split, into a warp's row tile.
+template <int FMT, int NB, int MODE, AttnKind KIND>
 __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const AttnStep& x,
+                                          AttnPowers<NB, AttnShape<FMT, NB, MODE>::NR>& powers,
                                           const uint32_t (&qf)[AttnShape<FMT, NB, MODE>::Q_SMEM ? 1 : NB * 2][4],
                                           const uint4* q_smem, const int (&begin)[AttnShape<FMT, NB, MODE>::NR],
                                           const int (&end)[AttnShape<FMT, NB, MODE>::NR], int lane)
 {
     using Sh = AttnShape<FMT, NB, MODE>;
+    constexpr bool EDGE = KIND != ATTN_FULL, POWERS = KIND == ATTN_AGAIN && FMT != QGEMV_KV_F16;
     constexpr int NT = EDGE ? 1 : Sh::STEP, NR = Sh::NR, NV = 4 * NR, SCALES = NB * KV_TILE * kv_code_bytes(FMT);
     const int g = lane >> 2, t = lane & 3;
 
@@ -552,19 +627,21 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
             }
     }
 
-    // ---- the largest of V's scales
+    // ---- the largest of V's scales, and the least: lane g's of block g
     int e = st.e;
-    if constexpr (FMT != QGEMV_KV_F16) {
-        __half2 top = bits_h2(0u);  // hmax2 takes the number of a number and a NaN
+    if constexpr (FMT != QGEMV_KV_F16 && !POWERS) {
+        __half2 top = bits_h2(0u);  // hmax2 and hmin2 take the number of a number and a NaN
 #pragma unroll
         for (int u = 0; u < NT; ++u) {
-#pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                uint2 w = *reinterpret_cast<const uint2*>(x.tile + u * Sh::TILE + Sh::HALF + SCALES + b * 32 + 8 * t);
-                if (EDGE) w.x &= live[u][0], w.y &= live[u][1];
-                if (FMT == QGEMV_KV_Q4_0) w.x &= 0x7fff7fffu, w.y &= 0x7fff7fffu;  // q8_0's are never negative
-                top = __hmax2(top, __hmax2(bits_h2(w.x), bits_h2(w.y)));
+            uint2 w = *reinterpret_cast<const uint2*>(x.tile + u * Sh::TILE + Sh::HALF + SCALES + g % NB * 32 + 8 * t);
+            if (FMT == QGEMV_KV_Q4_0) w.x &= 0x7fff7fffu, w.y &= 0x7fff7fffu;  // q8_0's are never negative
+            uint2 v = w;
+            if (EDGE) {
+                w.x &= live[u][0], w.y &= live[u][1];
+                v.x |= ~live[u][0], v.y |= ~live[u][1];
             }
+            top = __hmax2(top, __hmax2(bits_h2(w.x), bits_h2(w.y)));
+            st.least = __hmin2(st.least, __hmin2(bits_h2(v.x), bits_h2(v.y)));
         }
         top = __hmax2(top, __lowhigh2highlow(top));
         const uint32_t bits = __reduce_max_sync(0xffffffffu, h2_bits(top) & 0xffffu);
@@ -587,25 +664,19 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
     }
     if (__any_sync(0xffffffffu, grow)) {
         const float down = __int_as_float((127 + st.e - e) << 23);
-        float f[NR];
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
-            const float mn = fmaxf(st.m[r], mx[r]);
-            f[r] = ex2(st.m[r] - attn_base(mn));
-            st.l[r] *= f[r];
-            f[r] *= down;
+            const float mn = fmaxf(st.m[r], mx[r]), f = ex2(st.m[r] - attn_base(mn));
+            st.l[r] *= f;
             st.m[r] = mn;
+            const int rise = (128 - (int)(__float_as_uint(f) >> 23)) >> 1;  // 4^rise >= 1 / f
+#pragma unroll
+            for (int b = 0; b < NB; ++b) st.scale(r, b, POWERS ? f * powers.change(r, b, rise) : f * down);
         }
         st.e = e;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int nn = 0; nn < 4; ++nn)
-#pragma unroll
-                for (int c = 0; c < 4; ++c) st.o[b][nn][c] *= f[MODE == ATTN_PAIR ? 0 : c >> 1];
     }
     // weights, and from here on times the outputs' scale
-    const float up = FMT == QGEMV_KV_F16 ? 0x1p11f : __int_as_float((127 + 25 - st.e) << 23);
+    const float up = FMT == QGEMV_KV_F16 ? 0x1p11f : (POWERS ? 1.0f : __int_as_float((127 + 25 - st.e) << 23));
 #pragma unroll
     for (int r = 0; r < NR; ++r) {
         const float bs = -attn_base(st.m[r]);
@@ -629,7 +700,7 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
     for (int u = 0; u < NT; ++u) {
         const uint8_t* v8 = x.tile + u * Sh::TILE + Sh::HALF;
         uint32_t hi[4], lo[4];  // A fragments; ATTN_PAIR: hi alone, with the low terms in its upper rows
-        auto weights = [&](const float2 (&d)[2]) {
+        auto weights = [&](const float2 (&d)[2], int b) {
             float w[NV];
 #pragma unroll
             for (int k = 0; k < NV; k += 2) mul_f32x2(w[k], w[k + 1], y[u][k], y[u][k + 1], d[(k >> 1) & 1].x, d[(k >> 1) & 1].y);
@@ -637,6 +708,26 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
 #pragma unroll
                 for (int k = 0; k < NV; ++k)
                     if (hidden >> (u * 8 + k) & 1) w[k] = 0.0f;
+            }
+            if constexpr (POWERS) {
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    float most = 0.0f;  // (a number of a number and a NaN)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        w[4 * r + k] *= powers.of(r, b);
+                        most = fmaxf(most, fabsf(w[4 * r + k]));
+                    }
+                    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+                    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+                    const int fall = most >= 0x1p15f ? ((int)(__float_as_uint(most) >> 23) - 127 - 10) >> 1 : 0;
+                    if (__any_sync(0xffffffffu, fall > 0)) {
+                        const float by = powers.change(r, b, -fall);
+                        st.scale(r, b, by);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) w[4 * r + k] *= by;
+                    }
+                }
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -651,14 +742,14 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
         bool odd_values = false;  // fp16 caches at an edge: infinities or NaN that some row sees
         if constexpr (FMT == QGEMV_KV_F16) {
             const float2 one[2] = {{1.0f, 1.0f}, {1.0f, 1.0f}};
-            weights(one);
+            weights(one, 0);
         }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             if constexpr (FMT != QGEMV_KV_F16) {
                 uint2 w = *reinterpret_cast<const uint2*>(v8 + SCALES + b * 32 + 8 * t);
                 const float2 d[2] = {__half22float2(bits_h2(w.x)), __half22float2(bits_h2(w.y))};
-                weights(d);
+                weights(d, b);
             }
             uint32_t v0[4], v1[4];
             v_fragments<FMT>(v8, b, g, t, st.magic, v0, v1);
@@ -995,6 +1086,7 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
         bool poison = false;
         st.clear();
 
+        AttnPowers<NB, NR> powers;
         for (int tl = seg.ta; tl < seg.tb; tl += 2) {
             const int used = split * S + slot;
             if (!dead) dead = !__all_sync(0xffffffffu, mbar_wait_bounded(&full[used], phase));
@@ -1009,11 +1101,11 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
             if (++slot == S) slot = 0, phase ^= 1;
             if (!poison) {
                 if (tl + 2 <= seg.tb && x.pos >= clear_from && x.pos + 2 * KV_TILE <= clear_to) {
-                    attn_step<FMT, NB, MODE, false>(st, x, qf, q_smem, begin, end, lane);
+                    attn_step<FMT, NB, MODE, ATTN_FULL>(st, x, powers, qf, q_smem, begin, end, lane);
                 } else {
 #pragma unroll 1
                     for (int u = 0; u < 2 && tl + u < seg.tb; ++u) {
-                        attn_step<FMT, NB, MODE, true>(st, x, qf, q_smem, begin, end, lane);
+                        attn_step<FMT, NB, MODE, ATTN_EDGE>(st, x, powers, qf, q_smem, begin, end, lane);
                         x.tile += Sh::TILE;
                         x.pos += KV_TILE;
                     }
@@ -1021,6 +1113,30 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[used]);
+        }
+        if (!poison && !dead && st.far()) {
+            // once more, from the cache itself: the ring has gone on.  (Its tiles all had
+            // their addresses checked by the copying warp; a page whose number has
+            // changed meanwhile is no page.)
+            st.clear();
+            powers.clear();
+            const int tpp = a.L.tiles();
+#pragma unroll 1
+            for (int tl = seg.ta; tl < seg.tb; ++tl) {
+                const int tile = seg.first + tl, n = tile / tpp;
+                const int64_t off = a.L.tile_offset(a.table[seg.b * a.ld_table + n], kvh, tile - n * tpp);
+                if (off < 0 || !QG_OK(qg_in(off, Sh::TILE, a.L.bytes()), status, 732)) {
+                    poison = true;
+                    break;
+                }
+                const AttnStep x{a.cache + off, tile * KV_TILE, sp.first(), sp.last()};
+                attn_step<FMT, NB, MODE, ATTN_AGAIN>(st, x, powers, qf, q_smem, begin, end, lane);
+            }
+            // as if with one power, 2^25
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+#pragma unroll
+                for (int b = 0; b < NB; ++b) st.scale(r, b, 0x1p25f * attn_inverse(powers.of(r, b)));
         }
         st.finish(poison || dead);
 

@@ -544,8 +544,11 @@ int kv_read(int fmt, int type, const void* cache, int64_t n_pages, int page_toke
  *     out = sum_p softmax_p(scale q . k_p) v_p,   lse = ln sum_p e^{scale q . k_p}.
  * A row that sees no position (kv_lens[b] < rows - i) gets zeros and an lse of
  * minus infinity.  Scores, softmax and sums are fp32; products run on the
- * tensor cores on operands that carry 22 bits, whatever `type` is; one
- * rounding to `type` at the end.  The result
+ * tensor cores on operands that carry 22 bits, whatever `type` is: q to no
+ * less than 2^-38 of the row's largest magnitude, a weight times V's scale to
+ * 2^-23 of the largest such product in the row and block (the weights of an
+ * f16 cache to 2^-36 of the row's largest); one rounding to `type` at the
+ * end.  The result
  * is the same, bit for bit, on every call with the same arguments on one
  * kind of device; what lies at masked places of the cache never reaches it.
  *   q          rows of head_dim values, row (r, h) at r * q_row + h * q_head

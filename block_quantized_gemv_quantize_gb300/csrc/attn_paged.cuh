@@ -469,10 +469,21 @@ struct AttnState {
             for (int c = 0; c < 4; ++c)
                 if (MODE == ATTN_PAIR || c >> 1 == r) o[b][n][c] *= f;
     }
-    // whether the segment's scales are too far apart for one power
-    __device__ __forceinline__ bool far() const
+    // Whether the segment has to be gone through again: its scales are too far apart for
+    // one power; or its values, in an fp16 cache, hold an infinity or a NaN, which two
+    // terms of a weight (lo is often negative or zero) and weights of zero make NaN of.
+    __device__ __forceinline__ bool again() const
     {
-        if constexpr (FMT == QGEMV_KV_F16) return false;
+        if constexpr (FMT == QGEMV_KV_F16) {
+            float sum = 0.0f;
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) sum += o[b][n][c];
+            return __any_sync(0xffffffffu, !isfinite(sum));
+        }
         const uint32_t two = h2_bits(least), low = __reduce_min_sync(0xffffffffu, min(two & 0xffffu, two >> 16));
         return low < attn_least_scale(e);
     }
@@ -504,7 +515,8 @@ struct AttnState {
 __device__ __forceinline__ float attn_base(float m) { return m == -INFINITY ? 0.0f : m; }
 
 // How a step takes its tiles: two whose tokens all rows see; one, of which some tokens
-// may be hidden from some rows; and such a one with powers for each row and block.
+// may be hidden from some rows; and such a one with powers for each row and block, or
+// with the infinities and NaN of an fp16 cache's values apart from the products.
 enum AttnKind { ATTN_FULL, ATTN_EDGE, ATTN_AGAIN };
 
 // What one step needs to know of its tiles.
@@ -524,6 +536,7 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
 {
     using Sh = AttnShape<FMT, NB, MODE>;
     constexpr bool EDGE = KIND != ATTN_FULL, POWERS = KIND == ATTN_AGAIN && FMT != QGEMV_KV_F16;
+    constexpr bool APART = KIND == ATTN_AGAIN && FMT == QGEMV_KV_F16;
     constexpr int NT = EDGE ? 1 : Sh::STEP, NR = Sh::NR, NV = 4 * NR, SCALES = NB * KV_TILE * kv_code_bytes(FMT);
     const int g = lane >> 2, t = lane & 3;
 
@@ -739,7 +752,7 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
                 }
             }
         };
-        bool odd_values = false;  // fp16 caches at an edge: infinities or NaN that some row sees
+        bool odd_values = false;  // infinities or NaN that some row sees
         if constexpr (FMT == QGEMV_KV_F16) {
             const float2 one[2] = {{1.0f, 1.0f}, {1.0f, 1.0f}};
             weights(one, 0);
@@ -757,6 +770,7 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
 #pragma unroll
                 for (int nn = 0; nn < 4; ++nn) {
                     auto finite = [&](uint32_t w) {
+                        if (!APART) return w;
                         if ((w & 0x7c00u) == 0x7c00u) w &= 0xffff0000u, odd_values = true;
                         if ((w & 0x7c000000u) == 0x7c000000u) w &= 0x0000ffffu, odd_values = true;
                         return w;
@@ -770,7 +784,7 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
                 if constexpr (MODE == ATTN_TWO) mma_f16(st.o[b][nn], lo, v0[nn], v1[nn]);
             }
         }
-        if constexpr (FMT == QGEMV_KV_F16 && EDGE) {
+        if constexpr (APART) {
             // such values went in as zeros; add them to the rows that see them
             if (__any_sync(0xffffffffu, odd_values)) {
 #pragma unroll
@@ -1114,7 +1128,7 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[used]);
         }
-        if (!poison && !dead && st.far()) {
+        if (!poison && !dead && st.again()) {
             // once more, from the cache itself: the ring has gone on.  (Its tiles all had
             // their addresses checked by the copying warp; a page whose number has
             // changed meanwhile is no page.)
@@ -1132,11 +1146,12 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
                 const AttnStep x{a.cache + off, tile * KV_TILE, sp.first(), sp.last()};
                 attn_step<FMT, NB, MODE, ATTN_AGAIN>(st, x, powers, qf, q_smem, begin, end, lane);
             }
-            // as if with one power, 2^25
+            if constexpr (FMT != QGEMV_KV_F16) {  // as if with one power, 2^25
 #pragma unroll
-            for (int r = 0; r < NR; ++r)
+                for (int r = 0; r < NR; ++r)
 #pragma unroll
-                for (int b = 0; b < NB; ++b) st.scale(r, b, 0x1p25f * attn_inverse(powers.of(r, b)));
+                    for (int b = 0; b < NB; ++b) st.scale(r, b, 0x1p25f * attn_inverse(powers.of(r, b)));
+            }
         }
         st.finish(poison || dead);
 

@@ -601,6 +601,40 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
 #pragma unroll
             for (int b = 0; b < NB; ++b) block(b, u, u + 1);
     }
+    // An infinite key of an fp16 cache: the low term makes NaN of the high term's
+    // infinity, which alone is the score.
+    auto together = [](float hi, float lo) { return isfinite(hi) ? hi + lo : hi; };
+    if constexpr (FMT == QGEMV_KV_F16 && MODE == ATTN_TWO) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) sum += c16[u][j][c];
+        if (__any_sync(0xffffffffu, !isfinite(sum))) {
+#pragma unroll
+            for (int u = 0; u < NT; ++u) {
+                float hi[2][4] = {};
+#pragma unroll 1
+                for (int bs = 0; bs < NB * 2; ++bs) {
+                    const uint4 w = q_smem[bs * Sh::Q_TERMS * 32];
+                    const uint32_t qa[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t f[4];
+                        k_fragment<FMT>(x.tile + u * Sh::TILE, bs >> 1, tile_token(g >> 1, 2 * j + (g & 1)), t, st.magic, f);
+                        mma_f16(hi[j], qa, bs & 1 ? f[2] : f[0], bs & 1 ? f[3] : f[1]);
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        if (!isfinite(c16[u][j][c])) c16[u][j][c] = hi[j][c];
+            }
+        }
+    }
     uint32_t hidden = 0;  // bit 8 u + k: y[u][k] is masked
 #pragma unroll
     for (int u = 0; u < NT; ++u) {
@@ -611,7 +645,7 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
                 float &v0 = y[u][4 * r + 2 * j], &v1 = y[u][4 * r + 2 * j + 1];
                 if constexpr (FMT == QGEMV_KV_F16) {
                     v0 = c16[u][j][2 * r], v1 = c16[u][j][2 * r + 1];
-                    if (MODE == ATTN_PAIR) add_f32x2(v0, v1, v0, v1, c16[u][j][2], c16[u][j][3]);
+                    if (MODE == ATTN_PAIR) v0 = together(v0, c16[u][j][2]), v1 = together(v1, c16[u][j][3]);
                 }
                 mul_f32x2(v0, v1, v0, v1, st.rs[r], st.rs[r]);
             }
@@ -1074,6 +1108,7 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
             ex = max(-100, min(127, ex));
             const float up = __int_as_float((127 + 13 - ex) << 23);
             st.rs[r] = a.scale * 1.4426950408889634f * __int_as_float((127 - 13 + ex) << 23);
+            if (top >= 0x7f800000u) st.rs[r] = __int_as_float(0x7fffffff);  // no softmax of this row
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 uint32_t hi[4], lo[4];

@@ -551,9 +551,11 @@ int kv_read(int fmt, int type, const void* cache, int64_t n_pages, int page_toke
  * end.  The result
  * is the same, bit for bit, on every call with the same arguments on one
  * kind of device; what lies at masked places of the cache never reaches it.
- * Infinities among an f16 cache's values give what the formula has, wherever
- * they stand; a weight below 2^-126 of the row's largest counts as zero, and
- * zero times infinity is NaN.
+ * Infinities in an f16 cache give what the formula has, wherever they stand: a
+ * key of which the score is minus infinity has no weight.  A weight below
+ * 2^-126 of the row's largest counts as zero, an element of q below 2^-38 of
+ * the row's largest too, and zero times infinity is NaN.  A row of q that holds
+ * a NaN or an infinity is NaN, and so is its lse, where it sees any position.
  *   q          rows of head_dim values, row (r, h) at r * q_row + h * q_head
  *   out        written, row (r, h) at r * o_row + h * o_head; must not overlap q
  *   lse        fp32 [batch * rows][n_heads] (written), or NULL

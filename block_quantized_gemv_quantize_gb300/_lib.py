@@ -134,11 +134,19 @@ def _check(name: str, status: int) -> None:
         raise QgemvError(name, status)
 
 
-_raw_stream = torch._C._cuda_getCurrentRawStream  # (a Stream object for it takes 2 us)
+# (a Stream object takes 2 us; a torch without CUDA has neither)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device_now = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _stream(t: torch.Tensor) -> int:
-    return _raw_stream(t.get_device())
+    """The current stream of t's device, which must be the current device: the
+    library launches there."""
+    index = t.get_device()
+    if index != _device_now():
+        raise ValueError(f"the tensors are on cuda:{index}, which is not the current device "
+                         f"(with torch.cuda.device({index}): ...)")
+    return _raw_stream(index)
 
 
 def _dev(t: torch.Tensor, what: str) -> int:
@@ -541,8 +549,9 @@ def kv_write(cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slots: torch
         raise ValueError(f"{slots.numel()} slots for {n} tokens")
     if n == 0:
         return
-    _check("kv_write", LIB.kv_write(KV_FORMATS[fmt], _type(k, "k"), kp, k0, k1, vp, v0, v1, sp, cp, pages, page_tokens,
-                                    n, heads, dim, _stream(k)))
+    with torch.cuda.device(k.device):
+        _check("kv_write", LIB.kv_write(KV_FORMATS[fmt], _type(k, "k"), kp, k0, k1, vp, v0, v1, sp, cp, pages,
+                                        page_tokens, n, heads, dim, _stream(k)))
 
 
 def kv_read(cache: torch.Tensor, slots: torch.Tensor, fmt: str, page_tokens: int, n_kv_heads: int, head_dim: int,
@@ -568,8 +577,9 @@ def kv_read(cache: torch.Tensor, slots: torch.Tensor, fmt: str, page_tokens: int
     cp, pages = _kv_cache(cache, fmt, page_tokens, n_kv_heads, head_dim, k)
     sp = _kv_slots(slots, k)
     if n:
-        _check("kv_read", LIB.kv_read(KV_FORMATS[fmt], _type(k, "k"), cp, pages, page_tokens, sp, kp, k0, k1, vp, v0,
-                                      v1, n, n_kv_heads, head_dim, _stream(k)))
+        with torch.cuda.device(k.device):
+            _check("kv_read", LIB.kv_read(KV_FORMATS[fmt], _type(k, "k"), cp, pages, page_tokens, sp, kp, k0, k1, vp,
+                                          v0, v1, n, n_kv_heads, head_dim, _stream(k)))
     return k, v
 
 
@@ -620,19 +630,20 @@ def attn_paged(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, k
         raise ValueError(f"lse must be contiguous float32 [{n}, {heads}] on q's device")
     if batch == 0:
         return out
-    if ws is None:
-        need = attn_paged_workspace_bytes(q.dtype, rows, heads, n_kv_heads, dim)
-        # (one that a capture allocates belongs to its graph)
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=device) \
-            if torch.cuda.is_current_stream_capturing() else workspace(device, need, key="attn")
-    elif ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous():
+    if ws is not None and (ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous()):
         raise ValueError("ws must be contiguous uint8 on q's device")
-    with _attn_lock:  # no other thread's kernels between this call's two, which share the stream's workspace
-        done = LIB.attn_paged(
-            KV_FORMATS[fmt], _type(q, "q"), qp, q0, q1, cp, pages, page_tokens, page_table.data_ptr(),
-            ld[0] if batch > 1 else max(ld[0], max_pages), max_pages, kv_lens.data_ptr(), op, o0, o1,
-            None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), batch, rows, heads, n_kv_heads, dim,
-            dim ** -0.5 if scale is None else scale, window, _stream(q))
+    with torch.cuda.device(device):
+        if ws is None:
+            need = attn_paged_workspace_bytes(q.dtype, rows, heads, n_kv_heads, dim)
+            # (one that a capture allocates belongs to its graph)
+            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=device) \
+                if torch.cuda.is_current_stream_capturing() else workspace(device, need, key="attn")
+        with _attn_lock:  # no other thread's kernels between this call's two, which share the stream's workspace
+            done = LIB.attn_paged(
+                KV_FORMATS[fmt], _type(q, "q"), qp, q0, q1, cp, pages, page_tokens, page_table.data_ptr(),
+                ld[0] if batch > 1 else max(ld[0], max_pages), max_pages, kv_lens.data_ptr(), op, o0, o1,
+                None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(), batch, rows, heads, n_kv_heads,
+                dim, dim ** -0.5 if scale is None else scale, window, _stream(q))
     _check("attn_paged", done)
     return out
 

@@ -11,6 +11,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGraphsC10Utils.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -110,6 +111,7 @@ PyObject* kv_write(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     const int n = (int)k->size(0), heads = (int)k->size(1), dim = (int)k->size(2);
     int64_t pages;
     if (!cache_ok(*cache, device, page_bytes_entry(fmt, page, heads, dim), pages)) Py_RETURN_NONE;
+    const c10::cuda::CUDAGuard guard(device);
     void* stream = c10::cuda::getCurrentCUDAStream(device.index()).stream();
     return PyLong_FromLong(unlocked([&] {
         return kv_write_entry(fmt, type, k->data_ptr(), k->stride(0), k->stride(1), v->data_ptr(), v->stride(0),
@@ -131,6 +133,7 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     if (bad || !slots_ok(*slots, device) || slots->size(0) == 0 || slots->size(0) > INT32_MAX ||
         !cache_ok(*cache, device, page_bytes_entry(fmt, page, heads, dim), pages))
         Py_RETURN_NONE;
+    const c10::cuda::CUDAGuard guard(device);
     const int64_t n = slots->size(0), sizes[3] = {n, heads, dim};
     at::Tensor k, v;
     if (a[7] == Py_None && a[8] == Py_None) {
@@ -207,6 +210,7 @@ PyObject* attn_paged(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     }
     const size_t need = workspace_bytes_entry(type, rows, heads, kv_heads, dim);
     if (need == 0) Py_RETURN_NONE;
+    const c10::cuda::CUDAGuard guard(device);  // (the capture query below asks the current device's stream)
     void* stream = c10::cuda::getCurrentCUDAStream(device.index()).stream();
     at::Tensor out, ws;
     if (a[10] == Py_None) {

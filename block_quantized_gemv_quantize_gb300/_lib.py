@@ -15,6 +15,8 @@ import functools
 import importlib.util
 import os
 import threading
+import types
+import warnings
 
 import torch
 
@@ -109,16 +111,18 @@ LIB = _load()
 
 
 def _load_calls():
-    """csrc/binding.cpp, bound to the loaded library."""
-    if not os.path.exists(_build.CALLS):
-        raise ImportError(f"{_build.CALLS} is missing: build the library first "
-                          f"(python -m block_quantized_gemv_quantize_gb300.build)")
-    spec = importlib.util.spec_from_file_location("qgemv_calls", _build.CALLS)
-    calls = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(calls)
-    calls.init(*(ctypes.cast(getattr(LIB, name), ctypes.c_void_p).value for name in (
-        "kv_write", "kv_read", "attn_paged", "kv_page_bytes", "attn_paged_workspace_bytes")))
-    return calls
+    """csrc/binding.cpp, bound to the loaded library; where it is not there, a
+    stand-in that leaves every call to ctypes."""
+    try:
+        spec = importlib.util.spec_from_file_location("qgemv_calls", _build.CALLS)
+        calls = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(calls)
+        calls.init(*(ctypes.cast(getattr(LIB, name), ctypes.c_void_p).value for name in (
+            "kv_write", "kv_read", "attn_paged", "kv_page_bytes", "attn_paged_workspace_bytes")))
+        return calls
+    except (ImportError, OSError) as e:
+        warnings.warn(f"the paged cache's calls go through ctypes, twice as long on the host: {e}", RuntimeWarning)
+        return types.SimpleNamespace(**{name: lambda *args: None for name in ("kv_write", "kv_read", "attn_paged")})
 
 
 _CALLS = _load_calls()

@@ -111,8 +111,8 @@ LIB = _load()
 
 
 def _load_calls():
-    """csrc/binding.cpp, bound to the loaded library; where it is not there, a
-    stand-in that leaves every call to ctypes."""
+    """csrc/binding.cpp, bound to the loaded library; where there is none for this
+    torch and Python, a stand-in that leaves every call to ctypes."""
     try:
         spec = importlib.util.spec_from_file_location("qgemv_calls", _build.CALLS)
         calls = importlib.util.module_from_spec(spec)

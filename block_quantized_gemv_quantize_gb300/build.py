@@ -15,17 +15,18 @@ binding loads it when the environment has ``QGEMV_BOUNDS_CHECK=1``.
 """
 from __future__ import annotations
 
+import importlib.metadata
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libqgemv.so")
-CALLS = os.path.join(BUILD, "qgemv_calls.so")  # csrc/binding.cpp
 BUILD_DEBUG = os.path.join(BUILD, "debug")
 LIB_DEBUG = os.path.join(BUILD_DEBUG, "libqgemv.so")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
@@ -59,22 +60,42 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(f) <= t for f in _deps())
 
 
+def calls_path() -> str:
+    """The module of csrc/binding.cpp for the torch (its C++ interface) and the
+    Python that run."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        version = "none"
+    return os.path.join(BUILD, f"qgemv_calls.{sysconfig.get_config_var('SOABI')}.torch-{version}.so")
+
+
+CALLS = calls_path()
+
+
+def calls_deps() -> list[str]:
+    return [os.path.join(CSRC, "binding.cpp"), os.path.join(INCLUDE, "qgemv.h"), os.path.abspath(__file__)]
+
+
+def calls_up_to_date(path: str) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(f) <= os.path.getmtime(path) for f in calls_deps())
+
+
 def build_calls(force: bool = False) -> str:
     """Compile csrc/binding.cpp against the torch that is installed (host code
     only); returns its path."""
-    src = os.path.join(CSRC, "binding.cpp")
-    if not force and os.path.exists(CALLS) and os.path.getmtime(CALLS) >= os.path.getmtime(src):
+    if not force and calls_up_to_date(CALLS):
         return CALLS
-    import sysconfig
-
     import torch
 
+    src = os.path.join(CSRC, "binding.cpp")
     os.makedirs(BUILD, exist_ok=True)
     root = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(_nvcc()))
     tmp = CALLS + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", src, "-o", tmp,
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", sysconfig.get_paths()["include"],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"],
            "-isystem", os.path.join(root, "include"),
            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(cuda, "include"), "-L", os.path.join(root, "lib"),

@@ -19,23 +19,16 @@
 #include <map>
 #include <utility>
 
+#include "qgemv.h"
+
 namespace {
 
-using KvWrite = int (*)(int, int, const void*, int64_t, int64_t, const void*, int64_t, int64_t, const int64_t*, void*,
-                        int64_t, int, int, int, int, void*);
-using KvRead = int (*)(int, int, const void*, int64_t, int, const int64_t*, void*, int64_t, int64_t, void*, int64_t,
-                       int64_t, int, int, int, void*);
-using Attn = int (*)(int, int, const void*, int64_t, int64_t, const void*, int64_t, int, const int32_t*, int64_t, int,
-                     const int32_t*, void*, int64_t, int64_t, float*, void*, size_t, int, int, int, int, int, float,
-                     int, void*);
-using PageBytes = size_t (*)(int, int, int, int);
-using WorkspaceBytes = size_t (*)(int, int, int, int, int);
-
-KvWrite kv_write_entry;
-KvRead kv_read_entry;
-Attn attn_entry;
-PageBytes page_bytes_entry;
-WorkspaceBytes workspace_bytes_entry;
+// the library's entry points, by the addresses that init() gets
+decltype(&::kv_write) kv_write_entry;
+decltype(&::kv_read) kv_read_entry;
+decltype(&::attn_paged) attn_entry;
+decltype(&::kv_page_bytes) page_bytes_entry;
+decltype(&::attn_paged_workspace_bytes) workspace_bytes_entry;
 
 int type_code(const at::Tensor& t)
 {
@@ -96,7 +89,7 @@ int unlocked(F f)
 }
 
 // kv_write(cache, k, v, slots, fmt, page_tokens) -> status
-PyObject* kv_write(PyObject*, PyObject* const* a, Py_ssize_t n_args)
+PyObject* call_kv_write(PyObject*, PyObject* const* a, Py_ssize_t n_args)
 {
     const at::Tensor *cache, *k, *v, *slots;
     if (n_args != 6 || !(cache = tensor(a[0])) || !(k = tensor(a[1])) || !(v = tensor(a[2])) || !(slots = tensor(a[3])))
@@ -121,7 +114,7 @@ PyObject* kv_write(PyObject*, PyObject* const* a, Py_ssize_t n_args)
 }
 
 // kv_read(cache, slots, fmt, page_tokens, n_kv_heads, head_dim, type, k or None, v or None) -> status or (k, v)
-PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n_args)
+PyObject* call_kv_read(PyObject*, PyObject* const* a, Py_ssize_t n_args)
 {
     const at::Tensor *cache, *slots;
     if (n_args != 9 || !(cache = tensor(a[0])) || !(slots = tensor(a[1])) || !cache->is_cuda()) Py_RETURN_NONE;
@@ -176,7 +169,7 @@ at::Tensor& workspace(c10::Device device, void* stream, size_t bytes)
 
 // attn_paged(q, cache, page_table, kv_lens, fmt, page_tokens, n_kv_heads, rows, scale or None, window, out or None,
 //            lse or None, ws or None) -> status or out
-PyObject* attn_paged(PyObject*, PyObject* const* a, Py_ssize_t n_args)
+PyObject* call_attn_paged(PyObject*, PyObject* const* a, Py_ssize_t n_args)
 {
     const at::Tensor *q, *cache, *table, *lens, *lse = nullptr;
     if (n_args != 13 || !(q = tensor(a[0])) || !(cache = tensor(a[1])) || !(table = tensor(a[2])) ||
@@ -270,19 +263,19 @@ PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n_args)
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a null address");
             return nullptr;
         }
-    kv_write_entry = reinterpret_cast<KvWrite>(p[0]);
-    kv_read_entry = reinterpret_cast<KvRead>(p[1]);
-    attn_entry = reinterpret_cast<Attn>(p[2]);
-    page_bytes_entry = reinterpret_cast<PageBytes>(p[3]);
-    workspace_bytes_entry = reinterpret_cast<WorkspaceBytes>(p[4]);
+    kv_write_entry = reinterpret_cast<decltype(kv_write_entry)>(p[0]);
+    kv_read_entry = reinterpret_cast<decltype(kv_read_entry)>(p[1]);
+    attn_entry = reinterpret_cast<decltype(attn_entry)>(p[2]);
+    page_bytes_entry = reinterpret_cast<decltype(page_bytes_entry)>(p[3]);
+    workspace_bytes_entry = reinterpret_cast<decltype(workspace_bytes_entry)>(p[4]);
     Py_RETURN_NONE;
 }
 
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f))
 PyMethodDef methods[] = {{"init", FAST(init), METH_FASTCALL, nullptr},
-                         {"kv_write", FAST(guarded<kv_write>), METH_FASTCALL, nullptr},
-                         {"kv_read", FAST(guarded<kv_read>), METH_FASTCALL, nullptr},
-                         {"attn_paged", FAST(guarded<attn_paged>), METH_FASTCALL, nullptr},
+                         {"kv_write", FAST(guarded<call_kv_write>), METH_FASTCALL, nullptr},
+                         {"kv_read", FAST(guarded<call_kv_read>), METH_FASTCALL, nullptr},
+                         {"attn_paged", FAST(guarded<call_attn_paged>), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "qgemv_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

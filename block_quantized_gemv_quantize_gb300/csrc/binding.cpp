@@ -17,6 +17,7 @@
 
 #include <cmath>
 #include <map>
+#include <mutex>
 #include <utility>
 
 #include "qgemv.h"
@@ -77,15 +78,15 @@ at::Tensor empty(c10::IntArrayRef sizes, at::ScalarType type, c10::Device device
     return at::empty(sizes, at::TensorOptions().dtype(type).device(device));
 }
 
-// Runs f without the interpreter's lock.
+// Runs f without the interpreter's lock, which comes back if f throws, too.
 template <typename F>
 int unlocked(F f)
 {
-    int status;
-    Py_BEGIN_ALLOW_THREADS;
-    status = f();
-    Py_END_ALLOW_THREADS;
-    return status;
+    struct Released {
+        PyThreadState* state = PyEval_SaveThread();
+        ~Released() { PyEval_RestoreThread(state); }
+    } released;
+    return f();
 }
 
 // kv_write(cache, k, v, slots, fmt, page_tokens) -> status
@@ -157,14 +158,20 @@ PyObject* call_kv_read(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     return both;
 }
 
-// One workspace for each (device, stream); never freed, as the program may end
-// after CUDA has.
-at::Tensor& workspace(c10::Device device, void* stream, size_t bytes)
+// One workspace for each (device, stream), never freed, as the program may end
+// after CUDA has.  A call's two kernels share it: its lock keeps another thread's
+// from coming between them.
+struct Workspace {
+    std::mutex lock;
+    at::Tensor memory;
+};
+
+Workspace& workspace(c10::Device device, void* stream)
 {
-    static auto* all = new std::map<std::pair<int, void*>, at::Tensor>;
-    at::Tensor& ws = (*all)[{device.index(), stream}];
-    if (!ws.defined() || (size_t)ws.numel() < bytes) ws = empty({(int64_t)bytes}, at::kByte, device);
-    return ws;
+    static auto* all = new std::map<std::pair<int, void*>, Workspace>;
+    static auto* lock = new std::mutex;
+    const std::lock_guard<std::mutex> held(*lock);
+    return (*all)[{device.index(), stream}];
 }
 
 // attn_paged(q, cache, page_table, kv_lens, fmt, page_tokens, n_kv_heads, rows, scale or None, window, out or None,
@@ -206,6 +213,7 @@ PyObject* call_attn_paged(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     const c10::cuda::CUDAGuard guard(device);  // (the capture query below asks the current device's stream)
     void* stream = c10::cuda::getCurrentCUDAStream(device.index()).stream();
     at::Tensor out, ws;
+    Workspace* shared = nullptr;
     if (a[10] == Py_None) {
         out = empty(q->sizes(), q->scalar_type(), device);
     } else {
@@ -221,17 +229,23 @@ PyObject* call_attn_paged(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     } else if (c10::cuda::currentStreamCaptureStatusMayInitCtx() != c10::cuda::CaptureStatus::None) {
         ws = empty({(int64_t)need}, at::kByte, device);  // its graph's own
     } else {
-        ws = workspace(device, stream, need);
+        shared = &workspace(device, stream);
     }
     const int64_t ld = batch > 1 ? table->stride(0) : std::max(table->stride(0), max_pages);
-    // (With the interpreter's lock: the call's two kernels share the stream's
-    // workspace, and another thread's must not come between them.)
-    const int status =
-        attn_entry(fmt, type, q->data_ptr(), q->stride(0), q->stride(1), cache->data_ptr(), pages, page,
-                   static_cast<const int32_t*>(table->data_ptr()), ld, (int)max_pages,
-                   static_cast<const int32_t*>(lens->data_ptr()), out.data_ptr(), out.stride(0), out.stride(1),
-                   lse ? static_cast<float*>(lse->data_ptr()) : nullptr, ws.data_ptr(), (size_t)ws.numel(), (int)batch,
-                   rows, heads, kv_heads, dim, (float)scale, window, stream);
+    const int status = unlocked([&] {
+        std::unique_lock<std::mutex> held;
+        if (shared) {
+            held = std::unique_lock<std::mutex>(shared->lock);
+            if (!shared->memory.defined() || (size_t)shared->memory.numel() < need)
+                shared->memory = empty({(int64_t)need}, at::kByte, device);
+            ws = shared->memory;
+        }
+        return attn_entry(fmt, type, q->data_ptr(), q->stride(0), q->stride(1), cache->data_ptr(), pages, page,
+                          static_cast<const int32_t*>(table->data_ptr()), ld, (int)max_pages,
+                          static_cast<const int32_t*>(lens->data_ptr()), out.data_ptr(), out.stride(0), out.stride(1),
+                          lse ? static_cast<float*>(lse->data_ptr()) : nullptr, ws.data_ptr(), (size_t)ws.numel(),
+                          (int)batch, rows, heads, kv_heads, dim, (float)scale, window, stream);
+    });
     if (status) return PyLong_FromLong(status);
     if (a[10] != Py_None) return Py_NewRef(a[10]);
     return THPVariable_Wrap(std::move(out));

@@ -479,6 +479,13 @@ KV_FORMATS = {"f16": 0, "q8_0": 1, "q4_0": 2}
 _TYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 
 
+def _fits(bits: int, **numbers: int) -> None:
+    """ctypes would cut a number that a C integer of so many bits does not hold."""
+    for name, n in numbers.items():
+        if not -(1 << bits - 1) <= n < 1 << bits - 1:
+            raise ValueError(f"{name} = {n} does not fit {bits} bits")
+
+
 def _kv_format(fmt: str) -> int:
     if fmt not in KV_FORMATS:
         raise ValueError(f"fmt must be one of {', '.join(KV_FORMATS)}, not {fmt!r}")
@@ -527,12 +534,15 @@ def _kv_slots(slots: torch.Tensor, near: torch.Tensor) -> int:
 @functools.lru_cache(maxsize=1024)
 def kv_page_bytes(fmt: str, page_tokens: int, n_kv_heads: int, head_dim: int) -> int:
     """Bytes of one page of the cache; 0 for sizes that the calls refuse."""
+    _fits(32, page_tokens=page_tokens, n_kv_heads=n_kv_heads, head_dim=head_dim)
     return LIB.kv_page_bytes(_kv_format(fmt), page_tokens, n_kv_heads, head_dim)
 
 
 def kv_tile_offset(fmt: str, n_pages: int, page_tokens: int, n_kv_heads: int, head_dim: int, slot: int,
                    head: int) -> int:
     """Byte offset in the cache of the 16-token tile that holds a slot of a kv head; -1 outside the cache."""
+    _fits(64, n_pages=n_pages, slot=slot)
+    _fits(32, page_tokens=page_tokens, n_kv_heads=n_kv_heads, head_dim=head_dim, head=head)
     return LIB.kv_tile_offset(_kv_format(fmt), n_pages, page_tokens, n_kv_heads, head_dim, slot, head)
 
 
@@ -551,6 +561,7 @@ def kv_write(cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slots: torch
     sp = _kv_slots(slots, k)
     if slots.shape[0] != n:
         raise ValueError(f"{slots.numel()} slots for {n} tokens")
+    _fits(32, tokens=n)
     if n == 0:
         return
     with torch.cuda.device(k.device):
@@ -580,6 +591,7 @@ def kv_read(cache: torch.Tensor, slots: torch.Tensor, fmt: str, page_tokens: int
     vp, v0, v1 = _rows(v, "v", like=k)
     cp, pages = _kv_cache(cache, fmt, page_tokens, n_kv_heads, head_dim, k)
     sp = _kv_slots(slots, k)
+    _fits(32, tokens=n)
     if n:
         with torch.cuda.device(k.device):
             _check("kv_read", LIB.kv_read(KV_FORMATS[fmt], _type(k, "k"), cp, pages, page_tokens, sp, kp, k0, k1, vp,
@@ -591,6 +603,7 @@ def kv_read(cache: torch.Tensor, slots: torch.Tensor, fmt: str, page_tokens: int
 def attn_paged_workspace_bytes(dtype: torch.dtype, rows: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
     if dtype not in _TYPES:
         raise ValueError(f"dtype must be float32, float16 or bfloat16, not {dtype}")
+    _fits(32, rows=rows, n_heads=n_heads, n_kv_heads=n_kv_heads, head_dim=head_dim)
     return LIB.attn_paged_workspace_bytes(_TYPES[dtype], rows, n_heads, n_kv_heads, head_dim)
 
 
@@ -626,6 +639,8 @@ def attn_paged(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, k
     if kv_lens.dtype != torch.int32 or kv_lens.dim() != 1 or not kv_lens.is_contiguous() or kv_lens.device != device:
         raise ValueError("kv_lens must be contiguous int32 [batch] on q's device")
     batch, max_pages = page_table.shape
+    window = min(window, (1 << 31) - 1)  # (no sequence is longer)
+    _fits(32, rows=rows, window=window, batch=batch, pages=max_pages)
     if rows < 1 or n != batch * rows or kv_lens.shape[0] != batch:
         raise ValueError(f"q has {n} rows, kv_lens {kv_lens.shape[0]} and page_table {batch}: one length and one table "
                          f"row for each {rows} rows of q")

@@ -42,8 +42,9 @@ class Tensor:
 
 @pytest.fixture
 def machine(monkeypatch):
-    """Two devices, the first of them current; `calls` gets (name, device, stream) of each call of the library."""
-    state = types.SimpleNamespace(now=0, calls=[])
+    """Two devices, the first of them current; `calls` gets (name, device, stream) of each call of the library,
+    `args` its arguments."""
+    state = types.SimpleNamespace(now=0, calls=[], args=[])
 
     @contextlib.contextmanager
     def device(d):
@@ -54,6 +55,7 @@ def machine(monkeypatch):
     def entry(name):
         def call(*args):
             state.calls.append((name, state.now, args[-1]))
+            state.args.append(args)
             return 0
         return call
 

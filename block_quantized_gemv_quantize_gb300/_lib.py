@@ -779,6 +779,6 @@ def qgemv_debug_plant_bad_store() -> int:
 
 
 def qgemv_debug_drop_next_copy() -> int:
-    """Test only: the next small-M tensor-core Q4_0 launch skips one copy, so
-    one warp's bounded wait runs out (see include/qgemv.h)."""
+    """Test only: the next small-M tensor-core Q4_0 or attn_paged launch skips
+    one copy, so one warp's bounded wait runs out (see include/qgemv.h)."""
     return int(LIB.qgemv_debug_drop_next_copy())

@@ -119,6 +119,7 @@ struct AttnPlan {
     int stages;          // pairs of tiles a ring holds
     int cum[ATTN_WARPS + 1];  // shares of a CTA's part of the line: split s has cum[s] .. cum[s + 1] of cum[ws]
     uint32_t off_q, off_bar, bytes;  // shared memory
+    int drop_copy;       // test only: no copy for the stage with the first tile of the line
 };
 
 // How the line is cut: a CTA has `chunk` units of it, split s of the CTA those from
@@ -984,6 +985,7 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
             after();
         };
         if (more) settle();
+        const int dropped = p.drop_copy && more && w.line == 0 && w.ta == 0 ? 0 : -1;
         int idle = 0;
         while (__any_sync(0xffffffffu, more)) {
             const bool go = more && (round == 0 || mbar_test_wait(&em[slot], (round - 1) & 1));
@@ -1001,8 +1003,8 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
                             QG_OK(qg_in(off, apart ? Sh::TILE : (1 + two) * Sh::TILE, a.L.bytes()) &&
                                       qg_in(off2, Sh::TILE, a.L.bytes()), status, 731);
             bad[slot] = !ok;
-            mbar_arrive_expect_tx(&fl[slot], ok ? (1 + two) * Sh::TILE : 0u);
-            if (ok) {
+            if (issued != dropped) mbar_arrive_expect_tx(&fl[slot], ok ? (1 + two) * Sh::TILE : 0u);
+            if (ok && issued != dropped) {
                 uint8_t* to = ring + (size_t)slot * STAGE;
                 bulk_g2s(to, a.cache + off, two && !apart ? 2 * Sh::TILE : Sh::TILE, &fl[slot], policy);
                 if (apart) bulk_g2s(to + Sh::TILE, a.cache + off2, Sh::TILE, &fl[slot], policy);
@@ -1028,10 +1030,10 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
                 after();
             }
         }
-        if (more) {  // gave up: its own copies in flight
-            for (int q = issued > S ? issued - S : 0; q < issued; ++q) mbar_wait_bounded(&fl[q % S], (q / S) & 1);
-            atomicAdd_system(status, 1u);
-        }
+        // No copy outlives the CTA, whose warps may have given up waiting for theirs.
+        for (int q = issued > S ? issued - S : 0; q < issued; ++q)
+            if (q != dropped) mbar_wait_bounded(&fl[q % S], (q / S) & 1);
+        if (more) atomicAdd_system(status, 1u);  // gave up
         return;
     }
 
@@ -1383,7 +1385,7 @@ int launch_attn(const AttnArgs& a, cudaStream_t s)
     if (di.sms <= 0) return QGEMV_CUDA_ERROR;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return QGEMV_CUDA_ERROR;
-    const AttnPlan p = attn_plan<FMT, NB, MODE>(di, a.rows * a.group);
+    AttnPlan p = attn_plan<FMT, NB, MODE>(di, a.rows * a.group);
     if (p.stages < 2) return QGEMV_UNSUPPORTED_SHAPE;
     auto kern = attn_split_kernel<FMT, NB, MODE, T>;
     static std::once_flag once[64];
@@ -1395,6 +1397,7 @@ int launch_attn(const AttnArgs& a, cudaStream_t s)
         if (!ok[dev]) cudaGetLastError();
     });
     if (!ok[dev]) return QGEMV_CUDA_ERROR;
+    p.drop_copy = take_drop_request();
     if (launch_pdl(kern, dim3(p.splits / p.ws), dim3((p.ws * p.wr + 1) * 32), p.bytes, s, a, p, wait_timeout_counter()) !=
         cudaSuccess)
         return QGEMV_CUDA_ERROR;

@@ -47,7 +47,7 @@ unsigned int* wait_timeout_counter();
 // the counter is a device word, which the host cannot read without a copy).
 bool wait_timeouts_pending();
 // A test-only request (qgemv_debug_drop_next_copy) taken by the next launch of
-// the small-M Q4_0 kernel: 1 once, then 0.
+// the small-M Q4_0 kernel or of the attention over the paged cache: 1 once, then 0.
 int take_drop_request();
 // Debug build only (test hook): whether the next ring-kernel launch should
 // move one output store out of its extent, for its bounds check to catch.

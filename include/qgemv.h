@@ -600,8 +600,10 @@ int qgemv_take_wait_timeouts(unsigned int* count);
  * qgemv_q4_0_pair, 5 <= M <= 8, on its default path) issues no copy for the
  * first job of CTA 0, so the warp holding that job finds its bounded wait
  * running out (about a second); it counts the timeout and stops, with no copy
- * in flight for it, and the rest of the launch completes.  Process-wide; returns the previous
- * request (0 or 1).  (Not from the pages.) */
+ * in flight for it, and the rest of the launch completes.  The next attn_paged
+ * takes the request too: the copy of the first tile of its first sequence's
+ * first kv head is left out, whose rows come out NaN.  Process-wide; returns the
+ * previous request (0 or 1).  (Not from the pages.) */
 int qgemv_debug_drop_next_copy(void);
 
 /* qgemv_debug_fail_fused - for tests of the fail-closed fallback only: the

@@ -143,7 +143,6 @@ __device__ __forceinline__ float kv_top_pairs(const KvRaw<__nv_bfloat16>& x)
         __hmax2_nan(__hmax2_nan(__habs2(p[0]), __habs2(p[1])), __hmax2_nan(__habs2(p[2]), __habs2(p[3])));
     return max_abs(__low2float(m), __high2float(m));
 }
-__device__ __forceinline__ float kv_top_pairs(const KvRaw<float>&) { return 0.0f; }  // (not called)
 
 // Four blocks' tops over the quad: lane sub gets that of block sub.
 template <bool KEY>

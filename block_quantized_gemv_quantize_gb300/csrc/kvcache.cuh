@@ -90,26 +90,6 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { retu
 
 // N consecutive values; `wide`: p is aligned to N values (or to 16 bytes).
 template <int N, typename T>
-__device__ __forceinline__ void load_values(const T* p, bool wide, float (&v)[N])
-{
-    constexpr int BYTES = N * (int)sizeof(T), VEC = BYTES < 16 ? BYTES : 16, PER = VEC / (int)sizeof(T);
-    static_assert(VEC == 8 || VEC == 16, "two or four words at a time");
-    if (wide) {
-#pragma unroll
-        for (int i = 0; i < N / PER; ++i) {
-            alignas(16) T t[PER];
-            if constexpr (VEC == 16) *reinterpret_cast<uint4*>(t) = reinterpret_cast<const uint4*>(p)[i];
-            else *reinterpret_cast<uint2*>(t) = reinterpret_cast<const uint2*>(p)[i];
-#pragma unroll
-            for (int k = 0; k < PER; ++k) v[i * PER + k] = to_f32(t[k]);
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = to_f32(p[k]);
-    }
-}
-
-template <int N, typename T>
 __device__ __forceinline__ void store_values(T* p, bool wide, const float (&v)[N])
 {
     constexpr int BYTES = N * (int)sizeof(T), VEC = BYTES < 16 ? BYTES : 16, PER = VEC / (int)sizeof(T);

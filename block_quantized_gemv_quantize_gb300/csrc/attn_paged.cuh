@@ -77,12 +77,21 @@ enum AttnMode { ATTN_PAIR = 1, ATTN_TWO = 2 };
 inline int attn_mode(int rows) { return rows > 8 ? ATTN_TWO : ATTN_PAIR; }
 
 // Shares of a split whose warps share their schedulers with another's, and of one
-// whose warps do not.  The latter is faster where arithmetic bounds the kernel: with
-// 10 instead of 8, two of 131071 tokens in q4_0 take 98 us, not 101, 46 ragged
-// sequences 83, not 86, width 6 over 17391 tokens 30, not 32; where memory does it
-// is not: D = 64 in q8_0 takes 63 us, not 58, an f16 cache 45.6, not 44.3.
+// whose warps do not.  The latter is faster where arithmetic bounds the kernel, by the
+// rows a kv head and, for few of them, the format and D; where memory does it is not.
+// 8 and 10, 8 kv heads, 8 sequences of 16384 * 128 / D tokens (from 30 rows on half):
+//     rows       1              16             30
+//     q8_0 D=64  61.6, 67.2 us  83.2, 80.8     97.4, 90.4
+//     q8_0 D=128 54.4, 52.8     74.9, 73.0     86.4, 80.4
+//     q4_0 D=64  64.1, 67.6     84.4, 82.6     99.5, 92.3
+//     f16 D=64   85.9, 91.5     88.4, 93.4     77.6, 74.5
+//     f16 D=128  87.8, 89.9     89.1, 87.6     65.3, 61.4
+// (D = 96 and 256 like 128; from 48 rows on no split is alone, or all are.)
 constexpr int ATTN_SHARE = 8;
-constexpr int attn_share_alone(int fmt, int nb) { return fmt != QGEMV_KV_F16 && nb > 2 ? 10 : ATTN_SHARE; }
+inline int attn_share_alone(int fmt, int nb, int rows)
+{
+    return rows > (fmt == QGEMV_KV_F16 ? 16 : (nb > 2 ? 0 : 8)) ? 10 : ATTN_SHARE;
+}
 
 // Warps that compute (one more copies): eight warps leave a thread 255 registers.
 // Eleven (168 registers, q in shared memory) measured 1 to 4 % faster where the
@@ -1373,7 +1382,7 @@ AttnPlan attn_plan(const DeviceInfo& di, int rows)
     for (int s = 0; s < p.ws; ++s) {
         bool alone = true;
         for (int w = s * p.wr; w < (s + 1) * p.wr; ++w) alone = alone && on[w % 4] == 1;
-        p.cum[s + 1] = p.cum[s] + (alone ? attn_share_alone(FMT, NB) : ATTN_SHARE);
+        p.cum[s + 1] = p.cum[s] + (alone ? attn_share_alone(FMT, NB, rows) : ATTN_SHARE);
     }
     return p;
 }

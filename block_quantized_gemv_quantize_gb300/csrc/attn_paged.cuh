@@ -199,7 +199,8 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity)
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 bits_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
 
-// Codes to fp16 without a conversion: 0x6400 | n is the fp16 number 1024 + n.
+// Codes to fp16 without a conversion, by the well-known technique of an integer in
+// the mantissa of a power of two: 0x6400 | n is the fp16 number 1024 + n.
 // The 0x64 bytes (`magic`) are an argument of the kernel, which the compiler does
 // not see through: an instruction has room for one constant, so with two of them
 // it would spend a second instruction on every word.
@@ -621,7 +622,10 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) sum += c16[u][j][c];
+                for (int c = 0; c < 4; ++c) {
+                    const int p = x.pos + u * KV_TILE + tile_token(t, 2 * j + (c & 1));
+                    if (!EDGE || (p >= x.first && p < x.last)) sum += c16[u][j][c];  // (the others may be anything)
+                }
         if (__any_sync(0xffffffffu, !isfinite(sum))) {
 #pragma unroll
             for (int u = 0; u < NT; ++u) {

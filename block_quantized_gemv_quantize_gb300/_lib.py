@@ -10,6 +10,7 @@ library is missing, importing this module raises: build it first
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import importlib.util
@@ -153,6 +154,14 @@ def _stream(t: torch.Tensor) -> int:
     return _raw_stream(index)
 
 
+_HERE = contextlib.nullcontext()
+
+
+def _on(device: torch.device):
+    """That device current, for a with statement (torch's own takes 5 us even where it is)."""
+    return _HERE if device.index == _device_now() else torch.cuda.device(device)
+
+
 def _dev(t: torch.Tensor, what: str) -> int:
     if not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
@@ -192,8 +201,9 @@ _ws_cache: dict[tuple, torch.Tensor] = {}
 
 
 def workspace(device: torch.device, nbytes: int, key: str = "top1") -> torch.Tensor:
-    """A zero-filled device workspace, one per (device, stream, key); the
-    kernels leave it zero-filled after every call."""
+    """A device workspace, one per (device, stream, key), zero-filled when it is
+    made.  The kernels of every key but "attn" leave it zero-filled after every
+    call; attn_paged's, which may find anything in theirs, leave partial results."""
     index = torch.device(device).index
     if index is None:
         index = torch.cuda.current_device()
@@ -564,7 +574,7 @@ def kv_write(cache: torch.Tensor, k: torch.Tensor, v: torch.Tensor, slots: torch
     _fits(32, tokens=n)
     if n == 0:
         return
-    with torch.cuda.device(k.device):
+    with _on(k.device):
         _check("kv_write", LIB.kv_write(KV_FORMATS[fmt], _type(k, "k"), kp, k0, k1, vp, v0, v1, sp, cp, pages,
                                         page_tokens, n, heads, dim, _stream(k)))
 
@@ -593,7 +603,7 @@ def kv_read(cache: torch.Tensor, slots: torch.Tensor, fmt: str, page_tokens: int
     sp = _kv_slots(slots, k)
     _fits(32, tokens=n)
     if n:
-        with torch.cuda.device(k.device):
+        with _on(k.device):
             _check("kv_read", LIB.kv_read(KV_FORMATS[fmt], _type(k, "k"), cp, pages, page_tokens, sp, kp, k0, k1, vp,
                                           v0, v1, n, n_kv_heads, head_dim, _stream(k)))
     return k, v
@@ -651,7 +661,7 @@ def attn_paged(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, k
         return out
     if ws is not None and (ws.device != device or ws.dtype != torch.uint8 or not ws.is_contiguous()):
         raise ValueError("ws must be contiguous uint8 on q's device")
-    with torch.cuda.device(device):
+    with _on(device):
         if ws is None:
             need = attn_paged_workspace_bytes(q.dtype, rows, heads, n_kv_heads, dim)
             # (one that a capture allocates belongs to its graph)

@@ -122,7 +122,7 @@ def _load_calls():
             "kv_write", "kv_read", "attn_paged", "kv_page_bytes", "attn_paged_workspace_bytes")))
         return calls
     except (ImportError, OSError) as e:
-        warnings.warn(f"the paged cache's calls go through ctypes, twice as long on the host: {e}", RuntimeWarning)
+        warnings.warn(f"the paged cache's calls go through ctypes, three times as long on the host: {e}", RuntimeWarning)
         return types.SimpleNamespace(**{name: lambda *args: None for name in ("kv_write", "kv_read", "attn_paged")})
 
 

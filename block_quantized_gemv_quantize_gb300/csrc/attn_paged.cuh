@@ -19,8 +19,9 @@
 // that has met scales further apart, or of zero, goes through its tiles again
 // (ATTN_AGAIN), with powers for each row and block: then neither what other rows see,
 // nor what other blocks hold, nor tokens without weight take bits from a product.  That
-// makes a split two to four times as long (all of them, 131071 tokens in q4_0: 335 us,
-// not 94); such powers everywhere cost every call (17 rows at D = 256 98 us, not 76).
+// makes a split two to four times as long (all of them, two of 131071 tokens in q4_0:
+// 335 us, not 95); such powers in every step cost every call (17 rows at D = 256 98 us,
+// not 76).  An fp16 cache's infinities and NaN, too, are left for such a second pass.
 //
 // Rows in an instruction of 16 (MODE):
 //   ATTN_PAIR  8 rows: their hi in the lower half, their lo in the upper
@@ -44,15 +45,20 @@
 // does not depend on the order in which CTAs finish.
 //
 // What bounds it.  46 ragged sequences of up to 8192 tokens (q8_0, bf16 rows):
-// 81 us, 5.5 TB/s, nearly what the copies and the join take without the arithmetic.
+// 80 us, 5.6 TB/s, nearly what the copies and the join take without the arithmetic.
 // One kv head a query head in f16: 40 us, 5.2 TB/s, likewise.  Two sequences of
-// 131071 tokens in q4_0 (fp16 rows, pairs of terms): 96 us where the copies alone
-// take 58: 420 instructions a tile of 16 tokens and 8 rows, of which 32 are the
-// products, at 0.55 an SM quarter and cycle.  Width 6 over 17391 tokens (30 rows a
-// kv head, two terms): 30 us, of them 20 in the splits at one instruction in three
-// cycles a warp (two warps a scheduler, 255 registers each).  A call of 197 tokens
-// takes 10 us: two launches, three dependent reads before the first tile arrives
+// 131071 tokens in q4_0 (fp16 rows): 95 us where the copies alone take 58: 415
+// instructions a tile of 16 tokens and 8 rows, of which 32 are the products, at 0.56
+// an SM quarter and cycle.  Width 6 over 17391 tokens (30 rows a kv head): 30 us, of
+// them 20 in the splits at two instructions in five cycles an SM quarter (two warps
+// each, 232 registers a thread).  17 rows with a window at D = 256: 76 us, six warps a
+// CTA that each unpack every tile, at one instruction in three cycles.  A call of 197
+// tokens takes 10 us: two launches, three dependent reads before the first tile arrives
 // (lengths, page number, tile) and the join.
+//
+// Registers: 255 a thread do not hold all of D = 256.  Over 8 rows q8_0 and q4_0 spill
+// 44 bytes at most; an f16 cache 190 bytes up to 8 rows, where memory bounds it all the
+// same (8 sequences of 8192 tokens, 8 kv heads: 86 us, 6.3 TB/s), and 230 above.
 #pragma once
 
 #include <type_traits>

@@ -17,6 +17,8 @@
 // kv_write 6.2 (fp32 to q8_0), 5.2 (fp32 to q4_0), 6.4 to 6.7 (to f16), and 3.8
 // and 2.5 from bf16 to q8_0 and q4_0, where the instructions of the quantizing
 // bound it: half of a warp's blocks hold a value on a code's border (kv_encode).
+// (From fp32 to q4_0 and q8_0 four blocks' values do not fit the 64 registers that
+// four CTAs an SM leave a thread: 24 and 12 bytes of them are spilled.)
 #include "kvcache.cuh"
 
 namespace qgemv {

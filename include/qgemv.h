@@ -518,7 +518,7 @@ int64_t kv_tile_offset(int fmt, int64_t n_pages, int page_tokens, int n_kv_heads
  *              rows load faster).  Read.
  *   slots      int64 [n_tokens]: each token's slot; one outside the cache
  *              (negative, or past its last page) skips the token.  Two tokens
- *              with one slot in one call leave either's bytes.
+ *              with one slot in one call leave some bytes of either there.
  *   cache      written at those slots and nowhere else
  *   n_tokens   >= 0
  * Errors: QGEMV_INVALID_ARG (null pointer, unknown fmt or type, sizes out of
@@ -560,8 +560,8 @@ int kv_read(int fmt, int type, const void* cache, int64_t n_pages, int page_toke
  *   out        written, row (r, h) at r * o_row + h * o_head; must not overlap q
  *   lse        fp32 [batch * rows][n_heads] (written), or NULL
  *   page_table int32, page of positions j page_tokens .. of sequence b at
- *              b * ld_table + j, 0 <= j < max_pages; entries past a
- *              sequence's length are not used
+ *              b * ld_table + j, 0 <= j < max_pages <= ld_table; entries
+ *              past a sequence's length are not used
  *   kv_lens    int32 [batch], the lengths with the new tokens in them; <= 0
  *              for an unused place
  *   workspace  attn_paged_workspace_bytes() bytes, 16-byte aligned, with

@@ -16,7 +16,7 @@
 // exact power of two per row, w d_v to below 2^15 by one that follows the largest
 // d_v seen so far, so that neither leaves fp16's range.  That one power for all rows
 // and blocks loses nothing while the scales are within 2^12 of one another.  A warp
-// that has met scales further apart, or of zero, goes through its tiles again
+// that has met scales further apart, or some of zero, goes through its tiles again
 // (ATTN_AGAIN), with powers for each row and block: then neither what other rows see,
 // nor what other blocks hold, nor tokens without weight take bits from a product.  That
 // makes a split two to four times as long (all of them, two of 131071 tokens in q4_0:
@@ -460,7 +460,7 @@ struct AttnState {
     using Sh = AttnShape<FMT, NB, MODE>;
     float m[Sh::NR], l[Sh::NR], rs[Sh::NR];
     float o[NB][4][4];
-    int e;
+    int e;  // V's scales are below 2^(e - 14); -1: all are zero so far
     __half2 least;  // of the scales that some row sees, as far as this lane looks at them
     uint32_t magic;
 
@@ -474,7 +474,7 @@ struct AttnState {
             for (int n = 0; n < 4; ++n)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) o[b][n][c] = 0.0f;
-        e = 0;
+        e = -1;
         least = bits_h2(0x7c007c00u);
     }
     // the outputs of row r and block b times f
@@ -502,7 +502,7 @@ struct AttnState {
             return __any_sync(0xffffffffu, !isfinite(sum));
         }
         const uint32_t two = h2_bits(least), low = __reduce_min_sync(0xffffffffu, min(two & 0xffffu, two >> 16));
-        return low < attn_least_scale(e);
+        return e >= 0 && low < attn_least_scale(e);
     }
     // End of a segment: l over the quad; the two halves of a split row added
     // (an infinite output stands in the high half alone); the scale out.
@@ -712,7 +712,7 @@ __device__ __forceinline__ void attn_step(AttnState<FMT, NB, MODE>& st, const At
         }
         top = __hmax2(top, __lowhigh2highlow(top));
         const uint32_t bits = __reduce_max_sync(0xffffffffu, h2_bits(top) & 0xffffu);
-        if (bits < 0x7c00u) e = max(e, (int)(bits >> 10));  // d_v < 2^(e - 14)
+        if (bits > 0 && bits < 0x7c00u) e = max(e, (int)(bits >> 10));
     }
 
     // ---- the sums are rescaled only where a maximum is passed by 4 (a factor
@@ -1189,6 +1189,7 @@ __global__ void __launch_bounds__((AttnShape<FMT, NB, MODE>::WARPS + 1) * 32, 1)
             // their addresses checked by the copying warp; a page whose number has
             // changed meanwhile is no page.)
             st.clear();
+            st.e = 0;
             powers.clear();
             const int tpp = a.L.tiles();
 #pragma unroll 1

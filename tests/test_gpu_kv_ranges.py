@@ -120,3 +120,13 @@ def test_all_weight_on_a_token_of_zeros(ops, fmt, at, rows, heads, kv_heads, dim
     args, q, kv = attention_case(ops, fmt, "float32", [300], rows, heads, kv_heads, dim, 32, 0, plant=plant, spread=0.7)
     args["q"] = args["q"].abs()
     check(ops, args, np.abs(q), kv, [300])
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("kind", ["float32", "bfloat16"])
+def test_values_of_zero(ops, fmt, kind):  # noqa: F811
+    def plant(b, k, v):
+        v[:] = 0
+
+    args, q, kv = attention_case(ops, fmt, kind, [333, 1], 3, 4, 2, 128, 16, 0, plant=plant)
+    assert not bool(ops.attn_paged(**args).any())

@@ -442,7 +442,7 @@ struct AttnPowers {
             for (uint32_t& x : w[r]) x = ATTN_POWER_MOST * 0x01010101u;
     }
     __device__ __forceinline__ float of(int r, int b) const { return attn_power(w[r][b / 4], b); }
-    // 4^rise times, at most the largest; negative: a fourth as often, at least the smallest
+    // the power times 4^rise (of either sign), within the ends; returns by what it changed
     __device__ __forceinline__ float change(int r, int b, int rise)
     {
         uint32_t& x = w[r][b / 4];

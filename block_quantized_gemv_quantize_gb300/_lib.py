@@ -82,6 +82,20 @@ SIGNATURES = {
     "attn_paged_workspace_bytes": (_S, [_I, _I, _I, _I, _I]),
     "attn_paged": (_I, [_I, _I, _P, _L, _L, _P, _L, _I, _P, _L, _I, _P, _P, _L, _L, _P, _P, _S, _I, _I, _I, _I, _I,
                         ctypes.c_float, _I, _P]),
+    "mxfp4_bytes": (_S, [_L, _I]),
+    "quantize_mxfp4": (_I, [_I, _P, _L, _P, _L, _I, _P]),
+    "dequantize_mxfp4": (_I, [_I, _P, _P, _L, _L, _I, _P]),
+    "mxfp4_pack_bytes": (_S, [_I, _I, _I]),
+    "qpack_mxfp4": (_I, [_P, _P, _I, _I, _I, _P]),
+    "moe_route_workspace_bytes": (_S, [_I, _I, _I]),
+    "moe_route": (_I, [_I, _P, _L, _P, _P, _P, _P, _P, _S, _I, _I, _I, _I, _I, ctypes.c_float, _P]),
+    "moe_group": (_I, [_P, _P, _P, _P, _S, _I, _I, _I, _P]),
+    "qgemm_mxfp4_workspace_bytes": (_S, [_I, _I, _I, _I, _I, _I]),
+    "moe_gate_up_mxfp4_workspace_bytes": (_S, [_I, _I, _I, _I, _I, _I]),
+    "moe_down_mxfp4_workspace_bytes": (_S, [_I, _I, _I, _I, _I, _I]),
+    "qgemm_mxfp4": (_I, [_I, _P, _P, _L, _P, _P, _P, _L, _P, _S, _I, _I, _I, _I, _I, _P]),
+    "moe_gate_up_mxfp4": (_I, [_I, _P, _P, _P, _L, _P, _P, _P, _L, _P, _S, _I, _I, _I, _I, _I, _P]),
+    "moe_down_mxfp4": (_I, [_I, _P, _P, _L, _P, _P, _P, _P, _L, _P, _S, _I, _I, _I, _I, _I, _P]),
 }
 
 
@@ -675,6 +689,232 @@ def attn_paged(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, k
                 dim, dim ** -0.5 if scale is None else scale, window, _stream(q))
     _check("attn_paged", done)
     return out
+
+
+# ---------------------------------------------------------------- MXFP4 and the sparse layer
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _matrix(t: torch.Tensor, what: str, rows: int | None = None, columns: int | None = None,
+            like: torch.Tensor | None = None) -> int:
+    """Row stride of a CUDA tensor [rows, columns] with contiguous rows."""
+    if t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1) or (t.stride(0) < t.shape[1] and t.shape[0] > 1):
+        raise ValueError(f"{what} must be [rows, values] with contiguous rows that do not overlap")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if (rows is not None and t.shape[0] != rows) or (columns is not None and t.shape[1] != columns):
+        raise ValueError(f"{what} is {list(t.shape)}, not [{rows}, {columns}]")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{what} must have the type and device of its companion")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _array(t: torch.Tensor, what: str, dtype: torch.dtype, shape: tuple, near: torch.Tensor) -> int:
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != near.device or not t.is_cuda:
+        raise ValueError(f"{what} must be contiguous {dtype} {list(shape)} on {near.device}")
+    return t.data_ptr()
+
+
+def _scratch(ws: torch.Tensor | None, need: int, near: torch.Tensor):
+    """(tensor, address, bytes) of a call's workspace: the given one, or memory of its own."""
+    if ws is None:
+        if need == 0:
+            return None, None, 0
+        ws = torch.empty(need, dtype=torch.uint8, device=near.device)
+    elif ws.device != near.device or ws.dtype != torch.uint8 or not ws.is_contiguous():
+        raise ValueError(f"ws must be contiguous uint8 on {near.device}")
+    return ws, ws.data_ptr(), ws.numel()
+
+
+def _mx_blocks(blocks: torch.Tensor, what: str = "blocks") -> tuple[int, int]:
+    """(rows, K) of canonical MXFP4 blocks, uint8 [..., K/32, 17]."""
+    if blocks.dtype != torch.uint8 or blocks.dim() < 2 or blocks.shape[-1] != 17 or not blocks.is_contiguous() \
+            or not blocks.is_cuda:
+        raise ValueError(f"{what} must be contiguous CUDA uint8 [..., K/32, 17]")
+    return blocks.shape[:-2].numel(), 32 * blocks.shape[-2]
+
+
+def mxfp4_bytes(N: int, K: int) -> int:
+    """Bytes of N rows of K values in MXFP4 blocks; 0 for sizes that the calls refuse."""
+    _fits(64, N=N)
+    _fits(32, K=K)
+    return LIB.mxfp4_bytes(N, K)
+
+
+@functools.lru_cache(maxsize=1024)
+def mxfp4_pack_bytes(experts: int, N: int, K: int) -> int:
+    """Bytes of a pack of experts weights of N rows of K values; 0 for sizes that the calls refuse."""
+    _fits(32, experts=experts, N=N, K=K)
+    return LIB.mxfp4_pack_bytes(experts, N, K)
+
+
+def quantize_mxfp4(x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
+    """fp32, fp16 or bf16 x [N, K] (any row stride) -> MXFP4 blocks, uint8 [N, K/32, 17]."""
+    ld, code = _matrix(x, "x"), _type(x, "x")
+    N, K = x.shape
+    if K < 32 or K % 32:
+        raise ValueError(f"rows of {K} values: blocks have 32")
+    if out is None:
+        out = torch.empty((N, K // 32, 17), dtype=torch.uint8, device=x.device)
+    op = _array(out, "out", torch.uint8, (N, K // 32, 17), x)
+    _fits(32, K=K)
+    if N:
+        with _on(x.device):
+            _check("quantize_mxfp4", LIB.quantize_mxfp4(code, x.data_ptr(), ld, op, N, K, _stream(x)))
+    return out
+
+
+def dequantize_mxfp4(blocks: torch.Tensor, dtype: torch.dtype = torch.float32,
+                     out: torch.Tensor | None = None) -> torch.Tensor:
+    """MXFP4 blocks, uint8 [N, K/32, 17] -> the values [N, K] in dtype, or into out (any row stride)."""
+    N, K = _mx_blocks(blocks)
+    if out is None:
+        out = torch.empty((N, K), dtype=dtype, device=blocks.device)
+    ld, code = _matrix(out, "out", N, K), _type(out, "out")
+    if out.device != blocks.device:
+        raise ValueError("out is on another device")
+    _fits(32, K=K)
+    if N:
+        with _on(blocks.device):
+            _check("dequantize_mxfp4", LIB.dequantize_mxfp4(code, blocks.data_ptr(), out.data_ptr(), ld, N, K,
+                                                            _stream(blocks)))
+    return out
+
+
+def qpack_mxfp4(w_canon: torch.Tensor, experts: int, N: int, K: int, out: torch.Tensor | None = None) -> torch.Tensor:
+    """The blocks of experts weights of N rows of K values (uint8 [experts * N, K/32, 17]) -> the products' pack."""
+    rows, values = _mx_blocks(w_canon, "w_canon")
+    need = mxfp4_pack_bytes(experts, N, K)
+    if rows != experts * N or values != K:
+        raise ValueError(f"w_canon has {rows} rows of {values} values, not {experts} x {N} of {K}")
+    if need == 0:
+        raise ValueError(f"no such weights: {experts} of {N} rows of {K} values")
+    if out is None:
+        out = torch.empty(need, dtype=torch.uint8, device=w_canon.device)
+    op = _array(out, "out", torch.uint8, (need,), w_canon)
+    with _on(w_canon.device):
+        _check("qpack_mxfp4", LIB.qpack_mxfp4(w_canon.data_ptr(), op, experts, N, K, _stream(w_canon)))
+    return out
+
+
+def moe_route_workspace_bytes(tokens: int, experts: int, top_k: int) -> int:
+    _fits(32, tokens=tokens, experts=experts, top_k=top_k)
+    return LIB.moe_route_workspace_bytes(tokens, experts, top_k)
+
+
+def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+              ws: torch.Tensor | None = None):
+    """(ids, weights [tokens, top_k], offsets [experts + 1], order [tokens * top_k]):
+    the top_k experts of each row of logits [tokens, experts] in descending
+    order (lowest index first among equals; id -1 and weight 0 where none is
+    left: minus infinity and NaN are never chosen), their weights (softmax
+    over all experts, or sigmoid; divided by their sum with renormalize; times
+    scale), and the slots t * top_k + j sorted by expert: expert e's are
+    order[offsets[e]:offsets[e + 1]], those without an expert come last."""
+    if score not in SCORES:
+        raise ValueError(f"score must be one of {', '.join(SCORES)}, not {score!r}")
+    ld, code = _matrix(logits, "logits"), _type(logits, "logits")
+    tokens, experts = logits.shape
+    _fits(32, tokens=tokens, experts=experts, top_k=top_k)
+    if not 1 <= top_k <= experts:
+        raise ValueError(f"top_k = {top_k} of {experts} experts")
+    device = logits.device
+    ids = torch.empty((tokens, top_k), dtype=torch.int32, device=device)
+    weights = torch.empty((tokens, top_k), dtype=torch.float32, device=device)
+    offsets = torch.empty(experts + 1, dtype=torch.int32, device=device)
+    order = torch.empty(tokens * top_k, dtype=torch.int32, device=device)
+    if tokens == 0:  # (an empty tensor has no address)
+        return ids, weights, offsets.zero_(), order
+    ws, wp, wn = _scratch(ws, moe_route_workspace_bytes(tokens, experts, top_k), logits)
+    with _on(device):
+        _check("moe_route", LIB.moe_route(code, logits.data_ptr(), ld, ids.data_ptr(), weights.data_ptr(),
+                                          offsets.data_ptr(), order.data_ptr(), wp, wn, tokens, experts, top_k,
+                                          SCORES[score], int(renormalize), scale, _stream(logits)))
+    return ids, weights, offsets, order
+
+
+def moe_group(ids: torch.Tensor, experts: int, ws: torch.Tensor | None = None):
+    """(offsets, order) of given ids (int32 [tokens, top_k]), as moe_route makes them."""
+    if ids.dtype != torch.int32 or ids.dim() != 2 or not ids.is_contiguous() or not ids.is_cuda:
+        raise ValueError("ids must be contiguous CUDA int32 [tokens, top_k]")
+    tokens, top_k = ids.shape
+    _fits(32, tokens=tokens, experts=experts, top_k=top_k)
+    offsets = torch.empty(max(experts, 0) + 1, dtype=torch.int32, device=ids.device)
+    order = torch.empty(tokens * top_k, dtype=torch.int32, device=ids.device)
+    if tokens == 0:
+        return offsets.zero_(), order
+    ws, wp, wn = _scratch(ws, moe_route_workspace_bytes(tokens, experts, top_k), ids)
+    with _on(ids.device):
+        _check("moe_group", LIB.moe_group(ids.data_ptr(), offsets.data_ptr(), order.data_ptr(), wp, wn, tokens, experts,
+                                          top_k, _stream(ids)))
+    return offsets, order
+
+
+@functools.lru_cache(maxsize=1024)
+def _product_bytes(name: str, code: int, tokens: int, top_k: int, experts: int, K: int, N: int) -> int:
+    _fits(32, tokens=tokens, top_k=top_k, experts=experts, K=K, N=N)
+    return getattr(LIB, name + "_workspace_bytes")(code, tokens, top_k, experts, K, N)
+
+
+def _product(name: str, packs: tuple, x: torch.Tensor, offsets: torch.Tensor, order: torch.Tensor | None,
+             weights: torch.Tensor | None, tokens: int, top_k: int, rows: int, N: int, y: torch.Tensor | None,
+             ws: torch.Tensor | None) -> torch.Tensor:
+    ldx, code = _matrix(x, "x"), _type(x, "x")
+    K, device = x.shape[1], x.device
+    if offsets.dim() != 1 or offsets.shape[0] < 2:
+        raise ValueError("offsets must be [experts + 1]")
+    experts = offsets.shape[0] - 1
+    fp = _array(offsets, "offsets", torch.int32, (experts + 1,), x)
+    need = mxfp4_pack_bytes(experts, N, K)
+    if need == 0:
+        raise ValueError(f"no such weights: {experts} of {N} rows of {K} values")
+    pp = [_array(p, "the pack", torch.uint8, (need,), x) for p in packs]
+    if order is None:
+        if top_k != 1:
+            raise ValueError(f"top_k = {top_k} wants the order of the slots")
+        dp = None
+    else:
+        dp = _array(order, "order", torch.int32, (tokens * top_k,), x)
+    wp = () if weights is None else (_array(weights, "weights", torch.float32, (tokens, top_k), x),)
+    if y is None:
+        y = torch.empty((rows, N), dtype=x.dtype, device=device)
+    ldy = _matrix(y, "the output", rows, N, like=x)
+    if tokens == 0:
+        return y
+    ws, sp, sn = _scratch(ws, _product_bytes(name, code, tokens, top_k, experts, K, N), x)
+    with _on(device):
+        _check(name, getattr(LIB, name)(code, *pp, x.data_ptr(), ldx, fp, dp, *wp, y.data_ptr(), ldy, sp, sn, tokens,
+                                        top_k, experts, K, N, _stream(x)))
+    return y
+
+
+def qgemm_mxfp4(w_pack: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, N: int, order: torch.Tensor | None = None,
+                top_k: int = 1, y: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """y [tokens * top_k, N]: each slot's row of x [tokens, K] times its expert's
+    MXFP4 weight (a pack of experts weights of N rows).  Slots order[offsets[e]]
+    .. order[offsets[e + 1] - 1] are expert e's; without order (top_k 1) the
+    rows are sorted by expert already.  A slot without an expert gets zeros."""
+    return _product("qgemm_mxfp4", (w_pack,), x, offsets, order, None, x.shape[0], top_k, x.shape[0] * top_k, N, y, ws)
+
+
+def moe_gate_up_mxfp4(w_gate: torch.Tensor, w_up: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, N: int,
+                      order: torch.Tensor | None = None, top_k: int = 1, h: torch.Tensor | None = None,
+                      ws: torch.Tensor | None = None) -> torch.Tensor:
+    """h [tokens * top_k, N] = silu(gate x) * (up x) of each slot's expert, the
+    products never written; arguments as qgemm_mxfp4."""
+    return _product("moe_gate_up_mxfp4", (w_gate, w_up), x, offsets, order, None, x.shape[0], top_k,
+                    x.shape[0] * top_k, N, h, ws)
+
+
+def moe_down_mxfp4(w_down: torch.Tensor, h: torch.Tensor, offsets: torch.Tensor, N: int, order: torch.Tensor | None,
+                   weights: torch.Tensor, out: torch.Tensor | None = None, ws: torch.Tensor | None = None) -> torch.Tensor:
+    """out [tokens, N]: the sum over a token's slots of weights [tokens, top_k]
+    times the slot's row of h [tokens * top_k, K] through its expert's weight."""
+    if weights.dim() != 2 or weights.shape[1] < 1 or h.shape[0] != weights.numel():
+        raise ValueError(f"h has {h.shape[0]} rows, weights are {list(weights.shape)}: one row for each weight")
+    tokens, top_k = weights.shape
+    return _product("moe_down_mxfp4", (w_down,), h, offsets, order, weights, tokens, top_k, tokens, N, out, ws)
 
 
 def qgemv_block_dots_q4_0(w_pack: torch.Tensor, xq: torch.Tensor, M: int, K: int, N: int) -> torch.Tensor:

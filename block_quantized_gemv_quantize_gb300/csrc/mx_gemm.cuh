@@ -1,0 +1,443 @@
+// Products of MXFP4 experts with few rows each (mma.sync kernel).
+//
+// y[s][n] = sum_k w[n][k] x[s][k].  A code is a half exactly, so 16 rows of
+// codes are the A operand of m16n8k16 as the pack has them (four conversions a
+// word, no integer work), 8 rows of x the B operand, and a block's two
+// products a sum of 32 terms in fp32 that its scale then multiplies: one fused
+// multiply-add an output and block, exact but for the sum's own rounding.
+// x as halves: fp16 rows are what they are; bf16 rows go by a power of two
+// that brings the row's largest finite element to [2^14, 2^15), which keeps
+// every element to 2^-40 of it (all eight bits of those within 2^-31); fp32
+// rows are two such terms (22 bits and a sign) of elements within 2^-15.
+//
+// Bound by the weights' bytes: 17/32 of a byte a value, read once if an
+// expert's rows fit one row tile.  A warp streams units of 16 rows x 64 values
+// (544 B, contiguous over K) through a ring of its own in shared memory by
+// asynchronous copies, `parts` warps of a CTA share a tile's K and add up
+// through shared memory, and a CTA runs through a contiguous range of
+// (expert, row tile, tiles) so that x is staged once for many tiles.  The
+// ring runs ahead across tiles and experts.
+#pragma once
+
+#include "mxfp4.cuh"
+
+#include <type_traits>
+
+namespace qgemv {
+
+constexpr int MXS_THREADS = 256, MXS_WARPS = MXS_THREADS / 32;
+constexpr int MXS_RED = 20;  // floats of a column of 16 in the exchange (no bank conflicts)
+
+struct MxsPlan {
+    int rows;     // of x in a row tile
+    int parts;    // warps that share a tile's K
+    int stages;   // of a warp's ring
+    int x_bytes;  // of a staged row and term
+    int grid;
+    size_t smem;
+};
+
+__device__ __forceinline__ void cp_async16(void* smem, const void* gmem)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(gmem));
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The eight codes of a word as halves, two for each byte.
+__device__ __forceinline__ void e2m1_halves(uint32_t w, uint32_t (&h)[4])
+{
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+
+// The experts' row tiles: before[e] of them come before expert e's, whose
+// slots are order[start[e]] ...  Offsets that do not fit the slots are cut.
+__device__ __forceinline__ int mx_clamped(const int32_t* offsets, int e, int slots)
+{
+    return max(0, min(slots, offsets[e]));
+}
+
+template <int THREADS>
+__device__ int mx_row_tiles(const MxArgs& a, int rows, int* before, int* start, int* sums)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int base = 0;
+    for (int lo = 0; lo < a.L.experts; lo += THREADS) {
+        const int e = lo + threadIdx.x;
+        int n = 0;
+        if (e < a.L.experts) {
+            const int s0 = mx_clamped(a.offsets, e, a.slots), s1 = mx_clamped(a.offsets, e + 1, a.slots);
+            start[e] = s0;
+            n = s1 > s0 ? (s1 - s0 + rows - 1) / rows : 0;
+        }
+        int s = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int up = __shfl_up_sync(~0u, s, o);
+            if (lane >= o) s += up;
+        }
+        if (lane == 31) sums[warp] = s;
+        __syncthreads();
+        int mine = base;
+        for (int w = 0; w < THREADS / 32; ++w) {
+            if (w < warp) mine += sums[w];
+            base += sums[w];
+        }
+        if (e < a.L.experts) before[e] = mine + s - n;
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+        before[a.L.experts] = base;
+        start[a.L.experts] = mx_clamped(a.offsets, a.L.experts, a.slots);
+    }
+    __syncthreads();
+    return base;
+}
+
+// The rows of slots that no expert has.
+template <typename O>
+__device__ void mx_zero_rest(const MxArgs& a, O* y, unsigned int* status)
+{
+    const int lo = mx_clamped(a.offsets, 0, a.slots), hi = mx_clamped(a.offsets, a.L.experts, a.slots);
+    const int rest = lo + a.slots - hi;
+    for (int i = blockIdx.x; i < rest; i += gridDim.x) {
+        const int at = i < lo ? i : hi + i - lo;
+        const int s = a.order ? a.order[at] : at;
+        if (s < 0 || s >= a.slots) continue;
+        for (int n = threadIdx.x; n < a.L.N; n += blockDim.x)
+            if (QG_OK(qg_in((int64_t)s * a.ldy + n, 1, (int64_t)a.slots * a.ldy), status, 310))
+                y[(int64_t)s * a.ldy + n] = from_f32<O>(0.0f);
+    }
+}
+
+__device__ __forceinline__ float mx_silu(float g) { return g / (1.0f + expf(-g)); }
+
+template <typename T>
+constexpr int MX_TERMS = sizeof(T) == 4 ? 2 : 1;
+
+// Eight neighbouring values of a row (`wide`: 16-byte aligned), zeros from n on.
+template <typename T>
+__device__ __forceinline__ void mx_load8(const T* p, bool wide, int n, float (&v)[8])
+{
+    if (wide && n >= 8) {
+        alignas(16) T t[8];
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(t)[i] = reinterpret_cast<const uint4*>(p)[i];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = to_f32(t[k]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = k < n ? to_f32(p[k]) : 0.0f;
+    }
+}
+
+__device__ __forceinline__ uint32_t mx_halves(__half a, __half b)
+{
+    return (uint32_t)__half_as_ushort(a) | (uint32_t)__half_as_ushort(b) << 16;
+}
+
+// The cnt rows of a row tile into shared memory, as the product takes them: a
+// block has 16 bytes for each t, values 4 t, 4 t + 2, 16 + 4 t, 16 + 4 t + 2
+// and then those one further on each.  A warp takes 256 values of a row at a
+// time, a lane eight neighbouring ones: half a piece of two t each.
+template <typename T>
+__device__ void mxs_stage(const MxArgs& a, const MxsPlan& p, uint8_t* xs, const int* slot_of, int* x_exp,
+                          uint32_t* x_top, int cnt, unsigned int* status)
+{
+    constexpr int TERMS = MX_TERMS<T>;
+    constexpr bool SCALED = !std::is_same<T, __half>::value;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int K = a.L.K, padded = a.L.units() * MX_UNIT_K, pieces = (padded + 255) / 256;
+    const T* x = static_cast<const T*>(a.x);
+    const bool wide = ((reinterpret_cast<uintptr_t>(x) | (uintptr_t)(a.ldx * (int64_t)sizeof(T))) & 15u) == 0;
+    if constexpr (SCALED) {
+        for (int i = warp; i < cnt * pieces; i += MXS_WARPS) {
+            const int row = i / pieces, k = (i - row * pieces) * 256 + lane * 8, s = max(0, slot_of[row]);
+            float v[8];
+            mx_load8(x + (int64_t)(s / a.x_div) * a.ldx + k, wide, max(0, K - k), v);
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t m = __float_as_uint(v[j]) & 0x7FFFFFFFu;
+                top = max(top, m < 0x7F800000u ? m : 0u);
+            }
+            top = __reduce_max_sync(~0u, top);
+            if (lane == 0) atomicMax(&x_top[row], top);
+        }
+        __syncthreads();
+        // (a row whose largest is subnormal goes by 2^126, and keeps what it has to 2^-38 of 2^-126)
+        if ((int)threadIdx.x < cnt) x_exp[threadIdx.x] = x_top[threadIdx.x] ? max(-112, (int)(x_top[threadIdx.x] >> 23) - 141) : 0;
+        __syncthreads();
+    }
+    for (int i = warp; i < cnt * pieces; i += MXS_WARPS) {
+        const int row = i / pieces, k = (i - row * pieces) * 256 + lane * 8, s = max(0, slot_of[row]);
+        if (k >= padded) continue;
+        float v[8];
+        mx_load8(x + (int64_t)(s / a.x_div) * a.ldx + k, wide, max(0, K - k), v);
+        uint8_t* to = xs + (size_t)row * TERMS * p.x_bytes;
+        const float f = SCALED ? __uint_as_float((uint32_t)(127 - x_exp[row]) << 23) : 1.0f;
+        __half h[8], l[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float y = v[j] * f;
+            h[j] = __float2half_rn(y);
+            if constexpr (TERMS == 2) l[j] = isfinite(y) ? __float2half_rn(y - __half2float(h[j])) : __float2half_rn(0.0f);
+        }
+        if (QG_OK(qg_in(k * 2, 16, p.x_bytes - 64) && row < p.rows, status, 313)) {
+            const int q = (k >> 3) & 3;
+            uint32_t* o = reinterpret_cast<uint32_t*>(to + (k & ~31) * 2 + (q & 1) * 32 + (q >> 1) * 4);
+            o[0] = mx_halves(h[0], h[2]);
+            o[2] = mx_halves(h[1], h[3]);
+            o[4] = mx_halves(h[4], h[6]);
+            o[6] = mx_halves(h[5], h[7]);
+            if constexpr (TERMS == 2) {
+                o += p.x_bytes / 4;
+                o[0] = mx_halves(l[0], l[2]);
+                o[2] = mx_halves(l[1], l[3]);
+                o[4] = mx_halves(l[4], l[6]);
+                o[6] = mx_halves(l[5], l[7]);
+            }
+        }
+    }
+    __syncthreads();
+}
+
+// Where a warp is in its CTA's range.
+struct MxCursor {
+    int64_t left;   // items
+    int rt, g, e;   // row tile of all, group of tiles, expert
+    __device__ void next(const int* before, int groups)
+    {
+        --left;
+        if (++g == groups) {
+            g = 0;
+            ++rt;
+            if (left > 0)
+                while (rt >= before[e + 1]) ++e;
+        }
+    }
+};
+
+template <typename T, int NT, int MODE, int STAGES>
+__global__ void __launch_bounds__(MXS_THREADS) mxs_kernel(MxArgs a, MxsPlan p, unsigned int* status)
+{
+    using O = typename std::conditional<MODE == MX_DOWN, float, T>::type;
+    constexpr int W = MODE == MX_GATE_UP ? 2 : 1, TERMS = MX_TERMS<T>;
+    constexpr int COLS = 8 * NT, STAGE = W * MX_UNIT_BYTES;
+    extern __shared__ __align__(16) uint8_t sm[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    uint8_t* ring = sm + warp * (STAGES * STAGE);
+    float* red = reinterpret_cast<float*>(sm + MXS_WARPS * STAGES * STAGE);
+    constexpr int RED_ONE = MXS_WARPS * W * COLS * MXS_RED;
+    uint8_t* xs = reinterpret_cast<uint8_t*>(red + 2 * RED_ONE);
+    int* before = reinterpret_cast<int*>(xs + (size_t)p.rows * TERMS * p.x_bytes);
+    int* start = before + a.L.experts + 1;
+    int* sums = start + a.L.experts + 1;
+    int* slot_of = sums + 32;
+    int* x_exp = slot_of + COLS;
+    uint32_t* x_top = reinterpret_cast<uint32_t*>(x_exp + COLS);
+
+    pdl_launch_dependents();
+    pdl_wait();
+    const int n_rt = mx_row_tiles<MXS_THREADS>(a, p.rows, before, start, sums);
+    O* y = static_cast<O*>(a.y);
+    mx_zero_rest(a, y, status);
+
+    const int parts = p.parts, together = MXS_WARPS / parts;  // tiles that the CTA works on at a time
+    const int tiles = a.L.tiles(), units = a.L.units(), groups = (tiles + together - 1) / together;
+    const int64_t items = (int64_t)n_rt * groups;
+    const int64_t i0 = items * blockIdx.x / gridDim.x, i1 = items * (blockIdx.x + 1) / gridDim.x;
+    if (i0 >= i1) return;
+    const int mine = warp / parts, part = warp % parts;
+    const int u0 = units * part / parts, u1 = units * (part + 1) / parts;
+    const int64_t tile_bytes = a.L.tile_bytes(), expert_bytes = a.L.expert_bytes();
+
+    MxCursor load{i1 - i0, (int)(i0 / groups), (int)(i0 % groups), 0};
+    {
+        int lo = 0, hi = a.L.experts - 1;  // the last expert with before[e] <= rt: it has that row tile
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (before[mid] <= load.rt) lo = mid;
+            else hi = mid - 1;
+        }
+        load.e = lo;
+    }
+    MxCursor at = load;
+
+    int load_u = u1, load_stage = 0;
+    const uint8_t *lw = nullptr, *lw2 = nullptr;
+    bool load_first = true;
+    // One more unit of the warp's stream into the ring (or an empty group at its end).
+    auto issue = [&]() {
+        while (load_u >= u1 && load.left > 0) {  // the next item that has units for this warp
+            if (!load_first) load.next(before, groups);
+            load_first = false;
+            if (load.left > 0 && load.g * together + mine < tiles && u0 < u1) {
+                const int64_t off = load.e * expert_bytes + (int64_t)(load.g * together + mine) * tile_bytes;
+                lw = a.w + off;
+                if constexpr (W == 2) lw2 = a.w2 + off;
+                load_u = u0;
+            }
+        }
+        if (load.left > 0) {
+            uint8_t* to = ring + load_stage * STAGE;
+            const int64_t off = (int64_t)load_u * MX_UNIT_BYTES;
+            if (QG_OK(qg_in(lw - a.w + off, MX_UNIT_BYTES, a.L.bytes()), status, 311)) {
+                cp_async16(to + lane * 16, lw + off + lane * 16);
+                if constexpr (W == 2) {
+                    cp_async16(to + MX_UNIT_BYTES + lane * 16, lw2 + off + lane * 16);
+                    if (lane < 4) {
+                        const int o = MX_UNIT_CODES + (lane & 1) * 16;
+                        cp_async16(to + (lane >> 1) * MX_UNIT_BYTES + o, (lane < 2 ? lw : lw2) + off + o);
+                    }
+                } else if (lane < 2) {
+                    cp_async16(to + MX_UNIT_CODES + lane * 16, lw + off + MX_UNIT_CODES + lane * 16);
+                }
+            }
+            ++load_u;
+            if (++load_stage == STAGES) load_stage = 0;
+        }
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i) issue();
+
+    int rt_now = -1, cnt = 0, stage = 0, flip = 0;
+    const uint8_t* xrow[NT];
+    for (; at.left > 0; at.next(before, groups)) {
+        if (at.rt != rt_now) {
+            rt_now = at.rt;
+            __syncthreads();  // the rows before are done with
+            const int s0 = start[at.e] + (at.rt - before[at.e]) * p.rows;
+            cnt = min(p.rows, start[at.e + 1] - s0);
+            if (threadIdx.x < COLS) {
+                int s = -1;
+                if ((int)threadIdx.x < cnt) {
+                    s = a.order ? a.order[s0 + threadIdx.x] : s0 + (int)threadIdx.x;
+                    if (s < 0 || s >= a.slots) s = -1;
+                }
+                slot_of[threadIdx.x] = s;
+                x_exp[threadIdx.x] = 0;
+                x_top[threadIdx.x] = 0;
+            }
+            __syncthreads();
+            mxs_stage<T>(a, p, xs, slot_of, x_exp, x_top, cnt, status);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)  // (columns behind the last row repeat it and go nowhere)
+                xrow[n] = xs + (size_t)min(8 * n + g, cnt - 1) * TERMS * p.x_bytes + t * 16;
+        }
+        // this thread's row of the group in the epilogue, and its scale
+        const int out_n = threadIdx.x & 15, out_tile = (threadIdx.x >> 4) % together;
+        const int tile = at.g * together + out_tile, n = tile * MX_TILE_N + out_n;
+        int top = 0, top2 = 0;
+        if (n < a.L.N) {
+            const int64_t o = at.e * expert_bytes + tile * tile_bytes + (int64_t)units * MX_UNIT_BYTES + out_n;
+            top = a.w[o];
+            if constexpr (W == 2) top2 = a.w2[o];
+        }
+        float acc[W][NT][4];
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) acc[w][i][j] = 0.0f;
+        if (at.g * together + mine < tiles)
+            for (int u = u0; u < u1; ++u) {
+                cp_async_wait<STAGES - 2>();
+                __syncwarp();
+                const uint8_t* from = ring + stage * STAGE;
+                uint4 code[W];
+                uint32_t scale[W];
+#pragma unroll
+                for (int w = 0; w < W; ++w) {
+                    code[w] = *reinterpret_cast<const uint4*>(from + w * MX_UNIT_BYTES + lane * 16);
+                    scale[w] = *reinterpret_cast<const uint32_t*>(from + w * MX_UNIT_BYTES + MX_UNIT_CODES + g * 4);
+                }
+                if (++stage == STAGES) stage = 0;
+                issue();  // (into the stage read one step ago: every lane has its words of it)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    uint32_t ag[W][4], ah[W][4];
+                    float sg[W], sh[W];
+#pragma unroll
+                    for (int w = 0; w < W; ++w) {
+                        e2m1_halves(b ? code[w].z : code[w].x, ag[w]);
+                        e2m1_halves(b ? code[w].w : code[w].y, ah[w]);
+                        sg[w] = __uint_as_float((b ? scale[w] << 7 : scale[w] << 23) & 0x7F800000u);
+                        sh[w] = __uint_as_float((b ? scale[w] >> 1 : scale[w] << 15) & 0x7F800000u);
+                    }
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) {
+                        if (8 * i >= cnt) break;
+                        uint4 x[TERMS];
+#pragma unroll
+                        for (int k = 0; k < TERMS; ++k)
+                            x[k] = *reinterpret_cast<const uint4*>(xrow[i] + (size_t)k * p.x_bytes + (2 * u + b) * 64);
+#pragma unroll
+                        for (int w = 0; w < W; ++w) {
+                            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                            for (int k = 0; k < TERMS; ++k) {
+                                mma_f16(c, ag[w][0], ah[w][0], ag[w][1], ah[w][1], x[k].x, x[k].y);
+                                mma_f16(c, ag[w][2], ah[w][2], ag[w][3], ah[w][3], x[k].z, x[k].w);
+                            }
+                            acc[w][i][0] = fmaf(c[0], sg[w], acc[w][i][0]);
+                            acc[w][i][1] = fmaf(c[1], sg[w], acc[w][i][1]);
+                            acc[w][i][2] = fmaf(c[2], sh[w], acc[w][i][2]);
+                            acc[w][i][3] = fmaf(c[3], sh[w], acc[w][i][3]);
+                        }
+                    }
+                }
+            }
+        float* r = red + flip * RED_ONE;
+        flip ^= 1;
+#pragma unroll
+        for (int w = 0; w < W; ++w)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                if (8 * i >= cnt) break;
+                float* c = r + ((warp * W + w) * COLS + 8 * i + 2 * t) * MXS_RED + g;
+                c[0] = acc[w][i][0];
+                c[MXS_RED] = acc[w][i][1];
+                c[8] = acc[w][i][2];
+                c[MXS_RED + 8] = acc[w][i][3];
+            }
+        __syncthreads();  // (the exchange has two halves: the next write to this one comes after the next barrier)
+        for (int c = (threadIdx.x >> 4) / together; c < cnt; c += MXS_THREADS / 16 / together) {
+            const int s = slot_of[c];
+            if (n >= a.L.N || s < 0) continue;
+            float v[W];
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                float sum = 0.0f;
+                for (int k = 0; k < parts; ++k) sum += r[(((out_tile * parts + k) * W + w) * COLS + c) * MXS_RED + out_n];
+                const int e = w ? top2 : top;
+                v[w] = e == 255 ? __uint_as_float(0x7FC00000u) : mul_pow2(sum, e - 127 + x_exp[c]);
+            }
+            float o = v[0];
+            if constexpr (MODE == MX_GATE_UP) o = mx_silu(v[0]) * v[W - 1];
+            if (QG_OK(qg_in((int64_t)s * a.ldy + n, 1, (int64_t)a.slots * a.ldy), status, 312))
+                y[(int64_t)s * a.ldy + n] = from_f32<O>(o);
+        }
+    }
+    cp_async_wait<0>();
+}
+
+}  // namespace qgemv

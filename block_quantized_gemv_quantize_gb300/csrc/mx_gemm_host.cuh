@@ -1,0 +1,83 @@
+// Launch plans of the experts' products.
+#pragma once
+
+#include "mx_gemm.cuh"
+
+#include <algorithm>
+#include <mutex>
+
+namespace qgemv {
+
+constexpr int MXS_STAGES = 6;  // of a warp's ring: 8 warps x 6 x 544 B (twice for a pair of weights)
+
+// Rows a tile, warps a tile's K, CTAs.
+template <typename T, int NT, int MODE>
+bool mxs_plan(const DeviceInfo& di, const MxArgs& a, MxsPlan& p)
+{
+    constexpr int W = MODE == MX_GATE_UP ? 2 : 1, TERMS = MX_TERMS<T>, COLS = 8 * NT;
+    const int units = a.L.units();
+    p.stages = MXS_STAGES;
+    p.x_bytes = units * MX_UNIT_K * 2 + 64;  // (neighbouring rows half of the banks apart)
+    const size_t fixed = (size_t)MXS_WARPS * MXS_STAGES * W * MX_UNIT_BYTES +
+                         2u * MXS_WARPS * W * COLS * MXS_RED * sizeof(float) +
+                         (size_t)(2 * (a.L.experts + 1) + 32 + 3 * COLS) * sizeof(int);
+    const size_t row = (size_t)TERMS * p.x_bytes;
+    const int want = std::max(1, std::min(COLS, a.slots));
+    // two CTAs an SM where that leaves the row tiles half of what they want
+    size_t each = ((size_t)di.smem_optin + 1024) / 2 - 1024;
+    int fit = each > fixed ? (int)((each - fixed) / row) : 0;
+    int ctas = 2;
+    if (2 * fit < want) {
+        each = di.smem_optin;
+        fit = each > fixed ? (int)((each - fixed) / row) : 0;
+        ctas = 1;
+    }
+    if (fit < 1) return false;
+    p.rows = std::min(want, fit);
+    p.smem = fixed + row * p.rows;
+    p.parts = units >= 32 ? 8 : units >= 12 ? 4 : units >= 4 ? 2 : 1;
+    const int groups = (a.L.tiles() * p.parts + MXS_WARPS - 1) / MXS_WARPS;
+    const int64_t most = (int64_t)groups * std::min<int64_t>(a.slots, (int64_t)a.slots / p.rows + a.L.experts);
+    p.grid = (int)std::min<int64_t>(most, (int64_t)di.sms * ctas);
+    return true;
+}
+
+template <typename T, int NT, int MODE>
+int launch_mxs(const MxArgs& a, cudaStream_t s)
+{
+    const DeviceInfo di = device_info();
+    int dev = 0;
+    if (di.sms <= 0 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return QGEMV_CUDA_ERROR;
+    MxsPlan p;
+    if (!mxs_plan<T, NT, MODE>(di, a, p)) return QGEMV_UNSUPPORTED_SHAPE;
+    auto kern = mxs_kernel<T, NT, MODE, MXS_STAGES>;
+    static std::once_flag once[64];
+    static bool ok[64];
+    std::call_once(once[dev], [&]() {
+        ok[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, di.smem_optin) == cudaSuccess;
+        if (!ok[dev]) cudaGetLastError();
+    });
+    if (!ok[dev]) return QGEMV_CUDA_ERROR;
+    return launch_pdl(kern, dim3((unsigned)p.grid), dim3(MXS_THREADS), p.smem, s, a, p, wait_timeout_counter()) == cudaSuccess
+               ? QGEMV_OK
+               : QGEMV_CUDA_ERROR;
+}
+
+template <typename T, int MODE>
+int launch_mx_mode(const MxArgs& a, cudaStream_t s)
+{
+    const double rows = (double)a.slots / (double)std::min<int64_t>(a.L.experts, a.slots);  // of an expert that has any, about
+    if (rows <= 6.0) return launch_mxs<T, 1, MODE>(a, s);
+    const int status = launch_mxs<T, 4, MODE>(a, s);
+    return status == QGEMV_UNSUPPORTED_SHAPE ? launch_mxs<T, 1, MODE>(a, s) : status;
+}
+
+template <typename T>
+int launch_mx_gemm_t(int mode, const MxArgs& a, cudaStream_t s)
+{
+    if (mode == MX_GEMM) return launch_mx_mode<T, MX_GEMM>(a, s);
+    if (mode == MX_GATE_UP) return launch_mx_mode<T, MX_GATE_UP>(a, s);
+    return launch_mx_mode<T, MX_DOWN>(a, s);
+}
+
+}  // namespace qgemv

@@ -1,0 +1,308 @@
+// MXFP4: quantizer, its inverse, and the repacker of weights.
+#include "mxfp4.cuh"
+
+namespace qgemv {
+namespace {
+
+constexpr int THREADS = 256;
+constexpr int RUN = 32;                     // blocks that a warp takes at a time
+constexpr int RUN_BYTES = RUN * MX_BYTES;   // 544, a multiple of 16: runs of the output stay aligned
+
+// A warp's run of blocks: 4 lanes a block, 8 blocks a step, 4 steps.  Lane
+// `sub` of a block has its values 8 sub .. 8 sub + 7.
+struct RunAt {
+    int64_t row;
+    int col;  // block of the row
+    int nb;
+    __device__ void next()
+    {
+        col += 8;
+        while (col >= nb) {
+            col -= nb;
+            ++row;
+        }
+    }
+};
+
+__device__ __forceinline__ RunAt run_at(uint32_t block, int nb)
+{
+    const uint32_t row = block / (uint32_t)nb;
+    return {row, (int)(block - row * (uint32_t)nb), nb};
+}
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, bool wide, float (&v)[8])
+{
+    if (wide) {
+        alignas(16) T t[8];
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+            reinterpret_cast<uint4*>(t)[i] = ld_stream_v4(reinterpret_cast<const uint4*>(p) + i);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = to_f32(t[k]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] = to_f32(p[k]);
+    }
+}
+
+// Two codes in a byte, `lo` in the low nibble: nearest, of two equally near the
+// even one, at most 6 in magnitude (what the format asks for).
+__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+// One pass over the data: reads 32 s bytes (s: bytes of an element), writes 17 a block, and is bound by
+// HBM.  The scale is an exponent, so both the quotient and the code are exact
+// but for the code's own rounding.
+template <typename T>
+__global__ void __launch_bounds__(THREADS) quantize_kernel(const T* __restrict__ x, int64_t ldx, uint8_t* out,
+                                                           uint32_t blocks, int nb, bool wide, int64_t rows,
+                                                           unsigned int* status)
+{
+    __shared__ __align__(16) uint8_t buf[THREADS / 32][RUN_BYTES];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & 3;
+    uint8_t* mine = buf[warp];
+    const uint32_t runs = (blocks + RUN - 1) / RUN;
+    for (uint32_t run = blockIdx.x * (THREADS / 32) + warp; run < runs; run += gridDim.x * (THREADS / 32)) {
+        const uint32_t first = run * RUN;
+        RunAt at = run_at(first + (lane >> 2), nb);
+        float v[4][8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (first + 8 * i + (lane >> 2) < blocks &&
+                QG_OK(at.row < rows && qg_in((int64_t)at.col * 32 + sub * 8, 8, (int64_t)nb * 32), status, 300))
+                load8(x + at.row * ldx + (int64_t)at.col * 32 + sub * 8, wide, v[i]);
+            else
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[i][k] = 0.0f;
+            at.next();
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t top = 0;  // magnitudes order like their bits; NaN and infinity come last
+#pragma unroll
+            for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[i][k]) & 0x7FFFFFFFu);
+            top = max(top, __shfl_xor_sync(~0u, top, 1));
+            top = max(top, __shfl_xor_sync(~0u, top, 2));
+            const bool fine = top < 0x7F800000u;
+            const int e = fine ? max(0, (int)(top >> 23) - 2) : 255;
+            const float f = __uint_as_float((uint32_t)(254 - min(e, 253)) << 23);  // 2^(127 - e)
+            uint32_t word = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) word |= e2m1_pair(v[i][2 * k] * f, v[i][2 * k + 1] * f) << (8 * k);
+            if (!fine) word = 0;
+            // lane sub < 2 has values 8 sub .., lane sub + 2 those 16 further
+            // on, which share the bytes 8 sub ..: each makes four of them
+            const uint32_t other = __shfl_xor_sync(~0u, word, 2);
+            uint32_t lo = sub < 2 ? word : other >> 16, hi = sub < 2 ? other : word >> 16;
+            lo &= 0xFFFFu;
+            hi &= 0xFFFFu;
+            lo = (lo | lo << 8) & 0x00FF00FFu;
+            lo = (lo | lo << 4) & 0x0F0F0F0Fu;
+            hi = (hi | hi << 8) & 0x00FF00FFu;
+            hi = (hi | hi << 4) & 0x0F0F0F0Fu;
+            const uint32_t bytes = lo | hi << 4;
+            uint8_t* b = mine + (8 * i + (lane >> 2)) * MX_BYTES;
+            if (sub == 0) b[0] = (uint8_t)e;
+            b += 1 + 8 * (sub & 1) + 4 * (sub >> 1);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) b[k] = (uint8_t)(bytes >> (8 * k));
+        }
+        __syncwarp();
+        uint8_t* to = out + (int64_t)first * MX_BYTES;
+        if (first + RUN <= blocks) {
+            for (int i = lane; i < RUN_BYTES / 16; i += 32) reinterpret_cast<uint4*>(to)[i] = reinterpret_cast<uint4*>(mine)[i];
+        } else {
+            for (int i = lane; i < (int)(blocks - first) * MX_BYTES; i += 32) to[i] = mine[i];
+        }
+        __syncwarp();
+    }
+}
+
+// The eight codes of nibble half `high` of eight bytes as fp32 values.
+__device__ __forceinline__ void e2m1_values(uint2 bytes, bool high, float (&v)[8])
+{
+    const uint32_t w[2] = {(high ? bytes.x >> 4 : bytes.x) & 0x0F0F0F0Fu, (high ? bytes.y >> 4 : bytes.y) & 0x0F0F0F0Fu};
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t p = w[i] | w[i] >> 4;  // bytes 0 and 2: two codes each
+        uint32_t a, b;
+        asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %2;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b2;\n\t}"
+            : "=r"(a), "=r"(b)
+            : "r"(p));
+        const float2 f = __half22float2(*reinterpret_cast<__half2*>(&a)), g = __half22float2(*reinterpret_cast<__half2*>(&b));
+        v[4 * i] = f.x;
+        v[4 * i + 1] = f.y;
+        v[4 * i + 2] = g.x;
+        v[4 * i + 3] = g.y;
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(THREADS) dequantize_kernel(const uint8_t* __restrict__ in, T* y, int64_t ldy,
+                                                             uint32_t blocks, int nb, bool wide, int64_t rows,
+                                                             unsigned int* status)
+{
+    __shared__ __align__(16) uint8_t buf[THREADS / 32][RUN_BYTES + 16];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane & 3;
+    uint8_t* mine = buf[warp];
+    const uint32_t runs = (blocks + RUN - 1) / RUN;
+    for (uint32_t run = blockIdx.x * (THREADS / 32) + warp; run < runs; run += gridDim.x * (THREADS / 32)) {
+        const uint32_t first = run * RUN;
+        const uint8_t* from = in + (int64_t)first * MX_BYTES;
+        if (first + RUN <= blocks) {
+            for (int i = lane; i < RUN_BYTES / 16; i += 32)
+                reinterpret_cast<uint4*>(mine)[i] = ld_stream_v4(reinterpret_cast<const uint4*>(from) + i);
+        } else {
+            for (int i = lane; i < (int)(blocks - first) * MX_BYTES; i += 32) mine[i] = from[i];
+        }
+        __syncwarp();
+        RunAt at = run_at(first + (lane >> 2), nb);
+#pragma unroll
+        for (int i = 0; i < 4; ++i, at.next()) {
+            const int b = 8 * i + (lane >> 2);
+            if (first + b < blocks) {
+                const int o = b * MX_BYTES + 1 + 8 * (sub & 1);
+                const uint32_t* w = reinterpret_cast<const uint32_t*>(mine) + (o >> 2);
+                const int shift = 8 * (o & 3);
+                const uint2 bytes = make_uint2(__funnelshift_r(w[0], w[1], shift), __funnelshift_r(w[1], w[2], shift));
+                const float scale = mx_scale(mine[b * MX_BYTES]);
+                float v[8];
+                e2m1_values(bytes, sub >= 2, v);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] *= scale;
+                if (QG_OK(at.row < rows && qg_in((int64_t)at.col * 32 + sub * 8, 8, (int64_t)nb * 32), status, 301))
+                    store_values<8>(y + at.row * ldy + (int64_t)at.col * 32 + sub * 8, wide, v);
+            }
+        }
+        __syncwarp();
+    }
+}
+
+// One CTA a tile: the rows' largest scales, then the units, a warp a unit.
+__global__ void __launch_bounds__(128) pack_kernel(const uint8_t* __restrict__ canon, uint8_t* pack, MxLayout L,
+                                                   int64_t tiles, unsigned int* status)
+{
+    __shared__ int tops[MX_TILE_N];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nb = L.K / 32;
+    pdl_launch_dependents();
+    pdl_wait();
+    for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+        const int expert = (int)(tile / L.tiles()), n0 = (int)(tile % L.tiles()) * MX_TILE_N;
+        const uint8_t* rows = canon + ((int64_t)expert * L.N + n0) * nb * MX_BYTES;
+        uint8_t* to = pack + tile * L.tile_bytes();
+        {
+            const int r = threadIdx.x / 8;
+            int top = 0;
+            for (int b = threadIdx.x & 7; b < nb && n0 + r < L.N; b += 8)
+                top = max(top, (int)rows[((int64_t)r * nb + b) * MX_BYTES]);  // (255, a NaN, is the largest)
+            top = max(top, __shfl_xor_sync(~0u, top, 1));
+            top = max(top, __shfl_xor_sync(~0u, top, 2));
+            top = max(top, __shfl_xor_sync(~0u, top, 4));
+            if ((threadIdx.x & 7) == 0) tops[r] = top;
+        }
+        __syncthreads();
+        const int g = lane >> 2, t = lane & 3;
+        for (int u = warp; u < L.units(); u += 4) {
+            uint32_t word[4];
+            uint32_t scale = 127;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = g + 8 * (j & 1), b = 2 * u + (j >> 1);
+                word[j] = 0;
+                const bool there = n0 + r < L.N && b < nb;
+                const uint8_t* block = rows + ((int64_t)r * nb + b) * MX_BYTES;
+                if (there) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {  // value 4 t + k % 4 of the block's half k / 4
+                        const uint32_t c = (block[1 + 4 * t + (k & 3)] >> (k < 4 ? 0 : 4)) & 15u;
+                        word[j] |= c << (4 * (k / 2 + 4 * (k & 1)));
+                    }
+                }
+                if (j == t) scale = there ? (uint32_t)max(1, 127 - (tops[r] - (int)block[0])) : 127u;
+            }
+            uint8_t* unit = to + (int64_t)u * MX_UNIT_BYTES;
+            if (QG_OK(qg_in(unit - pack, MX_UNIT_BYTES, L.bytes()), status, 302)) {
+                reinterpret_cast<uint4*>(unit)[lane] = make_uint4(word[0], word[1], word[2], word[3]);
+                unit[MX_UNIT_CODES + lane] = (uint8_t)scale;
+            }
+        }
+        if (threadIdx.x < MX_TILE_N) to[(int64_t)L.units() * MX_UNIT_BYTES + threadIdx.x] = (uint8_t)tops[threadIdx.x];
+        __syncthreads();
+    }
+}
+
+template <typename T>
+bool rows_wide(const void* p, int64_t ld)
+{
+    return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * (int64_t)sizeof(T))) & 15u) == 0;
+}
+
+unsigned run_grid(const DeviceInfo& di, int64_t blocks)
+{
+    const int64_t per_cta = THREADS / 32 * RUN, grid = (blocks + per_cta - 1) / per_cta;
+    return (unsigned)(grid < (int64_t)di.sms * 8 ? grid : (int64_t)di.sms * 8);
+}
+
+template <typename T>
+int quantize_t(const void* x, int64_t ldx, void* blocks, int64_t N, int K, cudaStream_t s)
+{
+    const DeviceInfo di = device_info();
+    if (di.sms <= 0) return QGEMV_CUDA_ERROR;
+    const int nb = K / 32;
+    return launch_pdl(quantize_kernel<T>, dim3(run_grid(di, N * nb)), dim3(THREADS), 0, s, static_cast<const T*>(x), ldx,
+                      static_cast<uint8_t*>(blocks), (uint32_t)(N * nb), nb, rows_wide<T>(x, ldx), N,
+                      wait_timeout_counter()) == cudaSuccess
+               ? QGEMV_OK
+               : QGEMV_CUDA_ERROR;
+}
+
+template <typename T>
+int dequantize_t(const void* blocks, void* y, int64_t ldy, int64_t N, int K, cudaStream_t s)
+{
+    const DeviceInfo di = device_info();
+    if (di.sms <= 0) return QGEMV_CUDA_ERROR;
+    const int nb = K / 32;
+    return launch_pdl(dequantize_kernel<T>, dim3(run_grid(di, N * nb)), dim3(THREADS), 0, s,
+                      static_cast<const uint8_t*>(blocks), static_cast<T*>(y), ldy, (uint32_t)(N * nb), nb,
+                      rows_wide<T>(y, ldy), N, wait_timeout_counter()) == cudaSuccess
+               ? QGEMV_OK
+               : QGEMV_CUDA_ERROR;
+}
+
+}  // namespace
+
+int launch_quantize_mxfp4(int type, const void* x, int64_t ldx, void* blocks, int64_t N, int K, cudaStream_t s)
+{
+    if (type == QGEMV_F32) return quantize_t<float>(x, ldx, blocks, N, K, s);
+    if (type == QGEMV_F16) return quantize_t<__half>(x, ldx, blocks, N, K, s);
+    return quantize_t<__nv_bfloat16>(x, ldx, blocks, N, K, s);
+}
+
+int launch_dequantize_mxfp4(int type, const void* blocks, void* y, int64_t ldy, int64_t N, int K, cudaStream_t s)
+{
+    if (type == QGEMV_F32) return dequantize_t<float>(blocks, y, ldy, N, K, s);
+    if (type == QGEMV_F16) return dequantize_t<__half>(blocks, y, ldy, N, K, s);
+    return dequantize_t<__nv_bfloat16>(blocks, y, ldy, N, K, s);
+}
+
+int launch_qpack_mxfp4(const void* canon, void* pack, const MxLayout& L, cudaStream_t s)
+{
+    const int64_t tiles = (int64_t)L.experts * L.tiles();
+    return launch_pdl(pack_kernel, dim3((unsigned)(tiles < 65535 ? tiles : 65535)), dim3(128), 0, s,
+                      static_cast<const uint8_t*>(canon), static_cast<uint8_t*>(pack), L, tiles,
+                      wait_timeout_counter()) == cudaSuccess
+               ? QGEMV_OK
+               : QGEMV_CUDA_ERROR;
+}
+
+}  // namespace qgemv

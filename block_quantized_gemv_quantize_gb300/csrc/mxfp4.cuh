@@ -1,0 +1,101 @@
+// Microscaled 4-bit floating point (MXFP4) and the sparse layer's calls on it:
+// formats, layouts and launch arguments (include/qgemv.h has the definitions).
+#pragma once
+
+#include "kvcache.cuh"  // element types of rows
+
+namespace qgemv {
+
+constexpr int MX_BYTES = 17;        // a block: the scale byte, 16 bytes of codes
+constexpr int MX_UNIT_K = 64;       // values of a row in one unit of the pack
+constexpr int MX_TILE_N = 16;       // rows of a tile
+constexpr int MX_UNIT_CODES = MX_TILE_N * MX_UNIT_K / 2;
+constexpr int MX_UNIT_BYTES = MX_UNIT_CODES + MX_TILE_N * MX_UNIT_K / 32;  // codes, scale bytes
+constexpr int MX_MAX_K = 1 << 15, MX_MAX_N = 1 << 24, MX_MAX_EXPERTS = 1024, MX_MAX_TOP_K = 32;
+
+// The pack: [expert][tile of 16 rows], a tile being
+//   units  [K / 64][544 B], the last one filled up with zeros.  512 bytes of
+//          codes, 16 for each lane 4 g + t of a warp: four words, of row g in
+//          the unit's first block, row g + 8 there, row g in its second block,
+//          row g + 8 there.  A word has the block's values 4 t .. 4 t + 3 and
+//          16 + 4 t .. 16 + 4 t + 3, of which nibble i < 4 is the (2 i)th and
+//          nibble i + 4 the (2 i + 1)th.  Then 32 scale bytes [g][4] in the
+//          order of a lane's words: b for the scale 2^(b - 127) relative to
+//          the row's largest, 1 .. 127.
+//   tops   [16] bytes: the row's largest scale byte, 255 for a row that holds
+//          a NaN block
+// A lane's 16 bytes are its operands of four m16n8k16 products, if the K index
+// runs through a block in the order in which the words have it; and as pairs
+// (2 i, 2 i + 1) they are the fragments of a 16 x 256-bit store to tensor
+// memory with K in its own order.
+struct MxLayout {
+    int experts, N, K;
+    __host__ __device__ int tiles() const { return (N + MX_TILE_N - 1) / MX_TILE_N; }
+    __host__ __device__ int units() const { return (K + MX_UNIT_K - 1) / MX_UNIT_K; }
+    __host__ __device__ int64_t tile_bytes() const { return (int64_t)units() * MX_UNIT_BYTES + MX_TILE_N; }
+    __host__ __device__ int64_t expert_bytes() const { return tiles() * tile_bytes(); }
+    __host__ __device__ int64_t bytes() const { return experts * expert_bytes(); }
+};
+
+// The value of scale byte e (255: NaN).  2^-127 is subnormal.
+__device__ __forceinline__ float mx_scale(int e)
+{
+    return __uint_as_float(e == 0 ? 0x00400000u : (e == 255 ? 0x7FC00000u : (uint32_t)e << 23));
+}
+
+// v * 2^p in one rounding (p: -380 .. 380): two factors that are fp32 numbers.
+// A product that leaves the range does so as the exact one would.
+__device__ __forceinline__ float mul_pow2(float v, int p)
+{
+    // (the second factor takes what the first leaves, so that only one of the
+    // two products rounds: the first is exact where the second shrinks)
+    const int a = max(-126, min(127, p)), r = p - a, b = max(-126, min(127, r)), c = r - b;
+    float y = v * __uint_as_float((uint32_t)(a + 127) << 23) * __uint_as_float((uint32_t)(b + 127) << 23);
+    if (c) y *= __uint_as_float((uint32_t)(max(-126, min(127, c)) + 127) << 23);
+    return y;
+}
+
+int launch_quantize_mxfp4(int type, const void* x, int64_t ldx, void* blocks, int64_t N, int K, cudaStream_t s);
+int launch_dequantize_mxfp4(int type, const void* blocks, void* y, int64_t ldy, int64_t N, int K, cudaStream_t s);
+int launch_qpack_mxfp4(const void* canon, void* pack, const MxLayout& L, cudaStream_t s);
+
+// ---- router -------------------------------------------------------------------
+
+struct RouteArgs {
+    const void* logits;  // null: the ids are given
+    int64_t ld;
+    int32_t* ids;
+    float* weights;
+    int32_t* offsets;
+    int32_t* order;
+    int32_t* counts;  // workspace [CTAs][experts + 1]
+    int tokens, experts, top_k;
+    bool sigmoid, renormalize;
+    float scale;
+};
+
+size_t route_workspace_bytes(int64_t slots, int experts);
+int launch_route(int type, const RouteArgs& a, cudaStream_t s);
+
+// ---- the experts' products ------------------------------------------------------
+
+enum MxMode { MX_GEMM = 0, MX_GATE_UP = 1, MX_DOWN = 2 };
+
+struct MxArgs {
+    const uint8_t* w;   // the pack (gate's)
+    const uint8_t* w2;  // up's
+    MxLayout L;
+    const void* x;
+    int64_t ldx, ldy;
+    const int32_t* offsets;
+    const int32_t* order;  // null: slot i is row i
+    int slots, top_k;      // x's row of slot s is s / x_div
+    int x_div;
+    void* y;               // gemm, gate_up: [slots]; down: fp32 partial results [slots][N]
+};
+
+int launch_mx_gemm(int mode, int type, const MxArgs& a, cudaStream_t s);
+int launch_mx_combine(int type, const float* parts, const float* weights, void* out, int64_t ldo, int tokens,
+                      int top_k, int N, cudaStream_t s);
+
+}  // namespace qgemv

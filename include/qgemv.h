@@ -579,6 +579,117 @@ int attn_paged(int fmt, int type, const void* q, int64_t q_row, int64_t q_head, 
                void* out, int64_t o_row, int64_t o_head, float* lse, void* workspace, size_t ws_bytes, int batch,
                int rows, int n_heads, int n_kv_heads, int head_dim, float scale, int window, void* stream);
 
+/* ---- microscaled 4-bit floating point and the sparse layer on it ---------- */
+
+/* A mixture-of-experts layer in MXFP4 between the attention and the next layer:
+ *     moe_route            each token's experts and weights, the slots sorted
+ *     moe_gate_up_mxfp4    h[s] = silu(G_e x) * (U_e x)
+ *     moe_down_mxfp4       out[t] = sum_j weight[t][j] D_e h[t k + j]
+ * and qgemm_mxfp4, the product alone (one expert: a dense layer of any number
+ * of rows).  (Not from the pages.)
+ *
+ * MXFP4 (the microscaling formats' four-bit type): blocks of 32 values of one
+ * row, 17 bytes: a scale byte e, then 16 bytes of codes, value i < 16 in the
+ * low nibble of byte i, value i + 16 in its high nibble.  A code is a sign, two
+ * bits of exponent and one of mantissa (e2m1): 0, .5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives; the value is the code's times 2^(e - 127), NaN for e = 255.
+ *
+ * mxfp4_bytes - bytes of N rows of K values, N * (K/32) * 17; 0 for sizes that
+ * the calls refuse (N (K/32) beyond 2^31 - 1, K % 32, K outside 32 .. 32768).
+ * Host-only.
+ *
+ * quantize_mxfp4 - rows of fp32, fp16 or bf16 values into blocks:
+ *     e = 127 + floor(log2 max|x|) - 2, limited to 0 .. 254;
+ *     code = the one nearest to x / 2^(e - 127), of two equally near the one
+ *            with even mantissa, at most 6 in magnitude;
+ * a block of zeros has e = 0, one with a NaN or an infinity e = 255.  Exact in
+ * fp32, so the bytes are those of the definition.
+ *   x       rows of K values of `type`, row stride ldx >= K, aligned to their
+ *           element (16-byte aligned rows load faster).  Read.
+ *   blocks  uint8 [N][K/32][17] (written), 16-byte aligned
+ * dequantize_mxfp4 - the inverse: y[n][k] in `type`, one rounding.
+ * Errors: QGEMV_INVALID_ARG (null pointer, unknown type, ld < K, sizes out of
+ * range), QGEMV_UNSUPPORTED_SHAPE (K % 32), QGEMV_MISALIGNED. */
+size_t mxfp4_bytes(int64_t N, int K);
+int quantize_mxfp4(int type, const void* x, int64_t ldx, void* blocks, int64_t N, int K, void* stream);
+int dequantize_mxfp4(int type, const void* blocks, void* y, int64_t ldy, int64_t N, int K, void* stream);
+
+/* qpack_mxfp4 - reorder the blocks of `experts` weights of N rows of K values
+ * ([experts][N][K/32][17]) into the products' tiles: 16 rows x 64 values in
+ * tensor-core operand order, scales relative to the row's largest (one more
+ * than 2^126 below it counts as 2^-126 of it).  w_pack takes
+ * mxfp4_pack_bytes() bytes and must not alias w_canon.
+ *   experts 1 .. 1024;  N 1 .. 2^24;  K a multiple of 32, 32 .. 32768 */
+size_t mxfp4_pack_bytes(int experts, int N, int K);
+int qpack_mxfp4(const void* w_canon, void* w_pack, int experts, int N, int K, void* stream);
+
+/* moe_route - for each token, the top_k experts of largest logit in descending
+ * order, of equal logits the lowest (-0 == +0); a logit of minus infinity or
+ * NaN is none.  A place that no expert is left for gets id -1 and weight 0.
+ *   QGEMV_SOFTMAX  weight = e^l / sum over all experts' e^l
+ *   QGEMV_SIGMOID  weight = 1 / (1 + e^-l)
+ * then, with `renormalize`, divided by the token's sum of weights, and times
+ * `scale`; fp32.  Place j of token t is slot t * top_k + j.  The slots are
+ * also sorted by expert: order[offsets[e]] .. order[offsets[e + 1] - 1] are
+ * expert e's, ascending; from offsets[experts] on come the slots without an
+ * expert.  The result is the same on every call.
+ *   logits    rows of `experts` values of `type`, row stride ld >= experts
+ *   ids       int32 [tokens][top_k] (written);  weights fp32, the same
+ *   offsets   int32 [experts + 1] (written);  order int32 [tokens * top_k]
+ *   workspace moe_route_workspace_bytes() bytes, 16-byte aligned, with anything
+ *             in it (NULL where that is 0).  Calls that share it must not
+ *             overlap in time.
+ *   tokens >= 0;  experts 1 .. 1024;  top_k 1 .. 32, <= experts;
+ *   tokens * top_k <= 2^30;  scale finite
+ * moe_group - the sorting alone, of given ids [tokens][top_k] (one outside
+ * 0 .. experts - 1 is a slot without an expert; top_k 1 .. 32).
+ * Errors: QGEMV_INVALID_ARG, QGEMV_MISALIGNED, QGEMV_WORKSPACE_TOO_SMALL. */
+#define QGEMV_SOFTMAX 0
+#define QGEMV_SIGMOID 1
+size_t moe_route_workspace_bytes(int tokens, int experts, int top_k);
+int moe_route(int type, const void* logits, int64_t ld, int32_t* ids, float* weights, int32_t* offsets, int32_t* order,
+              void* workspace, size_t ws_bytes, int tokens, int experts, int top_k, int score, int renormalize,
+              float scale, void* stream);
+int moe_group(const int32_t* ids, int32_t* offsets, int32_t* order, void* workspace, size_t ws_bytes, int tokens,
+              int experts, int top_k, void* stream);
+
+/* The experts' products, e(s) being the expert whose range of `order` has slot
+ * s; a slot in no expert's range gets zeros:
+ *   qgemm_mxfp4        y[s] = W_e(s) x[s / top_k]
+ *   moe_gate_up_mxfp4  h[s] = silu(G_e(s) x[s / top_k]) * (U_e(s) x[s / top_k]),
+ *                      silu(g) = g / (1 + e^-g)
+ *   moe_down_mxfp4     out[t] = sum_j weights[t][j] W_e(s) h[s], s = t top_k + j
+ * Products run on the tensor cores on the codes themselves; sums are fp32, and
+ * there is one rounding to `type` at the end.  Rows of x enter with 22 bits or
+ * all of theirs, but to no less than 2^-38 of the row's largest finite
+ * magnitude.  The result is the same on every call with the same arguments.
+ *   w_*       packs (qpack_mxfp4) of `experts` weights of N rows of K values
+ *   x, h      rows of `type`, row stride ldx / ldh (read; h of gate_up and y
+ *             and out are written, and overlap nothing that is read): x has
+ *             `tokens` rows of K values, h of moe_down tokens * top_k
+ *   offsets, order  as moe_route writes them, read on the device; entries out
+ *             of range are cut or skipped, nothing outside the arrays is
+ *             touched.  order may be NULL where top_k is 1: slot i is then at
+ *             place i, the rows are sorted already.
+ *   weights   fp32 [tokens][top_k]
+ *   workspace *_workspace_bytes() bytes, 16-byte aligned, with anything in it
+ *             (NULL where that is 0).  Calls that share it must not overlap.
+ *   tokens >= 0;  top_k 1 .. 32;  tokens * top_k <= 2^30
+ * Errors: QGEMV_INVALID_ARG, QGEMV_UNSUPPORTED_SHAPE (K % 32),
+ * QGEMV_MISALIGNED, QGEMV_WORKSPACE_TOO_SMALL. */
+size_t qgemm_mxfp4_workspace_bytes(int type, int tokens, int top_k, int experts, int K, int N);
+size_t moe_gate_up_mxfp4_workspace_bytes(int type, int tokens, int top_k, int experts, int K, int N);
+size_t moe_down_mxfp4_workspace_bytes(int type, int tokens, int top_k, int experts, int K, int N);
+int qgemm_mxfp4(int type, const void* w_pack, const void* x, int64_t ldx, const int32_t* offsets, const int32_t* order,
+                void* y, int64_t ldy, void* workspace, size_t ws_bytes, int tokens, int top_k, int experts, int K, int N,
+                void* stream);
+int moe_gate_up_mxfp4(int type, const void* w_gate, const void* w_up, const void* x, int64_t ldx, const int32_t* offsets,
+                      const int32_t* order, void* h, int64_t ldh, void* workspace, size_t ws_bytes, int tokens, int top_k,
+                      int experts, int K, int N, void* stream);
+int moe_down_mxfp4(int type, const void* w_down, const void* h, int64_t ldh, const int32_t* offsets,
+                   const int32_t* order, const float* weights, void* out, int64_t ldo, void* workspace, size_t ws_bytes,
+                   int tokens, int top_k, int experts, int K, int N, void* stream);
+
 /* qgemv_q8_0_plan - the launch qgemv_q8_0 would make for this shape; writes
  * info[5] = {1, CTAs per cluster (the K parts), grid size, ring stages per
  * warp, blocks per job (8: a whole pack region; 4: half of one, taken where

@@ -66,7 +66,9 @@ size_t parts_bytes(int64_t slots, int N) { return ((size_t)slots * N * sizeof(fl
 size_t product_workspace(int mode, int type, int tokens, int top_k, int experts, int K, int N)
 {
     if (!known_type(type) || check_slots(tokens, top_k) || check_pack(experts, N, K)) return 0;
-    return mode == MX_DOWN ? parts_bytes((int64_t)tokens * top_k, N) : 0;
+    const int64_t slots = (int64_t)tokens * top_k;
+    return (mode == MX_DOWN ? parts_bytes(slots, N) : 0) +
+           (mx_many_rows(slots, experts) ? mx_planes_bytes(type, mode == MX_DOWN ? slots : tokens, K) : 0);
 }
 
 int product_call(int mode, int type, const void* w, const void* w2, const void* x, int64_t ldx, const int32_t* offsets,
@@ -102,6 +104,7 @@ int product_call(int mode, int type, const void* w, const void* w2, const void* 
     a.x_div = mode == MX_DOWN ? 1 : top_k;
     a.y = mode == MX_DOWN ? workspace : y;
     a.ldy = mode == MX_DOWN ? N : ldy;
+    a.planes = static_cast<uint8_t*>(workspace) + (mode == MX_DOWN ? parts_bytes(a.slots, N) : 0);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     st = launch_mx_gemm(mode, type, a, s);
     if (st || mode != MX_DOWN) return st;

@@ -79,6 +79,17 @@ int launch_mx_combine(int type, const float* parts, const float* weights, void* 
     return combine_t<__nv_bfloat16>(parts, weights, out, ldo, tokens, top_k, N, s);
 }
 
+bool mx_many_rows(int64_t slots, int experts)
+{
+    return slots >= 16 * (slots < experts ? slots : (int64_t)experts);
+}
+
+size_t mx_planes_bytes(int type, int64_t rows, int K)
+{
+    const int terms = type == QGEMV_F32 ? 3 : type == QGEMV_F16 ? 2 : 0;
+    return (size_t)terms * rows * ((K + MX_UNIT_K - 1) / MX_UNIT_K * MX_UNIT_K) * 2;
+}
+
 int launch_mx_gemm_f32(int mode, const MxArgs& a, cudaStream_t s);
 int launch_mx_gemm_f16(int mode, const MxArgs& a, cudaStream_t s);
 int launch_mx_gemm_bf16(int mode, const MxArgs& a, cudaStream_t s);

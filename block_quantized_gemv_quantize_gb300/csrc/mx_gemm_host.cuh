@@ -1,7 +1,7 @@
 // Launch plans of the experts' products.
 #pragma once
 
-#include "mx_gemm.cuh"
+#include "mx_gemm_tc.cuh"
 
 #include <algorithm>
 #include <mutex>
@@ -64,8 +64,49 @@ int launch_mxs(const MxArgs& a, cudaStream_t s)
 }
 
 template <typename T, int MODE>
+int launch_mxt(const MxArgs& a, cudaStream_t s)
+{
+    const DeviceInfo di = device_info();
+    int dev = 0;
+    if (di.sms <= 0 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return QGEMV_CUDA_ERROR;
+    auto kern = mxt_kernel<T, MODE>;
+    static std::once_flag once[64];
+    static bool ok[64];
+    static unsigned int* timeouts[64];
+    std::call_once(once[dev], [&]() {
+        timeouts[dev] = wait_timeout_counter();
+        ok[dev] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, di.smem_optin) == cudaSuccess &&
+                  timeouts[dev] != nullptr;
+        if (!ok[dev]) cudaGetLastError();
+    });
+    if (!ok[dev]) return QGEMV_CUDA_ERROR;
+    const auto wide = [](const void* p, int64_t bytes) { return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)bytes) & 15u) == 0; };
+    const bool x_wide = wide(a.x, a.ldx * (int64_t)sizeof(T));
+    MxtRows x;
+    if constexpr (MxtShape<T>::TERMS == 1) {
+        x = {static_cast<const __nv_bfloat16*>(a.x), a.ldx, 0, a.L.K, x_wide};
+    } else {
+        const int padded = a.L.units() * MX_UNIT_K;
+        const int64_t rows = a.slots / a.x_div, pieces = rows * (padded / 8), ctas = (pieces + 255) / 256;
+        x = {static_cast<const __nv_bfloat16*>(a.planes), padded, rows * padded, padded, true};
+        if (launch_pdl(mxt_planes_kernel<T>, dim3((unsigned)std::min<int64_t>(ctas, (int64_t)di.sms * 8)), dim3(256), 0, s,
+                       static_cast<const T*>(a.x), a.ldx, static_cast<uint16_t*>(a.planes), rows, a.L.K, padded, x_wide,
+                       timeouts[dev]) != cudaSuccess)
+            return QGEMV_CUDA_ERROR;
+    }
+    constexpr int GROUP = MODE == MX_GATE_UP ? 8 : 16, ROWS = MxtShape<T>::ROWS;
+    const int64_t groups = (a.L.tiles() + GROUP - 1) / GROUP;
+    const int64_t most = groups * std::min<int64_t>(a.slots, (int64_t)a.slots / ROWS + a.L.experts);
+    return launch_pdl(kern, dim3((unsigned)std::min<int64_t>(most, di.sms)), dim3(MXT_THREADS), mxt_smem<T>(a.L.experts), s,
+                      a, x, timeouts[dev]) == cudaSuccess
+               ? QGEMV_OK
+               : QGEMV_CUDA_ERROR;
+}
+
+template <typename T, int MODE>
 int launch_mx_mode(const MxArgs& a, cudaStream_t s)
 {
+    if (mx_many_rows(a.slots, a.L.experts)) return launch_mxt<T, MODE>(a, s);
     const double rows = (double)a.slots / (double)std::min<int64_t>(a.L.experts, a.slots);  // of an expert that has any, about
     if (rows <= 6.0) return launch_mxs<T, 1, MODE>(a, s);
     const int status = launch_mxs<T, 4, MODE>(a, s);

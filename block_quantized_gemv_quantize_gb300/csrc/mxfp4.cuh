@@ -92,7 +92,13 @@ struct MxArgs {
     int slots, top_k;      // x's row of slot s is s / x_div
     int x_div;
     void* y;               // gemm, gate_up: [slots]; down: fp32 partial results [slots][N]
+    void* planes;          // workspace for x in terms, where the type needs them (mx_planes_bytes)
 };
+
+// Whether a call's experts have many rows each (the tcgen05 kernel), about.
+bool mx_many_rows(int64_t slots, int experts);
+// Workspace of that kernel: rows of x as bf16 terms; 0 for bf16 rows.
+size_t mx_planes_bytes(int type, int64_t rows, int K);
 
 int launch_mx_gemm(int mode, int type, const MxArgs& a, cudaStream_t s);
 int launch_mx_combine(int type, const float* parts, const float* weights, void* out, int64_t ldo, int tokens,

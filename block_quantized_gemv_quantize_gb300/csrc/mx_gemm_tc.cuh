@@ -29,6 +29,7 @@ namespace qgemv {
 constexpr int MXT_THREADS = 512;
 constexpr int MXT_CONVERT = 8, MXT_EPI = 4, MXT_MMA_WARP = 12, MXT_LOAD_WARP = 13, MXT_LOAD = 3;
 constexpr int MXT_A_STAGES = 2;
+constexpr long long MXT_WAIT_CLOCKS = 2000000000;  // about a second
 
 template <typename T>
 struct MxtShape;
@@ -57,7 +58,7 @@ constexpr size_t mxt_smem(int experts)
 {
     using S = MxtShape<T>;
     return 1024 + (size_t)S::STAGES * S::TERMS * S::ROWS * 128 + 2 * S::ROWS * sizeof(void*) +
-           MXT_EPI * S::ROWS * sizeof(int) + (2 * S::STAGES + 2 * MXT_A_STAGES + 3) * sizeof(uint64_t) +
+           MXT_EPI * S::ROWS * sizeof(int64_t) + (2 * S::STAGES + 2 * MXT_A_STAGES + 3) * sizeof(uint64_t) +
            (size_t)(2 * (experts + 1) + 32 + 4) * sizeof(int);
 }
 
@@ -224,8 +225,8 @@ __global__ void __launch_bounds__(MXT_THREADS, 1) mxt_kernel(MxArgs a, MxtRows x
     uint64_t* full_b = reinterpret_cast<uint64_t*>(ptrs + 2 * ROWS);
     uint64_t *empty_b = full_b + STAGES, *full_a = empty_b + STAGES, *empty_a = full_a + MXT_A_STAGES;
     uint64_t *acc_full = empty_a + MXT_A_STAGES, *acc_empty = acc_full + 1, *all_done = acc_empty + 1;
-    int* epi_slots = reinterpret_cast<int*>(all_done + 1);
-    int* before = epi_slots + MXT_EPI * ROWS;
+    int64_t* epi_offs = reinterpret_cast<int64_t*>(all_done + 1);
+    int* before = reinterpret_cast<int*>(epi_offs + MXT_EPI * ROWS);
     int* start = before + a.L.experts + 1;
     int* sums = start + a.L.experts + 1;
     volatile int* gave_up = sums + 32;
@@ -274,10 +275,10 @@ __global__ void __launch_bounds__(MXT_THREADS, 1) mxt_kernel(MxArgs a, MxtRows x
     // A bounded wait; where one runs out, all roles stop.
     auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
         if (mbar_try_wait(bar, parity)) return true;
-        const uint64_t t0 = globaltimer_ns();
+        const long long t0 = clock64();  // (the wall clock's register takes longer to read than most waits)
         while (!mbar_try_wait(bar, parity)) {
             if (*gave_up) return false;
-            if (globaltimer_ns() - t0 > 1000000000ull) {
+            if (clock64() - t0 > MXT_WAIT_CLOCKS) {
                 *gave_up = 1;
                 if (lane == 0) atomicAdd_system(status, 1u);
                 return false;
@@ -475,60 +476,74 @@ __global__ void __launch_bounds__(MXT_THREADS, 1) mxt_kernel(MxArgs a, MxtRows x
     } else {
         // ---- results
         const int quad = warp & 3;
-        int* slots = epi_slots + quad * ROWS;
+        int64_t* offs = epi_offs + quad * ROWS;  // where the rows' outputs are, -1 for none
         const uint32_t from = tmem + ((uint32_t)(32 * quad) << 16);
         O* y = static_cast<O*>(a.y);
-        const int64_t extent = (int64_t)a.slots * a.ldy;
         uint32_t phase = 0;
         bool ok = true;
         for (bool more = walk.find(); more && ok; more = walk.next()) {
-            for (int r = lane; r < walk.cnt; r += 32) slots[r] = mxt_slot(a, walk.s0 + r);
-            const int row = quad * 32 + lane;  // of the accumulators
-            int n[2], e[2];
+            __syncwarp();
+            for (int r = lane; r < walk.n; r += 32) {
+                const int s = r < walk.cnt ? mxt_slot(a, walk.s0 + r) : -1;
+                offs[r] = s < 0 ? -1 : s * a.ldy;
+            }
+            int n[2];
+            float f[2][2];  // the row's power of two, in two factors
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                n[h] = walk.g * GROUP_TILES * MX_TILE_N + row + (MODE == MX_GATE_UP ? 0 : h * 128);
+                n[h] = walk.g * GROUP_TILES * MX_TILE_N + quad * 32 + lane + (MODE == MX_GATE_UP ? 0 : h * 128);
                 const uint8_t* w = MODE == MX_GATE_UP && h ? a.w2 : a.w;
-                e[h] = n[h] < a.L.N ? w[walk.e * a.L.expert_bytes() + (n[h] / MX_TILE_N) * a.L.tile_bytes() +
-                                        (int64_t)units * MX_UNIT_BYTES + n[h] % MX_TILE_N]
-                                    : 127;
+                const int e = n[h] < a.L.N ? w[walk.e * a.L.expert_bytes() + (n[h] / MX_TILE_N) * a.L.tile_bytes() +
+                                               (int64_t)units * MX_UNIT_BYTES + n[h] % MX_TILE_N]
+                                           : 127;
+                const int p = e - 127 + MXT_SHIFT;
+                f[h][0] = e == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(min(p, 127) + 127) << 23);
+                f[h][1] = __uint_as_float((uint32_t)(max(p - 127, 0) + 127) << 23);
             }
             __syncwarp();
             ok = __all_sync(~0u, wait(acc_full, phase));
             phase ^= 1;
             if (!ok) break;
             tc_fence_after();
-            auto value = [&](uint32_t bits, int h) {
-                return e[h] == 255 ? __uint_as_float(0x7FC00000u) : mul_pow2(__uint_as_float(bits), e[h] - 127 + MXT_SHIFT);
-            };
-            if constexpr (MODE == MX_GATE_UP) {
-                for (int c0 = 0; c0 < walk.n; c0 += 16) {
-                    uint32_t v[2][16];
-                    tc_ld_32x32b_x16(from + c0, v[0]);
-                    tc_ld_32x32b_x16(from + ROWS + c0, v[1]);
-                    tc_wait_ld();
+            // 16 columns a step, the next ones on their way from tensor memory meanwhile
+            auto store = [&](const uint32_t (&v)[16], const uint32_t (&v2)[16], int c0, int h) {
+                const bool mine = n[h] < a.L.N;
+                O* to = y + n[h];
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        if (c0 + c >= walk.cnt) break;
-                        const int s = slots[c0 + c];
-                        if (n[0] < a.L.N && s >= 0 && QG_OK(qg_in(s * a.ldy + n[0], 1, extent), status, 332))
-                            y[s * a.ldy + n[0]] = from_f32<O>(mx_silu(value(v[0][c], 0)) * value(v[1][c], 1));
-                    }
+                for (int c = 0; c < 16; ++c) {
+                    float o = __uint_as_float(v[c]) * f[h][0] * f[h][1];
+                    if constexpr (MODE == MX_GATE_UP) o = mx_silu(o) * (__uint_as_float(v2[c]) * f[1][0] * f[1][1]);
+                    const int64_t at = offs[c0 + c];
+                    if (mine && at >= 0 && QG_OK(qg_in(at + n[h], 1, (int64_t)a.slots * a.ldy), status, 332)) to[at] = from_f32<O>(o);
                 }
-            } else {
-                for (int h = 0; h < 2; ++h)
-                    for (int c0 = 0; c0 < walk.n; c0 += 16) {
-                        uint32_t v[16];
-                        tc_ld_32x32b_x16(from + h * ROWS + c0, v);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            if (c0 + c >= walk.cnt) break;
-                            const int s = slots[c0 + c];
-                            if (n[h] < a.L.N && s >= 0 && QG_OK(qg_in(s * a.ldy + n[h], 1, extent), status, 333))
-                                y[s * a.ldy + n[h]] = from_f32<O>(value(v[c], h));
-                        }
-                    }
+            };
+            const int steps = (MODE == MX_GATE_UP ? 1 : 2) * (walk.n / 16);
+            auto load = [&](int i, uint32_t (&v)[16], uint32_t (&v2)[16]) {
+                if constexpr (MODE == MX_GATE_UP) {
+                    tc_ld_32x32b_x16(from + 16 * i, v);
+                    tc_ld_32x32b_x16(from + ROWS + 16 * i, v2);
+                } else {
+                    const int h = i >= walk.n / 16;
+                    tc_ld_32x32b_x16(from + h * ROWS + 16 * (i - h * (walk.n / 16)), v);
+                }
+            };
+            auto put = [&](int i, const uint32_t (&v)[16], const uint32_t (&v2)[16]) {
+                const int h = MODE == MX_GATE_UP ? 0 : i >= walk.n / 16;
+                const int c0 = 16 * (i - h * (walk.n / 16));
+                if (h) store(v, v2, c0, 1);
+                else store(v, v2, c0, 0);
+            };
+            uint32_t va[16], va2[16], vb[16], vb2[16];
+            load(0, va, va2);
+            for (int i = 0; i < steps; i += 2) {
+                tc_wait_ld();
+                if (i + 1 < steps) load(i + 1, vb, vb2);
+                put(i, va, va2);
+                if (i + 1 < steps) {
+                    tc_wait_ld();
+                    if (i + 2 < steps) load(i + 2, va, va2);
+                    put(i + 1, vb, vb2);
+                }
             }
             tc_fence_before();
             __syncwarp();

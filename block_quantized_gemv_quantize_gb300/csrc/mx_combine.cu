@@ -86,7 +86,7 @@ bool mx_many_rows(int64_t slots, int experts)
 
 size_t mx_planes_bytes(int type, int64_t rows, int K)
 {
-    const int terms = type == QGEMV_F32 ? 3 : type == QGEMV_F16 ? 2 : 0;
+    const int terms = type == QGEMV_F32 ? 3 : type == QGEMV_F16 ? 2 : 1;
     return (size_t)terms * rows * ((K + MX_UNIT_K - 1) / MX_UNIT_K * MX_UNIT_K) * 2;
 }
 

@@ -80,27 +80,39 @@ int launch_mxt(const MxArgs& a, cudaStream_t s)
         if (!ok[dev]) cudaGetLastError();
     });
     if (!ok[dev]) return QGEMV_CUDA_ERROR;
-    const auto wide = [](const void* p, int64_t bytes) { return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)bytes) & 15u) == 0; };
-    const bool x_wide = wide(a.x, a.ldx * (int64_t)sizeof(T));
-    MxtRows x;
-    if constexpr (MxtShape<T>::TERMS == 1) {
-        x = {static_cast<const __nv_bfloat16*>(a.x), a.ldx, 0, a.L.K, x_wide};
-    } else {
-        const int padded = a.L.units() * MX_UNIT_K;
-        const int64_t rows = a.slots / a.x_div, pieces = rows * (padded / 8), ctas = (pieces + 255) / 256;
-        x = {static_cast<const __nv_bfloat16*>(a.planes), padded, rows * padded, padded, true};
+    // x itself where its rows are bf16 and aligned, bf16 terms of it in the workspace otherwise
+    constexpr int TERMS = MxtShape<T>::TERMS;
+    const int padded = a.L.units() * MX_UNIT_K;
+    const int64_t rows = a.slots / a.x_div;
+    const bool wide = ((reinterpret_cast<uintptr_t>(a.x) | (uintptr_t)(a.ldx * (int64_t)sizeof(T))) & 15u) == 0;
+    const bool direct = TERMS == 1 && wide;
+    const MxtRows x{static_cast<const __nv_bfloat16*>(direct ? a.x : a.planes), direct ? a.ldx : padded, rows * padded,
+                    direct ? a.L.K : padded};
+    if (!direct) {
+        const int64_t ctas = (rows * (padded / 8) + 255) / 256;
         if (launch_pdl(mxt_planes_kernel<T>, dim3((unsigned)std::min<int64_t>(ctas, (int64_t)di.sms * 8)), dim3(256), 0, s,
-                       static_cast<const T*>(a.x), a.ldx, static_cast<uint16_t*>(a.planes), rows, a.L.K, padded, x_wide,
+                       static_cast<const T*>(a.x), a.ldx, static_cast<uint16_t*>(a.planes), rows, a.L.K, padded, wide,
                        timeouts[dev]) != cudaSuccess)
             return QGEMV_CUDA_ERROR;
     }
-    constexpr int GROUP = MODE == MX_GATE_UP ? 8 : 16, ROWS = MxtShape<T>::ROWS;
+    constexpr int GROUP = MODE == MX_GATE_UP ? 8 : 16;
     const int64_t groups = (a.L.tiles() + GROUP - 1) / GROUP;
-    const int64_t most = groups * std::min<int64_t>(a.slots, (int64_t)a.slots / ROWS + a.L.experts);
-    return launch_pdl(kern, dim3((unsigned)std::min<int64_t>(most, di.sms)), dim3(MXT_THREADS), mxt_smem<T>(a.L.experts), s,
-                      a, x, timeouts[dev]) == cudaSuccess
-               ? QGEMV_OK
-               : QGEMV_CUDA_ERROR;
+    const int64_t most = groups * std::min<int64_t>(a.slots, (int64_t)a.slots / MXT_ROWS + a.L.experts);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2u * (unsigned)std::min<int64_t>(most, di.sms / 2));
+    cfg.blockDim = dim3(MXT_THREADS);
+    cfg.dynamicSmemBytes = mxt_smem<T>(a.L.experts);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 2;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, a, x, timeouts[dev]) == cudaSuccess ? QGEMV_OK : QGEMV_CUDA_ERROR;
 }
 
 template <typename T, int MODE>

@@ -1,83 +1,106 @@
 // Products of MXFP4 experts with many rows each (tcgen05 kernel).
 //
-// y[s][n] = sum_k w[n][k] x[s][k] with the weights as operand A (128 rows of
-// a tcgen05.mma, from tensor memory) and up to MXT_ROWS rows of x as operand B
-// (shared memory).  A code times its scale is a bf16 number exactly; rows of x
-// are one bf16 term (bf16), two (fp16) or three (fp32), which hold them
-// exactly, so that only the tensor core's fp32 sums round.  The codes come
-// from the pack's words with integer operations, one multiplication in pairs
-// for the scale, and go to tensor memory as fragments (16x256b): that operand
-// then costs no shared-memory bandwidth, which is what bounds such a kernel
-// with both operands there (64 KB a step of 256 x 192 x 64 for A alone).
+// y[s][n] = sum_k w[n][k] x[s][k] with the weights as operand A (256 rows of
+// a tcgen05.mma over a pair of SMs, from tensor memory) and up to MXT_ROWS
+// rows of x as operand B (half in each SM's shared memory).  A code times its
+// scale is a bf16 number exactly; rows of x are one bf16 term (bf16), two
+// (fp16) or three (fp32), which hold them exactly, so that only the tensor
+// core's fp32 sums round.  The codes come from the pack's words with integer
+// operations, one multiplication in pairs for the scale, and go to tensor
+// memory as fragments (16x256b): that operand costs no shared-memory bandwidth, and
+// the pair halves what the other one costs.
 //
 // Scales in A are relative to the row's largest and times 2^-20, so that the
 // sums stay in range wherever x is a bf16 number; the epilogue multiplies by
 // the row's power of two.
 //
-// A CTA an SM: 8 warps convert weights (each the 32 rows of its quadrant of
-// tensor memory), 3 gather rows of x into 128-byte-swizzled shared memory by asynchronous
-// copies, one thread issues the products, 4 warps write the results.  256 rows
-// of weights (128 of gate and of up) by one row tile is an item; items go
-// round-robin over CTAs, row tiles of an expert are of even size, N is the row
-// tile's count rounded up to 16.
+// In each CTA of a pair 8 warps convert weights (32 rows of tensor memory
+// each, every other unit), 3 gather rows of x by asynchronous copies into
+// 128-byte-swizzled shared memory (TMA's gather of four rows takes twice as long), 4 write
+// results while the next item's products run (two accumulators); one thread
+// of the first CTA issues the products for both.  256 rows of weights (128 of gate and of up,
+// 16 by 16, so that a warp has both of a row) by one row tile is an item;
+// items go round-robin over pairs, row tiles of an expert are of even size, N
+// is the row tile's count rounded up to 16.
 #pragma once
 
 #include "mx_gemm.cuh"
 
 namespace qgemv {
 
-constexpr int MXT_THREADS = 512;
 constexpr int MXT_CONVERT = 8, MXT_EPI = 4, MXT_MMA_WARP = 12, MXT_LOAD_WARP = 13, MXT_LOAD = 3;
-constexpr int MXT_A_STAGES = 2;
+constexpr int MXT_THREADS = (MXT_LOAD_WARP + MXT_LOAD) * 32;
+constexpr int MXT_ROWS = 160;    // of x an item: two accumulators of that many columns
+constexpr int MXT_A_STAGES = 3;  // of two units, 64 columns each: what hides a round trip between the roles
+constexpr uint32_t MXT_A_COL = 2 * MXT_ROWS;
+static_assert(MXT_A_COL + MXT_A_STAGES * 64 <= 512, "tensor memory");
 constexpr long long MXT_WAIT_CLOCKS = 2000000000;  // about a second
+constexpr int MXT_SHIFT = 20;                      // the scales in A are 2^-20 of what they are
 
+// Terms of a row of x; the ring for them: batches of steps, a step being half a
+// row tile of two units of 64 values.  A batch is announced and given back as
+// one: the fence between the copies' writes and the tensor core takes half a
+// thousand clocks.
 template <typename T>
 struct MxtShape;
 template <>
 struct MxtShape<__nv_bfloat16> {
-    static constexpr int TERMS = 1, ROWS = 192, STAGES = 7;
+    static constexpr int TERMS = 1, BATCH = 2, BATCHES = 5;
 };
 template <>
 struct MxtShape<__half> {
-    static constexpr int TERMS = 2, ROWS = 192, STAGES = 4;
+    static constexpr int TERMS = 2, BATCH = 1, BATCHES = 5;
 };
 template <>
 struct MxtShape<float> {
-    static constexpr int TERMS = 3, ROWS = 128, STAGES = 4;
+    static constexpr int TERMS = 3, BATCH = 1, BATCHES = 3;
 };
 
 struct MxtRows {
-    const __nv_bfloat16* x;  // row r of term i at x + i * plane + r * ld
+    const __nv_bfloat16* x;  // row r of term i at x + i * plane + r * ld, 16-byte aligned
     int64_t ld, plane;
     int values;  // of a row that are there
-    bool wide;
 };
 
 template <typename T>
 constexpr size_t mxt_smem(int experts)
 {
     using S = MxtShape<T>;
-    return 1024 + (size_t)S::STAGES * S::TERMS * S::ROWS * 128 + 2 * S::ROWS * sizeof(void*) +
-           MXT_EPI * S::ROWS * sizeof(int64_t) + (2 * S::STAGES + 2 * MXT_A_STAGES + 3) * sizeof(uint64_t) +
+    return 1024 + (size_t)S::BATCHES * S::BATCH * 2 * S::TERMS * (MXT_ROWS / 2) * 128 +
+           (2 * S::BATCHES + 2 * MXT_A_STAGES + 5) * sizeof(uint64_t) + MXT_EPI * MXT_ROWS * sizeof(int64_t) +
            (size_t)(2 * (experts + 1) + 32 + 4) * sizeof(int);
 }
 
-// ---- tcgen05 --------------------------------------------------------------------
+// ---- tcgen05, clusters, TMA --------------------------------------------------------
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-__device__ __forceinline__ void tc_commit(uint64_t* bar)
+// The warp's one thread that issues for it (the others run along, which keeps
+// the operands in uniform registers).
+__device__ __forceinline__ bool elected()
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
 }
 
-__device__ __forceinline__ void tc_mma_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add)
+// Arrives at the barrier of both CTAs once what this thread has issued is done.
+__device__ __forceinline__ void tc_commit_both(uint32_t bar, bool on)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+        "h"((uint16_t)3), "r"((uint32_t)on)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_f16(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add, bool on)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add), "r"((uint32_t)on)
         : "memory");
 }
 
@@ -112,9 +135,37 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t smem)
            (uint64_t)2 << 61;
 }
 
-// D fp32, A and B bf16, both K-major, 128 x n.
-__device__ __forceinline__ uint32_t tc_idesc(int n) { return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(n >> 3) << 17 | 8u << 24; }
+// D fp32, A and B bf16, both K-major, 256 x n.
+__device__ __forceinline__ uint32_t tc_idesc(int n) { return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(n >> 3) << 17 | 16u << 24; }
 
+__device__ __forceinline__ uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_at(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+// One arrival at that barrier of the pair's first CTA.
+__device__ __forceinline__ void arrive_first(uint64_t* bar)
+{
+    asm volatile(
+        "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, 0;\n\t"
+        "mbarrier.arrive.shared::cluster.b64 _, [r];\n\t}" ::"r"(smem_u32(bar))
+        : "memory");
+}
 // A word's eight codes, times a scale (in both halves), as four pairs of bf16.
 __device__ __forceinline__ void e2m1_bf16(uint32_t w, uint32_t scale, uint32_t& p0, uint32_t& p1, uint32_t& p2, uint32_t& p3)
 {
@@ -127,8 +178,6 @@ __device__ __forceinline__ void e2m1_bf16(uint32_t w, uint32_t scale, uint32_t& 
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(p2) : "r"(t2), "r"(scale));
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(p3) : "r"(t3), "r"(scale));
 }
-
-constexpr int MXT_SHIFT = 20;  // the scales in A are 2^-20 of what they are
 
 // ---- rows of x as bf16 terms ------------------------------------------------------
 
@@ -179,7 +228,7 @@ __global__ void __launch_bounds__(256) mxt_planes_kernel(const T* __restrict__ x
 // An item: a row tile and a group of weight tiles.  Every role walks the same ones.
 struct MxtWalk {
     const int *before, *start;
-    int rows_most, groups;
+    int groups;
     int64_t item, items;
     int step;
     int e, g, s0, cnt, n;  // expert, group, first place, rows, rows rounded up to 16
@@ -191,7 +240,7 @@ struct MxtWalk {
         while (rt >= before[e + 1]) ++e;
         const int first = start[e], all = start[e + 1] - first;
         const int tiles = before[e + 1] - before[e];
-        const int each = min(rows_most, ((all + tiles - 1) / tiles + 15) & ~15);
+        const int each = min(MXT_ROWS, ((all + tiles - 1) / tiles + 15) & ~15);
         s0 = first + (rt - before[e]) * each;
         cnt = min(each, first + all - s0);
         n = (cnt + 15) & ~15;
@@ -204,6 +253,20 @@ struct MxtWalk {
     }
 };
 
+// A place in a ring of N stages; `phase` is the parity that a wait for its data wants.
+template <int N>
+struct MxtStage {
+    int i = 0;
+    uint32_t phase = 0;
+    __device__ void next()
+    {
+        if (++i == N) {
+            i = 0;
+            phase ^= 1;
+        }
+    }
+};
+
 __device__ __forceinline__ int mxt_slot(const MxArgs& a, int place)
 {
     const int s = a.order ? a.order[place] : place;
@@ -211,100 +274,112 @@ __device__ __forceinline__ int mxt_slot(const MxArgs& a, int place)
 }
 
 template <typename T, int MODE>
-__global__ void __launch_bounds__(MXT_THREADS, 1) mxt_kernel(MxArgs a, MxtRows x, unsigned int* status)
+__global__ void __launch_bounds__(MXT_THREADS, 1)
+    mxt_kernel(MxArgs a, MxtRows x, unsigned int* status)
 {
     using S = MxtShape<T>;
     using O = typename std::conditional<MODE == MX_DOWN, float, T>::type;
-    constexpr int ROWS = S::ROWS, TERMS = S::TERMS, STAGES = S::STAGES, LAG = STAGES - 2;
-    constexpr int STAGE_BYTES = TERMS * ROWS * 128;
-    constexpr uint32_t A_COL = 2 * ROWS;  // tensor memory: two accumulators of ROWS columns, then the stages of A
-    static_assert(A_COL + MXT_A_STAGES * 64 <= 512, "tensor memory");
+    constexpr int TERMS = S::TERMS, BATCH = S::BATCH, BATCHES = S::BATCHES;
+    constexpr int TERM_BYTES = MXT_ROWS / 2 * 128, UNIT_BYTES = TERMS * TERM_BYTES, STEP_BYTES = 2 * UNIT_BYTES;
     extern __shared__ uint8_t sm_raw[];
     uint8_t* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
-    const __nv_bfloat16** ptrs = reinterpret_cast<const __nv_bfloat16**>(sm + STAGES * STAGE_BYTES);
-    uint64_t* full_b = reinterpret_cast<uint64_t*>(ptrs + 2 * ROWS);
-    uint64_t *empty_b = full_b + STAGES, *full_a = empty_b + STAGES, *empty_a = full_a + MXT_A_STAGES;
-    uint64_t *acc_full = empty_a + MXT_A_STAGES, *acc_empty = acc_full + 1, *all_done = acc_empty + 1;
+    uint64_t* full_b = reinterpret_cast<uint64_t*>(sm + BATCHES * BATCH * STEP_BYTES);
+    uint64_t *empty_b = full_b + BATCHES, *full_a = empty_b + BATCHES;
+    uint64_t *empty_a = full_a + MXT_A_STAGES, *acc_full = empty_a + MXT_A_STAGES, *acc_empty = acc_full + 2;
+    uint64_t* all_done = acc_empty + 2;
     int64_t* epi_offs = reinterpret_cast<int64_t*>(all_done + 1);
-    int* before = reinterpret_cast<int*>(epi_offs + MXT_EPI * ROWS);
+    int* before = reinterpret_cast<int*>(epi_offs + MXT_EPI * MXT_ROWS);
     int* start = before + a.L.experts + 1;
     int* sums = start + a.L.experts + 1;
     volatile int* gave_up = sums + 32;
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(sums + 33);
 
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
+    const uint32_t rank = cluster_rank();
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
-        for (int i = 0; i < STAGES; ++i) {
+        for (int i = 0; i < BATCHES; ++i) {
             mbar_init(full_b + i, MXT_LOAD);
             mbar_init(empty_b + i, 1);
         }
         for (int i = 0; i < MXT_A_STAGES; ++i) {
-            mbar_init(full_a + i, MXT_CONVERT);
+            mbar_init(full_a + i, 2 * MXT_CONVERT);
             mbar_init(empty_a + i, 1);
         }
-        mbar_init(acc_full, 1);
-        mbar_init(acc_empty, MXT_EPI);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(acc_full + i, 1);
+            mbar_init(acc_empty + i, 2 * MXT_EPI);
+        }
         mbar_init(all_done, 1);
         fence_barrier_init();
         *gave_up = 0;
     }
     if (warp == MXT_MMA_WARP) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_at)) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_at)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
         tc_fence_before();
     }
     pdl_wait();
-    const int n_rt = mx_row_tiles<MXT_THREADS>(a, ROWS, before, start, sums);  // (ends with a barrier)
+    const int n_rt = mx_row_tiles<MXT_THREADS>(a, MXT_ROWS, before, start, sums);
+    cluster_barrier();  // both CTAs' barriers and tensor memory are there
     tc_fence_after();
     const uint32_t tmem = *tmem_at;
     mx_zero_rest(a, static_cast<O*>(a.y), status);
 
-    constexpr int GROUP_TILES = MODE == MX_GATE_UP ? 8 : 16;
-    const int units = a.L.units(), tiles = a.L.tiles();
+    constexpr int GROUP_TILES = MODE == MX_GATE_UP ? 8 : 16;  // of a pair
+    const int units = a.L.units(), steps = (units + 1) / 2, tiles = a.L.tiles();
     MxtWalk walk;
     walk.before = before;
     walk.start = start;
-    walk.rows_most = ROWS;
     walk.groups = (tiles + GROUP_TILES - 1) / GROUP_TILES;
     walk.items = (int64_t)n_rt * walk.groups;
-    walk.item = blockIdx.x;
-    walk.step = gridDim.x;
+    walk.item = blockIdx.x / 2;
+    walk.step = gridDim.x / 2;
     walk.e = 0;
 
-    // A bounded wait; where one runs out, all roles stop.
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        if (mbar_try_wait(bar, parity)) return true;
-        const long long t0 = clock64();  // (the wall clock's register takes longer to read than most waits)
-        while (!mbar_try_wait(bar, parity)) {
-            if (*gave_up) return false;
-            if (clock64() - t0 > MXT_WAIT_CLOCKS) {
-                *gave_up = 1;
-                if (lane == 0) atomicAdd_system(status, 1u);
-                return false;
+    // A bounded wait (by the SM's clock: the wall clock's register takes longer
+    // to read than most waits); where one runs out, all roles of the CTA stop,
+    // and with them the other CTA's, whose waits run out then.
+    auto wait_at = [&](uint32_t bar, uint32_t parity) -> bool {
+        bool ok = mbar_try_wait_at(bar, parity);
+        if (!ok) {
+            const long long t0 = clock64();
+            while (!(ok = mbar_try_wait_at(bar, parity))) {
+                if (*gave_up) break;
+                if (clock64() - t0 > MXT_WAIT_CLOCKS) {
+                    *gave_up = 1;
+                    if (lane == 0) atomicAdd_system(status, 1u);
+                    break;
+                }
             }
         }
-        return true;
+        return __all_sync(~0u, ok);
+    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return wait_at(smem_u32(bar), parity); };
+    // The 16-row tile of this CTA's rows 32 quad + 16 i, and its place in the weight's tiles.
+    auto weight = [&](int i) { return MODE == MX_GATE_UP && i ? a.w2 : a.w; };
+    auto tile_of = [&](int quad, int i) {
+        return walk.g * GROUP_TILES + (int)rank * (GROUP_TILES / 2) + (MODE == MX_GATE_UP ? quad : 2 * quad + i);
     };
 
     if (warp < MXT_CONVERT) {
-        // ---- weights into tensor memory
-        const int quad = warp & 3, half = warp >> 2, g = lane >> 2;
-        const uint8_t* w = MODE == MX_GATE_UP && half ? a.w2 : a.w;
-        const int tile0 = (MODE == MX_GATE_UP ? 0 : half * 8) + quad * 2;
-        const uint32_t to = tmem + A_COL + half * 32 + ((uint32_t)(32 * quad) << 16);
-        constexpr int AHEAD = 3;
+        // ---- weights into tensor memory: four warps take a step's first unit, four its second
+        const int quad = warp & 3, odd = warp >> 2, g = lane >> 2;
+        const uint32_t to = tmem + MXT_A_COL + 32 * odd + ((uint32_t)(32 * quad) << 16);
+        constexpr int AHEAD = 2;  // steps on their way from global memory
         uint4 code[AHEAD][2];
         uint32_t scale[AHEAD][2];
         bool more = walk.find();
-        int64_t left = more ? (walk.items - walk.item + walk.step - 1) / walk.step * units : 0;  // steps
-        int u = 0;
-        const uint8_t* from[2] = {nullptr, nullptr};
+        int64_t left = more ? (walk.items - walk.item + walk.step - 1) / walk.step * steps : 0;
+        int u = odd;
+        const uint8_t* from[2];
+        bool there[2];
         auto locate = [&]() {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int tile = walk.g * GROUP_TILES + tile0 + i;
-                from[i] = tile < tiles ? w + walk.e * a.L.expert_bytes() + tile * a.L.tile_bytes() : nullptr;
+                const int tile = tile_of(quad, i);
+                there[i] = tile < tiles;
+                from[i] = weight(i) + walk.e * a.L.expert_bytes() + (there[i] ? tile : 0) * a.L.tile_bytes() + odd * MX_UNIT_BYTES;
             }
         };
         auto fetch = [&](uint4 (&c)[2], uint32_t (&s)[2]) {
@@ -313,23 +388,25 @@ __global__ void __launch_bounds__(MXT_THREADS, 1) mxt_kernel(MxArgs a, MxtRows x
             for (int i = 0; i < 2; ++i) {
                 c[i] = make_uint4(0, 0, 0, 0);
                 s[i] = 0x7F7F7F7Fu;
-                const uint8_t* p = from[i] + (int64_t)u * MX_UNIT_BYTES;
-                if (from[i] && QG_OK(qg_in(p - w, MX_UNIT_BYTES, a.L.bytes()), status, 331)) {
-                    c[i] = __ldg(reinterpret_cast<const uint4*>(p) + lane);
-                    s[i] = __ldg(reinterpret_cast<const uint32_t*>(p + MX_UNIT_CODES) + g);
+                if (there[i] && u < units && QG_OK(qg_in(from[i] - weight(i), MX_UNIT_BYTES, a.L.bytes()), status, 331)) {
+                    c[i] = __ldg(reinterpret_cast<const uint4*>(from[i] + lane * 16));
+                    s[i] = __ldg(reinterpret_cast<const uint32_t*>(from[i] + MX_UNIT_CODES + g * 4));
                 }
+                from[i] += 2 * MX_UNIT_BYTES;
             }
-            if (++u == units) {
-                u = 0;
+            u += 2;
+            if (u >= 2 * steps) {
+                u = odd;
                 more = walk.next();
                 if (more) locate();
             }
         };
         if (more) locate();
 #pragma unroll
-        for (int i = 0; i < AHEAD; ++i) fetch(code[i], scale[i]);
-        int stage = 0;
-        uint32_t phase = 1;
+        for (int j = 0; j < AHEAD; ++j) fetch(code[j], scale[j]);
+        MxtStage<MXT_A_STAGES> st;
+        MxtStage<BATCHES> b;
+        int in = 0;
         bool ok = true;
         while (left > 0 && ok) {
 #pragma unroll
@@ -341,145 +418,143 @@ __global__ void __launch_bounds__(MXT_THREADS, 1) mxt_kernel(MxArgs a, MxtRows x
                     const uint32_t wd[4] = {code[j][i].x, code[j][i].y, code[j][i].z, code[j][i].w};
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {  // rows g and g + 8 of the first block, then of the second
-                        // 2^(b - 127) 2^126 2^-20 as bf16
-                        const uint32_t e = ((scale[j][i] >> (8 * k) & 255u) + 126 - MXT_SHIFT) << 7;
+                        // 2^(b - 127) 2^126 2^-20 as bf16, in both halves
+                        const uint32_t e = (__byte_perm(scale[j][i], 0, 0x4040 + 0x0101 * k) + (126 - MXT_SHIFT) * 0x10001u) << 7;
                         const int o = 8 * (k >> 1) + 2 * (k & 1);
-                        e2m1_bf16(wd[k], e | e << 16, r[i][o], r[i][o + 1], r[i][o + 4], r[i][o + 5]);
+                        e2m1_bf16(wd[k], e, r[i][o], r[i][o + 1], r[i][o + 4], r[i][o + 5]);
                     }
                 }
                 fetch(code[j], scale[j]);
-                ok = wait(empty_a + stage, phase);
-                ok = __all_sync(~0u, ok);
+                ok = wait(empty_a + st.i, st.phase ^ 1);
                 if (!ok) break;
                 tc_fence_after();
-                tc_st_16x256b_x4(to + stage * 64, r[0]);
-                tc_st_16x256b_x4(to + stage * 64 + (16u << 16), r[1]);
+                tc_st_16x256b_x4(to + st.i * 64, r[0]);
+                tc_st_16x256b_x4(to + st.i * 64 + (16u << 16), r[1]);
                 tc_wait_st();
                 tc_fence_before();
-                __syncwarp();
-                if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(full_a + stage)) : "memory");
-                if (++stage == MXT_A_STAGES) {
-                    stage = 0;
-                    phase ^= 1;
+                // one of the eight announces the rows of x too, which came long ago
+                if (warp == 0 && in == 0) {
+                    ok = wait(full_b + b.i, b.phase);
+                    if (!ok) break;
+                    b.next();
                 }
+                if (++in == BATCH) in = 0;
+                __syncwarp();
+                if (lane == 0) arrive_first(full_a + st.i);
+                st.next();
                 --left;
             }
         }
     } else if (warp >= MXT_LOAD_WARP) {
-        // ---- rows of x into shared memory
+        // ---- rows of x into shared memory: this CTA's half of a row tile, a 16-byte piece of every 16th row a thread
+        constexpr int STEP = MXT_LOAD * 4, EACH = (MXT_ROWS / 2 + STEP - 1) / STEP, LAG = BATCHES - 2;
         const int id = threadIdx.x - MXT_LOAD_WARP * 32, c = id & 7, r0 = id >> 3;
-        constexpr int STEP = MXT_LOAD * 32 / 8;
-        int stage = 0, flip = 0, issued = 0, told = 0;
-        uint32_t phase = 1;
+        static_assert(STEP % 8 == 4, "every other row: the swizzle's other half");
+        const uint32_t at[2] = {smem_u32(sm) + r0 * 128 + ((c ^ (r0 & 7)) << 4), smem_u32(sm) + r0 * 128 + ((c ^ (r0 & 7) ^ 4) << 4)};
+        const int64_t plane = x.plane * 2;
+        MxtStage<BATCHES> st, told;
+        int in = 0, issued = 0;  // steps of the batch, batches not yet announced
         bool ok = true;
-        auto tell = [&]() {  // the oldest stage not yet announced has landed
+        auto tell = [&]() {  // the oldest of them has landed
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0)
-                asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(full_b + told)) : "memory");
-            if (++told == STAGES) told = 0;
+            if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(full_b + told.i)) : "memory");
+            told.next();
             --issued;
         };
         for (bool more = walk.find(); more && ok; more = walk.next()) {
-            const __nv_bfloat16** rows = ptrs + flip * ROWS;
-            flip ^= 1;
-            for (int r = id; r < walk.n; r += MXT_LOAD * 32) {  // (rows behind the last repeat it and go nowhere)
-                const int s = mxt_slot(a, walk.s0 + min(r, walk.cnt - 1));
-                rows[r] = x.x + (int64_t)(max(0, s) / a.x_div) * x.ld;
+            const int half = walk.n / 2;
+            const uint8_t* from[EACH];
+#pragma unroll
+            for (int j = 0; j < EACH; ++j) {  // (rows behind the last repeat it and go nowhere)
+                const int place = walk.s0 + min((int)rank * half + r0 + j * STEP, walk.cnt - 1);
+                from[j] = reinterpret_cast<const uint8_t*>(x.x + (int64_t)(max(0, mxt_slot(a, place)) / a.x_div) * x.ld + c * 8);
             }
-            asm volatile("bar.sync 1, %0;" ::"n"(MXT_LOAD * 32) : "memory");
-            for (int u = 0; u < units && ok; ++u) {
-                ok = __all_sync(~0u, wait(empty_b + stage, phase));
+            for (int u = 0; u < units; ++u) {
+                if (in == 0 && u % 2 == 0) ok = wait(empty_b + st.i, st.phase ^ 1);
                 if (!ok) break;
-                uint8_t* to = sm + stage * STAGE_BYTES;
-                const int k = u * MX_UNIT_K + c * 8;
-                const bool there = k < x.values;
-#pragma unroll 4
-                for (int r = r0; r < walk.n; r += STEP) {
-                    const __nv_bfloat16* p = rows[r] + k;
-                    uint8_t* at = to + r * 128 + ((c ^ (r & 7)) << 4);
+                const uint32_t unit = (st.i * BATCH + in) * STEP_BYTES + (u & 1) * UNIT_BYTES;
+                const int bytes = u * MX_UNIT_K + c * 8 < x.values ? 16 : 0;  // (zeros behind a row, nothing read)
+                const uint32_t to[2] = {at[0] + unit, at[1] + unit};
 #pragma unroll
-                    for (int i = 0; i < TERMS; ++i) {
-                        if (x.wide) {
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(at + i * ROWS * 128)),
-                                         "l"(there ? p + i * x.plane : x.x), "r"(there ? 16 : 0)
+                for (int j = 0; j < EACH; ++j) {
+                    if (r0 + j * STEP < half)
+#pragma unroll
+                        for (int i = 0; i < TERMS; ++i)
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to[j & 1] + j * STEP * 128 + i * TERM_BYTES),
+                                         "l"(from[j] + i * plane), "r"(bytes)
                                          : "memory");
-                        } else {
-                            uint32_t v[4];
-#pragma unroll
-                            for (int m = 0; m < 4; ++m) {
-                                const uint16_t* q = reinterpret_cast<const uint16_t*>(p + i * x.plane) + 2 * m;
-                                v[m] = there ? (uint32_t)q[0] | (uint32_t)q[1] << 16 : 0u;
-                            }
-                            *reinterpret_cast<uint4*>(at + i * ROWS * 128) = make_uint4(v[0], v[1], v[2], v[3]);
-                        }
+                    from[j] += 2 * MX_UNIT_K;
+                }
+                if ((u & 1) == 0 && u + 1 < units) continue;
+                if (++in == BATCH) {
+                    in = 0;
+                    cp_async_commit();
+                    st.next();
+                    if (++issued > LAG) {
+                        cp_async_wait<LAG>();
+                        tell();
                     }
-                }
-                cp_async_commit();
-                if (++stage == STAGES) {
-                    stage = 0;
-                    phase ^= 1;
-                }
-                if (++issued > LAG) {
-                    cp_async_wait<LAG>();
-                    tell();
                 }
             }
         }
+        cp_async_commit();
+        if (in) ++issued;  // (a last batch that is not full)
         cp_async_wait<0>();
         while (issued > 0) tell();
     } else if (warp == MXT_MMA_WARP) {
-        // ---- products
-        int sa = 0, sb = 0;
-        uint32_t pa = 0, pb = 0, pe = 1;
-        bool ok = true;
-        for (bool more = walk.find(); more && ok; more = walk.next()) {
-            const uint32_t idesc = tc_idesc(walk.n);
-            ok = __all_sync(~0u, wait(acc_empty, pe));
-            pe ^= 1;
-            for (int u = 0; u < units && ok; ++u) {
-                ok = wait(full_b + sb, pb) && wait(full_a + sa, pa);
-                ok = __all_sync(~0u, ok);
-                if (!ok) break;
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint64_t b = tc_desc(smem_u32(sm + sb * STAGE_BYTES));
-                    const uint32_t at = tmem + A_COL + sa * 64;
+        // ---- products: a wait, eight products and a commit or two a step
+        if (rank == 0) {
+            const bool on = elected();
+            const uint32_t full = smem_u32(full_a), empty = smem_u32(empty_a), spent = smem_u32(empty_b), done = smem_u32(acc_full);
+            const uint64_t b0 = tc_desc(smem_u32(sm));
+            MxtStage<BATCHES> sb;
+            MxtStage<MXT_A_STAGES> sa;
+            MxtStage<2> acc;
+            int in = 0;
+            bool ok = true;
+            for (bool more = walk.find(); more && ok; more = walk.next()) {
+                const uint32_t idesc = tc_idesc(__shfl_sync(~0u, walk.n, 0)), d = tmem + acc.i * MXT_ROWS;
+                ok = wait(acc_empty + acc.i, acc.phase ^ 1);
+                uint32_t add = 0;
+                for (int u = 0; u < units && ok; u += 2) {
+                    ok = wait_at(full + 8 * sa.i, sa.phase);  // of both CTAs, and their rows of x
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t b = b0 + (uint64_t)((sb.i * BATCH + in) * (STEP_BYTES / 16));
+                    const uint32_t at = tmem + MXT_A_COL + sa.i * 64;
 #pragma unroll
-                    for (int i = 0; i < TERMS; ++i)
+                    for (int h = 0; h < 2; ++h)
+                        if (h == 0 || u + 1 < units) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
+                            for (int i = 0; i < TERMS; ++i)
 #pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                tc_mma_f16(tmem + h * ROWS, at + h * 32 + k * 8,
-                                           b + (uint64_t)(i * (ROWS * 128 / 16) + k * 2), idesc, u > 0 || i > 0 || k > 0);
-                    tc_commit(empty_b + sb);
-                    tc_commit(empty_a + sa);
+                                for (int k = 0; k < 4; ++k) {
+                                    tc_mma_f16(d, at + h * 32 + k * 8, b + (uint64_t)(h * (UNIT_BYTES / 16) + i * (TERM_BYTES / 16) + k * 2),
+                                               idesc, add, on);
+                                    add = 1;
+                                }
+                        }
+                    tc_commit_both(empty + 8 * sa.i, on);
+                    if (++in == BATCH) {
+                        in = 0;
+                        tc_commit_both(spent + 8 * sb.i, on);
+                        sb.next();
+                    }
+                    sa.next();
                 }
-                __syncwarp();
-                if (++sb == STAGES) {
-                    sb = 0;
-                    pb ^= 1;
-                }
-                if (++sa == MXT_A_STAGES) {
-                    sa = 0;
-                    pa ^= 1;
-                }
+                if (ok) tc_commit_both(done + 8 * acc.i, on);
+                acc.next();
             }
-            if (ok && lane == 0) tc_commit(acc_full);
-            __syncwarp();
         }
-        // what was issued ends before tensor memory is given back
-        if (lane == 0) tc_commit(all_done);
-        __syncwarp();
-        if (!mbar_wait_bounded(all_done, 0) && lane == 0) atomicAdd_system(status, 1u);
     } else {
         // ---- results
-        const int quad = warp & 3;
-        int64_t* offs = epi_offs + quad * ROWS;  // where the rows' outputs are, -1 for none
+        const int quad = warp & 3, i = lane >> 4;
+        int64_t* offs = epi_offs + quad * MXT_ROWS;  // where the rows' outputs are, -1 for none
         const uint32_t from = tmem + ((uint32_t)(32 * quad) << 16);
+        const uint8_t* w = weight(i);
         O* y = static_cast<O*>(a.y);
-        uint32_t phase = 0;
+        MxtStage<2> acc;
         bool ok = true;
         for (bool more = walk.find(); more && ok; more = walk.next()) {
             __syncwarp();
@@ -487,74 +562,79 @@ __global__ void __launch_bounds__(MXT_THREADS, 1) mxt_kernel(MxArgs a, MxtRows x
                 const int s = r < walk.cnt ? mxt_slot(a, walk.s0 + r) : -1;
                 offs[r] = s < 0 ? -1 : s * a.ldy;
             }
-            int n[2];
-            float f[2][2];  // the row's power of two, in two factors
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                n[h] = walk.g * GROUP_TILES * MX_TILE_N + quad * 32 + lane + (MODE == MX_GATE_UP ? 0 : h * 128);
-                const uint8_t* w = MODE == MX_GATE_UP && h ? a.w2 : a.w;
-                const int e = n[h] < a.L.N ? w[walk.e * a.L.expert_bytes() + (n[h] / MX_TILE_N) * a.L.tile_bytes() +
-                                               (int64_t)units * MX_UNIT_BYTES + n[h] % MX_TILE_N]
-                                           : 127;
-                const int p = e - 127 + MXT_SHIFT;
-                f[h][0] = e == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(min(p, 127) + 127) << 23);
-                f[h][1] = __uint_as_float((uint32_t)(max(p - 127, 0) + 127) << 23);
-            }
+            const int tile = tile_of(quad, i), n = tile * MX_TILE_N + (lane & 15);
+            const bool mine = n < a.L.N;
+            // the row's power of two, in two factors
+            const int e = mine ? w[walk.e * a.L.expert_bytes() + tile * a.L.tile_bytes() + (int64_t)units * MX_UNIT_BYTES + (lane & 15)] : 127;
+            const int p = e - 127 + MXT_SHIFT;
+            const float f0 = e == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(min(p, 127) + 127) << 23);
+            const float f1 = __uint_as_float((uint32_t)(max(p - 127, 0) + 127) << 23);
             __syncwarp();
-            ok = __all_sync(~0u, wait(acc_full, phase));
-            phase ^= 1;
+            ok = wait(acc_full + acc.i, acc.phase);
             if (!ok) break;
             tc_fence_after();
             // 16 columns a step, the next ones on their way from tensor memory meanwhile
-            auto store = [&](const uint32_t (&v)[16], const uint32_t (&v2)[16], int c0, int h) {
-                const bool mine = n[h] < a.L.N;
-                O* to = y + n[h];
-#pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    float o = __uint_as_float(v[c]) * f[h][0] * f[h][1];
-                    if constexpr (MODE == MX_GATE_UP) o = mx_silu(o) * (__uint_as_float(v2[c]) * f[1][0] * f[1][1]);
-                    const int64_t at = offs[c0 + c];
-                    if (mine && at >= 0 && QG_OK(qg_in(at + n[h], 1, (int64_t)a.slots * a.ldy), status, 332)) to[at] = from_f32<O>(o);
-                }
-            };
-            const int steps = (MODE == MX_GATE_UP ? 1 : 2) * (walk.n / 16);
-            auto load = [&](int i, uint32_t (&v)[16], uint32_t (&v2)[16]) {
+            auto put = [&](const uint32_t (&v)[16], int c0) {
+                O* to = y + n;
                 if constexpr (MODE == MX_GATE_UP) {
-                    tc_ld_32x32b_x16(from + 16 * i, v);
-                    tc_ld_32x32b_x16(from + ROWS + 16 * i, v2);
+                    // a lane of the gate's rows and the one of the same row of up
+                    // have two columns: one each
+                    float x[16];
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) x[c] = __uint_as_float(v[c]) * f0 * f1;
+#pragma unroll
+                    for (int c = 0; c < 16; c += 2) {
+                        const float other = __shfl_xor_sync(~0u, i ? x[c] : x[c + 1], 16);
+                        const float o = mx_silu(i ? other : x[c]) * (i ? x[c + 1] : other);
+                        const int64_t at = offs[c0 + c + i];
+                        if (mine && at >= 0 && QG_OK(qg_in(at + n, 1, (int64_t)a.slots * a.ldy), status, 332)) to[at] = from_f32<O>(o);
+                    }
                 } else {
-                    const int h = i >= walk.n / 16;
-                    tc_ld_32x32b_x16(from + h * ROWS + 16 * (i - h * (walk.n / 16)), v);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        const int64_t at = offs[c0 + c];
+                        if (mine && at >= 0 && QG_OK(qg_in(at + n, 1, (int64_t)a.slots * a.ldy), status, 333))
+                            to[at] = from_f32<O>(__uint_as_float(v[c]) * f0 * f1);
+                    }
                 }
             };
-            auto put = [&](int i, const uint32_t (&v)[16], const uint32_t (&v2)[16]) {
-                const int h = MODE == MX_GATE_UP ? 0 : i >= walk.n / 16;
-                const int c0 = 16 * (i - h * (walk.n / 16));
-                if (h) store(v, v2, c0, 1);
-                else store(v, v2, c0, 0);
-            };
-            uint32_t va[16], va2[16], vb[16], vb2[16];
-            load(0, va, va2);
-            for (int i = 0; i < steps; i += 2) {
+            const uint32_t d = from + acc.i * MXT_ROWS;
+            uint32_t va[16], vb[16];
+            tc_ld_32x32b_x16(d, va);
+            for (int c0 = 0; c0 < walk.n; c0 += 32) {
                 tc_wait_ld();
-                if (i + 1 < steps) load(i + 1, vb, vb2);
-                put(i, va, va2);
-                if (i + 1 < steps) {
+                if (c0 + 16 < walk.n) tc_ld_32x32b_x16(d + c0 + 16, vb);
+                put(va, c0);
+                if (c0 + 16 < walk.n) {
                     tc_wait_ld();
-                    if (i + 2 < steps) load(i + 2, va, va2);
-                    put(i + 1, vb, vb2);
+                    if (c0 + 32 < walk.n) tc_ld_32x32b_x16(d + c0 + 32, va);
+                    put(vb, c0 + 16);
                 }
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(acc_empty)) : "memory");
+            if (lane == 0) arrive_first(acc_empty + acc.i);
+            acc.next();
         }
     }
+    if (warp == MXT_MMA_WARP && rank == 0) {  // what was issued ends before tensor memory is given back
+        tc_commit_both(smem_u32(all_done), elected());
+    }
+    if (warp == MXT_MMA_WARP) {
+        const long long t0 = clock64();
+        while (!mbar_try_wait(all_done, 0))
+            if (clock64() - t0 > MXT_WAIT_CLOCKS) {
+                if (lane == 0) atomicAdd_system(status, 1u);
+                break;
+            }
+        __syncwarp();
+    }
+    __syncwarp();
     tc_fence_before();
-    __syncthreads();
+    cluster_barrier();
     if (warp == MXT_MMA_WARP) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem));
     }
 }
 

@@ -97,7 +97,8 @@ struct MxArgs {
 
 // Whether a call's experts have many rows each (the tcgen05 kernel), about.
 bool mx_many_rows(int64_t slots, int experts);
-// Workspace of that kernel: rows of x as bf16 terms; 0 for bf16 rows.
+// Workspace of that kernel: rows of x as bf16 terms (of bf16 rows where they
+// start off 16-byte boundaries).
 size_t mx_planes_bytes(int type, int64_t rows, int K);
 
 int launch_mx_gemm(int mode, int type, const MxArgs& a, cudaStream_t s);

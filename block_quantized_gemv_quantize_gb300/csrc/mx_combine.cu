@@ -86,8 +86,8 @@ bool mx_many_rows(int64_t slots, int experts)
 
 size_t mx_planes_bytes(int type, int64_t rows, int K)
 {
-    const int terms = type == QGEMV_F32 ? 3 : type == QGEMV_F16 ? 2 : 1;
-    return (size_t)terms * rows * ((K + MX_UNIT_K - 1) / MX_UNIT_K * MX_UNIT_K) * 2;
+    const size_t halves = (size_t)((K + MX_UNIT_K - 1) / MX_UNIT_K) * MX_UNIT_K * (type == QGEMV_F32 ? 2 : 1);
+    return (size_t)rows * (halves * 2 + sizeof(float));
 }
 
 int launch_mx_gemm_f32(int mode, const MxArgs& a, cudaStream_t s);

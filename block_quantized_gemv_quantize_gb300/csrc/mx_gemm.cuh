@@ -28,6 +28,10 @@ namespace qgemv {
 constexpr int MXS_THREADS = 256, MXS_WARPS = MXS_THREADS / 32;
 constexpr int MXS_RED = 20;  // floats of a column of 16 in the exchange (no bank conflicts)
 
+// Halves that a value of a row of x takes.
+template <typename T>
+constexpr int MX_TERMS = sizeof(T) == 4 ? 2 : 1;
+
 struct MxsPlan {
     int rows;     // of x in a row tile
     int parts;    // warps that share a tile's K
@@ -128,9 +132,6 @@ __device__ void mx_zero_rest(const MxArgs& a, O* y, unsigned int* status)
 
 __device__ __forceinline__ float mx_silu(float g) { return g / (1.0f + expf(-g)); }
 
-template <typename T>
-constexpr int MX_TERMS = sizeof(T) == 4 ? 2 : 1;
-
 // Eight neighbouring values of a row (`wide`: 16-byte aligned), zeros from n on.
 template <typename T>
 __device__ __forceinline__ void mx_load8(const T* p, bool wide, int n, float (&v)[8])
@@ -152,10 +153,27 @@ __device__ __forceinline__ uint32_t mx_halves(__half a, __half b)
     return (uint32_t)__half_as_ushort(a) | (uint32_t)__half_as_ushort(b) << 16;
 }
 
+// The power of two that a row goes by, from its largest finite magnitude's bits:
+// 2^-e brings it to [2^14, 2^15).  (A row of subnormal numbers goes by 2^112,
+// and keeps what it has to 2^-39 of 2^-126.)
+__device__ __forceinline__ int mx_row_exponent(uint32_t top) { return top ? max(-112, (int)(top >> 23) - 141) : 0; }
+
+// Eight values times f = 2^-e as halves, and of fp32 values what that leaves.
+template <typename T>
+__device__ __forceinline__ void mx_row_halves(const float (&v)[8], float f, __half (&h)[8], __half (&l)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float y = v[j] * f;
+        h[j] = __float2half_rn(y);
+        if constexpr (MX_TERMS<T> == 2) l[j] = isfinite(y) ? __float2half_rn(y - __half2float(h[j])) : __float2half_rn(0.0f);
+    }
+}
+
 // The cnt rows of a row tile into shared memory, as the product takes them: a
-// block has 16 bytes for each t, values 4 t, 4 t + 2, 16 + 4 t, 16 + 4 t + 2
-// and then those one further on each.  A warp takes 256 values of a row at a
-// time, a lane eight neighbouring ones: half a piece of two t each.
+// block has 16 bytes for each t, values 4 t .. 4 t + 3 and 16 + 4 t .. 16 + 4 t
+// + 3.  A warp takes 256 values of a row at a time, a lane eight neighbouring
+// ones: half a piece of two t each.
 template <typename T>
 __device__ void mxs_stage(const MxArgs& a, const MxsPlan& p, uint8_t* xs, const int* slot_of, int* x_exp,
                           uint32_t* x_top, int cnt, unsigned int* status)
@@ -181,8 +199,7 @@ __device__ void mxs_stage(const MxArgs& a, const MxsPlan& p, uint8_t* xs, const 
             if (lane == 0) atomicMax(&x_top[row], top);
         }
         __syncthreads();
-        // (a row whose largest is subnormal goes by 2^126, and keeps what it has to 2^-38 of 2^-126)
-        if ((int)threadIdx.x < cnt) x_exp[threadIdx.x] = x_top[threadIdx.x] ? max(-112, (int)(x_top[threadIdx.x] >> 23) - 141) : 0;
+        if ((int)threadIdx.x < cnt) x_exp[threadIdx.x] = mx_row_exponent(x_top[threadIdx.x]);
         __syncthreads();
     }
     for (int i = warp; i < cnt * pieces; i += MXS_WARPS) {
@@ -193,25 +210,16 @@ __device__ void mxs_stage(const MxArgs& a, const MxsPlan& p, uint8_t* xs, const 
         uint8_t* to = xs + (size_t)row * TERMS * p.x_bytes;
         const float f = SCALED ? __uint_as_float((uint32_t)(127 - x_exp[row]) << 23) : 1.0f;
         __half h[8], l[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float y = v[j] * f;
-            h[j] = __float2half_rn(y);
-            if constexpr (TERMS == 2) l[j] = isfinite(y) ? __float2half_rn(y - __half2float(h[j])) : __float2half_rn(0.0f);
-        }
+        mx_row_halves<T>(v, f, h, l);
         if (QG_OK(qg_in(k * 2, 16, p.x_bytes - 64) && row < p.rows, status, 313)) {
             const int q = (k >> 3) & 3;
-            uint32_t* o = reinterpret_cast<uint32_t*>(to + (k & ~31) * 2 + (q & 1) * 32 + (q >> 1) * 4);
-            o[0] = mx_halves(h[0], h[2]);
-            o[2] = mx_halves(h[1], h[3]);
-            o[4] = mx_halves(h[4], h[6]);
-            o[6] = mx_halves(h[5], h[7]);
+            uint8_t* o = to + (k & ~31) * 2 + (q & 1) * 32 + (q >> 1) * 8;
+            *reinterpret_cast<uint2*>(o) = make_uint2(mx_halves(h[0], h[1]), mx_halves(h[2], h[3]));
+            *reinterpret_cast<uint2*>(o + 16) = make_uint2(mx_halves(h[4], h[5]), mx_halves(h[6], h[7]));
             if constexpr (TERMS == 2) {
-                o += p.x_bytes / 4;
-                o[0] = mx_halves(l[0], l[2]);
-                o[2] = mx_halves(l[1], l[3]);
-                o[4] = mx_halves(l[4], l[6]);
-                o[6] = mx_halves(l[5], l[7]);
+                o += p.x_bytes;
+                *reinterpret_cast<uint2*>(o) = make_uint2(mx_halves(l[0], l[1]), mx_halves(l[2], l[3]));
+                *reinterpret_cast<uint2*>(o + 16) = make_uint2(mx_halves(l[4], l[5]), mx_halves(l[6], l[7]));
             }
         }
     }

@@ -80,19 +80,19 @@ int launch_mxt(const MxArgs& a, cudaStream_t s)
         if (!ok[dev]) cudaGetLastError();
     });
     if (!ok[dev]) return QGEMV_CUDA_ERROR;
-    // x itself where its rows are bf16 and aligned, bf16 terms of it in the workspace otherwise
-    constexpr int TERMS = MxtShape<T>::TERMS;
+    // x itself where its rows are halves and aligned, halves in the workspace otherwise
+    constexpr int TERMS = MX_TERMS<T>;
+    constexpr bool HALVES = std::is_same<T, __half>::value;
     const int padded = a.L.units() * MX_UNIT_K;
     const int64_t rows = a.slots / a.x_div;
     const bool wide = ((reinterpret_cast<uintptr_t>(a.x) | (uintptr_t)(a.ldx * (int64_t)sizeof(T))) & 15u) == 0;
-    const bool direct = TERMS == 1 && wide;
-    const MxtRows x{static_cast<const __nv_bfloat16*>(direct ? a.x : a.planes), direct ? a.ldx : padded, rows * padded,
-                    direct ? a.L.K : padded};
-    if (!direct) {
-        const int64_t ctas = (rows * (padded / 8) + 255) / 256;
-        if (launch_pdl(mxt_planes_kernel<T>, dim3((unsigned)std::min<int64_t>(ctas, (int64_t)di.sms * 8)), dim3(256), 0, s,
-                       static_cast<const T*>(a.x), a.ldx, static_cast<uint16_t*>(a.planes), rows, a.L.K, padded, wide,
-                       timeouts[dev]) != cudaSuccess)
+    MxtRows x{static_cast<const __half*>(a.x), a.ldx, 0, a.L.K, nullptr};
+    if (!HALVES || !wide) {
+        __half* planes = static_cast<__half*>(a.planes);
+        float* scale = reinterpret_cast<float*>(planes + TERMS * rows * padded);
+        x = {planes, padded, rows * padded, padded, HALVES ? nullptr : scale};
+        if (launch_pdl(mxt_rows_kernel<T>, dim3((unsigned)std::min<int64_t>((rows + 7) / 8, (int64_t)di.sms * 8)), dim3(256), 0,
+                       s, static_cast<const T*>(a.x), a.ldx, planes, scale, rows, a.L.K, padded, wide, timeouts[dev]) != cudaSuccess)
             return QGEMV_CUDA_ERROR;
     }
     constexpr int GROUP = MODE == MX_GATE_UP ? 8 : 16;
@@ -101,7 +101,7 @@ int launch_mxt(const MxArgs& a, cudaStream_t s)
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2u * (unsigned)std::min<int64_t>(most, di.sms / 2));
     cfg.blockDim = dim3(MXT_THREADS);
-    cfg.dynamicSmemBytes = mxt_smem<T>(a.L.experts);
+    cfg.dynamicSmemBytes = mxt_smem<TERMS>(a.L.experts);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -2,17 +2,17 @@
 //
 // y[s][n] = sum_k w[n][k] x[s][k] with the weights as operand A (256 rows of
 // a tcgen05.mma over a pair of SMs, from tensor memory) and up to MXT_ROWS
-// rows of x as operand B (half in each SM's shared memory).  A code times its
-// scale is a bf16 number exactly; rows of x are one bf16 term (bf16), two
-// (fp16) or three (fp32), which hold them exactly, so that only the tensor
-// core's fp32 sums round.  The codes come from the pack's words with integer
-// operations, one multiplication in pairs for the scale, and go to tensor
-// memory as fragments (16x256b): that operand costs no shared-memory bandwidth, and
-// the pair halves what the other one costs.
-//
-// Scales in A are relative to the row's largest and times 2^-20, so that the
-// sums stay in range wherever x is a bf16 number; the epilogue multiplies by
-// the row's power of two.
+// rows of x as operand B (half in each SM's shared memory).  Both are halves: a
+// code times its scale relative to the row's largest, times 2^13, is one
+// exactly (the pack has no scale below 2^-27); fp16 rows are what they are;
+// bf16 rows go by a power of two that brings the row's largest finite element
+// to [2^14, 2^15), which keeps every element to 2^-40 of it (all eight bits of
+// those within 2^-31), fp32 rows as two such terms, in a pass of its own.  (As
+// bf16 numbers the weights take 19 instructions a word instead of 8, and
+// bound the kernel: 1240 clocks a step of 660.)  The codes go from the pack's words
+// to tensor memory as fragments (16x256b): that operand costs no
+// shared-memory bandwidth, and the pair halves what the other one costs.
+// Sums are the tensor core's, in fp32; the epilogue multiplies by the powers of two.
 //
 // In each CTA of a pair 8 warps convert weights (32 rows of tensor memory
 // each, every other unit), 3 gather rows of x by asynchronous copies into
@@ -35,43 +35,33 @@ constexpr int MXT_A_STAGES = 3;  // of two units, 64 columns each: what hides a 
 constexpr uint32_t MXT_A_COL = 2 * MXT_ROWS;
 static_assert(MXT_A_COL + MXT_A_STAGES * 64 <= 512, "tensor memory");
 constexpr long long MXT_WAIT_CLOCKS = 2000000000;  // about a second
-constexpr int MXT_SHIFT = 20;                      // the scales in A are 2^-20 of what they are
+constexpr int MXT_SHIFT = 13;                      // the scales in A are 2^13 times what they are
 
 // Terms of a row of x; the ring for them: batches of steps, a step being half a
 // row tile of two units of 64 values.  A batch is announced and given back as
-// one: the fence between the copies' writes and the tensor core takes half a
-// thousand clocks.
-template <typename T>
-struct MxtShape;
-template <>
-struct MxtShape<__nv_bfloat16> {
-    static constexpr int TERMS = 1, BATCH = 2, BATCHES = 5;
-};
-template <>
-struct MxtShape<__half> {
-    static constexpr int TERMS = 2, BATCH = 1, BATCHES = 5;
-};
-template <>
-struct MxtShape<float> {
-    static constexpr int TERMS = 3, BATCH = 1, BATCHES = 3;
+// one.  AHEAD: steps of a converting warp's own ring of codes.
+template <int TERMS>
+struct MxtShape {
+    static constexpr int BATCH = TERMS == 1 ? 2 : 1, BATCHES = 4, AHEAD = 4;
 };
 
 struct MxtRows {
-    const __nv_bfloat16* x;  // row r of term i at x + i * plane + r * ld, 16-byte aligned
+    const __half* x;  // row r of term i at x + i * plane + r * ld, 16-byte aligned
     int64_t ld, plane;
-    int values;  // of a row that are there
+    int values;          // of a row that are there
+    const float* scale;  // null, or what a row's products are to be multiplied by
 };
 
-template <typename T>
+template <int TERMS>
 constexpr size_t mxt_smem(int experts)
 {
-    using S = MxtShape<T>;
-    return 1024 + (size_t)S::BATCHES * S::BATCH * 2 * S::TERMS * (MXT_ROWS / 2) * 128 +
-           (2 * S::BATCHES + 2 * MXT_A_STAGES + 5) * sizeof(uint64_t) + MXT_EPI * MXT_ROWS * sizeof(int64_t) +
-           (size_t)(2 * (experts + 1) + 32 + 4) * sizeof(int);
+    using S = MxtShape<TERMS>;
+    return 1024 + (size_t)S::BATCHES * S::BATCH * 2 * TERMS * (MXT_ROWS / 2) * 128 +
+           (size_t)MXT_CONVERT * S::AHEAD * 2 * MX_UNIT_BYTES + (2 * S::BATCHES + 2 * MXT_A_STAGES + 5) * sizeof(uint64_t) +
+           MXT_EPI * MXT_ROWS * (sizeof(int64_t) + sizeof(float)) + (size_t)(2 * (experts + 1) + 32 + 4) * sizeof(int);
 }
 
-// ---- tcgen05, clusters, TMA --------------------------------------------------------
+// ---- tcgen05, clusters --------------------------------------------------------
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -135,8 +125,8 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t smem)
            (uint64_t)2 << 61;
 }
 
-// D fp32, A and B bf16, both K-major, 256 x n.
-__device__ __forceinline__ uint32_t tc_idesc(int n) { return 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(n >> 3) << 17 | 16u << 24; }
+// D fp32, A and B fp16, both K-major, 256 x n.
+__device__ __forceinline__ uint32_t tc_idesc(int n) { return 1u << 4 | (uint32_t)(n >> 3) << 17 | 16u << 24; }
 
 __device__ __forceinline__ uint32_t cluster_rank()
 {
@@ -166,59 +156,62 @@ __device__ __forceinline__ void arrive_first(uint64_t* bar)
         "mbarrier.arrive.shared::cluster.b64 _, [r];\n\t}" ::"r"(smem_u32(bar))
         : "memory");
 }
-// A word's eight codes, times a scale (in both halves), as four pairs of bf16.
-__device__ __forceinline__ void e2m1_bf16(uint32_t w, uint32_t scale, uint32_t& p0, uint32_t& p1, uint32_t& p2, uint32_t& p3)
+// A word's eight codes, times a scale (in both halves), as four pairs of halves.
+__device__ __forceinline__ void e2m1_scaled(uint32_t w, uint32_t scale, uint32_t& p0, uint32_t& p1, uint32_t& p2, uint32_t& p3)
 {
-    // exponent and mantissa to bits 8 .. 6: the code times 2^-126 (0.5 is subnormal there as here)
-    const uint32_t m = 0x01C001C0u, s = 0x80008000u;
-    const uint32_t t0 = ((w << 6) & m) | ((w << 12) & s), t1 = ((w << 2) & m) | ((w << 8) & s);
-    const uint32_t t2 = ((w >> 2) & m) | ((w << 4) & s), t3 = ((w >> 6) & m) | (w & s);
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(p0) : "r"(t0), "r"(scale));
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(p1) : "r"(t1), "r"(scale));
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(p2) : "r"(t2), "r"(scale));
-    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(p3) : "r"(t3), "r"(scale));
+    uint32_t h[4];
+    e2m1_halves(w, h);
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(p0) : "r"(h[0]), "r"(scale));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(p1) : "r"(h[1]), "r"(scale));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(p2) : "r"(h[2]), "r"(scale));
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(p3) : "r"(h[3]), "r"(scale));
 }
 
-// ---- rows of x as bf16 terms ------------------------------------------------------
+// ---- rows of x as halves ------------------------------------------------------------
 
+// x [rows][K] -> planes [term][rows][padded], zeros behind a row, and each
+// row's power of two.  A warp a row, read twice (the second time from L1 or L2); bound by memory.
 template <typename T>
-__device__ __forceinline__ void mxt_terms(float v, uint16_t (&t)[MxtShape<T>::TERMS])
+__global__ void __launch_bounds__(256) mxt_rows_kernel(const T* __restrict__ x, int64_t ld, __half* planes, float* scale,
+                                                       int64_t rows, int K, int padded, bool wide, unsigned int* status)
 {
-    // cut off, not rounded: the largest numbers stay finite, and what is left is exact
-    float left = v;
-#pragma unroll
-    for (int i = 0; i < MxtShape<T>::TERMS; ++i) {
-        const uint32_t u = __float_as_uint(left);
-        t[i] = (uint16_t)(left != left ? 0x7FC0u : u >> 16);
-        left = isfinite(v) ? left - __uint_as_float(u & 0xFFFF0000u) : 0.0f;
-    }
-}
-
-// x [rows][K] -> planes [term][rows][padded], zeros behind a row.  One read, TERMS
-// writes of half its bytes (or all); bound by memory.
-template <typename T>
-__global__ void __launch_bounds__(256) mxt_planes_kernel(const T* __restrict__ x, int64_t ld, uint16_t* planes, int64_t rows,
-                                                         int K, int padded, bool wide, unsigned int* status)
-{
-    constexpr int TERMS = MxtShape<T>::TERMS;
+    constexpr int TERMS = MX_TERMS<T>;
+    constexpr bool SCALED = !std::is_same<T, __half>::value;
     pdl_launch_dependents();
     pdl_wait();
-    const int pieces = padded / 8;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < rows * pieces; i += (int64_t)gridDim.x * 256) {
-        const int64_t row = i / pieces;
-        const int k = (int)(i - row * pieces) * 8;
-        float v[8];
-        mx_load8(x + row * ld + k, wide, max(0, K - k), v);
-        uint16_t t[8][TERMS];
+    const int lane = threadIdx.x & 31;
+    for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += (int64_t)gridDim.x * 8) {
+        const T* from = x + row * ld;
+        int e = 0;
+        if constexpr (SCALED) {
+            uint32_t top = 0;
+#pragma unroll 4
+            for (int k = lane * 8; k < K; k += 256) {
+                float v[8];
+                mx_load8(from + k, wide, K - k, v);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) mxt_terms<T>(v[j], t[j]);
-        if (!QG_OK(qg_in(row * padded + k, 8, rows * padded), status, 330)) continue;
-#pragma unroll
-        for (int j = 0; j < TERMS; ++j) {
-            alignas(16) uint16_t o[8];
-#pragma unroll
-            for (int m = 0; m < 8; ++m) o[m] = t[m][j];
-            *reinterpret_cast<uint4*>(planes + (j * rows + row) * padded + k) = *reinterpret_cast<uint4*>(o);
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t m = __float_as_uint(v[j]) & 0x7FFFFFFFu;
+                    top = max(top, m < 0x7F800000u ? m : 0u);
+                }
+            }
+            e = mx_row_exponent(__reduce_max_sync(~0u, top));
+            if (lane == 0) scale[row] = __uint_as_float((uint32_t)(127 + e) << 23);
+        }
+        const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll 2
+        for (int k = lane * 8; k < padded; k += 256) {
+            float v[8];
+            mx_load8(from + k, wide, max(0, K - k), v);
+            __half h[8], l[8];
+            mx_row_halves<T>(v, f, h, l);
+            if (!QG_OK(qg_in(row * padded + k, 8, rows * padded), status, 330)) continue;
+            __half* to = planes + row * padded + k;
+            *reinterpret_cast<uint4*>(to) =
+                make_uint4(mx_halves(h[0], h[1]), mx_halves(h[2], h[3]), mx_halves(h[4], h[5]), mx_halves(h[6], h[7]));
+            if constexpr (TERMS == 2)
+                *reinterpret_cast<uint4*>(to + rows * padded) =
+                    make_uint4(mx_halves(l[0], l[1]), mx_halves(l[2], l[3]), mx_halves(l[4], l[5]), mx_halves(l[6], l[7]));
         }
     }
 }
@@ -277,18 +270,20 @@ template <typename T, int MODE>
 __global__ void __launch_bounds__(MXT_THREADS, 1)
     mxt_kernel(MxArgs a, MxtRows x, unsigned int* status)
 {
-    using S = MxtShape<T>;
+    constexpr int TERMS = MX_TERMS<T>;
+    using S = MxtShape<TERMS>;
     using O = typename std::conditional<MODE == MX_DOWN, float, T>::type;
-    constexpr int TERMS = S::TERMS, BATCH = S::BATCH, BATCHES = S::BATCHES;
+    constexpr int BATCH = S::BATCH, BATCHES = S::BATCHES;
     constexpr int TERM_BYTES = MXT_ROWS / 2 * 128, UNIT_BYTES = TERMS * TERM_BYTES, STEP_BYTES = 2 * UNIT_BYTES;
     extern __shared__ uint8_t sm_raw[];
     uint8_t* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
-    uint64_t* full_b = reinterpret_cast<uint64_t*>(sm + BATCHES * BATCH * STEP_BYTES);
+    uint64_t* full_b = reinterpret_cast<uint64_t*>(sm + BATCHES * BATCH * STEP_BYTES + MXT_CONVERT * S::AHEAD * 2 * MX_UNIT_BYTES);
     uint64_t *empty_b = full_b + BATCHES, *full_a = empty_b + BATCHES;
     uint64_t *empty_a = full_a + MXT_A_STAGES, *acc_full = empty_a + MXT_A_STAGES, *acc_empty = acc_full + 2;
     uint64_t* all_done = acc_empty + 2;
     int64_t* epi_offs = reinterpret_cast<int64_t*>(all_done + 1);
-    int* before = reinterpret_cast<int*>(epi_offs + MXT_EPI * MXT_ROWS);
+    float* epi_scale = reinterpret_cast<float*>(epi_offs + MXT_EPI * MXT_ROWS);
+    int* before = reinterpret_cast<int*>(epi_scale + MXT_EPI * MXT_ROWS);
     int* start = before + a.L.experts + 1;
     int* sums = start + a.L.experts + 1;
     volatile int* gave_up = sums + 32;
@@ -366,9 +361,8 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
         // ---- weights into tensor memory: four warps take a step's first unit, four its second
         const int quad = warp & 3, odd = warp >> 2, g = lane >> 2;
         const uint32_t to = tmem + MXT_A_COL + 32 * odd + ((uint32_t)(32 * quad) << 16);
-        constexpr int AHEAD = 2;  // steps on their way from global memory
-        uint4 code[AHEAD][2];
-        uint32_t scale[AHEAD][2];
+        constexpr int AHEAD = S::AHEAD;
+        uint8_t* ring = sm + BATCHES * BATCH * STEP_BYTES + warp * (AHEAD * 2 * MX_UNIT_BYTES);
         bool more = walk.find();
         int64_t left = more ? (walk.items - walk.item + walk.step - 1) / walk.step * steps : 0;
         int u = odd;
@@ -382,69 +376,81 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
                 from[i] = weight(i) + walk.e * a.L.expert_bytes() + (there[i] ? tile : 0) * a.L.tile_bytes() + odd * MX_UNIT_BYTES;
             }
         };
-        auto fetch = [&](uint4 (&c)[2], uint32_t (&s)[2]) {
-            if (!more) return;
+        int slot = 0;
+        // The unit's codes and scales of two tiles into the warp's ring.  (A tile behind the last leaves what
+        // was there: rows of the product that go nowhere.)
+        auto fetch = [&]() {
+            if (more) {
+                uint8_t* to = ring + slot * (2 * MX_UNIT_BYTES);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                c[i] = make_uint4(0, 0, 0, 0);
-                s[i] = 0x7F7F7F7Fu;
-                if (there[i] && u < units && QG_OK(qg_in(from[i] - weight(i), MX_UNIT_BYTES, a.L.bytes()), status, 331)) {
-                    c[i] = __ldg(reinterpret_cast<const uint4*>(from[i] + lane * 16));
-                    s[i] = __ldg(reinterpret_cast<const uint32_t*>(from[i] + MX_UNIT_CODES + g * 4));
+                for (int i = 0; i < 2; ++i)
+                    if (there[i] && u < units && QG_OK(qg_in(from[i] - weight(i), MX_UNIT_BYTES, a.L.bytes()), status, 331)) {
+                        cp_async16(to + i * MX_UNIT_BYTES + lane * 16, from[i] + lane * 16);
+                        if (lane < 2) cp_async16(to + i * MX_UNIT_BYTES + MX_UNIT_CODES + lane * 16, from[i] + MX_UNIT_CODES + lane * 16);
+                    }
+                from[0] += 2 * MX_UNIT_BYTES;
+                from[1] += 2 * MX_UNIT_BYTES;
+                if (++slot == AHEAD) slot = 0;
+                u += 2;
+                if (u >= 2 * steps) {
+                    u = odd;
+                    more = walk.next();
+                    if (more) locate();
                 }
-                from[i] += 2 * MX_UNIT_BYTES;
             }
-            u += 2;
-            if (u >= 2 * steps) {
-                u = odd;
-                more = walk.next();
-                if (more) locate();
-            }
+            cp_async_commit();
         };
         if (more) locate();
 #pragma unroll
-        for (int j = 0; j < AHEAD; ++j) fetch(code[j], scale[j]);
+        for (int j = 0; j < AHEAD - 1; ++j) fetch();
+        int mine = 0;
         MxtStage<MXT_A_STAGES> st;
         MxtStage<BATCHES> b;
         int in = 0;
-        bool ok = true;
-        while (left > 0 && ok) {
+        // (one body, not unrolled: the roles' loops share the instruction caches)
+#pragma unroll 1
+        for (; left > 0; --left) {
+            cp_async_wait<AHEAD - 2>();
+            __syncwarp();
+            uint4 code[2];
+            uint32_t scale[2];
 #pragma unroll
-            for (int j = 0; j < AHEAD; ++j) {
-                if (left <= 0 || !ok) break;
-                uint32_t r[2][16];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t wd[4] = {code[j][i].x, code[j][i].y, code[j][i].z, code[j][i].w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {  // rows g and g + 8 of the first block, then of the second
-                        // 2^(b - 127) 2^126 2^-20 as bf16, in both halves
-                        const uint32_t e = (__byte_perm(scale[j][i], 0, 0x4040 + 0x0101 * k) + (126 - MXT_SHIFT) * 0x10001u) << 7;
-                        const int o = 8 * (k >> 1) + 2 * (k & 1);
-                        e2m1_bf16(wd[k], e, r[i][o], r[i][o + 1], r[i][o + 4], r[i][o + 5]);
-                    }
-                }
-                fetch(code[j], scale[j]);
-                ok = wait(empty_a + st.i, st.phase ^ 1);
-                if (!ok) break;
-                tc_fence_after();
-                tc_st_16x256b_x4(to + st.i * 64, r[0]);
-                tc_st_16x256b_x4(to + st.i * 64 + (16u << 16), r[1]);
-                tc_wait_st();
-                tc_fence_before();
-                // one of the eight announces the rows of x too, which came long ago
-                if (warp == 0 && in == 0) {
-                    ok = wait(full_b + b.i, b.phase);
-                    if (!ok) break;
-                    b.next();
-                }
-                if (++in == BATCH) in = 0;
-                __syncwarp();
-                if (lane == 0) arrive_first(full_a + st.i);
-                st.next();
-                --left;
+            for (int i = 0; i < 2; ++i) {
+                const uint8_t* at = ring + (mine * 2 + i) * MX_UNIT_BYTES;
+                code[i] = *reinterpret_cast<const uint4*>(at + lane * 16);
+                scale[i] = *reinterpret_cast<const uint32_t*>(at + MX_UNIT_CODES + g * 4);
             }
+            if (++mine == AHEAD) mine = 0;
+            fetch();  // (into the slot read one step ago)
+            uint32_t r[2][16];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t wd[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {  // rows g and g + 8 of the first block, then of the second
+                    // 2^(b - 127 + 13) as a half, twice
+                    const uint32_t e = (__byte_perm(scale[i], 0, 0x4040 + 0x0101 * k) - (127 - MXT_SHIFT - 15) * 0x10001u) << 10;
+                    const int o = 8 * (k >> 1) + 2 * (k & 1);
+                    e2m1_scaled(wd[k], e, r[i][o], r[i][o + 1], r[i][o + 4], r[i][o + 5]);
+                }
+            }
+            if (!wait(empty_a + st.i, st.phase ^ 1)) break;
+            tc_fence_after();
+            tc_st_16x256b_x4(to + st.i * 64, r[0]);
+            tc_st_16x256b_x4(to + st.i * 64 + (16u << 16), r[1]);
+            tc_wait_st();
+            tc_fence_before();
+            // one of the eight announces the rows of x too, which came long ago
+            if (warp == 0 && in == 0) {
+                if (!wait(full_b + b.i, b.phase)) break;
+                b.next();
+            }
+            if (++in == BATCH) in = 0;
+            __syncwarp();
+            if (lane == 0) arrive_first(full_a + st.i);
+            st.next();
         }
+        cp_async_wait<0>();
     } else if (warp >= MXT_LOAD_WARP) {
         // ---- rows of x into shared memory: this CTA's half of a row tile, a 16-byte piece of every 16th row a thread
         constexpr int STEP = MXT_LOAD * 4, EACH = (MXT_ROWS / 2 + STEP - 1) / STEP, LAG = BATCHES - 2;
@@ -470,23 +476,27 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
                 const int place = walk.s0 + min((int)rank * half + r0 + j * STEP, walk.cnt - 1);
                 from[j] = reinterpret_cast<const uint8_t*>(x.x + (int64_t)(max(0, mxt_slot(a, place)) / a.x_div) * x.ld + c * 8);
             }
-            for (int u = 0; u < units; ++u) {
-                if (in == 0 && u % 2 == 0) ok = wait(empty_b + st.i, st.phase ^ 1);
+            const int rows = (half - r0 + STEP - 1) / STEP;  // of this thread
+            for (int u = 0; u < units; u += 2) {
+                if (in == 0) ok = wait(empty_b + st.i, st.phase ^ 1);
                 if (!ok) break;
-                const uint32_t unit = (st.i * BATCH + in) * STEP_BYTES + (u & 1) * UNIT_BYTES;
-                const int bytes = u * MX_UNIT_K + c * 8 < x.values ? 16 : 0;  // (zeros behind a row, nothing read)
-                const uint32_t to[2] = {at[0] + unit, at[1] + unit};
+                const uint32_t step = (st.i * BATCH + in) * STEP_BYTES;
+                const uint32_t to[2] = {at[0] + step, at[1] + step};
+                // zeros behind a row, nothing read (16 bytes a piece: it is there or it is not)
+                const int b0 = u * MX_UNIT_K + c * 8 < x.values ? 16 : 0, b1 = (u + 1) * MX_UNIT_K + c * 8 < x.values ? 16 : 0;
 #pragma unroll
                 for (int j = 0; j < EACH; ++j) {
-                    if (r0 + j * STEP < half)
+                    if (j < rows)
 #pragma unroll
-                        for (int i = 0; i < TERMS; ++i)
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to[j & 1] + j * STEP * 128 + i * TERM_BYTES),
-                                         "l"(from[j] + i * plane), "r"(bytes)
+                        for (int i = 0; i < TERMS; ++i) {
+                            const uint32_t d = to[j & 1] + j * STEP * 128 + i * TERM_BYTES;
+                            asm volatile("cp.async.cg.shared.global [%0], [%2], 16, %3;\n\t"
+                                         "cp.async.cg.shared.global [%1], [%2 + 128], 16, %4;" ::"r"(d),
+                                         "r"(d + UNIT_BYTES), "l"(from[j] + i * plane), "r"(b0), "r"(b1)
                                          : "memory");
-                    from[j] += 2 * MX_UNIT_K;
+                        }
+                    from[j] += 4 * MX_UNIT_K;
                 }
-                if ((u & 1) == 0 && u + 1 < units) continue;
                 if (++in == BATCH) {
                     in = 0;
                     cp_async_commit();
@@ -551,6 +561,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
         // ---- results
         const int quad = warp & 3, i = lane >> 4;
         int64_t* offs = epi_offs + quad * MXT_ROWS;  // where the rows' outputs are, -1 for none
+        float* scales = epi_scale + quad * MXT_ROWS;
         const uint32_t from = tmem + ((uint32_t)(32 * quad) << 16);
         const uint8_t* w = weight(i);
         O* y = static_cast<O*>(a.y);
@@ -561,14 +572,15 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
             for (int r = lane; r < walk.n; r += 32) {
                 const int s = r < walk.cnt ? mxt_slot(a, walk.s0 + r) : -1;
                 offs[r] = s < 0 ? -1 : s * a.ldy;
+                scales[r] = s < 0 || !x.scale ? 1.0f : x.scale[s / a.x_div];
             }
             const int tile = tile_of(quad, i), n = tile * MX_TILE_N + (lane & 15);
             const bool mine = n < a.L.N;
             // the row's power of two, in two factors
             const int e = mine ? w[walk.e * a.L.expert_bytes() + tile * a.L.tile_bytes() + (int64_t)units * MX_UNIT_BYTES + (lane & 15)] : 127;
-            const int p = e - 127 + MXT_SHIFT;
-            const float f0 = e == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(min(p, 127) + 127) << 23);
-            const float f1 = __uint_as_float((uint32_t)(max(p - 127, 0) + 127) << 23);
+            const int p = e - 127 - MXT_SHIFT;
+            const float f0 = e == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(max(p, -126) + 127) << 23);
+            const float f1 = __uint_as_float((uint32_t)(min(p + 126, 0) + 127) << 23);
             __syncwarp();
             ok = wait(acc_full + acc.i, acc.phase);
             if (!ok) break;
@@ -579,13 +591,13 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
                 if constexpr (MODE == MX_GATE_UP) {
                     // a lane of the gate's rows and the one of the same row of up
                     // have two columns: one each
-                    float x[16];
+                    float z[16];
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) x[c] = __uint_as_float(v[c]) * f0 * f1;
+                    for (int c = 0; c < 16; ++c) z[c] = __uint_as_float(v[c]) * scales[c0 + c] * f0 * f1;
 #pragma unroll
                     for (int c = 0; c < 16; c += 2) {
-                        const float other = __shfl_xor_sync(~0u, i ? x[c] : x[c + 1], 16);
-                        const float o = mx_silu(i ? other : x[c]) * (i ? x[c + 1] : other);
+                        const float other = __shfl_xor_sync(~0u, i ? z[c] : z[c + 1], 16);
+                        const float o = mx_silu(i ? other : z[c]) * (i ? z[c + 1] : other);
                         const int64_t at = offs[c0 + c + i];
                         if (mine && at >= 0 && QG_OK(qg_in(at + n, 1, (int64_t)a.slots * a.ldy), status, 332)) to[at] = from_f32<O>(o);
                     }
@@ -594,7 +606,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
                     for (int c = 0; c < 16; ++c) {
                         const int64_t at = offs[c0 + c];
                         if (mine && at >= 0 && QG_OK(qg_in(at + n, 1, (int64_t)a.slots * a.ldy), status, 333))
-                            to[at] = from_f32<O>(__uint_as_float(v[c]) * f0 * f1);
+                            to[at] = from_f32<O>(__uint_as_float(v[c]) * scales[c0 + c] * f0 * f1);
                     }
                 }
             };

@@ -223,12 +223,12 @@ __global__ void __launch_bounds__(128) pack_kernel(const uint8_t* __restrict__ c
                 const uint8_t* block = rows + ((int64_t)r * nb + b) * MX_BYTES;
                 if (there) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {  // value 4 t + k % 4 of the block's half k / 4
-                        const uint32_t c = (block[1 + 4 * t + (k & 3)] >> (k < 4 ? 0 : 4)) & 15u;
-                        word[j] |= c << (4 * (k / 2 + 4 * (k & 1)));
-                    }
+                    for (int k = 0; k < 8; ++k)  // value 4 t + k % 4 of the block's half k / 4
+                        word[j] |= (uint32_t)((block[1 + 4 * t + (k & 3)] >> (k < 4 ? 0 : 4)) & 15u) << (4 * k);
                 }
-                if (j == t) scale = there ? (uint32_t)max(1, 127 - (tops[r] - (int)block[0])) : 127u;
+                const int rel = there ? 127 - (tops[r] - (int)block[0]) : 127;
+                if (rel < MX_SCALE_MIN) word[j] = 0;
+                if (j == t) scale = (uint32_t)max(MX_SCALE_MIN, rel);
             }
             uint8_t* unit = to + (int64_t)u * MX_UNIT_BYTES;
             if (QG_OK(qg_in(unit - pack, MX_UNIT_BYTES, L.bytes()), status, 302)) {

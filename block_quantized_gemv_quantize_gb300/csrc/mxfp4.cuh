@@ -11,6 +11,7 @@ constexpr int MX_UNIT_K = 64;       // values of a row in one unit of the pack
 constexpr int MX_TILE_N = 16;       // rows of a tile
 constexpr int MX_UNIT_CODES = MX_TILE_N * MX_UNIT_K / 2;
 constexpr int MX_UNIT_BYTES = MX_UNIT_CODES + MX_TILE_N * MX_UNIT_K / 32;  // codes, scale bytes
+constexpr int MX_SCALE_MIN = 100;  // of the pack's scale bytes
 constexpr int MX_MAX_K = 1 << 15, MX_MAX_N = 1 << 24, MX_MAX_EXPERTS = 1024, MX_MAX_TOP_K = 32;
 
 // The pack: [expert][tile of 16 rows], a tile being
@@ -18,16 +19,17 @@ constexpr int MX_MAX_K = 1 << 15, MX_MAX_N = 1 << 24, MX_MAX_EXPERTS = 1024, MX_
 //          codes, 16 for each lane 4 g + t of a warp: four words, of row g in
 //          the unit's first block, row g + 8 there, row g in its second block,
 //          row g + 8 there.  A word has the block's values 4 t .. 4 t + 3 and
-//          16 + 4 t .. 16 + 4 t + 3, of which nibble i < 4 is the (2 i)th and
-//          nibble i + 4 the (2 i + 1)th.  Then 32 scale bytes [g][4] in the
-//          order of a lane's words: b for the scale 2^(b - 127) relative to
-//          the row's largest, 1 .. 127.
+//          16 + 4 t .. 16 + 4 t + 3, a nibble each in that order.  Then 32
+//          scale bytes [g][4] in the order of a lane's words: b for the scale
+//          2^(b - 127) relative to the row's largest, 100 .. 127; a block
+//          with a smaller one is zeros (with codes as halves it would have to
+//          round, and it is below 2^-27 of the row's largest).
 //   tops   [16] bytes: the row's largest scale byte, 255 for a row that holds
 //          a NaN block
 // A lane's 16 bytes are its operands of four m16n8k16 products, if the K index
-// runs through a block in the order in which the words have it; and as pairs
-// (2 i, 2 i + 1) they are the fragments of a 16 x 256-bit store to tensor
-// memory with K in its own order.
+// runs through a block in the order in which the words have it; and its pairs
+// are the fragments of a 16 x 256-bit store to tensor memory with K in its own
+// order.
 struct MxLayout {
     int experts, N, K;
     __host__ __device__ int tiles() const { return (N + MX_TILE_N - 1) / MX_TILE_N; }
@@ -92,13 +94,12 @@ struct MxArgs {
     int slots, top_k;      // x's row of slot s is s / x_div
     int x_div;
     void* y;               // gemm, gate_up: [slots]; down: fp32 partial results [slots][N]
-    void* planes;          // workspace for x in terms, where the type needs them (mx_planes_bytes)
+    void* planes;          // workspace for rows of x as halves (mx_planes_bytes)
 };
 
 // Whether a call's experts have many rows each (the tcgen05 kernel), about.
 bool mx_many_rows(int64_t slots, int experts);
-// Workspace of that kernel: rows of x as bf16 terms (of bf16 rows where they
-// start off 16-byte boundaries).
+// Workspace of that kernel: rows of x as halves, and their powers of two.
 size_t mx_planes_bytes(int type, int64_t rows, int K);
 
 int launch_mx_gemm(int mode, int type, const MxArgs& a, cudaStream_t s);

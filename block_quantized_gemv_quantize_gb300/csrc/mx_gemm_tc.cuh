@@ -15,7 +15,7 @@
 // Sums are the tensor core's, in fp32; the epilogue multiplies by the powers of two.
 //
 // In each CTA of a pair 8 warps convert weights (32 rows of tensor memory
-// each, every other unit), 3 gather rows of x by asynchronous copies into
+// each, every other step), 3 gather rows of x by asynchronous copies into
 // 128-byte-swizzled shared memory (TMA's gather of four rows takes twice as long), 4 write
 // results while the next item's products run (two accumulators); one thread
 // of the first CTA issues the products for both.  256 rows of weights (128 of gate and of up,
@@ -42,7 +42,7 @@ constexpr int MXT_SHIFT = 13;                      // the scales in A are 2^13 t
 // one.  AHEAD: steps of a converting warp's own ring of codes.
 template <int TERMS>
 struct MxtShape {
-    static constexpr int BATCH = TERMS == 1 ? 2 : 1, BATCHES = 4, AHEAD = 4;
+    static constexpr int BATCH = TERMS == 1 ? 2 : 1, BATCHES = 4, AHEAD = 2;
 };
 
 struct MxtRows {
@@ -57,8 +57,8 @@ constexpr size_t mxt_smem(int experts)
 {
     using S = MxtShape<TERMS>;
     return 1024 + (size_t)S::BATCHES * S::BATCH * 2 * TERMS * (MXT_ROWS / 2) * 128 +
-           (size_t)MXT_CONVERT * S::AHEAD * 2 * MX_UNIT_BYTES + (2 * S::BATCHES + 2 * MXT_A_STAGES + 5) * sizeof(uint64_t) +
-           MXT_EPI * MXT_ROWS * (sizeof(int64_t) + sizeof(float)) + (size_t)(2 * (experts + 1) + 32 + 4) * sizeof(int);
+           (size_t)MXT_CONVERT * S::AHEAD * 4 * MX_UNIT_BYTES + (2 * S::BATCHES + 2 * MXT_A_STAGES + 5) * sizeof(uint64_t) +
+           8 + MXT_EPI * MXT_ROWS * (sizeof(int) + sizeof(float)) + (size_t)(2 * (experts + 1) + 32 + 4) * sizeof(int);
 }
 
 // ---- tcgen05, clusters --------------------------------------------------------
@@ -277,12 +277,12 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
     constexpr int TERM_BYTES = MXT_ROWS / 2 * 128, UNIT_BYTES = TERMS * TERM_BYTES, STEP_BYTES = 2 * UNIT_BYTES;
     extern __shared__ uint8_t sm_raw[];
     uint8_t* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
-    uint64_t* full_b = reinterpret_cast<uint64_t*>(sm + BATCHES * BATCH * STEP_BYTES + MXT_CONVERT * S::AHEAD * 2 * MX_UNIT_BYTES);
+    uint64_t* full_b = reinterpret_cast<uint64_t*>(sm + BATCHES * BATCH * STEP_BYTES + MXT_CONVERT * S::AHEAD * 4 * MX_UNIT_BYTES);
     uint64_t *empty_b = full_b + BATCHES, *full_a = empty_b + BATCHES;
     uint64_t *empty_a = full_a + MXT_A_STAGES, *acc_full = empty_a + MXT_A_STAGES, *acc_empty = acc_full + 2;
     uint64_t* all_done = acc_empty + 2;
-    int64_t* epi_offs = reinterpret_cast<int64_t*>(all_done + 1);
-    float* epi_scale = reinterpret_cast<float*>(epi_offs + MXT_EPI * MXT_ROWS);
+    int* epi_slots = reinterpret_cast<int*>(all_done + 1 + (reinterpret_cast<uintptr_t>(all_done + 1) & 8) / 8);
+    float* epi_scale = reinterpret_cast<float*>(epi_slots + MXT_EPI * MXT_ROWS);
     int* before = reinterpret_cast<int*>(epi_scale + MXT_EPI * MXT_ROWS);
     int* start = before + a.L.experts + 1;
     int* sums = start + a.L.experts + 1;
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
             mbar_init(empty_b + i, 1);
         }
         for (int i = 0; i < MXT_A_STAGES; ++i) {
-            mbar_init(full_a + i, 2 * MXT_CONVERT);
+            mbar_init(full_a + i, MXT_CONVERT);  // four warps of each CTA
             mbar_init(empty_a + i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -358,14 +358,14 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
     };
 
     if (warp < MXT_CONVERT) {
-        // ---- weights into tensor memory: four warps take a step's first unit, four its second
+        // ---- weights into tensor memory: four warps take the even steps, four the odd ones
         const int quad = warp & 3, odd = warp >> 2, g = lane >> 2;
-        const uint32_t to = tmem + MXT_A_COL + 32 * odd + ((uint32_t)(32 * quad) << 16);
-        constexpr int AHEAD = S::AHEAD;
-        uint8_t* ring = sm + BATCHES * BATCH * STEP_BYTES + warp * (AHEAD * 2 * MX_UNIT_BYTES);
+        const uint32_t to = tmem + MXT_A_COL + ((uint32_t)(32 * quad) << 16);
+        constexpr int AHEAD = S::AHEAD, SLOT = 4 * MX_UNIT_BYTES;  // two tiles' two units
+        uint8_t* ring = sm + BATCHES * BATCH * STEP_BYTES + warp * (AHEAD * SLOT);
         bool more = walk.find();
-        int64_t left = more ? (walk.items - walk.item + walk.step - 1) / walk.step * steps : 0;
-        int u = odd;
+        int64_t left = more ? (walk.items - walk.item + walk.step - 1) / walk.step * steps - odd : 0;  // of the CTA, from this warp's on
+        int u = 0;
         const uint8_t* from[2];
         bool there[2];
         auto locate = [&]() {
@@ -373,83 +373,95 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
             for (int i = 0; i < 2; ++i) {
                 const int tile = tile_of(quad, i);
                 there[i] = tile < tiles;
-                from[i] = weight(i) + walk.e * a.L.expert_bytes() + (there[i] ? tile : 0) * a.L.tile_bytes() + odd * MX_UNIT_BYTES;
+                from[i] = weight(i) + walk.e * a.L.expert_bytes() + (there[i] ? tile : 0) * a.L.tile_bytes();
+            }
+        };
+        auto advance = [&](int n) {  // steps
+            u += 2 * n;
+            while (more && u >= 2 * steps) {
+                u -= 2 * steps;
+                more = walk.next();
+                if (more) locate();
             }
         };
         int slot = 0;
-        // The unit's codes and scales of two tiles into the warp's ring.  (A tile behind the last leaves what
-        // was there: rows of the product that go nowhere.)
+        // A step's codes and scales into the warp's ring.  (A tile behind the last leaves what
+        // was there: rows of the product that go nowhere; so does a unit behind the last.)
         auto fetch = [&]() {
             if (more) {
-                uint8_t* to = ring + slot * (2 * MX_UNIT_BYTES);
+                const int n = min(2, units - u) * (MX_UNIT_BYTES / 16);
+                uint8_t* at = ring + slot * SLOT + lane * 16;
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (there[i] && u < units && QG_OK(qg_in(from[i] - weight(i), MX_UNIT_BYTES, a.L.bytes()), status, 331)) {
-                        cp_async16(to + i * MX_UNIT_BYTES + lane * 16, from[i] + lane * 16);
-                        if (lane < 2) cp_async16(to + i * MX_UNIT_BYTES + MX_UNIT_CODES + lane * 16, from[i] + MX_UNIT_CODES + lane * 16);
+                for (int i = 0; i < 2; ++i) {
+                    const uint8_t* p = from[i] + u * MX_UNIT_BYTES + lane * 16;
+                    if (there[i] && QG_OK(qg_in(from[i] - weight(i) + (int64_t)u * MX_UNIT_BYTES, n * 16, a.L.bytes()), status, 331)) {
+                        cp_async16(at + i * 2 * MX_UNIT_BYTES, p);
+                        if (lane + 32 < n) cp_async16(at + i * 2 * MX_UNIT_BYTES + 512, p + 512);
+                        if (lane + 64 < n) cp_async16(at + i * 2 * MX_UNIT_BYTES + 1024, p + 1024);
                     }
-                from[0] += 2 * MX_UNIT_BYTES;
-                from[1] += 2 * MX_UNIT_BYTES;
-                if (++slot == AHEAD) slot = 0;
-                u += 2;
-                if (u >= 2 * steps) {
-                    u = odd;
-                    more = walk.next();
-                    if (more) locate();
                 }
+                if (++slot == AHEAD) slot = 0;
+                advance(2);
             }
             cp_async_commit();
         };
         if (more) locate();
+        advance(odd);
 #pragma unroll
         for (int j = 0; j < AHEAD - 1; ++j) fetch();
-        int mine = 0;
-        MxtStage<MXT_A_STAGES> st;
+        int mine = 0, stage = odd;
+        uint32_t phase = 1;
         MxtStage<BATCHES> b;
-        int in = 0;
+        if (BATCH == 1 && odd) b.next();
         // (one body, not unrolled: the roles' loops share the instruction caches)
 #pragma unroll 1
-        for (; left > 0; --left) {
+        for (; left > 0; left -= 2) {
             cp_async_wait<AHEAD - 2>();
             __syncwarp();
-            uint4 code[2];
-            uint32_t scale[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint8_t* at = ring + (mine * 2 + i) * MX_UNIT_BYTES;
-                code[i] = *reinterpret_cast<const uint4*>(at + lane * 16);
-                scale[i] = *reinterpret_cast<const uint32_t*>(at + MX_UNIT_CODES + g * 4);
-            }
+            const uint8_t* at = ring + mine * SLOT;
             if (++mine == AHEAD) mine = 0;
             fetch();  // (into the slot read one step ago)
-            uint32_t r[2][16];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t wd[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+            for (int h = 0; h < 2; ++h) {
+                uint32_t r[2][16];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {  // rows g and g + 8 of the first block, then of the second
-                    // 2^(b - 127 + 13) as a half, twice
-                    const uint32_t e = (__byte_perm(scale[i], 0, 0x4040 + 0x0101 * k) - (127 - MXT_SHIFT - 15) * 0x10001u) << 10;
-                    const int o = 8 * (k >> 1) + 2 * (k & 1);
-                    e2m1_scaled(wd[k], e, r[i][o], r[i][o + 1], r[i][o + 4], r[i][o + 5]);
+                for (int i = 0; i < 2; ++i) {
+                    const uint8_t* unit = at + (2 * i + h) * MX_UNIT_BYTES;
+                    const uint4 code = *reinterpret_cast<const uint4*>(unit + lane * 16);
+                    const uint32_t scale = *reinterpret_cast<const uint32_t*>(unit + MX_UNIT_CODES + g * 4);
+                    const uint32_t wd[4] = {code.x, code.y, code.z, code.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {  // rows g and g + 8 of the first block, then of the second
+                        // 2^(b - 127 + 13) as a half, twice
+                        const uint32_t e = (__byte_perm(scale, 0, 0x4040 + 0x0101 * k) - (127 - MXT_SHIFT - 15) * 0x10001u) << 10;
+                        const int o = 8 * (k >> 1) + 2 * (k & 1);
+                        e2m1_scaled(wd[k], e, r[i][o], r[i][o + 1], r[i][o + 4], r[i][o + 5]);
+                    }
                 }
+                if (h == 0) {
+                    if (!wait(empty_a + stage, phase)) goto stop;
+                    tc_fence_after();
+                }
+                tc_st_16x256b_x4(to + stage * 64 + 32 * h, r[0]);
+                tc_st_16x256b_x4(to + stage * 64 + 32 * h + (16u << 16), r[1]);
             }
-            if (!wait(empty_a + st.i, st.phase ^ 1)) break;
-            tc_fence_after();
-            tc_st_16x256b_x4(to + st.i * 64, r[0]);
-            tc_st_16x256b_x4(to + st.i * 64 + (16u << 16), r[1]);
             tc_wait_st();
             tc_fence_before();
-            // one of the eight announces the rows of x too, which came long ago
-            if (warp == 0 && in == 0) {
+            // one of the four announces the rows of x too, which came long ago
+            if (quad == 0 && (BATCH == 1 || odd == 0)) {
                 if (!wait(full_b + b.i, b.phase)) break;
                 b.next();
+                if (BATCH == 1) b.next();
             }
-            if (++in == BATCH) in = 0;
             __syncwarp();
-            if (lane == 0) arrive_first(full_a + st.i);
-            st.next();
+            if (lane == 0) arrive_first(full_a + stage);
+            stage += 2;
+            if (stage >= MXT_A_STAGES) {
+                stage -= MXT_A_STAGES;
+                phase ^= 1;
+            }
         }
+    stop:
         cp_async_wait<0>();
     } else if (warp >= MXT_LOAD_WARP) {
         // ---- rows of x into shared memory: this CTA's half of a row tile, a 16-byte piece of every 16th row a thread
@@ -560,7 +572,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
     } else {
         // ---- results
         const int quad = warp & 3, i = lane >> 4;
-        int64_t* offs = epi_offs + quad * MXT_ROWS;  // where the rows' outputs are, -1 for none
+        int* slots = epi_slots + quad * MXT_ROWS;  // the rows' slots, -1 for none, and powers of two
         float* scales = epi_scale + quad * MXT_ROWS;
         const uint32_t from = tmem + ((uint32_t)(32 * quad) << 16);
         const uint8_t* w = weight(i);
@@ -571,7 +583,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
             __syncwarp();
             for (int r = lane; r < walk.n; r += 32) {
                 const int s = r < walk.cnt ? mxt_slot(a, walk.s0 + r) : -1;
-                offs[r] = s < 0 ? -1 : s * a.ldy;
+                slots[r] = s;
                 scales[r] = s < 0 || !x.scale ? 1.0f : x.scale[s / a.x_div];
             }
             const int tile = tile_of(quad, i), n = tile * MX_TILE_N + (lane & 15);
@@ -585,28 +597,43 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
             ok = wait(acc_full + acc.i, acc.phase);
             if (!ok) break;
             tc_fence_after();
+            const bool plain = __all_sync(~0u, p >= -126 || e == 255);  // one factor does
             // 16 columns a step, the next ones on their way from tensor memory meanwhile
             auto put = [&](const uint32_t (&v)[16], int c0) {
                 O* to = y + n;
+                const int64_t extent = (int64_t)a.slots * a.ldy;
+                (void)extent;
+                float z[16];
+#pragma unroll
+                for (int c = 0; c < 16; c += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(scales + c0 + c);
+                    z[c] = __uint_as_float(v[c]) * f.x * f0;
+                    z[c + 1] = __uint_as_float(v[c + 1]) * f.y * f0;
+                    z[c + 2] = __uint_as_float(v[c + 2]) * f.z * f0;
+                    z[c + 3] = __uint_as_float(v[c + 3]) * f.w * f0;
+                }
+                if (!plain)
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) z[c] *= f1;
                 if constexpr (MODE == MX_GATE_UP) {
                     // a lane of the gate's rows and the one of the same row of up
                     // have two columns: one each
-                    float z[16];
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) z[c] = __uint_as_float(v[c]) * scales[c0 + c] * f0 * f1;
 #pragma unroll
                     for (int c = 0; c < 16; c += 2) {
                         const float other = __shfl_xor_sync(~0u, i ? z[c] : z[c + 1], 16);
-                        const float o = mx_silu(i ? other : z[c]) * (i ? z[c + 1] : other);
-                        const int64_t at = offs[c0 + c + i];
-                        if (mine && at >= 0 && QG_OK(qg_in(at + n, 1, (int64_t)a.slots * a.ldy), status, 332)) to[at] = from_f32<O>(o);
+                        const float o = mx_silu<T>(i ? other : z[c]) * (i ? z[c + 1] : other);
+                        const int s = slots[c0 + c + i];
+                        if (mine && s >= 0 && QG_OK(qg_in(s * a.ldy + n, 1, extent), status, 332)) to[s * a.ldy] = from_f32<O>(o);
                     }
                 } else {
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) {
-                        const int64_t at = offs[c0 + c];
-                        if (mine && at >= 0 && QG_OK(qg_in(at + n, 1, (int64_t)a.slots * a.ldy), status, 333))
-                            to[at] = from_f32<O>(__uint_as_float(v[c]) * scales[c0 + c] * f0 * f1);
+                    for (int c = 0; c < 16; c += 4) {
+                        const int4 s = *reinterpret_cast<const int4*>(slots + c0 + c);
+                        const int at[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (mine && at[k] >= 0 && QG_OK(qg_in(at[k] * a.ldy + n, 1, extent), status, 333))
+                                to[at[k] * a.ldy] = from_f32<O>(z[c + k]);
                     }
                 }
             };

@@ -61,13 +61,15 @@ int route_call(int type, RouteArgs a, void* workspace, size_t ws_bytes, void* st
     return launch_route(type, a, static_cast<cudaStream_t>(stream));
 }
 
+// Partial results, then each slot's place among them.
 size_t parts_bytes(int64_t slots, int N) { return ((size_t)slots * N * sizeof(float) + 15) & ~(size_t)15; }
+size_t places_bytes(int64_t slots) { return ((size_t)slots * sizeof(int32_t) + 15) & ~(size_t)15; }
 
 size_t product_workspace(int mode, int type, int tokens, int top_k, int experts, int K, int N)
 {
     if (!known_type(type) || check_slots(tokens, top_k) || check_pack(experts, N, K)) return 0;
     const int64_t slots = (int64_t)tokens * top_k;
-    return (mode == MX_DOWN ? parts_bytes(slots, N) : 0) +
+    return (mode == MX_DOWN ? parts_bytes(slots, N) + places_bytes(slots) : 0) +
            (mx_many_rows(slots, experts) ? mx_planes_bytes(type, mode == MX_DOWN ? slots : tokens, K) : 0);
 }
 
@@ -104,11 +106,16 @@ int product_call(int mode, int type, const void* w, const void* w2, const void* 
     a.x_div = mode == MX_DOWN ? 1 : top_k;
     a.y = mode == MX_DOWN ? workspace : y;
     a.ldy = mode == MX_DOWN ? N : ldy;
-    a.planes = static_cast<uint8_t*>(workspace) + (mode == MX_DOWN ? parts_bytes(a.slots, N) : 0);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    if (mode == MX_DOWN) {
+        a.place_of = reinterpret_cast<int32_t*>(ws + parts_bytes(a.slots, N));
+        ws += parts_bytes(a.slots, N) + places_bytes(a.slots);
+    }
+    a.planes = ws;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     st = launch_mx_gemm(mode, type, a, s);
     if (st || mode != MX_DOWN) return st;
-    return launch_mx_combine(type, static_cast<const float*>(workspace), weights, y, ldy, tokens, top_k, N, s);
+    return launch_mx_combine(type, static_cast<const float*>(workspace), a.place_of, weights, y, ldy, tokens, top_k, N, s);
 }
 
 }  // namespace

@@ -1,6 +1,6 @@
-// The last step of the down product: out[t] = sum_j weight[t][j] part[t k + j], in
-// the order of j, in fp32.  Reads the partial results once; bound by them (HBM, or
-// L2 where they are few).
+// The last step of the down product: out[t] = sum_j weight[t][j] part[place of
+// slot t k + j], in the order of j, in fp32.  Reads the partial results once; bound by
+// them (HBM, or L2 where they are few).
 #include "mxfp4.cuh"
 
 namespace qgemv {
@@ -10,33 +10,37 @@ constexpr int THREADS = 256;
 
 // Four outputs of one token a thread.
 template <typename T>
-__global__ void __launch_bounds__(THREADS) combine_kernel(const float* __restrict__ parts, const float* weights, T* out,
-                                                          int64_t ldo, int tokens, int top_k, int N, int quads, bool wide,
-                                                          unsigned int* status)
+__global__ void __launch_bounds__(THREADS) combine_kernel(const float* __restrict__ parts, const int32_t* place_of,
+                                                          const float* weights, T* out, int64_t ldo, int tokens,
+                                                          int top_k, int N, int quads, bool wide, unsigned int* status)
 {
     pdl_launch_dependents();
     pdl_wait();
     const int64_t all = (int64_t)tokens * quads;
+    const int slots = tokens * top_k;
     for (int64_t i = (int64_t)blockIdx.x * THREADS + threadIdx.x; i < all; i += (int64_t)gridDim.x * THREADS) {
         const int t = (int)(i / quads), n = (int)(i - (int64_t)t * quads) * 4;
-        const float* p = parts + (int64_t)t * top_k * N + n;
         const float* w = weights + (int64_t)t * top_k;
+        const int32_t* places = place_of + (int64_t)t * top_k;
         float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (!QG_OK(qg_in(t * ldo + n, 1, tokens * ldo), status, 320)) continue;
-        if (N % 4 == 0) {
-            for (int j = 0; j < top_k; ++j) {
-                const float4 q = *reinterpret_cast<const float4*>(p + (int64_t)j * N);
-                const float f = w[j];
+#pragma unroll 4
+        for (int j = 0; j < top_k; ++j) {
+            const int at = places[j];
+            if (at < 0 || at >= slots) continue;  // (a slot without an expert)
+            const float f = w[j];
+            const float* p = parts + (int64_t)at * N + n;
+            if (N % 4 == 0) {
+                const float4 q = *reinterpret_cast<const float4*>(p);
                 v[0] = fmaf(f, q.x, v[0]);
                 v[1] = fmaf(f, q.y, v[1]);
                 v[2] = fmaf(f, q.z, v[2]);
                 v[3] = fmaf(f, q.w, v[3]);
-            }
-        } else {
-            for (int j = 0; j < top_k; ++j)
+            } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if (n + k < N) v[k] = fmaf(w[j], p[(int64_t)j * N + k], v[k]);
+                    if (n + k < N) v[k] = fmaf(f, p[k], v[k]);
+            }
         }
         T* o = out + t * ldo + n;
         if (wide) {
@@ -54,7 +58,8 @@ __global__ void __launch_bounds__(THREADS) combine_kernel(const float* __restric
 }
 
 template <typename T>
-int combine_t(const float* parts, const float* weights, void* out, int64_t ldo, int tokens, int top_k, int N, cudaStream_t s)
+int combine_t(const float* parts, const int32_t* place_of, const float* weights, void* out, int64_t ldo, int tokens, int top_k,
+              int N, cudaStream_t s)
 {
     const DeviceInfo di = device_info();
     if (di.sms <= 0) return QGEMV_CUDA_ERROR;
@@ -63,7 +68,7 @@ int combine_t(const float* parts, const float* weights, void* out, int64_t ldo, 
     const bool wide = N % 4 == 0 && ((reinterpret_cast<uintptr_t>(out) | (uintptr_t)(ldo * (int64_t)sizeof(T))) &
                                      (4 * sizeof(T) - 1)) == 0;
     return launch_pdl(combine_kernel<T>, dim3((unsigned)(ctas < di.sms * 8 ? ctas : di.sms * 8)), dim3(THREADS), 0, s,
-                      parts, weights, static_cast<T*>(out), ldo, tokens, top_k, N, quads, wide,
+                      parts, place_of, weights, static_cast<T*>(out), ldo, tokens, top_k, N, quads, wide,
                       wait_timeout_counter()) == cudaSuccess
                ? QGEMV_OK
                : QGEMV_CUDA_ERROR;
@@ -71,12 +76,12 @@ int combine_t(const float* parts, const float* weights, void* out, int64_t ldo, 
 
 }  // namespace
 
-int launch_mx_combine(int type, const float* parts, const float* weights, void* out, int64_t ldo, int tokens, int top_k,
-                      int N, cudaStream_t s)
+int launch_mx_combine(int type, const float* parts, const int32_t* place_of, const float* weights, void* out, int64_t ldo,
+                      int tokens, int top_k, int N, cudaStream_t s)
 {
-    if (type == QGEMV_F32) return combine_t<float>(parts, weights, out, ldo, tokens, top_k, N, s);
-    if (type == QGEMV_F16) return combine_t<__half>(parts, weights, out, ldo, tokens, top_k, N, s);
-    return combine_t<__nv_bfloat16>(parts, weights, out, ldo, tokens, top_k, N, s);
+    if (type == QGEMV_F32) return combine_t<float>(parts, place_of, weights, out, ldo, tokens, top_k, N, s);
+    if (type == QGEMV_F16) return combine_t<__half>(parts, place_of, weights, out, ldo, tokens, top_k, N, s);
+    return combine_t<__nv_bfloat16>(parts, place_of, weights, out, ldo, tokens, top_k, N, s);
 }
 
 bool mx_many_rows(int64_t slots, int experts)

@@ -114,9 +114,10 @@ __device__ int mx_row_tiles(const MxArgs& a, int rows, int* before, int* start, 
     return base;
 }
 
-// The rows of slots that no expert has.
-template <typename O>
-__device__ void mx_zero_rest(const MxArgs& a, O* y, unsigned int* status)
+// The slots that no expert has: rows of zeros, and no place among the partial
+// results.
+template <int MODE, typename O>
+__device__ void mx_rest(const MxArgs& a, O* y, unsigned int* status)
 {
     const int lo = mx_clamped(a.offsets, 0, a.slots), hi = mx_clamped(a.offsets, a.L.experts, a.slots);
     const int rest = lo + a.slots - hi;
@@ -124,9 +125,13 @@ __device__ void mx_zero_rest(const MxArgs& a, O* y, unsigned int* status)
         const int at = i < lo ? i : hi + i - lo;
         const int s = a.order ? a.order[at] : at;
         if (s < 0 || s >= a.slots) continue;
-        for (int n = threadIdx.x; n < a.L.N; n += blockDim.x)
-            if (QG_OK(qg_in((int64_t)s * a.ldy + n, 1, (int64_t)a.slots * a.ldy), status, 310))
-                y[(int64_t)s * a.ldy + n] = from_f32<O>(0.0f);
+        if constexpr (MODE == MX_DOWN) {
+            if (threadIdx.x == 0) a.place_of[s] = -1;
+        } else {
+            for (int n = threadIdx.x; n < a.L.N; n += blockDim.x)
+                if (QG_OK(qg_in((int64_t)s * a.ldy + n, 1, (int64_t)a.slots * a.ldy), status, 310))
+                    y[(int64_t)s * a.ldy + n] = from_f32<O>(0.0f);
+        }
     }
 }
 
@@ -271,7 +276,7 @@ __global__ void __launch_bounds__(MXS_THREADS) mxs_kernel(MxArgs a, MxsPlan p, u
     pdl_wait();
     const int n_rt = mx_row_tiles<MXS_THREADS>(a, p.rows, before, start, sums);
     O* y = static_cast<O*>(a.y);
-    mx_zero_rest(a, y, status);
+    mx_rest<MODE>(a, y, status);
 
     const int parts = p.parts, together = MXS_WARPS / parts;  // tiles that the CTA works on at a time
     const int tiles = a.L.tiles(), units = a.L.units(), groups = (tiles + together - 1) / together;
@@ -332,13 +337,14 @@ __global__ void __launch_bounds__(MXS_THREADS) mxs_kernel(MxArgs a, MxsPlan p, u
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i) issue();
 
-    int rt_now = -1, cnt = 0, stage = 0, flip = 0;
+    int rt_now = -1, cnt = 0, place = 0, stage = 0, flip = 0;
     const uint8_t* xrow[NT];
     for (; at.left > 0; at.next(before, groups)) {
         if (at.rt != rt_now) {
             rt_now = at.rt;
             __syncthreads();  // the rows before are done with
             const int s0 = start[at.e] + (at.rt - before[at.e]) * p.rows;
+            place = s0;
             cnt = min(p.rows, start[at.e + 1] - s0);
             if (threadIdx.x < COLS) {
                 int s = -1;
@@ -347,6 +353,7 @@ __global__ void __launch_bounds__(MXS_THREADS) mxs_kernel(MxArgs a, MxsPlan p, u
                     if (s < 0 || s >= a.slots) s = -1;
                 }
                 slot_of[threadIdx.x] = s;
+                if (MODE == MX_DOWN && s >= 0) a.place_of[s] = s0 + threadIdx.x;  // (whoever has this row tile writes the same)
                 x_exp[threadIdx.x] = 0;
                 x_top[threadIdx.x] = 0;
             }
@@ -435,8 +442,8 @@ __global__ void __launch_bounds__(MXS_THREADS) mxs_kernel(MxArgs a, MxsPlan p, u
             }
         __syncthreads();  // (the exchange has two halves: the next write to this one comes after the next barrier)
         for (int c = (threadIdx.x >> 4) / together; c < cnt; c += MXS_THREADS / 16 / together) {
-            const int s = slot_of[c];
-            if (n >= a.L.N || s < 0) continue;
+            if (n >= a.L.N || slot_of[c] < 0) continue;
+            const int s = MODE == MX_DOWN ? place + c : slot_of[c];  // the output's row
             float v[W];
 #pragma unroll
             for (int w = 0; w < W; ++w) {

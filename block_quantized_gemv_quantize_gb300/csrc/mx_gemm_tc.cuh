@@ -40,6 +40,8 @@ constexpr int MXT_SHIFT = 13;                      // the scales in A are 2^13 t
 // Terms of a row of x; the ring for them: batches of steps, a step being half a
 // row tile of two units of 64 values.  A batch is announced and given back as
 // one.  AHEAD: steps of a converting warp's own ring of codes.
+constexpr int MXT_EPI_BYTES = 2 * 16 * 128 * 4;  // two halves of 16 columns of results
+
 template <int TERMS>
 struct MxtShape {
     static constexpr int BATCH = TERMS == 1 ? 2 : 1, BATCHES = 4, AHEAD = 2;
@@ -57,8 +59,8 @@ constexpr size_t mxt_smem(int experts)
 {
     using S = MxtShape<TERMS>;
     return 1024 + (size_t)S::BATCHES * S::BATCH * 2 * TERMS * (MXT_ROWS / 2) * 128 +
-           (size_t)MXT_CONVERT * S::AHEAD * 4 * MX_UNIT_BYTES + (2 * S::BATCHES + 2 * MXT_A_STAGES + 5) * sizeof(uint64_t) +
-           8 + MXT_EPI * MXT_ROWS * (sizeof(int) + sizeof(float)) + (size_t)(2 * (experts + 1) + 32 + 4) * sizeof(int);
+           (size_t)MXT_CONVERT * S::AHEAD * 4 * MX_UNIT_BYTES + MXT_EPI_BYTES + (2 * S::BATCHES + 2 * MXT_A_STAGES + 5) * sizeof(uint64_t) +
+           8 + 2 * MXT_ROWS * (sizeof(int) + sizeof(float)) + (size_t)(2 * (experts + 1) + 32 + 4) * sizeof(int);
 }
 
 // ---- tcgen05, clusters --------------------------------------------------------
@@ -277,13 +279,14 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
     constexpr int TERM_BYTES = MXT_ROWS / 2 * 128, UNIT_BYTES = TERMS * TERM_BYTES, STEP_BYTES = 2 * UNIT_BYTES;
     extern __shared__ uint8_t sm_raw[];
     uint8_t* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
-    uint64_t* full_b = reinterpret_cast<uint64_t*>(sm + BATCHES * BATCH * STEP_BYTES + MXT_CONVERT * S::AHEAD * 4 * MX_UNIT_BYTES);
+    uint64_t* full_b = reinterpret_cast<uint64_t*>(sm + BATCHES * BATCH * STEP_BYTES + MXT_CONVERT * S::AHEAD * 4 * MX_UNIT_BYTES + MXT_EPI_BYTES);
+    uint8_t* epi_stage = reinterpret_cast<uint8_t*>(full_b) - MXT_EPI_BYTES;
     uint64_t *empty_b = full_b + BATCHES, *full_a = empty_b + BATCHES;
     uint64_t *empty_a = full_a + MXT_A_STAGES, *acc_full = empty_a + MXT_A_STAGES, *acc_empty = acc_full + 2;
     uint64_t* all_done = acc_empty + 2;
     int* epi_slots = reinterpret_cast<int*>(all_done + 1 + (reinterpret_cast<uintptr_t>(all_done + 1) & 8) / 8);
-    float* epi_scale = reinterpret_cast<float*>(epi_slots + MXT_EPI * MXT_ROWS);
-    int* before = reinterpret_cast<int*>(epi_scale + MXT_EPI * MXT_ROWS);
+    float* epi_scale = reinterpret_cast<float*>(epi_slots + 2 * MXT_ROWS);
+    int* before = reinterpret_cast<int*>(epi_scale + 2 * MXT_ROWS);
     int* start = before + a.L.experts + 1;
     int* sums = start + a.L.experts + 1;
     volatile int* gave_up = sums + 32;
@@ -319,7 +322,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
     cluster_barrier();  // both CTAs' barriers and tensor memory are there
     tc_fence_after();
     const uint32_t tmem = *tmem_at;
-    mx_zero_rest(a, static_cast<O*>(a.y), status);
+    mx_rest<MODE>(a, static_cast<O*>(a.y), status);
 
     constexpr int GROUP_TILES = MODE == MX_GATE_UP ? 8 : 16;  // of a pair
     const int units = a.L.units(), steps = (units + 1) / 2, tiles = a.L.tiles();
@@ -570,39 +573,73 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
             }
         }
     } else {
-        // ---- results
+        // ---- results: 16 columns at a time through shared memory, so that a lane stores 16 bytes of a column
+        constexpr int WIDE = MODE == MX_GATE_UP ? 64 : 128;  // neighbouring outputs of a column
+        constexpr int EACH = 16 / sizeof(O), LANES = WIDE / EACH, COLUMNS = 32 / LANES;  // a column's outputs by so many lanes
+        constexpr int PER = (MXT_ROWS + 31) / 32;
         const int quad = warp & 3, i = lane >> 4;
-        int* slots = epi_slots + quad * MXT_ROWS;  // the rows' slots, -1 for none, and powers of two
-        float* scales = epi_scale + quad * MXT_ROWS;
         const uint32_t from = tmem + ((uint32_t)(32 * quad) << 16);
-        const uint8_t* w = weight(i);
         O* y = static_cast<O*>(a.y);
+        O* stage = reinterpret_cast<O*>(epi_stage);
+        // this lane's place among a column's
+        const int in_column = MODE == MX_GATE_UP ? 16 * quad + (lane & 15) : 32 * quad + lane;
+        // An item's slots, their powers of two and this lane's row's, read ahead.
+        int next_slot[PER], next_e;
+        float next_scale[PER];
+        auto look = [&](const MxtWalk& w) {
+#pragma unroll
+            for (int j = 0; j < PER; ++j) next_slot[j] = lane + 32 * j < w.cnt ? mxt_slot(a, w.s0 + lane + 32 * j) : -1;
+            const int tile = w.g * GROUP_TILES + (int)rank * (GROUP_TILES / 2) + (MODE == MX_GATE_UP ? quad : 2 * quad + i);
+            next_e = tile < tiles ? weight(i)[w.e * a.L.expert_bytes() + tile * a.L.tile_bytes() + (int64_t)units * MX_UNIT_BYTES + (lane & 15)]
+                                  : 127;
+        };
+        auto look_scales = [&]() {
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                next_scale[j] = next_slot[j] < 0 || !x.scale ? 1.0f : x.scale[next_slot[j] / a.x_div];
+        };
+        const bool wide = ((reinterpret_cast<uintptr_t>(y) | (uintptr_t)(a.ldy * (int64_t)sizeof(O))) & 15u) == 0;
         MxtStage<2> acc;
-        bool ok = true;
-        for (bool more = walk.find(); more && ok; more = walk.next()) {
+        int half = 0;  // of the staging buffer
+        bool more = walk.find();
+        if (more) {
+            look(walk);
+            look_scales();
+        }
+        while (more) {
+            int* slots = epi_slots + acc.i * MXT_ROWS;  // (the four warps write the same)
+            float* scales = epi_scale + acc.i * MXT_ROWS;
+#pragma unroll
+            for (int j = 0; j < PER; ++j)
+                if (lane + 32 * j < MXT_ROWS) {
+                    slots[lane + 32 * j] = next_slot[j];
+                    scales[lane + 32 * j] = next_scale[j];
+                }
             __syncwarp();
-            for (int r = lane; r < walk.n; r += 32) {
-                const int s = r < walk.cnt ? mxt_slot(a, walk.s0 + r) : -1;
-                slots[r] = s;
-                scales[r] = s < 0 || !x.scale ? 1.0f : x.scale[s / a.x_div];
-            }
-            const int tile = tile_of(quad, i), n = tile * MX_TILE_N + (lane & 15);
-            const bool mine = n < a.L.N;
-            // the row's power of two, in two factors
-            const int e = mine ? w[walk.e * a.L.expert_bytes() + tile * a.L.tile_bytes() + (int64_t)units * MX_UNIT_BYTES + (lane & 15)] : 127;
-            const int p = e - 127 - MXT_SHIFT;
+            // the row's power of two, in two factors of which one nearly always does
+            const int e = next_e, p = e - 127 - MXT_SHIFT;
             const float f0 = e == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(max(p, -126) + 127) << 23);
             const float f1 = __uint_as_float((uint32_t)(min(p + 126, 0) + 127) << 23);
-            __syncwarp();
-            ok = wait(acc_full + acc.i, acc.phase);
-            if (!ok) break;
+            const bool plain = __all_sync(~0u, p >= -126 || e == 255);
+            const int n0 = (walk.g * GROUP_TILES + (int)rank * (GROUP_TILES / 2)) * MX_TILE_N;
+            const int outputs = max(0, min(WIDE, a.L.N - n0)), columns = walk.n;
+            // the output's row of a column: the slot's, of partial results the place's (next to one another: the
+            // slots of an expert are far apart, every row of them on another page of memory)
+            auto out_row = [&](int c) -> int64_t { return slots[c] < 0 ? -1 : MODE == MX_DOWN ? walk.s0 + c : slots[c]; };
+            if (MODE == MX_DOWN && walk.g == 0 && rank == 0 && quad == 0)
+                for (int r = lane; r < walk.cnt; r += 32)
+                    if (slots[r] >= 0) a.place_of[slots[r]] = walk.s0 + r;
+            MxtWalk after = walk;
+            more = after.next();
+            if (more) look(after);
+            if (!wait(acc_full + acc.i, acc.phase)) break;
             tc_fence_after();
-            const bool plain = __all_sync(~0u, p >= -126 || e == 255);  // one factor does
-            // 16 columns a step, the next ones on their way from tensor memory meanwhile
-            auto put = [&](const uint32_t (&v)[16], int c0) {
-                O* to = y + n;
-                const int64_t extent = (int64_t)a.slots * a.ldy;
-                (void)extent;
+            const uint32_t d = from + acc.i * MXT_ROWS;
+            uint32_t v[16];
+            tc_ld_32x32b_x16(d, v);
+#pragma unroll 1
+            for (int c0 = 0; c0 < columns; c0 += 16) {
+                tc_wait_ld();
                 float z[16];
 #pragma unroll
                 for (int c = 0; c < 16; c += 4) {
@@ -612,48 +649,48 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
                     z[c + 2] = __uint_as_float(v[c + 2]) * f.z * f0;
                     z[c + 3] = __uint_as_float(v[c + 3]) * f.w * f0;
                 }
+                if (c0 + 16 < columns) {
+                    tc_ld_32x32b_x16(d + c0 + 16, v);  // on its way meanwhile
+                } else {  // the accumulator is free again
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_first(acc_empty + acc.i);
+                }
+                if (c0 == 0 && more) look_scales();
                 if (!plain)
 #pragma unroll
                     for (int c = 0; c < 16; ++c) z[c] *= f1;
+                O* to = stage + half * (16 * 128) + in_column;
                 if constexpr (MODE == MX_GATE_UP) {
                     // a lane of the gate's rows and the one of the same row of up
                     // have two columns: one each
 #pragma unroll
                     for (int c = 0; c < 16; c += 2) {
                         const float other = __shfl_xor_sync(~0u, i ? z[c] : z[c + 1], 16);
-                        const float o = mx_silu<T>(i ? other : z[c]) * (i ? z[c + 1] : other);
-                        const int s = slots[c0 + c + i];
-                        if (mine && s >= 0 && QG_OK(qg_in(s * a.ldy + n, 1, extent), status, 332)) to[s * a.ldy] = from_f32<O>(o);
+                        to[(c + i) * WIDE] = from_f32<O>(mx_silu<T>(i ? other : z[c]) * (i ? z[c + 1] : other));
                     }
                 } else {
 #pragma unroll
-                    for (int c = 0; c < 16; c += 4) {
-                        const int4 s = *reinterpret_cast<const int4*>(slots + c0 + c);
-                        const int at[4] = {s.x, s.y, s.z, s.w};
+                    for (int c = 0; c < 16; ++c) to[c * WIDE] = from_f32<O>(z[c]);
+                }
+                asm volatile("bar.sync 1, %0;" ::"n"(MXT_EPI * 32) : "memory");  // (the next write to this half comes after the next one)
+                const O* have = stage + half * (16 * 128);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (mine && at[k] >= 0 && QG_OK(qg_in(at[k] * a.ldy + n, 1, extent), status, 333))
-                                to[at[k] * a.ldy] = from_f32<O>(z[c + k]);
-                    }
+                for (int j = 0; j < 16; j += 4 * COLUMNS) {
+                    const int c = j + quad * COLUMNS + lane / LANES, r = lane % LANES * EACH;
+                    const int64_t s = out_row(c0 + c);
+                    O* at = y + s * a.ldy + n0 + r;
+                    if (s < 0 || r >= outputs || !QG_OK(qg_in(s * a.ldy + n0 + r, min(EACH, outputs - r), (int64_t)a.slots * a.ldy), status, 332))
+                        continue;
+                    if (wide && r + EACH <= outputs)
+                        *reinterpret_cast<uint4*>(at) = *reinterpret_cast<const uint4*>(have + c * WIDE + r);
+                    else
+                        for (int k = 0; k < EACH && r + k < outputs; ++k) at[k] = have[c * WIDE + r + k];
                 }
-            };
-            const uint32_t d = from + acc.i * MXT_ROWS;
-            uint32_t va[16], vb[16];
-            tc_ld_32x32b_x16(d, va);
-            for (int c0 = 0; c0 < walk.n; c0 += 32) {
-                tc_wait_ld();
-                if (c0 + 16 < walk.n) tc_ld_32x32b_x16(d + c0 + 16, vb);
-                put(va, c0);
-                if (c0 + 16 < walk.n) {
-                    tc_wait_ld();
-                    if (c0 + 32 < walk.n) tc_ld_32x32b_x16(d + c0 + 32, va);
-                    put(vb, c0 + 16);
-                }
+                half ^= 1;
             }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_first(acc_empty + acc.i);
             acc.next();
+            walk = after;
         }
     }
     if (warp == MXT_MMA_WARP && rank == 0) {  // what was issued ends before tensor memory is given back

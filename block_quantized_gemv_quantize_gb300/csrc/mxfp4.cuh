@@ -93,7 +93,8 @@ struct MxArgs {
     const int32_t* order;  // null: slot i is row i
     int slots, top_k;      // x's row of slot s is s / x_div
     int x_div;
-    void* y;               // gemm, gate_up: [slots]; down: fp32 partial results [slots][N]
+    void* y;               // gemm, gate_up: [slots]; down: fp32 partial results [place][N]
+    int32_t* place_of;     // down, [slots]: a slot's place (its row of the partial results), -1 for none
     void* planes;          // workspace for rows of x as halves (mx_planes_bytes)
 };
 
@@ -103,7 +104,7 @@ bool mx_many_rows(int64_t slots, int experts);
 size_t mx_planes_bytes(int type, int64_t rows, int K);
 
 int launch_mx_gemm(int mode, int type, const MxArgs& a, cudaStream_t s);
-int launch_mx_combine(int type, const float* parts, const float* weights, void* out, int64_t ldo, int tokens,
+int launch_mx_combine(int type, const float* parts, const int32_t* place_of, const float* weights, void* out, int64_t ldo, int tokens,
                       int top_k, int N, cudaStream_t s);
 
 }  // namespace qgemv

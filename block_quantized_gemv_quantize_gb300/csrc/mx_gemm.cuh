@@ -25,7 +25,9 @@
 
 namespace qgemv {
 
-constexpr int MXS_THREADS = 256, MXS_WARPS = MXS_THREADS / 32;
+// Warps of a CTA (one an SM), for row tiles of 8 NT: as many as their registers let run.
+template <int NT>
+constexpr int MXS_WARPS = NT == 1 ? 24 : 16;
 constexpr int MXS_RED = 20;  // floats of a column of 16 in the exchange (no bank conflicts)
 
 // Halves that a value of a row of x takes.
@@ -44,6 +46,10 @@ struct MxsPlan {
 __device__ __forceinline__ void cp_async16(void* smem, const void* gmem)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(gmem));
+}
+__device__ __forceinline__ void cp_async16(uint32_t smem, const void* gmem)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(gmem));
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -185,7 +191,7 @@ __device__ __forceinline__ void mx_row_halves(const float (&v)[8], float f, __ha
 // block has 16 bytes for each t, values 4 t .. 4 t + 3 and 16 + 4 t .. 16 + 4 t
 // + 3.  A warp takes 256 values of a row at a time, a lane eight neighbouring
 // ones: half a piece of two t each.
-template <typename T>
+template <typename T, int WARPS>
 __device__ void mxs_stage(const MxArgs& a, const MxsPlan& p, uint8_t* xs, const int* slot_of, int* x_exp,
                           uint32_t* x_top, int cnt, unsigned int* status)
 {
@@ -196,7 +202,7 @@ __device__ void mxs_stage(const MxArgs& a, const MxsPlan& p, uint8_t* xs, const 
     const T* x = static_cast<const T*>(a.x);
     const bool wide = ((reinterpret_cast<uintptr_t>(x) | (uintptr_t)(a.ldx * (int64_t)sizeof(T))) & 15u) == 0;
     if constexpr (SCALED) {
-        for (int i = warp; i < cnt * pieces; i += MXS_WARPS) {
+        for (int i = warp; i < cnt * pieces; i += WARPS) {
             const int row = i / pieces, k = (i - row * pieces) * 256 + lane * 8, s = max(0, slot_of[row]);
             float v[8];
             mx_load8(x + (int64_t)(s / a.x_div) * a.ldx + k, wide, max(0, K - k), v);
@@ -213,7 +219,7 @@ __device__ void mxs_stage(const MxArgs& a, const MxsPlan& p, uint8_t* xs, const 
         if ((int)threadIdx.x < cnt) x_exp[threadIdx.x] = mx_row_exponent(x_top[threadIdx.x]);
         __syncthreads();
     }
-    for (int i = warp; i < cnt * pieces; i += MXS_WARPS) {
+    for (int i = warp; i < cnt * pieces; i += WARPS) {
         const int row = i / pieces, k = (i - row * pieces) * 256 + lane * 8, s = max(0, slot_of[row]);
         if (k >= padded) continue;
         float v[8];
@@ -254,17 +260,17 @@ struct MxCursor {
 };
 
 template <typename T, int NT, int MODE, int STAGES>
-__global__ void __launch_bounds__(MXS_THREADS) mxs_kernel(MxArgs a, MxsPlan p, unsigned int* status)
+__global__ void __launch_bounds__(MXS_WARPS<NT> * 32, 1) mxs_kernel(MxArgs a, MxsPlan p, unsigned int* status)
 {
     using O = typename std::conditional<MODE == MX_DOWN, float, T>::type;
     constexpr int W = MODE == MX_GATE_UP ? 2 : 1, TERMS = MX_TERMS<T>;
-    constexpr int COLS = 8 * NT, STAGE = W * MX_UNIT_BYTES;
+    constexpr int COLS = 8 * NT, STAGE = W * MX_UNIT_BYTES, WARPS = MXS_WARPS<NT>;
     extern __shared__ __align__(16) uint8_t sm[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     uint8_t* ring = sm + warp * (STAGES * STAGE);
-    float* red = reinterpret_cast<float*>(sm + MXS_WARPS * STAGES * STAGE);
-    constexpr int RED_ONE = MXS_WARPS * W * COLS * MXS_RED;
-    uint8_t* xs = reinterpret_cast<uint8_t*>(red + 2 * RED_ONE);
+    float* red = reinterpret_cast<float*>(sm + WARPS * STAGES * STAGE);
+    constexpr int RED_ONE = WARPS * W * COLS * MXS_RED;
+    uint8_t* xs = reinterpret_cast<uint8_t*>(red + RED_ONE);
     int* before = reinterpret_cast<int*>(xs + (size_t)p.rows * TERMS * p.x_bytes);
     int* start = before + a.L.experts + 1;
     int* sums = start + a.L.experts + 1;
@@ -274,11 +280,11 @@ __global__ void __launch_bounds__(MXS_THREADS) mxs_kernel(MxArgs a, MxsPlan p, u
 
     pdl_launch_dependents();
     pdl_wait();
-    const int n_rt = mx_row_tiles<MXS_THREADS>(a, p.rows, before, start, sums);
+    const int n_rt = mx_row_tiles<WARPS * 32>(a, p.rows, before, start, sums);
     O* y = static_cast<O*>(a.y);
     mx_rest<MODE>(a, y, status);
 
-    const int parts = p.parts, together = MXS_WARPS / parts;  // tiles that the CTA works on at a time
+    const int parts = p.parts, together = WARPS / parts;  // tiles that the CTA works on at a time
     const int tiles = a.L.tiles(), units = a.L.units(), groups = (tiles + together - 1) / together;
     const int64_t items = (int64_t)n_rt * groups;
     const int64_t i0 = items * blockIdx.x / gridDim.x, i1 = items * (blockIdx.x + 1) / gridDim.x;
@@ -299,37 +305,36 @@ __global__ void __launch_bounds__(MXS_THREADS) mxs_kernel(MxArgs a, MxsPlan p, u
     }
     MxCursor at = load;
 
-    int load_u = u1, load_stage = 0;
-    const uint8_t *lw = nullptr, *lw2 = nullptr;
+    int load_n = 0, load_stage = 0;  // units left of the item, stage of the next one
     bool load_first = true;
+    // this lane's 16 bytes of a unit's codes, of both weights, and of its scales (lanes 0 and 1, of both 0 .. 3)
+    const uint8_t *lw = nullptr, *lw2 = nullptr, *ls = nullptr;
+    const uint32_t ring_at = smem_u32(ring) + lane * 16;
+    const uint32_t ring_scale = smem_u32(ring) + (lane >> 1) * MX_UNIT_BYTES + MX_UNIT_CODES + (lane & 1) * 16;
     // One more unit of the warp's stream into the ring (or an empty group at its end).
     auto issue = [&]() {
-        while (load_u >= u1 && load.left > 0) {  // the next item that has units for this warp
+        while (load_n == 0 && load.left > 0) {  // the next item that has units for this warp
             if (!load_first) load.next(before, groups);
             load_first = false;
             if (load.left > 0 && load.g * together + mine < tiles && u0 < u1) {
-                const int64_t off = load.e * expert_bytes + (int64_t)(load.g * together + mine) * tile_bytes;
-                lw = a.w + off;
-                if constexpr (W == 2) lw2 = a.w2 + off;
-                load_u = u0;
+                const int64_t off = load.e * expert_bytes + (int64_t)(load.g * together + mine) * tile_bytes + (int64_t)u0 * MX_UNIT_BYTES;
+                lw = a.w + off + lane * 16;
+                if constexpr (W == 2) lw2 = a.w2 + off + lane * 16;
+                ls = (W == 2 && lane >= 2 ? a.w2 : a.w) + off + MX_UNIT_CODES + (lane & 1) * 16;
+                load_n = u1 - u0;
             }
         }
-        if (load.left > 0) {
-            uint8_t* to = ring + load_stage * STAGE;
-            const int64_t off = (int64_t)load_u * MX_UNIT_BYTES;
-            if (QG_OK(qg_in(lw - a.w + off, MX_UNIT_BYTES, a.L.bytes()), status, 311)) {
-                cp_async16(to + lane * 16, lw + off + lane * 16);
-                if constexpr (W == 2) {
-                    cp_async16(to + MX_UNIT_BYTES + lane * 16, lw2 + off + lane * 16);
-                    if (lane < 4) {
-                        const int o = MX_UNIT_CODES + (lane & 1) * 16;
-                        cp_async16(to + (lane >> 1) * MX_UNIT_BYTES + o, (lane < 2 ? lw : lw2) + off + o);
-                    }
-                } else if (lane < 2) {
-                    cp_async16(to + MX_UNIT_CODES + lane * 16, lw + off + MX_UNIT_CODES + lane * 16);
-                }
+        if (load_n > 0) {
+            const uint32_t to = load_stage * STAGE;
+            if (QG_OK(qg_in(lw - lane * 16 - a.w, MX_UNIT_BYTES, a.L.bytes()), status, 311)) {
+                cp_async16(ring_at + to, lw);
+                if constexpr (W == 2) cp_async16(ring_at + to + MX_UNIT_BYTES, lw2);
+                if (lane < 2 * W) cp_async16(ring_scale + to, ls);
             }
-            ++load_u;
+            lw += MX_UNIT_BYTES;
+            if constexpr (W == 2) lw2 += MX_UNIT_BYTES;
+            ls += MX_UNIT_BYTES;
+            --load_n;
             if (++load_stage == STAGES) load_stage = 0;
         }
         cp_async_commit();
@@ -337,7 +342,12 @@ __global__ void __launch_bounds__(MXS_THREADS) mxs_kernel(MxArgs a, MxsPlan p, u
 #pragma unroll
     for (int i = 0; i < STAGES - 1; ++i) issue();
 
-    int rt_now = -1, cnt = 0, place = 0, stage = 0, flip = 0;
+    // the warps of a tile (a barrier of their own, so that tiles run on their own)
+    auto together_barrier = [&]() {
+        if (parts > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + mine), "r"(parts * 32) : "memory");
+        else __syncwarp();
+    };
+    int rt_now = -1, cnt = 0, place = 0, stage = 0;
     const uint8_t* xrow[NT];
     for (; at.left > 0; at.next(before, groups)) {
         if (at.rt != rt_now) {
@@ -358,17 +368,16 @@ __global__ void __launch_bounds__(MXS_THREADS) mxs_kernel(MxArgs a, MxsPlan p, u
                 x_top[threadIdx.x] = 0;
             }
             __syncthreads();
-            mxs_stage<T>(a, p, xs, slot_of, x_exp, x_top, cnt, status);
+            mxs_stage<T, WARPS>(a, p, xs, slot_of, x_exp, x_top, cnt, status);
 #pragma unroll
             for (int n = 0; n < NT; ++n)  // (columns behind the last row repeat it and go nowhere)
                 xrow[n] = xs + (size_t)min(8 * n + g, cnt - 1) * TERMS * p.x_bytes + t * 16;
         }
-        // this thread's row of the group in the epilogue, and its scale
-        const int out_n = threadIdx.x & 15, out_tile = (threadIdx.x >> 4) % together;
-        const int tile = at.g * together + out_tile, n = tile * MX_TILE_N + out_n;
+        // this thread's row of the tile in the epilogue, and its scale
+        const int tile = at.g * together + mine, n = tile * MX_TILE_N + (lane & 15);
         int top = 0, top2 = 0;
         if (n < a.L.N) {
-            const int64_t o = at.e * expert_bytes + tile * tile_bytes + (int64_t)units * MX_UNIT_BYTES + out_n;
+            const int64_t o = at.e * expert_bytes + tile * tile_bytes + (int64_t)units * MX_UNIT_BYTES + (lane & 15);
             top = a.w[o];
             if constexpr (W == 2) top2 = a.w2[o];
         }
@@ -379,7 +388,8 @@ __global__ void __launch_bounds__(MXS_THREADS) mxs_kernel(MxArgs a, MxsPlan p, u
             for (int i = 0; i < NT; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) acc[w][i][j] = 0.0f;
-        if (at.g * together + mine < tiles)
+        if (tile < tiles)
+#pragma unroll 1
             for (int u = u0; u < u1; ++u) {
                 cp_async_wait<STAGES - 2>();
                 __syncwarp();
@@ -419,36 +429,36 @@ __global__ void __launch_bounds__(MXS_THREADS) mxs_kernel(MxArgs a, MxsPlan p, u
                                 mma_f16(c, ag[w][0], ah[w][0], ag[w][1], ah[w][1], x[k].x, x[k].y);
                                 mma_f16(c, ag[w][2], ah[w][2], ag[w][3], ah[w][3], x[k].z, x[k].w);
                             }
-                            acc[w][i][0] = fmaf(c[0], sg[w], acc[w][i][0]);
-                            acc[w][i][1] = fmaf(c[1], sg[w], acc[w][i][1]);
-                            acc[w][i][2] = fmaf(c[2], sh[w], acc[w][i][2]);
-                            acc[w][i][3] = fmaf(c[3], sh[w], acc[w][i][3]);
+                            fma_f32x2(acc[w][i][0], acc[w][i][1], c[0], c[1], sg[w], sg[w]);
+                            fma_f32x2(acc[w][i][2], acc[w][i][3], c[2], c[3], sh[w], sh[w]);
                         }
                     }
                 }
             }
-        float* r = red + flip * RED_ONE;
-        flip ^= 1;
+        // the warps of a tile add up and write it on their own
+        float* r = red + (warp - part) * (W * COLS * MXS_RED);
 #pragma unroll
         for (int w = 0; w < W; ++w)
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
                 if (8 * i >= cnt) break;
-                float* c = r + ((warp * W + w) * COLS + 8 * i + 2 * t) * MXS_RED + g;
+                float* c = r + ((part * W + w) * COLS + 8 * i + 2 * t) * MXS_RED + g;
                 c[0] = acc[w][i][0];
                 c[MXS_RED] = acc[w][i][1];
                 c[8] = acc[w][i][2];
                 c[MXS_RED + 8] = acc[w][i][3];
             }
-        __syncthreads();  // (the exchange has two halves: the next write to this one comes after the next barrier)
-        for (int c = (threadIdx.x >> 4) / together; c < cnt; c += MXS_THREADS / 16 / together) {
+        together_barrier();
+        for (int c = 2 * part + (lane >> 4); c < cnt; c += 2 * parts) {
             if (n >= a.L.N || slot_of[c] < 0) continue;
             const int s = MODE == MX_DOWN ? place + c : slot_of[c];  // the output's row
             float v[W];
 #pragma unroll
             for (int w = 0; w < W; ++w) {
+                const float* from = r + (w * COLS + c) * MXS_RED + (lane & 15);
                 float sum = 0.0f;
-                for (int k = 0; k < parts; ++k) sum += r[(((out_tile * parts + k) * W + w) * COLS + c) * MXS_RED + out_n];
+#pragma unroll 4
+                for (int k = 0; k < parts; ++k) sum += from[k * (W * COLS * MXS_RED)];
                 const int e = w ? top2 : top;
                 v[w] = e == 255 ? __uint_as_float(0x7FC00000u) : mul_pow2(sum, e - 127 + x_exp[c]);
             }
@@ -457,6 +467,7 @@ __global__ void __launch_bounds__(MXS_THREADS) mxs_kernel(MxArgs a, MxsPlan p, u
             if (QG_OK(qg_in((int64_t)s * a.ldy + n, 1, (int64_t)a.slots * a.ldy), status, 312))
                 y[(int64_t)s * a.ldy + n] = from_f32<O>(o);
         }
+        together_barrier();
     }
     cp_async_wait<0>();
 }

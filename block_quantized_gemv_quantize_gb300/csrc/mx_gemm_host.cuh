@@ -8,37 +8,35 @@
 
 namespace qgemv {
 
-constexpr int MXS_STAGES = 6;  // of a warp's ring: 8 warps x 6 x 544 B (twice for a pair of weights)
+// Stages of a warp's ring, 544 B each (twice that for a pair of weights, which takes fewer).
+template <int MODE>
+constexpr int MXS_STAGES = MODE == MX_GATE_UP ? 4 : 6;
 
 // Rows a tile, warps a tile's K, CTAs.
 template <typename T, int NT, int MODE>
 bool mxs_plan(const DeviceInfo& di, const MxArgs& a, MxsPlan& p)
 {
-    constexpr int W = MODE == MX_GATE_UP ? 2 : 1, TERMS = MX_TERMS<T>, COLS = 8 * NT;
+    constexpr int W = MODE == MX_GATE_UP ? 2 : 1, TERMS = MX_TERMS<T>, COLS = 8 * NT, WARPS = MXS_WARPS<NT>;
     const int units = a.L.units();
-    p.stages = MXS_STAGES;
+    p.stages = MXS_STAGES<MODE>;
     p.x_bytes = units * MX_UNIT_K * 2 + 64;  // (neighbouring rows half of the banks apart)
-    const size_t fixed = (size_t)MXS_WARPS * MXS_STAGES * W * MX_UNIT_BYTES +
-                         2u * MXS_WARPS * W * COLS * MXS_RED * sizeof(float) +
+    const size_t fixed = (size_t)WARPS * p.stages * W * MX_UNIT_BYTES + WARPS * W * COLS * MXS_RED * sizeof(float) +
                          (size_t)(2 * (a.L.experts + 1) + 32 + 3 * COLS) * sizeof(int);
     const size_t row = (size_t)TERMS * p.x_bytes;
     const int want = std::max(1, std::min(COLS, a.slots));
-    // two CTAs an SM where that leaves the row tiles half of what they want
-    size_t each = ((size_t)di.smem_optin + 1024) / 2 - 1024;
-    int fit = each > fixed ? (int)((each - fixed) / row) : 0;
-    int ctas = 2;
-    if (2 * fit < want) {
-        each = di.smem_optin;
-        fit = each > fixed ? (int)((each - fixed) / row) : 0;
-        ctas = 1;
-    }
+    const int fit = (size_t)di.smem_optin > fixed ? (int)(((size_t)di.smem_optin - fixed) / row) : 0;
     if (fit < 1) return false;
     p.rows = std::min(want, fit);
     p.smem = fixed + row * p.rows;
-    p.parts = units >= 32 ? 8 : units >= 12 ? 4 : units >= 4 ? 2 : 1;
-    const int groups = (a.L.tiles() * p.parts + MXS_WARPS - 1) / MXS_WARPS;
+    // as few warps a tile as leave two and a half tiles' parts for each warp of the GPU, of three units at least
+    const int64_t tiles = (int64_t)a.L.tiles() * std::min<int64_t>(a.L.experts, a.slots), warps = (int64_t)di.sms * WARPS;
+    static constexpr int PARTS[2][5] = {{2, 4, 8, 12, 24}, {2, 4, 8, 16, 16}};
+    int i = 0;
+    while (i < 4 && tiles * PARTS[NT > 1][i] * 2 < warps * 5 && units >= PARTS[NT > 1][i + 1] * 3) ++i;
+    p.parts = PARTS[NT > 1][i];
+    const int groups = (a.L.tiles() * p.parts + WARPS - 1) / WARPS;
     const int64_t most = (int64_t)groups * std::min<int64_t>(a.slots, (int64_t)a.slots / p.rows + a.L.experts);
-    p.grid = (int)std::min<int64_t>(most, (int64_t)di.sms * ctas);
+    p.grid = (int)std::min<int64_t>(most, di.sms);
     return true;
 }
 
@@ -50,7 +48,7 @@ int launch_mxs(const MxArgs& a, cudaStream_t s)
     if (di.sms <= 0 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return QGEMV_CUDA_ERROR;
     MxsPlan p;
     if (!mxs_plan<T, NT, MODE>(di, a, p)) return QGEMV_UNSUPPORTED_SHAPE;
-    auto kern = mxs_kernel<T, NT, MODE, MXS_STAGES>;
+    auto kern = mxs_kernel<T, NT, MODE, MXS_STAGES<MODE>>;
     static std::once_flag once[64];
     static bool ok[64];
     std::call_once(once[dev], [&]() {
@@ -58,7 +56,7 @@ int launch_mxs(const MxArgs& a, cudaStream_t s)
         if (!ok[dev]) cudaGetLastError();
     });
     if (!ok[dev]) return QGEMV_CUDA_ERROR;
-    return launch_pdl(kern, dim3((unsigned)p.grid), dim3(MXS_THREADS), p.smem, s, a, p, wait_timeout_counter()) == cudaSuccess
+    return launch_pdl(kern, dim3((unsigned)p.grid), dim3(MXS_WARPS<NT> * 32), p.smem, s, a, p, wait_timeout_counter()) == cudaSuccess
                ? QGEMV_OK
                : QGEMV_CUDA_ERROR;
 }
@@ -118,10 +116,15 @@ int launch_mxt(const MxArgs& a, cudaStream_t s)
 template <typename T, int MODE>
 int launch_mx_mode(const MxArgs& a, cudaStream_t s)
 {
+#ifndef EXP_FORCE
     if (mx_many_rows(a.slots, a.L.experts)) return launch_mxt<T, MODE>(a, s);
+#endif
+#ifdef EXP_FORCE
+    return EXP_FORCE == 9 ? launch_mxt<T, MODE>(a, s) : EXP_FORCE == 1 ? launch_mxs<T, 1, MODE>(a, s) : EXP_FORCE == 2 ? launch_mxs<T, 2, MODE>(a, s) : launch_mxs<T, 4, MODE>(a, s);
+#endif
     const double rows = (double)a.slots / (double)std::min<int64_t>(a.L.experts, a.slots);  // of an expert that has any, about
     if (rows <= 6.0) return launch_mxs<T, 1, MODE>(a, s);
-    const int status = launch_mxs<T, 4, MODE>(a, s);
+    const int status = launch_mxs<T, 2, MODE>(a, s);
     return status == QGEMV_UNSUPPORTED_SHAPE ? launch_mxs<T, 1, MODE>(a, s) : status;
 }
 

@@ -26,8 +26,12 @@
 namespace qgemv {
 
 // Warps of a CTA (one an SM), for row tiles of 8 NT: as many as their registers let run.
-template <int NT>
-constexpr int MXS_WARPS = NT == 1 ? 24 : 16;
+template <int NT, int W>
+#ifdef EXP_WARPS
+constexpr int MXS_WARPS = NT == 1 ? EXP_WARPS : 16;
+#else
+constexpr int MXS_WARPS = NT == 1 && W == 1 ? 24 : 16;
+#endif
 constexpr int MXS_RED = 20;  // floats of a column of 16 in the exchange (no bank conflicts)
 
 // Halves that a value of a row of x takes.
@@ -243,28 +247,49 @@ __device__ void mxs_stage(const MxArgs& a, const MxsPlan& p, uint8_t* xs, const 
     __syncthreads();
 }
 
-// Where a warp is in its CTA's range.
+// Where a warp is in its CTA's range of tiles: tile `tile` of row tile rt, whose
+// tiles below `end` are the CTA's, `left` tiles after those.  The warps of a tile
+// take every step-th one from `first` on.
 struct MxCursor {
-    int64_t left;   // items
-    int rt, g, e;   // row tile of all, group of tiles, expert
-    __device__ void next(const int* before, int groups)
+    int64_t left;
+    int rt, e, tile, end, tiles, first, step;
+    __device__ void start(int64_t i0, int64_t i1, int all_tiles, int mine, int together, const int* before, int experts)
     {
-        --left;
-        if (++g == groups) {
-            g = 0;
-            ++rt;
-            if (left > 0)
-                while (rt >= before[e + 1]) ++e;
+        tiles = all_tiles;
+        first = mine;
+        step = together;
+        rt = (int)(i0 / tiles);
+        const int lo_tile = (int)(i0 - (int64_t)rt * tiles);
+        end = (int)min((int64_t)tiles, lo_tile + (i1 - i0));
+        left = i1 - i0 - (end - lo_tile);
+        tile = lo_tile + first;
+        int lo = 0, hi = experts - 1;  // the last expert with before[e] <= rt: it has that row tile
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (before[mid] <= rt) lo = mid;
+            else hi = mid - 1;
         }
+        e = lo;
+    }
+    // The next row tile of the range, if there is one.
+    __device__ bool next_rows(const int* before)
+    {
+        if (left == 0) return false;
+        ++rt;
+        while (rt >= before[e + 1]) ++e;
+        end = (int)min((int64_t)tiles, left);
+        left -= end;
+        tile = first;
+        return true;
     }
 };
 
 template <typename T, int NT, int MODE, int STAGES>
-__global__ void __launch_bounds__(MXS_WARPS<NT> * 32, 1) mxs_kernel(MxArgs a, MxsPlan p, unsigned int* status)
+__global__ void __launch_bounds__(MXS_WARPS<NT, MODE == MX_GATE_UP ? 2 : 1> * 32, 1) mxs_kernel(MxArgs a, MxsPlan p, unsigned int* status)
 {
     using O = typename std::conditional<MODE == MX_DOWN, float, T>::type;
     constexpr int W = MODE == MX_GATE_UP ? 2 : 1, TERMS = MX_TERMS<T>;
-    constexpr int COLS = 8 * NT, STAGE = W * MX_UNIT_BYTES, WARPS = MXS_WARPS<NT>;
+    constexpr int COLS = 8 * NT, STAGE = W * MX_UNIT_BYTES, WARPS = MXS_WARPS<NT, W>;
     extern __shared__ __align__(16) uint8_t sm[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     uint8_t* ring = sm + warp * (STAGES * STAGE);
@@ -285,44 +310,39 @@ __global__ void __launch_bounds__(MXS_WARPS<NT> * 32, 1) mxs_kernel(MxArgs a, Mx
     mx_rest<MODE>(a, y, status);
 
     const int parts = p.parts, together = WARPS / parts;  // tiles that the CTA works on at a time
-    const int tiles = a.L.tiles(), units = a.L.units(), groups = (tiles + together - 1) / together;
-    const int64_t items = (int64_t)n_rt * groups;
+    const int tiles = a.L.tiles(), units = a.L.units();
+    const int64_t items = (int64_t)n_rt * tiles;
     const int64_t i0 = items * blockIdx.x / gridDim.x, i1 = items * (blockIdx.x + 1) / gridDim.x;
     if (i0 >= i1) return;
     const int mine = warp / parts, part = warp % parts;
     const int u0 = units * part / parts, u1 = units * (part + 1) / parts;
     const int64_t tile_bytes = a.L.tile_bytes(), expert_bytes = a.L.expert_bytes();
 
-    MxCursor load{i1 - i0, (int)(i0 / groups), (int)(i0 % groups), 0};
-    {
-        int lo = 0, hi = a.L.experts - 1;  // the last expert with before[e] <= rt: it has that row tile
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (before[mid] <= load.rt) lo = mid;
-            else hi = mid - 1;
-        }
-        load.e = lo;
-    }
+    MxCursor load;
+    load.start(i0, i1, tiles, mine, together, before, a.L.experts);
     MxCursor at = load;
 
     int load_n = 0, load_stage = 0;  // units left of the item, stage of the next one
-    bool load_first = true;
+    bool load_more = u0 < u1;
+    load.tile -= together;  // (one before the first)
     // this lane's 16 bytes of a unit's codes, of both weights, and of its scales (lanes 0 and 1, of both 0 .. 3)
     const uint8_t *lw = nullptr, *lw2 = nullptr, *ls = nullptr;
     const uint32_t ring_at = smem_u32(ring) + lane * 16;
     const uint32_t ring_scale = smem_u32(ring) + (lane >> 1) * MX_UNIT_BYTES + MX_UNIT_CODES + (lane & 1) * 16;
     // One more unit of the warp's stream into the ring (or an empty group at its end).
     auto issue = [&]() {
-        while (load_n == 0 && load.left > 0) {  // the next item that has units for this warp
-            if (!load_first) load.next(before, groups);
-            load_first = false;
-            if (load.left > 0 && load.g * together + mine < tiles && u0 < u1) {
-                const int64_t off = load.e * expert_bytes + (int64_t)(load.g * together + mine) * tile_bytes + (int64_t)u0 * MX_UNIT_BYTES;
-                lw = a.w + off + lane * 16;
-                if constexpr (W == 2) lw2 = a.w2 + off + lane * 16;
-                ls = (W == 2 && lane >= 2 ? a.w2 : a.w) + off + MX_UNIT_CODES + (lane & 1) * 16;
-                load_n = u1 - u0;
+        while (load_n == 0 && load_more) {  // the next tile
+            load.tile += together;
+            if (load.tile >= load.end) {
+                load_more = load.next_rows(before);
+                load.tile -= together;
+                continue;
             }
+            const int64_t off = load.e * expert_bytes + load.tile * tile_bytes + (int64_t)u0 * MX_UNIT_BYTES;
+            lw = a.w + off + lane * 16;
+            if constexpr (W == 2) lw2 = a.w2 + off + lane * 16;
+            ls = (W == 2 && lane >= 2 ? a.w2 : a.w) + off + MX_UNIT_CODES + (lane & 1) * 16;
+            load_n = u1 - u0;
         }
         if (load_n > 0) {
             const uint32_t to = load_stage * STAGE;
@@ -347,48 +367,44 @@ __global__ void __launch_bounds__(MXS_WARPS<NT> * 32, 1) mxs_kernel(MxArgs a, Mx
         if (parts > 1) asm volatile("bar.sync %0, %1;" ::"r"(1 + mine), "r"(parts * 32) : "memory");
         else __syncwarp();
     };
-    int rt_now = -1, cnt = 0, place = 0, stage = 0;
+    int stage = 0;
     const uint8_t* xrow[NT];
-    for (; at.left > 0; at.next(before, groups)) {
-        if (at.rt != rt_now) {
-            rt_now = at.rt;
-            __syncthreads();  // the rows before are done with
-            const int s0 = start[at.e] + (at.rt - before[at.e]) * p.rows;
-            place = s0;
-            cnt = min(p.rows, start[at.e + 1] - s0);
-            if (threadIdx.x < COLS) {
-                int s = -1;
-                if ((int)threadIdx.x < cnt) {
-                    s = a.order ? a.order[s0 + threadIdx.x] : s0 + (int)threadIdx.x;
-                    if (s < 0 || s >= a.slots) s = -1;
-                }
-                slot_of[threadIdx.x] = s;
-                if (MODE == MX_DOWN && s >= 0) a.place_of[s] = s0 + threadIdx.x;  // (whoever has this row tile writes the same)
-                x_exp[threadIdx.x] = 0;
-                x_top[threadIdx.x] = 0;
+    do {
+        __syncthreads();  // the rows before are done with
+        const int place = start[at.e] + (at.rt - before[at.e]) * p.rows, cnt = min(p.rows, start[at.e + 1] - place);
+        if (threadIdx.x < COLS) {
+            int s = -1;
+            if ((int)threadIdx.x < cnt) {
+                s = a.order ? a.order[place + threadIdx.x] : place + (int)threadIdx.x;
+                if (s < 0 || s >= a.slots) s = -1;
             }
-            __syncthreads();
-            mxs_stage<T, WARPS>(a, p, xs, slot_of, x_exp, x_top, cnt, status);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)  // (columns behind the last row repeat it and go nowhere)
-                xrow[n] = xs + (size_t)min(8 * n + g, cnt - 1) * TERMS * p.x_bytes + t * 16;
+            slot_of[threadIdx.x] = s;
+            if (MODE == MX_DOWN && s >= 0) a.place_of[s] = place + threadIdx.x;  // (whoever has this row tile writes the same)
+            x_exp[threadIdx.x] = 0;
+            x_top[threadIdx.x] = 0;
         }
-        // this thread's row of the tile in the epilogue, and its scale
-        const int tile = at.g * together + mine, n = tile * MX_TILE_N + (lane & 15);
-        int top = 0, top2 = 0;
-        if (n < a.L.N) {
-            const int64_t o = at.e * expert_bytes + tile * tile_bytes + (int64_t)units * MX_UNIT_BYTES + (lane & 15);
-            top = a.w[o];
-            if constexpr (W == 2) top2 = a.w2[o];
-        }
-        float acc[W][NT][4];
+        __syncthreads();
+        mxs_stage<T, WARPS>(a, p, xs, slot_of, x_exp, x_top, cnt, status);
 #pragma unroll
-        for (int w = 0; w < W; ++w)
+        for (int n = 0; n < NT; ++n)  // (columns behind the last row repeat it and go nowhere)
+            xrow[n] = xs + (size_t)min(8 * n + g, cnt - 1) * TERMS * p.x_bytes + t * 16;
+#pragma unroll 1
+        for (; at.tile < at.end; at.tile += together) {
+            // this thread's row of the tile in the epilogue, and its scale
+            const int tile = at.tile, n = tile * MX_TILE_N + (lane & 15);
+            int top = 0, top2 = 0;
+            if (n < a.L.N) {
+                const int64_t o = at.e * expert_bytes + tile * tile_bytes + (int64_t)units * MX_UNIT_BYTES + (lane & 15);
+                top = a.w[o];
+                if constexpr (W == 2) top2 = a.w2[o];
+            }
+            float acc[W][NT][4];
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+            for (int w = 0; w < W; ++w)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) acc[w][i][j] = 0.0f;
-        if (tile < tiles)
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[w][i][j] = 0.0f;
 #pragma unroll 1
             for (int u = u0; u < u1; ++u) {
                 cp_async_wait<STAGES - 2>();
@@ -435,40 +451,41 @@ __global__ void __launch_bounds__(MXS_WARPS<NT> * 32, 1) mxs_kernel(MxArgs a, Mx
                     }
                 }
             }
-        // the warps of a tile add up and write it on their own
-        float* r = red + (warp - part) * (W * COLS * MXS_RED);
+            // the warps of a tile add up and write it on their own
+            float* r = red + (warp - part) * (W * COLS * MXS_RED);
 #pragma unroll
-        for (int w = 0; w < W; ++w)
+            for (int w = 0; w < W; ++w)
 #pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                if (8 * i >= cnt) break;
-                float* c = r + ((part * W + w) * COLS + 8 * i + 2 * t) * MXS_RED + g;
-                c[0] = acc[w][i][0];
-                c[MXS_RED] = acc[w][i][1];
-                c[8] = acc[w][i][2];
-                c[MXS_RED + 8] = acc[w][i][3];
-            }
-        together_barrier();
-        for (int c = 2 * part + (lane >> 4); c < cnt; c += 2 * parts) {
-            if (n >= a.L.N || slot_of[c] < 0) continue;
-            const int s = MODE == MX_DOWN ? place + c : slot_of[c];  // the output's row
-            float v[W];
+                for (int i = 0; i < NT; ++i) {
+                    if (8 * i >= cnt) break;
+                    float* c = r + ((part * W + w) * COLS + 8 * i + 2 * t) * MXS_RED + g;
+                    c[0] = acc[w][i][0];
+                    c[MXS_RED] = acc[w][i][1];
+                    c[8] = acc[w][i][2];
+                    c[MXS_RED + 8] = acc[w][i][3];
+                }
+            together_barrier();
+            for (int c = 2 * part + (lane >> 4); c < cnt; c += 2 * parts) {
+                if (n >= a.L.N || slot_of[c] < 0) continue;
+                const int s = MODE == MX_DOWN ? place + c : slot_of[c];  // the output's row
+                float v[W];
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                const float* from = r + (w * COLS + c) * MXS_RED + (lane & 15);
-                float sum = 0.0f;
+                for (int w = 0; w < W; ++w) {
+                    const float* from = r + (w * COLS + c) * MXS_RED + (lane & 15);
+                    float sum = 0.0f;
 #pragma unroll 4
-                for (int k = 0; k < parts; ++k) sum += from[k * (W * COLS * MXS_RED)];
-                const int e = w ? top2 : top;
-                v[w] = e == 255 ? __uint_as_float(0x7FC00000u) : mul_pow2(sum, e - 127 + x_exp[c]);
+                    for (int k = 0; k < parts; ++k) sum += from[k * (W * COLS * MXS_RED)];
+                    const int e = w ? top2 : top;
+                    v[w] = e == 255 ? __uint_as_float(0x7FC00000u) : mul_pow2(sum, e - 127 + x_exp[c]);
+                }
+                float o = v[0];
+                if constexpr (MODE == MX_GATE_UP) o = mx_silu<T>(v[0]) * v[W - 1];
+                if (QG_OK(qg_in((int64_t)s * a.ldy + n, 1, (int64_t)a.slots * a.ldy), status, 312))
+                    y[(int64_t)s * a.ldy + n] = from_f32<O>(o);
             }
-            float o = v[0];
-            if constexpr (MODE == MX_GATE_UP) o = mx_silu<T>(v[0]) * v[W - 1];
-            if (QG_OK(qg_in((int64_t)s * a.ldy + n, 1, (int64_t)a.slots * a.ldy), status, 312))
-                y[(int64_t)s * a.ldy + n] = from_f32<O>(o);
+            together_barrier();
         }
-        together_barrier();
-    }
+    } while (at.next_rows(before));
     cp_async_wait<0>();
 }
 

@@ -16,7 +16,7 @@ constexpr int MXS_STAGES = MODE == MX_GATE_UP ? 4 : 6;
 template <typename T, int NT, int MODE>
 bool mxs_plan(const DeviceInfo& di, const MxArgs& a, MxsPlan& p)
 {
-    constexpr int W = MODE == MX_GATE_UP ? 2 : 1, TERMS = MX_TERMS<T>, COLS = 8 * NT, WARPS = MXS_WARPS<NT>;
+    constexpr int W = MODE == MX_GATE_UP ? 2 : 1, TERMS = MX_TERMS<T>, COLS = 8 * NT, WARPS = MXS_WARPS<NT, W>;
     const int units = a.L.units();
     p.stages = MXS_STAGES<MODE>;
     p.x_bytes = units * MX_UNIT_K * 2 + 64;  // (neighbouring rows half of the banks apart)
@@ -32,10 +32,9 @@ bool mxs_plan(const DeviceInfo& di, const MxArgs& a, MxsPlan& p)
     const int64_t tiles = (int64_t)a.L.tiles() * std::min<int64_t>(a.L.experts, a.slots), warps = (int64_t)di.sms * WARPS;
     static constexpr int PARTS[2][5] = {{2, 4, 8, 12, 24}, {2, 4, 8, 16, 16}};
     int i = 0;
-    while (i < 4 && tiles * PARTS[NT > 1][i] * 2 < warps * 5 && units >= PARTS[NT > 1][i + 1] * 3) ++i;
-    p.parts = PARTS[NT > 1][i];
-    const int groups = (a.L.tiles() * p.parts + WARPS - 1) / WARPS;
-    const int64_t most = (int64_t)groups * std::min<int64_t>(a.slots, (int64_t)a.slots / p.rows + a.L.experts);
+    while (i < 4 && tiles * PARTS[WARPS == 16][i] * 2 < warps * 5 && units >= PARTS[WARPS == 16][i + 1] * 3) ++i;
+    p.parts = PARTS[WARPS == 16][i];
+    const int64_t most = (int64_t)a.L.tiles() * std::min<int64_t>(a.slots, (int64_t)a.slots / p.rows + a.L.experts);
     p.grid = (int)std::min<int64_t>(most, di.sms);
     return true;
 }
@@ -56,7 +55,7 @@ int launch_mxs(const MxArgs& a, cudaStream_t s)
         if (!ok[dev]) cudaGetLastError();
     });
     if (!ok[dev]) return QGEMV_CUDA_ERROR;
-    return launch_pdl(kern, dim3((unsigned)p.grid), dim3(MXS_WARPS<NT> * 32), p.smem, s, a, p, wait_timeout_counter()) == cudaSuccess
+    return launch_pdl(kern, dim3((unsigned)p.grid), dim3(MXS_WARPS<NT, MODE == MX_GATE_UP ? 2 : 1> * 32), p.smem, s, a, p, wait_timeout_counter()) == cudaSuccess
                ? QGEMV_OK
                : QGEMV_CUDA_ERROR;
 }

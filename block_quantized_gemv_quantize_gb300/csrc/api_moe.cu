@@ -51,7 +51,7 @@ int route_call(int type, RouteArgs a, void* workspace, size_t ws_bytes, void* st
     if (a.experts < 1 || a.experts > MX_MAX_EXPERTS) return QGEMV_INVALID_ARG;
     const int st = check_slots(a.tokens, a.top_k);
     if (st) return st;
-    const size_t need = route_workspace_bytes((int64_t)a.tokens * a.top_k, a.experts);
+    const size_t need = route_workspace_bytes(a.tokens, a.experts);
     if (need && !workspace) return QGEMV_INVALID_ARG;
     if (ws_bytes < need) return QGEMV_WORKSPACE_TOO_SMALL;
     if (!aligned_to(a.ids, 4) || !aligned_to(a.weights, 4) || !aligned_to(a.offsets, 4) || !aligned_to(a.order, 4) ||
@@ -70,7 +70,7 @@ size_t product_workspace(int mode, int type, int tokens, int top_k, int experts,
     if (!known_type(type) || check_slots(tokens, top_k) || check_pack(experts, N, K)) return 0;
     const int64_t slots = (int64_t)tokens * top_k;
     return (mode == MX_DOWN ? parts_bytes(slots, N) + places_bytes(slots) : 0) +
-           (mx_many_rows(slots, experts) ? mx_planes_bytes(type, mode == MX_DOWN ? slots : tokens, K) : 0);
+           (mx_many_rows(slots, experts, K) ? mx_planes_bytes(type, mode == MX_DOWN ? slots : tokens, K) : 0);
 }
 
 int product_call(int mode, int type, const void* w, const void* w2, const void* x, int64_t ldx, const int32_t* offsets,
@@ -152,7 +152,7 @@ int qpack_mxfp4(const void* w_canon, void* w_pack, int experts, int N, int K, vo
 size_t moe_route_workspace_bytes(int tokens, int experts, int top_k)
 {
     if (experts < 1 || experts > MX_MAX_EXPERTS || check_slots(tokens, top_k)) return 0;
-    return route_workspace_bytes((int64_t)tokens * top_k, experts);
+    return route_workspace_bytes(tokens, experts);
 }
 
 int moe_route(int type, const void* logits, int64_t ld, int32_t* ids, float* weights, int32_t* offsets, int32_t* order,

@@ -6,9 +6,10 @@
 // expert.  Weights from the same registers.  Sort: a stable counting sort
 // over contiguous ranges of slots, one a CTA.  Every count is an integer, so
 // that neither the order of atomics nor the grid changes the result.
-// Up to SMALL_SLOTS slots one CTA does all of it in one launch (latency);
-// beyond, a first kernel routes and counts, a second adds the counts of the
-// ranges before its own and places the slots.
+// Up to SMALL_TOKENS tokens one CTA does all of it in one launch (latency);
+// beyond, a first kernel routes and counts, a second adds up each bin's counts
+// over the ranges, a third places the slots.  Bound by latency: of a token's
+// top_k rounds, and of the three launches.
 #include "mxfp4.cuh"
 
 #include <mutex>
@@ -17,16 +18,11 @@ namespace qgemv {
 namespace {
 
 constexpr int THREADS = 512, WARPS = THREADS / 32;
-constexpr int SMALL_SLOTS = 2048;
+constexpr int SMALL_TOKENS = 4 * WARPS;
 constexpr int MAX_RANGES = 512;  // CTAs of a large call
 
-// A range a CTA, whole tokens.
-__host__ __device__ inline int range_tokens(int tokens, int top_k, int ranges_most)
-{
-    const int least = (1024 + top_k - 1) / top_k;
-    const int even = (tokens + ranges_most - 1) / ranges_most;
-    return even > least ? even : least;
-}
+// A range a CTA: a token a warp, or more where that would be too many CTAs.
+__host__ __device__ inline int range_tokens(int tokens) { return max(WARPS, (tokens + MAX_RANGES - 1) / MAX_RANGES); }
 
 // Larger value, larger key; of -0 and +0 one key; NaN and minus infinity 0.
 __device__ __forceinline__ uint32_t logit_key(float v)
@@ -235,6 +231,34 @@ __global__ void __launch_bounds__(THREADS) count_kernel(RouteArgs a, int per)
     for (int i = threadIdx.x; i < bins; i += THREADS) a.counts[(int64_t)blockIdx.x * bins + i] = sm[i];
 }
 
+// A bin a warp: its counts become the sums over the ranges before, its total goes behind them all.
+__global__ void __launch_bounds__(128) sum_kernel(RouteArgs a, int ranges)
+{
+    const int lane = threadIdx.x & 31, bins = a.experts + 1, b = blockIdx.x * 4 + (threadIdx.x >> 5);
+    pdl_launch_dependents();
+    pdl_wait();
+    if (b >= bins) return;
+    constexpr int PER = MAX_RANGES / 32;
+    int n[PER], sum = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) n[i] = lane * PER + i < ranges ? a.counts[(int64_t)(lane * PER + i) * bins + b] : 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) sum += n[i];
+    int at = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(~0u, at, o);
+        if (lane >= o) at += up;
+    }
+    if (lane == 31) a.counts[(int64_t)MAX_RANGES * bins + b] = at;
+    at -= sum;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        if (lane * PER + i < ranges) a.counts[(int64_t)(lane * PER + i) * bins + b] = at;
+        at += n[i];
+    }
+}
+
 __global__ void __launch_bounds__(THREADS) place_kernel(RouteArgs a, int per)
 {
     extern __shared__ int sm[];
@@ -243,34 +267,21 @@ __global__ void __launch_bounds__(THREADS) place_kernel(RouteArgs a, int per)
     const int t0 = min(a.tokens, (int)blockIdx.x * per), t1 = min(a.tokens, t0 + per);
     pdl_launch_dependents();
     pdl_wait();
-    // each bin: all ranges' count, and that of the ranges before this one (in
-    // parts of the ranges, so that all threads have bins to add)
-    for (int i = threadIdx.x; i < 2 * bins; i += THREADS) sm[i] = 0;  // (the second half in per_warp's place)
-    __syncthreads();
-    const int ranges = gridDim.x, parts = max(1, THREADS / bins);
-    for (int i = threadIdx.x; i < bins * parts; i += THREADS) {
-        const int b = i % bins, p = i / bins;
-        int all = 0, before = 0;
-        for (int r = p; r < ranges; r += parts) {
-            const int n = a.counts[(int64_t)r * bins + b];
-            all += n;
-            if (r < (int)blockIdx.x) before += n;
-        }
-        atomicAdd(&first[b], all);
-        atomicAdd(&per_warp[b], before);
-    }
-    __syncthreads();
-    int before[(MX_MAX_EXPERTS + THREADS) / THREADS];
+    constexpr int PER = (MX_MAX_EXPERTS + THREADS) / THREADS;
+    int before[PER];  // this range's first place in the bin
 #pragma unroll
-    for (int i = 0; i < (MX_MAX_EXPERTS + THREADS) / THREADS; ++i)
-        before[i] = (int)threadIdx.x + i * THREADS < bins ? per_warp[threadIdx.x + i * THREADS] : 0;
+    for (int i = 0; i < PER; ++i) {
+        const int b = threadIdx.x + i * THREADS;
+        before[i] = b < bins ? a.counts[(int64_t)blockIdx.x * bins + b] : 0;
+        if (b < bins) first[b] = a.counts[(int64_t)MAX_RANGES * bins + b];
+    }
     __syncthreads();
     scan_bins(first, bins, sums);
     if (blockIdx.x == 0)
         for (int i = threadIdx.x; i < bins; i += THREADS) a.offsets[i] = first[i];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < (MX_MAX_EXPERTS + THREADS) / THREADS; ++i)
+    for (int i = 0; i < PER; ++i)
         if ((int)threadIdx.x + i * THREADS < bins) first[threadIdx.x + i * THREADS] += before[i];
     __syncthreads();
     place_range(a, a.ids, t0 * a.top_k, t1 * a.top_k, first, per_warp);
@@ -283,7 +294,7 @@ int route_tp(const RouteArgs& a, cudaStream_t s)
     int dev = 0;
     if (di.sms <= 0 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return QGEMV_CUDA_ERROR;
     const size_t smem = (size_t)smem_ints(a.experts) * sizeof(int);
-    if ((int64_t)a.tokens * a.top_k <= SMALL_SLOTS) {
+    if (a.tokens <= SMALL_TOKENS) {
         static std::once_flag once[64];
         static bool ok[64];
         auto kern = small_kernel<T, PER, ROUTE>;
@@ -294,7 +305,7 @@ int route_tp(const RouteArgs& a, cudaStream_t s)
         if (!ok[dev]) return QGEMV_CUDA_ERROR;
         return launch_pdl(kern, dim3(1), dim3(THREADS), smem, s, a) == cudaSuccess ? QGEMV_OK : QGEMV_CUDA_ERROR;
     }
-    const int per = range_tokens(a.tokens, a.top_k, di.sms < MAX_RANGES ? di.sms : MAX_RANGES);
+    const int per = range_tokens(a.tokens);
     const unsigned grid = (unsigned)((a.tokens + per - 1) / per);
     static std::once_flag once[64];
     static bool ok[64];
@@ -306,6 +317,8 @@ int route_tp(const RouteArgs& a, cudaStream_t s)
     if (!ok[dev]) return QGEMV_CUDA_ERROR;
     if (launch_pdl(count_kernel<T, PER, ROUTE>, dim3(grid), dim3(THREADS), (size_t)(a.experts + 1) * sizeof(int), s, a,
                    per) != cudaSuccess)
+        return QGEMV_CUDA_ERROR;
+    if (launch_pdl(sum_kernel, dim3((unsigned)(a.experts + 4) / 4), dim3(128), 0, s, a, (int)grid) != cudaSuccess)
         return QGEMV_CUDA_ERROR;
     return launch_pdl(place_kernel, dim3(grid), dim3(THREADS), smem, s, a, per) == cudaSuccess ? QGEMV_OK
                                                                                                : QGEMV_CUDA_ERROR;
@@ -322,9 +335,9 @@ int route_t(const RouteArgs& a, cudaStream_t s)
 
 }  // namespace
 
-size_t route_workspace_bytes(int64_t slots, int experts)
+size_t route_workspace_bytes(int tokens, int experts)
 {
-    return slots <= SMALL_SLOTS ? 0 : (size_t)MAX_RANGES * (experts + 1) * sizeof(int32_t);
+    return tokens <= SMALL_TOKENS ? 0 : (size_t)(MAX_RANGES + 1) * (experts + 1) * sizeof(int32_t);
 }
 
 int launch_route(int type, const RouteArgs& a, cudaStream_t s)

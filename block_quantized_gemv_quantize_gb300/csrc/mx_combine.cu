@@ -84,9 +84,13 @@ int launch_mx_combine(int type, const float* parts, const int32_t* place_of, con
     return combine_t<__nv_bfloat16>(parts, place_of, weights, out, ldo, tokens, top_k, N, s);
 }
 
-bool mx_many_rows(int64_t slots, int experts)
+// From 8 rows an expert on (of those that can have any).  64 experts of 1408 x
+// 5120, gate and up, 8 rows each: 118 us by the mma.sync kernel, 175 by this one,
+// 12 rows: 200 and 176 (a second row tile reads the weights again); one of
+// 17408 x 5120, 8 rows: 25 and 28, 12 rows: 37 and 28.
+bool mx_many_rows(int64_t slots, int experts, int K)
 {
-    return slots >= 16 * (slots < experts ? slots : (int64_t)experts);
+    return slots > 8 * (slots < experts ? slots : (int64_t)experts) || K > 16384;
 }
 
 size_t mx_planes_bytes(int type, int64_t rows, int K)

@@ -25,13 +25,9 @@
 
 namespace qgemv {
 
-// Warps of a CTA (one an SM), for row tiles of 8 NT: as many as their registers let run.
-template <int NT, int W>
-#ifdef EXP_WARPS
-constexpr int MXS_WARPS = NT == 1 ? EXP_WARPS : 16;
-#else
-constexpr int MXS_WARPS = NT == 1 && W == 1 ? 24 : 16;
-#endif
+constexpr int MXS_WARPS = 16, MXS_THREADS = MXS_WARPS * 32;  // of a CTA, one an SM
+constexpr int MXS_STAGES = 4;  // of a warp's ring, a unit of two tiles each
+constexpr int MXS_ROWS = 8;    // of x at most in a row tile
 constexpr int MXS_RED = 20;  // floats of a column of 16 in the exchange (no bank conflicts)
 
 // Halves that a value of a row of x takes.
@@ -41,7 +37,6 @@ constexpr int MX_TERMS = sizeof(T) == 4 ? 2 : 1;
 struct MxsPlan {
     int rows;     // of x in a row tile
     int parts;    // warps that share a tile's K
-    int stages;   // of a warp's ring
     int x_bytes;  // of a staged row and term
     int grid;
     size_t smem;
@@ -195,7 +190,7 @@ __device__ __forceinline__ void mx_row_halves(const float (&v)[8], float f, __ha
 // block has 16 bytes for each t, values 4 t .. 4 t + 3 and 16 + 4 t .. 16 + 4 t
 // + 3.  A warp takes 256 values of a row at a time, a lane eight neighbouring
 // ones: half a piece of two t each.
-template <typename T, int WARPS>
+template <typename T>
 __device__ void mxs_stage(const MxArgs& a, const MxsPlan& p, uint8_t* xs, const int* slot_of, int* x_exp,
                           uint32_t* x_top, int cnt, unsigned int* status)
 {
@@ -206,7 +201,7 @@ __device__ void mxs_stage(const MxArgs& a, const MxsPlan& p, uint8_t* xs, const 
     const T* x = static_cast<const T*>(a.x);
     const bool wide = ((reinterpret_cast<uintptr_t>(x) | (uintptr_t)(a.ldx * (int64_t)sizeof(T))) & 15u) == 0;
     if constexpr (SCALED) {
-        for (int i = warp; i < cnt * pieces; i += WARPS) {
+        for (int i = warp; i < cnt * pieces; i += MXS_WARPS) {
             const int row = i / pieces, k = (i - row * pieces) * 256 + lane * 8, s = max(0, slot_of[row]);
             float v[8];
             mx_load8(x + (int64_t)(s / a.x_div) * a.ldx + k, wide, max(0, K - k), v);
@@ -223,7 +218,7 @@ __device__ void mxs_stage(const MxArgs& a, const MxsPlan& p, uint8_t* xs, const 
         if ((int)threadIdx.x < cnt) x_exp[threadIdx.x] = mx_row_exponent(x_top[threadIdx.x]);
         __syncthreads();
     }
-    for (int i = warp; i < cnt * pieces; i += WARPS) {
+    for (int i = warp; i < cnt * pieces; i += MXS_WARPS) {
         const int row = i / pieces, k = (i - row * pieces) * 256 + lane * 8, s = max(0, slot_of[row]);
         if (k >= padded) continue;
         float v[8];
@@ -247,7 +242,7 @@ __device__ void mxs_stage(const MxArgs& a, const MxsPlan& p, uint8_t* xs, const 
     __syncthreads();
 }
 
-// Where a warp is in its CTA's range of tiles: tile `tile` of row tile rt, whose
+// Where a warp is in its CTA's range of (pairs of) tiles: tile `tile` of row tile rt, whose
 // tiles below `end` are the CTA's, `left` tiles after those.  The warps of a tile
 // take every step-th one from `first` on.
 struct MxCursor {
@@ -284,12 +279,14 @@ struct MxCursor {
     }
 };
 
-template <typename T, int NT, int MODE, int STAGES>
-__global__ void __launch_bounds__(MXS_WARPS<NT, MODE == MX_GATE_UP ? 2 : 1> * 32, 1) mxs_kernel(MxArgs a, MxsPlan p, unsigned int* status)
+template <typename T, int MODE>
+__global__ void __launch_bounds__(MXS_THREADS, 1) mxs_kernel(MxArgs a, MxsPlan p, unsigned int* status)
 {
     using O = typename std::conditional<MODE == MX_DOWN, float, T>::type;
-    constexpr int W = MODE == MX_GATE_UP ? 2 : 1, TERMS = MX_TERMS<T>;
-    constexpr int COLS = 8 * NT, STAGE = W * MX_UNIT_BYTES, WARPS = MXS_WARPS<NT, W>;
+    constexpr int TERMS = MX_TERMS<T>, WARPS = MXS_WARPS, STAGES = MXS_STAGES, COLS = MXS_ROWS;
+    // two tiles at a time: gate's and up's, or neighbours of one weight
+    constexpr int W = 2, STAGE = W * MX_UNIT_BYTES;
+    constexpr bool PAIR = MODE == MX_GATE_UP;
     extern __shared__ __align__(16) uint8_t sm[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     uint8_t* ring = sm + warp * (STAGES * STAGE);
@@ -310,7 +307,7 @@ __global__ void __launch_bounds__(MXS_WARPS<NT, MODE == MX_GATE_UP ? 2 : 1> * 32
     mx_rest<MODE>(a, y, status);
 
     const int parts = p.parts, together = WARPS / parts;  // tiles that the CTA works on at a time
-    const int tiles = a.L.tiles(), units = a.L.units();
+    const int tiles = PAIR ? a.L.tiles() : (a.L.tiles() + 1) / 2, units = a.L.units();  // (pairs of tiles)
     const int64_t items = (int64_t)n_rt * tiles;
     const int64_t i0 = items * blockIdx.x / gridDim.x, i1 = items * (blockIdx.x + 1) / gridDim.x;
     if (i0 >= i1) return;
@@ -318,6 +315,16 @@ __global__ void __launch_bounds__(MXS_WARPS<NT, MODE == MX_GATE_UP ? 2 : 1> * 32
     const int u0 = units * part / parts, u1 = units * (part + 1) / parts;
     const int64_t tile_bytes = a.L.tile_bytes(), expert_bytes = a.L.expert_bytes();
 
+    // Where a pair's two tiles start (one behind the last tile is the last again, and goes nowhere).
+    auto tile_pair = [&](int e, int pair, const uint8_t*& w, const uint8_t*& w2) {
+        if constexpr (PAIR) {
+            w = a.w + e * expert_bytes + pair * tile_bytes;
+            w2 = a.w2 + e * expert_bytes + pair * tile_bytes;
+        } else {
+            w = a.w + e * expert_bytes + 2 * pair * tile_bytes;
+            w2 = 2 * pair + 1 < a.L.tiles() ? w + tile_bytes : w;
+        }
+    };
     MxCursor load;
     load.start(i0, i1, tiles, mine, together, before, a.L.experts);
     MxCursor at = load;
@@ -325,7 +332,7 @@ __global__ void __launch_bounds__(MXS_WARPS<NT, MODE == MX_GATE_UP ? 2 : 1> * 32
     int load_n = 0, load_stage = 0;  // units left of the item, stage of the next one
     bool load_more = u0 < u1;
     load.tile -= together;  // (one before the first)
-    // this lane's 16 bytes of a unit's codes, of both weights, and of its scales (lanes 0 and 1, of both 0 .. 3)
+    // this lane's 16 bytes of a unit's codes, of both tiles, and (lanes 0 .. 3) of their scales
     const uint8_t *lw = nullptr, *lw2 = nullptr, *ls = nullptr;
     const uint32_t ring_at = smem_u32(ring) + lane * 16;
     const uint32_t ring_scale = smem_u32(ring) + (lane >> 1) * MX_UNIT_BYTES + MX_UNIT_CODES + (lane & 1) * 16;
@@ -338,21 +345,24 @@ __global__ void __launch_bounds__(MXS_WARPS<NT, MODE == MX_GATE_UP ? 2 : 1> * 32
                 load.tile -= together;
                 continue;
             }
-            const int64_t off = load.e * expert_bytes + load.tile * tile_bytes + (int64_t)u0 * MX_UNIT_BYTES;
-            lw = a.w + off + lane * 16;
-            if constexpr (W == 2) lw2 = a.w2 + off + lane * 16;
-            ls = (W == 2 && lane >= 2 ? a.w2 : a.w) + off + MX_UNIT_CODES + (lane & 1) * 16;
+            const uint8_t *w = a.w, *w2 = a.w2;
+            tile_pair(load.e, load.tile, w, w2);
+            w += (int64_t)u0 * MX_UNIT_BYTES;
+            w2 += (int64_t)u0 * MX_UNIT_BYTES;
+            lw = w + lane * 16;
+            lw2 = w2 + lane * 16;
+            ls = (lane >= 2 ? w2 : w) + MX_UNIT_CODES + (lane & 1) * 16;
             load_n = u1 - u0;
         }
         if (load_n > 0) {
             const uint32_t to = load_stage * STAGE;
             if (QG_OK(qg_in(lw - lane * 16 - a.w, MX_UNIT_BYTES, a.L.bytes()), status, 311)) {
                 cp_async16(ring_at + to, lw);
-                if constexpr (W == 2) cp_async16(ring_at + to + MX_UNIT_BYTES, lw2);
-                if (lane < 2 * W) cp_async16(ring_scale + to, ls);
+                cp_async16(ring_at + to + MX_UNIT_BYTES, lw2);
+                if (lane < 4) cp_async16(ring_scale + to, ls);
             }
             lw += MX_UNIT_BYTES;
-            if constexpr (W == 2) lw2 += MX_UNIT_BYTES;
+            lw2 += MX_UNIT_BYTES;
             ls += MX_UNIT_BYTES;
             --load_n;
             if (++load_stage == STAGES) load_stage = 0;
@@ -368,7 +378,6 @@ __global__ void __launch_bounds__(MXS_WARPS<NT, MODE == MX_GATE_UP ? 2 : 1> * 32
         else __syncwarp();
     };
     int stage = 0;
-    const uint8_t* xrow[NT];
     do {
         __syncthreads();  // the rows before are done with
         const int place = start[at.e] + (at.rt - before[at.e]) * p.rows, cnt = min(p.rows, start[at.e + 1] - place);
@@ -384,27 +393,21 @@ __global__ void __launch_bounds__(MXS_WARPS<NT, MODE == MX_GATE_UP ? 2 : 1> * 32
             x_top[threadIdx.x] = 0;
         }
         __syncthreads();
-        mxs_stage<T, WARPS>(a, p, xs, slot_of, x_exp, x_top, cnt, status);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)  // (columns behind the last row repeat it and go nowhere)
-            xrow[n] = xs + (size_t)min(8 * n + g, cnt - 1) * TERMS * p.x_bytes + t * 16;
+        mxs_stage<T>(a, p, xs, slot_of, x_exp, x_top, cnt, status);
+        // (columns behind the last row repeat it and go nowhere)
+        const uint8_t* xrow = xs + (size_t)min(g, cnt - 1) * TERMS * p.x_bytes + t * 16;
 #pragma unroll 1
         for (; at.tile < at.end; at.tile += together) {
-            // this thread's row of the tile in the epilogue, and its scale
-            const int tile = at.tile, n = tile * MX_TILE_N + (lane & 15);
-            int top = 0, top2 = 0;
-            if (n < a.L.N) {
-                const int64_t o = at.e * expert_bytes + tile * tile_bytes + (int64_t)units * MX_UNIT_BYTES + (lane & 15);
-                top = a.w[o];
-                if constexpr (W == 2) top2 = a.w2[o];
+            // this lane's row of the tiles in the epilogue, and its scales
+            const int n = at.tile * (PAIR ? MX_TILE_N : 2 * MX_TILE_N) + (lane & 15);
+            int tops[2];
+            {
+                const uint8_t *w, *w2;
+                tile_pair(at.e, at.tile, w, w2);
+                tops[0] = w[(int64_t)units * MX_UNIT_BYTES + (lane & 15)];
+                tops[1] = w2[(int64_t)units * MX_UNIT_BYTES + (lane & 15)];
             }
-            float acc[W][NT][4];
-#pragma unroll
-            for (int w = 0; w < W; ++w)
-#pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[w][i][j] = 0.0f;
+            float acc[W][4] = {};
 #pragma unroll 1
             for (int u = u0; u < u1; ++u) {
                 cp_async_wait<STAGES - 2>();
@@ -430,44 +433,37 @@ __global__ void __launch_bounds__(MXS_WARPS<NT, MODE == MX_GATE_UP ? 2 : 1> * 32
                         sg[w] = __uint_as_float((b ? scale[w] << 7 : scale[w] << 23) & 0x7F800000u);
                         sh[w] = __uint_as_float((b ? scale[w] >> 1 : scale[w] << 15) & 0x7F800000u);
                     }
+                    uint4 x[TERMS];
 #pragma unroll
-                    for (int i = 0; i < NT; ++i) {
-                        if (8 * i >= cnt) break;
-                        uint4 x[TERMS];
+                    for (int k = 0; k < TERMS; ++k)
+                        x[k] = *reinterpret_cast<const uint4*>(xrow + (size_t)k * p.x_bytes + (2 * u + b) * 64);
 #pragma unroll
-                        for (int k = 0; k < TERMS; ++k)
-                            x[k] = *reinterpret_cast<const uint4*>(xrow[i] + (size_t)k * p.x_bytes + (2 * u + b) * 64);
+                    for (int w = 0; w < W; ++w) {
+                        float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                        for (int w = 0; w < W; ++w) {
-                            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                            for (int k = 0; k < TERMS; ++k) {
-                                mma_f16(c, ag[w][0], ah[w][0], ag[w][1], ah[w][1], x[k].x, x[k].y);
-                                mma_f16(c, ag[w][2], ah[w][2], ag[w][3], ah[w][3], x[k].z, x[k].w);
-                            }
-                            fma_f32x2(acc[w][i][0], acc[w][i][1], c[0], c[1], sg[w], sg[w]);
-                            fma_f32x2(acc[w][i][2], acc[w][i][3], c[2], c[3], sh[w], sh[w]);
+                        for (int k = 0; k < TERMS; ++k) {
+                            mma_f16(c, ag[w][0], ah[w][0], ag[w][1], ah[w][1], x[k].x, x[k].y);
+                            mma_f16(c, ag[w][2], ah[w][2], ag[w][3], ah[w][3], x[k].z, x[k].w);
                         }
+                        fma_f32x2(acc[w][0], acc[w][1], c[0], c[1], sg[w], sg[w]);
+                        fma_f32x2(acc[w][2], acc[w][3], c[2], c[3], sh[w], sh[w]);
                     }
                 }
             }
             // the warps of a tile add up and write it on their own
             float* r = red + (warp - part) * (W * COLS * MXS_RED);
 #pragma unroll
-            for (int w = 0; w < W; ++w)
-#pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    if (8 * i >= cnt) break;
-                    float* c = r + ((part * W + w) * COLS + 8 * i + 2 * t) * MXS_RED + g;
-                    c[0] = acc[w][i][0];
-                    c[MXS_RED] = acc[w][i][1];
-                    c[8] = acc[w][i][2];
-                    c[MXS_RED + 8] = acc[w][i][3];
-                }
+            for (int w = 0; w < W; ++w) {
+                float* c = r + ((part * W + w) * COLS + 2 * t) * MXS_RED + g;
+                c[0] = acc[w][0];
+                c[MXS_RED] = acc[w][1];
+                c[8] = acc[w][2];
+                c[MXS_RED + 8] = acc[w][3];
+            }
             together_barrier();
             for (int c = 2 * part + (lane >> 4); c < cnt; c += 2 * parts) {
-                if (n >= a.L.N || slot_of[c] < 0) continue;
-                const int s = MODE == MX_DOWN ? place + c : slot_of[c];  // the output's row
+                if (slot_of[c] < 0) continue;
+                const int64_t s = MODE == MX_DOWN ? place + c : slot_of[c];  // the output's row
                 float v[W];
 #pragma unroll
                 for (int w = 0; w < W; ++w) {
@@ -475,13 +471,17 @@ __global__ void __launch_bounds__(MXS_WARPS<NT, MODE == MX_GATE_UP ? 2 : 1> * 32
                     float sum = 0.0f;
 #pragma unroll 4
                     for (int k = 0; k < parts; ++k) sum += from[k * (W * COLS * MXS_RED)];
-                    const int e = w ? top2 : top;
-                    v[w] = e == 255 ? __uint_as_float(0x7FC00000u) : mul_pow2(sum, e - 127 + x_exp[c]);
+                    v[w] = tops[w] == 255 ? __uint_as_float(0x7FC00000u) : mul_pow2(sum, tops[w] - 127 + x_exp[c]);
                 }
-                float o = v[0];
-                if constexpr (MODE == MX_GATE_UP) o = mx_silu<T>(v[0]) * v[W - 1];
-                if (QG_OK(qg_in((int64_t)s * a.ldy + n, 1, (int64_t)a.slots * a.ldy), status, 312))
-                    y[(int64_t)s * a.ldy + n] = from_f32<O>(o);
+                if constexpr (PAIR) {
+                    if (n < a.L.N && QG_OK(qg_in(s * a.ldy + n, 1, (int64_t)a.slots * a.ldy), status, 312))
+                        y[s * a.ldy + n] = from_f32<O>(mx_silu<T>(v[0]) * v[1]);
+                } else {
+#pragma unroll
+                    for (int w = 0; w < W; ++w)
+                        if (n + w * MX_TILE_N < a.L.N && QG_OK(qg_in(s * a.ldy + n + w * MX_TILE_N, 1, (int64_t)a.slots * a.ldy), status, 314))
+                            y[s * a.ldy + n + w * MX_TILE_N] = from_f32<O>(v[w]);
+                }
             }
             together_barrier();
         }

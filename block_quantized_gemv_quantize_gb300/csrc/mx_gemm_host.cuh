@@ -8,46 +8,40 @@
 
 namespace qgemv {
 
-// Stages of a warp's ring, 544 B each (twice that for a pair of weights, which takes fewer).
-template <int MODE>
-constexpr int MXS_STAGES = MODE == MX_GATE_UP ? 4 : 6;
-
 // Rows a tile, warps a tile's K, CTAs.
-template <typename T, int NT, int MODE>
+template <typename T, int MODE>
 bool mxs_plan(const DeviceInfo& di, const MxArgs& a, MxsPlan& p)
 {
-    constexpr int W = MODE == MX_GATE_UP ? 2 : 1, TERMS = MX_TERMS<T>, COLS = 8 * NT, WARPS = MXS_WARPS<NT, W>;
+    constexpr int TERMS = MX_TERMS<T>;
     const int units = a.L.units();
-    p.stages = MXS_STAGES<MODE>;
     p.x_bytes = units * MX_UNIT_K * 2 + 64;  // (neighbouring rows half of the banks apart)
-    const size_t fixed = (size_t)WARPS * p.stages * W * MX_UNIT_BYTES + WARPS * W * COLS * MXS_RED * sizeof(float) +
-                         (size_t)(2 * (a.L.experts + 1) + 32 + 3 * COLS) * sizeof(int);
+    const size_t fixed = (size_t)MXS_WARPS * MXS_STAGES * 2 * MX_UNIT_BYTES + MXS_WARPS * 2 * MXS_ROWS * MXS_RED * sizeof(float) +
+                         (size_t)(2 * (a.L.experts + 1) + 32 + 3 * MXS_ROWS) * sizeof(int);
     const size_t row = (size_t)TERMS * p.x_bytes;
-    const int want = std::max(1, std::min(COLS, a.slots));
+    const int want = std::max(1, std::min(MXS_ROWS, a.slots));
     const int fit = (size_t)di.smem_optin > fixed ? (int)(((size_t)di.smem_optin - fixed) / row) : 0;
     if (fit < 1) return false;
     p.rows = std::min(want, fit);
     p.smem = fixed + row * p.rows;
-    // as few warps a tile as leave two and a half tiles' parts for each warp of the GPU, of three units at least
-    const int64_t tiles = (int64_t)a.L.tiles() * std::min<int64_t>(a.L.experts, a.slots), warps = (int64_t)di.sms * WARPS;
-    static constexpr int PARTS[2][5] = {{2, 4, 8, 12, 24}, {2, 4, 8, 16, 16}};
-    int i = 0;
-    while (i < 4 && tiles * PARTS[WARPS == 16][i] * 2 < warps * 5 && units >= PARTS[WARPS == 16][i + 1] * 3) ++i;
-    p.parts = PARTS[WARPS == 16][i];
-    const int64_t most = (int64_t)a.L.tiles() * std::min<int64_t>(a.slots, (int64_t)a.slots / p.rows + a.L.experts);
+    // as few warps a pair of tiles as leave two and a half pairs' parts for each warp of the GPU, of three units at least
+    const int pairs = MODE == MX_GATE_UP ? a.L.tiles() : (a.L.tiles() + 1) / 2;
+    const int64_t all = pairs * std::min<int64_t>(a.L.experts, a.slots), warps = (int64_t)di.sms * MXS_WARPS;
+    p.parts = 2;
+    while (p.parts < MXS_WARPS && all * p.parts * 2 < warps * 5 && units >= p.parts * 6) p.parts *= 2;
+    const int64_t most = (int64_t)pairs * std::min<int64_t>(a.slots, (int64_t)a.slots / p.rows + a.L.experts);
     p.grid = (int)std::min<int64_t>(most, di.sms);
     return true;
 }
 
-template <typename T, int NT, int MODE>
+template <typename T, int MODE>
 int launch_mxs(const MxArgs& a, cudaStream_t s)
 {
     const DeviceInfo di = device_info();
     int dev = 0;
     if (di.sms <= 0 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return QGEMV_CUDA_ERROR;
     MxsPlan p;
-    if (!mxs_plan<T, NT, MODE>(di, a, p)) return QGEMV_UNSUPPORTED_SHAPE;
-    auto kern = mxs_kernel<T, NT, MODE, MXS_STAGES<MODE>>;
+    if (!mxs_plan<T, MODE>(di, a, p)) return QGEMV_UNSUPPORTED_SHAPE;
+    auto kern = mxs_kernel<T, MODE>;
     static std::once_flag once[64];
     static bool ok[64];
     std::call_once(once[dev], [&]() {
@@ -55,7 +49,7 @@ int launch_mxs(const MxArgs& a, cudaStream_t s)
         if (!ok[dev]) cudaGetLastError();
     });
     if (!ok[dev]) return QGEMV_CUDA_ERROR;
-    return launch_pdl(kern, dim3((unsigned)p.grid), dim3(MXS_WARPS<NT, MODE == MX_GATE_UP ? 2 : 1> * 32), p.smem, s, a, p, wait_timeout_counter()) == cudaSuccess
+    return launch_pdl(kern, dim3((unsigned)p.grid), dim3(MXS_THREADS), p.smem, s, a, p, wait_timeout_counter()) == cudaSuccess
                ? QGEMV_OK
                : QGEMV_CUDA_ERROR;
 }
@@ -115,16 +109,7 @@ int launch_mxt(const MxArgs& a, cudaStream_t s)
 template <typename T, int MODE>
 int launch_mx_mode(const MxArgs& a, cudaStream_t s)
 {
-#ifndef EXP_FORCE
-    if (mx_many_rows(a.slots, a.L.experts)) return launch_mxt<T, MODE>(a, s);
-#endif
-#ifdef EXP_FORCE
-    return EXP_FORCE == 9 ? launch_mxt<T, MODE>(a, s) : EXP_FORCE == 1 ? launch_mxs<T, 1, MODE>(a, s) : EXP_FORCE == 2 ? launch_mxs<T, 2, MODE>(a, s) : launch_mxs<T, 4, MODE>(a, s);
-#endif
-    const double rows = (double)a.slots / (double)std::min<int64_t>(a.L.experts, a.slots);  // of an expert that has any, about
-    if (rows <= 6.0) return launch_mxs<T, 1, MODE>(a, s);
-    const int status = launch_mxs<T, 2, MODE>(a, s);
-    return status == QGEMV_UNSUPPORTED_SHAPE ? launch_mxs<T, 1, MODE>(a, s) : status;
+    return mx_many_rows(a.slots, a.L.experts, a.L.K) ? launch_mxt<T, MODE>(a, s) : launch_mxs<T, MODE>(a, s);
 }
 
 template <typename T>

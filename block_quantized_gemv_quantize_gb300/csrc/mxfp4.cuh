@@ -70,13 +70,13 @@ struct RouteArgs {
     float* weights;
     int32_t* offsets;
     int32_t* order;
-    int32_t* counts;  // workspace [CTAs][experts + 1]
+    int32_t* counts;  // workspace [ranges + 1][experts + 1]
     int tokens, experts, top_k;
     bool sigmoid, renormalize;
     float scale;
 };
 
-size_t route_workspace_bytes(int64_t slots, int experts);
+size_t route_workspace_bytes(int tokens, int experts);
 int launch_route(int type, const RouteArgs& a, cudaStream_t s);
 
 // ---- the experts' products ------------------------------------------------------
@@ -98,8 +98,9 @@ struct MxArgs {
     void* planes;          // workspace for rows of x as halves (mx_planes_bytes)
 };
 
-// Whether a call's experts have many rows each (the tcgen05 kernel), about.
-bool mx_many_rows(int64_t slots, int experts);
+// Whether a call takes the tcgen05 kernel: its experts have many rows each, about (or
+// rows of x that are too long for the other's shared memory).
+bool mx_many_rows(int64_t slots, int experts, int K);
 // Workspace of that kernel: rows of x as halves, and their powers of two.
 size_t mx_planes_bytes(int type, int64_t rows, int K);
 

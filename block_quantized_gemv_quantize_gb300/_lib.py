@@ -1,5 +1,6 @@
 """Thin ctypes binding of libqgemv.so (argument marshalling only; the paged
-cache's calls first take the compiled short way of csrc/binding.cpp).
+cache's and the sparse layer's calls first take the compiled short way of
+csrc/binding.cpp).
 
 Every function here has the name of the C entry point it calls, takes torch
 tensors (device memory) plus sizes, passes raw pointers and the current CUDA
@@ -133,11 +134,15 @@ def _load_calls():
         calls = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(calls)
         calls.init(*(ctypes.cast(getattr(LIB, name), ctypes.c_void_p).value for name in (
-            "kv_write", "kv_read", "attn_paged", "kv_page_bytes", "attn_paged_workspace_bytes")))
+            "kv_write", "kv_read", "attn_paged", "kv_page_bytes", "attn_paged_workspace_bytes", "quantize_mxfp4",
+            "dequantize_mxfp4", "moe_route", "moe_route_workspace_bytes", "mxfp4_pack_bytes", "qgemm_mxfp4",
+            "moe_gate_up_mxfp4", "moe_down_mxfp4", "qgemm_mxfp4_workspace_bytes", "moe_gate_up_mxfp4_workspace_bytes",
+            "moe_down_mxfp4_workspace_bytes")))
         return calls
     except (ImportError, OSError) as e:
         warnings.warn(f"the paged cache's calls go through ctypes, three times as long on the host: {e}", RuntimeWarning)
-        return types.SimpleNamespace(**{name: lambda *args: None for name in ("kv_write", "kv_read", "attn_paged")})
+        return types.SimpleNamespace(**{name: lambda *args: None for name in (
+            "kv_write", "kv_read", "attn_paged", "quantize_mxfp4", "dequantize_mxfp4", "moe_route", "product")})
 
 
 _CALLS = _load_calls()
@@ -694,6 +699,7 @@ def attn_paged(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, k
 # ---------------------------------------------------------------- MXFP4 and the sparse layer
 
 SCORES = {"softmax": 0, "sigmoid": 1}
+_PRODUCTS = {"qgemm_mxfp4": 0, "moe_gate_up_mxfp4": 1, "moe_down_mxfp4": 2}
 
 
 def _matrix(t: torch.Tensor, what: str, rows: int | None = None, columns: int | None = None,
@@ -751,6 +757,11 @@ def mxfp4_pack_bytes(experts: int, N: int, K: int) -> int:
 
 def quantize_mxfp4(x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Tensor:
     """fp32, fp16 or bf16 x [N, K] (any row stride) -> MXFP4 blocks, uint8 [N, K/32, 17]."""
+    done = _CALLS.quantize_mxfp4(x, out)
+    if type(done) is int:
+        _check("quantize_mxfp4", done)
+    elif done is not None:
+        return done
     ld, code = _matrix(x, "x"), _type(x, "x")
     N, K = x.shape
     if K < 32 or K % 32:
@@ -768,6 +779,11 @@ def quantize_mxfp4(x: torch.Tensor, out: torch.Tensor | None = None) -> torch.Te
 def dequantize_mxfp4(blocks: torch.Tensor, dtype: torch.dtype = torch.float32,
                      out: torch.Tensor | None = None) -> torch.Tensor:
     """MXFP4 blocks, uint8 [N, K/32, 17] -> the values [N, K] in dtype, or into out (any row stride)."""
+    done = _CALLS.dequantize_mxfp4(blocks, _TYPES.get(dtype, -1), out)
+    if type(done) is int:
+        _check("dequantize_mxfp4", done)
+    elif done is not None:
+        return done
     N, K = _mx_blocks(blocks)
     if out is None:
         out = torch.empty((N, K), dtype=dtype, device=blocks.device)
@@ -812,6 +828,11 @@ def moe_route(logits: torch.Tensor, top_k: int, score: str = "softmax", renormal
     over all experts, or sigmoid; divided by their sum with renormalize; times
     scale), and the slots t * top_k + j sorted by expert: expert e's are
     order[offsets[e]:offsets[e + 1]], those without an expert come last."""
+    done = _CALLS.moe_route(logits, top_k, SCORES.get(score, -1), renormalize, scale, ws)
+    if type(done) is int:
+        _check("moe_route", done)
+    elif done is not None:
+        return done
     if score not in SCORES:
         raise ValueError(f"score must be one of {', '.join(SCORES)}, not {score!r}")
     ld, code = _matrix(logits, "logits"), _type(logits, "logits")
@@ -860,6 +881,12 @@ def _product_bytes(name: str, code: int, tokens: int, top_k: int, experts: int, 
 def _product(name: str, packs: tuple, x: torch.Tensor, offsets: torch.Tensor, order: torch.Tensor | None,
              weights: torch.Tensor | None, tokens: int, top_k: int, rows: int, N: int, y: torch.Tensor | None,
              ws: torch.Tensor | None) -> torch.Tensor:
+    done = _CALLS.product(_PRODUCTS[name], packs[0], packs[1] if len(packs) > 1 else None, x, offsets, order, weights, top_k,
+                          N, y, ws)
+    if type(done) is int:
+        _check(name, done)
+    elif done is not None:
+        return done
     ldx, code = _matrix(x, "x"), _type(x, "x")
     K, device = x.shape[1], x.device
     if offsets.dim() != 1 or offsets.shape[0] < 2:

@@ -32,6 +32,24 @@ __device__ __forceinline__ uint32_t logit_key(float v)
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// The same for the 16-bit types, whose key leaves room for the expert (the lower, the
+// larger), so that one maximum finds both.
+template <typename T>
+__device__ __forceinline__ uint32_t logit_key16(T v, int e)
+{
+    const float f = to_f32(v);
+    if (!(f > -INFINITY)) return 0u;
+    const uint32_t u = f == 0.0f ? 0u : (uint32_t)*reinterpret_cast<const uint16_t*>(&v);
+    return (((u & 0x8000u) ? ~u & 0xFFFFu : (u | 0x8000u)) << 16) | (uint32_t)(0xFFFF - e);
+}
+template <typename T>
+__device__ __forceinline__ float key16_logit(uint32_t k)
+{
+    const uint32_t o = k >> 16;
+    const uint16_t u = (uint16_t)((o & 0x8000u) ? (o & 0x7FFFu) : ~o);
+    return to_f32(*reinterpret_cast<const T*>(&u));
+}
+
 __device__ __forceinline__ float key_logit(uint32_t k)
 {
     return __uint_as_float((k & 0x80000000u) ? (k & 0x7FFFFFFFu) : ~k);
@@ -48,20 +66,26 @@ __device__ __forceinline__ float warp_sum(float v)
 template <typename T, int PER>
 __device__ __forceinline__ void route_token(const T* row, const RouteArgs& a, int lane, int& id, float& weight)
 {
+    constexpr bool SHORT = sizeof(T) == 2;
+    auto value = [](uint32_t k) { if constexpr (SHORT) return key16_logit<T>(k); else return key_logit(k); };
     uint32_t key[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) key[i] = lane + 32 * i < a.experts ? logit_key(to_f32(row[lane + 32 * i])) : 0u;
+    for (int i = 0; i < PER; ++i) {
+        const int e = lane + 32 * i;
+        if constexpr (SHORT) key[i] = e < a.experts ? logit_key16(row[e], e) : 0u;
+        else key[i] = e < a.experts ? logit_key(row[e]) : 0u;
+    }
     uint32_t mine = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) mine = max(mine, key[i]);
     const uint32_t top = __reduce_max_sync(~0u, mine);
-    const float best = top ? key_logit(top) : 0.0f;
+    const float best = top ? value(top) : 0.0f;
     float total = 1.0f;
     if (!a.sigmoid && !a.renormalize) {
         float s = 0.0f;
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-            if (key[i]) s += expf(key_logit(key[i]) - best);
+            if (key[i]) s += expf(value(key[i]) - best);
         total = warp_sum(s);
     }
     id = -1;
@@ -69,16 +93,18 @@ __device__ __forceinline__ void route_token(const T* row, const RouteArgs& a, in
     for (int j = 0; j < a.top_k; ++j) {
         const uint32_t k = __reduce_max_sync(~0u, mine);
         if (k == 0) break;
-        int at = MX_MAX_EXPERTS;
-        if (mine == k) {
+        int at = SHORT ? 0xFFFF - (int)(k & 0xFFFFu) : MX_MAX_EXPERTS;
+        if constexpr (!SHORT) {
+            if (mine == k) {
 #pragma unroll
-            for (int i = PER - 1; i >= 0; --i)
-                if (key[i] == k) at = lane + 32 * i;
+                for (int i = PER - 1; i >= 0; --i)
+                    if (key[i] == k) at = lane + 32 * i;
+            }
+            at = __reduce_min_sync(~0u, at);
         }
-        at = __reduce_min_sync(~0u, at);
         if (lane == j) {
             id = at;
-            logit = key_logit(k);
+            logit = value(k);
         }
         if ((at & 31) == lane) {
             mine = 0;

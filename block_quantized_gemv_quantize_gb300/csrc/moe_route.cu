@@ -19,10 +19,13 @@ namespace {
 
 constexpr int THREADS = 512, WARPS = THREADS / 32;
 constexpr int SMALL_TOKENS = 4 * WARPS;
-constexpr int MAX_RANGES = 512;  // CTAs of a large call
+constexpr int MAX_RANGES = 1024;  // CTAs of a large call
 
-// A range a CTA: a token a warp, or more where that would be too many CTAs.
-__host__ __device__ inline int range_tokens(int tokens) { return max(WARPS, (tokens + MAX_RANGES - 1) / MAX_RANGES); }
+// A range a CTA: a token a warp, or as many more as keep to MAX_RANGES.
+__host__ __device__ inline int range_tokens(int tokens)
+{
+    return WARPS * max(1, (tokens + WARPS * MAX_RANGES - 1) / (WARPS * MAX_RANGES));
+}
 
 // Larger value, larger key; of -0 and +0 one key; NaN and minus infinity 0.
 __device__ __forceinline__ uint32_t logit_key(float v)
@@ -89,32 +92,39 @@ __device__ __forceinline__ void route_token(const T* row, const RouteArgs& a, in
         total = warp_sum(s);
     }
     id = -1;
-    float logit = -INFINITY;
+    uint32_t chosen = 0;
     for (int j = 0; j < a.top_k; ++j) {
         const uint32_t k = __reduce_max_sync(~0u, mine);
         if (k == 0) break;
-        int at = SHORT ? 0xFFFF - (int)(k & 0xFFFFu) : MX_MAX_EXPERTS;
-        if constexpr (!SHORT) {
+        if (lane == j) chosen = k;
+        if constexpr (SHORT) {  // (no two keys are the same)
+            mine = 0;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                if (key[i] == k) key[i] = 0;
+                mine = max(mine, key[i]);
+            }
+        } else {
+            int at = MX_MAX_EXPERTS;
             if (mine == k) {
 #pragma unroll
                 for (int i = PER - 1; i >= 0; --i)
                     if (key[i] == k) at = lane + 32 * i;
             }
             at = __reduce_min_sync(~0u, at);
-        }
-        if (lane == j) {
-            id = at;
-            logit = value(k);
-        }
-        if ((at & 31) == lane) {
-            mine = 0;
+            if (lane == j) id = at;
+            if ((at & 31) == lane) {
+                mine = 0;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                if (at == lane + 32 * i) key[i] = 0;
-                mine = max(mine, key[i]);
+                for (int i = 0; i < PER; ++i) {
+                    if (at == lane + 32 * i) key[i] = 0;
+                    mine = max(mine, key[i]);
+                }
             }
         }
     }
+    if (SHORT && chosen) id = 0xFFFF - (int)(chosen & 0xFFFFu);
+    const float logit = chosen ? value(chosen) : -INFINITY;
     if (a.sigmoid) {
         // sigmoid(l) over the sum of them: from their logarithms, so that logits far below zero keep their ratios
         const float ls = logit > 0.0f ? -log1pf(expf(-logit)) : logit - log1pf(expf(logit));

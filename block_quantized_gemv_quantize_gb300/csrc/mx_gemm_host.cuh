@@ -23,11 +23,14 @@ bool mxs_plan(const DeviceInfo& di, const MxArgs& a, MxsPlan& p)
     if (fit < 1) return false;
     p.rows = std::min(want, fit);
     p.smem = fixed + row * p.rows;
-    // as few warps a pair of tiles as leave two and a half pairs' parts for each warp of the GPU, of three units at least
+    // Warps that share a pair of tiles: 8 to 20 units each keep the ring and the
+    // sum over the warps in proportion, more warps where a CTA has too few pairs.  (64 experts, a row
+    // each: gate and up of 1408 x 5120 with 2, 4, 8 warps 95, 89, 95 us, down of
+    // 5120 x 1408 57, 60, 76; a token of 6 experts, gate and up 26, 20, 19.5.)
     const int pairs = MODE == MX_GATE_UP ? a.L.tiles() : (a.L.tiles() + 1) / 2;
-    const int64_t all = pairs * std::min<int64_t>(a.L.experts, a.slots), warps = (int64_t)di.sms * MXS_WARPS;
-    p.parts = 2;
-    while (p.parts < MXS_WARPS && all * p.parts * 2 < warps * 5 && units >= p.parts * 6) p.parts *= 2;
+    const int64_t all = pairs * std::min<int64_t>(a.L.experts, a.slots);
+    p.parts = units >= 32 ? 4 : units >= 12 ? 2 : 1;
+    while (p.parts < MXS_WARPS && all * p.parts < (int64_t)di.sms * MXS_WARPS && units >= p.parts * 6) p.parts *= 2;
     const int64_t most = (int64_t)pairs * std::min<int64_t>(a.slots, (int64_t)a.slots / p.rows + a.L.experts);
     p.grid = (int)std::min<int64_t>(most, di.sms);
     return true;

@@ -573,7 +573,8 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
             }
         }
     } else {
-        // ---- results: 16 columns at a time through shared memory, so that a lane stores 16 bytes of a column
+        // ---- results: 16 columns at a time, rows of slots (anywhere) through shared memory, so that a lane
+        // stores 16 bytes of a column
         constexpr int WIDE = MODE == MX_GATE_UP ? 64 : 128;  // neighbouring outputs of a column
         constexpr int EACH = 16 / sizeof(O), LANES = WIDE / EACH, COLUMNS = 32 / LANES;  // a column's outputs by so many lanes
         constexpr int PER = (MXT_ROWS + 31) / 32;
@@ -623,9 +624,6 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
             const bool plain = __all_sync(~0u, p >= -126 || e == 255);
             const int n0 = (walk.g * GROUP_TILES + (int)rank * (GROUP_TILES / 2)) * MX_TILE_N;
             const int outputs = max(0, min(WIDE, a.L.N - n0)), columns = walk.n;
-            // the output's row of a column: the slot's, of partial results the place's (next to one another: the
-            // slots of an expert are far apart, every row of them on another page of memory)
-            auto out_row = [&](int c) -> int64_t { return slots[c] < 0 ? -1 : MODE == MX_DOWN ? walk.s0 + c : slots[c]; };
             if (MODE == MX_DOWN && walk.g == 0 && rank == 0 && quad == 0)
                 for (int r = lane; r < walk.cnt; r += 32)
                     if (slots[r] >= 0) a.place_of[slots[r]] = walk.s0 + r;
@@ -660,6 +658,17 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
                 if (!plain)
 #pragma unroll
                     for (int c = 0; c < 16; ++c) z[c] *= f1;
+                if constexpr (MODE == MX_DOWN) {
+                    // rows of the partial results lie next to one another: straight from the registers
+                    O* at = y + (int64_t)(walk.s0 + c0) * a.ldy + n0 + in_column;
+                    if (in_column < outputs)
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) {
+                            if (c0 + c < walk.cnt && QG_OK(qg_in(at - y, 1, (int64_t)a.slots * a.ldy), status, 333)) *at = z[c];
+                            at += a.ldy;
+                        }
+                    continue;
+                }
                 O* to = stage + half * (16 * 128) + in_column;
                 if constexpr (MODE == MX_GATE_UP) {
                     // a lane of the gate's rows and the one of the same row of up
@@ -678,7 +687,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
 #pragma unroll
                 for (int j = 0; j < 16; j += 4 * COLUMNS) {
                     const int c = j + quad * COLUMNS + lane / LANES, r = lane % LANES * EACH;
-                    const int64_t s = out_row(c0 + c);
+                    const int64_t s = slots[c0 + c];
                     O* at = y + s * a.ldy + n0 + r;
                     if (s < 0 || r >= outputs || !QG_OK(qg_in(s * a.ldy + n0 + r, min(EACH, outputs - r), (int64_t)a.slots * a.ldy), status, 332))
                         continue;

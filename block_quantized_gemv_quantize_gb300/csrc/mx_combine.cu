@@ -10,7 +10,7 @@ constexpr int THREADS = 256;
 
 // Four outputs of one token a thread.
 template <typename T>
-__global__ void __launch_bounds__(THREADS) combine_kernel(const float* __restrict__ parts, const int32_t* place_of,
+__global__ void __launch_bounds__(THREADS) combine_kernel(const float* parts, const int32_t* place_of,
                                                           const float* weights, T* out, int64_t ldo, int tokens,
                                                           int top_k, int N, int quads, bool wide, unsigned int* status)
 {

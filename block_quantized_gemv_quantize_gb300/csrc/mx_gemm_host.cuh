@@ -80,15 +80,16 @@ int launch_mxt(const MxArgs& a, cudaStream_t s)
     const int padded = a.L.units() * MX_UNIT_K;
     const int64_t rows = a.slots / a.x_div;
     const bool wide = ((reinterpret_cast<uintptr_t>(a.x) | (uintptr_t)(a.ldx * (int64_t)sizeof(T))) & 15u) == 0;
-    MxtRows x{static_cast<const __half*>(a.x), a.ldx, 0, a.L.K, nullptr};
+    MxtRows x{static_cast<const __half*>(a.x), a.ldx, 0, a.L.K, nullptr, 0};
     if (!HALVES || !wide) {
         __half* planes = static_cast<__half*>(a.planes);
         float* scale = reinterpret_cast<float*>(planes + TERMS * rows * padded);
-        x = {planes, padded, rows * padded, padded, HALVES ? nullptr : scale};
+        x = {planes, padded, rows * padded, padded, HALVES ? nullptr : scale, 0};
         if (launch_pdl(mxt_rows_kernel<T>, dim3((unsigned)std::min<int64_t>((rows + 7) / 8, (int64_t)di.sms * 8)), dim3(256), 0,
                        s, static_cast<const T*>(a.x), a.ldx, planes, scale, rows, a.L.K, padded, wide, timeouts[dev]) != cudaSuccess)
             return QGEMV_CUDA_ERROR;
     }
+    x.drop = take_drop_request();
     constexpr int GROUP = MODE == MX_GATE_UP ? 8 : 16;
     const int64_t groups = (a.L.tiles() + GROUP - 1) / GROUP;
     const int64_t most = groups * std::min<int64_t>(a.slots, (int64_t)a.slots / MXT_ROWS + a.L.experts);

@@ -30,6 +30,15 @@ __device__ __forceinline__ RunAt run_at(uint32_t block, int nb)
     return {row, (int)(block - row * (uint32_t)nb), nb};
 }
 
+// Sixteen bytes that are read once.  (Not by the read-only path: under programmatic
+// launch an earlier kernel may have been writing them when this one started.)
+__device__ __forceinline__ uint4 load_once(const void* p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, bool wide, float (&v)[8])
 {
@@ -37,7 +46,7 @@ __device__ __forceinline__ void load8(const T* p, bool wide, float (&v)[8])
         alignas(16) T t[8];
 #pragma unroll
         for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-            reinterpret_cast<uint4*>(t)[i] = ld_stream_v4(reinterpret_cast<const uint4*>(p) + i);
+            reinterpret_cast<uint4*>(t)[i] = load_once(reinterpret_cast<const uint4*>(p) + i);
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = to_f32(t[k]);
     } else {
@@ -59,7 +68,7 @@ __device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi)
 // HBM.  The scale is an exponent, so both the quotient and the code are exact
 // but for the code's own rounding.
 template <typename T>
-__global__ void __launch_bounds__(THREADS) quantize_kernel(const T* __restrict__ x, int64_t ldx, uint8_t* out,
+__global__ void __launch_bounds__(THREADS) quantize_kernel(const T* x, int64_t ldx, uint8_t* out,
                                                            uint32_t blocks, int nb, bool wide, int64_t rows,
                                                            unsigned int* status)
 {
@@ -146,7 +155,7 @@ __device__ __forceinline__ void e2m1_values(uint2 bytes, bool high, float (&v)[8
 }
 
 template <typename T>
-__global__ void __launch_bounds__(THREADS) dequantize_kernel(const uint8_t* __restrict__ in, T* y, int64_t ldy,
+__global__ void __launch_bounds__(THREADS) dequantize_kernel(const uint8_t* in, T* y, int64_t ldy,
                                                              uint32_t blocks, int nb, bool wide, int64_t rows,
                                                              unsigned int* status)
 {
@@ -161,7 +170,7 @@ __global__ void __launch_bounds__(THREADS) dequantize_kernel(const uint8_t* __re
         const uint8_t* from = in + (int64_t)first * MX_BYTES;
         if (first + RUN <= blocks) {
             for (int i = lane; i < RUN_BYTES / 16; i += 32)
-                reinterpret_cast<uint4*>(mine)[i] = ld_stream_v4(reinterpret_cast<const uint4*>(from) + i);
+                reinterpret_cast<uint4*>(mine)[i] = load_once(reinterpret_cast<const uint4*>(from) + i);
         } else {
             for (int i = lane; i < (int)(blocks - first) * MX_BYTES; i += 32) mine[i] = from[i];
         }
@@ -189,7 +198,7 @@ __global__ void __launch_bounds__(THREADS) dequantize_kernel(const uint8_t* __re
 }
 
 // One CTA a tile: the rows' largest scales, then the units, a warp a unit.
-__global__ void __launch_bounds__(128) pack_kernel(const uint8_t* __restrict__ canon, uint8_t* pack, MxLayout L,
+__global__ void __launch_bounds__(128) pack_kernel(const uint8_t* canon, uint8_t* pack, MxLayout L,
                                                    int64_t tiles, unsigned int* status)
 {
     __shared__ int tops[MX_TILE_N];

@@ -713,7 +713,10 @@ int qgemv_take_wait_timeouts(unsigned int* count);
  * running out (about a second); it counts the timeout and stops, with no copy
  * in flight for it, and the rest of the launch completes.  The next attn_paged
  * takes the request too: the copy of the first tile of its first sequence's
- * first kv head is left out, whose rows come out NaN.  Process-wide; returns the
+ * first kv head is left out, whose rows come out NaN; and the next product of
+ * MXFP4 experts with many rows (qgemm_mxfp4, moe_gate_up_mxfp4 or
+ * moe_down_mxfp4) whose first CTA then does not announce its first rows of x and
+ * leaves its outputs unwritten.  Process-wide; returns the
  * previous request (0 or 1).  (Not from the pages.) */
 int qgemv_debug_drop_next_copy(void);
 

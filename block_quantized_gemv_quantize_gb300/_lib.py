@@ -133,14 +133,16 @@ def _load_calls():
         spec = importlib.util.spec_from_file_location("qgemv_calls", _build.CALLS)
         calls = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(calls)
-        calls.init(*(ctypes.cast(getattr(LIB, name), ctypes.c_void_p).value for name in (
-            "kv_write", "kv_read", "attn_paged", "kv_page_bytes", "attn_paged_workspace_bytes", "quantize_mxfp4",
-            "dequantize_mxfp4", "moe_route", "moe_route_workspace_bytes", "mxfp4_pack_bytes", "qgemm_mxfp4",
+        address = lambda name: ctypes.cast(getattr(LIB, name), ctypes.c_void_p).value  # noqa: E731
+        calls.init(*map(address, ("kv_write", "kv_read", "attn_paged", "kv_page_bytes", "attn_paged_workspace_bytes")))
+        calls.init_sparse(*map(address, (
+            "quantize_mxfp4", "dequantize_mxfp4", "moe_route", "moe_route_workspace_bytes", "mxfp4_pack_bytes", "qgemm_mxfp4",
             "moe_gate_up_mxfp4", "moe_down_mxfp4", "qgemm_mxfp4_workspace_bytes", "moe_gate_up_mxfp4_workspace_bytes",
             "moe_down_mxfp4_workspace_bytes")))
         return calls
     except (ImportError, OSError) as e:
-        warnings.warn(f"the paged cache's calls go through ctypes, three times as long on the host: {e}", RuntimeWarning)
+        warnings.warn(f"the paged cache's and the sparse layer's calls go through ctypes, three times as long on the host: {e}",
+                      RuntimeWarning)
         return types.SimpleNamespace(**{name: lambda *args: None for name in (
             "kv_write", "kv_read", "attn_paged", "quantize_mxfp4", "dequantize_mxfp4", "moe_route", "product")})
 

@@ -3,7 +3,7 @@
 // and calls the library.  A call that it would refuse, or whose tensors it does not
 // know how to take, returns None and goes through the ctypes binding (_lib.py), which
 // does the same and says what is wrong.  Only host code: the kernels are the
-// library's, by the addresses of its entry points that init() gets.  A call of
+// library's, by the addresses of its entry points that init() and init_sparse() get.  A call of
 // attn_paged takes the host 7 us, of kv_read with new outputs 5 and of kv_write 2, by
 // ctypes 20, 15 and 8, beside 2 to 10 us of kernels on small inputs.
 // As many calls are the sparse layer's: a router, two products, MXFP4 rows in and out.
@@ -466,40 +466,56 @@ PyObject* guarded(PyObject* self, PyObject* const* args, Py_ssize_t n)
     }
 }
 
-// init(addresses of the entry points above, in their order)
-PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n_args)
+// N addresses of entry points
+template <int N>
+bool addresses(PyObject* const* a, Py_ssize_t n_args, void* (&p)[N])
 {
-    constexpr int N = 16;
-    void* p[N];
     if (n_args != N) {
-        PyErr_SetString(PyExc_TypeError, "sixteen addresses");
-        return nullptr;
+        PyErr_Format(PyExc_TypeError, "%d addresses", N);
+        return false;
     }
     for (int i = 0; i < N; ++i)
         if (!(p[i] = PyLong_AsVoidPtr(a[i]))) {
             if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "a null address");
-            return nullptr;
+            return false;
         }
+    return true;
+}
+
+// init(addresses of kv_write, kv_read, attn_paged, kv_page_bytes, attn_paged_workspace_bytes)
+PyObject* init(PyObject*, PyObject* const* a, Py_ssize_t n_args)
+{
+    void* p[5];
+    if (!addresses(a, n_args, p)) return nullptr;
     kv_write_entry = reinterpret_cast<decltype(kv_write_entry)>(p[0]);
     kv_read_entry = reinterpret_cast<decltype(kv_read_entry)>(p[1]);
     attn_entry = reinterpret_cast<decltype(attn_entry)>(p[2]);
     page_bytes_entry = reinterpret_cast<decltype(page_bytes_entry)>(p[3]);
     workspace_bytes_entry = reinterpret_cast<decltype(workspace_bytes_entry)>(p[4]);
-    quantize_entry = reinterpret_cast<decltype(quantize_entry)>(p[5]);
-    dequantize_entry = reinterpret_cast<decltype(dequantize_entry)>(p[6]);
-    route_entry = reinterpret_cast<decltype(route_entry)>(p[7]);
-    route_bytes_entry = reinterpret_cast<decltype(route_bytes_entry)>(p[8]);
-    pack_bytes_entry = reinterpret_cast<decltype(pack_bytes_entry)>(p[9]);
-    gemm_entry = reinterpret_cast<decltype(gemm_entry)>(p[10]);
-    gate_up_entry = reinterpret_cast<decltype(gate_up_entry)>(p[11]);
-    down_entry = reinterpret_cast<decltype(down_entry)>(p[12]);
-    for (int i = 0; i < 3; ++i)
-        product_bytes_entry[i] = reinterpret_cast<decltype(&::qgemm_mxfp4_workspace_bytes)>(p[13 + i]);
+    Py_RETURN_NONE;
+}
+
+// init_sparse(addresses of quantize_mxfp4, dequantize_mxfp4, moe_route, moe_route_workspace_bytes, mxfp4_pack_bytes,
+//             qgemm_mxfp4, moe_gate_up_mxfp4, moe_down_mxfp4 and the three's workspace queries)
+PyObject* init_sparse(PyObject*, PyObject* const* a, Py_ssize_t n_args)
+{
+    void* p[11];
+    if (!addresses(a, n_args, p)) return nullptr;
+    quantize_entry = reinterpret_cast<decltype(quantize_entry)>(p[0]);
+    dequantize_entry = reinterpret_cast<decltype(dequantize_entry)>(p[1]);
+    route_entry = reinterpret_cast<decltype(route_entry)>(p[2]);
+    route_bytes_entry = reinterpret_cast<decltype(route_bytes_entry)>(p[3]);
+    pack_bytes_entry = reinterpret_cast<decltype(pack_bytes_entry)>(p[4]);
+    gemm_entry = reinterpret_cast<decltype(gemm_entry)>(p[5]);
+    gate_up_entry = reinterpret_cast<decltype(gate_up_entry)>(p[6]);
+    down_entry = reinterpret_cast<decltype(down_entry)>(p[7]);
+    for (int i = 0; i < 3; ++i) product_bytes_entry[i] = reinterpret_cast<decltype(&::qgemm_mxfp4_workspace_bytes)>(p[8 + i]);
     Py_RETURN_NONE;
 }
 
 #define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f))
 PyMethodDef methods[] = {{"init", FAST(init), METH_FASTCALL, nullptr},
+                         {"init_sparse", FAST(init_sparse), METH_FASTCALL, nullptr},
                          {"kv_write", FAST(guarded<call_kv_write>), METH_FASTCALL, nullptr},
                          {"kv_read", FAST(guarded<call_kv_read>), METH_FASTCALL, nullptr},
                          {"attn_paged", FAST(guarded<call_attn_paged>), METH_FASTCALL, nullptr},

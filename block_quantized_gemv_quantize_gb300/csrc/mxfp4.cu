@@ -1,10 +1,13 @@
 // MXFP4: quantizer, its inverse, and the repacker of weights.
 #include "mxfp4.cuh"
 
+#include <type_traits>
+
 namespace qgemv {
 namespace {
 
 constexpr int THREADS = 256;
+constexpr int QUANTIZE_CTAS = 5;            // an SM
 constexpr int RUN = 32;                     // blocks that a warp takes at a time
 constexpr int RUN_BYTES = RUN * MX_BYTES;   // 544, a multiple of 16: runs of the output stay aligned
 
@@ -39,36 +42,96 @@ __device__ __forceinline__ uint4 load_once(const void* p)
     return v;
 }
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, bool wide, float (&v)[8])
+// Four bytes of two codes each, lo[i] in the low nibble: nearest, of two equally near the
+// even one, at most 6 in magnitude (what the format asks for).
+__device__ __forceinline__ uint32_t e2m1_bytes(const float (&lo)[4], const float (&hi)[4])
 {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %5, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, %6, %2;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %7, %3;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, %8, %4;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(r)
+        : "f"(lo[0]), "f"(lo[1]), "f"(lo[2]), "f"(lo[3]), "f"(hi[0]), "f"(hi[1]), "f"(hi[2]), "f"(hi[3]));
+    return r;
+}
+
+// Eight values as they lie in memory.
+template <typename T>
+struct Raw {
+    uint32_t w[2 * sizeof(T)];
+};
+template <typename T>
+__device__ __forceinline__ Raw<T> load_raw(const T* p, bool wide)
+{
+    Raw<T> r;
     if (wide) {
-        alignas(16) T t[8];
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-            reinterpret_cast<uint4*>(t)[i] = load_once(reinterpret_cast<const uint4*>(p) + i);
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+            const uint4 v = load_once(reinterpret_cast<const uint4*>(p) + i);
+            r.w[4 * i] = v.x;
+            r.w[4 * i + 1] = v.y;
+            r.w[4 * i + 2] = v.z;
+            r.w[4 * i + 3] = v.w;
+        }
+    } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = to_f32(t[k]);
+        for (int i = 0; i < 8; ++i) r.w[i] = __float_as_uint(p[i]);
     } else {
+        const uint16_t* u = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = to_f32(p[k]);
+        for (int i = 0; i < 4; ++i) r.w[i] = (uint32_t)u[2 * i] | (uint32_t)u[2 * i + 1] << 16;
+    }
+    return r;
+}
+
+// The largest magnitude's fp32 bits.  (Magnitudes order like their bits; NaN and infinity come last.)
+template <typename T>
+__device__ __forceinline__ uint32_t top_bits(const Raw<T>& r)
+{
+    if constexpr (sizeof(T) == 4) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max(top, r.w[i] & 0x7FFFFFFFu);
+        return top;
+    } else {
+        uint32_t m = r.w[0] & 0x7FFF7FFFu;
+#pragma unroll
+        for (int i = 1; i < 4; ++i) m = __vmaxu2(m, r.w[i] & 0x7FFF7FFFu);
+        const uint32_t top = max(m & 0xFFFFu, m >> 16);
+        if constexpr (std::is_same<T, __nv_bfloat16>::value) return top << 16;
+        else return __float_as_uint(__half2float(__ushort_as_half((unsigned short)top)));
     }
 }
 
-// Two codes in a byte, `lo` in the low nibble: nearest, of two equally near the
-// even one, at most 6 in magnitude (what the format asks for).
-__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi)
+// Four values, of which the first sits in w[0].
+template <typename T>
+__device__ __forceinline__ void values4(const uint32_t* w, float (&v)[4])
 {
-    uint32_t r;
-    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(r) : "f"(lo), "f"(hi));
-    return r;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(w + i));
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    }
 }
 
 // One pass over the data: reads 32 s bytes (s: bytes of an element), writes 17 a block, and is bound by
 // HBM.  The scale is an exponent, so both the quotient and the code are exact
 // but for the code's own rounding.
 template <typename T>
-__global__ void __launch_bounds__(THREADS) quantize_kernel(const T* x, int64_t ldx, uint8_t* out,
+__global__ void __launch_bounds__(THREADS, QUANTIZE_CTAS) quantize_kernel(const T* x, int64_t ldx, uint8_t* out,
                                                            uint32_t blocks, int nb, bool wide, int64_t rows,
                                                            unsigned int* status)
 {
@@ -81,42 +144,43 @@ __global__ void __launch_bounds__(THREADS) quantize_kernel(const T* x, int64_t l
     for (uint32_t run = blockIdx.x * (THREADS / 32) + warp; run < runs; run += gridDim.x * (THREADS / 32)) {
         const uint32_t first = run * RUN;
         RunAt at = run_at(first + (lane >> 2), nb);
-        float v[4][8];
+        Raw<T> v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (first + 8 * i + (lane >> 2) < blocks &&
                 QG_OK(at.row < rows && qg_in((int64_t)at.col * 32 + sub * 8, 8, (int64_t)nb * 32), status, 300))
-                load8(x + at.row * ldx + (int64_t)at.col * 32 + sub * 8, wide, v[i]);
+                v[i] = load_raw(x + at.row * ldx + (int64_t)at.col * 32 + sub * 8, wide);
             else
-#pragma unroll
-                for (int k = 0; k < 8; ++k) v[i][k] = 0.0f;
+                v[i] = Raw<T>{};
             at.next();
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            uint32_t top = 0;  // magnitudes order like their bits; NaN and infinity come last
-#pragma unroll
-            for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(v[i][k]) & 0x7FFFFFFFu);
+            uint32_t top = top_bits<T>(v[i]);
             top = max(top, __shfl_xor_sync(~0u, top, 1));
             top = max(top, __shfl_xor_sync(~0u, top, 2));
             const bool fine = top < 0x7F800000u;
             const int e = fine ? max(0, (int)(top >> 23) - 2) : 255;
             const float f = __uint_as_float((uint32_t)(254 - min(e, 253)) << 23);  // 2^(127 - e)
-            uint32_t word = 0;
+            // lane sub < 2 has values 8 sub .., lane sub + 2 those 16 further on, which share
+            // bytes 8 sub ..: each takes four of them, the first two words of both or the last
+            constexpr int H = sizeof(T);  // words of four values
+            uint32_t lo[H], hi[H];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) word |= e2m1_pair(v[i][2 * k] * f, v[i][2 * k + 1] * f) << (8 * k);
-            if (!fine) word = 0;
-            // lane sub < 2 has values 8 sub .., lane sub + 2 those 16 further
-            // on, which share the bytes 8 sub ..: each makes four of them
-            const uint32_t other = __shfl_xor_sync(~0u, word, 2);
-            uint32_t lo = sub < 2 ? word : other >> 16, hi = sub < 2 ? other : word >> 16;
-            lo &= 0xFFFFu;
-            hi &= 0xFFFFu;
-            lo = (lo | lo << 8) & 0x00FF00FFu;
-            lo = (lo | lo << 4) & 0x0F0F0F0Fu;
-            hi = (hi | hi << 8) & 0x00FF00FFu;
-            hi = (hi | hi << 4) & 0x0F0F0F0Fu;
-            const uint32_t bytes = lo | hi << 4;
+            for (int k = 0; k < H; ++k) {
+                const uint32_t other = __shfl_xor_sync(~0u, sub < 2 ? v[i].w[H + k] : v[i].w[k], 2);
+                lo[k] = sub < 2 ? v[i].w[k] : other;
+                hi[k] = sub < 2 ? other : v[i].w[H + k];
+            }
+            float a[4], c[4];
+            values4<T>(lo, a);
+            values4<T>(hi, c);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                a[k] *= f;
+                c[k] *= f;
+            }
+            const uint32_t bytes = fine ? e2m1_bytes(a, c) : 0u;
             uint8_t* b = mine + (8 * i + (lane >> 2)) * MX_BYTES;
             if (sub == 0) b[0] = (uint8_t)e;
             b += 1 + 8 * (sub & 1) + 4 * (sub >> 1);
@@ -155,7 +219,7 @@ __device__ __forceinline__ void e2m1_values(uint2 bytes, bool high, float (&v)[8
 }
 
 template <typename T>
-__global__ void __launch_bounds__(THREADS) dequantize_kernel(const uint8_t* in, T* y, int64_t ldy,
+__global__ void __launch_bounds__(THREADS, 8) dequantize_kernel(const uint8_t* in, T* y, int64_t ldy,
                                                              uint32_t blocks, int nb, bool wide, int64_t rows,
                                                              unsigned int* status)
 {
@@ -256,10 +320,11 @@ bool rows_wide(const void* p, int64_t ld)
     return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * (int64_t)sizeof(T))) & 15u) == 0;
 }
 
-unsigned run_grid(const DeviceInfo& di, int64_t blocks)
+// (as many CTAs an SM as are there at once: a second wave would end half empty)
+unsigned run_grid(const DeviceInfo& di, int64_t blocks, int ctas)
 {
     const int64_t per_cta = THREADS / 32 * RUN, grid = (blocks + per_cta - 1) / per_cta;
-    return (unsigned)(grid < (int64_t)di.sms * 8 ? grid : (int64_t)di.sms * 8);
+    return (unsigned)(grid < (int64_t)di.sms * ctas ? grid : (int64_t)di.sms * ctas);
 }
 
 template <typename T>
@@ -268,7 +333,7 @@ int quantize_t(const void* x, int64_t ldx, void* blocks, int64_t N, int K, cudaS
     const DeviceInfo di = device_info();
     if (di.sms <= 0) return QGEMV_CUDA_ERROR;
     const int nb = K / 32;
-    return launch_pdl(quantize_kernel<T>, dim3(run_grid(di, N * nb)), dim3(THREADS), 0, s, static_cast<const T*>(x), ldx,
+    return launch_pdl(quantize_kernel<T>, dim3(run_grid(di, N * nb, QUANTIZE_CTAS)), dim3(THREADS), 0, s, static_cast<const T*>(x), ldx,
                       static_cast<uint8_t*>(blocks), (uint32_t)(N * nb), nb, rows_wide<T>(x, ldx), N,
                       wait_timeout_counter()) == cudaSuccess
                ? QGEMV_OK
@@ -281,7 +346,7 @@ int dequantize_t(const void* blocks, void* y, int64_t ldy, int64_t N, int K, cud
     const DeviceInfo di = device_info();
     if (di.sms <= 0) return QGEMV_CUDA_ERROR;
     const int nb = K / 32;
-    return launch_pdl(dequantize_kernel<T>, dim3(run_grid(di, N * nb)), dim3(THREADS), 0, s,
+    return launch_pdl(dequantize_kernel<T>, dim3(run_grid(di, N * nb, 8)), dim3(THREADS), 0, s,
                       static_cast<const uint8_t*>(blocks), static_cast<T*>(y), ldy, (uint32_t)(N * nb), nb,
                       rows_wide<T>(y, ldy), N, wait_timeout_counter()) == cudaSuccess
                ? QGEMV_OK

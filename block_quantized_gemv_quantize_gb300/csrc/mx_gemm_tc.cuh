@@ -14,8 +14,8 @@
 // shared-memory bandwidth, and the pair halves what the other one costs.
 // Sums are the tensor core's, in fp32; the epilogue multiplies by the powers of two.
 //
-// In each CTA of a pair 8 warps convert weights (32 rows of tensor memory
-// each, every other step), 3 gather rows of x by asynchronous copies into
+// In each CTA of a pair 12 warps convert weights (32 rows of tensor memory
+// each, every third step), 3 gather rows of x by asynchronous copies into
 // 128-byte-swizzled shared memory (TMA's gather of four rows takes twice as long), 4 write
 // results while the next item's products run (two accumulators); one thread
 // of the first CTA issues the products for both.  256 rows of weights (128 of gate and of up,
@@ -28,10 +28,14 @@
 
 namespace qgemv {
 
-constexpr int MXT_CONVERT = 8, MXT_EPI = 4, MXT_MMA_WARP = 12, MXT_LOAD_WARP = 13, MXT_LOAD = 3;
+constexpr int MXT_CONVERT = 12, MXT_EPI = 4, MXT_EPI_WARP = 12, MXT_MMA_WARP = 16, MXT_LOAD_WARP = 17, MXT_LOAD = 3;
 constexpr int MXT_THREADS = (MXT_LOAD_WARP + MXT_LOAD) * 32;
 constexpr int MXT_ROWS = 160;    // of x an item: two accumulators of that many columns
 constexpr int MXT_A_STAGES = 3;  // of two units, 64 columns each: what hides a round trip between the roles
+static_assert(MXT_CONVERT == 4 * MXT_A_STAGES, "a warpgroup a stage");
+// Registers a thread: 640 of 96 at launch, of which the results' warpgroup gets 24 each of the last one's.
+constexpr int MXT_REGS = 96, MXT_EPI_REGS = 120, MXT_REST_REGS = 72;
+static_assert(MXT_THREADS == 640 && MXT_CONVERT * MXT_REGS + MXT_EPI * MXT_EPI_REGS + 4 * MXT_REST_REGS == 20 * MXT_REGS, "register shares");
 constexpr uint32_t MXT_A_COL = 2 * MXT_ROWS;
 static_assert(MXT_A_COL + MXT_A_STAGES * 64 <= 512, "tensor memory");
 constexpr long long MXT_WAIT_CLOCKS = 2000000000;  // about a second
@@ -44,7 +48,7 @@ constexpr int MXT_EPI_BYTES = 2 * 16 * 128 * 4;  // two halves of 16 columns of 
 
 template <int TERMS>
 struct MxtShape {
-    static constexpr int BATCH = TERMS == 1 ? 2 : 1, BATCHES = 4, AHEAD = 2;
+    static constexpr int BATCH = TERMS == 1 ? 2 : 1, BATCHES = 3, AHEAD = 2;
 };
 
 struct MxtRows {
@@ -302,7 +306,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
             mbar_init(empty_b + i, 1);
         }
         for (int i = 0; i < MXT_A_STAGES; ++i) {
-            mbar_init(full_a + i, MXT_CONVERT);  // four warps of each CTA
+            mbar_init(full_a + i, 8);  // four warps of each CTA
             mbar_init(empty_a + i, 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -361,14 +365,17 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
         return walk.g * GROUP_TILES + (int)rank * (GROUP_TILES / 2) + (MODE == MX_GATE_UP ? quad : 2 * quad + i);
     };
 
+    if (warp >= MXT_MMA_WARP) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(MXT_REST_REGS));
+    else if (warp >= MXT_EPI_WARP) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(MXT_EPI_REGS));
+
     if (warp < MXT_CONVERT) {
-        // ---- weights into tensor memory: four warps take the even steps, four the odd ones
-        const int quad = warp & 3, odd = warp >> 2, g = lane >> 2;
-        const uint32_t to = tmem + MXT_A_COL + ((uint32_t)(32 * quad) << 16);
+        // ---- weights into tensor memory: a warpgroup takes every third step, always into the same stage
+        const int quad = warp & 3, stage = warp >> 2, g = lane >> 2;
+        const uint32_t to = tmem + MXT_A_COL + stage * 64 + ((uint32_t)(32 * quad) << 16);
         constexpr int AHEAD = S::AHEAD, SLOT = 4 * MX_UNIT_BYTES;  // two tiles' two units
         uint8_t* ring = sm + BATCHES * BATCH * STEP_BYTES + warp * (AHEAD * SLOT);
         bool more = walk.find();
-        int64_t left = more ? (walk.items - walk.item + walk.step - 1) / walk.step * steps - odd : 0;  // of the CTA, from this warp's on
+        int64_t left = more ? (walk.items - walk.item + walk.step - 1) / walk.step * steps - stage : 0;  // of the CTA, from this warp's on
         int u = 0;
         const uint8_t* from[2];
         bool there[2];
@@ -405,21 +412,19 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
                     }
                 }
                 if (++slot == AHEAD) slot = 0;
-                advance(2);
+                advance(MXT_A_STAGES);
             }
             cp_async_commit();
         };
         if (more) locate();
-        advance(odd);
+        advance(stage);
 #pragma unroll
         for (int j = 0; j < AHEAD - 1; ++j) fetch();
-        int mine = 0, stage = odd;
+        int mine = 0, at_step = stage;  // of the CTA's, over all items
         uint32_t phase = 1;
-        MxtStage<BATCHES> b;
-        if (BATCH == 1 && odd) b.next();
         // (one body, not unrolled: the roles' loops share the instruction caches)
 #pragma unroll 1
-        for (; left > 0; left -= 2) {
+        for (; left > 0; left -= MXT_A_STAGES, at_step += MXT_A_STAGES, phase ^= 1) {
             cp_async_wait<AHEAD - 2>();
             __syncwarp();
             const uint8_t* at = ring + mine * SLOT;
@@ -446,24 +451,18 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
                     if (!wait(empty_a + stage, phase)) goto stop;
                     tc_fence_after();
                 }
-                tc_st_16x256b_x4(to + stage * 64 + 32 * h, r[0]);
-                tc_st_16x256b_x4(to + stage * 64 + 32 * h + (16u << 16), r[1]);
+                tc_st_16x256b_x4(to + 32 * h, r[0]);
+                tc_st_16x256b_x4(to + 32 * h + (16u << 16), r[1]);
             }
             tc_wait_st();
             tc_fence_before();
             // one of the four announces the rows of x too, which came long ago
-            if (quad == 0 && (BATCH == 1 || odd == 0)) {
-                if (!wait(full_b + b.i, b.phase)) break;
-                b.next();
-                if (BATCH == 1) b.next();
+            if (quad == 0 && at_step % BATCH == 0) {
+                const int b = at_step / BATCH;
+                if (!wait(full_b + b % BATCHES, b / BATCHES & 1)) break;
             }
             __syncwarp();
             if (lane == 0) arrive_first(full_a + stage);
-            stage += 2;
-            if (stage >= MXT_A_STAGES) {
-                stage -= MXT_A_STAGES;
-                phase ^= 1;
-            }
         }
     stop:
         cp_async_wait<0>();

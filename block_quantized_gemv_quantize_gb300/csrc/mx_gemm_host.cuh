@@ -85,8 +85,11 @@ int launch_mxt(const MxArgs& a, cudaStream_t s)
         __half* planes = static_cast<__half*>(a.planes);
         float* scale = reinterpret_cast<float*>(planes + TERMS * rows * padded);
         x = {planes, padded, rows * padded, padded, HALVES ? nullptr : scale, 0};
-        if (launch_pdl(mxt_rows_kernel<T>, dim3((unsigned)std::min<int64_t>((rows + 7) / 8, (int64_t)di.sms * 8)), dim3(256), 0,
-                       s, static_cast<const T*>(a.x), a.ldx, planes, scale, rows, a.L.K, padded, wide, timeouts[dev]) != cudaSuccess)
+        // (a warp a row where that fills the GPU and a row its registers)
+        const bool narrow = padded <= (int)(4096 / sizeof(T)) && rows >= 4 * (int64_t)di.sms;
+        const unsigned ctas = (unsigned)std::min<int64_t>(narrow ? (rows + 3) / 4 : rows, (int64_t)di.sms * 8);
+        if (launch_pdl(narrow ? mxt_rows_kernel<T, 1> : mxt_rows_kernel<T, 4>, dim3(ctas), dim3(MXT_ROW_THREADS), 0, s,
+                       static_cast<const T*>(a.x), a.ldx, planes, scale, rows, a.L.K, padded, wide, timeouts[dev]) != cudaSuccess)
             return QGEMV_CUDA_ERROR;
     }
     x.drop = take_drop_request();

@@ -177,48 +177,98 @@ __device__ __forceinline__ void e2m1_scaled(uint32_t w, uint32_t scale, uint32_t
 // ---- rows of x as halves ------------------------------------------------------------
 
 // x [rows][K] -> planes [term][rows][padded], zeros behind a row, and each
-// row's power of two.  A warp a row, read twice (the second time from L1 or L2); bound by memory.
-template <typename T>
-__global__ void __launch_bounds__(256) mxt_rows_kernel(const T* x, int64_t ld, __half* planes, float* scale,
-                                                       int64_t rows, int K, int padded, bool wide, unsigned int* status)
+// row's power of two.  WARPS warps a row, eight values a lane at a time, the first
+// 2048 WARPS (fp32: 1024) of a row kept in registers between its maximum and its conversion (a longer
+// row's rest is read twice); bound by memory, or by latency where rows are few.
+constexpr int MXT_ROW_THREADS = 128;
+
+template <typename T, int WARPS>
+__global__ void __launch_bounds__(MXT_ROW_THREADS, 8) mxt_rows_kernel(const T* x, int64_t ld, __half* planes, float* scale,
+                                                                   int64_t rows, int K, int padded, bool wide,
+                                                                   unsigned int* status)
 {
-    constexpr int TERMS = MX_TERMS<T>;
+    constexpr int TERMS = MX_TERMS<T>, ROWS = MXT_ROW_THREADS / 32 / WARPS, STEP = 256 * WARPS, KEEP = 16 / sizeof(T);
     constexpr bool SCALED = !std::is_same<T, __half>::value;
+    __shared__ uint32_t tops[MXT_ROW_THREADS / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int k0 = (threadIdx.x % (32 * WARPS)) * 8;
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    for (int64_t row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); row < rows; row += (int64_t)gridDim.x * 8) {
+    for (int64_t first = (int64_t)blockIdx.x * ROWS; first < rows; first += (int64_t)gridDim.x * ROWS) {
+        const int64_t row = first + warp / WARPS;
+        const bool there = row < rows;
         const T* from = x + row * ld;
-        int e = 0;
-        if constexpr (SCALED) {
-            uint32_t top = 0;
-#pragma unroll 4
-            for (int k = lane * 8; k < K; k += 256) {
-                float v[8];
-                mx_load8(from + k, wide, K - k, v);
+        Raw<T> v[KEEP];
+        uint32_t top = 0;
+        auto values = [](const Raw<T>& r, float (&f)[8]) {
+            float a[4], b[4];
+            values4<T>(r.w, a);
+            values4<T>(r.w + sizeof(T), b);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t m = __float_as_uint(v[j]) & 0x7FFFFFFFu;
-                    top = max(top, m < 0x7F800000u ? m : 0u);
-                }
+            for (int j = 0; j < 4; ++j) {
+                f[j] = a[j];
+                f[4 + j] = b[j];
             }
-            e = mx_row_exponent(__reduce_max_sync(~0u, top));
-            if (lane == 0) scale[row] = __uint_as_float((uint32_t)(127 + e) << 23);
+        };
+        auto take = [&](const float (&f)[8]) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t m = __float_as_uint(f[j]) & 0x7FFFFFFFu;
+                top = max(top, m < 0x7F800000u ? m : 0u);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i) {
+            const int k = k0 + i * STEP;
+            if (there && k < K) v[i] = load_raw(from + k, wide);  // (K is a multiple of 32)
+            else v[i] = Raw<T>{};
         }
+        if constexpr (SCALED) {
+#pragma unroll
+            for (int i = 0; i < KEEP; ++i) {
+                float f[8];
+                values(v[i], f);
+                take(f);
+            }
+            for (int k = k0 + KEEP * STEP; k < K && there; k += STEP) {
+                float f[8];
+                mx_load8(from + k, wide, K - k, f);
+                take(f);
+            }
+            top = __reduce_max_sync(~0u, top);
+            if constexpr (WARPS > 1) {
+                __syncthreads();  // (the row before is done with)
+                if (lane == 0) tops[warp] = top;
+                __syncthreads();
+#pragma unroll
+                for (int i = 0; i < WARPS; ++i) top = max(top, tops[warp / WARPS * WARPS + i]);
+            }
+        }
+        const int e = SCALED ? mx_row_exponent(top) : 0;
+        if (SCALED && there && k0 == 0) scale[row] = __uint_as_float((uint32_t)(127 + e) << 23);
         const float f = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll 2
-        for (int k = lane * 8; k < padded; k += 256) {
-            float v[8];
-            mx_load8(from + k, wide, max(0, K - k), v);
+        auto put = [&](int k, const float (&z)[8]) {
             __half h[8], l[8];
-            mx_row_halves<T>(v, f, h, l);
-            if (!QG_OK(qg_in(row * padded + k, 8, rows * padded), status, 330)) continue;
+            mx_row_halves<T>(z, f, h, l);
+            if (!QG_OK(qg_in(row * padded + k, 8, rows * padded), status, 330)) return;
             __half* to = planes + row * padded + k;
             *reinterpret_cast<uint4*>(to) =
                 make_uint4(mx_halves(h[0], h[1]), mx_halves(h[2], h[3]), mx_halves(h[4], h[5]), mx_halves(h[6], h[7]));
             if constexpr (TERMS == 2)
                 *reinterpret_cast<uint4*>(to + rows * padded) =
                     make_uint4(mx_halves(l[0], l[1]), mx_halves(l[2], l[3]), mx_halves(l[4], l[5]), mx_halves(l[6], l[7]));
+        };
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i)
+            if (there && k0 + i * STEP < padded) {
+                float z[8];
+                values(v[i], z);
+                put(k0 + i * STEP, z);
+            }
+        for (int k = k0 + KEEP * STEP; k < padded && there; k += STEP) {
+            float z[8];
+            mx_load8(from + k, wide, max(0, K - k), z);
+            put(k, z);
         }
     }
 }

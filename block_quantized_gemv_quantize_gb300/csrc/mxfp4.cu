@@ -1,8 +1,6 @@
 // MXFP4: quantizer, its inverse, and the repacker of weights.
 #include "mxfp4.cuh"
 
-#include <type_traits>
-
 namespace qgemv {
 namespace {
 
@@ -33,15 +31,6 @@ __device__ __forceinline__ RunAt run_at(uint32_t block, int nb)
     return {row, (int)(block - row * (uint32_t)nb), nb};
 }
 
-// Sixteen bytes that are read once.  (Not by the read-only path: under programmatic
-// launch an earlier kernel may have been writing them when this one started.)
-__device__ __forceinline__ uint4 load_once(const void* p)
-{
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
-    return v;
-}
-
 // Four bytes of two codes each, lo[i] in the low nibble: nearest, of two equally near the
 // even one, at most 6 in magnitude (what the format asks for).
 __device__ __forceinline__ uint32_t e2m1_bytes(const float (&lo)[4], const float (&hi)[4])
@@ -53,35 +42,6 @@ __device__ __forceinline__ uint32_t e2m1_bytes(const float (&lo)[4], const float
         "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
         : "=r"(r)
         : "f"(lo[0]), "f"(lo[1]), "f"(lo[2]), "f"(lo[3]), "f"(hi[0]), "f"(hi[1]), "f"(hi[2]), "f"(hi[3]));
-    return r;
-}
-
-// Eight values as they lie in memory.
-template <typename T>
-struct Raw {
-    uint32_t w[2 * sizeof(T)];
-};
-template <typename T>
-__device__ __forceinline__ Raw<T> load_raw(const T* p, bool wide)
-{
-    Raw<T> r;
-    if (wide) {
-#pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
-            const uint4 v = load_once(reinterpret_cast<const uint4*>(p) + i);
-            r.w[4 * i] = v.x;
-            r.w[4 * i + 1] = v.y;
-            r.w[4 * i + 2] = v.z;
-            r.w[4 * i + 3] = v.w;
-        }
-    } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r.w[i] = __float_as_uint(p[i]);
-    } else {
-        const uint16_t* u = reinterpret_cast<const uint16_t*>(p);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) r.w[i] = (uint32_t)u[2 * i] | (uint32_t)u[2 * i + 1] << 16;
-    }
     return r;
 }
 
@@ -101,29 +61,6 @@ __device__ __forceinline__ uint32_t top_bits(const Raw<T>& r)
         const uint32_t top = max(m & 0xFFFFu, m >> 16);
         if constexpr (std::is_same<T, __nv_bfloat16>::value) return top << 16;
         else return __float_as_uint(__half2float(__ushort_as_half((unsigned short)top)));
-    }
-}
-
-// Four values, of which the first sits in w[0].
-template <typename T>
-__device__ __forceinline__ void values4(const uint32_t* w, float (&v)[4])
-{
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
-    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(w + i));
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
-        }
     }
 }
 

@@ -2,6 +2,8 @@
 // formats, layouts and launch arguments (include/qgemv.h has the definitions).
 #pragma once
 
+#include <type_traits>
+
 #include "kvcache.cuh"  // element types of rows
 
 namespace qgemv {
@@ -55,6 +57,69 @@ __device__ __forceinline__ float mul_pow2(float v, int p)
     float y = v * __uint_as_float((uint32_t)(a + 127) << 23) * __uint_as_float((uint32_t)(b + 127) << 23);
     if (c) y *= __uint_as_float((uint32_t)(max(-126, min(127, c)) + 127) << 23);
     return y;
+}
+
+// ---- rows of values -------------------------------------------------------------
+
+// Sixteen bytes that are read once.  (Not by the read-only path: under programmatic
+// launch an earlier kernel may have been writing them when this one started.)
+__device__ __forceinline__ uint4 load_once(const void* p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+
+// Eight values as they lie in memory.
+template <typename T>
+struct Raw {
+    uint32_t w[2 * sizeof(T)];
+};
+template <typename T>
+__device__ __forceinline__ Raw<T> load_raw(const T* p, bool wide)
+{
+    Raw<T> r;
+    if (wide) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+            const uint4 v = load_once(reinterpret_cast<const uint4*>(p) + i);
+            r.w[4 * i] = v.x;
+            r.w[4 * i + 1] = v.y;
+            r.w[4 * i + 2] = v.z;
+            r.w[4 * i + 3] = v.w;
+        }
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r.w[i] = __float_as_uint(p[i]);
+    } else {
+        const uint16_t* u = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.w[i] = (uint32_t)u[2 * i] | (uint32_t)u[2 * i + 1] << 16;
+    }
+    return r;
+}
+
+// Four values, of which the first sits in w[0].
+template <typename T>
+__device__ __forceinline__ void values4(const uint32_t* w, float (&v)[4])
+{
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
+    } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(w + i));
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    }
 }
 
 int launch_quantize_mxfp4(int type, const void* x, int64_t ldx, void* blocks, int64_t N, int K, cudaStream_t s);

@@ -9,7 +9,8 @@
 // Up to SMALL_TOKENS tokens one CTA does all of it in one launch (latency);
 // beyond, a first kernel routes and counts, a second adds up each bin's counts
 // over the ranges, a third places the slots.  Bound by latency: of a token's
-// top_k rounds, and of the three launches.
+// top_k rounds, and of the three launches (17391 tokens, 8 of 128 experts: 21 us,
+// one token 3.6; a second kernel in which each CTA added up all ranges' counts took 25 us more).
 #include "mxfp4.cuh"
 
 #include <mutex>

@@ -22,6 +22,12 @@
 // 16 by 16, so that a warp has both of a row) by one row tile is an item;
 // items go round-robin over pairs, row tiles of an expert are of even size, N
 // is the row tile's count rounded up to 16.
+//
+// Bound by the tensor pipe where K is long: 4096 tokens of 6 of 64 experts, gate
+// and up of 1408 x 5120, 709 GFLOP in 423 us, 1.68 PFLOP/s.  Where K is short the results
+// take as long (down of 5120 x 1408: 11 steps an item, 372 us with the pass over h and the sum).  A
+// product of 16 values of K takes 75 clocks for any N up to 160, that of its 256 rows
+// of weights: 64 experts of 12 rows take 178 us for their 490 MB.
 #pragma once
 
 #include "mx_gemm.cuh"
@@ -41,11 +47,14 @@ static_assert(MXT_A_COL + MXT_A_STAGES * 64 <= 512, "tensor memory");
 constexpr long long MXT_WAIT_CLOCKS = 2000000000;  // about a second
 constexpr int MXT_SHIFT = 13;                      // the scales in A are 2^13 times what they are
 
-// Terms of a row of x; the ring for them: batches of steps, a step being half a
-// row tile of two units of 64 values.  A batch is announced and given back as
-// one.  AHEAD: steps of a converting warp's own ring of codes.
+// Items whose slots and powers of two are in shared memory: a warp that writes results may be
+// ahead of another by two (an accumulator that is free again takes all of them).
+constexpr int MXT_SETS = 3;
 constexpr int MXT_EPI_BYTES = 2 * 16 * 128 * 4;  // two halves of 16 columns of results
 
+// For rows of x of so many terms: the ring for them, batches of steps, a step
+// being half a row tile of two units of 64 values (a batch is announced and given
+// back as one), and the steps of a converting warp's own ring of codes.
 template <int TERMS>
 struct MxtShape {
     static constexpr int BATCH = TERMS == 1 ? 2 : 1, BATCHES = 3, AHEAD = 2;
@@ -55,7 +64,7 @@ struct MxtRows {
     const __half* x;  // row r of term i at x + i * plane + r * ld, 16-byte aligned
     int64_t ld, plane;
     int values;          // of a row that are there
-    const float* scale;  // null, or what a row's products are to be multiplied by
+    const float* scale;  // what a row's products are to be multiplied by (fp16 rows: null, by nothing)
     int drop;            // test only: the first CTA does not announce its first rows
 };
 
@@ -65,7 +74,7 @@ constexpr size_t mxt_smem(int experts)
     using S = MxtShape<TERMS>;
     return 1024 + (size_t)S::BATCHES * S::BATCH * 2 * TERMS * (MXT_ROWS / 2) * 128 +
            (size_t)MXT_CONVERT * S::AHEAD * 4 * MX_UNIT_BYTES + MXT_EPI_BYTES + (2 * S::BATCHES + 2 * MXT_A_STAGES + 5) * sizeof(uint64_t) +
-           8 + 2 * MXT_ROWS * (sizeof(int) + sizeof(float)) + (size_t)(2 * (experts + 1) + 32 + 4) * sizeof(int);
+           8 + MXT_SETS * MXT_ROWS * (sizeof(int) + sizeof(float)) + (size_t)(2 * (experts + 1) + 32 + 4) * sizeof(int);
 }
 
 // ---- tcgen05, clusters --------------------------------------------------------
@@ -340,8 +349,8 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
     uint64_t *empty_a = full_a + MXT_A_STAGES, *acc_full = empty_a + MXT_A_STAGES, *acc_empty = acc_full + 2;
     uint64_t* all_done = acc_empty + 2;
     int* epi_slots = reinterpret_cast<int*>(all_done + 1 + (reinterpret_cast<uintptr_t>(all_done + 1) & 8) / 8);
-    float* epi_scale = reinterpret_cast<float*>(epi_slots + 2 * MXT_ROWS);
-    int* before = reinterpret_cast<int*>(epi_scale + 2 * MXT_ROWS);
+    float* epi_scale = reinterpret_cast<float*>(epi_slots + MXT_SETS * MXT_ROWS);
+    int* before = reinterpret_cast<int*>(epi_scale + MXT_SETS * MXT_ROWS);
     int* start = before + a.L.experts + 1;
     int* sums = start + a.L.experts + 1;
     volatile int* gave_up = sums + 32;
@@ -377,7 +386,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
     cluster_barrier();  // both CTAs' barriers and tensor memory are there
     tc_fence_after();
     const uint32_t tmem = *tmem_at;
-    mx_rest<MODE>(a, static_cast<O*>(a.y), status);
+    mx_rest<MODE>(a, static_cast<O*>(a.y), start, status);
 
     constexpr int GROUP_TILES = MODE == MX_GATE_UP ? 8 : 16;  // of a pair
     const int units = a.L.units(), steps = (units + 1) / 2, tiles = a.L.tiles();
@@ -629,6 +638,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
         constexpr int WIDE = MODE == MX_GATE_UP ? 64 : 128;  // neighbouring outputs of a column
         constexpr int EACH = 16 / sizeof(O), LANES = WIDE / EACH, COLUMNS = 32 / LANES;  // a column's outputs by so many lanes
         constexpr int PER = (MXT_ROWS + 31) / 32;
+        constexpr bool SCALED = !std::is_same<T, __half>::value;
         const int quad = warp & 3, i = lane >> 4;
         const uint32_t from = tmem + ((uint32_t)(32 * quad) << 16);
         O* y = static_cast<O*>(a.y);
@@ -648,31 +658,37 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
         auto look_scales = [&]() {
 #pragma unroll
             for (int j = 0; j < PER; ++j)
-                next_scale[j] = next_slot[j] < 0 || !x.scale ? 1.0f : x.scale[next_slot[j] / a.x_div];
+                next_scale[j] = SCALED && next_slot[j] >= 0 ? x.scale[next_slot[j] / a.x_div] : 1.0f;
         };
         const bool wide = ((reinterpret_cast<uintptr_t>(y) | (uintptr_t)(a.ldy * (int64_t)sizeof(O))) & 15u) == 0;
         MxtStage<2> acc;
+        MxtStage<MXT_SETS> set;
         int half = 0;  // of the staging buffer
+        bool stopped = false;
         bool more = walk.find();
         if (more) {
             look(walk);
             look_scales();
         }
         while (more) {
-            int* slots = epi_slots + acc.i * MXT_ROWS;  // (the four warps write the same)
-            float* scales = epi_scale + acc.i * MXT_ROWS;
+            int* slots = epi_slots + set.i * MXT_ROWS;  // (the four warps write the same)
+            float* scales = epi_scale + set.i * MXT_ROWS;
 #pragma unroll
             for (int j = 0; j < PER; ++j)
                 if (lane + 32 * j < MXT_ROWS) {
                     slots[lane + 32 * j] = next_slot[j];
-                    scales[lane + 32 * j] = next_scale[j];
+                    if (SCALED) scales[lane + 32 * j] = next_scale[j];
                 }
             __syncwarp();
-            // the row's power of two, in two factors of which one nearly always does
+            // the weight's power of two, and whether its product with a row's is sure to be an
+            // fp32 number (nearly always), exact then
             const int e = next_e, p = e - 127 - MXT_SHIFT;
             const float f0 = e == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(max(p, -126) + 127) << 23);
-            const float f1 = __uint_as_float((uint32_t)(min(p + 126, 0) + 127) << 23);
-            const bool plain = __all_sync(~0u, p >= -126 || e == 255);
+            bool mild = e == 255 || (p >= (SCALED ? -63 : -126) && p <= (SCALED ? 63 : 127));
+            if constexpr (SCALED)
+#pragma unroll
+                for (int j = 0; j < PER; ++j) mild &= next_scale[j] >= 0x1p-63f && next_scale[j] <= 0x1p64f;
+            mild = __all_sync(~0u, mild);
             const int n0 = (walk.g * GROUP_TILES + (int)rank * (GROUP_TILES / 2)) * MX_TILE_N;
             const int outputs = max(0, min(WIDE, a.L.N - n0)), columns = walk.n;
             if (MODE == MX_DOWN && walk.g == 0 && rank == 0 && quad == 0)
@@ -681,75 +697,91 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
             MxtWalk after = walk;
             more = after.next();
             if (more) look(after);
-            if (!wait(acc_full + acc.i, acc.phase)) break;
-            tc_fence_after();
             const uint32_t d = from + acc.i * MXT_ROWS;
-            uint32_t v[16];
-            tc_ld_32x32b_x16(d, v);
+            auto results = [&](auto exact) {
+                uint32_t v[16];
+                tc_ld_32x32b_x16(d, v);
 #pragma unroll 1
-            for (int c0 = 0; c0 < columns; c0 += 16) {
-                tc_wait_ld();
-                float z[16];
+                for (int c0 = 0; c0 < columns; c0 += 16) {
+                    tc_wait_ld();
+                    float z[16];
+                    if (exact) {
 #pragma unroll
-                for (int c = 0; c < 16; c += 4) {
-                    const float4 f = *reinterpret_cast<const float4*>(scales + c0 + c);
-                    z[c] = __uint_as_float(v[c]) * f.x * f0;
-                    z[c + 1] = __uint_as_float(v[c + 1]) * f.y * f0;
-                    z[c + 2] = __uint_as_float(v[c + 2]) * f.z * f0;
-                    z[c + 3] = __uint_as_float(v[c + 3]) * f.w * f0;
-                }
-                if (c0 + 16 < columns) {
-                    tc_ld_32x32b_x16(d + c0 + 16, v);  // on its way meanwhile
-                } else {  // the accumulator is free again
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) arrive_first(acc_empty + acc.i);
-                }
-                if (c0 == 0 && more) look_scales();
-                if (!plain)
-#pragma unroll
-                    for (int c = 0; c < 16; ++c) z[c] *= f1;
-                if constexpr (MODE == MX_DOWN) {
-                    // rows of the partial results lie next to one another: straight from the registers
-                    O* at = y + (int64_t)(walk.s0 + c0) * a.ldy + n0 + in_column;
-                    if (in_column < outputs)
+                        for (int c = 0; c < 16; c += 4) {
+                            const float4 f = SCALED ? *reinterpret_cast<const float4*>(scales + c0 + c) : make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+                            z[c] = __uint_as_float(v[c]) * (f.x * f0);
+                            z[c + 1] = __uint_as_float(v[c + 1]) * (f.y * f0);
+                            z[c + 2] = __uint_as_float(v[c + 2]) * (f.z * f0);
+                            z[c + 3] = __uint_as_float(v[c + 3]) * (f.w * f0);
+                        }
+                    } else {  // two factors, of which the first takes what it can
 #pragma unroll
                         for (int c = 0; c < 16; ++c) {
-                            if (c0 + c < walk.cnt && QG_OK(qg_in(at - y, 1, (int64_t)a.slots * a.ldy), status, 333)) *at = z[c];
-                            at += a.ldy;
+                            const int q = p + (SCALED ? (int)(__float_as_uint(scales[c0 + c]) >> 23) - 127 : 0), q0 = max(-126, min(127, q));
+                            z[c] = __uint_as_float(v[c]) * __uint_as_float((uint32_t)(q0 + 127) << 23) * __uint_as_float((uint32_t)(q - q0 + 127) << 23);
+                            if (e == 255) z[c] = f0;
                         }
-                    continue;
-                }
-                O* to = stage + half * (16 * 128) + in_column;
-                if constexpr (MODE == MX_GATE_UP) {
-                    // a lane of the gate's rows and the one of the same row of up
-                    // have two columns: one each
-#pragma unroll
-                    for (int c = 0; c < 16; c += 2) {
-                        const float other = __shfl_xor_sync(~0u, i ? z[c] : z[c + 1], 16);
-                        to[(c + i) * WIDE] = from_f32<O>(mx_silu<T>(i ? other : z[c]) * (i ? z[c + 1] : other));
                     }
-                } else {
+                    if (c0 + 16 < columns) {
+                        tc_ld_32x32b_x16(d + c0 + 16, v);  // on its way meanwhile
+                    } else {  // the accumulator is free again
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) arrive_first(acc_empty + acc.i);
+                    }
+                    if (c0 == 0 && more) look_scales();
+                    if constexpr (MODE == MX_DOWN) {
+                        // rows of the partial results lie next to one another: straight from the registers
+                        O* at = y + (int64_t)(walk.s0 + c0) * a.ldy + n0 + in_column;
+                        if (in_column < outputs)
 #pragma unroll
-                    for (int c = 0; c < 16; ++c) to[c * WIDE] = from_f32<O>(z[c]);
-                }
-                asm volatile("bar.sync 1, %0;" ::"n"(MXT_EPI * 32) : "memory");  // (the next write to this half comes after the next one)
-                const O* have = stage + half * (16 * 128);
-#pragma unroll
-                for (int j = 0; j < 16; j += 4 * COLUMNS) {
-                    const int c = j + quad * COLUMNS + lane / LANES, r = lane % LANES * EACH;
-                    const int64_t s = slots[c0 + c];
-                    O* at = y + s * a.ldy + n0 + r;
-                    if (s < 0 || r >= outputs || !QG_OK(qg_in(s * a.ldy + n0 + r, min(EACH, outputs - r), (int64_t)a.slots * a.ldy), status, 332))
+                            for (int c = 0; c < 16; ++c) {
+                                if (c0 + c < walk.cnt && QG_OK(qg_in(at - y, 1, (int64_t)a.slots * a.ldy), status, 333)) *at = z[c];
+                                at += a.ldy;
+                            }
                         continue;
-                    if (wide && r + EACH <= outputs)
-                        *reinterpret_cast<uint4*>(at) = *reinterpret_cast<const uint4*>(have + c * WIDE + r);
-                    else
-                        for (int k = 0; k < EACH && r + k < outputs; ++k) at[k] = have[c * WIDE + r + k];
+                    }
+                    O* to = stage + half * (16 * 128) + in_column;
+                    if constexpr (MODE == MX_GATE_UP) {
+                        // a lane of the gate's rows and the one of the same row of up
+                        // have two columns: one each
+#pragma unroll
+                        for (int c = 0; c < 16; c += 2) {
+                            const float other = __shfl_xor_sync(~0u, i ? z[c] : z[c + 1], 16);
+                            to[(c + i) * WIDE] = from_f32<O>(mx_silu<T>(i ? other : z[c]) * (i ? z[c + 1] : other));
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) to[c * WIDE] = from_f32<O>(z[c]);
+                    }
+                    asm volatile("bar.sync 1, %0;" ::"n"(MXT_EPI * 32) : "memory");  // (the next write to this half comes after the next one)
+                    const O* have = stage + half * (16 * 128);
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4 * COLUMNS) {
+                        const int c = j + quad * COLUMNS + lane / LANES, r = lane % LANES * EACH;
+                        const int64_t s = slots[c0 + c];
+                        O* at = y + s * a.ldy + n0 + r;
+                        if (s < 0 || r >= outputs || !QG_OK(qg_in(s * a.ldy + n0 + r, min(EACH, outputs - r), (int64_t)a.slots * a.ldy), status, 332))
+                            continue;
+                        if (wide && r + EACH <= outputs)
+                            *reinterpret_cast<uint4*>(at) = *reinterpret_cast<const uint4*>(have + c * WIDE + r);
+                        else
+                            for (int k = 0; k < EACH && r + k < outputs; ++k) at[k] = have[c * WIDE + r + k];
+                    }
+                    half ^= 1;
                 }
-                half ^= 1;
+            };
+            if (!stopped) stopped = !wait(acc_full + acc.i, acc.phase);
+            if (!stopped) {
+                tc_fence_after();
+                if (MODE != MX_GEMM) results(mild);  // (as two loops, down takes 468 us for 404)
+                else if (mild) results(std::true_type{});
+                else results(std::false_type{});
+            } else if constexpr (MODE != MX_DOWN) {  // it still comes to the barriers that the four warps have together
+                for (int c0 = 0; c0 < columns; c0 += 16) asm volatile("bar.sync 1, %0;" ::"n"(MXT_EPI * 32) : "memory");
             }
             acc.next();
+            set.next();
             walk = after;
         }
     }

@@ -668,8 +668,8 @@ int moe_group(const int32_t* ids, int32_t* offsets, int32_t* order, void* worksp
  *             and out are written, and overlap nothing that is read): x has
  *             `tokens` rows of K values, h of moe_down tokens * top_k
  *   offsets, order  as moe_route writes them, read on the device; entries out
- *             of range are cut or skipped, nothing outside the arrays is
- *             touched.  order may be NULL where top_k is 1: slot i is then at
+ *             of range are cut or skipped, an offset below an earlier one
+ *             counts as that; nothing outside the arrays is touched.  order may be NULL where top_k is 1: slot i is then at
  *             place i, the rows are sorted already.
  *   weights   fp32 [tokens][top_k]
  *   workspace *_workspace_bytes() bytes, 16-byte aligned, with anything in it

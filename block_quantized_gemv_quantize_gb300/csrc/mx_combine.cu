@@ -85,9 +85,10 @@ int launch_mx_combine(int type, const float* parts, const int32_t* place_of, con
 }
 
 // From 8 rows an expert on (of those that can have any).  64 experts of 1408 x
-// 5120, gate and up, 8 rows each: 118 us by the mma.sync kernel, 175 by this one,
-// 12 rows: 200 and 176 (a second row tile reads the weights again); one of
-// 17408 x 5120, 8 rows: 25 and 28, 12 rows: 37 and 28.
+// 5120, gate and up, 8 rows each: 113 us by the mma.sync kernel, 125 by this one,
+// 12 rows: 183 and 126 (a second row tile reads the weights again); one of
+// 17408 x 5120, 4 rows: 18 and 18, 8 rows: 23 and 18, 9: 32 and 18; one of
+// 4096 x 4096, 8 rows: 13.5 and 15, 9: 16 and 15.
 bool mx_many_rows(int64_t slots, int experts, int K)
 {
     return slots > 8 * (slots < experts ? slots : (int64_t)experts) || K > 16384;

@@ -95,7 +95,7 @@ int launch_mxt(const MxArgs& a, cudaStream_t s)
     x.drop = take_drop_request();
     constexpr int GROUP = MODE == MX_GATE_UP ? 8 : 16;
     const int64_t groups = (a.L.tiles() + GROUP - 1) / GROUP;
-    const int64_t most = groups * std::min<int64_t>(a.slots, (int64_t)a.slots / MXT_ROWS + a.L.experts);
+    const int64_t most = groups * std::min<int64_t>(a.slots, (int64_t)a.slots / MXT_ROWS<TERMS> + a.L.experts);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2u * (unsigned)std::min<int64_t>(most, di.sms / 2));
     cfg.blockDim = dim3(MXT_THREADS);

@@ -1,7 +1,7 @@
 // Products of MXFP4 experts with many rows each (tcgen05 kernel).
 //
 // y[s][n] = sum_k w[n][k] x[s][k] with the weights as operand A (256 rows of
-// a tcgen05.mma over a pair of SMs, from tensor memory) and up to MXT_ROWS
+// a tcgen05.mma over a pair of SMs, from tensor memory) and up to 160
 // rows of x as operand B (half in each SM's shared memory).  Both are halves: a
 // code times its scale relative to the row's largest, times 2^13, is one
 // exactly (the pack has no scale below 2^-27); fp16 rows are what they are;
@@ -12,7 +12,7 @@
 // bound the kernel: 1240 clocks a step of 660.)  The codes go from the pack's words
 // to tensor memory as fragments (16x256b): that operand costs no
 // shared-memory bandwidth, and the pair halves what the other one costs.
-// Sums are the tensor core's, in fp32; the epilogue multiplies by the powers of two.
+// Sums are the tensor core's, in fp32 (of fp32 rows, those of 256 values each); the epilogue multiplies by the powers of two.
 //
 // In each CTA of a pair 12 warps convert weights (32 rows of tensor memory
 // each, every third step), 3 gather rows of x by asynchronous copies into
@@ -36,13 +36,22 @@ namespace qgemv {
 
 constexpr int MXT_CONVERT = 12, MXT_EPI = 4, MXT_EPI_WARP = 12, MXT_MMA_WARP = 16, MXT_LOAD_WARP = 17, MXT_LOAD = 3;
 constexpr int MXT_THREADS = (MXT_LOAD_WARP + MXT_LOAD) * 32;
-constexpr int MXT_ROWS = 160;    // of x an item: two accumulators of that many columns
+// Rows of x an item: two accumulators of that many columns, and for fp32 rows their sums.
+template <int TERMS>
+constexpr int MXT_ROWS = TERMS == 1 ? 160 : 96;
+// Steps of fp32 rows that an accumulator takes.  The tensor core cuts what does not fit its sum's 24
+// bits, always towards zero: 5120 values in one accumulator come out 8e-6 too small, where 16-bit outputs
+// have steps of 5e-4 and more.  Of fp32 rows every two steps (256 values) are added up by the
+// results' warps, rounding to nearest, in tensor memory: 3e-7 off, and 64 experts of 768 x 2048,
+// gate and up, 16 rows each, take 53 us for 50, 32 rows 60 for 53.
+constexpr int MXT_CHUNK = 2;
 constexpr int MXT_A_STAGES = 3;  // of two units, 64 columns each: what hides a round trip between the roles
 static_assert(MXT_CONVERT == 4 * MXT_A_STAGES, "a warpgroup a stage");
 // Registers a thread: 640 of 96 at launch, of which the results' warpgroup gets 24 each of the last one's.
 constexpr int MXT_REGS = 96, MXT_EPI_REGS = 120, MXT_REST_REGS = 72;
 static_assert(MXT_THREADS == 640 && MXT_CONVERT * MXT_REGS + MXT_EPI * MXT_EPI_REGS + 4 * MXT_REST_REGS == 20 * MXT_REGS, "register shares");
-constexpr uint32_t MXT_A_COL = 2 * MXT_ROWS;
+constexpr uint32_t MXT_A_COL = 320;
+static_assert(2 * MXT_ROWS<1> <= MXT_A_COL && 3 * MXT_ROWS<2> <= MXT_A_COL, "accumulators");
 static_assert(MXT_A_COL + MXT_A_STAGES * 64 <= 512, "tensor memory");
 constexpr long long MXT_WAIT_CLOCKS = 2000000000;  // about a second
 constexpr int MXT_SHIFT = 13;                      // the scales in A are 2^13 times what they are
@@ -72,9 +81,9 @@ template <int TERMS>
 constexpr size_t mxt_smem(int experts)
 {
     using S = MxtShape<TERMS>;
-    return 1024 + (size_t)S::BATCHES * S::BATCH * 2 * TERMS * (MXT_ROWS / 2) * 128 +
+    return 1024 + (size_t)S::BATCHES * S::BATCH * 2 * TERMS * (MXT_ROWS<TERMS> / 2) * 128 +
            (size_t)MXT_CONVERT * S::AHEAD * 4 * MX_UNIT_BYTES + MXT_EPI_BYTES + (2 * S::BATCHES + 2 * MXT_A_STAGES + 5) * sizeof(uint64_t) +
-           8 + MXT_SETS * MXT_ROWS * (sizeof(int) + sizeof(float)) + (size_t)(2 * (experts + 1) + 32 + 4) * sizeof(int);
+           8 + MXT_SETS * MXT_ROWS<TERMS> * (sizeof(int) + sizeof(float)) + (size_t)(2 * (experts + 1) + 32 + 4) * sizeof(int);
 }
 
 // ---- tcgen05, clusters --------------------------------------------------------
@@ -130,6 +139,19 @@ __device__ __forceinline__ void tc_ld_32x32b_x16(uint32_t at, uint32_t (&r)[16])
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(at)
         : "memory");
+}
+__device__ __forceinline__ void tc_st_32x32b_x16(uint32_t at, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void add_sums(uint32_t (&v)[16], const uint32_t (&s)[16])
+{
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(s[i]));
 }
 __device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
@@ -285,6 +307,7 @@ __global__ void __launch_bounds__(MXT_ROW_THREADS, 8) mxt_rows_kernel(const T* x
 // ---- the kernel -------------------------------------------------------------------
 
 // An item: a row tile and a group of weight tiles.  Every role walks the same ones.
+template <int ROWS>
 struct MxtWalk {
     const int *before, *start;
     int groups;
@@ -299,7 +322,7 @@ struct MxtWalk {
         while (rt >= before[e + 1]) ++e;
         const int first = start[e], all = start[e + 1] - first;
         const int tiles = before[e + 1] - before[e];
-        const int each = min(MXT_ROWS, ((all + tiles - 1) / tiles + 15) & ~15);
+        const int each = min(ROWS, ((all + tiles - 1) / tiles + 15) & ~15);
         s0 = first + (rt - before[e]) * each;
         cnt = min(each, first + all - s0);
         n = (cnt + 15) & ~15;
@@ -340,7 +363,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
     using S = MxtShape<TERMS>;
     using O = typename std::conditional<MODE == MX_DOWN, float, T>::type;
     constexpr int BATCH = S::BATCH, BATCHES = S::BATCHES;
-    constexpr int TERM_BYTES = MXT_ROWS / 2 * 128, UNIT_BYTES = TERMS * TERM_BYTES, STEP_BYTES = 2 * UNIT_BYTES;
+    constexpr int ROWS = MXT_ROWS<TERMS>, TERM_BYTES = ROWS / 2 * 128, UNIT_BYTES = TERMS * TERM_BYTES, STEP_BYTES = 2 * UNIT_BYTES;
     extern __shared__ uint8_t sm_raw[];
     uint8_t* sm = sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u);
     uint64_t* full_b = reinterpret_cast<uint64_t*>(sm + BATCHES * BATCH * STEP_BYTES + MXT_CONVERT * S::AHEAD * 4 * MX_UNIT_BYTES + MXT_EPI_BYTES);
@@ -349,8 +372,8 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
     uint64_t *empty_a = full_a + MXT_A_STAGES, *acc_full = empty_a + MXT_A_STAGES, *acc_empty = acc_full + 2;
     uint64_t* all_done = acc_empty + 2;
     int* epi_slots = reinterpret_cast<int*>(all_done + 1 + (reinterpret_cast<uintptr_t>(all_done + 1) & 8) / 8);
-    float* epi_scale = reinterpret_cast<float*>(epi_slots + MXT_SETS * MXT_ROWS);
-    int* before = reinterpret_cast<int*>(epi_scale + MXT_SETS * MXT_ROWS);
+    float* epi_scale = reinterpret_cast<float*>(epi_slots + MXT_SETS * ROWS);
+    int* before = reinterpret_cast<int*>(epi_scale + MXT_SETS * ROWS);
     int* start = before + a.L.experts + 1;
     int* sums = start + a.L.experts + 1;
     volatile int* gave_up = sums + 32;
@@ -382,7 +405,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
         tc_fence_before();
     }
     pdl_wait();
-    const int n_rt = mx_row_tiles<MXT_THREADS>(a, MXT_ROWS, before, start, sums);
+    const int n_rt = mx_row_tiles<MXT_THREADS>(a, ROWS, before, start, sums);
     cluster_barrier();  // both CTAs' barriers and tensor memory are there
     tc_fence_after();
     const uint32_t tmem = *tmem_at;
@@ -390,7 +413,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
 
     constexpr int GROUP_TILES = MODE == MX_GATE_UP ? 8 : 16;  // of a pair
     const int units = a.L.units(), steps = (units + 1) / 2, tiles = a.L.tiles();
-    MxtWalk walk;
+    MxtWalk<ROWS> walk;
     walk.before = before;
     walk.start = start;
     walk.groups = (tiles + GROUP_TILES - 1) / GROUP_TILES;
@@ -527,7 +550,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
         cp_async_wait<0>();
     } else if (warp >= MXT_LOAD_WARP) {
         // ---- rows of x into shared memory: this CTA's half of a row tile, a 16-byte piece of every 16th row a thread
-        constexpr int STEP = MXT_LOAD * 4, EACH = (MXT_ROWS / 2 + STEP - 1) / STEP, LAG = BATCHES - 2;
+        constexpr int STEP = MXT_LOAD * 4, EACH = (ROWS / 2 + STEP - 1) / STEP, LAG = BATCHES - 2;
         const int id = threadIdx.x - MXT_LOAD_WARP * 32, c = id & 7, r0 = id >> 3;
         static_assert(STEP % 8 == 4, "every other row: the swizzle's other half");
         const uint32_t at[2] = {smem_u32(sm) + r0 * 128 + ((c ^ (r0 & 7)) << 4), smem_u32(sm) + r0 * 128 + ((c ^ (r0 & 7) ^ 4) << 4)};
@@ -599,27 +622,34 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
             int in = 0;
             bool ok = true;
             for (bool more = walk.find(); more && ok; more = walk.next()) {
-                const uint32_t idesc = tc_idesc(__shfl_sync(~0u, walk.n, 0)), d = tmem + acc.i * MXT_ROWS;
-                ok = wait(acc_empty + acc.i, acc.phase ^ 1);
-                uint32_t add = 0;
+                const uint32_t idesc = tc_idesc(__shfl_sync(~0u, walk.n, 0));
+                uint32_t d = tmem + acc.i * ROWS, add = 0;
+                if constexpr (TERMS == 1) ok = wait(acc_empty + acc.i, acc.phase ^ 1);
                 for (int u = 0; u < units && ok; u += 2) {
+                    if constexpr (TERMS == 2)
+                        if (u % (2 * MXT_CHUNK) == 0) {
+                            d = tmem + acc.i * ROWS;
+                            add = 0;
+                            ok = wait(acc_empty + acc.i, acc.phase ^ 1);
+                            if (!ok) break;
+                        }
                     ok = wait_at(full + 8 * sa.i, sa.phase);  // of both CTAs, and their rows of x
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t b = b0 + (uint64_t)((sb.i * BATCH + in) * (STEP_BYTES / 16));
                     const uint32_t at = tmem + MXT_A_COL + sa.i * 64;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (h == 0 || u + 1 < units) {
+                    for (int i = TERMS - 1; i >= 0; --i)  // (the small terms first, while the sum cuts little of them)
 #pragma unroll
-                            for (int i = 0; i < TERMS; ++i)
+                        for (int h = 0; h < 2; ++h)
+                            if (h == 0 || u + 1 < units) {
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
                                     tc_mma_f16(d, at + h * 32 + k * 8, b + (uint64_t)(h * (UNIT_BYTES / 16) + i * (TERM_BYTES / 16) + k * 2),
                                                idesc, add, on);
                                     add = 1;
                                 }
-                        }
+                            }
                     tc_commit_both(empty + 8 * sa.i, on);
                     if (++in == BATCH) {
                         in = 0;
@@ -627,9 +657,16 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
                         sb.next();
                     }
                     sa.next();
+                    if constexpr (TERMS == 2)
+                        if ((u + 2) % (2 * MXT_CHUNK) == 0 || u + 2 >= units) {
+                            tc_commit_both(done + 8 * acc.i, on);
+                            acc.next();
+                        }
                 }
-                if (ok) tc_commit_both(done + 8 * acc.i, on);
-                acc.next();
+                if constexpr (TERMS == 1) {
+                    if (ok) tc_commit_both(done + 8 * acc.i, on);
+                    acc.next();
+                }
             }
         }
     } else {
@@ -637,7 +674,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
         // stores 16 bytes of a column
         constexpr int WIDE = MODE == MX_GATE_UP ? 64 : 128;  // neighbouring outputs of a column
         constexpr int EACH = 16 / sizeof(O), LANES = WIDE / EACH, COLUMNS = 32 / LANES;  // a column's outputs by so many lanes
-        constexpr int PER = (MXT_ROWS + 31) / 32;
+        constexpr int PER = (ROWS + 31) / 32;
         constexpr bool SCALED = !std::is_same<T, __half>::value;
         const int quad = warp & 3, i = lane >> 4;
         const uint32_t from = tmem + ((uint32_t)(32 * quad) << 16);
@@ -648,7 +685,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
         // An item's slots, their powers of two and this lane's row's, read ahead.
         int next_slot[PER], next_e;
         float next_scale[PER];
-        auto look = [&](const MxtWalk& w) {
+        auto look = [&](const MxtWalk<ROWS>& w) {
 #pragma unroll
             for (int j = 0; j < PER; ++j) next_slot[j] = lane + 32 * j < w.cnt ? mxt_slot(a, w.s0 + lane + 32 * j) : -1;
             const int tile = w.g * GROUP_TILES + (int)rank * (GROUP_TILES / 2) + (MODE == MX_GATE_UP ? quad : 2 * quad + i);
@@ -671,11 +708,11 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
             look_scales();
         }
         while (more) {
-            int* slots = epi_slots + set.i * MXT_ROWS;  // (the four warps write the same)
-            float* scales = epi_scale + set.i * MXT_ROWS;
+            int* slots = epi_slots + set.i * ROWS;  // (the four warps write the same)
+            float* scales = epi_scale + set.i * ROWS;
 #pragma unroll
             for (int j = 0; j < PER; ++j)
-                if (lane + 32 * j < MXT_ROWS) {
+                if (lane + 32 * j < ROWS) {
                     slots[lane + 32 * j] = next_slot[j];
                     if (SCALED) scales[lane + 32 * j] = next_scale[j];
                 }
@@ -694,16 +731,45 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
             if (MODE == MX_DOWN && walk.g == 0 && rank == 0 && quad == 0)
                 for (int r = lane; r < walk.cnt; r += 32)
                     if (slots[r] >= 0) a.place_of[slots[r]] = walk.s0 + r;
-            MxtWalk after = walk;
+            MxtWalk<ROWS> after = walk;
             more = after.next();
             if (more) look(after);
-            const uint32_t d = from + acc.i * MXT_ROWS;
+            const uint32_t sums_at = from + 2 * ROWS;
+            const bool summed = TERMS == 2 && units > 2 * MXT_CHUNK;
+            if constexpr (TERMS == 2)
+#pragma unroll 1
+                for (int u = 2 * MXT_CHUNK; u < units && !stopped; u += 2 * MXT_CHUNK) {  // all accumulators of the item but the last
+                    stopped = !wait(acc_full + acc.i, acc.phase);
+                    if (stopped) break;
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int c0 = 0; c0 < columns; c0 += 16) {
+                        uint32_t v[16], s[16];
+                        tc_ld_32x32b_x16(from + acc.i * ROWS + c0, v);
+                        if (u > 2 * MXT_CHUNK) {
+                            tc_ld_32x32b_x16(sums_at + c0, s);
+                            tc_wait_ld();
+                            add_sums(v, s);
+                        } else {
+                            tc_wait_ld();
+                        }
+                        tc_st_32x32b_x16(sums_at + c0, v);
+                    }
+                    tc_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) arrive_first(acc_empty + acc.i);
+                    acc.next();
+                }
+            const uint32_t d = from + acc.i * ROWS;
             auto results = [&](auto exact) {
-                uint32_t v[16];
+                uint32_t v[16], s[16];
                 tc_ld_32x32b_x16(d, v);
+                if (summed) tc_ld_32x32b_x16(sums_at, s);
 #pragma unroll 1
                 for (int c0 = 0; c0 < columns; c0 += 16) {
                     tc_wait_ld();
+                    if (summed) add_sums(v, s);
                     float z[16];
                     if (exact) {
 #pragma unroll
@@ -724,6 +790,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
                     }
                     if (c0 + 16 < columns) {
                         tc_ld_32x32b_x16(d + c0 + 16, v);  // on its way meanwhile
+                        if (summed) tc_ld_32x32b_x16(sums_at + c0 + 16, s);
                     } else {  // the accumulator is free again
                         tc_fence_before();
                         __syncwarp();

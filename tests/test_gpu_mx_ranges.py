@@ -253,3 +253,18 @@ def test_powers_of_rows_and_weights_far_apart(ops, kind, lo, tokens):  # noqa: F
     got = ops.qgemm_mxfp4(c.packs[0], x, c.offsets, c.N, order=c.order)
     bound = torch.where(y.isinf(), 0.0, R.rounded(y, bound, c.dtype))
     R.close(got, y, bound)
+
+
+@pytest.mark.parametrize("tokens,K", [(90, 256), (90, 320), (90, 5120), (200, 16384), (2, 32768)])
+def test_sums_of_fp32_rows_of_one_sign(ops, tokens, K):  # noqa: F811
+    """Sums that only grow lose the most to an accumulator that cuts: one of 256 values has 32
+    products (two terms of x), each cut by 2^-23 at most; then a rounding for each of them, x's
+    own (2^-23) and the output's."""
+    N = 40
+    blocks = R.random_blocks(gen(K), N, K)
+    blocks[..., 1:] &= 0x77
+    x = torch.rand((tokens, K), generator=gen(tokens)).cuda()
+    pack = ops.qpack_mxfp4(blocks.cuda(), 1, N, K)
+    want = x.double() @ R.values(blocks.cuda()).T
+    got = ops.qgemm_mxfp4(pack, x, torch.tensor([0, tokens], dtype=torch.int32, device="cuda"), N)
+    R.close(got, want, want * (33 * 2.0 ** -23 + (K / 256 + 1) * 2.0 ** -24))

@@ -21,7 +21,7 @@
 // of the first CTA issues the products for both.  256 rows of weights (128 of gate and of up,
 // 16 by 16, so that a warp has both of a row) by one row tile is an item;
 // items go round-robin over pairs, row tiles of an expert are of even size, N
-// is the row tile's count rounded up to 16.
+// is the row tile's count rounded up to 32.
 //
 // Bound by the tensor pipe where K is long: 4096 tokens of 6 of 64 experts, gate
 // and up of 1408 x 5120, 709 GFLOP in 423 us, 1.68 PFLOP/s.  Where K is short the results
@@ -31,6 +31,7 @@
 #pragma once
 
 #include "mx_gemm.cuh"
+#include "mx_row_tile.cuh"
 
 namespace qgemv {
 
@@ -45,6 +46,7 @@ constexpr int MXT_ROWS = TERMS == 1 ? 160 : 96;
 // results' warps, rounding to nearest, in tensor memory: 3e-7 off, and 64 experts of 768 x 2048,
 // gate and up, 16 rows each, take 53 us for 50, 32 rows 60 for 53.
 constexpr int MXT_CHUNK = 2;
+static_assert(MXT_ROWS<1> % MXT_N_STEP == 0 && MXT_ROWS<2> % MXT_N_STEP == 0, "whole products");
 constexpr int MXT_A_STAGES = 3;  // of two units, 64 columns each: what hides a round trip between the roles
 static_assert(MXT_CONVERT == 4 * MXT_A_STAGES, "a warpgroup a stage");
 // Registers a thread: 640 of 96 at launch, of which the results' warpgroup gets 24 each of the last one's.
@@ -163,7 +165,7 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t smem)
            (uint64_t)2 << 61;
 }
 
-// D fp32, A and B fp16, both K-major, 256 x n.
+// D fp32, A and B fp16, both K-major, 256 x n (n in steps of MXT_N_STEP).
 __device__ __forceinline__ uint32_t tc_idesc(int n) { return 1u << 4 | (uint32_t)(n >> 3) << 17 | 16u << 24; }
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -313,7 +315,7 @@ struct MxtWalk {
     int groups;
     int64_t item, items;
     int step;
-    int e, g, s0, cnt, n;  // expert, group, first place, rows, rows rounded up to 16
+    int e, g, s0, cnt, n;  // expert, group, first place, rows, the product's N
     __device__ bool find()
     {
         if (item >= items) return false;
@@ -322,10 +324,10 @@ struct MxtWalk {
         while (rt >= before[e + 1]) ++e;
         const int first = start[e], all = start[e + 1] - first;
         const int tiles = before[e + 1] - before[e];
-        const int each = min(ROWS, ((all + tiles - 1) / tiles + 15) & ~15);
-        s0 = first + (rt - before[e]) * each;
-        cnt = min(each, first + all - s0);
-        n = (cnt + 15) & ~15;
+        const MxRowTile t = mxt_row_tile(all, tiles, rt - before[e], ROWS);
+        s0 = first + t.first;
+        cnt = t.cnt;
+        n = t.n;
         return true;
     }
     __device__ bool next()
@@ -727,7 +729,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
                 for (int j = 0; j < PER; ++j) mild &= next_scale[j] >= 0x1p-63f && next_scale[j] <= 0x1p64f;
             mild = __all_sync(~0u, mild);
             const int n0 = (walk.g * GROUP_TILES + (int)rank * (GROUP_TILES / 2)) * MX_TILE_N;
-            const int outputs = max(0, min(WIDE, a.L.N - n0)), columns = walk.n;
+            const int outputs = max(0, min(WIDE, a.L.N - n0)), columns = (walk.cnt + 15) & ~15;
             if (MODE == MX_DOWN && walk.g == 0 && rank == 0 && quad == 0)
                 for (int r = lane; r < walk.cnt; r += 32)
                     if (slots[r] >= 0) a.place_of[slots[r]] = walk.s0 + r;

@@ -7,7 +7,7 @@
 // multiply-add an output and block, exact but for the sum's own rounding.
 // x as halves: fp16 rows are what they are; bf16 rows go by a power of two
 // that brings the row's largest finite element to [2^14, 2^15), which keeps
-// every element to 2^-40 of it (all eight bits of those within 2^-31); fp32
+// every element to 2^-39 of it (all eight bits of those within 2^-31); fp32
 // rows are two such terms (22 bits and a sign) of elements within 2^-15.
 //
 // Bound by the weights' bytes: 17/32 of a byte a value, read once if an
@@ -188,17 +188,30 @@ __device__ __forceinline__ uint32_t mx_halves(__half a, __half b)
 }
 
 // The power of two that a row goes by, from its largest finite magnitude's bits:
-// 2^-e brings it to [2^14, 2^15).  (A row of subnormal numbers goes by 2^112,
-// and keeps what it has to 2^-39 of 2^-126.)
-__device__ __forceinline__ int mx_row_exponent(uint32_t top) { return top ? max(-112, (int)(top >> 23) - 141) : 0; }
+// 2^-e brings it to [2^14, 2^15), a subnormal one too (e: -163 .. 113).
+__device__ __forceinline__ int mx_row_exponent(uint32_t top)
+{
+    return top == 0 ? 0 : top < 0x00800000u ? -132 - __clz((int)top) : (int)(top >> 23) - 141;
+}
 
-// Eight values times f = 2^-e as halves, and of fp32 values what that leaves.
+// 2^-e as two factors: fp32 numbers end at 2^127.
+struct MxRowFactor {
+    float a, b;
+    __device__ explicit MxRowFactor(int e)
+    {
+        const int p = min(127, -e);
+        a = __uint_as_float((uint32_t)(p + 127) << 23);
+        b = __uint_as_float((uint32_t)(-e - p + 127) << 23);
+    }
+};
+
+// Eight values times 2^-e as halves, and of fp32 values what that leaves.
 template <typename T>
-__device__ __forceinline__ void mx_row_halves(const float (&v)[8], float f, __half (&h)[8], __half (&l)[8])
+__device__ __forceinline__ void mx_row_halves(const float (&v)[8], const MxRowFactor& f, __half (&h)[8], __half (&l)[8])
 {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const float y = v[j] * f;
+        const float y = v[j] * f.a * f.b;
         h[j] = __float2half_rn(y);
         if constexpr (MX_TERMS<T> == 2) l[j] = isfinite(y) ? __float2half_rn(y - __half2float(h[j])) : __float2half_rn(0.0f);
     }
@@ -242,9 +255,8 @@ __device__ void mxs_stage(const MxArgs& a, const MxsPlan& p, uint8_t* xs, const 
         float v[8];
         mx_load8(x + (int64_t)(s / a.x_div) * a.ldx + k, wide, max(0, K - k), v);
         uint8_t* to = xs + (size_t)row * TERMS * p.x_bytes;
-        const float f = SCALED ? __uint_as_float((uint32_t)(127 - x_exp[row]) << 23) : 1.0f;
         __half h[8], l[8];
-        mx_row_halves<T>(v, f, h, l);
+        mx_row_halves<T>(v, MxRowFactor(SCALED ? x_exp[row] : 0), h, l);
         if (QG_OK(qg_in(k * 2, 16, p.x_bytes - 64) && row < p.rows, status, 313)) {
             const int q = (k >> 3) & 3;
             uint8_t* o = to + (k & ~31) * 2 + (q & 1) * 32 + (q >> 1) * 8;

@@ -6,7 +6,7 @@
 // code times its scale relative to the row's largest, times 2^13, is one
 // exactly (the pack has no scale below 2^-27); fp16 rows are what they are;
 // bf16 rows go by a power of two that brings the row's largest finite element
-// to [2^14, 2^15), which keeps every element to 2^-40 of it (all eight bits of
+// to [2^14, 2^15), which keeps every element to 2^-39 of it (all eight bits of
 // those within 2^-31), fp32 rows as two such terms, in a pass of its own.  (As
 // bf16 numbers the weights take 19 instructions a word instead of 8, and
 // bound the kernel: 1240 clocks a step of 660.)  The codes go from the pack's words
@@ -75,7 +75,7 @@ struct MxtRows {
     const __half* x;  // row r of term i at x + i * plane + r * ld, 16-byte aligned
     int64_t ld, plane;
     int values;          // of a row that are there
-    const float* scale;  // what a row's products are to be multiplied by (fp16 rows: null, by nothing)
+    const float* scale;  // what a row's products are to be multiplied by, as mxt_power has it (fp16 rows: null, by nothing)
     int drop;            // test only: the first CTA does not announce its first rows
 };
 
@@ -209,6 +209,14 @@ __device__ __forceinline__ void e2m1_scaled(uint32_t w, uint32_t scale, uint32_t
 
 // ---- rows of x as halves ------------------------------------------------------------
 
+// A row's power of two as the products read it: the number 2^e, or e itself (below
+// zero) where that is none of fp32's normal ones.
+__device__ __forceinline__ float mxt_power(int e) { return e < -126 ? (float)e : __uint_as_float((uint32_t)(e + 127) << 23); }
+__device__ __forceinline__ int mxt_exponent(float power)
+{
+    return power < 0.0f ? (int)power : (int)(__float_as_uint(power) >> 23) - 127;
+}
+
 // x [rows][K] -> planes [term][rows][padded], zeros behind a row, and each
 // row's power of two.  WARPS warps a row, eight values a lane at a time, the first
 // 2048 WARPS (fp32: 1024) of a row kept in registers between its maximum and its conversion (a longer
@@ -278,8 +286,8 @@ __global__ void __launch_bounds__(MXT_ROW_THREADS, 8) mxt_rows_kernel(const T* x
             }
         }
         const int e = SCALED ? mx_row_exponent(top) : 0;
-        if (SCALED && there && k0 == 0) scale[row] = __uint_as_float((uint32_t)(127 + e) << 23);
-        const float f = __uint_as_float((uint32_t)(127 - e) << 23);
+        if (SCALED && there && k0 == 0) scale[row] = mxt_power(e);
+        const MxRowFactor f(e);
         auto put = [&](int k, const float (&z)[8]) {
             __half h[8], l[8];
             mx_row_halves<T>(z, f, h, l);
@@ -782,13 +790,10 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
                             z[c + 2] = __uint_as_float(v[c + 2]) * (f.z * f0);
                             z[c + 3] = __uint_as_float(v[c + 3]) * (f.w * f0);
                         }
-                    } else {  // two factors, of which the first takes what it can
+                    } else {
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) {
-                            const int q = p + (SCALED ? (int)(__float_as_uint(scales[c0 + c]) >> 23) - 127 : 0), q0 = max(-126, min(127, q));
-                            z[c] = __uint_as_float(v[c]) * __uint_as_float((uint32_t)(q0 + 127) << 23) * __uint_as_float((uint32_t)(q - q0 + 127) << 23);
-                            if (e == 255) z[c] = f0;
-                        }
+                        for (int c = 0; c < 16; ++c)
+                            z[c] = e == 255 ? f0 : mul_pow2(__uint_as_float(v[c]), p + (SCALED ? mxt_exponent(scales[c0 + c]) : 0));
                     }
                     if (c0 + 16 < columns) {
                         tc_ld_32x32b_x16(d + c0 + 16, v);  // on its way meanwhile

@@ -47,16 +47,14 @@ __device__ __forceinline__ float mx_scale(int e)
     return __uint_as_float(e == 0 ? 0x00400000u : (e == 255 ? 0x7FC00000u : (uint32_t)e << 23));
 }
 
-// v * 2^p in one rounding (p: -380 .. 380): two factors that are fp32 numbers.
-// A product that leaves the range does so as the exact one would.
+// v * 2^p in one rounding (p: -378 .. 380): factors that are fp32 numbers, the least of
+// them first.  Where the product is 2^-150 or more, all before the last are exact;
+// one that leaves the range does so as the exact one would.
 __device__ __forceinline__ float mul_pow2(float v, int p)
 {
-    // (the second factor takes what the first leaves, so that only one of the
-    // two products rounds: the first is exact where the second shrinks)
     const int a = max(-126, min(127, p)), r = p - a, b = max(-126, min(127, r)), c = r - b;
-    float y = v * __uint_as_float((uint32_t)(a + 127) << 23) * __uint_as_float((uint32_t)(b + 127) << 23);
-    if (c) y *= __uint_as_float((uint32_t)(max(-126, min(127, c)) + 127) << 23);
-    return y;
+    if (c) v *= __uint_as_float((uint32_t)(c + 127) << 23);
+    return v * __uint_as_float((uint32_t)(b + 127) << 23) * __uint_as_float((uint32_t)(a + 127) << 23);
 }
 
 // ---- rows of values -------------------------------------------------------------

@@ -72,3 +72,23 @@ def test_rows_of_the_smallest_numbers(ops, kind, tokens):  # noqa: F811
     pack = ops.qpack_mxfp4(blocks.cuda(), 1, 16, 32)
     got = ops.qgemm_mxfp4(pack, x.to(dtype).cuda(), torch.tensor([0, tokens], dtype=torch.int32, device="cuda"), 16)
     assert torch.equal(got.cpu().double(), x @ R.values(blocks).T)
+
+
+@pytest.mark.parametrize("tokens", [6, 96])
+@pytest.mark.parametrize("shift", [-103, -106, -107, -109, -112, -118])
+def test_subnormal_outputs_round_once(ops, tokens, shift):  # noqa: F811
+    """Outputs between 2^-122 and 2^-139, each one product of an element that two halves hold
+    exactly (23 bits): the fp32 number nearest to it, of two the even one."""
+    K = 64
+    blocks = torch.zeros((K, 2, 17), dtype=torch.uint8)
+    n = torch.arange(1, K)
+    blocks[n, n // 32, 0] = 127 + shift
+    blocks[n, n // 32, 1 + n % 16] = torch.where(n % 32 < 16, 2, 2 << 4).to(torch.uint8)  # code 1
+    pack = ops.qpack_mxfp4(blocks.cuda(), 1, K, K)
+    x = torch.randint(1 << 22, 1 << 23, (tokens, K), generator=gen(5)).double() * 2.0 ** -42  # [2^-20, 2^-19)
+    x[:, 0] = 2.0 ** -4  # the row's largest, which no weight meets
+    x[:, 1::3] *= -1
+    got = ops.qgemm_mxfp4(pack, x.float().cuda(), torch.tensor([0, tokens], dtype=torch.int32, device="cuda"), K)
+    want = x * 2.0 ** shift
+    want[:, 0] = 0.0
+    assert torch.equal(got.cpu(), want.float())

@@ -923,7 +923,8 @@ def qgemm_mxfp4(w_pack: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor, N:
     """y [tokens * top_k, N]: each slot's row of x [tokens, K] times its expert's
     MXFP4 weight (a pack of experts weights of N rows).  Slots order[offsets[e]]
     .. order[offsets[e + 1] - 1] are expert e's; without order (top_k 1) the
-    rows are sorted by expert already.  A slot without an expert gets zeros."""
+    rows are sorted by expert already.  A slot without an expert gets zeros;
+    one that order does not name at all leaves its row as it was."""
     return _product("qgemm_mxfp4", (w_pack,), x, offsets, order, None, x.shape[0], top_k, x.shape[0] * top_k, N, y, ws)
 
 

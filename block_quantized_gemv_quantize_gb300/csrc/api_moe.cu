@@ -115,7 +115,8 @@ int product_call(int mode, int type, const void* w, const void* w2, const void* 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     st = launch_mx_gemm(mode, type, a, s);
     if (st || mode != MX_DOWN) return st;
-    return launch_mx_combine(type, static_cast<const float*>(workspace), a.place_of, weights, y, ldy, tokens, top_k, N, s);
+    return launch_mx_combine(type, static_cast<const float*>(workspace), a.place_of, order, weights, y, ldy, tokens, top_k,
+                             N, s);
 }
 
 }  // namespace

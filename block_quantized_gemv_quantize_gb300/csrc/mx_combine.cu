@@ -1,5 +1,7 @@
 // The last step of the down product: out[t] = sum_j weight[t][j] part[place of
-// slot t k + j], in the order of j, in fp32.  Reads the partial results once; bound by
+// slot t k + j], in the order of j, in fp32.  A slot's place is written where the order names
+// the slot; of one that it does not name the workspace holds anything, so a place counts
+// only if the order has the slot there.  Reads the partial results once; bound by
 // them (HBM, or L2 where they are few): 4096 tokens x 6 x 5120, 503 MB, 80 us.
 #include "mxfp4.cuh"
 
@@ -8,10 +10,12 @@ namespace {
 
 constexpr int THREADS = 256;
 
-// Four outputs of one token a thread.
-template <typename T>
+// Four outputs of one token a thread, TERMS of the sum in flight.  (Eight where a thread has one
+// quad: 96 tokens x 8 x 2048, product and sum, 43.3 us by eight and 44.6 by two; two beyond: 4096
+// tokens x 6 x 5120 384 us and 452 by eight, whose registers leave fewer threads.)
+template <typename T, int TERMS>
 __global__ void __launch_bounds__(THREADS) combine_kernel(const float* parts, const int32_t* place_of,
-                                                          const float* weights, T* out, int64_t ldo, int tokens,
+                                                          const int32_t* order, const float* weights, T* out, int64_t ldo, int tokens,
                                                           int top_k, int N, int quads, bool wide, unsigned int* status)
 {
     pdl_launch_dependents();
@@ -24,23 +28,25 @@ __global__ void __launch_bounds__(THREADS) combine_kernel(const float* parts, co
         const int32_t* places = place_of + (int64_t)t * top_k;
         float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (!QG_OK(qg_in(t * ldo + n, 1, tokens * ldo), status, 320)) continue;
-#pragma unroll 4
+#pragma unroll TERMS
         for (int j = 0; j < top_k; ++j) {
-            const int at = places[j];
-            if (at < 0 || at >= slots) continue;  // (a slot without an expert)
+            const int s = t * top_k + j, place = places[j];
+            const int at = place < 0 || place >= slots ? 0 : place;  // (loads that wait for no other: place 0 is there)
+            const int named = order ? order[at] : at;
             const float f = w[j];
             const float* p = parts + (int64_t)at * N + n;
+            float q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             if (N % 4 == 0) {
-                const float4 q = *reinterpret_cast<const float4*>(p);
-                v[0] = fmaf(f, q.x, v[0]);
-                v[1] = fmaf(f, q.y, v[1]);
-                v[2] = fmaf(f, q.z, v[2]);
-                v[3] = fmaf(f, q.w, v[3]);
+                const float4 r = *reinterpret_cast<const float4*>(p);
+                q[0] = r.x, q[1] = r.y, q[2] = r.z, q[3] = r.w;
             } else {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    if (n + k < N) v[k] = fmaf(f, p[k], v[k]);
+                    if (n + k < N) q[k] = p[k];
             }
+            if (at == place && named == s)  // (not a slot without an expert)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = fmaf(f, q[k], v[k]);
         }
         T* o = out + t * ldo + n;
         if (wide) {
@@ -58,7 +64,7 @@ __global__ void __launch_bounds__(THREADS) combine_kernel(const float* parts, co
 }
 
 template <typename T>
-int combine_t(const float* parts, const int32_t* place_of, const float* weights, void* out, int64_t ldo, int tokens, int top_k,
+int combine_t(const float* parts, const int32_t* place_of, const int32_t* order, const float* weights, void* out, int64_t ldo, int tokens, int top_k,
               int N, cudaStream_t s)
 {
     const DeviceInfo di = device_info();
@@ -67,8 +73,9 @@ int combine_t(const float* parts, const int32_t* place_of, const float* weights,
     const int64_t ctas = ((int64_t)tokens * quads + THREADS - 1) / THREADS;
     const bool wide = N % 4 == 0 && ((reinterpret_cast<uintptr_t>(out) | (uintptr_t)(ldo * (int64_t)sizeof(T))) &
                                      (4 * sizeof(T) - 1)) == 0;
-    return launch_pdl(combine_kernel<T>, dim3((unsigned)(ctas < di.sms * 8 ? ctas : di.sms * 8)), dim3(THREADS), 0, s,
-                      parts, place_of, weights, static_cast<T*>(out), ldo, tokens, top_k, N, quads, wide,
+    return launch_pdl(ctas <= di.sms * 8 ? combine_kernel<T, 8> : combine_kernel<T, 2>,
+                      dim3((unsigned)(ctas < di.sms * 8 ? ctas : di.sms * 8)), dim3(THREADS), 0, s,
+                      parts, place_of, order, weights, static_cast<T*>(out), ldo, tokens, top_k, N, quads, wide,
                       wait_timeout_counter()) == cudaSuccess
                ? QGEMV_OK
                : QGEMV_CUDA_ERROR;
@@ -76,12 +83,12 @@ int combine_t(const float* parts, const int32_t* place_of, const float* weights,
 
 }  // namespace
 
-int launch_mx_combine(int type, const float* parts, const int32_t* place_of, const float* weights, void* out, int64_t ldo,
-                      int tokens, int top_k, int N, cudaStream_t s)
+int launch_mx_combine(int type, const float* parts, const int32_t* place_of, const int32_t* order, const float* weights,
+                      void* out, int64_t ldo, int tokens, int top_k, int N, cudaStream_t s)
 {
-    if (type == QGEMV_F32) return combine_t<float>(parts, place_of, weights, out, ldo, tokens, top_k, N, s);
-    if (type == QGEMV_F16) return combine_t<__half>(parts, place_of, weights, out, ldo, tokens, top_k, N, s);
-    return combine_t<__nv_bfloat16>(parts, place_of, weights, out, ldo, tokens, top_k, N, s);
+    if (type == QGEMV_F32) return combine_t<float>(parts, place_of, order, weights, out, ldo, tokens, top_k, N, s);
+    if (type == QGEMV_F16) return combine_t<__half>(parts, place_of, order, weights, out, ldo, tokens, top_k, N, s);
+    return combine_t<__nv_bfloat16>(parts, place_of, order, weights, out, ldo, tokens, top_k, N, s);
 }
 
 // From 8 rows an expert on (of those that can have any).  64 experts of 1408 x

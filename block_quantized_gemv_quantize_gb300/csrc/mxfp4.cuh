@@ -157,7 +157,7 @@ struct MxArgs {
     int slots, top_k;      // x's row of slot s is s / x_div
     int x_div;
     void* y;               // gemm, gate_up: [slots]; down: fp32 partial results [place][N]
-    int32_t* place_of;     // down, [slots]: a slot's place (its row of the partial results), -1 for none
+    int32_t* place_of;     // down, [slots]: a slot's place (its row of the partial results), -1 for none; of a slot that order does not name: anything
     void* planes;          // workspace for rows of x as halves (mx_planes_bytes)
 };
 
@@ -168,7 +168,7 @@ bool mx_many_rows(int64_t slots, int experts, int K);
 size_t mx_planes_bytes(int type, int64_t rows, int K);
 
 int launch_mx_gemm(int mode, int type, const MxArgs& a, cudaStream_t s);
-int launch_mx_combine(int type, const float* parts, const int32_t* place_of, const float* weights, void* out, int64_t ldo, int tokens,
-                      int top_k, int N, cudaStream_t s);
+int launch_mx_combine(int type, const float* parts, const int32_t* place_of, const int32_t* order, const float* weights,
+                      void* out, int64_t ldo, int tokens, int top_k, int N, cudaStream_t s);
 
 }  // namespace qgemv

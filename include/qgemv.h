@@ -662,15 +662,19 @@ int moe_group(const int32_t* ids, int32_t* offsets, int32_t* order, void* worksp
  * Products run on the tensor cores on the codes themselves; sums are fp32, and
  * there is one rounding to `type` at the end.  Rows of x enter with 22 bits or
  * all of theirs, but to no less than 2^-38 of the row's largest finite
- * magnitude.  The result is the same on every call with the same arguments.
+ * magnitude.  The result is the same on every call with the same arguments
+ * (whatever the workspace holds).
  *   w_*       packs (qpack_mxfp4) of `experts` weights of N rows of K values
  *   x, h      rows of `type`, row stride ldx / ldh (read; h of gate_up and y
  *             and out are written, and overlap nothing that is read): x has
  *             `tokens` rows of K values, h of moe_down tokens * top_k
- *   offsets, order  as moe_route writes them, read on the device; entries out
- *             of range are cut or skipped, an offset below an earlier one
- *             counts as that; nothing outside the arrays is touched.  order may be NULL where top_k is 1: slot i is then at
- *             place i, the rows are sorted already.
+ *   offsets, order  as moe_route writes them, read on the device: order names
+ *             each slot once.  Entries out of range are cut or skipped, an offset
+ *             below an earlier one counts as that; nothing outside the arrays is
+ *             touched.  A slot that order does not name leaves its row of y or h
+ *             as it was, and is no term of moe_down's sum; of one that it names
+ *             more than once, any of the places counts.  order may be NULL where
+ *             top_k is 1: slot i is then at place i, the rows are sorted already.
  *   weights   fp32 [tokens][top_k]
  *   workspace *_workspace_bytes() bytes, 16-byte aligned, with anything in it
  *             (NULL where that is 0).  Calls that share it must not overlap.

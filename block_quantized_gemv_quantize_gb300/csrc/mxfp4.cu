@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(THREADS, 8) dequantize_kernel(const uint8_t* i
     }
 }
 
-// One CTA a tile: the rows' largest scales, then the units, a warp a unit.
+// One CTA a tile: the rows' largest scales (of blocks that are not all zeros), then the units, a warp a unit.
 __global__ void __launch_bounds__(128) pack_kernel(const uint8_t* canon, uint8_t* pack, MxLayout L,
                                                    int64_t tiles, unsigned int* status)
 {
@@ -215,8 +215,15 @@ __global__ void __launch_bounds__(128) pack_kernel(const uint8_t* canon, uint8_t
         {
             const int r = threadIdx.x / 8;
             int top = 0;
-            for (int b = threadIdx.x & 7; b < nb && n0 + r < L.N; b += 8)
-                top = max(top, (int)rows[((int64_t)r * nb + b) * MX_BYTES]);  // (255, a NaN, is the largest)
+            for (int b = threadIdx.x & 7; b < nb && n0 + r < L.N; b += 8) {
+                const uint8_t* block = rows + ((int64_t)r * nb + b) * MX_BYTES;
+                const int e = block[0];
+                if (e <= top) continue;
+                uint32_t any = e == 255;  // (NaN, whatever the codes)
+#pragma unroll
+                for (int k = 1; k <= 16; ++k) any |= block[k] & 0x77u;
+                if (any) top = e;  // (a block of zeros has none to keep)
+            }
             top = max(top, __shfl_xor_sync(~0u, top, 1));
             top = max(top, __shfl_xor_sync(~0u, top, 2));
             top = max(top, __shfl_xor_sync(~0u, top, 4));
@@ -238,7 +245,7 @@ __global__ void __launch_bounds__(128) pack_kernel(const uint8_t* canon, uint8_t
                     for (int k = 0; k < 8; ++k)  // value 4 t + k % 4 of the block's half k / 4
                         word[j] |= (uint32_t)((block[1 + 4 * t + (k & 3)] >> (k < 4 ? 0 : 4)) & 15u) << (4 * k);
                 }
-                const int rel = there ? 127 - (tops[r] - (int)block[0]) : 127;
+                const int rel = there ? min(127, 127 - (tops[r] - (int)block[0])) : 127;
                 if (rel < MX_SCALE_MIN) word[j] = 0;
                 if (j == t) scale = (uint32_t)max(MX_SCALE_MIN, rel);
             }

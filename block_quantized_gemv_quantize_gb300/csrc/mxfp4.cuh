@@ -26,8 +26,8 @@ constexpr int MX_MAX_K = 1 << 15, MX_MAX_N = 1 << 24, MX_MAX_EXPERTS = 1024, MX_
 //          2^(b - 127) relative to the row's largest, 100 .. 127; a block
 //          with a smaller one is zeros (with codes as halves it would have to
 //          round, and it is below 2^-27 of the row's largest).
-//   tops   [16] bytes: the row's largest scale byte, 255 for a row that holds
-//          a NaN block
+//   tops   [16] bytes: the row's largest scale byte among blocks that are not all
+//          zeros, 255 for a row that holds a NaN block
 // A lane's 16 bytes are its operands of four m16n8k16 products, if the K index
 // runs through a block in the order in which the words have it; and its pairs
 // are the fragments of a 16 x 256-bit store to tensor memory with K in its own

@@ -45,6 +45,14 @@ struct MxsPlan {
     size_t smem;
 };
 
+// Where the row tiles' table lies in shared memory: after the rings, the exchange and the rows of x.
+template <int TERMS>
+__device__ __forceinline__ int* mxs_before(uint8_t* sm, const MxsPlan& p)
+{
+    return reinterpret_cast<int*>(sm + MXS_WARPS * MXS_STAGES * 2 * MX_UNIT_BYTES + MXS_WARPS * 2 * MXS_ROWS * MXS_RED * sizeof(float) +
+                                  (size_t)p.rows * TERMS * p.x_bytes);
+}
+
 __device__ __forceinline__ void cp_async16(void* smem, const void* gmem)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(gmem));
@@ -163,6 +171,100 @@ __device__ __forceinline__ float mx_silu(float g)
     } else {
         const float t = __expf(-fabsf(g));
         return __fdividef(g < 0.0f ? g * t : g, 1.0f + t);
+    }
+}
+
+// ---- rows of a weight with scales far apart ------------------------------------------
+//
+// What the products make of a row marked by 255 is anything, in that row alone; its results
+// are then written over by these, a warp a row and slot: NaN, or fp32 sums of the blocks, apart
+// by 64 powers of two.  Hardly ever needed (neighbouring blocks are about as large as one another), and
+// slow: one row of the weights in 1000 makes a token's gate and up (64 experts of 1408 x 5120) 35 us for 20, 4096 tokens' 3.7 ms
+// for 0.43.  Behind the products' loops, from hidden arguments, it takes none of their registers.
+
+// The arguments with sizes that the compiler does not know for those of the products: what it
+// could compute once for both would take registers of their loops.
+__device__ __forceinline__ MxArgs mx_hidden(MxArgs a)
+{
+    asm volatile("" : "+r"(a.L.experts), "+r"(a.L.N), "+r"(a.L.K));
+    return a;
+}
+
+// The largest scale byte of row r of a tile among blocks that are not all zeros, 255 if one is NaN.
+// By a warp, four lanes a block.
+__device__ __forceinline__ int mx_marked_top(const uint8_t* tile, int units, int r)
+{
+    const int lane = threadIdx.x & 31;
+    int top = 0;
+    for (int b = lane >> 2; b < 2 * units; b += 8) {
+        const uint8_t* unit = tile + (b >> 1) * MX_UNIT_BYTES;
+        const int at = (b & 1) * 2 + (r >> 3), e = unit[MX_UNIT_CODES + (r & 7) * 4 + at];
+        const uint32_t word = *reinterpret_cast<const uint32_t*>(unit + (4 * (r & 7) + (lane & 3)) * 16 + at * 4);
+        if ((word & 0x77777777u) || e == 255) top = max(top, e);
+    }
+    return __reduce_max_sync(~0u, top);
+}
+
+// Row r of a tile times a row of x, 2^p being what scale byte `top` stands for.  By a warp, four
+// lanes a block.
+template <typename X>
+__device__ __forceinline__ float mx_marked_product(const uint8_t* tile, int units, int r, int top, int p, const X& x)
+{
+    const int lane = threadIdx.x & 31, t = lane & 3;
+    float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int b = lane >> 2; b < 2 * units; b += 8) {
+        const uint8_t* unit = tile + (b >> 1) * MX_UNIT_BYTES;
+        const int at = (b & 1) * 2 + (r >> 3), l = max(0, top - (int)unit[MX_UNIT_CODES + (r & 7) * 4 + at]);
+        uint32_t h[4];
+        e2m1_halves(*reinterpret_cast<const uint32_t*>(unit + (4 * (r & 7) + t) * 16 + at * 4), h);
+        float v[8], sum = 0.0f;
+        x.values(b, t, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 w = __half22float2(*reinterpret_cast<const __half2*>(h + i));
+            sum = fmaf(w.y, v[2 * i + 1], fmaf(w.x, v[2 * i], sum));
+        }
+        sum *= __uint_as_float((uint32_t)(127 - (l & 63)) << 23);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) part[j] += l >> 6 == j ? sum : 0.0f;
+    }
+    float y = 0.0f;
+#pragma unroll
+    for (int j = 3; j >= 0; --j) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) part[j] += __shfl_xor_sync(~0u, part[j], o);
+        y += mul_pow2(part[j], max(-378, p + x.exponent - 64 * j));
+    }
+    return y;
+}
+
+// The outputs of row r of an expert's tile for the cnt slots from place s0 on, if it is marked.
+// By a warp.
+template <typename T, int MODE, typename O, typename X>
+__device__ __forceinline__ void mx_marked_row(const MxArgs& a, O* y, int e, int tile, int r, int64_t s0, int cnt, X& x,
+                                              unsigned int* status)
+{
+    constexpr bool PAIR = MODE == MX_GATE_UP;
+    const int units = a.L.units(), n = tile * MX_TILE_N + r;
+    if (tile >= a.L.tiles() || n >= a.L.N) return;
+    const int64_t at = e * a.L.expert_bytes() + tile * a.L.tile_bytes();
+    const uint8_t *w = a.w + at, *w2 = PAIR ? a.w2 + at : w;
+    const uint8_t mark = w[units * MX_UNIT_BYTES + r], mark2 = w2[units * MX_UNIT_BYTES + r];
+    if (mark != 255 && mark2 != 255) return;
+    // (the other of a pair need not be marked: its bytes are 127 - l)
+    const int top = mark == 255 ? mx_marked_top(w, units, r) : 127, top2 = PAIR && mark2 == 255 ? mx_marked_top(w2, units, r) : 127;
+    const bool nan = top == 255 || top2 == 255;
+    const int p = (mark == 255 ? top : mark) - 127, p2 = (mark2 == 255 ? top2 : mark2) - 127;
+    for (int c = 0; c < cnt; ++c) {
+        const int s = x.take(c);
+        if (s < 0) continue;
+        float v = __uint_as_float(0x7FC00000u);
+        if (!nan) {
+            v = mx_marked_product(w, units, r, top, p, x);
+            if constexpr (PAIR) v = mx_silu<T>(v) * mx_marked_product(w2, units, r, top2, p2, x);
+        }
+        const int64_t to = (MODE == MX_DOWN ? s0 + c : (int64_t)s) * a.ldy + n;
+        if ((threadIdx.x & 31) == 0 && QG_OK(qg_in(to, 1, (int64_t)a.slots * a.ldy), status, 315)) y[to] = from_f32<O>(v);
     }
 }
 
@@ -309,6 +411,65 @@ struct MxCursor {
     }
 };
 
+// Rows of x as they are in memory, for mx_marked_row: take() goes to one, and returns its slot.
+template <typename T>
+struct MxsPlaceRows {
+    const MxArgs& a;
+    int place;
+    const T* row = nullptr;
+    int exponent = 0;
+    __device__ int take(int c)
+    {
+        const int s = a.order ? a.order[place + c] : place + c;
+        if (s < 0 || s >= a.slots) return -1;
+        row = static_cast<const T*>(a.x) + (int64_t)(s / a.x_div) * a.ldx;
+        if constexpr (!std::is_same<T, __half>::value) {
+            uint32_t top = 0;
+            for (int k = threadIdx.x & 31; k < a.L.K; k += 32) {
+                const uint32_t m = __float_as_uint(to_f32(row[k])) & 0x7FFFFFFFu;
+                top = max(top, m < 0x7F800000u ? m : 0u);
+            }
+            exponent = mx_row_exponent(__reduce_max_sync(~0u, top));
+        }
+        return s;
+    }
+    __device__ void values(int b, int t, float (&v)[8]) const
+    {
+        const MxRowFactor f(exponent);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = 32 * b < a.L.K ? to_f32(row[32 * b + 4 * t + (i & 3) + (i >> 2) * 16]) * f.a * f.b : 0.0f;
+    }
+};
+
+// The marked rows of a warp's tiles, once more.
+template <typename T, int MODE>
+__device__ __forceinline__ void mxs_marked_rows(const MxArgs& a, const MxsPlan& p, const int* before, unsigned int* status)
+{
+    using O = typename std::conditional<MODE == MX_DOWN, float, T>::type;
+    constexpr int W = MODE == MX_GATE_UP ? 1 : 2;
+    const int* start = before + a.L.experts + 1;
+    const int warp = threadIdx.x >> 5, tiles = (a.L.tiles() + W - 1) / W;
+    const int64_t items = (int64_t)before[a.L.experts] * tiles;
+    MxCursor at;
+    at.start(items * blockIdx.x / gridDim.x, items * (blockIdx.x + 1) / gridDim.x, tiles, warp / p.parts, MXS_WARPS / p.parts, before,
+             a.L.experts);
+    do {
+        const int place = start[at.e] + (at.rt - before[at.e]) * p.rows, cnt = min(p.rows, start[at.e + 1] - place);
+        MxsPlaceRows<T> rows{a, place};
+        for (; at.tile < at.end; at.tile += at.step)
+            for (int i = warp % p.parts; i < W * MX_TILE_N; i += p.parts)
+                mx_marked_row<T, MODE>(a, static_cast<O*>(a.y), at.e, at.tile * W + i / MX_TILE_N, i % MX_TILE_N, place, cnt, rows, status);
+    } while (at.next_rows(before));
+}
+
+// (A call leaves the registers of the loop before it alone, mostly: six fp32 tokens' down product takes
+// 35.4 us with it, 37.1 without; their gate and up 55.9 and 53.4.)
+template <typename T, int MODE>
+__device__ __noinline__ void mxs_marked_call(MxArgs a, MxsPlan p, const int* before, unsigned int* status)
+{
+    mxs_marked_rows<T, MODE>(a, p, before, status);
+}
+
 template <typename T, int MODE>
 __global__ void __launch_bounds__(MXS_THREADS, 1) mxs_kernel(MxArgs a, MxsPlan p, unsigned int* status)
 {
@@ -323,7 +484,7 @@ __global__ void __launch_bounds__(MXS_THREADS, 1) mxs_kernel(MxArgs a, MxsPlan p
     float* red = reinterpret_cast<float*>(sm + WARPS * STAGES * STAGE);
     constexpr int RED_ONE = WARPS * W * COLS * MXS_RED;
     uint8_t* xs = reinterpret_cast<uint8_t*>(red + RED_ONE);
-    int* before = reinterpret_cast<int*>(xs + (size_t)p.rows * TERMS * p.x_bytes);
+    int* before = mxs_before<TERMS>(sm, p);
     int* start = before + a.L.experts + 1;
     int* sums = start + a.L.experts + 1;
     int* slot_of = sums + 32;
@@ -408,6 +569,7 @@ __global__ void __launch_bounds__(MXS_THREADS, 1) mxs_kernel(MxArgs a, MxsPlan p
         else __syncwarp();
     };
     int stage = 0;
+    bool marked = false;  // a row met
     do {
         __syncthreads();  // the rows before are done with
         const int place = start[at.e] + (at.rt - before[at.e]) * p.rows, cnt = min(p.rows, start[at.e + 1] - place);
@@ -501,7 +663,7 @@ __global__ void __launch_bounds__(MXS_THREADS, 1) mxs_kernel(MxArgs a, MxsPlan p
                     float sum = 0.0f;
 #pragma unroll 4
                     for (int k = 0; k < parts; ++k) sum += from[k * (W * COLS * MXS_RED)];
-                    v[w] = tops[w] == 255 ? __uint_as_float(0x7FC00000u) : mul_pow2(sum, tops[w] - 127 + x_exp[c]);
+                    v[w] = mul_pow2(sum, tops[w] - 127 + x_exp[c]);
                 }
                 if constexpr (PAIR) {
                     if (n < a.L.N && QG_OK(qg_in(s * a.ldy + n, 1, (int64_t)a.slots * a.ldy), status, 312))
@@ -514,9 +676,17 @@ __global__ void __launch_bounds__(MXS_THREADS, 1) mxs_kernel(MxArgs a, MxsPlan p
                 }
             }
             together_barrier();
+            marked |= tops[0] == 255 || tops[1] == 255;
         }
     } while (at.next_rows(before));
     cp_async_wait<0>();
+    if (__any_sync(~0u, marked)) {  // (the warps of a tile have met the same)
+        uint32_t zero = 0;
+        asm volatile("" : "+r"(zero));
+        const int* table = mxs_before<TERMS>(sm + zero, p);
+        if constexpr (PAIR) mxs_marked_rows<T, MODE>(mx_hidden(a), p, table, status);
+        else mxs_marked_call<T, MODE>(a, p, table, status);
+    }
 }
 
 }  // namespace qgemv

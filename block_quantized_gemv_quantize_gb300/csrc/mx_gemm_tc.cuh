@@ -4,7 +4,7 @@
 // a tcgen05.mma over a pair of SMs, from tensor memory) and up to 160
 // rows of x as operand B (half in each SM's shared memory).  Both are halves: a
 // code times its scale relative to the row's largest, times 2^13, is one
-// exactly (the pack has no scale below 2^-27); fp16 rows are what they are;
+// exactly (a row with a scale below 2^-27 is marked, and computed at the end); fp16 rows are what they are;
 // bf16 rows go by a power of two that brings the row's largest finite element
 // to [2^14, 2^15), which keeps every element to 2^-39 of it (all eight bits of
 // those within 2^-31), fp32 rows as two such terms, in a pass of its own.  (As
@@ -86,6 +86,19 @@ constexpr size_t mxt_smem(int experts)
     return 1024 + (size_t)S::BATCHES * S::BATCH * 2 * TERMS * (MXT_ROWS<TERMS> / 2) * 128 +
            (size_t)MXT_CONVERT * S::AHEAD * 4 * MX_UNIT_BYTES + MXT_EPI_BYTES + (2 * S::BATCHES + 2 * MXT_A_STAGES + 5) * sizeof(uint64_t) +
            8 + MXT_SETS * MXT_ROWS<TERMS> * (sizeof(int) + sizeof(float)) + (size_t)(2 * (experts + 1) + 32 + 4) * sizeof(int);
+}
+
+// Where the row tiles' table lies in shared memory: after the rings, the results' buffer, 8-byte
+// barriers (and what aligns what follows to 16), the items' slots and powers.
+template <int TERMS>
+__device__ __forceinline__ int* mxt_before(uint8_t* sm_raw)
+{
+    using S = MxtShape<TERMS>;
+    constexpr size_t BARRIERS = (2 * S::BATCHES + 2 * MXT_A_STAGES + 5) * sizeof(uint64_t);
+    constexpr size_t AT = (size_t)S::BATCHES * S::BATCH * 2 * TERMS * (MXT_ROWS<TERMS> / 2) * 128 +
+                          (size_t)MXT_CONVERT * S::AHEAD * 4 * MX_UNIT_BYTES + MXT_EPI_BYTES + BARRIERS;
+    return reinterpret_cast<int*>(sm_raw + ((1024u - (smem_u32(sm_raw) & 1023u)) & 1023u) + AT + AT % 16 +
+                                  MXT_SETS * MXT_ROWS<TERMS> * (sizeof(int) + sizeof(float)));
 }
 
 // ---- tcgen05, clusters --------------------------------------------------------
@@ -365,6 +378,67 @@ __device__ __forceinline__ int mxt_slot(const MxArgs& a, int place)
     return s < 0 || s >= a.slots ? -1 : s;
 }
 
+// Rows of x as halves, from place s0 on, for mx_marked_row: take() goes to one, and returns its slot.
+template <int TERMS>
+struct MxtPlaceRows {
+    const MxArgs& a;
+    const MxtRows& x;
+    int s0;
+    const __half* row = nullptr;
+    int exponent = 0;
+    __device__ int take(int c)
+    {
+        const int s = mxt_slot(a, s0 + c);
+        if (s < 0) return s;
+        row = x.x + (int64_t)(s / a.x_div) * x.ld;
+        if (x.scale) exponent = mxt_exponent(x.scale[s / a.x_div]);
+        return s;
+    }
+    __device__ void values(int b, int t, float (&v)[8]) const
+    {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint2 q[TERMS];
+#pragma unroll
+            for (int i = 0; i < TERMS; ++i)
+                q[i] = 32 * b < x.values ? *reinterpret_cast<const uint2*>(row + i * x.plane + 32 * b + 4 * t + 16 * h) : make_uint2(0, 0);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float f = 0.0f;
+#pragma unroll
+                for (int i = 0; i < TERMS; ++i) f += __half2float(__ushort_as_half((unsigned short)((k < 2 ? q[i].x : q[i].y) >> 16 * (k & 1))));
+                v[4 * h + k] = f;
+            }
+        }
+    }
+};
+
+// The marked rows of the items of this CTA, if it has met any.  By the converting warps.
+template <typename T, int MODE>
+__device__ __forceinline__ void mxt_marked_rows(const MxArgs& a, const MxtRows& x, const int* before, unsigned int* status)
+{
+    using O = typename std::conditional<MODE == MX_DOWN, float, T>::type;
+    constexpr int GROUP_TILES = MODE == MX_GATE_UP ? 8 : 16;
+    const int* start = before + a.L.experts + 1;
+    const volatile int* sums = start + a.L.experts + 1;
+    if (sums[32] || !sums[34]) return;  // (gave up; marks seen)
+    MxtWalk<MXT_ROWS<MX_TERMS<T>>> walk;
+    walk.before = before;
+    walk.start = start;
+    walk.groups = (a.L.tiles() + GROUP_TILES - 1) / GROUP_TILES;
+    walk.items = (int64_t)before[a.L.experts] * walk.groups;
+    walk.item = blockIdx.x / 2;
+    walk.step = gridDim.x / 2;
+    walk.e = 0;
+    const int tile = (int)cluster_rank() * (GROUP_TILES / 2);
+    for (bool more = walk.find(); more; more = walk.next()) {
+        MxtPlaceRows<MX_TERMS<T>> rows{a, x, walk.s0};
+        for (int i = (threadIdx.x >> 5) - MXT_LOAD_WARP; i < GROUP_TILES / 2 * MX_TILE_N; i += MXT_LOAD)
+            mx_marked_row<T, MODE>(a, static_cast<O*>(a.y), walk.e, walk.g * GROUP_TILES + tile + i / MX_TILE_N, i % MX_TILE_N, walk.s0,
+                                   walk.cnt, rows, status);
+    }
+}
+
 template <typename T, int MODE>
 __global__ void __launch_bounds__(MXT_THREADS, 1)
     mxt_kernel(MxArgs a, MxtRows x, unsigned int* status)
@@ -383,11 +457,12 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
     uint64_t* all_done = acc_empty + 2;
     int* epi_slots = reinterpret_cast<int*>(all_done + 1 + (reinterpret_cast<uintptr_t>(all_done + 1) & 8) / 8);
     float* epi_scale = reinterpret_cast<float*>(epi_slots + MXT_SETS * ROWS);
-    int* before = reinterpret_cast<int*>(epi_scale + MXT_SETS * ROWS);
+    int* before = mxt_before<TERMS>(sm_raw);
     int* start = before + a.L.experts + 1;
     int* sums = start + a.L.experts + 1;
     volatile int* gave_up = sums + 32;
     uint32_t* tmem_at = reinterpret_cast<uint32_t*>(sums + 33);
+    volatile int* marks = sums + 34;  // this CTA's weights have rows marked by 255
 
     const int lane = threadIdx.x & 31, warp = __shfl_sync(~0u, threadIdx.x >> 5, 0);
     const uint32_t rank = cluster_rank();
@@ -408,6 +483,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
         mbar_init(all_done, 1);
         fence_barrier_init();
         *gave_up = 0;
+        *marks = 0;
     }
     if (warp == MXT_MMA_WARP) {
         asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(tmem_at)) : "memory");
@@ -620,6 +696,10 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
         if (in) ++issued;  // (a last batch that is not full)
         cp_async_wait<0>();
         while (issued > 0) tell();
+        asm volatile("bar.sync 2, %0;" ::"n"((MXT_LOAD + MXT_EPI) * 32) : "memory");  // every result of this CTA is written
+        uint32_t zero = 0;
+        asm volatile("" : "+r"(zero));
+        mxt_marked_rows<T, MODE>(mx_hidden(a), x, mxt_before<TERMS>(sm_raw + zero), status);
     } else if (warp == MXT_MMA_WARP) {
         // ---- products: a wait, eight products and a commit or two a step
         if (rank == 0) {
@@ -730,6 +810,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
             // the weight's power of two, and whether its product with a row's is sure to be an
             // fp32 number (nearly always), exact then
             const int e = next_e, p = e - 127 - MXT_SHIFT;
+            if (e == 255) *marks = 1;
             const float f0 = e == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float((uint32_t)(max(p, -126) + 127) << 23);
             bool mild = e == 255 || (p >= (SCALED ? -63 : -126) && p <= (SCALED ? 63 : 127));
             if constexpr (SCALED)
@@ -858,6 +939,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
             set.next();
             walk = after;
         }
+        asm volatile("bar.arrive 2, %0;" ::"n"((MXT_LOAD + MXT_EPI) * 32) : "memory");
     }
     if (warp == MXT_MMA_WARP && rank == 0) {  // what was issued ends before tensor memory is given back
         tc_commit_both(smem_u32(all_done), elected());

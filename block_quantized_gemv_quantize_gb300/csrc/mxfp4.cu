@@ -214,20 +214,22 @@ __global__ void __launch_bounds__(128) pack_kernel(const uint8_t* canon, uint8_t
         uint8_t* to = pack + tile * L.tile_bytes();
         {
             const int r = threadIdx.x / 8;
-            int top = 0;
+            int top = 0, least = 255;
             for (int b = threadIdx.x & 7; b < nb && n0 + r < L.N; b += 8) {
                 const uint8_t* block = rows + ((int64_t)r * nb + b) * MX_BYTES;
                 const int e = block[0];
-                if (e <= top) continue;
+                if (e <= top && e >= least) continue;
                 uint32_t any = e == 255;  // (NaN, whatever the codes)
 #pragma unroll
                 for (int k = 1; k <= 16; ++k) any |= block[k] & 0x77u;
-                if (any) top = e;  // (a block of zeros has none to keep)
+                if (any) top = max(top, e), least = min(least, e);  // (a block of zeros has no scale to keep)
             }
-            top = max(top, __shfl_xor_sync(~0u, top, 1));
-            top = max(top, __shfl_xor_sync(~0u, top, 2));
-            top = max(top, __shfl_xor_sync(~0u, top, 4));
-            if ((threadIdx.x & 7) == 0) tops[r] = top;
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                top = max(top, __shfl_xor_sync(~0u, top, o));
+                least = min(least, __shfl_xor_sync(~0u, least, o));
+            }
+            if ((threadIdx.x & 7) == 0) tops[r] = top - least > MX_NEAR ? 255 : top;
         }
         __syncthreads();
         const int g = lane >> 2, t = lane & 3;
@@ -245,9 +247,10 @@ __global__ void __launch_bounds__(128) pack_kernel(const uint8_t* canon, uint8_t
                     for (int k = 0; k < 8; ++k)  // value 4 t + k % 4 of the block's half k / 4
                         word[j] |= (uint32_t)((block[1 + 4 * t + (k & 3)] >> (k < 4 ? 0 : 4)) & 15u) << (4 * k);
                 }
-                const int rel = there ? min(127, 127 - (tops[r] - (int)block[0])) : 127;
-                if (rel < MX_SCALE_MIN) word[j] = 0;
-                if (j == t) scale = (uint32_t)max(MX_SCALE_MIN, rel);
+                uint32_t any = word[j] & 0x77777777u;
+                any |= __shfl_xor_sync(~0u, any, 1);
+                any |= __shfl_xor_sync(~0u, any, 2);
+                if (j == t) scale = tops[r] != 255 ? 127 - (any ? tops[r] - (int)block[0] : 0) : there ? block[0] : 0;
             }
             uint8_t* unit = to + (int64_t)u * MX_UNIT_BYTES;
             if (QG_OK(qg_in(unit - pack, MX_UNIT_BYTES, L.bytes()), status, 302)) {

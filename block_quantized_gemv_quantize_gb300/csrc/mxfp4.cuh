@@ -13,7 +13,7 @@ constexpr int MX_UNIT_K = 64;       // values of a row in one unit of the pack
 constexpr int MX_TILE_N = 16;       // rows of a tile
 constexpr int MX_UNIT_CODES = MX_TILE_N * MX_UNIT_K / 2;
 constexpr int MX_UNIT_BYTES = MX_UNIT_CODES + MX_TILE_N * MX_UNIT_K / 32;  // codes, scale bytes
-constexpr int MX_SCALE_MIN = 100;  // of the pack's scale bytes
+constexpr int MX_NEAR = 27;  // how far (in powers of two) a block's scale may be below its row's largest
 constexpr int MX_MAX_K = 1 << 15, MX_MAX_N = 1 << 24, MX_MAX_EXPERTS = 1024, MX_MAX_TOP_K = 32;
 
 // The pack: [expert][tile of 16 rows], a tile being
@@ -22,12 +22,12 @@ constexpr int MX_MAX_K = 1 << 15, MX_MAX_N = 1 << 24, MX_MAX_EXPERTS = 1024, MX_
 //          the unit's first block, row g + 8 there, row g in its second block,
 //          row g + 8 there.  A word has the block's values 4 t .. 4 t + 3 and
 //          16 + 4 t .. 16 + 4 t + 3, a nibble each in that order.  Then 32
-//          scale bytes [g][4] in the order of a lane's words: b for the scale
-//          2^(b - 127) relative to the row's largest, 100 .. 127; a block
-//          with a smaller one is zeros (with codes as halves it would have to
-//          round, and it is below 2^-27 of the row's largest).
+//          scale bytes [g][4] in the order of a lane's words: 127 - l for a block
+//          whose scale is 2^-l of the row's largest (l = 0 for a block of zeros), the
+//          block's own byte in a row marked by 255
 //   tops   [16] bytes: the row's largest scale byte among blocks that are not all
-//          zeros, 255 for a row that holds a NaN block
+//          zeros; 255 for a row that holds a NaN block, or one that is farther than
+//          2^-27 (MX_NEAR) below the largest: no half holds its values beside those
 // A lane's 16 bytes are its operands of four m16n8k16 products, if the K index
 // runs through a block in the order in which the words have it; and its pairs
 // are the fragments of a 16 x 256-bit store to tensor memory with K in its own

@@ -616,8 +616,9 @@ int dequantize_mxfp4(int type, const void* blocks, void* y, int64_t ldy, int64_t
 
 /* qpack_mxfp4 - reorder the blocks of `experts` weights of N rows of K values
  * ([experts][N][K/32][17]) into the products' tiles: 16 rows x 64 values in
- * tensor-core operand order, scales relative to the row's largest (a block whose
- * scale is more than 2^27 below it counts as zeros).  w_pack takes
+ * tensor-core operand order, scales relative to the row's largest.  (A row with
+ * a block, not all zeros, whose scale is more than 2^27 below the largest is
+ * multiplied apart from the others, and slowly.)  w_pack takes
  * mxfp4_pack_bytes() bytes and must not alias w_canon.
  *   experts 1 .. 1024;  N 1 .. 2^24;  K a multiple of 32, 32 .. 32768 */
 size_t mxfp4_pack_bytes(int experts, int N, int K);

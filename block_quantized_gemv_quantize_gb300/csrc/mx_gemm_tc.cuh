@@ -41,8 +41,10 @@ constexpr int MXT_THREADS = (MXT_LOAD_WARP + MXT_LOAD) * 32;
 template <int TERMS>
 constexpr int MXT_ROWS = TERMS == 1 ? 160 : 96;
 // Steps of fp32 rows that an accumulator takes.  The tensor core cuts what does not fit its sum's 24
-// bits, always towards zero: 5120 values in one accumulator come out 8e-6 too small, where 16-bit outputs
-// have steps of 5e-4 and more.  Of fp32 rows every two steps (256 values) are added up by the
+// bits, always towards zero, by up to 2^-23 for a product of 16 values: 5120 values of one sign in one accumulator
+// come out 9e-6 too small, 32768 (the longest) 1.2e-4.  16-bit rows are summed so: their outputs'
+// half steps are 4.9e-4 and 3.9e-3, and sums apart would leave tensor memory for 96 rows an item
+// in place of 160.  Of fp32 rows every two steps (256 values) are added up by the
 // results' warps, rounding to nearest, in tensor memory: 3e-7 off, and 64 experts of 768 x 2048,
 // gate and up, 16 rows each, take 53 us for 50, 32 rows 60 for 53.
 constexpr int MXT_CHUNK = 2;

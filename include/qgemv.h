@@ -663,7 +663,11 @@ int moe_group(const int32_t* ids, int32_t* offsets, int32_t* order, void* worksp
  * Products run on the tensor cores on the codes themselves; sums are fp32, and
  * there is one rounding to `type` at the end.  Rows of x enter with 22 bits or
  * all of theirs, but to no less than 2^-38 of the row's largest finite
- * magnitude.  The result is the same on every call with the same arguments
+ * magnitude.  A sum of 16-bit rows may come out too small by up to 2^-23 of its
+ * terms' magnitudes for each 16 values of K (tensor cores cut what an fp32 accumulator
+ * does not hold: about 9e-6 at K = 5120, 1.2e-4 at 32768 with terms of one sign); one of fp32 rows
+ * is rounded to nearest after every 256.
+ * The result is the same on every call with the same arguments
  * (whatever the workspace holds).
  *   w_*       packs (qpack_mxfp4) of `experts` weights of N rows of K values
  *   x, h      rows of `type`, row stride ldx / ldh (read; h of gate_up and y

@@ -366,8 +366,8 @@ PyObject* call_route(PyObject*, PyObject* const* a, Py_ssize_t n_args)
     }
     const auto device = logits->device();
     const int64_t tokens = logits->size(0), experts = logits->size(1);
-    if (bad || type < 0 || tokens < 1 || tokens > INT32_MAX || experts < 1 || experts > INT32_MAX || top_k < 1 || top_k > experts ||
-        tokens * top_k > (1 << 30))
+    if (bad || type < 0 || (score != QGEMV_SOFTMAX && score != QGEMV_SIGMOID) || tokens < 1 || tokens > INT32_MAX || experts < 1 ||
+        experts > 1024 || top_k < 1 || top_k > 32 || top_k > experts || tokens * top_k > (1 << 30) || !std::isfinite((float)scale))
         Py_RETURN_NONE;
     const c10::cuda::CUDAGuard guard(device);
     at::Tensor ws;

@@ -154,12 +154,15 @@ __device__ __forceinline__ void route_range(const RouteArgs& a, int t0, int t1)
         int id;
         float weight;
         route_token<T, PER>(static_cast<const T*>(a.logits) + t * a.ld, a, lane, id, weight);
-        if (lane < a.top_k) {
+        if (lane < a.top_k && QG_OK(qg_in((int64_t)t * a.top_k + lane, 1, (int64_t)a.tokens * a.top_k), a.status, 340)) {
             a.ids[(int64_t)t * a.top_k + lane] = id;
             a.weights[(int64_t)t * a.top_k + lane] = weight;
         }
     }
 }
+
+// An index of the workspace's counts.
+__device__ __forceinline__ bool counts_in(int64_t i, int bins) { return qg_in(i, 1, (int64_t)(MAX_RANGES + 1) * bins); }
 
 // The bin of an id: its expert, or `experts` for a slot without one.
 __device__ __forceinline__ int bin_of(int id, int experts) { return id >= 0 && id < experts ? id : experts; }
@@ -224,7 +227,7 @@ __device__ void place_range(const RouteArgs& a, const int32_t* ids, int s0, int 
         if (b >= 0) at = mine[b];
         __syncwarp();
         if (b >= 0) {
-            a.order[at + rank] = s;
+            if (QG_OK(qg_in(at + rank, 1, (int64_t)a.tokens * a.top_k), a.status, 341)) a.order[at + rank] = s;
             if (rank == 0) mine[b] = at + __popc(same);
         }
         __syncwarp();
@@ -265,7 +268,8 @@ __global__ void __launch_bounds__(THREADS) count_kernel(RouteArgs a, int per)
     for (int s = t0 * a.top_k + threadIdx.x; s < t1 * a.top_k; s += THREADS)
         atomicAdd(&sm[bin_of(a.ids[s], a.experts)], 1);
     __syncthreads();
-    for (int i = threadIdx.x; i < bins; i += THREADS) a.counts[(int64_t)blockIdx.x * bins + i] = sm[i];
+    for (int i = threadIdx.x; i < bins; i += THREADS)
+        if (QG_OK(counts_in((int64_t)blockIdx.x * bins + i, bins), a.status, 342)) a.counts[(int64_t)blockIdx.x * bins + i] = sm[i];
 }
 
 // Each bin's counts become the sums over the ranges before, its total goes behind them all.  Eight
@@ -302,13 +306,14 @@ __global__ void __launch_bounds__(SUM_THREADS) sum_kernel(RouteArgs a, int range
         }
         part[lane][warp] = at - own;
         const int whose = blockIdx.x * SUM_BINS + warp;
-        if (lane == 31 && whose < bins) a.counts[(int64_t)MAX_RANGES * bins + whose] = at;
+        if (lane == 31 && whose < bins && QG_OK(counts_in((int64_t)MAX_RANGES * bins + whose, bins), a.status, 343))
+            a.counts[(int64_t)MAX_RANGES * bins + whose] = at;
     }
     __syncthreads();
     int at = part[group][sub];
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        if (i < mine) counts[i * bins] = at;
+        if (i < mine && QG_OK(counts_in(counts - a.counts + i * bins, bins), a.status, 344)) counts[i * bins] = at;
         at += n[i];
     }
 }
@@ -394,8 +399,10 @@ size_t route_workspace_bytes(int tokens, int experts)
     return tokens <= SMALL_TOKENS ? 0 : (size_t)(MAX_RANGES + 1) * (experts + 1) * sizeof(int32_t);
 }
 
-int launch_route(int type, const RouteArgs& a, cudaStream_t s)
+int launch_route(int type, const RouteArgs& args, cudaStream_t s)
 {
+    RouteArgs a = args;
+    a.status = wait_timeout_counter();
     if (!a.logits) return route_tp<float, 1, false>(a, s);
     if (type == QGEMV_F32) return route_t<float>(a, s);
     if (type == QGEMV_F16) return route_t<__half>(a, s);

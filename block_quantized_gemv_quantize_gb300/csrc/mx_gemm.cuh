@@ -150,7 +150,7 @@ __device__ void mx_rest(const MxArgs& a, O* y, const int* start, unsigned int* s
         const int s = a.order ? a.order[at] : at;
         if (s < 0 || s >= a.slots) continue;
         if constexpr (MODE == MX_DOWN) {
-            if (threadIdx.x == 0) a.place_of[s] = -1;
+            if (threadIdx.x == 0 && QG_OK(qg_in(s, 1, a.slots), status, 316)) a.place_of[s] = -1;
         } else {
             for (int n = threadIdx.x; n < a.L.N; n += blockDim.x)
                 if (QG_OK(qg_in((int64_t)s * a.ldy + n, 1, (int64_t)a.slots * a.ldy), status, 310))
@@ -580,7 +580,8 @@ __global__ void __launch_bounds__(MXS_THREADS, 1) mxs_kernel(MxArgs a, MxsPlan p
                 if (s < 0 || s >= a.slots) s = -1;
             }
             slot_of[threadIdx.x] = s;
-            if (MODE == MX_DOWN && s >= 0) a.place_of[s] = place + threadIdx.x;  // (whoever has this row tile writes the same)
+            if (MODE == MX_DOWN && s >= 0 && QG_OK(qg_in(s, 1, a.slots), status, 317))
+                a.place_of[s] = place + threadIdx.x;  // (whoever has this row tile writes the same)
             x_exp[threadIdx.x] = 0;
             x_top[threadIdx.x] = 0;
         }

@@ -823,7 +823,7 @@ __global__ void __launch_bounds__(MXT_THREADS, 1)
             const int outputs = max(0, min(WIDE, a.L.N - n0)), columns = (walk.cnt + 15) & ~15;
             if (MODE == MX_DOWN && walk.g == 0 && rank == 0 && quad == 0)
                 for (int r = lane; r < walk.cnt; r += 32)
-                    if (slots[r] >= 0) a.place_of[slots[r]] = walk.s0 + r;
+                    if (slots[r] >= 0 && QG_OK(qg_in(slots[r], 1, a.slots), status, 334)) a.place_of[slots[r]] = walk.s0 + r;
             MxtWalk<ROWS> after = walk;
             more = after.next();
             if (more) look(after);

@@ -133,7 +133,8 @@ struct RouteArgs {
     float* weights;
     int32_t* offsets;
     int32_t* order;
-    int32_t* counts;  // workspace [ranges + 1][experts + 1]
+    int32_t* counts;  // workspace [MAX_RANGES + 1][experts + 1]
+    unsigned int* status;  // of the bounds-checking build
     int tokens, experts, top_k;
     bool sigmoid, renormalize;
     float scale;

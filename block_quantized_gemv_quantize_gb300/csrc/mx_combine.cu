@@ -91,11 +91,12 @@ int launch_mx_combine(int type, const float* parts, const int32_t* place_of, con
     return combine_t<__nv_bfloat16>(parts, place_of, order, weights, out, ldo, tokens, top_k, N, s);
 }
 
-// From 8 rows an expert on (of those that can have any).  64 experts of 1408 x
-// 5120, gate and up, 8 rows each: 113 us by the mma.sync kernel, 125 by this one,
-// 12 rows: 183 and 126 (a second row tile reads the weights again); one of
-// 17408 x 5120, 4 rows: 18 and 18, 8 rows: 23 and 18, 9: 32 and 18; one of
-// 4096 x 4096, 8 rows: 13.5 and 15, 9: 16 and 15.
+// From 8 rows an expert on (of those that can have any: how the slots fall the host does not know).
+// By the mma.sync kernel and by this one, bf16 rows if not said otherwise: 64 experts of 1408 x 5120, gate
+// and up, 8 rows each 112 and 132 us, 12 rows 183 and 126 (a second row tile reads the weights again); one of
+// 17408 x 5120, 4 rows 17.5 and 21.8, 8 rows 22.7 and 22.0 (fp32 33.4 and 27.0), 9 rows 32 and 22; one of 4096 x
+// 4096, 8 rows 13.0 and 15.0 (fp32 15.0 and 17.6), 9 rows 16 and 15.  512 slots all of one expert of 64 take 95 us,
+// less than the even ones, where this one would take 24.
 bool mx_many_rows(int64_t slots, int experts, int K)
 {
     return slots > 8 * (slots < experts ? slots : (int64_t)experts) || K > 16384;

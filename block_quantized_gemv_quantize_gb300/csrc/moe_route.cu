@@ -8,8 +8,8 @@
 // that neither the order of atomics nor the grid changes the result.
 // Up to SMALL_TOKENS tokens one CTA does all of it in one launch (latency);
 // beyond, a first kernel routes and counts, a second adds up each bin's counts
-// over the ranges, a third places the slots.  Bound by latency: of a token's
-// top_k rounds, and of the three launches (17391 tokens, 8 of 128 experts: 18.5 us,
+// over the ranges, a third places the slots.  Bound by the instructions of a
+// token's top_k rounds (2.5 of 4 issued a clock), and the three launches (17391 tokens, 8 of 128 experts: 18.5 us,
 // one token 3.6; a second kernel in which each CTA added up all ranges' counts took 25 us more).
 #include "mxfp4.cuh"
 

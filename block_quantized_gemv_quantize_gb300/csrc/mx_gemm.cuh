@@ -18,8 +18,8 @@
 // own, and a CTA runs through a contiguous range of (expert, row tile, pair), so that x is
 // staged once for many tiles.  The ring runs ahead across tiles and experts.
 // 64 experts of 1408 x 5120, gate and up, a bf16 row each: 490 MB in 90 us, 5.4 TB/s;
-// six fp32 tokens of 6 of 64 experts, 199 MB in 56 us (two terms of x, uneven shares);
-// one token, 46 MB in 19.5 us, of which 5 before the first product.
+// six fp32 tokens of 6 of 64 experts, 199 MB in 53 us (two terms of x, uneven shares);
+// one token, 46 MB in 19.4 us, of which 5 before the first product.
 #pragma once
 
 #include "mxfp4.cuh"

@@ -24,8 +24,9 @@
 // is the row tile's count rounded up to 32.
 //
 // Bound by the tensor pipe where K is long: 4096 tokens of 6 of 64 experts, gate
-// and up of 1408 x 5120, 709 GFLOP in 423 us, 1.68 PFLOP/s.  Where K is short the results
-// take as long (down of 5120 x 1408: 11 steps an item, 372 us with the pass over h and the sum).  A
+// and up of 1408 x 5120, 709 GFLOP in 429 us, 1.65 PFLOP/s (call after call, under the power cap,
+// 490 us, 1.45).  Where K is short the results
+// take as long (down of 5120 x 1408: 11 steps an item, 379 us with the pass over h and the sum).  A
 // product of 16 values of K takes 75 clocks for any N up to 160, that of its 256 rows
 // of weights: 64 experts of 12 rows take 126 us for their 490 MB.
 #pragma once

@@ -234,24 +234,25 @@ __global__ void __launch_bounds__(128) pack_kernel(const uint8_t* canon, uint8_t
         __syncthreads();
         const int g = lane >> 2, t = lane & 3;
         for (int u = warp; u < L.units(); u += 4) {
-            uint32_t word[4];
-            uint32_t scale = 127;
+            uint32_t word[4], live = 0;  // bit j: block j is not all zeros
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int r = g + 8 * (j & 1), b = 2 * u + (j >> 1);
                 word[j] = 0;
-                const bool there = n0 + r < L.N && b < nb;
                 const uint8_t* block = rows + ((int64_t)r * nb + b) * MX_BYTES;
-                if (there) {
+                if (n0 + r < L.N && b < nb) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k)  // value 4 t + k % 4 of the block's half k / 4
                         word[j] |= (uint32_t)((block[1 + 4 * t + (k & 3)] >> (k < 4 ? 0 : 4)) & 15u) << (4 * k);
                 }
-                uint32_t any = word[j] & 0x77777777u;
-                any |= __shfl_xor_sync(~0u, any, 1);
-                any |= __shfl_xor_sync(~0u, any, 2);
-                if (j == t) scale = tops[r] != 255 ? 127 - (any ? tops[r] - (int)block[0] : 0) : there ? block[0] : 0;
+                if (word[j] & 0x77777777u) live |= 1u << j;
             }
+            live |= __shfl_xor_sync(~0u, live, 1);
+            live |= __shfl_xor_sync(~0u, live, 2);
+            // this lane's scale: block t's
+            const int r = g + 8 * (t & 1), b = 2 * u + (t >> 1);
+            const int own = n0 + r < L.N && b < nb ? rows[((int64_t)r * nb + b) * MX_BYTES] : 0;
+            const int scale = tops[r] == 255 ? own : 127 - (live >> t & 1u ? tops[r] - own : 0);
             uint8_t* unit = to + (int64_t)u * MX_UNIT_BYTES;
             if (QG_OK(qg_in(unit - pack, MX_UNIT_BYTES, L.bytes()), status, 302)) {
                 reinterpret_cast<uint4*>(unit)[lane] = make_uint4(word[0], word[1], word[2], word[3]);

@@ -658,7 +658,8 @@ int moe_group(const int32_t* ids, int32_t* offsets, int32_t* order, void* worksp
  * s; a slot in no expert's range gets zeros:
  *   qgemm_mxfp4        y[s] = W_e(s) x[s / top_k]
  *   moe_gate_up_mxfp4  h[s] = silu(G_e(s) x[s / top_k]) * (U_e(s) x[s / top_k]),
- *                      silu(g) = g / (1 + e^-g)
+ *                      silu(g) = g / (1 + e^-g), for 16-bit types to
+ *                      (4 + 1.2 |g|) 2^-23 of it
  *   moe_down_mxfp4     out[t] = sum_j weights[t][j] W_e(s) h[s], s = t top_k + j
  * Products run on the tensor cores on the codes themselves; sums are fp32, and
  * there is one rounding to `type` at the end.  Rows of x enter with 22 bits or
